@@ -16,7 +16,7 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
-from typing import Optional, Tuple
+from typing import NamedTuple, Optional, Tuple
 
 import torch
 
@@ -91,6 +91,20 @@ def load_library():
                                                    u64, vp, vp]
         lib.ckv_compress_decode_norm_rope_store.argtypes = [i32, i32, i32, i32, vp, u64, vp, vp, vp, vp, vp, u32, vp,
                                                             f32, vp, u32, vp, i32, vp, u64, vp, vp]
+        qc = ctypes.POINTER(Q8CacheArg)
+        lib.ckv_capacity_q8_store.argtypes = [u32, u32, u32]
+        lib.ckv_capacity_q8_store.restype = u32
+        lib.ckv_plan_q8_store.argtypes = [qc, vp, vp, vp, u32, u32, vp, u64, u32, u32, i32, vp, vp, vp, vp]
+        lib.ckv_q8_store.argtypes = [qc, i32, vp, vp, u32, vp, vp, u32, vp, vp]
+        for f in (lib.ckv_q8_attn_plan_bytes, lib.ckv_q8_attn_workspace_bytes):
+            f.argtypes = [qc, u32, u32, u32]
+            f.restype = u64
+        lib.ckv_plan_q8_attn.argtypes = [qc, u32, u32, vp, vp, vp, vp, u32, u32, vp, u64, vp, vp]
+        lib.ckv_q8_attn.argtypes = [qc, u32, u32, f32, vp, u32, u32, vp, u64, u32, vp, u64, i32, vp, vp, vp, u64, vp,
+                                    vp]
+        lib.ckv_q8_weigh.argtypes = [qc, u32, u32, f32, f32, vp, vp, u32, vp, vp, vp, vp, u32, vp, u64, u32, vp, vp,
+                                     vp]
+        lib.ckv_q8_evict.argtypes = [qc, vp, vp, vp, u32, vp, u64, vp, u64, u32, u32, u32, u32, vp, vp, vp, vp]
         lib.ckv_error_string.argtypes = [i32]
         lib.ckv_error_string.restype = ctypes.c_char_p
         lib.ckv_version.restype = i32
@@ -503,6 +517,231 @@ def compress_decode_norm_rope_store(head_dim: int, state: torch.Tensor, kv_score
         _ptr(kv_score), _ptr(ape), _ptr(plan_d), _ptr(rid_hint), _ptr(seq_lens_hint), batch, _ptr(norm_weight),
         float(eps), _ptr(freqs), freqs.shape[0], _ptr(out_loc), dtype_code(kv_cache.dtype), _ptr(kv_cache),
         kv_cache.shape[0], _ptr(status), _stream(stream)), "ckv_compress_decode_norm_rope_store")
+
+
+# ------------------------------------------------------------------------------ 8-bit paged cache
+class Q8CacheArg(ctypes.Structure):
+    """ckv_q8_cache_t."""
+    _fields_ = [("k", ctypes.c_void_p), ("k_scale", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("num_blocks", ctypes.c_uint32), ("block_tokens", ctypes.c_uint32),
+                ("n_kv_heads", ctypes.c_uint32), ("head_dim", ctypes.c_uint32)]
+
+
+class Q8Cache(NamedTuple):
+    """A paged cache in 8 bits: ``k`` (and ``v``) ``[num_blocks, n_kv_heads, block_tokens, head_dim]``
+    float8_e4m3fn, ``k_scale`` (and ``v_scale``) fp32 ``[num_blocks, n_kv_heads]``; the value held is
+    ``k * k_scale``.  Without ``v`` the entries are keys and values at once (a latent cache)."""
+    k: torch.Tensor
+    k_scale: torch.Tensor
+    v: Optional[torch.Tensor] = None
+    v_scale: Optional[torch.Tensor] = None
+
+
+def new_q8_cache(num_blocks: int, n_kv_heads: int, block_tokens: int, head_dim: int, latent: bool = False,
+                 device=None) -> Q8Cache:
+    """An empty cache (zeros, scales 1); ``latent``: no separate values."""
+    dev = device or "cuda"
+
+    def side():
+        pool = torch.zeros(num_blocks, n_kv_heads, block_tokens, head_dim, dtype=torch.uint8, device=dev)
+        return pool.view(torch.float8_e4m3fn), torch.ones(num_blocks, n_kv_heads, device=dev)
+
+    k, ks = side()
+    v, vs = (None, None) if latent else side()
+    return Q8Cache(k, ks, v, vs)
+
+
+def _q8(cache: Q8Cache) -> Q8CacheArg:
+    k, ks, v, vs = cache
+    shape = k.shape
+    if k.dtype != torch.float8_e4m3fn or len(shape) != 4:
+        raise ValueError("a q8 cache's k is float8_e4m3fn [num_blocks, n_kv_heads, block_tokens, head_dim]")
+    if ks.dtype != torch.float32 or ks.shape != shape[:2]:
+        raise ValueError("a q8 cache's scales are fp32 [num_blocks, n_kv_heads]")
+    if (v is None) != (vs is None):
+        raise ValueError("v and v_scale go together")
+    if v is not None and (v.dtype != k.dtype or v.shape != shape or vs.dtype != torch.float32 or
+                          vs.shape != shape[:2]):
+        raise ValueError("a q8 cache's v and v_scale are shaped like its k and k_scale")
+    ptrs = _ptr(k), _ptr(ks), _ptr(v), _ptr(vs)
+    if k.device.index != torch.cuda.current_device():
+        raise ValueError("the q8 cache is not on the current device")
+    return Q8CacheArg(*ptrs, shape[0], shape[2], shape[1], shape[3])
+
+
+def _on(device, *ts: Optional[torch.Tensor]) -> None:
+    for t in ts:
+        if t is not None and t.device != device:
+            raise ValueError("tensors are on different devices")
+
+
+def _table(table: torch.Tensor):
+    """(pointer, stride, rows) of a block table ``[num_reqs, blocks]`` int32."""
+    if table.dtype != torch.int32 or table.dim() != 2:
+        raise ValueError("a block table is int32 [num_reqs, blocks]")
+    return _ptr(table), table.shape[1], table.shape[0]
+
+
+def _shaped(t: Optional[torch.Tensor], what: str, dtype: torch.dtype, *shape: int) -> None:
+    if t is not None and (t.dtype != dtype or t.shape != shape):
+        raise ValueError(f"{what} must be {dtype} {list(shape)} (got {t.dtype} {list(t.shape)})")
+
+
+def capacity_q8_store(batch: int, num_rows: int, block_tokens: int) -> int:
+    return int(load_library().ckv_capacity_q8_store(batch, num_rows, block_tokens))
+
+
+def plan_q8_store(cache: Q8Cache, rid: torch.Tensor, kv_lens: torch.Tensor, new_lens: torch.Tensor, num_rows: int,
+                  block_table: torch.Tensor, capacity: Optional[int] = None, pad_invalid: bool = False,
+                  plan: Optional[torch.Tensor] = None, counts: Optional[torch.Tensor] = None,
+                  status: Optional[torch.Tensor] = None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """The blocks that a step's new rows touch: ``(plan [cap, 16] u8, counts [4] int32)``.  ``kv_lens`` counts the
+    new entries (``new_lens``, 0 allowed); the plan serves every layer of the step."""
+    arg, batch = _q8(cache), _lengths(rid, kv_lens, new_lens)
+    _on(cache.k.device, rid, kv_lens, new_lens, block_table, plan, counts, status)
+    if capacity is None:
+        capacity = capacity_q8_store(batch, num_rows, arg.block_tokens)
+    if plan is None:
+        plan = torch.empty(max(capacity, 1), 16, dtype=torch.uint8, device=rid.device)
+    elif plan.dtype != torch.uint8 or plan.dim() != 2 or plan.shape[1] != 16 or plan.shape[0] < capacity:
+        raise ValueError("a store plan is a uint8 tensor [capacity, 16]")
+    if counts is None:
+        counts = torch.empty(4, dtype=torch.int32, device=rid.device)
+    _shaped(counts, "counts", torch.int32, 4)
+    _check(load_library().ckv_plan_q8_store(arg, _ptr(rid), _ptr(kv_lens), _ptr(new_lens), batch, num_rows,
+                                            *_table(block_table), capacity, int(pad_invalid), _ptr(plan),
+                                            _ptr(counts), _ptr(status), _stream(stream)), "ckv_plan_q8_store")
+    return plan[:capacity], counts
+
+
+def q8_store(cache: Q8Cache, k_rows: torch.Tensor, v_rows: Optional[torch.Tensor], plan: torch.Tensor,
+             counts: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Quantises rows ``[num_rows, n_kv_heads, head_dim]`` into the cache; ``v_rows`` is None for a latent cache."""
+    arg = _q8(cache)
+    _on(cache.k.device, k_rows, v_rows, plan, counts, status)
+    shape = (k_rows.shape[0], arg.n_kv_heads, arg.head_dim)
+    _shaped(k_rows, "k_rows", k_rows.dtype, *shape)
+    _shaped(v_rows, "v_rows", k_rows.dtype, *shape)
+    if (v_rows is None) != (cache.v is None):
+        raise ValueError("v_rows go with a cache that has v")
+    if plan.dtype != torch.uint8 or plan.dim() != 2 or plan.shape[1] != 16:
+        raise ValueError("a store plan is a uint8 tensor [capacity, 16]")
+    _shaped(counts, "counts", torch.int32, 4)
+    _check(load_library().ckv_q8_store(arg, dtype_code(k_rows.dtype), _ptr(k_rows), _ptr(v_rows), shape[0],
+                                       _ptr(plan), _ptr(counts), plan.shape[0], _ptr(status), _stream(stream)),
+           "ckv_q8_store")
+
+
+class Q8AttnPlan(NamedTuple):
+    """What ``plan_q8_attn`` made (device memory) and the shape it holds for."""
+    buffer: torch.Tensor
+    n_heads: int
+    ratio: int
+    batch: int
+    num_q: int
+
+
+def plan_q8_attn(cache: Q8Cache, n_heads: int, ratio: int, rid: torch.Tensor, seq_lens: torch.Tensor,
+                 extend_lens: torch.Tensor, kv_lens: torch.Tensor, num_q: int, buffer: Optional[torch.Tensor] = None,
+                 status: Optional[torch.Tensor] = None, stream=None) -> Q8AttnPlan:
+    """Shares a step's attention out over the SMs.  Request b's ``extend_lens[b]`` queries are the last tokens of
+    ``seq_lens[b]``; it has ``kv_lens[b]`` entries of ``ratio`` tokens each.  Serves every layer of the step."""
+    arg, batch = _q8(cache), _lengths(rid, seq_lens, extend_lens, kv_lens)
+    _on(cache.k.device, rid, seq_lens, extend_lens, kv_lens, buffer, status)
+    lib = load_library()
+    if buffer is None:
+        buffer = torch.empty(max(lib.ckv_q8_attn_plan_bytes(arg, n_heads, batch, num_q), 16), dtype=torch.uint8,
+                             device=rid.device)
+    elif buffer.dtype != torch.uint8:
+        raise ValueError("a plan buffer is a uint8 tensor")
+    _check(lib.ckv_plan_q8_attn(arg, n_heads, ratio, _ptr(rid), _ptr(seq_lens), _ptr(extend_lens), _ptr(kv_lens),
+                                batch, num_q, _ptr(buffer), buffer.numel(), _ptr(status), _stream(stream)),
+           "ckv_plan_q8_attn")
+    return Q8AttnPlan(buffer, n_heads, ratio, batch, num_q)
+
+
+def q8_attn_workspace(cache: Q8Cache, n_heads: int, batch: int, num_q: int) -> torch.Tensor:
+    """Workspace for ``q8_attn`` calls of this shape; calls that may run at the same time need one each."""
+    n = load_library().ckv_q8_attn_workspace_bytes(_q8(cache), n_heads, batch, num_q)
+    return torch.empty(max(n, 16), dtype=torch.uint8, device=cache.k.device)
+
+
+def q8_attn(cache: Q8Cache, q: torch.Tensor, plan: Q8AttnPlan, block_table: torch.Tensor, scale: float,
+            out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+            out_dtype: torch.dtype = torch.bfloat16, workspace: Optional[torch.Tensor] = None,
+            status: Optional[torch.Tensor] = None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Softmax attention of ``q`` (bf16 ``[num_q, n_heads, head_dim]``) over the cache: ``(out, lse)``, ``lse`` fp32
+    ``[num_q, n_heads]``.  Queries that see nothing get zeros and -inf."""
+    arg = _q8(cache)
+    _on(cache.k.device, q, plan.buffer, block_table, out, lse, workspace, status)
+    shape = (plan.num_q, plan.n_heads, arg.head_dim)
+    _shaped(q, "q", torch.bfloat16, *shape)
+    if out is None:
+        out = torch.empty(shape, dtype=out_dtype, device=q.device)
+    _shaped(out, "out", out.dtype, *shape)
+    if lse is None:
+        lse = torch.empty(shape[:2], dtype=torch.float32, device=q.device)
+    _shaped(lse, "lse", torch.float32, *shape[:2])
+    lib = load_library()
+    if workspace is None:
+        need = lib.ckv_q8_attn_workspace_bytes(arg, plan.n_heads, plan.batch, plan.num_q)
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+    elif workspace.dtype != torch.uint8:
+        raise ValueError("a workspace is a uint8 tensor")
+    _check(lib.ckv_q8_attn(arg, plan.n_heads, plan.ratio, float(scale), _ptr(q), plan.batch, plan.num_q,
+                           *_table(block_table), _ptr(plan.buffer), plan.buffer.numel(), dtype_code(out.dtype),
+                           _ptr(out), _ptr(lse), _ptr(workspace), workspace.numel(), _ptr(status), _stream(stream)),
+           "ckv_q8_attn")
+    return out, lse
+
+
+def q8_weigh(cache: Q8Cache, q: torch.Tensor, lse: torch.Tensor, weights: torch.Tensor, ratio: int,
+             rid: torch.Tensor, seq_lens: torch.Tensor, extend_lens: torch.Tensor, kv_lens: torch.Tensor,
+             block_table: torch.Tensor, scale: float, decay: float = 1.0, status: Optional[torch.Tensor] = None,
+             stream=None) -> torch.Tensor:
+    """``weights[slot] = decay * weights[slot] +`` the softmax weight that the step's queries gave the entry, over all
+    heads; ``weights`` fp32 ``[num_blocks, block_tokens]``, ``lse`` as ``q8_attn`` returned it."""
+    arg, batch = _q8(cache), _lengths(rid, seq_lens, extend_lens, kv_lens)
+    _on(cache.k.device, q, lse, weights, rid, seq_lens, extend_lens, kv_lens, block_table, status)
+    if q.dim() != 3:
+        raise ValueError("q is bf16 [num_q, n_heads, head_dim]")
+    num_q, n_heads = q.shape[0], q.shape[1]
+    _shaped(q, "q", torch.bfloat16, num_q, n_heads, arg.head_dim)
+    _shaped(lse, "lse", torch.float32, num_q, n_heads)
+    _shaped(weights, "weights", torch.float32, arg.num_blocks, arg.block_tokens)
+    _check(load_library().ckv_q8_weigh(arg, n_heads, ratio, float(scale), float(decay), _ptr(q), _ptr(lse), num_q,
+                                       _ptr(rid), _ptr(seq_lens), _ptr(extend_lens), _ptr(kv_lens), batch,
+                                       *_table(block_table), _ptr(weights), _ptr(status), _stream(stream)),
+           "ckv_q8_weigh")
+    return weights
+
+
+def q8_evict(cache: Q8Cache, weights: torch.Tensor, rid: torch.Tensor, kv_lens: torch.Tensor,
+             block_table: torch.Tensor, dst_table: torch.Tensor, budget: int, sinks: int = 0, recent: int = 0,
+             kept: Optional[torch.Tensor] = None, new_lens: Optional[torch.Tensor] = None,
+             status: Optional[torch.Tensor] = None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Keeps each request's ``budget`` entries of largest weight, its first ``sinks`` and newest ``recent`` among
+    them, and moves them (with their weights) into the blocks of ``dst_table``, which must be no source's.  Returns
+    ``(kept [batch, budget] int32 old positions, -1 past the end, new_lens [batch] int64)``."""
+    arg, batch = _q8(cache), _lengths(rid, kv_lens)
+    _on(cache.k.device, weights, rid, kv_lens, block_table, dst_table, kept, new_lens, status)
+    if min(budget, sinks, recent) < 0:
+        raise ValueError("budget, sinks and recent are counts")
+    _shaped(weights, "weights", torch.float32, arg.num_blocks, arg.block_tokens)
+    src, stride, reqs = _table(block_table)
+    dst, dst_stride, dst_reqs = _table(dst_table)
+    if dst_reqs != reqs:
+        raise ValueError("block_table and dst_table have a row for each request")
+    if kept is None:
+        kept = torch.empty(batch, budget, dtype=torch.int32, device=rid.device)
+    _shaped(kept, "kept", torch.int32, batch, budget)
+    if new_lens is None:
+        new_lens = torch.empty(batch, dtype=torch.int64, device=rid.device)
+    _shaped(new_lens, "new_lens", torch.int64, batch)
+    _check(load_library().ckv_q8_evict(arg, _ptr(weights), _ptr(rid), _ptr(kv_lens), batch, src, stride, dst,
+                                       dst_stride, reqs, budget, sinks, recent, _ptr(kept), _ptr(new_lens),
+                                       _ptr(status), _stream(stream)), "ckv_q8_evict")
+    return kept, new_lens
 
 
 # ------------------------------------------------------------------------------ convenience

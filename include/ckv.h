@@ -460,12 +460,140 @@ int ckv_compress_decode_norm_rope_store(int ratio, int head_dim, int rope_dim, i
                                         int cache_dtype, void* kv_cache, uint64_t cache_rows, uint32_t* d_status,
                                         ckv_stream_t stream);
 
+/* ------------------------------------------------------ 8-bit paged cache */
+/* A cache of compressed (or plain) entries held in 8 bits, the attention that
+ * reads it, the attention weight each entry received, and eviction by that
+ * weight.  The pages name an fp8 store after norm + RoPE without showing it;
+ * this cache and its operators are this library's own.
+ *
+ * Layout.  k and v are pools [num_blocks, n_kv_heads, block_tokens, head_dim]
+ * of e4m3 values, k_scale and v_scale fp32 [num_blocks, n_kv_heads]; the value
+ * held is e4m3 * scale.  v == NULL (with v_scale == NULL) makes a latent cache:
+ * the entries are keys and values at once, as the compressed rows are.
+ * Entry p of request rid is slot p % block_tokens of block
+ * block_table[rid * table_stride + p / block_tokens] (int32, [num_reqs,
+ * table_stride]; unused places may hold anything).  block_tokens is 16, 32, 64
+ * or 128, head_dim 64, 128, 256 or 512, n_kv_heads 1 .. CKV_Q8_MAX_KV_HEADS.
+ * The struct is host memory, read during the call only.
+ *
+ * Scales are powers of two between 2^-48 and 2^48: the smallest with which a
+ * block's largest finite value fits e4m3 (448 * scale); larger values and
+ * infinities are stored as +-448 * scale, NaN as NaN. */
+typedef struct ckv_q8_cache {
+  void* k;
+  float* k_scale;
+  void* v;
+  float* v_scale;
+  uint32_t num_blocks;
+  uint32_t block_tokens;
+  uint32_t n_kv_heads;
+  uint32_t head_dim;
+} ckv_q8_cache_t;
+
+enum { CKV_Q8_MAX_KV_HEADS = 256, CKV_Q8_MAX_GROUP = 256 };
+
+/* One block that a step's new rows touch (16 bytes): input rows row .. row +
+ * count - 1 go to slots slot .. of the block; slot_count = slot | count << 16.
+ * Invalid = all bytes 0xFF. */
+typedef struct ckv_q8_store_plan {
+  int32_t block;
+  uint32_t row;
+  uint32_t slot_count;
+  uint32_t reserved;
+} ckv_q8_store_plan_t;
+
+/* Records that ckv_plan_q8_store writes at most. */
+uint32_t ckv_capacity_q8_store(uint32_t batch, uint32_t num_rows, uint32_t block_tokens);
+
+/* Store plan: request b appends new_lens[b] >= 0 rows, the next ones of the
+ * ragged input, as its entries kv_lens[b] - new_lens[b] .. kv_lens[b] - 1 (kv_lens
+ * counts the new ones).  rid, kv_lens, new_lens: int64 [batch], batch <=
+ * 1024; sum(new_lens) = num_rows.  plan[capacity] in batch and position
+ * order; d_counts[4] = {records, sum(new_lens), 0, 0} (16-byte aligned).  A bad
+ * length, or a kv_len past the table, sets CKV_STATUS_BAD_LENGTH and drops the
+ * request; a block number outside the pool sets CKV_STATUS_BAD_INDEX and makes
+ * its record invalid.  pad_invalid fills [records, capacity).  One plan
+ * serves every layer of a step. */
+int ckv_plan_q8_store(const ckv_q8_cache_t* cache, const int64_t* rid, const int64_t* kv_lens,
+                      const int64_t* new_lens, uint32_t batch, uint32_t num_rows, const int32_t* block_table,
+                      uint64_t table_stride, uint32_t num_reqs, uint32_t capacity, int pad_invalid,
+                      ckv_q8_store_plan_t* plan, uint32_t* d_counts, uint32_t* d_status, ckv_stream_t stream);
+
+/* Quantising store of the rows k_rows (and v_rows: NULL for a latent cache)
+ * [num_rows, n_kv_heads, head_dim] (in_dtype).  A block that starts with the
+ * step's rows gets its scale from them; one that earlier rows began keeps the
+ * larger of its scale and theirs, and when that grows the earlier entries are
+ * rewritten with it (exact, but for e4m3's subnormals).  Slots after the
+ * stored rows are left as they were.  No two records may name one block. */
+int ckv_q8_store(const ckv_q8_cache_t* cache, int in_dtype, const void* k_rows, const void* v_rows, uint32_t num_rows,
+                 const ckv_q8_store_plan_t* plan, const uint32_t* d_counts, uint32_t capacity, uint32_t* d_status,
+                 ckv_stream_t stream);
+
+/* Attention plan: shares the step's work out evenly over the SMs.  Request b
+ * has extend_lens[b] >= 0 queries (the next ones of the ragged num_q), the
+ * last tokens of its seq_lens[b], and kv_lens[b] cached entries of `ratio` tokens each
+ * (1 .. 65536; 1: an entry per token).  A query at 0-based position t sees the first
+ *     kv_len - (floor(seq_len / ratio) - floor((t + 1) / ratio))
+ * entries: those complete when it was the newest token (ratio 1: causal), counted
+ * back from the newest, so evicting older ones changes nothing.  plan is
+ * ckv_q8_attn_plan_bytes (0: bad sizes) of device memory; it holds for every
+ * layer of the step whose n_heads and cache shape are these. */
+uint64_t ckv_q8_attn_plan_bytes(const ckv_q8_cache_t* cache, uint32_t n_heads, uint32_t batch, uint32_t num_q);
+
+int ckv_plan_q8_attn(const ckv_q8_cache_t* cache, uint32_t n_heads, uint32_t ratio, const int64_t* rid,
+                     const int64_t* seq_lens, const int64_t* extend_lens, const int64_t* kv_lens, uint32_t batch,
+                     uint32_t num_q, void* plan, uint64_t plan_bytes, uint32_t* d_status, ckv_stream_t stream);
+
+/* Softmax attention over the cache: q is bf16 [num_q, n_heads, head_dim], query
+ * heads h * group .. h * group + group - 1 read kv head h (group = n_heads /
+ * n_kv_heads, at most CKV_Q8_MAX_GROUP), scores are scale * <q, k> (scale > 0).
+ * out [num_q, n_heads, head_dim] in out_dtype; lse (NULL: not wanted) fp32
+ * [num_q, n_heads] is log(sum(exp(score))).  A query that sees nothing gets
+ * zeros and lse -infinity.  Entries a query does not see, and slots past a request's
+ * end, do not count whatever they hold, NaN included.  Weights are rounded to
+ * fp16 (2^-12 relative) before they meet the values; everything else is exact
+ * or fp32.  workspace: ckv_q8_attn_workspace_bytes of device memory that no
+ * other call uses meanwhile (calls on one stream may share it); its content does not
+ * matter.  A block number outside the pool sets CKV_STATUS_BAD_INDEX and its
+ * entries do not count; a plan that does not fit the call sets it too. */
+uint64_t ckv_q8_attn_workspace_bytes(const ckv_q8_cache_t* cache, uint32_t n_heads, uint32_t batch, uint32_t num_q);
+
+int ckv_q8_attn(const ckv_q8_cache_t* cache, uint32_t n_heads, uint32_t ratio, float scale, const void* q,
+                uint32_t batch, uint32_t num_q, const int32_t* block_table, uint64_t table_stride, uint32_t num_reqs,
+                const void* plan, uint64_t plan_bytes, int out_dtype, void* out, float* lse, void* workspace,
+                uint64_t workspace_bytes, uint32_t* d_status, ckv_stream_t stream);
+
+/* Accumulated attention weight: for every entry of the requests that have
+ * queries, weights[slot] = decay * weights[slot] + the sum over the step's
+ * queries and heads of the softmax weight it received (0 <= decay <= 1; 0
+ * overwrites).  weights is fp32 [num_blocks, block_tokens]; q, ratio, scale and
+ * the lengths as in the attention, lse its output.  Deterministic.  Two
+ * requests that share a block must not both be in the batch. */
+int ckv_q8_weigh(const ckv_q8_cache_t* cache, uint32_t n_heads, uint32_t ratio, float scale, float decay,
+                 const void* q, const float* lse, uint32_t num_q, const int64_t* rid, const int64_t* seq_lens,
+                 const int64_t* extend_lens, const int64_t* kv_lens, uint32_t batch, const int32_t* block_table,
+                 uint64_t table_stride, uint32_t num_reqs, float* weights, uint32_t* d_status, ckv_stream_t stream);
+
+/* Eviction: a request with more than budget entries keeps its first `sinks`,
+ * its newest `recent` (sinks + recent <= budget) and, of the others, those of
+ * largest weight (equal weights: the lower position; NaN counts as the
+ * least), budget in all; one with fewer keeps all.  Kept entries move, in
+ * order, with their weights, into the blocks dst_table[rid * dst_stride + ...],
+ * whose scales become the largest of their sources'; the sources are left as they were and
+ * may be shared.  No block of dst_table may be a source, or be named twice.
+ * kept: int32 [batch, budget], the old position of each kept entry, -1 past
+ * the end; new_lens: int64 [batch]. */
+int ckv_q8_evict(const ckv_q8_cache_t* cache, float* weights, const int64_t* rid, const int64_t* kv_lens,
+                 uint32_t batch, const int32_t* block_table, uint64_t table_stride, const int32_t* dst_table,
+                 uint64_t dst_stride, uint32_t num_reqs, uint32_t budget, uint32_t sinks, uint32_t recent,
+                 int32_t* kept, int64_t* new_lens, uint32_t* d_status, ckv_stream_t stream);
+
 /* ------------------------------------------------------------------ misc */
 /* Short text for a CKV_OK / CKV_ERR_* code (static storage). */
 const char* ckv_error_string(int code);
-/* Library ABI version: major * 100 + minor (220: 2.00's decode boundary-row
- * list and prefetch hints, 2.10's prefill prefetch hints, and the fused C4
- * decode + norm + RoPE + store). */
+/* Library ABI version: major * 100 + minor (230: 2.00's decode boundary-row
+ * list and prefetch hints, 2.10's prefill prefetch hints, 2.20's fused C4
+ * decode + norm + RoPE + store, and the 8-bit paged cache). */
 int ckv_version(void);
 
 #ifdef __cplusplus
