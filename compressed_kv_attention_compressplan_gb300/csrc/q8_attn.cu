@@ -18,7 +18,7 @@
 // Precision.  k8 and v8 are exact in fp16.  A query row is scaled by a power of
 // two that puts its largest value in [2^14, 2^15), then rounded to fp16: exact for
 // bf16 input down to 2^-28 of that value.  Products accumulate in fp32; the
-// weights' rounding to fp16 (2^-12 relative) is the one rounding that costs
+// weights' rounding to fp16 (2^-11 relative) is the one rounding that costs
 // anything, and is below the bf16 output's.
 #include <algorithm>
 
