@@ -551,40 +551,91 @@ def new_q8_cache(num_blocks: int, n_kv_heads: int, block_tokens: int, head_dim: 
     return Q8Cache(k, ks, v, vs)
 
 
-def _q8(cache: Q8Cache) -> Q8CacheArg:
+# These calls are made once a layer on few microseconds of work, so what they check is checked in few Python steps:
+# a tensor's address is taken, with the checks that make it usable, by _at(); lengths by _lens().
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _at(device: int, t: Optional[torch.Tensor]) -> Optional[int]:
+    """The address of a contiguous tensor on the given CUDA device."""
+    if t is None:
+        return None
+    if t.get_device() != device:
+        raise ValueError("libckv takes CUDA tensors of one device only")
+    if not t.is_contiguous():
+        raise ValueError("libckv takes contiguous tensors only")
+    return t.data_ptr()
+
+
+def _stream_of(device: int, stream):
+    if stream is not None:
+        return stream.cuda_stream
+    return _raw_stream(device) if _raw_stream is not None else torch.cuda.current_stream(device).cuda_stream
+
+
+def _lens(device: int, *ts: torch.Tensor):
+    """The batch and the addresses of per-request arrays: int64, one dimension, one length."""
+    shape, at = ts[0].shape, []
+    for t in ts:
+        if t.dtype is not torch.int64 or t.shape != shape:
+            _lengths(*ts)
+        at.append(_at(device, t))
+    if len(shape) != 1:
+        _lengths(*ts)
+    return shape[0], at
+
+
+def _q8(cache: Q8Cache) -> Tuple[Q8CacheArg, int]:
+    """ckv_q8_cache_t, and the device: the cache's, which must be the current one."""
     k, ks, v, vs = cache
     shape = k.shape
-    if k.dtype != torch.float8_e4m3fn or len(shape) != 4:
+    if k.dtype is not torch.float8_e4m3fn or len(shape) != 4:
         raise ValueError("a q8 cache's k is float8_e4m3fn [num_blocks, n_kv_heads, block_tokens, head_dim]")
-    if ks.dtype != torch.float32 or ks.shape != shape[:2]:
+    if ks.dtype is not torch.float32 or ks.shape != shape[:2]:
         raise ValueError("a q8 cache's scales are fp32 [num_blocks, n_kv_heads]")
-    if (v is None) != (vs is None):
-        raise ValueError("v and v_scale go together")
-    if v is not None and (v.dtype != k.dtype or v.shape != shape or vs.dtype != torch.float32 or
-                          vs.shape != shape[:2]):
-        raise ValueError("a q8 cache's v and v_scale are shaped like its k and k_scale")
-    ptrs = _ptr(k), _ptr(ks), _ptr(v), _ptr(vs)
-    if k.device.index != torch.cuda.current_device():
+    device = k.get_device()
+    if device < 0:
+        raise ValueError("libckv takes CUDA tensors only")
+    v_at = vs_at = None
+    if v is not None or vs is not None:
+        if v is None or vs is None:
+            raise ValueError("v and v_scale go together")
+        if (v.dtype is not torch.float8_e4m3fn or v.shape != shape or vs.dtype is not torch.float32 or
+                vs.shape != ks.shape):
+            raise ValueError("a q8 cache's v and v_scale are shaped like its k and k_scale")
+        v_at, vs_at = _at(device, v), _at(device, vs)
+    arg = Q8CacheArg(_at(device, k), _at(device, ks), v_at, vs_at, shape[0], shape[2], shape[1], shape[3])
+    if device != torch._C._cuda_getDevice():
         raise ValueError("the q8 cache is not on the current device")
-    return Q8CacheArg(*ptrs, shape[0], shape[2], shape[1], shape[3])
+    return arg, device
 
 
-def _on(device, *ts: Optional[torch.Tensor]) -> None:
-    for t in ts:
-        if t is not None and t.device != device:
-            raise ValueError("tensors are on different devices")
-
-
-def _table(table: torch.Tensor):
-    """(pointer, stride, rows) of a block table ``[num_reqs, blocks]`` int32."""
-    if table.dtype != torch.int32 or table.dim() != 2:
+def _table(device: int, table: torch.Tensor):
+    """(address, stride, rows) of a block table ``[num_reqs, blocks]`` int32."""
+    shape = table.shape
+    if table.dtype is not torch.int32 or len(shape) != 2:
         raise ValueError("a block table is int32 [num_reqs, blocks]")
-    return _ptr(table), table.shape[1], table.shape[0]
+    return _at(device, table), shape[1], shape[0]
 
 
-def _shaped(t: Optional[torch.Tensor], what: str, dtype: torch.dtype, *shape: int) -> None:
-    if t is not None and (t.dtype != dtype or t.shape != shape):
+def _is(t: torch.Tensor, what: str, dtype: torch.dtype, *shape: int) -> None:
+    if t.dtype is not dtype or t.shape != shape:
         raise ValueError(f"{what} must be {dtype} {list(shape)} (got {t.dtype} {list(t.shape)})")
+
+
+def _bytes_of(t: torch.Tensor, what: str) -> int:
+    if t.dtype is not torch.uint8:
+        raise ValueError(f"{what} is a uint8 tensor")
+    return t.numel()
+
+
+def _store_plan(plan: torch.Tensor, capacity: int) -> None:
+    if plan.dtype is not torch.uint8 or plan.dim() != 2 or plan.shape[1] != 16 or plan.shape[0] < capacity:
+        raise ValueError("a store plan is a uint8 tensor [capacity, 16]")
+
+
+def _q8_error(rc: int, func: str):
+    raise CkvError(rc, func, load_library().ckv_error_string(rc).decode())
 
 
 def capacity_q8_store(batch: int, num_rows: int, block_tokens: int) -> int:
@@ -597,39 +648,44 @@ def plan_q8_store(cache: Q8Cache, rid: torch.Tensor, kv_lens: torch.Tensor, new_
                   status: Optional[torch.Tensor] = None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
     """The blocks that a step's new rows touch: ``(plan [cap, 16] u8, counts [4] int32)``.  ``kv_lens`` counts the
     new entries (``new_lens``, 0 allowed); the plan serves every layer of the step."""
-    arg, batch = _q8(cache), _lengths(rid, kv_lens, new_lens)
-    _on(cache.k.device, rid, kv_lens, new_lens, block_table, plan, counts, status)
+    lib = _lib or load_library()
+    arg, dev = _q8(cache)
+    batch, (rid_at, kv_at, new_at) = _lens(dev, rid, kv_lens, new_lens)
     if capacity is None:
-        capacity = capacity_q8_store(batch, num_rows, arg.block_tokens)
+        capacity = lib.ckv_capacity_q8_store(batch, num_rows, arg.block_tokens)
     if plan is None:
-        plan = torch.empty(max(capacity, 1), 16, dtype=torch.uint8, device=rid.device)
-    elif plan.dtype != torch.uint8 or plan.dim() != 2 or plan.shape[1] != 16 or plan.shape[0] < capacity:
-        raise ValueError("a store plan is a uint8 tensor [capacity, 16]")
+        plan = torch.empty((capacity, 16), dtype=torch.uint8, device=rid.device)
+    _store_plan(plan, capacity)
     if counts is None:
         counts = torch.empty(4, dtype=torch.int32, device=rid.device)
-    _shaped(counts, "counts", torch.int32, 4)
-    _check(load_library().ckv_plan_q8_store(arg, _ptr(rid), _ptr(kv_lens), _ptr(new_lens), batch, num_rows,
-                                            *_table(block_table), capacity, int(pad_invalid), _ptr(plan),
-                                            _ptr(counts), _ptr(status), _stream(stream)), "ckv_plan_q8_store")
-    return plan[:capacity], counts
+    _is(counts, "counts", torch.int32, 4)
+    table, stride, reqs = _table(dev, block_table)
+    rc = lib.ckv_plan_q8_store(arg, rid_at, kv_at, new_at, batch, num_rows, table, stride, reqs, capacity,
+                               int(pad_invalid), _at(dev, plan), _at(dev, counts), _at(dev, status),
+                               _stream_of(dev, stream))
+    if rc:
+        _q8_error(rc, "ckv_plan_q8_store")
+    return (plan if plan.shape[0] == capacity else plan[:capacity]), counts
 
 
 def q8_store(cache: Q8Cache, k_rows: torch.Tensor, v_rows: Optional[torch.Tensor], plan: torch.Tensor,
              counts: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None, stream=None) -> None:
     """Quantises rows ``[num_rows, n_kv_heads, head_dim]`` into the cache; ``v_rows`` is None for a latent cache."""
-    arg = _q8(cache)
-    _on(cache.k.device, k_rows, v_rows, plan, counts, status)
-    shape = (k_rows.shape[0], arg.n_kv_heads, arg.head_dim)
-    _shaped(k_rows, "k_rows", k_rows.dtype, *shape)
-    _shaped(v_rows, "v_rows", k_rows.dtype, *shape)
+    lib = _lib or load_library()
+    arg, dev = _q8(cache)
+    n = k_rows.shape[0]
+    _is(k_rows, "k_rows", k_rows.dtype, n, arg.n_kv_heads, arg.head_dim)
     if (v_rows is None) != (cache.v is None):
         raise ValueError("v_rows go with a cache that has v")
-    if plan.dtype != torch.uint8 or plan.dim() != 2 or plan.shape[1] != 16:
-        raise ValueError("a store plan is a uint8 tensor [capacity, 16]")
-    _shaped(counts, "counts", torch.int32, 4)
-    _check(load_library().ckv_q8_store(arg, dtype_code(k_rows.dtype), _ptr(k_rows), _ptr(v_rows), shape[0],
-                                       _ptr(plan), _ptr(counts), plan.shape[0], _ptr(status), _stream(stream)),
-           "ckv_q8_store")
+    if v_rows is not None:
+        _is(v_rows, "v_rows", k_rows.dtype, n, arg.n_kv_heads, arg.head_dim)
+    _store_plan(plan, 0)
+    if counts is not None:
+        _is(counts, "counts", torch.int32, 4)
+    rc = lib.ckv_q8_store(arg, dtype_code(k_rows.dtype), _at(dev, k_rows), _at(dev, v_rows), n, _at(dev, plan),
+                          _at(dev, counts), plan.shape[0], _at(dev, status), _stream_of(dev, stream))
+    if rc:
+        _q8_error(rc, "ckv_q8_store")
 
 
 class Q8AttnPlan(NamedTuple):
@@ -646,23 +702,22 @@ def plan_q8_attn(cache: Q8Cache, n_heads: int, ratio: int, rid: torch.Tensor, se
                  status: Optional[torch.Tensor] = None, stream=None) -> Q8AttnPlan:
     """Shares a step's attention out over the SMs.  Request b's ``extend_lens[b]`` queries are the last tokens of
     ``seq_lens[b]``; it has ``kv_lens[b]`` entries of ``ratio`` tokens each.  Serves every layer of the step."""
-    arg, batch = _q8(cache), _lengths(rid, seq_lens, extend_lens, kv_lens)
-    _on(cache.k.device, rid, seq_lens, extend_lens, kv_lens, buffer, status)
-    lib = load_library()
+    lib = _lib or load_library()
+    arg, dev = _q8(cache)
+    batch, (rid_at, seq_at, ext_at, kv_at) = _lens(dev, rid, seq_lens, extend_lens, kv_lens)
     if buffer is None:
         buffer = torch.empty(max(lib.ckv_q8_attn_plan_bytes(arg, n_heads, batch, num_q), 16), dtype=torch.uint8,
                              device=rid.device)
-    elif buffer.dtype != torch.uint8:
-        raise ValueError("a plan buffer is a uint8 tensor")
-    _check(lib.ckv_plan_q8_attn(arg, n_heads, ratio, _ptr(rid), _ptr(seq_lens), _ptr(extend_lens), _ptr(kv_lens),
-                                batch, num_q, _ptr(buffer), buffer.numel(), _ptr(status), _stream(stream)),
-           "ckv_plan_q8_attn")
+    rc = lib.ckv_plan_q8_attn(arg, n_heads, ratio, rid_at, seq_at, ext_at, kv_at, batch, num_q, _at(dev, buffer),
+                              _bytes_of(buffer, "a plan buffer"), _at(dev, status), _stream_of(dev, stream))
+    if rc:
+        _q8_error(rc, "ckv_plan_q8_attn")
     return Q8AttnPlan(buffer, n_heads, ratio, batch, num_q)
 
 
 def q8_attn_workspace(cache: Q8Cache, n_heads: int, batch: int, num_q: int) -> torch.Tensor:
     """Workspace for ``q8_attn`` calls of this shape; calls that may run at the same time need one each."""
-    n = load_library().ckv_q8_attn_workspace_bytes(_q8(cache), n_heads, batch, num_q)
+    n = load_library().ckv_q8_attn_workspace_bytes(_q8(cache)[0], n_heads, batch, num_q)
     return torch.empty(max(n, 16), dtype=torch.uint8, device=cache.k.device)
 
 
@@ -672,26 +727,28 @@ def q8_attn(cache: Q8Cache, q: torch.Tensor, plan: Q8AttnPlan, block_table: torc
             status: Optional[torch.Tensor] = None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
     """Softmax attention of ``q`` (bf16 ``[num_q, n_heads, head_dim]``) over the cache: ``(out, lse)``, ``lse`` fp32
     ``[num_q, n_heads]``.  Queries that see nothing get zeros and -inf."""
-    arg = _q8(cache)
-    _on(cache.k.device, q, plan.buffer, block_table, out, lse, workspace, status)
-    shape = (plan.num_q, plan.n_heads, arg.head_dim)
-    _shaped(q, "q", torch.bfloat16, *shape)
+    lib = _lib or load_library()
+    arg, dev = _q8(cache)
+    buffer, n_heads, ratio, batch, num_q = plan
+    _is(q, "q", torch.bfloat16, num_q, n_heads, arg.head_dim)
     if out is None:
-        out = torch.empty(shape, dtype=out_dtype, device=q.device)
-    _shaped(out, "out", out.dtype, *shape)
+        out = torch.empty(q.shape, dtype=out_dtype, device=q.device)
+    else:
+        _is(out, "out", out.dtype, num_q, n_heads, arg.head_dim)
     if lse is None:
-        lse = torch.empty(shape[:2], dtype=torch.float32, device=q.device)
-    _shaped(lse, "lse", torch.float32, *shape[:2])
-    lib = load_library()
+        lse = torch.empty((num_q, n_heads), dtype=torch.float32, device=q.device)
+    else:
+        _is(lse, "lse", torch.float32, num_q, n_heads)
     if workspace is None:
-        need = lib.ckv_q8_attn_workspace_bytes(arg, plan.n_heads, plan.batch, plan.num_q)
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
-    elif workspace.dtype != torch.uint8:
-        raise ValueError("a workspace is a uint8 tensor")
-    _check(lib.ckv_q8_attn(arg, plan.n_heads, plan.ratio, float(scale), _ptr(q), plan.batch, plan.num_q,
-                           *_table(block_table), _ptr(plan.buffer), plan.buffer.numel(), dtype_code(out.dtype),
-                           _ptr(out), _ptr(lse), _ptr(workspace), workspace.numel(), _ptr(status), _stream(stream)),
-           "ckv_q8_attn")
+        workspace = torch.empty(max(lib.ckv_q8_attn_workspace_bytes(arg, n_heads, batch, num_q), 16),
+                                dtype=torch.uint8, device=q.device)
+    table, stride, reqs = _table(dev, block_table)
+    rc = lib.ckv_q8_attn(arg, n_heads, ratio, scale, _at(dev, q), batch, num_q, table, stride, reqs,
+                         _at(dev, buffer), buffer.numel(), dtype_code(out.dtype), _at(dev, out), _at(dev, lse),
+                         _at(dev, workspace), _bytes_of(workspace, "a workspace"), _at(dev, status),
+                         _stream_of(dev, stream))
+    if rc:
+        _q8_error(rc, "ckv_q8_attn")
     return out, lse
 
 
@@ -701,18 +758,21 @@ def q8_weigh(cache: Q8Cache, q: torch.Tensor, lse: torch.Tensor, weights: torch.
              stream=None) -> torch.Tensor:
     """``weights[slot] = decay * weights[slot] +`` the softmax weight that the step's queries gave the entry, over all
     heads; ``weights`` fp32 ``[num_blocks, block_tokens]``, ``lse`` as ``q8_attn`` returned it."""
-    arg, batch = _q8(cache), _lengths(rid, seq_lens, extend_lens, kv_lens)
-    _on(cache.k.device, q, lse, weights, rid, seq_lens, extend_lens, kv_lens, block_table, status)
+    lib = _lib or load_library()
+    arg, dev = _q8(cache)
+    batch, (rid_at, seq_at, ext_at, kv_at) = _lens(dev, rid, seq_lens, extend_lens, kv_lens)
     if q.dim() != 3:
         raise ValueError("q is bf16 [num_q, n_heads, head_dim]")
-    num_q, n_heads = q.shape[0], q.shape[1]
-    _shaped(q, "q", torch.bfloat16, num_q, n_heads, arg.head_dim)
-    _shaped(lse, "lse", torch.float32, num_q, n_heads)
-    _shaped(weights, "weights", torch.float32, arg.num_blocks, arg.block_tokens)
-    _check(load_library().ckv_q8_weigh(arg, n_heads, ratio, float(scale), float(decay), _ptr(q), _ptr(lse), num_q,
-                                       _ptr(rid), _ptr(seq_lens), _ptr(extend_lens), _ptr(kv_lens), batch,
-                                       *_table(block_table), _ptr(weights), _ptr(status), _stream(stream)),
-           "ckv_q8_weigh")
+    num_q, n_heads, _ = q.shape
+    _is(q, "q", torch.bfloat16, num_q, n_heads, arg.head_dim)
+    _is(lse, "lse", torch.float32, num_q, n_heads)
+    _is(weights, "weights", torch.float32, arg.num_blocks, arg.block_tokens)
+    table, stride, reqs = _table(dev, block_table)
+    rc = lib.ckv_q8_weigh(arg, n_heads, ratio, scale, decay, _at(dev, q), _at(dev, lse), num_q, rid_at, seq_at, ext_at,
+                          kv_at, batch, table, stride, reqs, _at(dev, weights), _at(dev, status),
+                          _stream_of(dev, stream))
+    if rc:
+        _q8_error(rc, "ckv_q8_weigh")
     return weights
 
 
@@ -723,24 +783,29 @@ def q8_evict(cache: Q8Cache, weights: torch.Tensor, rid: torch.Tensor, kv_lens: 
     """Keeps each request's ``budget`` entries of largest weight, its first ``sinks`` and newest ``recent`` among
     them, and moves them (with their weights) into the blocks of ``dst_table``, which must be no source's.  Returns
     ``(kept [batch, budget] int32 old positions, -1 past the end, new_lens [batch] int64)``."""
-    arg, batch = _q8(cache), _lengths(rid, kv_lens)
-    _on(cache.k.device, weights, rid, kv_lens, block_table, dst_table, kept, new_lens, status)
-    if min(budget, sinks, recent) < 0:
+    lib = _lib or load_library()
+    arg, dev = _q8(cache)
+    batch, (rid_at, kv_at) = _lens(dev, rid, kv_lens)
+    if budget < 0 or sinks < 0 or recent < 0:
         raise ValueError("budget, sinks and recent are counts")
-    _shaped(weights, "weights", torch.float32, arg.num_blocks, arg.block_tokens)
-    src, stride, reqs = _table(block_table)
-    dst, dst_stride, dst_reqs = _table(dst_table)
+    _is(weights, "weights", torch.float32, arg.num_blocks, arg.block_tokens)
+    src, stride, reqs = _table(dev, block_table)
+    dst, dst_stride, dst_reqs = _table(dev, dst_table)
     if dst_reqs != reqs:
         raise ValueError("block_table and dst_table have a row for each request")
     if kept is None:
-        kept = torch.empty(batch, budget, dtype=torch.int32, device=rid.device)
-    _shaped(kept, "kept", torch.int32, batch, budget)
+        kept = torch.empty((batch, budget), dtype=torch.int32, device=rid.device)
+    else:
+        _is(kept, "kept", torch.int32, batch, budget)
     if new_lens is None:
         new_lens = torch.empty(batch, dtype=torch.int64, device=rid.device)
-    _shaped(new_lens, "new_lens", torch.int64, batch)
-    _check(load_library().ckv_q8_evict(arg, _ptr(weights), _ptr(rid), _ptr(kv_lens), batch, src, stride, dst,
-                                       dst_stride, reqs, budget, sinks, recent, _ptr(kept), _ptr(new_lens),
-                                       _ptr(status), _stream(stream)), "ckv_q8_evict")
+    else:
+        _is(new_lens, "new_lens", torch.int64, batch)
+    rc = lib.ckv_q8_evict(arg, _at(dev, weights), rid_at, kv_at, batch, src, stride, dst, dst_stride, reqs, budget,
+                          sinks, recent, _at(dev, kept), _at(dev, new_lens), _at(dev, status),
+                          _stream_of(dev, stream))
+    if rc:
+        _q8_error(rc, "ckv_q8_evict")
     return kept, new_lens
 
 
