@@ -101,8 +101,9 @@ __global__ __launch_bounds__(kPlanThreads) void plan_q8_attn_kernel(const AttnPl
         min(s_ql[*b] - 1, static_cast<uint32_t>((static_cast<unsigned long long>(j + 1) * M - 1) / G));
     return static_cast<uint32_t>(q8_visible(s_kv[*b], s_ql[*b] - 1 - last, s_ph[*b], a.ratio));
   };
-  auto cost_of = [](uint32_t seen) -> unsigned long long {
-    return kQ8StartCost + ((static_cast<unsigned long long>(seen) + 15) & ~15ull);
+  const uint32_t start = a.g.start_cost, grain = a.g.grain;
+  auto cost_of = [&](uint32_t seen) -> unsigned long long {
+    return start + (static_cast<unsigned long long>(seen) + grain - 1) / grain * grain;
   };
   unsigned long long mine = 0;
   for (uint32_t i = t; i < nt; i += kPlanThreads) {
@@ -152,8 +153,8 @@ __global__ __launch_bounds__(kPlanThreads) void plan_q8_attn_kernel(const AttnPl
       r.q_start = s_qs[rb];
       r.q_len = s_ql[rb];
       r.row0 = (i0 + s - s_tile[rb]) * M;
-      r.kv_begin = o0 > kQ8StartCost ? static_cast<uint32_t>(o0 - kQ8StartCost) : 0;
-      r.kv_end = o1 > kQ8StartCost ? min(seen, static_cast<uint32_t>(o1 - kQ8StartCost)) : 0;
+      r.kv_begin = o0 > start ? static_cast<uint32_t>(o0 - start) : 0;
+      r.kv_end = o1 > start ? min(seen, static_cast<uint32_t>(o1 - start)) : 0;
       r.kv_len = s_kv[rb];
       r.phase = s_ph[rb];
       r.part = static_cast<int32_t>(s_part[s]);
@@ -219,10 +220,22 @@ int q8_attn_geom(const Q8Cache& c, uint32_t batch, uint32_t num_q, uint32_t n_he
   if (n_heads == 0 || n_heads % c.heads != 0 || n_heads / c.heads > CKV_Q8_MAX_GROUP) return CKV_ERR_SIZE;
   g->group = n_heads / c.heads;
   if (static_cast<uint64_t>(num_q) * g->group > 0x7FFFFFFFull) return CKV_ERR_SIZE;  // row numbers are 32-bit
-  g->rows = 16;
-  g->ctas = std::max<uint32_t>(1, static_cast<uint32_t>(sm_count()) * per_sm_of(c.head_dim) / c.heads);
-  g->min_quota = 128;
-  g->round = 64;
+  // The split kernel's tiles are 16 rows; the tensor-core kernel's are 128 (64 from 256 channels on), and separate keys
+  // and values of 512 channels do not fit its shared memory.
+  g->tc = batch > 0 && static_cast<uint64_t>(num_q) * g->group >= 48ull * batch && (c.head_dim < 512 || c.v == nullptr);
+  if (g->tc) {
+    g->rows = c.head_dim <= 128 ? 128 : 64;
+    g->ctas = std::max<uint32_t>(1, static_cast<uint32_t>(sm_count()) / c.heads);
+    g->start_cost = g->grain = g->round = 128;
+    g->min_quota = 256;
+  } else {
+    g->rows = 16;
+    g->ctas = std::max<uint32_t>(1, static_cast<uint32_t>(sm_count()) * per_sm_of(c.head_dim) / c.heads);
+    g->start_cost = 32;
+    g->grain = 16;
+    g->round = 64;
+    g->min_quota = 128;
+  }
   const uint64_t tiles = static_cast<uint64_t>(num_q) * g->group / g->rows + batch;
   const uint64_t items = tiles + g->ctas;
   g->cap_items = static_cast<uint32_t>(items);
@@ -239,48 +252,11 @@ int q8_attn_geom(const Q8Cache& c, uint32_t batch, uint32_t num_q, uint32_t n_he
 namespace {
 
 // ----------------------------------------------------------------- attention
-struct AttnArgs {
-  Q8Cache c;
-  Q8Geom g;
-  const __nv_bfloat16* q;
-  uint32_t num_q;
-  uint32_t n_heads;
-  uint32_t ratio;
-  float scale_log2;
-  const int32_t* table;
-  uint32_t stride;
-  uint32_t num_reqs;
-  const uint8_t* plan;
-  int out_f32;
-  void* out;
-  float* lse;
-  float* part_o;    // [part][kv head][row][head_dim]
-  float2* part_ml;  // [part][kv head][row]
-  uint32_t* d_status;
-};
-
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-  const __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-
-__device__ __forceinline__ bool item_fits(const Q8Item& item, const AttnArgs& a) {
-  return item.rid < a.num_reqs && static_cast<uint64_t>(item.q_start) + item.q_len <= a.num_q &&
-         item.row0 < static_cast<uint64_t>(item.q_len) * a.g.group &&
-         item.kv_len <= static_cast<uint64_t>(a.stride) * a.c.block_tokens && item.kv_end <= item.kv_len &&
-         (item.part < 0 || (static_cast<uint64_t>(item.part) + item.chunks <= a.g.cap_parts && item.chunk < item.chunks));
-}
-
-__device__ __forceinline__ bool plan_fits(const Q8Header* h, const AttnArgs& a) {
-  return h->rows == a.g.rows && h->group == a.g.group && h->num_q == a.num_q && h->ratio == a.ratio &&
-         h->cap_ctas == a.g.ctas;
 }
 
 // Byte offset of 16-byte chunk cc of token t in a tile of kDw-byte rows.  The
@@ -295,17 +271,6 @@ __device__ __forceinline__ uint32_t tile_off(uint32_t t, uint32_t cc) {
   }
   const uint32_t line = t * (kDw / 128) + (cc >> 3);
   return line * 128 + (((cc & 7) ^ (t & 7)) << 4);
-}
-
-// Takes the NaNs out of a word of four channels of entry e, noting the first entry with one for each channel.
-__device__ __forceinline__ uint32_t without_nan(uint32_t w, int e, int* s_nan, int* s_any_nan) {
-  const uint32_t bad = q8_nan_bytes(w);
-  if (bad) {
-    for (int z = 0; z < 4; ++z)
-      if (bad >> (8 * z) & 1) atomicMin(s_nan + z, e);
-    *s_any_nan = 1;
-  }
-  return w & ~bad;
 }
 
 // Fragments.  A warp's 16 rows are the MMA's m, 16 entries its n (scores) and k
@@ -325,7 +290,7 @@ __global__ __launch_bounds__(kAttnThreads, (Cfg<kDw, kNp, kShared>::kPerSm)) voi
   constexpr int kOt = kDw / 8;       // output column tiles
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float s_m[C::kGroups][16], s_l[C::kGroups][16];
-  __shared__ float s_x[kNp == 2 ? C::kGroups : 1][2][2][kNp == 2 ? 256 : 1];  // partial scores of a row's two warps
+  __shared__ __align__(16) float s_x[kNp == 2 ? C::kGroups : 1][2][2][kNp == 2 ? 256 : 1];  // partial scores of a row's two warps
   __shared__ int s_nan[C::kD];  // first entry with a NaN value, by channel
   __shared__ int s_any_nan;
 
@@ -677,8 +642,8 @@ __global__ __launch_bounds__(kAttnThreads, (Cfg<kDw, kNp, kShared>::kPerSm)) voi
 }
 
 // ------------------------------------------------------------------- combine
-// One CTA per (split tile, kv head, row): the row's parts joined in their
-// order.  A row reads chunks * (head_dim + 2) floats, at most a few hundred KB
+// A CTA takes a (split tile, kv head, row) at a time: the row's parts joined in
+// their order.  A row reads chunks * (head_dim + 2) floats, at most a few hundred KB
 // in all, so what counts is that the rows spread over the SMs.
 constexpr int kCombineThreads = 128;
 constexpr int kMaxParts = 2048;
@@ -692,71 +657,77 @@ __global__ __launch_bounds__(kCombineThreads) void q8_combine_kernel(const AttnA
   pdl_wait();
   pdl_release();
   const Q8Header* head = reinterpret_cast<const Q8Header*>(a.plan);
-  if (!plan_fits(head, a) || blockIdx.x >= head->splits) return;
-  const uint32_t first = reinterpret_cast<const uint32_t*>(a.plan + a.g.off_split)[blockIdx.x];
-  if (first >= a.g.cap_items) return;
-  const Q8Item item = reinterpret_cast<const Q8Item*>(a.plan + a.g.off_items)[first];
-  const uint32_t G = a.g.group, H = a.c.heads, h = blockIdx.y, row = blockIdx.z, M = a.g.rows;
-  if (!item_fits(item, a) || item.part < 0 || item.chunks > kMaxParts ||
-      static_cast<uint64_t>(item.row0) + row >= static_cast<uint64_t>(item.q_len) * G)
-    return;
+  if (!plan_fits(head, a)) return;
+  const uint32_t G = a.g.group, H = a.c.heads, M = a.g.rows;
+  const uint32_t* splits = reinterpret_cast<const uint32_t*>(a.plan + a.g.off_split);
+  const Q8Item* items = reinterpret_cast<const Q8Item*>(a.plan + a.g.off_items);
+  const uint32_t work = min(head->splits, a.g.ctas) * H * M;
   const int tid = threadIdx.x;
-  const size_t r0 = (static_cast<size_t>(item.part) * H + h) * M + row, step = static_cast<size_t>(H) * M;
-  float top = -3.4e38f;
-  for (uint32_t p = tid; p < item.chunks; p += kCombineThreads) top = fmaxf(top, a.part_ml[r0 + p * step].x);
+  for (uint32_t x = blockIdx.x; x < work; x += gridDim.x) {
+    const uint32_t row = x % M, h = x / M % H, first = splits[x / M / H];
+    if (first >= a.g.cap_items) continue;
+    const Q8Item item = items[first];
+    if (!item_fits(item, a) || item.part < 0 || item.chunks > kMaxParts ||
+        static_cast<uint64_t>(item.row0) + row >= static_cast<uint64_t>(item.q_len) * G)
+      continue;
+    const size_t r0 = (static_cast<size_t>(item.part) * H + h) * M + row, step = static_cast<size_t>(H) * M;
+    __syncthreads();  // the previous row's reads of shared memory are done
+    float top = -3.4e38f;
+    for (uint32_t p = tid; p < item.chunks; p += kCombineThreads) top = fmaxf(top, a.part_ml[r0 + p * step].x);
 #pragma unroll
-  for (int s = 16; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, s));
-  if ((tid & 31) == 0) s_red[tid >> 5] = top;
-  __syncthreads();
+    for (int s = 16; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, s));
+    if ((tid & 31) == 0) s_red[tid >> 5] = top;
+    __syncthreads();
 #pragma unroll
-  for (int w = 0; w < kCombineThreads / 32; ++w) top = fmaxf(top, s_red[w]);
-  __syncthreads();
-  float sum = 0.0f;
-  for (uint32_t p = tid; p < item.chunks; p += kCombineThreads) {
-    const float2 ml = a.part_ml[r0 + p * step];
-    const float w = ex2(ml.x - top);
-    s_w[p] = w;
-    sum = fmaf(ml.y, w, sum);
-  }
-#pragma unroll
-  for (int s = 16; s > 0; s >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, s);
-  if ((tid & 31) == 0) s_red[tid >> 5] = sum;
-  __syncthreads();
-  sum = 0.0f;
-#pragma unroll
-  for (int w = 0; w < kCombineThreads / 32; ++w) sum += s_red[w];
-
-  const int ch = (tid % kLanes) * 4;
-  float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-  for (uint32_t p = tid / kLanes; p < item.chunks; p += kSplit) {
-    const float4 x = *reinterpret_cast<const float4*>(a.part_o + (r0 + p * step) * kD + ch);
-    const float w = s_w[p];
-    v.x = fmaf(x.x, w, v.x);
-    v.y = fmaf(x.y, w, v.y);
-    v.z = fmaf(x.z, w, v.z);
-    v.w = fmaf(x.w, w, v.w);
-  }
-  s_o[tid] = v;
-  __syncthreads();
-  if (tid < kLanes) {
-    for (int k = 1; k < kSplit; ++k) {
-      const float4 x = s_o[tid + k * kLanes];
-      v.x += x.x;
-      v.y += x.y;
-      v.z += x.z;
-      v.w += x.w;
+    for (int w = 0; w < kCombineThreads / 32; ++w) top = fmaxf(top, s_red[w]);
+    __syncthreads();
+    float sum = 0.0f;
+    for (uint32_t p = tid; p < item.chunks; p += kCombineThreads) {
+      const float2 ml = a.part_ml[r0 + p * step];
+      const float w = ex2(ml.x - top);
+      s_w[p] = w;
+      sum = fmaf(ml.y, w, sum);
     }
-    const float inv = sum == 0.0f ? 0.0f : __fdiv_rn(1.0f, sum);
-    const uint32_t rho = item.row0 + row, i = rho / G, hg = rho % G;
-    const size_t out_row = static_cast<size_t>(item.q_start + i) * a.n_heads + h * G + hg;
-    const float r[4] = {v.x * inv, v.y * inv, v.z * inv, v.w * inv};
-    if (a.out_f32)
-      store_row_chunk<float, 4>(static_cast<float*>(a.out) + out_row * kD + ch, r);
-    else
-      store_row_chunk<__nv_bfloat16, 4>(static_cast<__nv_bfloat16*>(a.out) + out_row * kD + ch, r);
-    if (tid == 0 && a.lse != nullptr)
-      a.lse[out_row] = sum == 0.0f ? -INFINITY : (top + __log2f(sum)) * 0.69314718055994530942f;
+#pragma unroll
+    for (int s = 16; s > 0; s >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, s);
+    if ((tid & 31) == 0) s_red[tid >> 5] = sum;
+    __syncthreads();
+    sum = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kCombineThreads / 32; ++w) sum += s_red[w];
+
+    const int ch = (tid % kLanes) * 4;
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+    for (uint32_t p = tid / kLanes; p < item.chunks; p += kSplit) {
+      const float4 o = *reinterpret_cast<const float4*>(a.part_o + (r0 + p * step) * kD + ch);
+      const float w = s_w[p];
+      v.x = fmaf(o.x, w, v.x);
+      v.y = fmaf(o.y, w, v.y);
+      v.z = fmaf(o.z, w, v.z);
+      v.w = fmaf(o.w, w, v.w);
+    }
+    s_o[tid] = v;
+    __syncthreads();
+    if (tid < kLanes) {
+      for (int k = 1; k < kSplit; ++k) {
+        const float4 o = s_o[tid + k * kLanes];
+        v.x += o.x;
+        v.y += o.y;
+        v.z += o.z;
+        v.w += o.w;
+      }
+      const float inv = sum == 0.0f ? 0.0f : __fdiv_rn(1.0f, sum);
+      const uint32_t rho = item.row0 + row, i = rho / G, hg = rho % G;
+      const size_t out_row = static_cast<size_t>(item.q_start + i) * a.n_heads + h * G + hg;
+      const float r[4] = {v.x * inv, v.y * inv, v.z * inv, v.w * inv};
+      if (a.out_f32)
+        store_row_chunk<float, 4>(static_cast<float*>(a.out) + out_row * kD + ch, r);
+      else
+        store_row_chunk<__nv_bfloat16, 4>(static_cast<__nv_bfloat16*>(a.out) + out_row * kD + ch, r);
+      if (tid == 0 && a.lse != nullptr)
+        a.lse[out_row] = sum == 0.0f ? -INFINITY : (top + __log2f(sum)) * 0.69314718055994530942f;
+    }
   }
 }
 
@@ -768,9 +739,29 @@ int launch_attn(const AttnArgs& a, cudaStream_t s) {
     cudaGetLastError();
     return CKV_ERR_LAUNCH;
   }
-  const int rc = launch_pdl(kernel, dim3(a.g.ctas, a.c.heads), dim3(kAttnThreads), C::kSmem, s, a);
-  if (rc) return rc;
-  return launch_pdl(q8_combine_kernel<C::kD>, dim3(a.g.ctas, a.c.heads, a.g.rows), dim3(kCombineThreads), 0, s, a);
+  return launch_pdl(kernel, dim3(a.g.ctas, a.c.heads), dim3(kAttnThreads), C::kSmem, s, a);
+}
+
+int launch_split(const AttnArgs& a, cudaStream_t s) {
+  const bool shared = a.c.v == nullptr;
+  switch (a.c.head_dim) {
+    case 64: return shared ? launch_attn<64, 1, true>(a, s) : launch_attn<64, 1, false>(a, s);
+    case 128: return shared ? launch_attn<128, 1, true>(a, s) : launch_attn<128, 1, false>(a, s);
+    case 256: return shared ? launch_attn<256, 1, true>(a, s) : launch_attn<256, 1, false>(a, s);
+    default: return shared ? launch_attn<256, 2, true>(a, s) : launch_attn<256, 2, false>(a, s);
+  }
+}
+
+int launch_combine(const AttnArgs& a, cudaStream_t s) {
+  // at most eight CTAs to an SM; they walk the rows
+  const uint64_t rows = static_cast<uint64_t>(a.g.ctas) * a.c.heads * a.g.rows;
+  const dim3 grid(static_cast<uint32_t>(std::min<uint64_t>(rows, 8ull * sm_count())));
+  switch (a.c.head_dim) {
+    case 64: return launch_pdl(q8_combine_kernel<64>, grid, dim3(kCombineThreads), 0, s, a);
+    case 128: return launch_pdl(q8_combine_kernel<128>, grid, dim3(kCombineThreads), 0, s, a);
+    case 256: return launch_pdl(q8_combine_kernel<256>, grid, dim3(kCombineThreads), 0, s, a);
+    default: return launch_pdl(q8_combine_kernel<512>, grid, dim3(kCombineThreads), 0, s, a);
+  }
 }
 
 }  // namespace
@@ -855,14 +846,10 @@ int ckv_q8_attn(const ckv_q8_cache_t* cache, uint32_t n_heads, uint32_t ratio, f
   a.part_o = static_cast<float*>(workspace);
   a.part_ml = reinterpret_cast<float2*>(a.part_o + static_cast<size_t>(a.g.cap_parts) * a.c.heads * a.g.rows * a.c.head_dim);
   a.d_status = d_status;
+  a.wait_ns = wait_limit_ns();
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const bool shared = a.c.v == nullptr;
-  switch (a.c.head_dim) {
-    case 64: return shared ? launch_attn<64, 1, true>(a, s) : launch_attn<64, 1, false>(a, s);
-    case 128: return shared ? launch_attn<128, 1, true>(a, s) : launch_attn<128, 1, false>(a, s);
-    case 256: return shared ? launch_attn<256, 1, true>(a, s) : launch_attn<256, 1, false>(a, s);
-    default: return shared ? launch_attn<256, 2, true>(a, s) : launch_attn<256, 2, false>(a, s);
-  }
+  rc = a.g.tc ? launch_q8_attn_tc(a, s) : launch_split(a, s);
+  return rc ? rc : launch_combine(a, s);
 }
 
 }  // extern "C"

@@ -1,0 +1,584 @@
+// q8_attn_tc.cu -- attention over the 8-bit paged cache on the 5th-generation
+// tensor cores, for tiles of many rows: prefill chunks, and decode where many
+// heads share one latent cache.  The mathematics is the split kernel's.
+//
+// Transposed products.  A tile is 128 entries, the M of both products:
+//     S^T [128 entries x N rows] = K8 Q^T,   O^T [128 channels x N rows] += V8^T W^T,
+// one O^T per 128 channels.  With entries on the lanes of tensor memory and rows
+// on its columns, a thread owns one entry: the entry's scales are two registers
+// of its own, row sums stay in registers until the end, and no score crosses
+// lanes but in the rare step that raises a row's reference (one vote a tile asks
+// for it).  The accumulator of 512 channels by 64 rows takes 256 columns, so
+// the whole width of a latent entry fits beside the scores; the weights W^T go
+// through shared memory as they stand, an entry's row of N weights being the
+// swizzled row that the second product reads.
+//
+// Roles.  Converting warps load e4m3 from memory into registers, a few slices of
+// 64 channels ahead, and store them as fp16 (exact) in the operands' swizzled
+// layout; one thread issues the products; groups of four warps take 32 rows
+// each through the softmax.  K and V have buffers of their own, two each where
+// they fit, so the products of a tile overlap the softmax of the one before; in a latent
+// cache one buffer is both operands, and its slices are handed back as the
+// second product finishes with them.
+//
+// Bound.  Shared memory feeds everything: for 128 channels and 128 rows a tile
+// writes 96 KB and the products read 128 KB, about 1.8 k cycles at 128 bytes a
+// cycle, where the products alone are 1.0 k.
+#include <algorithm>
+
+#include "async_copy.cuh"
+#include "q8_plan.cuh"
+#include "tcgen05.cuh"
+
+namespace ckv {
+namespace {
+
+constexpr int kEntries = 128;
+constexpr uint32_t kSlice = kEntries * 128;  // bytes of 64 channels of a tile in fp16
+
+template <int kD, bool kShared>
+struct TcCfg {
+  static constexpr int kRows = kD <= 128 ? 128 : 64;
+  static constexpr int kSlices = kD / 64;
+  static constexpr int kBlocks = kD <= 128 ? 1 : kD / 128;  // accumulators of 128 channels
+  static constexpr int kStages = kShared ? (kD <= 256 ? 2 : 1) : (kD <= 128 ? 2 : 1);
+  static constexpr bool kLag = kStages == 2 || !kShared;  // the second product runs a tile behind the first
+  static constexpr int kFree = kShared ? kBlocks : 1;     // barriers that hand a K stage back
+  static constexpr int kGroups = kRows / 32;              // softmax groups of four warps
+  static constexpr int kSoftWarps = 4 * kGroups;
+  static constexpr int kConvWarps = 4;
+  static constexpr int kWarps = kSoftWarps + kConvWarps + 1;
+  static constexpr int kThreads = 32 * kWarps;
+  static constexpr int kLoads = kEntries / (8 * kConvWarps);  // 16-byte loads of a converting thread per slice
+  static constexpr int kUnits = kSlices * (kShared ? 1 : 2);  // slices of a tile, K's and V's
+  static constexpr int kAhead = kUnits < 2 ? 1 : kD <= 128 ? 2 : 4;
+  static constexpr uint32_t kQBytes = kSlices * kRows * 128;
+  static constexpr uint32_t kKBytes = kStages * kSlices * kSlice;
+  static constexpr uint32_t kVBytes = kShared ? 0 : kKBytes;
+  static constexpr uint32_t kPBytes = kRows / 64 * kSlice;
+  static constexpr uint32_t kBytes = kQBytes + kKBytes + kVBytes + kPBytes + 1024;  // and the alignment
+  // one CTA to an SM: a second would wait for the first one's tensor memory
+  static constexpr uint32_t kSmem = kBytes < 120 * 1024 ? 120 * 1024 : kBytes;
+  static constexpr uint32_t kOCol = 2 * kRows;  // scores: two buffers, then the accumulators
+  static constexpr uint32_t kCols = kOCol + kBlocks * kRows <= 256 ? 256 : 512;
+  static_assert(kOCol + kBlocks * kRows <= 512, "");
+};
+
+template <int kD, bool kShared>
+struct alignas(16) TcShared {
+  using C = TcCfg<kD, kShared>;
+  uint64_t k_full[C::kStages][C::kSlices], k_free[C::kStages][C::kFree];
+  uint64_t v_full[C::kStages][C::kSlices], v_free[C::kStages];
+  uint64_t s_full[2], s_free[2], p_full, pv_done, idle;
+  alignas(16) float rf[C::kRows];  // read four at a time
+  alignas(16) float m[C::kRows];
+  float fac[C::kRows];
+  int vis[C::kRows];
+  size_t out_row[C::kRows];
+  float red[4][C::kRows];
+  int nan[kShared ? 1 : kD];  // first entry with a NaN (a latent cache: in any channel, else by channel)
+  int any_nan;
+  uint32_t tmem;
+};
+
+// A wait that, once it has run out, lets the rest of the loop run without waiting: every barrier is
+// still reached, the kernel ends, and the status says so.
+struct Waiter {
+  uint64_t limit;
+  bool live;
+  template <bool kShort>
+  __device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity) {
+    if (live) live = warp_wait_for<kShort>(smem_addr(bar), parity, limit);
+  }
+};
+
+__device__ __forceinline__ bool group_any(int id, bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %2, 0;\n\t"
+      "bar.red.or.pred q, %1, 128, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(id), "r"(x ? 1u : 0u)
+      : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ void group_sync(int id) { asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory"); }
+
+template <int kD, bool kShared, bool kShort>
+__global__ __launch_bounds__((TcCfg<kD, kShared>::kThreads), 1) void q8_attn_tc_kernel(const AttnArgs a) {
+  using C = TcCfg<kD, kShared>;
+  constexpr int kN = C::kRows;
+  extern __shared__ uint8_t raw[];
+  __shared__ TcShared<kD, kShared> sh;
+  pdl_wait();
+  pdl_release();
+  const Q8Header* head = reinterpret_cast<const Q8Header*>(a.plan);
+  const uint32_t h = blockIdx.y;
+  if (!plan_fits(head, a)) {
+    if (blockIdx.x == 0 && h == 0 && threadIdx.x == 0) status_or(a.d_status, CKV_STATUS_BAD_INDEX);
+    return;
+  }
+  if (blockIdx.x >= head->ctas) return;
+  const uint32_t* first = reinterpret_cast<const uint32_t*>(a.plan + a.g.off_first);
+  const Q8Item* items = reinterpret_cast<const Q8Item*>(a.plan + a.g.off_items);
+  const uint32_t item0 = first[blockIdx.x], item1 = min(first[blockIdx.x + 1], a.g.cap_items);
+
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t G = a.g.group, H = a.c.heads, T = a.c.block_tokens;
+  const uint32_t base = (smem_addr(raw) + 1023) & ~1023u;
+  const uint32_t q_at = base, k_at = q_at + C::kQBytes, v_at = kShared ? k_at : k_at + C::kKBytes;
+  const uint32_t p_at = k_at + C::kKBytes + C::kVBytes;
+  const bool conv = warp >= C::kSoftWarps && warp < C::kSoftWarps + C::kConvWarps;
+  const bool soft = warp < C::kSoftWarps;
+
+  if (warp == C::kWarps - 1) tmem_alloc(smem_addr(&sh.tmem), C::kCols);
+  if (tid == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      for (int x = 0; x < C::kSlices; ++x) {
+        mbar_init(smem_addr(&sh.k_full[s][x]), C::kConvWarps);
+        mbar_init(smem_addr(&sh.v_full[s][x]), C::kConvWarps);
+      }
+      for (int x = 0; x < C::kFree; ++x) mbar_init(smem_addr(&sh.k_free[s][x]), 1);
+      mbar_init(smem_addr(&sh.v_free[s]), 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(smem_addr(&sh.s_full[s]), 1);
+      mbar_init(smem_addr(&sh.s_free[s]), C::kSoftWarps);
+    }
+    mbar_init(smem_addr(&sh.p_full), C::kSoftWarps);
+    mbar_init(smem_addr(&sh.pv_done), 1);
+    mbar_init(smem_addr(&sh.idle), 1);
+    fence_mbar_init();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+  Waiter w{a.wait_ns, true};
+  uint32_t tiles_before = 0;  // tiles of earlier items: the barriers' phases go on
+
+  for (uint32_t it = item0; it < item1; ++it) {
+    const Q8Item item = items[it];
+    if (!item_fits(item, a)) {
+      if (tid == 0) status_or(a.d_status, CKV_STATUS_BAD_INDEX);
+      continue;
+    }
+    const uint32_t rows = min(static_cast<uint32_t>(kN), item.q_len * G - item.row0);
+    const int32_t* table = a.table + static_cast<size_t>(item.rid) * a.stride;
+    const uint32_t n_tiles =
+        item.kv_end > item.kv_begin ? (item.kv_end - item.kv_begin + kEntries - 1) / kEntries : 0;
+    const uint32_t vis_min = min(item.kv_end, static_cast<uint32_t>(q8_visible(item.kv_len, item.q_len - 1 - item.row0 / G,
+                                                                             item.phase, a.ratio)));
+    // ---- the rows: query operand, scaling, visibility
+    for (int n = warp; n < kN; n += C::kWarps) {
+      constexpr int kPer = kD / 32;  // consecutive channels of a lane
+      const bool in = static_cast<uint32_t>(n) < rows;
+      const uint32_t rho = item.row0 + (in ? n : 0), i = rho / G, hg = rho % G;
+      const size_t row = static_cast<size_t>(item.q_start + i) * a.n_heads + h * G + hg;
+      const uint32_t* p = reinterpret_cast<const uint32_t*>(a.q + row * kD + lane * kPer);
+      uint32_t x[kPer / 2];
+      float m = 0.0f;
+#pragma unroll
+      for (int e = 0; e < kPer / 2; ++e) {
+        x[e] = in ? __ldg(p + e) : 0u;
+        m = fmaxf(m, fmaxf(fabsf(bf16lo(x[e])), fabsf(bf16hi(x[e]))));
+      }
+#pragma unroll
+      for (int s = 16; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, s));
+      const int ex = min(126, 14 - (static_cast<int>(__float_as_uint(m) >> 23) - 127));
+      const float up = pow2f(ex);
+#pragma unroll
+      for (int e = 0; e < kPer / 2; ++e) {
+        const uint32_t c = lane * kPer + 2 * e;
+        sts_u32(q_at + (c >> 6) * (kN * 128) + n * 128 + ((((c & 63) >> 3) ^ (n & 7)) << 4) + (c & 7) * 2,
+                pack_f16x2(bf16lo(x[e]) * up, bf16hi(x[e]) * up));
+      }
+      if (lane == 0) {
+        sh.rf[n] = pow2f(-ex) * a.scale_log2;
+        sh.m[n] = -3.4e38f;
+        sh.vis[n] = in ? static_cast<int>(q8_visible(item.kv_len, item.q_len - 1 - i, item.phase, a.ratio)) : 0x7FFFFFFF;
+        sh.out_row[n] = row;
+      }
+    }
+    for (int c = tid; c < (kShared ? 1 : kD); c += C::kThreads) sh.nan[c] = 0x7FFFFFFF;
+    if (tid == 0) sh.any_nan = 0;
+    fence_async_smem();
+    __syncthreads();
+
+    if (conv) {
+      // ---- e4m3 -> fp16 operands.  Lane l takes 16 channels, chunk l % 4 of a slice, of entries l / 4 + 8 * ...: the
+      // eight lanes of a store's phase take two entries, whose chunks the swizzle puts in different banks.
+      const int cw = warp - C::kSoftWarps, q = lane & 3;
+      uint32_t tok[C::kLoads];
+      size_t off[C::kLoads], off_next[C::kLoads];
+      uint32_t here = 0, here_next = 0;  // bit i: load i's entry exists
+      bool bad = false;
+#pragma unroll
+      for (int i = 0; i < C::kLoads; ++i) tok[i] = i * (8 * C::kConvWarps) + cw * 8 + (lane >> 2);
+      auto locate = [&](uint32_t tile, size_t(&o)[C::kLoads]) -> uint32_t {
+        uint32_t mask = 0;
+#pragma unroll
+        for (int i = 0; i < C::kLoads; ++i) {
+          const uint32_t e = item.kv_begin + tile * kEntries + tok[i];
+          o[i] = 0;
+          if (tile < n_tiles && e < item.kv_end) {
+            const int32_t b = __ldg(table + e / T);
+            if (b >= 0 && static_cast<uint32_t>(b) < a.c.num_blocks) {
+              o[i] = ((static_cast<size_t>(b) * H + h) * T + e % T) * kD + q * 16;
+              mask |= 1u << i;
+            } else {
+              bad = true;
+            }
+          }
+        }
+        return mask;
+      };
+      uint4 buf[C::kAhead][C::kLoads];
+      auto load = [&](uint4(&d)[C::kLoads], int unit, const size_t(&o)[C::kLoads], uint32_t mask) {
+        const uint8_t* pool = unit < C::kSlices ? a.c.k : a.c.v;
+        const int s = unit % C::kSlices;
+#pragma unroll
+        for (int i = 0; i < C::kLoads; ++i)
+          d[i] = mask >> i & 1 ? ld_stream16(pool + o[i] + s * 64) : make_uint4(0, 0, 0, 0);
+      };
+      here = locate(0, off);
+#pragma unroll
+      for (int u = 0; u < C::kAhead; ++u) load(buf[u], u, off, here);
+      for (uint32_t j = 0; j < n_tiles; ++j) {
+        const uint32_t g = tiles_before + j, st = g % C::kStages, use = g / C::kStages;
+        const uint32_t e0 = item.kv_begin + j * kEntries;
+        const bool edge = e0 + kEntries > vis_min;
+        here_next = locate(j + 1, off_next);
+#pragma unroll
+        for (int u = 0; u < C::kUnits; ++u) {
+          const int s = u % C::kSlices;
+          const bool is_v = u >= C::kSlices;
+          if (!is_v) {
+            if (kShared ? (s % 2 == 0) : s == 0) w.wait<kShort>(&sh.k_free[st][kShared ? s / 2 : 0], (use & 1) ^ 1);
+          } else if (s == 0) {
+            w.wait<kShort>(&sh.v_free[st], (use & 1) ^ 1);
+          }
+          const uint32_t dst = (is_v ? v_at : k_at) + (st * C::kSlices + s) * kSlice;
+#pragma unroll
+          for (int i = 0; i < C::kLoads; ++i) {
+            uint4 x = buf[u % C::kAhead][i];
+            // NaNs of an edge tile's values: see the split kernel
+            if ((is_v || kShared) && edge) {
+              uint32_t* y = reinterpret_cast<uint32_t*>(&x);
+#pragma unroll
+              for (int z = 0; z < 4; ++z) {
+                if (kShared) {
+                  const uint32_t nb = q8_nan_bytes(y[z]);
+                  if (nb) {
+                    atomicMin(&sh.nan[0], static_cast<int>(e0 + tok[i]));
+                    sh.any_nan = 1;
+                    y[z] &= ~nb;
+                  }
+                } else {
+                  y[z] = without_nan(y[z], e0 + tok[i], sh.nan + s * 64 + q * 16 + z * 4, &sh.any_nan);
+                }
+              }
+            }
+            const uint32_t row = dst + tok[i] * 128, sw = tok[i] & 7;
+            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(row + (((2 * q) ^ sw) << 4)),
+                         "r"(q8_lo_f16x2(x.x)), "r"(q8_hi_f16x2(x.x)), "r"(q8_lo_f16x2(x.y)), "r"(q8_hi_f16x2(x.y))
+                         : "memory");
+            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(row + (((2 * q + 1) ^ sw) << 4)),
+                         "r"(q8_lo_f16x2(x.z)), "r"(q8_hi_f16x2(x.z)), "r"(q8_lo_f16x2(x.w)), "r"(q8_hi_f16x2(x.w))
+                         : "memory");
+          }
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_addr(is_v ? &sh.v_full[st][s] : &sh.k_full[st][s]));
+          // the slice that is kAhead units on, of this tile or the next
+          if (u + C::kAhead < C::kUnits)
+            load(buf[u % C::kAhead], u + C::kAhead, off, here);
+          else
+            load(buf[u % C::kAhead], u + C::kAhead - C::kUnits, off_next, here_next);
+        }
+        here = here_next;
+#pragma unroll
+        for (int i = 0; i < C::kLoads; ++i) off[i] = off_next[i];
+      }
+      if (bad) status_or(a.d_status, CKV_STATUS_BAD_INDEX);
+    } else if (soft) {
+      // ---- softmax of 32 rows (columns of S^T); this thread's entry is its lane
+      const int group = warp >> 2, quarter = warp & 3, bar = 1 + group;
+      const int c0 = group * 32, entry = quarter * 32 + lane;
+      const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
+      float l[32];
+#pragma unroll
+      for (int c = 0; c < 32; ++c) l[c] = 0.0f;
+      // the entry's block a tile ahead of its scales, and those a tile ahead of their use
+      auto block_of = [&](uint32_t tile) -> int32_t {
+        const uint32_t e = item.kv_begin + tile * kEntries + entry;
+        if (tile >= n_tiles || e >= item.kv_end) return -1;
+        const int32_t b = __ldg(table + e / T);
+        return b >= 0 && static_cast<uint32_t>(b) < a.c.num_blocks ? b : -1;
+      };
+      auto scale_of = [&](const float* s, int32_t b) { return b >= 0 ? __ldg(s + static_cast<size_t>(b) * H + h) : 1.0f; };
+      const float* vs = kShared ? a.c.k_scale : a.c.v_scale;
+      int32_t b_now = block_of(0), b_next = block_of(1);
+      float ks_now = scale_of(a.c.k_scale, b_now), vs_now = scale_of(vs, b_now);
+      for (uint32_t j = 0; j < n_tiles; ++j) {
+        const uint32_t g = tiles_before + j, sb = g & 1;
+        const float kf = ks_now, lv = __log2f(vs_now), iv = __fdiv_rn(1.0f, vs_now);
+        const bool exists = b_now >= 0;
+        b_now = b_next;
+        ks_now = scale_of(a.c.k_scale, b_now);
+        vs_now = scale_of(vs, b_now);
+        b_next = block_of(j + 2);
+        const uint32_t e0 = item.kv_begin + j * kEntries;
+
+        w.wait<kShort>(&sh.s_full[sb], (g >> 1) & 1);
+        tc_fence_after();
+        float t[32];
+        tmem_load32(tmem + lanes + sb * kN + c0, t);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&sh.s_free[sb]));
+        bool over = false;
+#pragma unroll
+        for (int c = 0; c < 32; c += 4) {
+          const float4 rf = *reinterpret_cast<const float4*>(sh.rf + c0 + c);
+          t[c] = fmaf(t[c], kf * rf.x, lv);
+          t[c + 1] = fmaf(t[c + 1], kf * rf.y, lv);
+          t[c + 2] = fmaf(t[c + 2], kf * rf.z, lv);
+          t[c + 3] = fmaf(t[c + 3], kf * rf.w, lv);
+        }
+        if (e0 + kEntries > vis_min || !exists) {
+          const int e = static_cast<int>(e0 + entry);
+#pragma unroll
+          for (int c = 0; c < 32; ++c)
+            if (!exists || e >= sh.vis[c0 + c]) t[c] = -INFINITY;
+        }
+#pragma unroll
+        for (int c = 0; c < 32; c += 4) {
+          const float4 m = *reinterpret_cast<const float4*>(sh.m + c0 + c);
+          over |= t[c] > m.x + 14.0f;
+          over |= t[c + 1] > m.y + 14.0f;
+          over |= t[c + 2] > m.z + 14.0f;
+          over |= t[c + 3] > m.w + 14.0f;
+        }
+        if (group_any(bar, over)) {  // raise the rows' references
+          float top = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < 32; ++c) {
+            float x = t[c];
+#pragma unroll
+            for (int s = 16; s > 0; s >>= 1) x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, s));
+            if (lane == c) top = x;
+          }
+          sh.red[quarter][c0 + lane] = top;
+          group_sync(bar);
+          if (quarter == 0) {
+            const int c = c0 + lane;
+            top = fmaxf(fmaxf(sh.red[0][c], sh.red[1][c]), fmaxf(sh.red[2][c], sh.red[3][c]));
+            const float was = sh.m[c], now = fmaxf(was, top - 6.0f);
+            sh.m[c] = now;
+            sh.fac[c] = ex2(was - now);
+          }
+          group_sync(bar);
+#pragma unroll
+          for (int c = 0; c < 32; ++c) l[c] *= sh.fac[c0 + c];
+          if (j > 0) {
+            w.wait<kShort>(&sh.pv_done, (g & 1) ^ 1);
+            tc_fence_after();
+#pragma unroll 1
+            for (int b = 0; b < C::kBlocks; ++b) {
+              float o[32];
+              const uint32_t at = tmem + lanes + C::kOCol + b * kN + c0;
+              tmem_load32(at, o);
+#pragma unroll
+              for (int c = 0; c < 32; ++c) o[c] *= sh.fac[c0 + c];
+              tmem_store32(at, o);
+            }
+            tc_fence_before();
+          }
+        }
+        uint32_t p[16];
+#pragma unroll
+        for (int c = 0; c < 32; c += 4) {
+          const float4 m = *reinterpret_cast<const float4*>(sh.m + c0 + c);
+          const float w0 = ex2(t[c] - m.x), w1 = ex2(t[c + 1] - m.y);
+          const float w2 = ex2(t[c + 2] - m.z), w3 = ex2(t[c + 3] - m.w);
+          l[c] = fmaf(w0, iv, l[c]);
+          l[c + 1] = fmaf(w1, iv, l[c + 1]);
+          l[c + 2] = fmaf(w2, iv, l[c + 2]);
+          l[c + 3] = fmaf(w3, iv, l[c + 3]);
+          p[c / 2] = pack_f16x2(w0, w1);
+          p[c / 2 + 1] = pack_f16x2(w2, w3);
+        }
+        w.wait<kShort>(&sh.pv_done, (g & 1) ^ 1);  // the second product is done with the tile before
+        const uint32_t row = p_at + (group >> 1) * kSlice + entry * 128;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(row + ((((group & 1) * 4 + i) ^ (entry & 7)) << 4)),
+                       "r"(p[4 * i]), "r"(p[4 * i + 1]), "r"(p[4 * i + 2]), "r"(p[4 * i + 3])
+                       : "memory");
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&sh.p_full));
+      }
+      // ---- the rows' sums, then the output
+      {
+        float mine = 0.0f;
+#pragma unroll
+        for (int c = 0; c < 32; ++c) {
+          float x = l[c];
+#pragma unroll
+          for (int s = 16; s > 0; s >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, s);
+          if (lane == c) mine = x;
+        }
+        sh.red[quarter][c0 + lane] = mine;
+        group_sync(bar);
+        if (quarter == 0) {
+          const int c = c0 + lane;
+          const float sum = (sh.red[0][c] + sh.red[1][c]) + (sh.red[2][c] + sh.red[3][c]);
+          sh.fac[c] = sum == 0.0f ? 0.0f : __fdiv_rn(1.0f, sum);
+          if (static_cast<uint32_t>(c) < rows) {
+            if (item.part >= 0)
+              a.part_ml[(static_cast<size_t>(item.part + static_cast<int>(item.chunk)) * H + h) * kN + c] =
+                  make_float2(sh.m[c], sum);
+            else if (a.lse != nullptr)
+              a.lse[sh.out_row[c]] = sum == 0.0f ? -INFINITY : (sh.m[c] + __log2f(sum)) * 0.69314718055994530942f;
+          }
+        }
+        group_sync(bar);
+      }
+      if (n_tiles > 0) w.wait<kShort>(&sh.pv_done, (tiles_before + n_tiles - 1) & 1);
+      tc_fence_after();
+      const int any_nan = sh.any_nan;
+#pragma unroll 1
+      for (int b = 0; b < C::kBlocks; ++b) {
+        const int d = b * 128 + entry;  // this lane's channel
+        float o[32];
+        if (n_tiles > 0) {
+          tmem_load32(tmem + lanes + C::kOCol + b * kN + c0, o);
+        } else {
+#pragma unroll
+          for (int c = 0; c < 32; ++c) o[c] = 0.0f;
+        }
+        if (d < kD) {
+          const int nan_at = any_nan ? sh.nan[kShared ? 0 : d] : 0x7FFFFFFF;
+#pragma unroll
+          for (int c = 0; c < 32; ++c) {
+            const int n = c0 + c;
+            if (static_cast<uint32_t>(n) < rows) {
+              float v = nan_at < sh.vis[n] ? __int_as_float(0x7FFFFFFF) : o[c];
+              if (item.part >= 0) {
+                a.part_o[((static_cast<size_t>(item.part + static_cast<int>(item.chunk)) * H + h) * kN + n) * kD + d] = v;
+              } else {
+                v *= sh.fac[n];
+                if (a.out_f32)
+                  static_cast<float*>(a.out)[sh.out_row[n] * kD + d] = v;
+                else
+                  static_cast<__nv_bfloat16*>(a.out)[sh.out_row[n] * kD + d] = __float2bfloat16_rn(v);
+              }
+            }
+          }
+        }
+      }
+      tc_fence_before();
+    } else {
+      // ---- the products: the warp waits together, one lane issues
+      auto scores = [&](uint32_t g) {
+        const uint32_t st = g % C::kStages, use = g / C::kStages, sb = g & 1;
+        w.wait<kShort>(&sh.s_free[sb], ((g >> 1) & 1) ^ 1);
+        for (int s = 0; s < C::kSlices; ++s) {
+          w.wait<kShort>(&sh.k_full[st][s], use & 1);
+          tc_fence_after();
+          if (lane == 0 && w.live) {
+            const uint64_t ka = smem_operand(k_at + (st * C::kSlices + s) * kSlice, 0);
+            const uint64_t qb = smem_operand(q_at + s * (kN * 128), 0);
+#pragma unroll
+            for (int x = 0; x < 4; ++x)  // 16 channels, 32 bytes of a row
+              tc_mma(tmem + sb * kN, ka + 2 * x, qb + 2 * x, mma_shape(128, kN, false, false), s > 0 || x > 0);
+          }
+        }
+        if (lane == 0) {
+          if (!kShared) tc_commit(smem_addr(&sh.k_free[st][0]));
+          tc_commit(smem_addr(&sh.s_full[sb]));
+        }
+        __syncwarp();
+      };
+      auto values = [&](uint32_t g, bool fresh) {
+        const uint32_t st = g % C::kStages, use = g / C::kStages;
+        w.wait<kShort>(&sh.p_full, g & 1);
+        for (int b = 0; b < C::kBlocks; ++b) {
+          if (!kShared) {
+            w.wait<kShort>(&sh.v_full[st][kD == 64 ? 0 : 2 * b], use & 1);
+            w.wait<kShort>(&sh.v_full[st][kD == 64 ? 0 : 2 * b + 1], use & 1);
+          }
+          tc_fence_after();
+          if (lane == 0) {
+            if (w.live) {
+              // 64 channels: both halves of M read the one slice, and the second is not used
+              const uint64_t va = smem_operand(v_at + (st * C::kSlices + 2 * b) * kSlice, kD == 64 ? 0 : kSlice);
+              const uint64_t pb = smem_operand(p_at, kSlice);
+#pragma unroll
+              for (int x = 0; x < 8; ++x)  // 16 entries, 16 rows of 128 bytes
+                tc_mma(tmem + C::kOCol + b * kN, va + 128 * x, pb + 128 * x, mma_shape(128, kN, true, true),
+                       !fresh || x > 0);
+            }
+            if (kShared) tc_commit(smem_addr(&sh.k_free[st][b]));
+          }
+          __syncwarp();
+        }
+        if (lane == 0) {
+          if (!kShared) tc_commit(smem_addr(&sh.v_free[st]));
+          tc_commit(smem_addr(&sh.pv_done));
+        }
+        __syncwarp();
+      };
+      for (uint32_t j = 0; j < n_tiles; ++j) {
+        const uint32_t g = tiles_before + j;
+        scores(g);
+        if (!C::kLag)
+          values(g, j == 0);
+        else if (j > 0)
+          values(g - 1, j == 1);
+      }
+      if (C::kLag && n_tiles > 0) values(tiles_before + n_tiles - 1, n_tiles == 1);
+    }
+    tiles_before += n_tiles;
+    __syncthreads();  // the next item's rows take the place of this one's
+    tc_fence_after();
+  }
+  if (warp == C::kWarps - 1) {
+    // every product is done before its memory is given back
+    if (lane == 0) tc_commit(smem_addr(&sh.idle));
+    __syncwarp();
+    const bool done = warp_wait_for<false>(smem_addr(&sh.idle), 0, kWaitLimitNs);
+    if (!done) w.live = false;
+    tmem_free(tmem, C::kCols);
+  }
+  if (!w.live && lane == 0) status_or(a.d_status, CKV_STATUS_TIMEOUT);
+}
+
+template <int kD, bool kShared>
+int launch(const AttnArgs& a, cudaStream_t s) {
+  using C = TcCfg<kD, kShared>;
+  auto* kernel = a.wait_ns < kShortWaitNs ? q8_attn_tc_kernel<kD, kShared, true> : q8_attn_tc_kernel<kD, kShared, false>;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) != cudaSuccess) {
+    cudaGetLastError();
+    return CKV_ERR_LAUNCH;
+  }
+  return launch_pdl(kernel, dim3(a.g.ctas, a.c.heads), dim3(C::kThreads), C::kSmem, s, a);
+}
+
+}  // namespace
+
+int launch_q8_attn_tc(const AttnArgs& a, cudaStream_t s) {
+  const bool shared = a.c.v == nullptr;
+  switch (a.c.head_dim) {
+    case 64: return shared ? launch<64, true>(a, s) : launch<64, false>(a, s);
+    case 128: return shared ? launch<128, true>(a, s) : launch<128, false>(a, s);
+    case 256: return shared ? launch<256, true>(a, s) : launch<256, false>(a, s);
+    default: return shared ? launch<512, true>(a, s) : CKV_ERR_SIZE;
+  }
+}
+
+}  // namespace ckv

@@ -3,7 +3,7 @@
 //
 // Work.  The rows of a request for one kv head are its q_len * group (query,
 // head) pairs; a tile is `rows` consecutive ones, and its cost is the entries
-// its last row sees, in units of entries, plus a fixed start-up of kQ8StartCost.
+// its last row sees, in units of entries, plus a fixed start-up.
 // The tiles' costs are laid end to end and cut at multiples of one quota, so
 // every CTA of a kv head gets the same number of entries whatever the lengths
 // are (one wave, no tail); a tile that a cut crosses leaves partial results,
@@ -15,8 +15,6 @@
 #include "q8.cuh"
 
 namespace ckv {
-
-constexpr uint32_t kQ8StartCost = 32;  // entries; a multiple of 16
 
 struct Q8Item {  // 48 bytes
   uint32_t rid;
@@ -49,11 +47,14 @@ struct Q8Header {  // 64 bytes
 static_assert(sizeof(Q8Header) == 64, "");
 
 struct Q8Geom {
+  bool tc;             // the tensor-core kernel takes it, not the split kernel
+  uint32_t start_cost; // entries that starting a tile costs; a multiple of 16
   uint32_t rows;       // rows of a tile
   uint32_t group;      // query heads of a kv head
   uint32_t ctas;       // CTAs of a kv head
   uint32_t min_quota;  // entries
-  uint32_t round;      // the quota is a multiple of this
+  uint32_t round;      // the quota is a multiple of this, itself one of grain
+  uint32_t grain;      // entries are counted in these: 16, or the tensor-core kernel's tile
   uint32_t cap_items;
   uint32_t cap_parts;
   uint64_t off_first, off_split, off_items, bytes;
@@ -63,5 +64,58 @@ struct Q8Geom {
 // From sizes alone (and the device's SM count), the same for the plan and the
 // attention call.  CKV_OK or CKV_ERR_SIZE.
 int q8_attn_geom(const Q8Cache& c, uint32_t batch, uint32_t num_q, uint32_t n_heads, Q8Geom* g);
+
+// Arguments of the attention kernels.
+struct AttnArgs {
+  Q8Cache c;
+  Q8Geom g;
+  const __nv_bfloat16* q;
+  uint32_t num_q;
+  uint32_t n_heads;
+  uint32_t ratio;
+  float scale_log2;
+  const int32_t* table;
+  uint32_t stride;
+  uint32_t num_reqs;
+  const uint8_t* plan;
+  int out_f32;
+  void* out;
+  float* lse;
+  float* part_o;    // [part][kv head][row][head_dim]
+  float2* part_ml;  // [part][kv head][row]
+  uint64_t wait_ns;
+  uint32_t* d_status;
+};
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+__device__ __forceinline__ bool item_fits(const Q8Item& item, const AttnArgs& a) {
+  return item.rid < a.num_reqs && static_cast<uint64_t>(item.q_start) + item.q_len <= a.num_q &&
+         item.row0 < static_cast<uint64_t>(item.q_len) * a.g.group &&
+         item.kv_len <= static_cast<uint64_t>(a.stride) * a.c.block_tokens && item.kv_end <= item.kv_len &&
+         (item.part < 0 || (static_cast<uint64_t>(item.part) + item.chunks <= a.g.cap_parts && item.chunk < item.chunks));
+}
+
+__device__ __forceinline__ bool plan_fits(const Q8Header* h, const AttnArgs& a) {
+  return h->rows == a.g.rows && h->group == a.g.group && h->num_q == a.num_q && h->ratio == a.ratio &&
+         h->cap_ctas == a.g.ctas;
+}
+
+// Takes the NaNs out of a word of four channels of entry e, noting the first entry with one for each channel.
+__device__ __forceinline__ uint32_t without_nan(uint32_t w, int e, int* s_nan, int* s_any_nan) {
+  const uint32_t bad = q8_nan_bytes(w);
+  if (bad) {
+    for (int z = 0; z < 4; ++z)
+      if (bad >> (8 * z) & 1) atomicMin(s_nan + z, e);
+    *s_any_nan = 1;
+  }
+  return w & ~bad;
+}
+
+// The tensor-core kernel, for tiles of many rows (g.tc); the parts that it leaves are joined by the caller.
+int launch_q8_attn_tc(const AttnArgs& a, cudaStream_t s);
 
 }  // namespace ckv

@@ -35,7 +35,7 @@ __device__ __forceinline__ uint64_t smem_operand(uint32_t addr, uint32_t lbo) {
 
 // Instruction descriptor: fp16 x fp16 -> fp32, M x N; a_outer / b_outer: that
 // operand's shared-memory rows run along M / N instead of K.
-constexpr uint32_t mma_shape(int m, int n, bool a_outer, bool b_outer) {
+__host__ __device__ constexpr uint32_t mma_shape(int m, int n, bool a_outer, bool b_outer) {
   return (1u << 4) | (a_outer ? 1u << 15 : 0u) | (b_outer ? 1u << 16 : 0u) | (static_cast<uint32_t>(n >> 3) << 17) |
          (static_cast<uint32_t>(m >> 4) << 24);
 }
@@ -60,14 +60,14 @@ __device__ __forceinline__ void tmem_load32(uint32_t addr, float (&v)[32]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
       "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,"
-      "%30,%31}, [%32];"
+      "%30,%31}, [%32];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"  // in the same statement: nothing may use a register before it
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
         "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
         "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
         "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(addr)
       : "memory");
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
