@@ -116,6 +116,13 @@ __device__ __forceinline__ uint32_t q8_rescale4(uint32_t w, float f) {
 // 0xFF in every byte of w that is an e4m3 NaN (0x7F or 0xFF).
 __device__ __forceinline__ uint32_t q8_nan_bytes(uint32_t w) { return __vcmpeq4(w & 0x7F7F7F7Fu, 0x7F7F7F7Fu); }
 
+// Two fp32 products at once (see f2_add and f2_fma).
+__device__ __forceinline__ F2 f2_mul(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+
 // ---------------------------------------------------------------- scans
 // Exclusive scan of v over a block of kThreads threads, and the total.
 // s_warp: kThreads / 32 + 1 words of shared memory; all threads call it.
@@ -186,6 +193,20 @@ __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commi
 template <int N>
 __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// A streamed 16-byte load, or zeros where `in` is false: predicated, so that nothing waits for it
+// before its first use (a branch around the load would, where the paths join).
+__device__ __forceinline__ uint4 ld_stream16_if(const void* p, bool in) {
+  uint4 v;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.u32 p, %5, 0;\n\t"
+      "mov.u32 %0, 0;\n\tmov.u32 %1, 0;\n\tmov.u32 %2, 0;\n\tmov.u32 %3, 0;\n\t"
+      "@p ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];\n\t}"
+      : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
+      : "l"(p), "r"(in ? 1u : 0u));
+  return v;
 }
 
 __device__ __forceinline__ uint4 lds16(uint32_t a) {

@@ -71,9 +71,10 @@ struct alignas(16) TcShared {
   uint64_t v_full[C::kStages][C::kSlices], v_free[C::kStages];
   uint64_t s_full[2], s_free[2], p_full, pv_done, idle;
   alignas(16) float rf[C::kRows];  // read four at a time
-  alignas(16) float m[C::kRows];
-  float fac[C::kRows];
+  alignas(16) float neg_m[C::kRows];
+  float fac[C::kRows], up[C::kRows];
   int vis[C::kRows];
+  int set[C::kRows];  // the row's reference has been set
   size_t out_row[C::kRows];
   float red[4][C::kRows];
   int nan[kShared ? 1 : kD];  // first entry with a NaN (a latent cache: in any channel, else by channel)
@@ -82,13 +83,24 @@ struct alignas(16) TcShared {
 };
 
 // A wait that, once it has run out, lets the rest of the loop run without waiting: every barrier is
-// still reached, the kernel ends, and the status says so.
+// still reached, the kernel ends, and the status says so.  The limit is counted in SM clocks, two to a
+// nanosecond (about the highest rate, so a slower clock only waits longer): the roles hand tiles to one another all the
+// time, and a read of the global timer in a wait that misses its first probe costs more than the wait.
 struct Waiter {
-  uint64_t limit;
+  long long limit;
   bool live;
   template <bool kShort>
-  __device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity) {
-    if (live) live = warp_wait_for<kShort>(smem_addr(bar), parity, limit);
+  __device__ __forceinline__ void wait(uint64_t* barrier, uint32_t parity) {
+    if (!live) return;
+    const uint32_t bar = smem_addr(barrier);
+    bool done = kShort ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity);
+    if (!done) {
+      const long long t0 = clock64();
+      do {
+        done = kShort ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity);
+      } while (!done && clock64() - t0 <= limit);
+    }
+    live = __all_sync(0xFFFFFFFFu, done);
   }
 };
 
@@ -105,6 +117,21 @@ __device__ __forceinline__ bool group_any(int id, bool x) {
   return r != 0;
 }
 __device__ __forceinline__ void group_sync(int id) { asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory"); }
+
+// Takes the NaNs out of 16 channels of entry e: see the split kernel.  Out of line: it runs for next to no tile.
+__device__ __noinline__ uint4 without_nans(uint4 x, int e, int* nan, int step, int* any) {
+  uint32_t* y = reinterpret_cast<uint32_t*>(&x);
+  for (int z = 0; z < 4; ++z) {
+    const uint32_t bad = q8_nan_bytes(y[z]);
+    if (bad) {
+      for (int b = 0; b < 4; ++b)
+        if (bad >> (8 * b) & 1) atomicMin(nan + step * (4 * z + b), e);
+      *any = 1;
+      y[z] &= ~bad;
+    }
+  }
+  return x;
+}
 
 template <int kD, bool kShared, bool kShort>
 __global__ __launch_bounds__((TcCfg<kD, kShared>::kThreads), 1) void q8_attn_tc_kernel(const AttnArgs a) {
@@ -126,7 +153,7 @@ __global__ __launch_bounds__((TcCfg<kD, kShared>::kThreads), 1) void q8_attn_tc_
   const uint32_t item0 = first[blockIdx.x], item1 = min(first[blockIdx.x + 1], a.g.cap_items);
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const uint32_t G = a.g.group, H = a.c.heads, T = a.c.block_tokens;
+  const uint32_t G = a.g.group, H = a.c.heads, T = a.c.block_tokens, t_shift = __ffs(T) - 1;
   const uint32_t base = (smem_addr(raw) + 1023) & ~1023u;
   const uint32_t q_at = base, k_at = q_at + C::kQBytes, v_at = kShared ? k_at : k_at + C::kKBytes;
   const uint32_t p_at = k_at + C::kKBytes + C::kVBytes;
@@ -156,7 +183,7 @@ __global__ __launch_bounds__((TcCfg<kD, kShared>::kThreads), 1) void q8_attn_tc_
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
-  Waiter w{a.wait_ns, true};
+  Waiter w{static_cast<long long>(a.wait_ns) * 2, true};
   uint32_t tiles_before = 0;  // tiles of earlier items: the barriers' phases go on
 
   for (uint32_t it = item0; it < item1; ++it) {
@@ -169,6 +196,7 @@ __global__ __launch_bounds__((TcCfg<kD, kShared>::kThreads), 1) void q8_attn_tc_
     const int32_t* table = a.table + static_cast<size_t>(item.rid) * a.stride;
     const uint32_t n_tiles =
         item.kv_end > item.kv_begin ? (item.kv_end - item.kv_begin + kEntries - 1) / kEntries : 0;
+    const uint32_t last = item.kv_end > 0 ? item.kv_end - 1 : 0;
     const uint32_t vis_min = min(item.kv_end, static_cast<uint32_t>(q8_visible(item.kv_len, item.q_len - 1 - item.row0 / G,
                                                                              item.phase, a.ratio)));
     // ---- the rows: query operand, scaling, visibility
@@ -197,7 +225,8 @@ __global__ __launch_bounds__((TcCfg<kD, kShared>::kThreads), 1) void q8_attn_tc_
       }
       if (lane == 0) {
         sh.rf[n] = pow2f(-ex) * a.scale_log2;
-        sh.m[n] = -3.4e38f;
+        sh.neg_m[n] = 0.0f;
+        sh.set[n] = 0;
         sh.vis[n] = in ? static_cast<int>(q8_visible(item.kv_len, item.q_len - 1 - i, item.phase, a.ratio)) : 0x7FFFFFFF;
         sh.out_row[n] = row;
       }
@@ -211,96 +240,95 @@ __global__ __launch_bounds__((TcCfg<kD, kShared>::kThreads), 1) void q8_attn_tc_
       // ---- e4m3 -> fp16 operands.  Lane l takes 16 channels, chunk l % 4 of a slice, of entries l / 4 + 8 * ...: the
       // eight lanes of a store's phase take two entries, whose chunks the swizzle puts in different banks.
       const int cw = warp - C::kSoftWarps, q = lane & 3;
-      uint32_t tok[C::kLoads];
-      size_t off[C::kLoads], off_next[C::kLoads];
-      uint32_t here = 0, here_next = 0;  // bit i: load i's entry exists
+      const uint32_t tok = cw * 8 + (lane >> 2);             // load i: entry tok + 32 i
+      const uint32_t st0 = tok * 128 + (((2 * q) ^ (tok & 7)) << 4), st1 = tok * 128 + (((2 * q + 1) ^ (tok & 7)) << 4);
+      const uint8_t* src[C::kLoads];       // the K addresses of this tile's entries
+      const uint8_t* src_next[C::kLoads];  // and of the next one's
+      uint32_t here = 0, here_next = 0;    // bit i: load i's entry exists
       bool bad = false;
+      // Block numbers are asked for a tile before the addresses are made from them, at places that always exist, so
+      // that no load here waits for another.
+      int32_t blk[C::kLoads];
+      auto ask = [&](uint32_t tile) {
 #pragma unroll
-      for (int i = 0; i < C::kLoads; ++i) tok[i] = i * (8 * C::kConvWarps) + cw * 8 + (lane >> 2);
-      auto locate = [&](uint32_t tile, size_t(&o)[C::kLoads]) -> uint32_t {
+        for (int i = 0; i < C::kLoads; ++i) {
+          const uint32_t e = item.kv_begin + tile * kEntries + tok + i * (8 * C::kConvWarps);
+          blk[i] = __ldg(table + (min(e, last) >> t_shift));
+        }
+      };
+      auto locate = [&](uint32_t tile, const uint8_t*(&o)[C::kLoads]) -> uint32_t {
         uint32_t mask = 0;
 #pragma unroll
         for (int i = 0; i < C::kLoads; ++i) {
-          const uint32_t e = item.kv_begin + tile * kEntries + tok[i];
-          o[i] = 0;
-          if (tile < n_tiles && e < item.kv_end) {
-            const int32_t b = __ldg(table + e / T);
-            if (b >= 0 && static_cast<uint32_t>(b) < a.c.num_blocks) {
-              o[i] = ((static_cast<size_t>(b) * H + h) * T + e % T) * kD + q * 16;
-              mask |= 1u << i;
-            } else {
-              bad = true;
-            }
-          }
+          const uint32_t e = item.kv_begin + tile * kEntries + tok + i * (8 * C::kConvWarps);
+          const bool in = tile < n_tiles && e < item.kv_end;
+          const bool ok = static_cast<uint32_t>(blk[i]) < a.c.num_blocks;  // negative ones are large
+          o[i] = a.c.k + (((static_cast<size_t>(ok ? blk[i] : 0) * H + h) << t_shift) + (e & (T - 1))) * kD + q * 16;
+          mask |= (in && ok ? 1u : 0u) << i;
+          bad |= in && !ok;
         }
         return mask;
       };
+      const ptrdiff_t v_off = kShared ? 0 : a.c.v - a.c.k;
       uint4 buf[C::kAhead][C::kLoads];
-      auto load = [&](uint4(&d)[C::kLoads], int unit, const size_t(&o)[C::kLoads], uint32_t mask) {
-        const uint8_t* pool = unit < C::kSlices ? a.c.k : a.c.v;
-        const int s = unit % C::kSlices;
+      auto load = [&](uint4(&d)[C::kLoads], int unit, const uint8_t* const(&o)[C::kLoads], uint32_t mask) {
+        const ptrdiff_t at = unit < C::kSlices ? unit * 64 : v_off + (unit - C::kSlices) * 64;
 #pragma unroll
-        for (int i = 0; i < C::kLoads; ++i)
-          d[i] = mask >> i & 1 ? ld_stream16(pool + o[i] + s * 64) : make_uint4(0, 0, 0, 0);
+        for (int i = 0; i < C::kLoads; ++i) d[i] = ld_stream16_if(o[i] + at, mask >> i & 1);
       };
-      here = locate(0, off);
+      ask(0);
+      here = locate(0, src);
+      ask(1);
 #pragma unroll
-      for (int u = 0; u < C::kAhead; ++u) load(buf[u], u, off, here);
+      for (int u = 0; u < C::kAhead; ++u) load(buf[u], u, src, here);
       for (uint32_t j = 0; j < n_tiles; ++j) {
         const uint32_t g = tiles_before + j, st = g % C::kStages, use = g / C::kStages;
         const uint32_t e0 = item.kv_begin + j * kEntries;
         const bool edge = e0 + kEntries > vis_min;
-        here_next = locate(j + 1, off_next);
+        here_next = locate(j + 1, src_next);
+        ask(j + 2);
+#pragma unroll 1
+        for (int u0 = 0; u0 < C::kUnits; u0 += C::kAhead) {
 #pragma unroll
-        for (int u = 0; u < C::kUnits; ++u) {
-          const int s = u % C::kSlices;
-          const bool is_v = u >= C::kSlices;
-          if (!is_v) {
-            if (kShared ? (s % 2 == 0) : s == 0) w.wait<kShort>(&sh.k_free[st][kShared ? s / 2 : 0], (use & 1) ^ 1);
-          } else if (s == 0) {
-            w.wait<kShort>(&sh.v_free[st], (use & 1) ^ 1);
-          }
-          const uint32_t dst = (is_v ? v_at : k_at) + (st * C::kSlices + s) * kSlice;
-#pragma unroll
-          for (int i = 0; i < C::kLoads; ++i) {
-            uint4 x = buf[u % C::kAhead][i];
-            // NaNs of an edge tile's values: see the split kernel
-            if ((is_v || kShared) && edge) {
-              uint32_t* y = reinterpret_cast<uint32_t*>(&x);
-#pragma unroll
-              for (int z = 0; z < 4; ++z) {
-                if (kShared) {
-                  const uint32_t nb = q8_nan_bytes(y[z]);
-                  if (nb) {
-                    atomicMin(&sh.nan[0], static_cast<int>(e0 + tok[i]));
-                    sh.any_nan = 1;
-                    y[z] &= ~nb;
-                  }
-                } else {
-                  y[z] = without_nan(y[z], e0 + tok[i], sh.nan + s * 64 + q * 16 + z * 4, &sh.any_nan);
-                }
-              }
+          for (int x = 0; x < C::kAhead; ++x) {
+            const int u = u0 + x;
+            const bool is_v = u >= C::kSlices;
+            const int s = is_v ? u - C::kSlices : u;
+            if (is_v) {
+              if (s == 0) w.wait<kShort>(&sh.v_free[st], (use & 1) ^ 1);
+            } else if (kShared ? s % 2 == 0 : s == 0) {
+              w.wait<kShort>(&sh.k_free[st][kShared ? s / 2 : 0], (use & 1) ^ 1);
             }
-            const uint32_t row = dst + tok[i] * 128, sw = tok[i] & 7;
-            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(row + (((2 * q) ^ sw) << 4)),
-                         "r"(q8_lo_f16x2(x.x)), "r"(q8_hi_f16x2(x.x)), "r"(q8_lo_f16x2(x.y)), "r"(q8_hi_f16x2(x.y))
-                         : "memory");
-            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(row + (((2 * q + 1) ^ sw) << 4)),
-                         "r"(q8_lo_f16x2(x.z)), "r"(q8_hi_f16x2(x.z)), "r"(q8_lo_f16x2(x.w)), "r"(q8_hi_f16x2(x.w))
-                         : "memory");
+            if ((is_v || kShared) && edge) {
+#pragma unroll
+              for (int i = 0; i < C::kLoads; ++i)
+                buf[x][i] = without_nans(buf[x][i], e0 + tok + i * (8 * C::kConvWarps),
+                                         kShared ? sh.nan : sh.nan + s * 64 + q * 16, kShared ? 0 : 1, &sh.any_nan);
+            }
+            const uint32_t dst = (is_v ? v_at : k_at) + (st * C::kSlices + s) * kSlice;
+#pragma unroll
+            for (int i = 0; i < C::kLoads; ++i) {
+              const uint4 y = buf[x][i];
+              asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(dst + st0 + i * (8 * C::kConvWarps) * 128),
+                           "r"(q8_lo_f16x2(y.x)), "r"(q8_hi_f16x2(y.x)), "r"(q8_lo_f16x2(y.y)), "r"(q8_hi_f16x2(y.y))
+                           : "memory");
+              asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(dst + st1 + i * (8 * C::kConvWarps) * 128),
+                           "r"(q8_lo_f16x2(y.z)), "r"(q8_hi_f16x2(y.z)), "r"(q8_lo_f16x2(y.w)), "r"(q8_hi_f16x2(y.w))
+                           : "memory");
+            }
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_addr(is_v ? &sh.v_full[st][s] : &sh.k_full[st][s]));
+            // the slice that is kAhead units on, of this tile or the next
+            if (u0 + C::kAhead < C::kUnits)
+              load(buf[x], u + C::kAhead, src, here);
+            else
+              load(buf[x], x, src_next, here_next);
           }
-          fence_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_addr(is_v ? &sh.v_full[st][s] : &sh.k_full[st][s]));
-          // the slice that is kAhead units on, of this tile or the next
-          if (u + C::kAhead < C::kUnits)
-            load(buf[u % C::kAhead], u + C::kAhead, off, here);
-          else
-            load(buf[u % C::kAhead], u + C::kAhead - C::kUnits, off_next, here_next);
         }
         here = here_next;
 #pragma unroll
-        for (int i = 0; i < C::kLoads; ++i) off[i] = off_next[i];
+        for (int i = 0; i < C::kLoads; ++i) src[i] = src_next[i];
       }
       if (bad) status_or(a.d_status, CKV_STATUS_BAD_INDEX);
     } else if (soft) {
@@ -311,21 +339,18 @@ __global__ __launch_bounds__((TcCfg<kD, kShared>::kThreads), 1) void q8_attn_tc_
       float l[32];
 #pragma unroll
       for (int c = 0; c < 32; ++c) l[c] = 0.0f;
-      // the entry's block a tile ahead of its scales, and those a tile ahead of their use
-      auto block_of = [&](uint32_t tile) -> int32_t {
-        const uint32_t e = item.kv_begin + tile * kEntries + entry;
-        if (tile >= n_tiles || e >= item.kv_end) return -1;
-        const int32_t b = __ldg(table + e / T);
-        return b >= 0 && static_cast<uint32_t>(b) < a.c.num_blocks ? b : -1;
-      };
-      auto scale_of = [&](const float* s, int32_t b) { return b >= 0 ? __ldg(s + static_cast<size_t>(b) * H + h) : 1.0f; };
+      // the entry's block is asked for a tile ahead of its scales, and those a tile ahead of their use
+      auto block_of = [&](uint32_t tile) { return __ldg(table + (min(item.kv_begin + tile * kEntries + entry, last) >> t_shift)); };
+      auto valid = [&](int32_t b) { return static_cast<uint32_t>(b) < a.c.num_blocks; };
+      auto scale_of = [&](const float* s, int32_t b) { return __ldg(s + static_cast<size_t>(valid(b) ? b : 0) * H + h); };
       const float* vs = kShared ? a.c.k_scale : a.c.v_scale;
+      bool missed = false;
       int32_t b_now = block_of(0), b_next = block_of(1);
       float ks_now = scale_of(a.c.k_scale, b_now), vs_now = scale_of(vs, b_now);
       for (uint32_t j = 0; j < n_tiles; ++j) {
         const uint32_t g = tiles_before + j, sb = g & 1;
         const float kf = ks_now, lv = __log2f(vs_now), iv = __fdiv_rn(1.0f, vs_now);
-        const bool exists = b_now >= 0;
+        const bool exists = valid(b_now) && item.kv_begin + j * kEntries + entry < item.kv_end;
         b_now = b_next;
         ks_now = scale_of(a.c.k_scale, b_now);
         vs_now = scale_of(vs, b_now);
@@ -334,90 +359,101 @@ __global__ __launch_bounds__((TcCfg<kD, kShared>::kThreads), 1) void q8_attn_tc_
 
         w.wait<kShort>(&sh.s_full[sb], (g >> 1) & 1);
         tc_fence_after();
-        float t[32];
-        tmem_load32(tmem + lanes + sb * kN + c0, t);
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_addr(&sh.s_free[sb]));
-        bool over = false;
-#pragma unroll
-        for (int c = 0; c < 32; c += 4) {
-          const float4 rf = *reinterpret_cast<const float4*>(sh.rf + c0 + c);
-          t[c] = fmaf(t[c], kf * rf.x, lv);
-          t[c + 1] = fmaf(t[c + 1], kf * rf.y, lv);
-          t[c + 2] = fmaf(t[c + 2], kf * rf.z, lv);
-          t[c + 3] = fmaf(t[c + 3], kf * rf.w, lv);
-        }
-        if (e0 + kEntries > vis_min || !exists) {
-          const int e = static_cast<int>(e0 + entry);
-#pragma unroll
-          for (int c = 0; c < 32; ++c)
-            if (!exists || e >= sh.vis[c0 + c]) t[c] = -INFINITY;
-        }
-#pragma unroll
-        for (int c = 0; c < 32; c += 4) {
-          const float4 m = *reinterpret_cast<const float4*>(sh.m + c0 + c);
-          over |= t[c] > m.x + 14.0f;
-          over |= t[c + 1] > m.y + 14.0f;
-          over |= t[c + 2] > m.z + 14.0f;
-          over |= t[c + 3] > m.w + 14.0f;
-        }
-        if (group_any(bar, over)) {  // raise the rows' references
-          float top = -INFINITY;
-#pragma unroll
-          for (int c = 0; c < 32; ++c) {
-            float x = t[c];
-#pragma unroll
-            for (int s = 16; s > 0; s >>= 1) x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, s));
-            if (lane == c) top = x;
-          }
-          sh.red[quarter][c0 + lane] = top;
-          group_sync(bar);
-          if (quarter == 0) {
-            const int c = c0 + lane;
-            top = fmaxf(fmaxf(sh.red[0][c], sh.red[1][c]), fmaxf(sh.red[2][c], sh.red[3][c]));
-            const float was = sh.m[c], now = fmaxf(was, top - 6.0f);
-            sh.m[c] = now;
-            sh.fac[c] = ex2(was - now);
-          }
-          group_sync(bar);
-#pragma unroll
-          for (int c = 0; c < 32; ++c) l[c] *= sh.fac[c0 + c];
-          if (j > 0) {
-            w.wait<kShort>(&sh.pv_done, (g & 1) ^ 1);
-            tc_fence_after();
-#pragma unroll 1
-            for (int b = 0; b < C::kBlocks; ++b) {
-              float o[32];
-              const uint32_t at = tmem + lanes + C::kOCol + b * kN + c0;
-              tmem_load32(at, o);
-#pragma unroll
-              for (int c = 0; c < 32; ++c) o[c] *= sh.fac[c0 + c];
-              tmem_store32(at, o);
-            }
-            tc_fence_before();
-          }
-        }
-        uint32_t p[16];
-#pragma unroll
-        for (int c = 0; c < 32; c += 4) {
-          const float4 m = *reinterpret_cast<const float4*>(sh.m + c0 + c);
-          const float w0 = ex2(t[c] - m.x), w1 = ex2(t[c + 1] - m.y);
-          const float w2 = ex2(t[c + 2] - m.z), w3 = ex2(t[c + 3] - m.w);
-          l[c] = fmaf(w0, iv, l[c]);
-          l[c + 1] = fmaf(w1, iv, l[c + 1]);
-          l[c + 2] = fmaf(w2, iv, l[c + 2]);
-          l[c + 3] = fmaf(w3, iv, l[c + 3]);
-          p[c / 2] = pack_f16x2(w0, w1);
-          p[c / 2 + 1] = pack_f16x2(w2, w3);
-        }
-        w.wait<kShort>(&sh.pv_done, (g & 1) ^ 1);  // the second product is done with the tile before
+        const bool edge = e0 + kEntries > vis_min || !exists;
+        // Rows see their entries from the first on, so the first tile sets every reference that will be used, unless
+        // entries were missing there.
+        const bool unset = j == 0 || missed;
+        missed = !exists && e0 + entry < item.kv_end;
+        const F2 kf2 = f2_pack(kf, kf), lv2 = f2_pack(lv, lv), iv2 = f2_pack(iv, iv);
         const uint32_t row = p_at + (group >> 1) * kSlice + entry * 128;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(row + ((((group & 1) * 4 + i) ^ (entry & 7)) << 4)),
-                       "r"(p[4 * i]), "r"(p[4 * i + 1]), "r"(p[4 * i + 2]), "r"(p[4 * i + 3])
-                       : "memory");
+        for (int half = 0; half < 2; ++half) {  // 16 rows at a time, for the registers
+          const int cb = c0 + 16 * half;
+          float x[16];  // the exponents t - m
+          tmem_load16(tmem + lanes + sb * kN + cb, x);
+          if (half == 1) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_addr(&sh.s_free[sb]));
+          }
+          float most = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < 16; c += 4) {
+            const float4 rf = *reinterpret_cast<const float4*>(sh.rf + cb + c);
+            const float4 nm = *reinterpret_cast<const float4*>(sh.neg_m + cb + c);
+            const F2 y0 = f2_fma(f2_pack(x[c], x[c + 1]), f2_mul(kf2, f2_pack(rf.x, rf.y)), f2_add(lv2, f2_pack(nm.x, nm.y)));
+            const F2 y1 =
+                f2_fma(f2_pack(x[c + 2], x[c + 3]), f2_mul(kf2, f2_pack(rf.z, rf.w)), f2_add(lv2, f2_pack(nm.z, nm.w)));
+            f2_unpack(y0, x[c], x[c + 1]);
+            f2_unpack(y1, x[c + 2], x[c + 3]);
+          }
+          if (edge) {
+            const int e = exists ? static_cast<int>(e0 + entry) : 0x7FFFFFFF;
+#pragma unroll
+            for (int c = 0; c < 16; ++c)
+              if (e >= sh.vis[cb + c]) x[c] = -INFINITY;
+          }
+#pragma unroll
+          for (int c = 0; c < 16; ++c) most = fmaxf(most, x[c]);
+          if (group_any(bar, most > 14.0f || unset)) {  // raise the rows' references
+            float top = -INFINITY;
+#pragma unroll
+            for (int c = 0; c < 16; ++c) {
+              float y = x[c];
+#pragma unroll
+              for (int s = 16; s > 0; s >>= 1) y = fmaxf(y, __shfl_xor_sync(0xFFFFFFFFu, y, s));
+              if (lane == c) top = y;
+            }
+            if (lane < 16) sh.red[quarter][cb + lane] = top;
+            group_sync(bar);
+            if (quarter == 0 && lane < 16) {
+              const int c = cb + lane;
+              top = fmaxf(fmaxf(sh.red[0][c], sh.red[1][c]), fmaxf(sh.red[2][c], sh.red[3][c]));
+              // a row's first entry sets its reference, wherever that is; later ones only raise it
+              const bool fresh = sh.set[c] == 0 && top > -INFINITY;
+              const float up = fresh ? top - 6.0f : fmaxf(0.0f, top - 6.0f);
+              sh.neg_m[c] -= up;
+              sh.up[c] = up;
+              sh.fac[c] = fresh ? 1.0f : ex2(-up);
+              if (fresh) sh.set[c] = 1;
+            }
+            group_sync(bar);
+#pragma unroll
+            for (int c = 0; c < 16; ++c) {
+              x[c] -= sh.up[cb + c];
+              l[16 * half + c] *= sh.fac[cb + c];
+            }
+            if (j > 0) {
+              w.wait<kShort>(&sh.pv_done, (g & 1) ^ 1);
+              tc_fence_after();
+#pragma unroll 1
+              for (int b = 0; b < C::kBlocks; ++b) {
+                float o[16];
+                const uint32_t at = tmem + lanes + C::kOCol + b * kN + cb;
+                tmem_load16(at, o);
+#pragma unroll
+                for (int c = 0; c < 16; ++c) o[c] *= sh.fac[cb + c];
+                tmem_store16(at, o);
+              }
+              tc_fence_before();
+            }
+          }
+          uint32_t p[8];
+#pragma unroll
+          for (int c = 0; c < 16; c += 2) {
+            const float w0 = ex2(x[c]), w1 = ex2(x[c + 1]);
+            const F2 sum = f2_fma(f2_pack(w0, w1), iv2, f2_pack(l[16 * half + c], l[16 * half + c + 1]));
+            f2_unpack(sum, l[16 * half + c], l[16 * half + c + 1]);
+            p[c / 2] = pack_f16x2(w0, w1);
+          }
+          if (half == 0) w.wait<kShort>(&sh.pv_done, (g & 1) ^ 1);  // the second product is done with the tile before
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            asm volatile(
+                "st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(row + ((((group & 1) * 4 + half * 2 + i) ^ (entry & 7)) << 4)),
+                "r"(p[4 * i]), "r"(p[4 * i + 1]), "r"(p[4 * i + 2]), "r"(p[4 * i + 3])
+                : "memory");
+        }
         fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_addr(&sh.p_full));
@@ -441,9 +477,9 @@ __global__ __launch_bounds__((TcCfg<kD, kShared>::kThreads), 1) void q8_attn_tc_
           if (static_cast<uint32_t>(c) < rows) {
             if (item.part >= 0)
               a.part_ml[(static_cast<size_t>(item.part + static_cast<int>(item.chunk)) * H + h) * kN + c] =
-                  make_float2(sh.m[c], sum);
+                  make_float2(sum == 0.0f ? -3.4e38f : -sh.neg_m[c], sum);
             else if (a.lse != nullptr)
-              a.lse[sh.out_row[c]] = sum == 0.0f ? -INFINITY : (sh.m[c] + __log2f(sum)) * 0.69314718055994530942f;
+              a.lse[sh.out_row[c]] = sum == 0.0f ? -INFINITY : (__log2f(sum) - sh.neg_m[c]) * 0.69314718055994530942f;
           }
         }
         group_sync(bar);
@@ -454,18 +490,20 @@ __global__ __launch_bounds__((TcCfg<kD, kShared>::kThreads), 1) void q8_attn_tc_
 #pragma unroll 1
       for (int b = 0; b < C::kBlocks; ++b) {
         const int d = b * 128 + entry;  // this lane's channel
-        float o[32];
-        if (n_tiles > 0) {
-          tmem_load32(tmem + lanes + C::kOCol + b * kN + c0, o);
-        } else {
+        const int nan_at = any_nan && d < kD ? sh.nan[kShared ? 0 : d] : 0x7FFFFFFF;
+#pragma unroll 1
+        for (int cb = c0; cb < c0 + 32; cb += 16) {
+          float o[16];
+          if (n_tiles > 0) {
+            tmem_load16(tmem + lanes + C::kOCol + b * kN + cb, o);
+          } else {
 #pragma unroll
-          for (int c = 0; c < 32; ++c) o[c] = 0.0f;
-        }
-        if (d < kD) {
-          const int nan_at = any_nan ? sh.nan[kShared ? 0 : d] : 0x7FFFFFFF;
+            for (int c = 0; c < 16; ++c) o[c] = 0.0f;
+          }
+          if (d >= kD) continue;
 #pragma unroll
-          for (int c = 0; c < 32; ++c) {
-            const int n = c0 + c;
+          for (int c = 0; c < 16; ++c) {
+            const int n = cb + c;
             if (static_cast<uint32_t>(n) < rows) {
               float v = nan_at < sh.vis[n] ? __int_as_float(0x7FFFFFFF) : o[c];
               if (item.part >= 0) {
@@ -487,10 +525,11 @@ __global__ __launch_bounds__((TcCfg<kD, kShared>::kThreads), 1) void q8_attn_tc_
       auto scores = [&](uint32_t g) {
         const uint32_t st = g % C::kStages, use = g / C::kStages, sb = g & 1;
         w.wait<kShort>(&sh.s_free[sb], ((g >> 1) & 1) ^ 1);
+#pragma unroll 1
         for (int s = 0; s < C::kSlices; ++s) {
           w.wait<kShort>(&sh.k_full[st][s], use & 1);
           tc_fence_after();
-          if (lane == 0 && w.live) {
+          if (w.live && elect_one()) {
             const uint64_t ka = smem_operand(k_at + (st * C::kSlices + s) * kSlice, 0);
             const uint64_t qb = smem_operand(q_at + s * (kN * 128), 0);
 #pragma unroll
@@ -498,7 +537,7 @@ __global__ __launch_bounds__((TcCfg<kD, kShared>::kThreads), 1) void q8_attn_tc_
               tc_mma(tmem + sb * kN, ka + 2 * x, qb + 2 * x, mma_shape(128, kN, false, false), s > 0 || x > 0);
           }
         }
-        if (lane == 0) {
+        if (elect_one()) {
           if (!kShared) tc_commit(smem_addr(&sh.k_free[st][0]));
           tc_commit(smem_addr(&sh.s_full[sb]));
         }
@@ -513,7 +552,7 @@ __global__ __launch_bounds__((TcCfg<kD, kShared>::kThreads), 1) void q8_attn_tc_
             w.wait<kShort>(&sh.v_full[st][kD == 64 ? 0 : 2 * b + 1], use & 1);
           }
           tc_fence_after();
-          if (lane == 0) {
+          if (elect_one()) {
             if (w.live) {
               // 64 channels: both halves of M read the one slice, and the second is not used
               const uint64_t va = smem_operand(v_at + (st * C::kSlices + 2 * b) * kSlice, kD == 64 ? 0 : kSlice);
@@ -527,7 +566,7 @@ __global__ __launch_bounds__((TcCfg<kD, kShared>::kThreads), 1) void q8_attn_tc_
           }
           __syncwarp();
         }
-        if (lane == 0) {
+        if (elect_one()) {
           if (!kShared) tc_commit(smem_addr(&sh.v_free[st]));
           tc_commit(smem_addr(&sh.pv_done));
         }
@@ -549,7 +588,7 @@ __global__ __launch_bounds__((TcCfg<kD, kShared>::kThreads), 1) void q8_attn_tc_
   }
   if (warp == C::kWarps - 1) {
     // every product is done before its memory is given back
-    if (lane == 0) tc_commit(smem_addr(&sh.idle));
+    if (elect_one()) tc_commit(smem_addr(&sh.idle));
     __syncwarp();
     const bool done = warp_wait_for<false>(smem_addr(&sh.idle), 0, kWaitLimitNs);
     if (!done) w.live = false;
