@@ -224,7 +224,7 @@ int q8_attn_geom(const Q8Cache& c, uint32_t batch, uint32_t num_q, uint32_t n_he
   // and values of 512 channels do not fit its shared memory.
   g->tc = batch > 0 && static_cast<uint64_t>(num_q) * g->group >= 48ull * batch && (c.head_dim < 512 || c.v == nullptr);
   if (g->tc) {
-    g->rows = c.head_dim <= 128 ? 128 : 64;
+    g->rows = c.head_dim <= 128 ? 256 : 64;
     g->ctas = std::max<uint32_t>(1, static_cast<uint32_t>(sm_count()) / c.heads);
     g->start_cost = g->grain = g->round = 128;
     g->min_quota = 256;
@@ -848,7 +848,7 @@ int ckv_q8_attn(const ckv_q8_cache_t* cache, uint32_t n_heads, uint32_t ratio, f
   a.d_status = d_status;
   a.wait_ns = wait_limit_ns();
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  rc = a.g.tc ? launch_q8_attn_tc(a, s) : launch_split(a, s);
+  rc = !a.g.tc ? launch_split(a, s) : a.c.head_dim <= 128 ? launch_q8_attn_rows(a, s) : launch_q8_attn_tc(a, s);
   return rc ? rc : launch_combine(a, s);
 }
 

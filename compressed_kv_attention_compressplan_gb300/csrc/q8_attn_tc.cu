@@ -26,18 +26,15 @@
 // cycle, where the products alone are 1.0 k.
 #include <algorithm>
 
-#include "async_copy.cuh"
-#include "q8_plan.cuh"
-#include "tcgen05.cuh"
+#include "q8_tc.cuh"
 
 namespace ckv {
 namespace {
 
-constexpr int kEntries = 128;
-constexpr uint32_t kSlice = kEntries * 128;  // bytes of 64 channels of a tile in fp16
-
 template <int kD, bool kShared>
 struct TcCfg {
+  static constexpr bool kLatent = kShared;
+  static constexpr bool kGroupScales = false;
   static constexpr int kRows = kD <= 128 ? 128 : 64;
   static constexpr int kSlices = kD / 64;
   static constexpr int kBlocks = kD <= 128 ? 1 : kD / 128;  // accumulators of 128 channels
@@ -82,28 +79,6 @@ struct alignas(16) TcShared {
   uint32_t tmem;
 };
 
-// A wait that, once it has run out, lets the rest of the loop run without waiting: every barrier is
-// still reached, the kernel ends, and the status says so.  The limit is counted in SM clocks, two to a
-// nanosecond (about the highest rate, so a slower clock only waits longer): the roles hand tiles to one another all the
-// time, and a read of the global timer in a wait that misses its first probe costs more than the wait.
-struct Waiter {
-  long long limit;
-  bool live;
-  template <bool kShort>
-  __device__ __forceinline__ void wait(uint64_t* barrier, uint32_t parity) {
-    if (!live) return;
-    const uint32_t bar = smem_addr(barrier);
-    bool done = kShort ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity);
-    if (!done) {
-      const long long t0 = clock64();
-      do {
-        done = kShort ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity);
-      } while (!done && clock64() - t0 <= limit);
-    }
-    live = __all_sync(0xFFFFFFFFu, done);
-  }
-};
-
 __device__ __forceinline__ bool group_any(int id, bool x) {
   uint32_t r;
   asm volatile(
@@ -117,21 +92,6 @@ __device__ __forceinline__ bool group_any(int id, bool x) {
   return r != 0;
 }
 __device__ __forceinline__ void group_sync(int id) { asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory"); }
-
-// Takes the NaNs out of 16 channels of entry e: see the split kernel.  Out of line: it runs for next to no tile.
-__device__ __noinline__ uint4 without_nans(uint4 x, int e, int* nan, int step, int* any) {
-  uint32_t* y = reinterpret_cast<uint32_t*>(&x);
-  for (int z = 0; z < 4; ++z) {
-    const uint32_t bad = q8_nan_bytes(y[z]);
-    if (bad) {
-      for (int b = 0; b < 4; ++b)
-        if (bad >> (8 * b) & 1) atomicMin(nan + step * (4 * z + b), e);
-      *any = 1;
-      y[z] &= ~bad;
-    }
-  }
-  return x;
-}
 
 template <int kD, bool kShared, bool kShort>
 __global__ __launch_bounds__((TcCfg<kD, kShared>::kThreads), 1) void q8_attn_tc_kernel(const AttnArgs a) {
@@ -237,100 +197,7 @@ __global__ __launch_bounds__((TcCfg<kD, kShared>::kThreads), 1) void q8_attn_tc_
     __syncthreads();
 
     if (conv) {
-      // ---- e4m3 -> fp16 operands.  Lane l takes 16 channels, chunk l % 4 of a slice, of entries l / 4 + 8 * ...: the
-      // eight lanes of a store's phase take two entries, whose chunks the swizzle puts in different banks.
-      const int cw = warp - C::kSoftWarps, q = lane & 3;
-      const uint32_t tok = cw * 8 + (lane >> 2);             // load i: entry tok + 32 i
-      const uint32_t st0 = tok * 128 + (((2 * q) ^ (tok & 7)) << 4), st1 = tok * 128 + (((2 * q + 1) ^ (tok & 7)) << 4);
-      const uint8_t* src[C::kLoads];       // the K addresses of this tile's entries
-      const uint8_t* src_next[C::kLoads];  // and of the next one's
-      uint32_t here = 0, here_next = 0;    // bit i: load i's entry exists
-      bool bad = false;
-      // Block numbers are asked for a tile before the addresses are made from them, at places that always exist, so
-      // that no load here waits for another.
-      int32_t blk[C::kLoads];
-      auto ask = [&](uint32_t tile) {
-#pragma unroll
-        for (int i = 0; i < C::kLoads; ++i) {
-          const uint32_t e = item.kv_begin + tile * kEntries + tok + i * (8 * C::kConvWarps);
-          blk[i] = __ldg(table + (min(e, last) >> t_shift));
-        }
-      };
-      auto locate = [&](uint32_t tile, const uint8_t*(&o)[C::kLoads]) -> uint32_t {
-        uint32_t mask = 0;
-#pragma unroll
-        for (int i = 0; i < C::kLoads; ++i) {
-          const uint32_t e = item.kv_begin + tile * kEntries + tok + i * (8 * C::kConvWarps);
-          const bool in = tile < n_tiles && e < item.kv_end;
-          const bool ok = static_cast<uint32_t>(blk[i]) < a.c.num_blocks;  // negative ones are large
-          o[i] = a.c.k + (((static_cast<size_t>(ok ? blk[i] : 0) * H + h) << t_shift) + (e & (T - 1))) * kD + q * 16;
-          mask |= (in && ok ? 1u : 0u) << i;
-          bad |= in && !ok;
-        }
-        return mask;
-      };
-      const ptrdiff_t v_off = kShared ? 0 : a.c.v - a.c.k;
-      uint4 buf[C::kAhead][C::kLoads];
-      auto load = [&](uint4(&d)[C::kLoads], int unit, const uint8_t* const(&o)[C::kLoads], uint32_t mask) {
-        const ptrdiff_t at = unit < C::kSlices ? unit * 64 : v_off + (unit - C::kSlices) * 64;
-#pragma unroll
-        for (int i = 0; i < C::kLoads; ++i) d[i] = ld_stream16_if(o[i] + at, mask >> i & 1);
-      };
-      ask(0);
-      here = locate(0, src);
-      ask(1);
-#pragma unroll
-      for (int u = 0; u < C::kAhead; ++u) load(buf[u], u, src, here);
-      for (uint32_t j = 0; j < n_tiles; ++j) {
-        const uint32_t g = tiles_before + j, st = g % C::kStages, use = g / C::kStages;
-        const uint32_t e0 = item.kv_begin + j * kEntries;
-        const bool edge = e0 + kEntries > vis_min;
-        here_next = locate(j + 1, src_next);
-        ask(j + 2);
-#pragma unroll 1
-        for (int u0 = 0; u0 < C::kUnits; u0 += C::kAhead) {
-#pragma unroll
-          for (int x = 0; x < C::kAhead; ++x) {
-            const int u = u0 + x;
-            const bool is_v = u >= C::kSlices;
-            const int s = is_v ? u - C::kSlices : u;
-            if (is_v) {
-              if (s == 0) w.wait<kShort>(&sh.v_free[st], (use & 1) ^ 1);
-            } else if (kShared ? s % 2 == 0 : s == 0) {
-              w.wait<kShort>(&sh.k_free[st][kShared ? s / 2 : 0], (use & 1) ^ 1);
-            }
-            if ((is_v || kShared) && edge) {
-#pragma unroll
-              for (int i = 0; i < C::kLoads; ++i)
-                buf[x][i] = without_nans(buf[x][i], e0 + tok + i * (8 * C::kConvWarps),
-                                         kShared ? sh.nan : sh.nan + s * 64 + q * 16, kShared ? 0 : 1, &sh.any_nan);
-            }
-            const uint32_t dst = (is_v ? v_at : k_at) + (st * C::kSlices + s) * kSlice;
-#pragma unroll
-            for (int i = 0; i < C::kLoads; ++i) {
-              const uint4 y = buf[x][i];
-              asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(dst + st0 + i * (8 * C::kConvWarps) * 128),
-                           "r"(q8_lo_f16x2(y.x)), "r"(q8_hi_f16x2(y.x)), "r"(q8_lo_f16x2(y.y)), "r"(q8_hi_f16x2(y.y))
-                           : "memory");
-              asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(dst + st1 + i * (8 * C::kConvWarps) * 128),
-                           "r"(q8_lo_f16x2(y.z)), "r"(q8_hi_f16x2(y.z)), "r"(q8_lo_f16x2(y.w)), "r"(q8_hi_f16x2(y.w))
-                           : "memory");
-            }
-            fence_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_addr(is_v ? &sh.v_full[st][s] : &sh.k_full[st][s]));
-            // the slice that is kAhead units on, of this tile or the next
-            if (u0 + C::kAhead < C::kUnits)
-              load(buf[x], u + C::kAhead, src, here);
-            else
-              load(buf[x], x, src_next, here_next);
-          }
-        }
-        here = here_next;
-#pragma unroll
-        for (int i = 0; i < C::kLoads; ++i) src[i] = src_next[i];
-      }
-      if (bad) status_or(a.d_status, CKV_STATUS_BAD_INDEX);
+      convert_tiles<C, kShort>(a, item, sh, w, warp - C::kSoftWarps, h, table, n_tiles, tiles_before, vis_min, k_at, v_at);
     } else if (soft) {
       // ---- softmax of 32 rows (columns of S^T); this thread's entry is its lane
       const int group = warp >> 2, quarter = warp & 3, bar = 1 + group;
@@ -613,8 +480,6 @@ int launch(const AttnArgs& a, cudaStream_t s) {
 int launch_q8_attn_tc(const AttnArgs& a, cudaStream_t s) {
   const bool shared = a.c.v == nullptr;
   switch (a.c.head_dim) {
-    case 64: return shared ? launch<64, true>(a, s) : launch<64, false>(a, s);
-    case 128: return shared ? launch<128, true>(a, s) : launch<128, false>(a, s);
     case 256: return shared ? launch<256, true>(a, s) : launch<256, false>(a, s);
     default: return shared ? launch<512, true>(a, s) : CKV_ERR_SIZE;
   }

@@ -115,7 +115,8 @@ __device__ __forceinline__ uint32_t without_nan(uint32_t w, int e, int* s_nan, i
   return w & ~bad;
 }
 
-// The tensor-core kernel, for tiles of many rows (g.tc); the parts that it leaves are joined by the caller.
-int launch_q8_attn_tc(const AttnArgs& a, cudaStream_t s);
+// The tensor-core kernels, for tiles of many rows (g.tc); the parts that they leave are joined by the caller.
+int launch_q8_attn_tc(const AttnArgs& a, cudaStream_t s);    // 256 channels and more
+int launch_q8_attn_rows(const AttnArgs& a, cudaStream_t s);  // up to 128 channels
 
 }  // namespace ckv
