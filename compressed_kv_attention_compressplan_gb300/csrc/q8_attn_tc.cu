@@ -1,29 +1,26 @@
 // q8_attn_tc.cu -- attention over the 8-bit paged cache on the 5th-generation
-// tensor cores, for tiles of many rows: prefill chunks, and decode where many
-// heads share one latent cache.  The mathematics is the split kernel's.
+// tensor cores from 256 channels on: decode where many heads share one latent
+// cache, and prefill chunks.  The mathematics is the split kernel's.
 //
 // Transposed products.  A tile is 128 entries, the M of both products:
-//     S^T [128 entries x N rows] = K8 Q^T,   O^T [128 channels x N rows] += V8^T W^T,
-// one O^T per 128 channels.  With entries on the lanes of tensor memory and rows
-// on its columns, a thread owns one entry: the entry's scales are two registers
-// of its own, row sums stay in registers until the end, and no score crosses
-// lanes but in the rare step that raises a row's reference (one vote a tile asks
-// for it).  The accumulator of 512 channels by 64 rows takes 256 columns, so
-// the whole width of a latent entry fits beside the scores; the weights W^T go
-// through shared memory as they stand, an entry's row of N weights being the
+//     S^T [128 entries x 64 rows] = K8 Q^T,   O^T [128 channels x 64 rows] += V8^T W^T,
+// one O^T per 128 channels.  The accumulators of 512 channels by 64 rows take
+// 256 columns of tensor memory, so the whole width of a latent entry fits beside the
+// scores and its keys are read and multiplied once.  With entries on the lanes a
+// thread owns one entry: the entry's scales are two registers of its own, row sums
+// stay in registers until the end, and no score crosses lanes but in the rare step
+// that raises a row's reference (one vote a tile asks for it).  The weights W^T go
+// through shared memory as they stand, an entry's row of 64 weights being the
 // swizzled row that the second product reads.
 //
-// Roles.  Converting warps load e4m3 from memory into registers, a few slices of
-// 64 channels ahead, and store them as fp16 (exact) in the operands' swizzled
-// layout; one thread issues the products; groups of four warps take 32 rows
-// each through the softmax.  K and V have buffers of their own, two each where
-// they fit, so the products of a tile overlap the softmax of the one before; in a latent
-// cache one buffer is both operands, and its slices are handed back as the
-// second product finishes with them.
+// Roles.  Eight warps turn e4m3 into fp16 operands (q8_tc.cuh); one thread issues the
+// products; groups of four warps take 16 rows each through the softmax.  In a latent
+// cache one buffer is both operands, and its slices are handed back as the second
+// product finishes with them.
 //
-// Bound.  Shared memory feeds everything: for 128 channels and 128 rows a tile
-// writes 96 KB and the products read 128 KB, about 1.8 k cycles at 128 bytes a
-// cycle, where the products alone are 1.0 k.
+// Bound.  Of 512 channels one tile fits in shared memory, so a tile's conversion, products
+// and softmax follow one another: the second product's blocks overlap the next tile's
+// conversion, the first product's slices the rest of it.
 #include <algorithm>
 
 #include "q8_tc.cuh"
@@ -33,26 +30,27 @@ namespace {
 
 template <int kD, bool kShared>
 struct TcCfg {
+  static_assert(kD == 256 || kD == 512, "");
   static constexpr bool kLatent = kShared;
   static constexpr bool kGroupScales = false;
-  static constexpr int kRows = kD <= 128 ? 128 : 64;
+  static constexpr int kRows = 64;
   static constexpr int kSlices = kD / 64;
-  static constexpr int kBlocks = kD <= 128 ? 1 : kD / 128;  // accumulators of 128 channels
-  static constexpr int kStages = kShared ? (kD <= 256 ? 2 : 1) : (kD <= 128 ? 2 : 1);
+  static constexpr int kBlocks = kD / 128;  // accumulators of 128 channels
+  static constexpr int kStages = kShared && kD == 256 ? 2 : 1;
   static constexpr bool kLag = kStages == 2 || !kShared;  // the second product runs a tile behind the first
   static constexpr int kFree = kShared ? kBlocks : 1;     // barriers that hand a K stage back
-  static constexpr int kGroups = kRows / 32;              // softmax groups of four warps
+  static constexpr int kGroups = kRows / 16;              // softmax groups of four warps
   static constexpr int kSoftWarps = 4 * kGroups;
-  static constexpr int kConvWarps = 4;
+  static constexpr int kConvWarps = 8;
   static constexpr int kWarps = kSoftWarps + kConvWarps + 1;
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kLoads = kEntries / (8 * kConvWarps);  // 16-byte loads of a converting thread per slice
   static constexpr int kUnits = kSlices * (kShared ? 1 : 2);  // slices of a tile, K's and V's
-  static constexpr int kAhead = kUnits < 2 ? 1 : kD <= 128 ? 2 : 4;
+  static constexpr int kAhead = 4;
   static constexpr uint32_t kQBytes = kSlices * kRows * 128;
   static constexpr uint32_t kKBytes = kStages * kSlices * kSlice;
   static constexpr uint32_t kVBytes = kShared ? 0 : kKBytes;
-  static constexpr uint32_t kPBytes = kRows / 64 * kSlice;
+  static constexpr uint32_t kPBytes = kSlice;
   static constexpr uint32_t kBytes = kQBytes + kKBytes + kVBytes + kPBytes + 1024;  // and the alignment
   // one CTA to an SM: a second would wait for the first one's tensor memory
   static constexpr uint32_t kSmem = kBytes < 120 * 1024 ? 120 * 1024 : kBytes;
@@ -199,13 +197,13 @@ __global__ __launch_bounds__((TcCfg<kD, kShared>::kThreads), 1) void q8_attn_tc_
     if (conv) {
       convert_tiles<C, kShort>(a, item, sh, w, warp - C::kSoftWarps, h, table, n_tiles, tiles_before, vis_min, k_at, v_at);
     } else if (soft) {
-      // ---- softmax of 32 rows (columns of S^T); this thread's entry is its lane
+      // ---- softmax of 16 rows (columns of S^T); this thread's entry is its lane
       const int group = warp >> 2, quarter = warp & 3, bar = 1 + group;
-      const int c0 = group * 32, entry = quarter * 32 + lane;
+      const int c0 = group * 16, entry = quarter * 32 + lane;
       const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
-      float l[32];
+      float l[16];
 #pragma unroll
-      for (int c = 0; c < 32; ++c) l[c] = 0.0f;
+      for (int c = 0; c < 16; ++c) l[c] = 0.0f;
       // the entry's block is asked for a tile ahead of its scales, and those a tile ahead of their use
       auto block_of = [&](uint32_t tile) { return __ldg(table + (min(item.kv_begin + tile * kEntries + entry, last) >> t_shift)); };
       auto valid = [&](int32_t b) { return static_cast<uint32_t>(b) < a.c.num_blocks; };
@@ -232,95 +230,89 @@ __global__ __launch_bounds__((TcCfg<kD, kShared>::kThreads), 1) void q8_attn_tc_
         const bool unset = j == 0 || missed;
         missed = !exists && e0 + entry < item.kv_end;
         const F2 kf2 = f2_pack(kf, kf), lv2 = f2_pack(lv, lv), iv2 = f2_pack(iv, iv);
-        const uint32_t row = p_at + (group >> 1) * kSlice + entry * 128;
+        const uint32_t row = p_at + entry * 128;
+        float x[16];  // the exponents t - m
+        tmem_load16(tmem + lanes + sb * kN + c0, x);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&sh.s_free[sb]));
+        float most = -INFINITY;
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {  // 16 rows at a time, for the registers
-          const int cb = c0 + 16 * half;
-          float x[16];  // the exponents t - m
-          tmem_load16(tmem + lanes + sb * kN + cb, x);
-          if (half == 1) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_addr(&sh.s_free[sb]));
-          }
-          float most = -INFINITY;
-#pragma unroll
-          for (int c = 0; c < 16; c += 4) {
-            const float4 rf = *reinterpret_cast<const float4*>(sh.rf + cb + c);
-            const float4 nm = *reinterpret_cast<const float4*>(sh.neg_m + cb + c);
-            const F2 y0 = f2_fma(f2_pack(x[c], x[c + 1]), f2_mul(kf2, f2_pack(rf.x, rf.y)), f2_add(lv2, f2_pack(nm.x, nm.y)));
-            const F2 y1 =
-                f2_fma(f2_pack(x[c + 2], x[c + 3]), f2_mul(kf2, f2_pack(rf.z, rf.w)), f2_add(lv2, f2_pack(nm.z, nm.w)));
-            f2_unpack(y0, x[c], x[c + 1]);
-            f2_unpack(y1, x[c + 2], x[c + 3]);
-          }
-          if (edge) {
-            const int e = exists ? static_cast<int>(e0 + entry) : 0x7FFFFFFF;
-#pragma unroll
-            for (int c = 0; c < 16; ++c)
-              if (e >= sh.vis[cb + c]) x[c] = -INFINITY;
-          }
-#pragma unroll
-          for (int c = 0; c < 16; ++c) most = fmaxf(most, x[c]);
-          if (group_any(bar, most > 14.0f || unset)) {  // raise the rows' references
-            float top = -INFINITY;
-#pragma unroll
-            for (int c = 0; c < 16; ++c) {
-              float y = x[c];
-#pragma unroll
-              for (int s = 16; s > 0; s >>= 1) y = fmaxf(y, __shfl_xor_sync(0xFFFFFFFFu, y, s));
-              if (lane == c) top = y;
-            }
-            if (lane < 16) sh.red[quarter][cb + lane] = top;
-            group_sync(bar);
-            if (quarter == 0 && lane < 16) {
-              const int c = cb + lane;
-              top = fmaxf(fmaxf(sh.red[0][c], sh.red[1][c]), fmaxf(sh.red[2][c], sh.red[3][c]));
-              // a row's first entry sets its reference, wherever that is; later ones only raise it
-              const bool fresh = sh.set[c] == 0 && top > -INFINITY;
-              const float up = fresh ? top - 6.0f : fmaxf(0.0f, top - 6.0f);
-              sh.neg_m[c] -= up;
-              sh.up[c] = up;
-              sh.fac[c] = fresh ? 1.0f : ex2(-up);
-              if (fresh) sh.set[c] = 1;
-            }
-            group_sync(bar);
-#pragma unroll
-            for (int c = 0; c < 16; ++c) {
-              x[c] -= sh.up[cb + c];
-              l[16 * half + c] *= sh.fac[cb + c];
-            }
-            if (j > 0) {
-              w.wait<kShort>(&sh.pv_done, (g & 1) ^ 1);
-              tc_fence_after();
-#pragma unroll 1
-              for (int b = 0; b < C::kBlocks; ++b) {
-                float o[16];
-                const uint32_t at = tmem + lanes + C::kOCol + b * kN + cb;
-                tmem_load16(at, o);
-#pragma unroll
-                for (int c = 0; c < 16; ++c) o[c] *= sh.fac[cb + c];
-                tmem_store16(at, o);
-              }
-              tc_fence_before();
-            }
-          }
-          uint32_t p[8];
-#pragma unroll
-          for (int c = 0; c < 16; c += 2) {
-            const float w0 = ex2(x[c]), w1 = ex2(x[c + 1]);
-            const F2 sum = f2_fma(f2_pack(w0, w1), iv2, f2_pack(l[16 * half + c], l[16 * half + c + 1]));
-            f2_unpack(sum, l[16 * half + c], l[16 * half + c + 1]);
-            p[c / 2] = pack_f16x2(w0, w1);
-          }
-          if (half == 0) w.wait<kShort>(&sh.pv_done, (g & 1) ^ 1);  // the second product is done with the tile before
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-            asm volatile(
-                "st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(row + ((((group & 1) * 4 + half * 2 + i) ^ (entry & 7)) << 4)),
-                "r"(p[4 * i]), "r"(p[4 * i + 1]), "r"(p[4 * i + 2]), "r"(p[4 * i + 3])
-                : "memory");
+        for (int c = 0; c < 16; c += 4) {
+          const float4 rf = *reinterpret_cast<const float4*>(sh.rf + c0 + c);
+          const float4 nm = *reinterpret_cast<const float4*>(sh.neg_m + c0 + c);
+          const F2 y0 = f2_fma(f2_pack(x[c], x[c + 1]), f2_mul(kf2, f2_pack(rf.x, rf.y)), f2_add(lv2, f2_pack(nm.x, nm.y)));
+          const F2 y1 =
+              f2_fma(f2_pack(x[c + 2], x[c + 3]), f2_mul(kf2, f2_pack(rf.z, rf.w)), f2_add(lv2, f2_pack(nm.z, nm.w)));
+          f2_unpack(y0, x[c], x[c + 1]);
+          f2_unpack(y1, x[c + 2], x[c + 3]);
         }
+        if (edge) {
+          const int e = exists ? static_cast<int>(e0 + entry) : 0x7FFFFFFF;
+#pragma unroll
+          for (int c = 0; c < 16; ++c)
+            if (e >= sh.vis[c0 + c]) x[c] = -INFINITY;
+        }
+#pragma unroll
+        for (int c = 0; c < 16; ++c) most = fmaxf(most, x[c]);
+        if (group_any(bar, most > 14.0f || unset)) {  // raise the rows' references
+          float top = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < 16; ++c) {
+            float y = x[c];
+#pragma unroll
+            for (int s = 16; s > 0; s >>= 1) y = fmaxf(y, __shfl_xor_sync(0xFFFFFFFFu, y, s));
+            if (lane == c) top = y;
+          }
+          if (lane < 16) sh.red[quarter][c0 + lane] = top;
+          group_sync(bar);
+          if (quarter == 0 && lane < 16) {
+            const int c = c0 + lane;
+            top = fmaxf(fmaxf(sh.red[0][c], sh.red[1][c]), fmaxf(sh.red[2][c], sh.red[3][c]));
+            // a row's first entry sets its reference, wherever that is; later ones only raise it
+            const bool fresh = sh.set[c] == 0 && top > -INFINITY;
+            const float up = fresh ? top - 6.0f : fmaxf(0.0f, top - 6.0f);
+            sh.neg_m[c] -= up;
+            sh.up[c] = up;
+            sh.fac[c] = fresh ? 1.0f : ex2(-up);
+            if (fresh) sh.set[c] = 1;
+          }
+          group_sync(bar);
+#pragma unroll
+          for (int c = 0; c < 16; ++c) {
+            x[c] -= sh.up[c0 + c];
+            l[c] *= sh.fac[c0 + c];
+          }
+          if (j > 0) {
+            w.wait<kShort>(&sh.pv_done, (g & 1) ^ 1);
+            tc_fence_after();
+#pragma unroll 1
+            for (int b = 0; b < C::kBlocks; ++b) {
+              float o[16];
+              const uint32_t at = tmem + lanes + C::kOCol + b * kN + c0;
+              tmem_load16(at, o);
+#pragma unroll
+              for (int c = 0; c < 16; ++c) o[c] *= sh.fac[c0 + c];
+              tmem_store16(at, o);
+            }
+            tc_fence_before();
+          }
+        }
+        uint32_t p[8];
+#pragma unroll
+        for (int c = 0; c < 16; c += 2) {
+          const float w0 = ex2(x[c]), w1 = ex2(x[c + 1]);
+          const F2 sum = f2_fma(f2_pack(w0, w1), iv2, f2_pack(l[c], l[c + 1]));
+          f2_unpack(sum, l[c], l[c + 1]);
+          p[c / 2] = pack_f16x2(w0, w1);
+        }
+        w.wait<kShort>(&sh.pv_done, (g & 1) ^ 1);  // the second product is done with the tile before
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          asm volatile(
+              "st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(row + (((group * 2 + i) ^ (entry & 7)) << 4)),
+              "r"(p[4 * i]), "r"(p[4 * i + 1]), "r"(p[4 * i + 2]), "r"(p[4 * i + 3])
+              : "memory");
         fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_addr(&sh.p_full));
@@ -329,15 +321,15 @@ __global__ __launch_bounds__((TcCfg<kD, kShared>::kThreads), 1) void q8_attn_tc_
       {
         float mine = 0.0f;
 #pragma unroll
-        for (int c = 0; c < 32; ++c) {
+        for (int c = 0; c < 16; ++c) {
           float x = l[c];
 #pragma unroll
           for (int s = 16; s > 0; s >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, s);
           if (lane == c) mine = x;
         }
-        sh.red[quarter][c0 + lane] = mine;
+        if (lane < 16) sh.red[quarter][c0 + lane] = mine;
         group_sync(bar);
-        if (quarter == 0) {
+        if (quarter == 0 && lane < 16) {
           const int c = c0 + lane;
           const float sum = (sh.red[0][c] + sh.red[1][c]) + (sh.red[2][c] + sh.red[3][c]);
           sh.fac[c] = sum == 0.0f ? 0.0f : __fdiv_rn(1.0f, sum);
@@ -357,31 +349,27 @@ __global__ __launch_bounds__((TcCfg<kD, kShared>::kThreads), 1) void q8_attn_tc_
 #pragma unroll 1
       for (int b = 0; b < C::kBlocks; ++b) {
         const int d = b * 128 + entry;  // this lane's channel
-        const int nan_at = any_nan && d < kD ? sh.nan[kShared ? 0 : d] : 0x7FFFFFFF;
-#pragma unroll 1
-        for (int cb = c0; cb < c0 + 32; cb += 16) {
-          float o[16];
-          if (n_tiles > 0) {
-            tmem_load16(tmem + lanes + C::kOCol + b * kN + cb, o);
-          } else {
+        const int nan_at = any_nan ? sh.nan[kShared ? 0 : d] : 0x7FFFFFFF;
+        float o[16];
+        if (n_tiles > 0) {
+          tmem_load16(tmem + lanes + C::kOCol + b * kN + c0, o);
+        } else {
 #pragma unroll
-            for (int c = 0; c < 16; ++c) o[c] = 0.0f;
-          }
-          if (d >= kD) continue;
+          for (int c = 0; c < 16; ++c) o[c] = 0.0f;
+        }
 #pragma unroll
-          for (int c = 0; c < 16; ++c) {
-            const int n = cb + c;
-            if (static_cast<uint32_t>(n) < rows) {
-              float v = nan_at < sh.vis[n] ? __int_as_float(0x7FFFFFFF) : o[c];
-              if (item.part >= 0) {
-                a.part_o[((static_cast<size_t>(item.part + static_cast<int>(item.chunk)) * H + h) * kN + n) * kD + d] = v;
-              } else {
-                v *= sh.fac[n];
-                if (a.out_f32)
-                  static_cast<float*>(a.out)[sh.out_row[n] * kD + d] = v;
-                else
-                  static_cast<__nv_bfloat16*>(a.out)[sh.out_row[n] * kD + d] = __float2bfloat16_rn(v);
-              }
+        for (int c = 0; c < 16; ++c) {
+          const int n = c0 + c;
+          if (static_cast<uint32_t>(n) < rows) {
+            float v = nan_at < sh.vis[n] ? __int_as_float(0x7FFFFFFF) : o[c];
+            if (item.part >= 0) {
+              a.part_o[((static_cast<size_t>(item.part + static_cast<int>(item.chunk)) * H + h) * kN + n) * kD + d] = v;
+            } else {
+              v *= sh.fac[n];
+              if (a.out_f32)
+                static_cast<float*>(a.out)[sh.out_row[n] * kD + d] = v;
+              else
+                static_cast<__nv_bfloat16*>(a.out)[sh.out_row[n] * kD + d] = __float2bfloat16_rn(v);
             }
           }
         }
@@ -415,15 +403,14 @@ __global__ __launch_bounds__((TcCfg<kD, kShared>::kThreads), 1) void q8_attn_tc_
         w.wait<kShort>(&sh.p_full, g & 1);
         for (int b = 0; b < C::kBlocks; ++b) {
           if (!kShared) {
-            w.wait<kShort>(&sh.v_full[st][kD == 64 ? 0 : 2 * b], use & 1);
-            w.wait<kShort>(&sh.v_full[st][kD == 64 ? 0 : 2 * b + 1], use & 1);
+            w.wait<kShort>(&sh.v_full[st][2 * b], use & 1);
+            w.wait<kShort>(&sh.v_full[st][2 * b + 1], use & 1);
           }
           tc_fence_after();
           if (elect_one()) {
             if (w.live) {
-              // 64 channels: both halves of M read the one slice, and the second is not used
-              const uint64_t va = smem_operand(v_at + (st * C::kSlices + 2 * b) * kSlice, kD == 64 ? 0 : kSlice);
-              const uint64_t pb = smem_operand(p_at, kSlice);
+              const uint64_t va = smem_operand(v_at + (st * C::kSlices + 2 * b) * kSlice, kSlice);
+              const uint64_t pb = smem_operand(p_at, 0);
 #pragma unroll
               for (int x = 0; x < 8; ++x)  // 16 entries, 16 rows of 128 bytes
                 tc_mma(tmem + C::kOCol + b * kN, va + 128 * x, pb + 128 * x, mma_shape(128, kN, true, true),
