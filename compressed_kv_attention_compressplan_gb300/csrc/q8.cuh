@@ -16,6 +16,8 @@
 // fp32's range (see the attention kernel's weights).
 #pragma once
 
+#include <atomic>
+
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
@@ -68,6 +70,20 @@ inline bool aligned_to(const void* p, uintptr_t n) {
 inline int check_table(const int32_t* table, uint64_t stride, uint32_t num_reqs) {
   if (stride == 0 || stride > 0x7FFFFFFFull || num_reqs == 0) return CKV_ERR_SIZE;
   return aligned_to(table, 4) ? CKV_OK : CKV_ERR_POINTER;
+}
+
+// Lets `kernel` use `bytes` of shared memory; asked of the driver once a device (`done`: a bit for each).
+inline int allow_smem(const void* kernel, uint32_t bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return CKV_ERR_LAUNCH;
+  const uint64_t bit = dev >= 0 && dev < 64 ? 1ull << dev : 0;
+  if (done.load(std::memory_order_relaxed) & bit) return CKV_OK;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes)) != cudaSuccess) {
+    cudaGetLastError();
+    return CKV_ERR_LAUNCH;
+  }
+  done.fetch_or(bit, std::memory_order_relaxed);
+  return CKV_OK;
 }
 
 // ---------------------------------------------------------------- e4m3
@@ -181,6 +197,73 @@ __device__ __forceinline__ int64_t q8_visible(int64_t kv_len, uint32_t after, ui
   return v < 0 ? 0 : v;
 }
 
+// ---------------------------------------------------------------- fragments
+// fp16 x fp16 -> fp32, 16 x 8 x 16
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Byte offset of 16-byte chunk cc of token t in a tile of 16 kDw-byte rows.  The
+// chunks of a 128-byte line are permuted by the token (or line), so that both
+// the K fragments' reads (2 tokens, 4 chunks of each) and the V fragments'
+// (4 tokens, 2 chunks) take every bank once.
+template <int kDw>
+__device__ __forceinline__ uint32_t tile_off(uint32_t t, uint32_t cc) {
+  if (kDw == 64) {
+    const uint32_t line = t >> 1, pos = (t & 1) * 4 + cc;
+    return line * 128 + ((pos ^ (line & 7)) << 4);
+  }
+  const uint32_t line = t * (kDw / 128) + (cc >> 3);
+  return line * 128 + (((cc & 7) ^ (t & 7)) << 4);
+}
+
+// Chunk j of the kDw / 64 that lane (g, q) = (lane / 4, lane % 4) multiplies per entry.
+template <int kDw>
+__device__ __forceinline__ int lane_chunk(int j, int q) {
+  return kDw == 64 ? q : 8 * (j >> 1) + 2 * q + (j & 1);
+}
+
+// A query row's part of the fragments (r: 0 for the lane's row g, 1 for g + 8): scaled by a power of two that puts
+// the row's largest value in [2^14, 2^15) and rounded to fp16; returns what undoes the scaling.
+template <int kDw>
+__device__ __forceinline__ float load_query(const __nv_bfloat16* p, bool in, int q, int r, uint32_t (&qf)[kDw / 16][4]) {
+  uint4 v[kDw / 64][2];
+  float m = 0.0f;
+#pragma unroll
+  for (int j = 0; j < kDw / 64; ++j) {
+    const int cc = lane_chunk<kDw>(j, q);
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      v[j][w] = in ? ld_cached16(p + cc * 16 + w * 8) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(unpack<__nv_bfloat16>(v[j][w], e)));
+    }
+  }
+  m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+  m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+  const int ex = min(126, 14 - (static_cast<int>(__float_as_uint(m) >> 23) - 127));
+  const float up = pow2f(ex);
+#pragma unroll
+  for (int j = 0; j < kDw / 64; ++j) {
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {  // k step 4 j + s: channels 4 s .. 4 s + 3 of the chunk
+      const uint4 x = v[j][s >> 1];
+      const int e = (s & 1) * 4;
+      qf[j * 4 + s][r] = pack_f16x2(unpack<__nv_bfloat16>(x, e) * up, unpack<__nv_bfloat16>(x, e + 1) * up);
+      qf[j * 4 + s][2 + r] = pack_f16x2(unpack<__nv_bfloat16>(x, e + 2) * up, unpack<__nv_bfloat16>(x, e + 3) * up);
+    }
+  }
+  return pow2f(-ex);
+}
+
 // ---------------------------------------------------------------- copies
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
   // bytes 16, or 0 to write zeros (src is not read then)
@@ -231,6 +314,23 @@ __device__ __forceinline__ uint32_t lds_u32(uint32_t a) {
 }
 __device__ __forceinline__ void sts_u32(uint32_t a, uint32_t v) {
   asm volatile("st.shared.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
+}
+
+// Scores of 16 query rows against the 16 entries of a tile at shared address st: s[n] are entries 8 n .. 8 n + 7.
+template <int kDw>
+__device__ __forceinline__ void tile_scores(uint32_t st, int g, int q, const uint32_t (&qf)[kDw / 16][4], float (&s)[2][4]) {
+#pragma unroll
+  for (int n = 0; n < 2; ++n) {
+    s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.0f;
+#pragma unroll
+    for (int j = 0; j < kDw / 64; ++j) {
+      const uint4 w = lds16(st + tile_off<kDw>(n * 8 + g, lane_chunk<kDw>(j, q)));
+      mma_f16(s[n], qf[j * 4 + 0], q8_lo_f16x2(w.x), q8_hi_f16x2(w.x));
+      mma_f16(s[n], qf[j * 4 + 1], q8_lo_f16x2(w.y), q8_hi_f16x2(w.y));
+      mma_f16(s[n], qf[j * 4 + 2], q8_lo_f16x2(w.z), q8_hi_f16x2(w.z));
+      mma_f16(s[n], qf[j * 4 + 3], q8_lo_f16x2(w.w), q8_hi_f16x2(w.w));
+    }
+  }
 }
 
 }  // namespace ckv

@@ -30,8 +30,6 @@ namespace ckv {
 // ------------------------------------------------------------------- plan
 namespace {
 
-constexpr int kPlanThreads = 1024;
-
 struct AttnPlanArgs {
   const int64_t* rid;
   const int64_t* seq_lens;
@@ -45,10 +43,12 @@ struct AttnPlanArgs {
   uint32_t* d_status;
 };
 
-// One CTA: requests are scanned once, then tiles in strips of 1024.
+// One CTA: requests are scanned once, then tiles in strips of kPlanThreads.  256 threads where the batch lets them:
+// the block-wide scans are what the kernel's time is made of.
+template <int kPlanThreads>
 __global__ __launch_bounds__(kPlanThreads) void plan_q8_attn_kernel(const AttnPlanArgs a) {
-  __shared__ uint32_t s_rid[CKV_MAX_BATCH], s_qs[CKV_MAX_BATCH], s_ql[CKV_MAX_BATCH], s_kv[CKV_MAX_BATCH],
-      s_ph[CKV_MAX_BATCH], s_tile[CKV_MAX_BATCH];
+  __shared__ uint32_t s_rid[kPlanThreads], s_qs[kPlanThreads], s_ql[kPlanThreads], s_kv[kPlanThreads],
+      s_ph[kPlanThreads], s_tile[kPlanThreads];
   __shared__ unsigned long long s_pos[kPlanThreads];
   __shared__ uint32_t s_item[kPlanThreads], s_part[kPlanThreads];
   __shared__ unsigned long long s_scan[kPlanThreads / 32 + 1];
@@ -252,27 +252,6 @@ int q8_attn_geom(const Q8Cache& c, uint32_t batch, uint32_t num_q, uint32_t n_he
 namespace {
 
 // ----------------------------------------------------------------- attention
-__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-// Byte offset of 16-byte chunk cc of token t in a tile of kDw-byte rows.  The
-// chunks of a 128-byte line are permuted by the token (or line), so that both
-// the K fragments' reads (2 tokens, 4 chunks of each) and the V fragments'
-// (4 tokens, 2 chunks) take every bank once.
-template <int kDw>
-__device__ __forceinline__ uint32_t tile_off(uint32_t t, uint32_t cc) {
-  if (kDw == 64) {
-    const uint32_t line = t >> 1, pos = (t & 1) * 4 + cc;
-    return line * 128 + ((pos ^ (line & 7)) << 4);
-  }
-  const uint32_t line = t * (kDw / 128) + (cc >> 3);
-  return line * 128 + (((cc & 7) ^ (t & 7)) << 4);
-}
-
 // Fragments.  A warp's 16 rows are the MMA's m, 16 entries its n (scores) and k
 // (values).  Sums over k may run in any order, so lane (g, q) = (lane / 4, lane % 4)
 // takes as the k of its score fragments 16 consecutive channels of entry g, i.e. the
@@ -286,7 +265,6 @@ template <int kDw, int kNp, bool kShared>
 __global__ __launch_bounds__(kAttnThreads, (Cfg<kDw, kNp, kShared>::kPerSm)) void q8_attn_kernel(const AttnArgs a) {
   using C = Cfg<kDw, kNp, kShared>;
   constexpr int kChunks = kDw / 16;  // 16-byte chunks of a row part
-  constexpr int kKj = kDw / 64;      // chunks a lane multiplies per entry
   constexpr int kOt = kDw / 8;       // output column tiles
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float s_m[C::kGroups][16], s_l[C::kGroups][16];
@@ -310,7 +288,7 @@ __global__ __launch_bounds__(kAttnThreads, (Cfg<kDw, kNp, kShared>::kPerSm)) voi
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, q = lane & 3;
   const int grp = warp / kNp, half = warp % kNp;
-  const uint32_t G = a.g.group, H = a.c.heads, T = a.c.block_tokens;
+  const uint32_t G = a.g.group, H = a.c.heads, T = a.c.block_tokens, t_shift = __ffs(T) - 1;
   const uint32_t ring = smem_addr(smem) + warp * C::kStages * C::kStageBytes;
 
   for (uint32_t it = item0; it < item1; ++it) {
@@ -329,7 +307,7 @@ __global__ __launch_bounds__(kAttnThreads, (Cfg<kDw, kNp, kShared>::kPerSm)) voi
     const uint32_t n_all = item.kv_end > item.kv_begin ? (item.kv_end - item.kv_begin + kTile - 1) / kTile : 0;
     const uint32_t n_mine = n_all > static_cast<uint32_t>(grp) ? (n_all - grp + C::kGroups - 1) / C::kGroups : 0;
     auto entry_of = [&](uint32_t i) { return item.kv_begin + (grp + i * C::kGroups) * kTile; };
-    auto block_at = [&](uint32_t i) -> int32_t { return i < n_mine ? __ldg(table + entry_of(i) / T) : -1; };
+    auto block_at = [&](uint32_t i) -> int32_t { return i < n_mine ? __ldg(table + (entry_of(i) >> t_shift)) : -1; };
     int32_t blocks_now = block_at(lane), blocks_next = block_at(32 + lane);
     bool bad_block = false;
     auto issue = [&](uint32_t i) {
@@ -343,7 +321,7 @@ __global__ __launch_bounds__(kAttnThreads, (Cfg<kDw, kNp, kShared>::kPerSm)) voi
         bad_block |= !ok;
         const uint32_t e0 = entry_of(i);
         const size_t bh = static_cast<size_t>(ok ? b : 0) * H + h;
-        const size_t base = (bh * T + e0 % T) * C::kD + half * kDw;
+        const size_t base = ((bh << t_shift) + (e0 & (T - 1))) * C::kD + half * kDw;
         const uint32_t dst = ring + (i % C::kStages) * C::kStageBytes;
         // entries past the request's end, and blocks that do not exist, read as zeros
         const uint32_t here = ok ? min(static_cast<uint32_t>(kTile), item.kv_len - e0) : 0;
@@ -367,7 +345,7 @@ __global__ __launch_bounds__(kAttnThreads, (Cfg<kDw, kNp, kShared>::kPerSm)) voi
     for (int s = 0; s < C::kStages - 1; ++s) issue(s);
 
     // ---- query fragments of rows g and g + 8
-    uint32_t qf[kKj * 4][4];
+    uint32_t qf[kDw / 16][4];
     float rf[2];     // undoes the row's scaling
     int64_t vis[2];  // entries the row sees
     const uint32_t vis_min =
@@ -381,33 +359,7 @@ __global__ __launch_bounds__(kAttnThreads, (Cfg<kDw, kNp, kShared>::kPerSm)) voi
       vis[r] = in ? q8_visible(item.kv_len, item.q_len - 1 - i, item.phase, a.ratio) : 0x7FFFFFFF;
       const __nv_bfloat16* p =
           a.q + (static_cast<size_t>(item.q_start + i) * a.n_heads + h * G + hg) * C::kD + half * kDw;
-      uint4 v[kKj][2];
-      float m = 0.0f;
-#pragma unroll
-      for (int j = 0; j < kKj; ++j) {
-        const int cc = kDw == 64 ? q : 8 * (j >> 1) + 2 * q + (j & 1);
-#pragma unroll
-        for (int w = 0; w < 2; ++w) {
-          v[j][w] = in ? ld_cached16(p + cc * 16 + w * 8) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(unpack<__nv_bfloat16>(v[j][w], e)));
-        }
-      }
-      m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-      m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-      const int ex = min(126, 14 - (static_cast<int>(__float_as_uint(m) >> 23) - 127));
-      const float up = pow2f(ex);
-      rf[r] = pow2f(-ex);
-#pragma unroll
-      for (int j = 0; j < kKj; ++j) {
-#pragma unroll
-        for (int s = 0; s < 4; ++s) {  // k step 4 j + s: channels 4 s .. 4 s + 3 of the chunk
-          const uint4 x = v[j][s >> 1];
-          const int e = (s & 1) * 4;
-          qf[j * 4 + s][r] = pack_f16x2(unpack<__nv_bfloat16>(x, e) * up, unpack<__nv_bfloat16>(x, e + 1) * up);
-          qf[j * 4 + s][2 + r] = pack_f16x2(unpack<__nv_bfloat16>(x, e + 2) * up, unpack<__nv_bfloat16>(x, e + 3) * up);
-        }
-      }
+      rf[r] = load_query<kDw>(p, in, q, r, qf);
     }
 
     float o[kOt][4];
@@ -424,19 +376,7 @@ __global__ __launch_bounds__(kAttnThreads, (Cfg<kDw, kNp, kShared>::kPerSm)) voi
       const bool tile_ok = lds_u32(st + C::kTileBytes + 8) != 0;
       // scores
       float s[2][4];
-#pragma unroll
-      for (int n = 0; n < 2; ++n) {
-        s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.0f;
-#pragma unroll
-        for (int j = 0; j < kKj; ++j) {
-          const int cc = kDw == 64 ? q : 8 * (j >> 1) + 2 * q + (j & 1);
-          const uint4 w = lds16(st + tile_off<kDw>(n * 8 + g, cc));
-          mma_f16(s[n], qf[j * 4 + 0], q8_lo_f16x2(w.x), q8_hi_f16x2(w.x));
-          mma_f16(s[n], qf[j * 4 + 1], q8_lo_f16x2(w.y), q8_hi_f16x2(w.y));
-          mma_f16(s[n], qf[j * 4 + 2], q8_lo_f16x2(w.z), q8_hi_f16x2(w.z));
-          mma_f16(s[n], qf[j * 4 + 3], q8_lo_f16x2(w.w), q8_hi_f16x2(w.w));
-        }
-      }
+      tile_scores<kDw>(st, g, q, qf, s);
       float f[2] = {rf[0] * a.scale_log2, rf[1] * a.scale_log2};
       if (kNp == 2) {  // the two warps of a row add their halves of the channels
         float* own = s_x[grp][i & 1][half];
@@ -642,11 +582,28 @@ __global__ __launch_bounds__(kAttnThreads, (Cfg<kDw, kNp, kShared>::kPerSm)) voi
 }
 
 // ------------------------------------------------------------------- combine
-// A CTA takes a (split tile, kv head, row) at a time: the row's parts joined in
-// their order.  A row reads chunks * (head_dim + 2) floats, at most a few hundred KB
-// in all, so what counts is that the rows spread over the SMs.
+// Joins a split tile's parts, in their order.  A CTA takes four rows of a (split
+// tile, kv head) at a time: a warp to a row where the parts are few, so that a row is
+// two trips to memory and no barrier; else the whole CTA to each row in turn.
 constexpr int kCombineThreads = 128;
+constexpr int kCombineRows = 4;
+constexpr uint32_t kFewParts = 16;
 constexpr int kMaxParts = 2048;
+
+__device__ __forceinline__ void store_out(const AttnArgs& a, size_t out_row, int d, int ch, float4 v, float inv) {
+  const float r[4] = {v.x * inv, v.y * inv, v.z * inv, v.w * inv};
+  if (a.out_f32)
+    store_row_chunk<float, 4>(static_cast<float*>(a.out) + out_row * d + ch, r);
+  else
+    store_row_chunk<__nv_bfloat16, 4>(static_cast<__nv_bfloat16*>(a.out) + out_row * d + ch, r);
+}
+
+__device__ __forceinline__ void add_scaled(float4& v, const float4 x, float w) {
+  v.x = fmaf(x.x, w, v.x);
+  v.y = fmaf(x.y, w, v.y);
+  v.z = fmaf(x.z, w, v.z);
+  v.w = fmaf(x.w, w, v.w);
+}
 
 template <int kD>
 __global__ __launch_bounds__(kCombineThreads) void q8_combine_kernel(const AttnArgs a) {
@@ -658,75 +615,96 @@ __global__ __launch_bounds__(kCombineThreads) void q8_combine_kernel(const AttnA
   pdl_release();
   const Q8Header* head = reinterpret_cast<const Q8Header*>(a.plan);
   if (!plan_fits(head, a)) return;
-  const uint32_t G = a.g.group, H = a.c.heads, M = a.g.rows;
+  const uint32_t G = a.g.group, H = a.c.heads, M = a.g.rows, quads = M / kCombineRows;
   const uint32_t* splits = reinterpret_cast<const uint32_t*>(a.plan + a.g.off_split);
   const Q8Item* items = reinterpret_cast<const Q8Item*>(a.plan + a.g.off_items);
-  const uint32_t work = min(head->splits, a.g.ctas) * H * M;
-  const int tid = threadIdx.x;
+  const uint32_t work = min(head->splits, a.g.ctas) * H * quads;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   for (uint32_t x = blockIdx.x; x < work; x += gridDim.x) {
-    const uint32_t row = x % M, h = x / M % H, first = splits[x / M / H];
+    const uint32_t row0 = x % quads * kCombineRows, h = x / quads % H, first = splits[x / quads / H];
     if (first >= a.g.cap_items) continue;
     const Q8Item item = items[first];
-    if (!item_fits(item, a) || item.part < 0 || item.chunks > kMaxParts ||
-        static_cast<uint64_t>(item.row0) + row >= static_cast<uint64_t>(item.q_len) * G)
-      continue;
-    const size_t r0 = (static_cast<size_t>(item.part) * H + h) * M + row, step = static_cast<size_t>(H) * M;
-    __syncthreads();  // the previous row's reads of shared memory are done
-    float top = -3.4e38f;
-    for (uint32_t p = tid; p < item.chunks; p += kCombineThreads) top = fmaxf(top, a.part_ml[r0 + p * step].x);
+    const uint64_t rows_left = static_cast<uint64_t>(item.q_len) * G - item.row0;
+    if (!item_fits(item, a) || item.part < 0 || item.chunks > kMaxParts || row0 >= rows_left) continue;
+    const size_t step = static_cast<size_t>(H) * M;
+    const uint32_t rows = static_cast<uint32_t>(min(static_cast<uint64_t>(kCombineRows), rows_left - row0));
+    if (item.chunks <= kFewParts) {
+      if (static_cast<uint32_t>(warp) >= rows) continue;
+      const uint32_t row = row0 + warp;
+      const size_t r0 = (static_cast<size_t>(item.part) * H + h) * M + row;
+      const bool in = static_cast<uint32_t>(lane) < item.chunks;
+      const float2 ml = in ? a.part_ml[r0 + lane * step] : make_float2(-3.4e38f, 0.0f);
+      float top = ml.x;
 #pragma unroll
-    for (int s = 16; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, s));
-    if ((tid & 31) == 0) s_red[tid >> 5] = top;
-    __syncthreads();
+      for (int s = 16; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, s));
+      const float w = in ? ex2(ml.x - top) : 0.0f;
+      float sum = ml.y * w;
 #pragma unroll
-    for (int w = 0; w < kCombineThreads / 32; ++w) top = fmaxf(top, s_red[w]);
-    __syncthreads();
-    float sum = 0.0f;
-    for (uint32_t p = tid; p < item.chunks; p += kCombineThreads) {
-      const float2 ml = a.part_ml[r0 + p * step];
-      const float w = ex2(ml.x - top);
-      s_w[p] = w;
-      sum = fmaf(ml.y, w, sum);
-    }
-#pragma unroll
-    for (int s = 16; s > 0; s >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, s);
-    if ((tid & 31) == 0) s_red[tid >> 5] = sum;
-    __syncthreads();
-    sum = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kCombineThreads / 32; ++w) sum += s_red[w];
-
-    const int ch = (tid % kLanes) * 4;
-    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-    for (uint32_t p = tid / kLanes; p < item.chunks; p += kSplit) {
-      const float4 o = *reinterpret_cast<const float4*>(a.part_o + (r0 + p * step) * kD + ch);
-      const float w = s_w[p];
-      v.x = fmaf(o.x, w, v.x);
-      v.y = fmaf(o.y, w, v.y);
-      v.z = fmaf(o.z, w, v.z);
-      v.w = fmaf(o.w, w, v.w);
-    }
-    s_o[tid] = v;
-    __syncthreads();
-    if (tid < kLanes) {
-      for (int k = 1; k < kSplit; ++k) {
-        const float4 o = s_o[tid + k * kLanes];
-        v.x += o.x;
-        v.y += o.y;
-        v.z += o.z;
-        v.w += o.w;
-      }
+      for (int s = 16; s > 0; s >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, s);
       const float inv = sum == 0.0f ? 0.0f : __fdiv_rn(1.0f, sum);
+      constexpr int kVecs = kD < 128 ? 1 : kD / 128;
+      const bool own = kD >= 128 || lane < kLanes;
+      float4 v[kVecs];
+#pragma unroll
+      for (int y = 0; y < kVecs; ++y) v[y] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      const float* o = a.part_o + r0 * kD + lane * 4;
+#pragma unroll 4
+      for (uint32_t p = 0; p < item.chunks; ++p) {
+        const float wp = __shfl_sync(0xFFFFFFFFu, w, p);
+#pragma unroll
+        for (int y = 0; y < kVecs; ++y)
+          if (own) add_scaled(v[y], *reinterpret_cast<const float4*>(o + p * step * kD + y * 128), wp);
+      }
       const uint32_t rho = item.row0 + row, i = rho / G, hg = rho % G;
       const size_t out_row = static_cast<size_t>(item.q_start + i) * a.n_heads + h * G + hg;
-      const float r[4] = {v.x * inv, v.y * inv, v.z * inv, v.w * inv};
-      if (a.out_f32)
-        store_row_chunk<float, 4>(static_cast<float*>(a.out) + out_row * kD + ch, r);
-      else
-        store_row_chunk<__nv_bfloat16, 4>(static_cast<__nv_bfloat16*>(a.out) + out_row * kD + ch, r);
-      if (tid == 0 && a.lse != nullptr)
+#pragma unroll
+      for (int y = 0; y < kVecs; ++y)
+        if (own) store_out(a, out_row, kD, lane * 4 + y * 128, v[y], inv);
+      if (lane == 0 && a.lse != nullptr)
         a.lse[out_row] = sum == 0.0f ? -INFINITY : (top + __log2f(sum)) * 0.69314718055994530942f;
+      continue;
+    }
+    for (uint32_t row = row0; row < row0 + rows; ++row) {
+      const size_t r0 = (static_cast<size_t>(item.part) * H + h) * M + row;
+      __syncthreads();  // the previous row's reads of shared memory are done
+      float top = -3.4e38f;
+      for (uint32_t p = tid; p < item.chunks; p += kCombineThreads) top = fmaxf(top, a.part_ml[r0 + p * step].x);
+#pragma unroll
+      for (int s = 16; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, s));
+      if (lane == 0) s_red[warp] = top;
+      __syncthreads();
+#pragma unroll
+      for (int w = 0; w < kCombineThreads / 32; ++w) top = fmaxf(top, s_red[w]);
+      __syncthreads();
+      float sum = 0.0f;
+      for (uint32_t p = tid; p < item.chunks; p += kCombineThreads) {
+        const float2 ml = a.part_ml[r0 + p * step];
+        const float w = ex2(ml.x - top);
+        s_w[p] = w;
+        sum = fmaf(ml.y, w, sum);
+      }
+#pragma unroll
+      for (int s = 16; s > 0; s >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, s);
+      if (lane == 0) s_red[warp] = sum;
+      __syncthreads();
+      sum = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kCombineThreads / 32; ++w) sum += s_red[w];
+      const int ch = (tid % kLanes) * 4;
+      float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+      for (uint32_t p = tid / kLanes; p < item.chunks; p += kSplit)
+        add_scaled(v, *reinterpret_cast<const float4*>(a.part_o + (r0 + p * step) * kD + ch), s_w[p]);
+      s_o[tid] = v;
+      __syncthreads();
+      if (tid < kLanes) {
+        for (int k = 1; k < kSplit; ++k) add_scaled(v, s_o[tid + k * kLanes], 1.0f);
+        const uint32_t rho = item.row0 + row, i = rho / G, hg = rho % G;
+        const size_t out_row = static_cast<size_t>(item.q_start + i) * a.n_heads + h * G + hg;
+        store_out(a, out_row, kD, ch, v, sum == 0.0f ? 0.0f : __fdiv_rn(1.0f, sum));
+        if (tid == 0 && a.lse != nullptr)
+          a.lse[out_row] = sum == 0.0f ? -INFINITY : (top + __log2f(sum)) * 0.69314718055994530942f;
+      }
     }
   }
 }
@@ -735,10 +713,9 @@ template <int kDw, int kNp, bool kShared>
 int launch_attn(const AttnArgs& a, cudaStream_t s) {
   using C = Cfg<kDw, kNp, kShared>;
   auto* kernel = q8_attn_kernel<kDw, kNp, kShared>;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) != cudaSuccess) {
-    cudaGetLastError();
-    return CKV_ERR_LAUNCH;
-  }
+  static std::atomic<uint64_t> done;
+  const int rc = allow_smem(reinterpret_cast<const void*>(kernel), C::kSmem, done);
+  if (rc) return rc;
   return launch_pdl(kernel, dim3(a.g.ctas, a.c.heads), dim3(kAttnThreads), C::kSmem, s, a);
 }
 
@@ -754,8 +731,8 @@ int launch_split(const AttnArgs& a, cudaStream_t s) {
 
 int launch_combine(const AttnArgs& a, cudaStream_t s) {
   // at most eight CTAs to an SM; they walk the rows
-  const uint64_t rows = static_cast<uint64_t>(a.g.ctas) * a.c.heads * a.g.rows;
-  const dim3 grid(static_cast<uint32_t>(std::min<uint64_t>(rows, 8ull * sm_count())));
+  const uint64_t quads = static_cast<uint64_t>(a.g.ctas) * a.c.heads * (a.g.rows / kCombineRows);
+  const dim3 grid(static_cast<uint32_t>(std::min<uint64_t>(quads, 8ull * sm_count())));
   switch (a.c.head_dim) {
     case 64: return launch_pdl(q8_combine_kernel<64>, grid, dim3(kCombineThreads), 0, s, a);
     case 128: return launch_pdl(q8_combine_kernel<128>, grid, dim3(kCombineThreads), 0, s, a);
@@ -809,7 +786,9 @@ int ckv_plan_q8_attn(const ckv_q8_cache_t* cache, uint32_t n_heads, uint32_t rat
   a.ratio = ratio;
   a.plan = static_cast<uint8_t*>(plan);
   a.d_status = d_status;
-  return launch_pdl(plan_q8_attn_kernel, dim3(1), dim3(kPlanThreads), 0, reinterpret_cast<cudaStream_t>(stream), a);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  return batch <= 256 ? launch_pdl(plan_q8_attn_kernel<256>, dim3(1), dim3(256), 0, s, a)
+                      : launch_pdl(plan_q8_attn_kernel<1024>, dim3(1), dim3(1024), 0, s, a);
 }
 
 int ckv_q8_attn(const ckv_q8_cache_t* cache, uint32_t n_heads, uint32_t ratio, float scale, const void* q,

@@ -375,10 +375,9 @@ template <int kD, bool kShared>
 int launch(const AttnArgs& a, cudaStream_t s) {
   using C = RowsCfg<kD, kShared>;
   auto* kernel = a.wait_ns < kShortWaitNs ? q8_attn_rows_kernel<kD, kShared, true> : q8_attn_rows_kernel<kD, kShared, false>;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) != cudaSuccess) {
-    cudaGetLastError();
-    return CKV_ERR_LAUNCH;
-  }
+  static std::atomic<uint64_t> done[2];
+  const int rc = allow_smem(reinterpret_cast<const void*>(kernel), C::kSmem, done[a.wait_ns < kShortWaitNs ? 1 : 0]);
+  if (rc) return rc;
   return launch_pdl(kernel, dim3(a.g.ctas, a.c.heads), dim3(C::kThreads), C::kSmem, s, a);
 }
 

@@ -283,11 +283,9 @@ extern "C" int ckv_q8_evict(const ckv_q8_cache_t* cache, float* weights, const i
   const uint64_t longest = static_cast<uint64_t>(table_stride) * a.c.block_tokens;
   a.keys_cap = longest <= budget ? 0 : static_cast<uint32_t>(std::min<uint64_t>(longest, kMaxKeys));
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (cudaFuncSetAttribute(q8_evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxKeys * 4) !=
-      cudaSuccess) {
-    cudaGetLastError();
-    return CKV_ERR_LAUNCH;
-  }
+  static std::atomic<uint64_t> done;
+  rc = allow_smem(reinterpret_cast<const void*>(q8_evict_select_kernel), kMaxKeys * 4, done);
+  if (rc) return rc;
   rc = launch_pdl(q8_evict_select_kernel, dim3(batch), dim3(kSelThreads), a.keys_cap * 4, s, a);
   if (rc) return rc;
   const uint64_t most = std::min<uint64_t>(budget, longest);

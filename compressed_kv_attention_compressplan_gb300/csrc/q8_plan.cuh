@@ -87,11 +87,6 @@ struct AttnArgs {
   uint32_t* d_status;
 };
 
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-  const __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-
 __device__ __forceinline__ bool item_fits(const Q8Item& item, const AttnArgs& a) {
   return item.rid < a.num_reqs && static_cast<uint64_t>(item.q_start) + item.q_len <= a.num_q &&
          item.row0 < static_cast<uint64_t>(item.q_len) * a.g.group &&

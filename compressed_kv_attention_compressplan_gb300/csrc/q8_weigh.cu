@@ -5,13 +5,17 @@
 // with lse the attention's log-sum-exp, so p is the softmax weight itself and
 // one pass over the keys does: the values are not read and no maximum is kept.
 //
-// Bound: the keys' bytes when a request has few rows; the exponentials and
-// products when it has many.  An entry belongs to one CTA, which walks all
-// rows and heads in a fixed order: no atomics, and results that repeat bit for
-// bit.  A warp holds 16 entries of one kv head as bf16 fragments (exact, and
-// queries are bf16 already, so a row tile costs loads and products only) and streams
-// the request's rows past them; the CTA's warps share out kv heads, then
-// entries, and the heads are summed through shared memory in head order.
+// An entry belongs to one CTA, which walks all rows and heads in a fixed order: no
+// atomics, and results that repeat bit for bit.  Two kernels:
+//
+// Few rows (a decode step): the keys' bytes bound it.  A warp keeps a head's query
+// fragments and streams its tiles of 16 entries through a ring of its own, as the split
+// attention does; the CTAs share the batch's tiles out evenly, and a CTA's warps take
+// one head each and are summed in head order once per run of 256 entries.
+//
+// Many rows (a window of queries): the products and exponentials bound it.  A warp
+// holds 32 entries of a head as bf16 fragments (exact, and queries are bf16 already, so
+// a row tile costs loads and products only) and streams the request's rows past them.
 #include <algorithm>
 
 #include "q8.cuh"
@@ -59,26 +63,18 @@ __device__ __forceinline__ uint32_t f16x2_to_bf16x2(uint32_t h) {
   return pack_bf16x2(f.x, f.y);
 }
 
-template <int kD>
-__global__ __launch_bounds__(kThreads) void q8_weigh_kernel(const WeighArgs a) {
-  constexpr int kKj = kD / 64;
-  __shared__ uint32_t s_unit[CKV_MAX_BATCH];
-  __shared__ uint32_t s_q[CKV_MAX_BATCH];
-  __shared__ uint32_t s_scan[kWarps + 1];
-  __shared__ unsigned long long s_scan64[kWarps + 1];
-  __shared__ float s_sum[kWarps][kTile];
-  pdl_wait();
-  pdl_release();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int g = lane >> 2, q = lane & 3;
-  const uint32_t T = a.c.block_tokens, H = a.c.heads, G = a.group;
-  const uint32_t unit_entries = kWarps / a.head_warps * kTile;
+__device__ __forceinline__ void put_weight(const WeighArgs& a, int32_t block, uint32_t slot, float w) {
+  float* dst = a.weights + static_cast<size_t>(block) * a.c.block_tokens + slot;
+  *dst = a.decay == 0.0f ? w : fmaf(a.decay, *dst, w);
+}
 
-  // units (runs of unit_entries entries) of every request, and its first ragged query
+// Units (runs of unit_entries entries) before every request that has queries, and its first ragged query.
+__device__ __forceinline__ uint32_t scan_requests(const WeighArgs& a, uint32_t unit_entries, uint32_t* s_unit, uint32_t* s_q,
+                                                  uint32_t* s_scan, unsigned long long* s_scan64) {
   uint32_t units = 0;
   unsigned long long queries = 0;
   for (uint32_t b0 = 0; b0 < a.batch; b0 += kThreads) {
-    const uint32_t b = b0 + tid;
+    const uint32_t b = b0 + threadIdx.x;
     uint32_t n = 0;
     unsigned long long ql = 0;
     if (b < a.batch) {
@@ -86,7 +82,7 @@ __global__ __launch_bounds__(kThreads) void q8_weigh_kernel(const WeighArgs a) {
       const bool len_ok = el >= 0 && el <= a.num_q;
       ql = len_ok ? static_cast<unsigned long long>(el) : 0;
       const bool ok = len_ok && sl >= el && sl <= 0x7FFFFFFF && kl >= 0 && kl <= 0x7FFFFFF0 &&
-                      kl <= static_cast<int64_t>(a.stride) * T && r >= 0 && r < a.num_reqs;
+                      kl <= static_cast<int64_t>(a.stride) * a.c.block_tokens && r >= 0 && r < a.num_reqs;
       if (!ok && blockIdx.x == 0) status_or(a.d_status, CKV_STATUS_BAD_LENGTH);
       n = ok && el > 0 ? static_cast<uint32_t>((kl + unit_entries - 1) / unit_entries) : 0;
     }
@@ -102,46 +98,77 @@ __global__ __launch_bounds__(kThreads) void q8_weigh_kernel(const WeighArgs a) {
     units += n_sum;
     queries += ql_sum;
   }
-  if (blockIdx.x == 0 && tid == 0 && queries != a.num_q) status_or(a.d_status, CKV_STATUS_BAD_TOTAL);
+  if (blockIdx.x == 0 && threadIdx.x == 0 && queries != a.num_q) status_or(a.d_status, CKV_STATUS_BAD_TOTAL);
   __syncthreads();
+  return units;
+}
 
+// kNt tiles of 16 entries to a warp.
+template <int kD, int kNt>
+__global__ __launch_bounds__(kThreads) void q8_weigh_rows_kernel(const WeighArgs a) {
+  constexpr int kKj = kD / 64;
+  __shared__ uint32_t s_unit[CKV_MAX_BATCH];
+  __shared__ uint32_t s_q[CKV_MAX_BATCH];
+  __shared__ uint32_t s_scan[kWarps + 1];
+  __shared__ unsigned long long s_scan64[kWarps + 1];
+  __shared__ float s_sum[kWarps][kNt * kTile];
+  pdl_wait();
+  pdl_release();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int g = lane >> 2, q = lane & 3;
+  const uint32_t T = a.c.block_tokens, H = a.c.heads, G = a.group;
+  const uint32_t unit_entries = kWarps / a.head_warps * (kNt * kTile);
+
+  const uint32_t units = scan_requests(a, unit_entries, s_unit, s_q, s_scan, s_scan64);
   for (uint32_t u = blockIdx.x; u < units; u += gridDim.x) {
     const uint32_t b = last_not_above(s_unit, a.batch, u);
     const uint32_t kv_len = static_cast<uint32_t>(a.kv_lens[b]);
     const uint32_t q_len = static_cast<uint32_t>(a.extend_lens[b]);
     const uint32_t phase = a.ratio - 1 - static_cast<uint32_t>(a.seq_lens[b]) % a.ratio;
     const uint32_t rows = q_len * G;
-    const uint32_t e0 = (u - s_unit[b]) * unit_entries + warp / a.head_warps * kTile;
-    float sum[2][2] = {};  // entries 8 n + 2q + {0, 1}
-    int32_t block = -1;
-    if (e0 < kv_len) {
-      block = __ldg(a.table + static_cast<size_t>(a.rid[b]) * a.stride + e0 / T);
-      if (block < 0 || static_cast<uint32_t>(block) >= a.c.num_blocks) {
-        if (lane == 0) status_or(a.d_status, CKV_STATUS_BAD_INDEX);
-        block = -1;
+    const uint32_t e0 = (u - s_unit[b]) * unit_entries + warp / a.head_warps * (kNt * kTile);
+    float sum[kNt][2][2] = {};  // entries 16 t + 8 n + 2q + {0, 1}
+    int32_t block[kNt];
+    bool any = false;
+#pragma unroll
+    for (int t = 0; t < kNt; ++t) {
+      const uint32_t e = e0 + t * kTile;
+      block[t] = -1;
+      if (e < kv_len) {
+        block[t] = __ldg(a.table + static_cast<size_t>(a.rid[b]) * a.stride + e / T);
+        if (static_cast<uint32_t>(block[t]) >= a.c.num_blocks) {
+          if (lane == 0) status_or(a.d_status, CKV_STATUS_BAD_INDEX);
+          block[t] = -1;
+        }
       }
+      any |= block[t] >= 0;
     }
-    if (block >= 0) {
+    if (any) {
       for (uint32_t h = warp % a.head_warps; h < H; h += a.head_warps) {
-        const size_t bh = static_cast<size_t>(block) * H + h;
-        const uint8_t* k = a.c.k + (bh * T + e0 % T) * kD;
-        const float f = a.scale_log2 * __ldg(a.c.k_scale + bh);
-        uint32_t kf[2][kKj * 4][2];
+        uint32_t kf[kNt][2][kKj * 4][2];
+        float f[kNt];
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
+        for (int t = 0; t < kNt; ++t) {
+          const uint32_t e = e0 + t * kTile;
+          const size_t bh = static_cast<size_t>(max(block[t], 0)) * H + h;
+          const uint8_t* k = a.c.k + (bh * T + e % T) * kD;
+          f[t] = a.scale_log2 * __ldg(a.c.k_scale + bh);
 #pragma unroll
-          for (int j = 0; j < kKj; ++j) {
-            const uint4 w = ld_stream16(k + static_cast<size_t>(n * 8 + g) * kD + (j * 4 + q) * 16);
-            const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+          for (int n = 0; n < 2; ++n) {
 #pragma unroll
-            for (int s = 0; s < 4; ++s) {
-              kf[n][j * 4 + s][0] = f16x2_to_bf16x2(q8_lo_f16x2(x[s]));
-              kf[n][j * 4 + s][1] = f16x2_to_bf16x2(q8_hi_f16x2(x[s]));
+            for (int j = 0; j < kKj; ++j) {
+              const uint4 w = ld_stream16_if(k + static_cast<size_t>(n * 8 + g) * kD + (j * 4 + q) * 16, block[t] >= 0);
+              const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+              for (int s = 0; s < 4; ++s) {
+                kf[t][n][j * 4 + s][0] = f16x2_to_bf16x2(q8_lo_f16x2(x[s]));
+                kf[t][n][j * 4 + s][1] = f16x2_to_bf16x2(q8_hi_f16x2(x[s]));
+              }
             }
           }
         }
         for (uint32_t r0 = 0; r0 < rows; r0 += 16) {
-          float s[2][4] = {};
+          float s[kNt][2][4] = {};
           float off[2];
           int64_t vis[2];
           const __nv_bfloat16* p[2];
@@ -171,17 +198,23 @@ __global__ __launch_bounds__(kThreads) void q8_weigh_kernel(const WeighArgs a) {
               af[1] = st & 1 ? x1.z : x1.x;
               af[2] = st & 1 ? x0.w : x0.y;
               af[3] = st & 1 ? x1.w : x1.y;
-              mma_bf16(s[0], af, kf[0][j * 4 + st][0], kf[0][j * 4 + st][1]);
-              mma_bf16(s[1], af, kf[1][j * 4 + st][0], kf[1][j * 4 + st][1]);
+#pragma unroll
+              for (int t = 0; t < kNt; ++t) {
+                mma_bf16(s[t][0], af, kf[t][0][j * 4 + st][0], kf[t][0][j * 4 + st][1]);
+                mma_bf16(s[t][1], af, kf[t][1][j * 4 + st][0], kf[t][1][j * 4 + st][1]);
+              }
             }
           }
 #pragma unroll
-          for (int n = 0; n < 2; ++n) {
+          for (int t = 0; t < kNt; ++t) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int64_t at = e0 + n * 8 + 2 * q + (e & 1);
-              const float w = ex2(fmaf(s[n][e], f, off[e >> 1]));
-              sum[n][e & 1] += at < vis[e >> 1] ? w : 0.0f;
+            for (int n = 0; n < 2; ++n) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int64_t at = e0 + t * kTile + n * 8 + 2 * q + (e & 1);
+                const float w = ex2(fmaf(s[t][n][e], f[t], off[e >> 1]));
+                sum[t][n][e & 1] += at < vis[e >> 1] ? w : 0.0f;
+              }
             }
           }
         }
@@ -189,29 +222,178 @@ __global__ __launch_bounds__(kThreads) void q8_weigh_kernel(const WeighArgs a) {
     }
     // rows of the fragment (the lanes of one column), then the heads' warps in order
 #pragma unroll
-    for (int n = 0; n < 2; ++n) {
+    for (int t = 0; t < kNt; ++t) {
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
+      for (int n = 0; n < 2; ++n) {
 #pragma unroll
-        for (int x = 4; x < 32; x <<= 1) sum[n][e] += __shfl_xor_sync(0xFFFFFFFFu, sum[n][e], x);
-        if (g == 0) s_sum[warp][n * 8 + 2 * q + e] = sum[n][e];
+        for (int e = 0; e < 2; ++e) {
+#pragma unroll
+          for (int x = 4; x < 32; x <<= 1) sum[t][n][e] += __shfl_xor_sync(0xFFFFFFFFu, sum[t][n][e], x);
+          if (g == 0) s_sum[warp][t * kTile + n * 8 + 2 * q + e] = sum[t][n][e];
+        }
       }
     }
     __syncthreads();
-    if (warp % a.head_warps == 0 && lane < kTile && block >= 0 && e0 + lane < kv_len) {
-      float w = 0.0f;
-      for (uint32_t x = 0; x < a.head_warps; ++x) w += s_sum[warp + x][lane];
-      float* dst = a.weights + static_cast<size_t>(block) * T + e0 % T + lane;
-      *dst = a.decay == 0.0f ? w : fmaf(a.decay, *dst, w);
+    if (warp % a.head_warps == 0) {
+#pragma unroll
+      for (int t = 0; t < kNt; ++t) {
+        const uint32_t e = e0 + t * kTile;
+        if (lane < kTile && block[t] >= 0 && e + lane < kv_len) {
+          float w = 0.0f;
+          for (uint32_t x = 0; x < a.head_warps; ++x) w += s_sum[warp + x][t * kTile + lane];
+          put_weight(a, block[t], e % T + lane, w);
+        }
+      }
     }
     __syncthreads();
   }
 }
 
+// ---------------------------------------------------------------- few rows
+template <int kD>
+struct StreamCfg {
+  static constexpr int kStages = kD == 64 ? 8 : kD == 128 ? 4 : kD == 256 ? 5 : 3;
+  static constexpr int kPerSm = kD <= 128 ? 2 : 1;
+  static constexpr int kStageBytes = kTile * kD + 16;  // and the tile's scale
+  static constexpr int kSmem = kWarps * kStages * kStageBytes;
+  static constexpr int kRun = 16;  // tiles that are summed over the heads at once
+};
+
+template <int kD>
+__global__ __launch_bounds__(kThreads, StreamCfg<kD>::kPerSm) void q8_weigh_stream_kernel(const WeighArgs a) {
+  using C = StreamCfg<kD>;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ uint32_t s_tile[CKV_MAX_BATCH];
+  __shared__ uint32_t s_q[CKV_MAX_BATCH];
+  __shared__ uint32_t s_scan[kWarps + 1];
+  __shared__ unsigned long long s_scan64[kWarps + 1];
+  __shared__ float s_sum[kWarps][C::kRun * kTile];
+  pdl_wait();
+  pdl_release();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int g = lane >> 2, q = lane & 3;
+  const uint32_t T = a.c.block_tokens, t_shift = __ffs(T) - 1, H = a.c.heads, G = a.group;
+  const uint32_t head0 = warp % a.head_warps, part = warp / a.head_warps, parts = kWarps / a.head_warps;
+  const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + warp * C::kStages * C::kStageBytes;
+  const uint32_t tiles = scan_requests(a, kTile, s_tile, s_q, s_scan, s_scan64);
+  // this CTA's share of the batch's tiles, request after request, in runs of at most kRun
+  const uint32_t from = static_cast<uint32_t>(static_cast<uint64_t>(tiles) * blockIdx.x / gridDim.x);
+  const uint32_t to = static_cast<uint32_t>(static_cast<uint64_t>(tiles) * (blockIdx.x + 1) / gridDim.x);
+  for (uint32_t t0 = from; t0 < to;) {
+    const uint32_t b = last_not_above(s_tile, a.batch, t0);
+    const uint32_t end = b + 1 < a.batch ? s_tile[b + 1] : tiles;
+    const uint32_t run = min(min(end, to) - t0, static_cast<uint32_t>(C::kRun));
+    const uint32_t first = (t0 - s_tile[b]) * kTile;
+    const uint32_t kv_len = static_cast<uint32_t>(a.kv_lens[b]);
+    const uint32_t q_len = static_cast<uint32_t>(a.extend_lens[b]);
+    const uint32_t phase = a.ratio - 1 - static_cast<uint32_t>(a.seq_lens[b]) % a.ratio;
+    const uint32_t rows = q_len * G;
+    const int32_t* table = a.table + static_cast<size_t>(a.rid[b]) * a.stride;
+    const uint32_t mine = run > part ? (run - part + parts - 1) / parts : 0;  // tiles part, part + parts, ...
+    // a run has at most 16 tiles: lane t keeps tile t's block number
+    const int32_t blk = __ldg(table + (min(first + (lane & 15) * kTile, kv_len - 1) >> t_shift));
+    const bool blk_ok = static_cast<uint32_t>(blk) < a.c.num_blocks;
+    if (!blk_ok && static_cast<uint32_t>(lane) < run) status_or(a.d_status, CKV_STATUS_BAD_INDEX);
+    for (uint32_t i = lane; i < C::kRun * kTile; i += 32) s_sum[warp][i] = 0.0f;
+    __syncwarp();
+    for (uint32_t h = head0; h < H; h += a.head_warps) {
+      for (uint32_t r0 = 0; r0 < rows; r0 += 16) {
+        auto issue = [&](uint32_t i) {
+          if (i < mine) {
+            const uint32_t t = part + i * parts, e = first + t * kTile;
+            const int32_t bk = __shfl_sync(0xFFFFFFFFu, blk, t);
+            const bool ok = static_cast<uint32_t>(bk) < a.c.num_blocks;
+            const size_t bh = static_cast<size_t>(ok ? bk : 0) * H + h;
+            const uint8_t* k = a.c.k + ((bh << t_shift) + (e & (T - 1))) * kD;
+            const uint32_t dst = ring + (i % C::kStages) * C::kStageBytes;
+#pragma unroll
+            for (int x = 0; x < kD / 32; ++x) {
+              const uint32_t c = x * 32 + lane, tok = c / (kD / 16), cc = c % (kD / 16);
+              cp_async16(dst + tile_off<kD>(tok, cc), k + tok * kD + cc * 16, ok ? 16u : 0u);
+            }
+            if (lane == 0) cp_async4(dst + kTile * kD, a.c.k_scale + bh);
+          }
+          cp_async_commit();
+        };
+#pragma unroll
+        for (int s = 0; s < C::kStages - 1; ++s) issue(s);
+        uint32_t qf[kD / 16][4];
+        float rf[2], off[2];
+        int64_t vis[2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const bool in = r0 + g + 8 * r < rows;
+          const uint32_t rho = in ? r0 + g + 8 * r : 0, i = rho / G, hg = rho % G;
+          const size_t row = static_cast<size_t>(s_q[b] + i) * a.n_heads + h * G + hg;
+          vis[r] = in ? q8_visible(kv_len, q_len - 1 - i, phase, a.ratio) : 0;
+          const float lse = in ? __ldg(a.lse + row) : 0.0f;
+          off[r] = lse == -INFINITY ? -INFINITY : lse * -kLog2e;  // a row that saw nothing weighs nothing
+          rf[r] = load_query<kD>(a.q + row * kD, in, q, r, qf) * a.scale_log2;
+        }
+        for (uint32_t i = 0; i < mine; ++i) {
+          cp_async_wait<C::kStages - 2>();
+          __syncwarp();  // every lane's copies of this tile are in; every lane has read the tile before it
+          issue(i + C::kStages - 1);
+          const uint32_t st = ring + (i % C::kStages) * C::kStageBytes, t = part + i * parts;
+          const float ks = lds_f32(st + kTile * kD);
+          float s[2][4];
+          tile_scores<kD>(st, g, q, qf, s);
+          const float f[2] = {rf[0] * ks, rf[1] * ks};
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            float sum[2] = {0.0f, 0.0f};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int64_t at = first + t * kTile + n * 8 + 2 * q + (e & 1);
+              const float w = ex2(fmaf(s[n][e], f[e >> 1], off[e >> 1]));
+              sum[e & 1] += at < vis[e >> 1] ? w : 0.0f;
+            }
+#pragma unroll
+            for (int x = 4; x < 32; x <<= 1) {
+              sum[0] += __shfl_xor_sync(0xFFFFFFFFu, sum[0], x);
+              sum[1] += __shfl_xor_sync(0xFFFFFFFFu, sum[1], x);
+            }
+            if (g == 0) {  // one lane to an entry, the same one every time
+              s_sum[warp][t * kTile + n * 8 + 2 * q] += sum[0];
+              s_sum[warp][t * kTile + n * 8 + 2 * q + 1] += sum[1];
+            }
+          }
+        }
+        cp_async_wait<0>();
+        __syncwarp();
+      }
+    }
+    __syncthreads();
+    for (uint32_t i = tid; i < run * kTile; i += kThreads) {
+      const uint32_t e = first + i;
+      if (e < kv_len) {
+        const int32_t block = __ldg(table + (e >> t_shift));
+        if (static_cast<uint32_t>(block) < a.c.num_blocks) {
+          const uint32_t w0 = (i / kTile) % parts * a.head_warps;
+          float w = 0.0f;
+          for (uint32_t x = 0; x < a.head_warps; ++x) w += s_sum[w0 + x][i];
+          put_weight(a, block, e & (T - 1), w);
+        }
+      }
+    }
+    __syncthreads();
+    t0 += run;
+  }
+}
+
 template <int kD>
 int launch_weigh(const WeighArgs& a, cudaStream_t s) {
-  const uint32_t grid = 2u * static_cast<uint32_t>(sm_count());
-  return launch_pdl(q8_weigh_kernel<kD>, dim3(grid), dim3(kThreads), 0, s, a);
+  // Rows of a request and kv head: up to 32 (two row tiles) the keys are streamed, once for each tile.
+  if (static_cast<uint64_t>(a.num_q) * a.group <= 32ull * a.batch) {
+    using C = StreamCfg<kD>;
+    static std::atomic<uint64_t> done;
+    const int rc = allow_smem(reinterpret_cast<const void*>(q8_weigh_stream_kernel<kD>), C::kSmem, done);
+    if (rc) return rc;
+    return launch_pdl(q8_weigh_stream_kernel<kD>, dim3(static_cast<uint32_t>(C::kPerSm * sm_count())), dim3(kThreads),
+                      C::kSmem, s, a);
+  }
+  constexpr int kNt = kD <= 128 ? 2 : 1;
+  return launch_pdl(q8_weigh_rows_kernel<kD, kNt>, dim3(2u * static_cast<uint32_t>(sm_count())), dim3(kThreads), 0, s, a);
 }
 
 }  // namespace
