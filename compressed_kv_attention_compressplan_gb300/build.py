@@ -19,7 +19,8 @@ OUT_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(OUT_DIR, "libckv.so")
 INCLUDE = os.path.join(ROOT, "include")
 SOURCES = ["plan.cu", "write.cu", "pool_c4.cu", "pool_c128.cu", "norm_rope.cu", "online.cu", "api.cu",
-           "q8_store.cu", "q8_attn.cu", "q8_attn_tc.cu", "q8_attn_rows.cu", "q8_weigh.cu", "q8_evict.cu"]
+           "q8_store.cu", "q8_attn.cu", "q8_attn_tc.cu", "q8_attn_rows.cu", "q8_weigh.cu", "q8_weigh_tc.cu",
+           "q8_evict.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2", "-I", INCLUDE]
 

@@ -582,11 +582,11 @@ __global__ __launch_bounds__(kAttnThreads, (Cfg<kDw, kNp, kShared>::kPerSm)) voi
 }
 
 // ------------------------------------------------------------------- combine
-// Joins a split tile's parts, in their order.  A CTA takes four rows of a (split
-// tile, kv head) at a time: a warp to a row where the parts are few, so that a row is
-// two trips to memory and no barrier; else the whole CTA to each row in turn.
-constexpr int kCombineThreads = 128;
-constexpr int kCombineRows = 4;
+// Joins a split tile's parts, in their order.  Where the parts are few a warp takes a
+// row, so that a row is two trips to memory and no barrier, and a CTA eight rows; else
+// the whole CTA takes a row.
+constexpr int kCombineThreads = 256;
+constexpr int kCombineRows = kCombineThreads / 32;
 constexpr uint32_t kFewParts = 16;
 constexpr int kMaxParts = 2048;
 
@@ -608,28 +608,27 @@ __device__ __forceinline__ void add_scaled(float4& v, const float4 x, float w) {
 template <int kD>
 __global__ __launch_bounds__(kCombineThreads) void q8_combine_kernel(const AttnArgs a) {
   constexpr int kLanes = kD / 4, kSplit = kCombineThreads / kLanes;
-  __shared__ float s_w[kMaxParts];
+  __shared__ float s_w[kMaxParts], s_l[kMaxParts];
   __shared__ float s_red[kCombineThreads / 32];
   __shared__ float4 s_o[kCombineThreads];
   pdl_wait();
   pdl_release();
   const Q8Header* head = reinterpret_cast<const Q8Header*>(a.plan);
   if (!plan_fits(head, a)) return;
-  const uint32_t G = a.g.group, H = a.c.heads, M = a.g.rows, quads = M / kCombineRows;
+  const uint32_t G = a.g.group, H = a.c.heads, M = a.g.rows;
   const uint32_t* splits = reinterpret_cast<const uint32_t*>(a.plan + a.g.off_split);
   const Q8Item* items = reinterpret_cast<const Q8Item*>(a.plan + a.g.off_items);
-  const uint32_t work = min(head->splits, a.g.ctas) * H * quads;
+  const uint32_t work = min(head->splits, a.g.ctas) * H * M;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   for (uint32_t x = blockIdx.x; x < work; x += gridDim.x) {
-    const uint32_t row0 = x % quads * kCombineRows, h = x / quads % H, first = splits[x / quads / H];
+    const uint32_t row0 = x % M, h = x / M % H, first = splits[x / M / H];
     if (first >= a.g.cap_items) continue;
     const Q8Item item = items[first];
     const uint64_t rows_left = static_cast<uint64_t>(item.q_len) * G - item.row0;
     if (!item_fits(item, a) || item.part < 0 || item.chunks > kMaxParts || row0 >= rows_left) continue;
     const size_t step = static_cast<size_t>(H) * M;
-    const uint32_t rows = static_cast<uint32_t>(min(static_cast<uint64_t>(kCombineRows), rows_left - row0));
     if (item.chunks <= kFewParts) {
-      if (static_cast<uint32_t>(warp) >= rows) continue;
+      if (row0 % kCombineRows != 0 || row0 + warp >= rows_left) continue;
       const uint32_t row = row0 + warp;
       const size_t r0 = (static_cast<size_t>(item.part) * H + h) * M + row;
       const bool in = static_cast<uint32_t>(lane) < item.chunks;
@@ -664,47 +663,49 @@ __global__ __launch_bounds__(kCombineThreads) void q8_combine_kernel(const AttnA
         a.lse[out_row] = sum == 0.0f ? -INFINITY : (top + __log2f(sum)) * 0.69314718055994530942f;
       continue;
     }
-    for (uint32_t row = row0; row < row0 + rows; ++row) {
-      const size_t r0 = (static_cast<size_t>(item.part) * H + h) * M + row;
-      __syncthreads();  // the previous row's reads of shared memory are done
-      float top = -3.4e38f;
-      for (uint32_t p = tid; p < item.chunks; p += kCombineThreads) top = fmaxf(top, a.part_ml[r0 + p * step].x);
+    const size_t r0 = (static_cast<size_t>(item.part) * H + h) * M + row0;
+    __syncthreads();  // the previous row's reads of shared memory are done
+    float top = -3.4e38f;
+    for (uint32_t p = tid; p < item.chunks; p += kCombineThreads) {
+      const float2 ml = a.part_ml[r0 + p * step];
+      s_w[p] = ml.x;
+      s_l[p] = ml.y;
+      top = fmaxf(top, ml.x);
+    }
 #pragma unroll
-      for (int s = 16; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, s));
-      if (lane == 0) s_red[warp] = top;
-      __syncthreads();
+    for (int s = 16; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, s));
+    if (lane == 0) s_red[warp] = top;
+    __syncthreads();
 #pragma unroll
-      for (int w = 0; w < kCombineThreads / 32; ++w) top = fmaxf(top, s_red[w]);
-      __syncthreads();
-      float sum = 0.0f;
-      for (uint32_t p = tid; p < item.chunks; p += kCombineThreads) {
-        const float2 ml = a.part_ml[r0 + p * step];
-        const float w = ex2(ml.x - top);
-        s_w[p] = w;
-        sum = fmaf(ml.y, w, sum);
-      }
+    for (int w = 0; w < kCombineThreads / 32; ++w) top = fmaxf(top, s_red[w]);
+    __syncthreads();
+    float sum = 0.0f;
+    for (uint32_t p = tid; p < item.chunks; p += kCombineThreads) {
+      const float w = ex2(s_w[p] - top);
+      s_w[p] = w;
+      sum = fmaf(s_l[p], w, sum);
+    }
 #pragma unroll
-      for (int s = 16; s > 0; s >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, s);
-      if (lane == 0) s_red[warp] = sum;
-      __syncthreads();
-      sum = 0.0f;
+    for (int s = 16; s > 0; s >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, s);
+    if (lane == 0) s_red[warp] = sum;
+    __syncthreads();
+    sum = 0.0f;
 #pragma unroll
-      for (int w = 0; w < kCombineThreads / 32; ++w) sum += s_red[w];
-      const int ch = (tid % kLanes) * 4;
-      float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-      for (uint32_t p = tid / kLanes; p < item.chunks; p += kSplit)
-        add_scaled(v, *reinterpret_cast<const float4*>(a.part_o + (r0 + p * step) * kD + ch), s_w[p]);
-      s_o[tid] = v;
-      __syncthreads();
-      if (tid < kLanes) {
-        for (int k = 1; k < kSplit; ++k) add_scaled(v, s_o[tid + k * kLanes], 1.0f);
-        const uint32_t rho = item.row0 + row, i = rho / G, hg = rho % G;
-        const size_t out_row = static_cast<size_t>(item.q_start + i) * a.n_heads + h * G + hg;
-        store_out(a, out_row, kD, ch, v, sum == 0.0f ? 0.0f : __fdiv_rn(1.0f, sum));
-        if (tid == 0 && a.lse != nullptr)
-          a.lse[out_row] = sum == 0.0f ? -INFINITY : (top + __log2f(sum)) * 0.69314718055994530942f;
-      }
+    for (int w = 0; w < kCombineThreads / 32; ++w) sum += s_red[w];
+    const int ch = (tid % kLanes) * 4;
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
+    for (uint32_t p = tid / kLanes; p < item.chunks; p += kSplit)
+      add_scaled(v, *reinterpret_cast<const float4*>(a.part_o + (r0 + p * step) * kD + ch), s_w[p]);
+    s_o[tid] = v;
+    __syncthreads();
+    if (tid < kLanes) {
+      for (int k = 1; k < kSplit; ++k) add_scaled(v, s_o[tid + k * kLanes], 1.0f);
+      const uint32_t rho = item.row0 + row0, i = rho / G, hg = rho % G;
+      const size_t out_row = static_cast<size_t>(item.q_start + i) * a.n_heads + h * G + hg;
+      store_out(a, out_row, kD, ch, v, sum == 0.0f ? 0.0f : __fdiv_rn(1.0f, sum));
+      if (tid == 0 && a.lse != nullptr)
+        a.lse[out_row] = sum == 0.0f ? -INFINITY : (top + __log2f(sum)) * 0.69314718055994530942f;
     }
   }
 }
@@ -730,9 +731,9 @@ int launch_split(const AttnArgs& a, cudaStream_t s) {
 }
 
 int launch_combine(const AttnArgs& a, cudaStream_t s) {
-  // at most eight CTAs to an SM; they walk the rows
-  const uint64_t quads = static_cast<uint64_t>(a.g.ctas) * a.c.heads * (a.g.rows / kCombineRows);
-  const dim3 grid(static_cast<uint32_t>(std::min<uint64_t>(quads, 8ull * sm_count())));
+  // at most four CTAs to an SM; they walk the rows
+  const uint64_t rows = static_cast<uint64_t>(a.g.ctas) * a.c.heads * a.g.rows;
+  const dim3 grid(static_cast<uint32_t>(std::min<uint64_t>(rows, 4ull * sm_count())));
   switch (a.c.head_dim) {
     case 64: return launch_pdl(q8_combine_kernel<64>, grid, dim3(kCombineThreads), 0, s, a);
     case 128: return launch_pdl(q8_combine_kernel<128>, grid, dim3(kCombineThreads), 0, s, a);

@@ -70,18 +70,27 @@ __global__ __launch_bounds__(kSelThreads) void q8_evict_select_kernel(const Evic
   const int32_t* table = a.table + static_cast<size_t>(r) * a.stride;
   const uint32_t n = len - a.sinks - a.recent;  // candidates: positions sinks .. sinks + n - 1
   const uint32_t want = a.budget - a.sinks - a.recent;
+  const uint32_t t_shift = __ffs(T) - 1;
   bool bad = false;
+  // nothing here branches, so that a thread's reads overlap: a block that does not exist reads block 0's weight and drops it
   auto read_key = [&](uint32_t i) -> uint32_t {
     const uint32_t p = a.sinks + i;
-    const int32_t blk = __ldg(table + p / T);
-    if (blk < 0 || static_cast<uint32_t>(blk) >= a.c.num_blocks) {
-      bad = true;
-      return 0;
-    }
-    return key_of(a.weights[static_cast<size_t>(blk) * T + p % T]);
+    const int32_t blk = __ldg(table + (p >> t_shift));
+    const bool ok = static_cast<uint32_t>(blk) < a.c.num_blocks;
+    bad |= !ok;
+    const uint32_t k = key_of(a.weights[(static_cast<size_t>(ok ? blk : 0) << t_shift) + (p & (T - 1))]);
+    return ok ? k : 0u;
   };
   const uint32_t cached = min(n, a.keys_cap);
-  for (uint32_t i = t; i < cached; i += kSelThreads) s_key[i] = read_key(i);
+#pragma unroll 1
+  for (uint32_t i0 = t; i0 < cached; i0 += 8 * kSelThreads) {
+    uint32_t k[8];
+#pragma unroll
+    for (int x = 0; x < 8; ++x) k[x] = read_key(min(i0 + x * kSelThreads, n - 1));
+#pragma unroll
+    for (int x = 0; x < 8; ++x)
+      if (i0 + x * kSelThreads < cached) s_key[i0 + x * kSelThreads] = k[x];
+  }
   auto key_at = [&](uint32_t i) { return i < cached ? s_key[i] : read_key(i); };
   __syncthreads();
 
@@ -219,23 +228,34 @@ __global__ __launch_bounds__(32 * kMoveWarps) void q8_evict_move_kernel(const Ev
     const float inv = top > 0.0f ? 1.0f / top : 0.0f;
     uint8_t* out = pool + (static_cast<size_t>(dst) * H + h) * T * D;
     const uint32_t step = per * wpu;
-#pragma unroll 4
-    for (uint32_t e0 = sub * per; e0 < n; e0 += step) {
-      const uint32_t e = e0 + lane / lanes, c = lane % lanes;
-      const uint32_t el = min(e, 127u);
-      // the factor of entry e sits in lane e % 32, register e / 32
-      const float s0 = __shfl_sync(0xFFFFFFFFu, s[0], el & 31), s1 = __shfl_sync(0xFFFFFFFFu, s[1], el & 31);
-      const float s2 = __shfl_sync(0xFFFFFFFFu, s[2], el & 31), s3 = __shfl_sync(0xFFFFFFFFu, s[3], el & 31);
-      const float f = (el < 32 ? s0 : el < 64 ? s1 : el < 96 ? s2 : s3) * inv;
-      if (e < n && s_blk[el] >= 0) {
-        uint4 v = ld_stream16(pool + ((static_cast<size_t>(s_blk[el]) * H + h) * T + s_slot[el]) * D + c * 16);
-        if (f != 1.0f) {
-          v.x = q8_rescale4(v.x, f);
-          v.y = q8_rescale4(v.y, f);
-          v.z = q8_rescale4(v.z, f);
-          v.w = q8_rescale4(v.w, f);
+    constexpr int kBatch = 8;  // entries of a lane whose loads are in flight together
+#pragma unroll 1
+    for (uint32_t e0 = sub * per; e0 < n; e0 += kBatch * step) {
+      const uint32_t c = lane % lanes;
+      uint4 v[kBatch];
+#pragma unroll
+      for (int x = 0; x < kBatch; ++x) {
+        const uint32_t e = e0 + x * step + lane / lanes, el = min(e, 127u);
+        const int32_t blk = s_blk[el];
+        v[x] = ld_stream16_if(pool + ((static_cast<size_t>(max(blk, 0)) * H + h) * T + s_slot[el]) * D + c * 16,
+                              e < n && blk >= 0);
+      }
+#pragma unroll
+      for (int x = 0; x < kBatch; ++x) {
+        const uint32_t e = e0 + x * step + lane / lanes, el = min(e, 127u);
+        // the factor of entry e sits in lane e % 32, register e / 32
+        const float s0 = __shfl_sync(0xFFFFFFFFu, s[0], el & 31), s1 = __shfl_sync(0xFFFFFFFFu, s[1], el & 31);
+        const float s2 = __shfl_sync(0xFFFFFFFFu, s[2], el & 31), s3 = __shfl_sync(0xFFFFFFFFu, s[3], el & 31);
+        const float f = (el < 32 ? s0 : el < 64 ? s1 : el < 96 ? s2 : s3) * inv;
+        if (e < n && s_blk[el] >= 0) {
+          if (f != 1.0f) {
+            v[x].x = q8_rescale4(v[x].x, f);
+            v[x].y = q8_rescale4(v[x].y, f);
+            v[x].z = q8_rescale4(v[x].z, f);
+            v[x].w = q8_rescale4(v[x].w, f);
+          }
+          st16(out + static_cast<size_t>(e) * D + c * 16, v[x]);
         }
-        st16(out + static_cast<size_t>(e) * D + c * 16, v);
       }
     }
     if (sub == 0 && lane == 0 && top > 0.0f) scales[static_cast<size_t>(dst) * H + h] = top;

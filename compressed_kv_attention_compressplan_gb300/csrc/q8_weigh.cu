@@ -13,12 +13,13 @@
 // attention does; the CTAs share the batch's tiles out evenly, and a CTA's warps take
 // one head each and are summed in head order once per run of 256 entries.
 //
-// Many rows (a window of queries): the products and exponentials bound it.  A warp
-// holds 32 entries of a head as bf16 fragments (exact, and queries are bf16 already, so
-// a row tile costs loads and products only) and streams the request's rows past them.
+// Many rows (a window of queries): the products and exponentials bound it.  Up to 128
+// channels the tensor cores take it (q8_weigh_tc.cu); from 256 on a warp holds 16 entries
+// of a head as bf16 fragments (exact, and queries are bf16 already) and streams the
+// request's rows past them.
 #include <algorithm>
 
-#include "q8.cuh"
+#include "q8_weigh.cuh"
 
 namespace ckv {
 namespace {
@@ -27,29 +28,6 @@ constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kTile = 16;
 
-struct WeighArgs {
-  Q8Cache c;
-  const __nv_bfloat16* q;
-  const float* lse;
-  uint32_t num_q;
-  uint32_t n_heads;
-  uint32_t group;
-  uint32_t ratio;
-  float scale_log2;
-  float decay;
-  float* weights;
-  const int64_t* rid;
-  const int64_t* seq_lens;
-  const int64_t* extend_lens;
-  const int64_t* kv_lens;
-  uint32_t batch;
-  const int32_t* table;
-  uint32_t stride;
-  uint32_t num_reqs;
-  uint32_t head_warps;  // warps that share a tile's heads: a power of two
-  uint32_t* d_status;
-};
-
 __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -57,56 +35,9 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// two e4m3 values (as an fp16 pair) -> a bf16 pair, exact
-__device__ __forceinline__ uint32_t f16x2_to_bf16x2(uint32_t h) {
-  const float2 f = f16x2_to_f32(h);
-  return pack_bf16x2(f.x, f.y);
-}
-
-__device__ __forceinline__ void put_weight(const WeighArgs& a, int32_t block, uint32_t slot, float w) {
-  float* dst = a.weights + static_cast<size_t>(block) * a.c.block_tokens + slot;
-  *dst = a.decay == 0.0f ? w : fmaf(a.decay, *dst, w);
-}
-
-// Units (runs of unit_entries entries) before every request that has queries, and its first ragged query.
-__device__ __forceinline__ uint32_t scan_requests(const WeighArgs& a, uint32_t unit_entries, uint32_t* s_unit, uint32_t* s_q,
-                                                  uint32_t* s_scan, unsigned long long* s_scan64) {
-  uint32_t units = 0;
-  unsigned long long queries = 0;
-  for (uint32_t b0 = 0; b0 < a.batch; b0 += kThreads) {
-    const uint32_t b = b0 + threadIdx.x;
-    uint32_t n = 0;
-    unsigned long long ql = 0;
-    if (b < a.batch) {
-      const int64_t el = a.extend_lens[b], kl = a.kv_lens[b], sl = a.seq_lens[b], r = a.rid[b];
-      const bool len_ok = el >= 0 && el <= a.num_q;
-      ql = len_ok ? static_cast<unsigned long long>(el) : 0;
-      const bool ok = len_ok && sl >= el && sl <= 0x7FFFFFFF && kl >= 0 && kl <= 0x7FFFFFF0 &&
-                      kl <= static_cast<int64_t>(a.stride) * a.c.block_tokens && r >= 0 && r < a.num_reqs;
-      if (!ok && blockIdx.x == 0) status_or(a.d_status, CKV_STATUS_BAD_LENGTH);
-      n = ok && el > 0 ? static_cast<uint32_t>((kl + unit_entries - 1) / unit_entries) : 0;
-    }
-    unsigned long long ql_sum;
-    const unsigned long long q0 = queries + block_exclusive<kThreads>(ql, &ql_sum, s_scan64);
-    if (q0 + ql > a.num_q) n = 0;
-    uint32_t n_sum;
-    const uint32_t u0 = units + block_exclusive<kThreads>(n, &n_sum, s_scan);
-    if (b < a.batch) {
-      s_unit[b] = u0;
-      s_q[b] = static_cast<uint32_t>(q0);
-    }
-    units += n_sum;
-    queries += ql_sum;
-  }
-  if (blockIdx.x == 0 && threadIdx.x == 0 && queries != a.num_q) status_or(a.d_status, CKV_STATUS_BAD_TOTAL);
-  __syncthreads();
-  return units;
-}
-
-// kNt tiles of 16 entries to a warp.
-template <int kD, int kNt>
+template <int kD>
 __global__ __launch_bounds__(kThreads) void q8_weigh_rows_kernel(const WeighArgs a) {
-  constexpr int kKj = kD / 64;
+  constexpr int kKj = kD / 64, kNt = 1;  // tiles of 16 entries to a warp
   __shared__ uint32_t s_unit[CKV_MAX_BATCH];
   __shared__ uint32_t s_q[CKV_MAX_BATCH];
   __shared__ uint32_t s_scan[kWarps + 1];
@@ -119,7 +50,7 @@ __global__ __launch_bounds__(kThreads) void q8_weigh_rows_kernel(const WeighArgs
   const uint32_t T = a.c.block_tokens, H = a.c.heads, G = a.group;
   const uint32_t unit_entries = kWarps / a.head_warps * (kNt * kTile);
 
-  const uint32_t units = scan_requests(a, unit_entries, s_unit, s_q, s_scan, s_scan64);
+  const uint32_t units = scan_requests<kThreads>(a, unit_entries, s_unit, s_q, s_scan, s_scan64);
   for (uint32_t u = blockIdx.x; u < units; u += gridDim.x) {
     const uint32_t b = last_not_above(s_unit, a.batch, u);
     const uint32_t kv_len = static_cast<uint32_t>(a.kv_lens[b]);
@@ -275,7 +206,7 @@ __global__ __launch_bounds__(kThreads, StreamCfg<kD>::kPerSm) void q8_weigh_stre
   const uint32_t T = a.c.block_tokens, t_shift = __ffs(T) - 1, H = a.c.heads, G = a.group;
   const uint32_t head0 = warp % a.head_warps, part = warp / a.head_warps, parts = kWarps / a.head_warps;
   const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + warp * C::kStages * C::kStageBytes;
-  const uint32_t tiles = scan_requests(a, kTile, s_tile, s_q, s_scan, s_scan64);
+  const uint32_t tiles = scan_requests<kThreads>(a, kTile, s_tile, s_q, s_scan, s_scan64);
   // this CTA's share of the batch's tiles, request after request, in runs of at most kRun
   const uint32_t from = static_cast<uint32_t>(static_cast<uint64_t>(tiles) * blockIdx.x / gridDim.x);
   const uint32_t to = static_cast<uint32_t>(static_cast<uint64_t>(tiles) * (blockIdx.x + 1) / gridDim.x);
@@ -392,8 +323,8 @@ int launch_weigh(const WeighArgs& a, cudaStream_t s) {
     return launch_pdl(q8_weigh_stream_kernel<kD>, dim3(static_cast<uint32_t>(C::kPerSm * sm_count())), dim3(kThreads),
                       C::kSmem, s, a);
   }
-  constexpr int kNt = kD <= 128 ? 2 : 1;
-  return launch_pdl(q8_weigh_rows_kernel<kD, kNt>, dim3(2u * static_cast<uint32_t>(sm_count())), dim3(kThreads), 0, s, a);
+  if (kD <= 128) return launch_q8_weigh_tc(a, s);
+  return launch_pdl(q8_weigh_rows_kernel<kD < 256 ? 256 : kD>, dim3(2u * static_cast<uint32_t>(sm_count())), dim3(kThreads), 0, s, a);
 }
 
 }  // namespace
@@ -439,6 +370,7 @@ extern "C" int ckv_q8_weigh(const ckv_q8_cache_t* cache, uint32_t n_heads, uint3
   a.num_reqs = num_reqs;
   a.head_warps = 1;
   while (a.head_warps * 2 <= std::min<uint32_t>(a.c.heads, kWarps)) a.head_warps *= 2;
+  a.wait_ns = wait_limit_ns();
   a.d_status = d_status;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   switch (a.c.head_dim) {

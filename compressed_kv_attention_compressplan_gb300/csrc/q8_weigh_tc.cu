@@ -1,0 +1,285 @@
+// q8_weigh_tc.cu -- the cached entries' attention weights when a request brings many
+// rows (a window of queries), on the 5th-generation tensor cores.
+//
+// A unit is 128 entries of a request with all its heads and rows:
+//     S^T [128 entries x 128 rows] = K8 Q^T   per head and chunk of rows,
+// so an entry is a lane of tensor memory, a thread owns it, and its weight
+//     sum over rows of 2^(scale log2(e) k_scale S - lse log2(e))
+// is one register: no lane or warp exchanges anything until the unit's two column
+// halves are added at its end.  Keys become bf16 (exact), the queries are bf16 and are
+// copied as they are, so a chunk costs its copy, its products and 2.5 instructions
+// for each weight.
+//
+// Bound.  128 channels: a chunk's products take 512 cycles, its exponentials 512.
+#include <algorithm>
+
+#include "q8_tc.cuh"
+#include "q8_weigh.cuh"
+
+namespace ckv {
+namespace {
+
+constexpr int kChunk = 128;  // rows
+
+template <int kD>
+struct WtCfg {
+  static constexpr int kSlices = kD / 64;
+  static constexpr int kExpWarps = 8;   // two groups of four; a group takes 64 rows of a chunk
+  static constexpr int kLoadWarps = 8;
+  static constexpr int kWarps = kExpWarps + kLoadWarps + 1;
+  static constexpr int kThreads = 32 * kWarps;
+  static constexpr uint32_t kTileBytes = kSlices * kSlice;  // 128 rows of kD bf16 values
+  static constexpr uint32_t kBytes = 4 * kTileBytes + 1024;  // two stages of keys, two of queries, the alignment
+  static constexpr uint32_t kSmem = kBytes < 120 * 1024 ? 120 * 1024 : kBytes;  // one CTA to an SM: see the attention
+  static constexpr uint32_t kCols = 256;
+};
+
+template <int kD>
+struct alignas(16) WtShared {
+  uint64_t k_full[2], k_free[2], q_full[2], q_free[2], s_full[2], s_free[2], idle;
+  alignas(16) float off[2][kChunk];
+  int vis[2][kChunk];
+  float half[128];
+  uint32_t unit[CKV_MAX_BATCH];
+  uint32_t first_q[CKV_MAX_BATCH];
+  unsigned long long scan64[WtCfg<kD>::kWarps + 1];
+  uint32_t scan[WtCfg<kD>::kWarps + 1];
+  uint32_t tmem;
+};
+
+// bf16 operands
+constexpr uint32_t kBf16 = (1u << 7) | (1u << 10);
+
+template <int kD, bool kShort>
+__global__ __launch_bounds__(WtCfg<kD>::kThreads, 1) void q8_weigh_tc_kernel(const WeighArgs a) {
+  using C = WtCfg<kD>;
+  extern __shared__ uint8_t raw[];
+  __shared__ WtShared<kD> sh;
+  pdl_wait();
+  pdl_release();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t T = a.c.block_tokens, t_shift = __ffs(T) - 1, H = a.c.heads, G = a.group;
+  const uint32_t units = scan_requests<C::kThreads>(a, kEntries, sh.unit, sh.first_q, sh.scan, sh.scan64);
+  if (blockIdx.x >= units) return;
+  const uint32_t base = (smem_addr(raw) + 1023) & ~1023u;
+  const uint32_t k_at = base, q_at = base + 2 * C::kTileBytes;
+  if (warp == C::kWarps - 1) tmem_alloc(smem_addr(&sh.tmem), C::kCols);
+  if (tid == 0) {
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(smem_addr(&sh.k_full[s]), C::kLoadWarps);
+      mbar_init(smem_addr(&sh.q_full[s]), C::kLoadWarps);
+      mbar_init(smem_addr(&sh.k_free[s]), 1);
+      mbar_init(smem_addr(&sh.q_free[s]), C::kExpWarps);
+      mbar_init(smem_addr(&sh.s_full[s]), 1);
+      mbar_init(smem_addr(&sh.s_free[s]), C::kExpWarps);
+    }
+    mbar_init(smem_addr(&sh.idle), 1);
+    fence_mbar_init();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+  Waiter w{static_cast<long long>(a.wait_ns) * 2, true};
+
+  // every role walks the same (unit, head, chunk) sequence; kc and qc count keys' tiles and chunks
+  uint32_t kc = 0, qc = 0;
+  for (uint32_t u = blockIdx.x; u < units; u += gridDim.x) {
+    const uint32_t b = last_not_above(sh.unit, a.batch, u);
+    const uint32_t kv_len = static_cast<uint32_t>(a.kv_lens[b]);
+    const uint32_t q_len = static_cast<uint32_t>(a.extend_lens[b]);
+    const uint32_t phase = a.ratio - 1 - static_cast<uint32_t>(a.seq_lens[b]) % a.ratio;
+    const uint32_t rows = q_len * G, chunks = (rows + kChunk - 1) / kChunk;
+    const uint32_t e0 = (u - sh.unit[b]) * kEntries;
+    const int32_t* table = a.table + static_cast<size_t>(a.rid[b]) * a.stride;
+    if (warp >= C::kExpWarps && warp < C::kExpWarps + C::kLoadWarps) {
+      // ---- keys into bf16, queries as they are
+      const int lw = warp - C::kExpWarps, q = lane & 3;
+      const uint32_t tok = lw * 8 + (lane >> 2);  // and tok + 64
+      const uint8_t* src[2];
+      bool ok[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t e = e0 + tok + 64 * i;
+        const int32_t blk = __ldg(table + (min(e, kv_len - 1) >> t_shift));
+        const bool valid = static_cast<uint32_t>(blk) < a.c.num_blocks;
+        ok[i] = valid && e < kv_len;
+        src[i] = a.c.k + ((static_cast<size_t>(valid ? blk : 0) * H << t_shift) + (e & (T - 1))) * kD + q * 16;
+      }
+      uint4 buf[C::kSlices][2];
+      auto load = [&](uint32_t h) {
+#pragma unroll
+        for (int s = 0; s < C::kSlices; ++s) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            buf[s][i] = ld_stream16_if(src[i] + (static_cast<size_t>(h) << t_shift) * kD + s * 64, ok[i] && h < H);
+        }
+      };
+      load(0);
+      for (uint32_t h = 0; h < H; ++h, ++kc) {
+        const uint32_t ks = kc & 1;
+        w.wait<kShort>(&sh.k_free[ks], ((kc >> 1) & 1) ^ 1);
+#pragma unroll
+        for (int s = 0; s < C::kSlices; ++s) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t at = k_at + ks * C::kTileBytes + s * kSlice + (tok + 64 * i) * 128, sw = tok & 7;
+            const uint32_t x[4] = {buf[s][i].x, buf[s][i].y, buf[s][i].z, buf[s][i].w};
+#pragma unroll
+            for (int y = 0; y < 2; ++y)
+              asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at + (((2 * q + y) ^ sw) << 4)),
+                           "r"(f16x2_to_bf16x2(q8_lo_f16x2(x[2 * y]))), "r"(f16x2_to_bf16x2(q8_hi_f16x2(x[2 * y]))),
+                           "r"(f16x2_to_bf16x2(q8_lo_f16x2(x[2 * y + 1]))), "r"(f16x2_to_bf16x2(q8_hi_f16x2(x[2 * y + 1])))
+                           : "memory");
+          }
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&sh.k_full[ks]));
+        load(h + 1);
+        for (uint32_t c = 0; c < chunks; ++c, ++qc) {
+          const uint32_t qs = qc & 1;
+          w.wait<kShort>(&sh.q_free[qs], ((qc >> 1) & 1) ^ 1);
+          // this warp's 16 rows, 16 bytes a lane at a time
+          constexpr int kRowChunks = kD / 8;  // 16-byte chunks of a row
+#pragma unroll
+          for (int x = 0; x < kRowChunks / 2; ++x) {
+            const uint32_t i = x * 32 + lane, n = lw * 16 + i / kRowChunks, cc = i % kRowChunks;
+            const uint32_t rho = min(c * kChunk + n, rows - 1);
+            const size_t row = static_cast<size_t>(sh.first_q[b] + rho / G) * a.n_heads + h * G + rho % G;
+            cp_async16(q_at + qs * C::kTileBytes + (cc >> 3) * kSlice + n * 128 + (((cc & 7) ^ (n & 7)) << 4),
+                       a.q + row * kD + cc * 8, 16u);
+          }
+          cp_async_commit();
+          if (lane < 16) {
+            const uint32_t n = lw * 16 + lane, at = c * kChunk + n, rho = min(at, rows - 1), i = rho / G;
+            const float lse = __ldg(a.lse + static_cast<size_t>(sh.first_q[b] + i) * a.n_heads + h * G + rho % G);
+            const int64_t see = at < rows ? q8_visible(kv_len, q_len - 1 - i, phase, a.ratio) : 0;
+            sh.vis[qs][n] = static_cast<int>(see);
+            // a row that saw nothing weighs nothing, nor does one past the last
+            sh.off[qs][n] = at >= rows || lse == -INFINITY ? -INFINITY : lse * -kLog2e;
+          }
+          cp_async_wait<0>();
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_addr(&sh.q_full[qs]));
+        }
+      }
+    } else if (warp < C::kExpWarps) {
+      const int group = warp >> 2, quarter = warp & 3, entry = quarter * 32 + lane;
+      const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
+      const uint32_t e = e0 + entry;
+      const int32_t blk = __ldg(table + (min(e, kv_len - 1) >> t_shift));
+      const bool valid = static_cast<uint32_t>(blk) < a.c.num_blocks;
+      if (!valid && e < kv_len && group == 0) status_or(a.d_status, CKV_STATUS_BAD_INDEX);
+      const float* scales = a.c.k_scale + static_cast<size_t>(valid ? blk : 0) * H;
+      float next = __ldg(scales);
+      F2 sum = f2_pack(0.0f, 0.0f);
+      for (uint32_t h = 0; h < H; ++h) {
+        const float f = next * a.scale_log2;
+        next = __ldg(scales + min(h + 1, H - 1));
+        const F2 f2 = f2_pack(f, f);
+        for (uint32_t c = 0; c < chunks; ++c, ++qc) {
+          const uint32_t qs = qc & 1;
+          // rows see more and more: the chunk's first row says whether the tile is whole for all
+          const int64_t least = q8_visible(kv_len, q_len - 1 - (c * kChunk) / G, phase, a.ratio);
+          const bool edge = static_cast<int64_t>(e0) + kEntries > least;
+          w.wait<kShort>(&sh.s_full[qs], (qc >> 1) & 1);
+          tc_fence_after();
+#pragma unroll 1
+          for (int x0 = 0; x0 < 64; x0 += 32) {
+            float s[32];
+            tmem_load32(tmem + lanes + qs * kChunk + group * 64 + x0, s);
+            const float* off = sh.off[qs] + group * 64 + x0;
+            const int* vis = sh.vis[qs] + group * 64 + x0;
+#pragma unroll
+            for (int x = 0; x < 32; x += 4) {
+              const float4 o = *reinterpret_cast<const float4*>(off + x);
+              float t0, t1, t2, t3;
+              f2_unpack(f2_fma(f2_pack(s[x], s[x + 1]), f2, f2_pack(o.x, o.y)), t0, t1);
+              f2_unpack(f2_fma(f2_pack(s[x + 2], s[x + 3]), f2, f2_pack(o.z, o.w)), t2, t3);
+              float w0 = ex2(t0), w1 = ex2(t1), w2 = ex2(t2), w3 = ex2(t3);
+              if (edge) {
+                w0 = static_cast<int>(e) < vis[x] ? w0 : 0.0f;
+                w1 = static_cast<int>(e) < vis[x + 1] ? w1 : 0.0f;
+                w2 = static_cast<int>(e) < vis[x + 2] ? w2 : 0.0f;
+                w3 = static_cast<int>(e) < vis[x + 3] ? w3 : 0.0f;
+              }
+              sum = f2_add(sum, f2_add(f2_pack(w0, w1), f2_pack(w2, w3)));
+            }
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(smem_addr(&sh.s_free[qs]));
+            mbar_arrive(smem_addr(&sh.q_free[qs]));
+          }
+        }
+      }
+      float s0, s1;
+      f2_unpack(sum, s0, s1);
+      if (group == 1) sh.half[entry] = s0 + s1;
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+      if (group == 0 && e < kv_len && valid) put_weight(a, blk, e & (T - 1), (s0 + s1) + sh.half[entry]);
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+    } else {
+      for (uint32_t h = 0; h < H; ++h, ++kc) {
+        const uint32_t ks = kc & 1;
+        w.wait<kShort>(&sh.k_full[ks], (kc >> 1) & 1);
+        for (uint32_t c = 0; c < chunks; ++c, ++qc) {
+          const uint32_t qs = qc & 1;
+          w.wait<kShort>(&sh.q_full[qs], (qc >> 1) & 1);
+          w.wait<kShort>(&sh.s_free[qs], ((qc >> 1) & 1) ^ 1);
+          tc_fence_after();
+          if (elect_one()) {
+            if (w.live) {
+#pragma unroll
+              for (int s = 0; s < C::kSlices; ++s) {
+                const uint64_t ka = smem_operand(k_at + ks * C::kTileBytes + s * kSlice, 0);
+                const uint64_t qb = smem_operand(q_at + qs * C::kTileBytes + s * kSlice, 0);
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                  tc_mma(tmem + qs * kChunk, ka + 2 * x, qb + 2 * x, mma_shape(128, kChunk, false, false) | kBf16,
+                         s > 0 || x > 0);
+              }
+            }
+            tc_commit(smem_addr(&sh.s_full[qs]));
+            if (c + 1 == chunks) tc_commit(smem_addr(&sh.k_free[ks]));
+          }
+          __syncwarp();
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == C::kWarps - 1) {
+    // every product is done before its memory is given back
+    if (elect_one()) tc_commit(smem_addr(&sh.idle));
+    __syncwarp();
+    const bool done = warp_wait_for<false>(smem_addr(&sh.idle), 0, kWaitLimitNs);
+    if (!done) w.live = false;
+    tmem_free(tmem, C::kCols);
+  }
+  if (!w.live && lane == 0) status_or(a.d_status, CKV_STATUS_TIMEOUT);
+}
+
+template <int kD>
+int launch(const WeighArgs& a, cudaStream_t s) {
+  using C = WtCfg<kD>;
+  const bool brief = a.wait_ns < kShortWaitNs;
+  auto* kernel = brief ? q8_weigh_tc_kernel<kD, true> : q8_weigh_tc_kernel<kD, false>;
+  static std::atomic<uint64_t> done[2];
+  const int rc = allow_smem(reinterpret_cast<const void*>(kernel), C::kSmem, done[brief ? 1 : 0]);
+  if (rc) return rc;
+  return launch_pdl(kernel, dim3(static_cast<uint32_t>(sm_count())), dim3(C::kThreads), C::kSmem, s, a);
+}
+
+}  // namespace
+
+int launch_q8_weigh_tc(const WeighArgs& a, cudaStream_t s) {
+  return a.c.head_dim == 64 ? launch<64>(a, s) : launch<128>(a, s);
+}
+
+}  // namespace ckv
