@@ -52,9 +52,11 @@ __global__ __launch_bounds__(kPlanThreads) void plan_q8_attn_kernel(const AttnPl
   __shared__ unsigned long long s_pos[kPlanThreads];
   __shared__ uint32_t s_item[kPlanThreads], s_part[kPlanThreads];
   __shared__ unsigned long long s_scan[kPlanThreads / 32 + 1];
+  __shared__ uint32_t s_most;
   pdl_wait();
   pdl_release();
   const uint32_t t = threadIdx.x;
+  if (t == 0) s_most = 0;  // the scans' barriers come before its use
   const uint32_t M = a.g.rows, G = a.g.group;
   Q8Header* head = reinterpret_cast<Q8Header*>(a.plan);
   uint32_t* first = reinterpret_cast<uint32_t*>(a.plan + a.g.off_first);
@@ -134,7 +136,10 @@ __global__ __launch_bounds__(kPlanThreads) void plan_q8_attn_kernel(const AttnPl
     s_pos[t] = p;
     s_item[t] = it;
     s_part[t] = n > 1 ? part0 + (static_cast<uint32_t>(ex >> 32) & 0xFFFFu) : kInvalidU32;
-    if (n > 1) split[split0 + static_cast<uint32_t>(ex >> 48)] = it;
+    if (n > 1) {
+      split[split0 + static_cast<uint32_t>(ex >> 48)] = it;
+      atomicMax(&s_most, n);
+    }
     __syncthreads();
     const uint32_t strip = min(static_cast<uint32_t>(kPlanThreads), nt - i0);
     const uint32_t end = item0 + static_cast<uint32_t>(packed_sum);
@@ -182,6 +187,7 @@ __global__ __launch_bounds__(kPlanThreads) void plan_q8_attn_kernel(const AttnPl
     head->num_q = a.num_q;
     head->ratio = a.ratio;
     head->cap_ctas = a.g.ctas;
+    head->most = s_most;  // (the last strip ended with a barrier)
     if (total_q != a.num_q) status_or(a.d_status, CKV_STATUS_BAD_TOTAL);
   }
 }
@@ -584,7 +590,8 @@ __global__ __launch_bounds__(kAttnThreads, (Cfg<kDw, kNp, kShared>::kPerSm)) voi
 // ------------------------------------------------------------------- combine
 // Joins a split tile's parts, in their order.  Where the parts are few a warp takes a
 // row, so that a row is two trips to memory and no barrier, and a CTA eight rows; else
-// the whole CTA takes a row.
+// the whole CTA takes a row: work number y + x * (rows / 8) is row x of the eight y,
+// and only tiles of many parts have work beyond x = 0.
 constexpr int kCombineThreads = 256;
 constexpr int kCombineRows = kCombineThreads / 32;
 constexpr uint32_t kFewParts = 16;
@@ -618,17 +625,19 @@ __global__ __launch_bounds__(kCombineThreads) void q8_combine_kernel(const AttnA
   const uint32_t G = a.g.group, H = a.c.heads, M = a.g.rows;
   const uint32_t* splits = reinterpret_cast<const uint32_t*>(a.plan + a.g.off_split);
   const Q8Item* items = reinterpret_cast<const Q8Item*>(a.plan + a.g.off_items);
-  const uint32_t work = min(head->splits, a.g.ctas) * H * M;
+  const uint32_t eights = min(head->splits, a.g.ctas) * H * (M / kCombineRows);
+  const uint32_t work = head->most > kFewParts ? eights * kCombineRows : eights;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   for (uint32_t x = blockIdx.x; x < work; x += gridDim.x) {
-    const uint32_t row0 = x % M, h = x / M % H, first = splits[x / M / H];
+    const uint32_t y = x % eights, of = M / kCombineRows, sub = x / eights;
+    const uint32_t row0 = y % of * kCombineRows + sub, h = y / of % H, first = splits[y / of / H];
     if (first >= a.g.cap_items) continue;
     const Q8Item item = items[first];
     const uint64_t rows_left = static_cast<uint64_t>(item.q_len) * G - item.row0;
     if (!item_fits(item, a) || item.part < 0 || item.chunks > kMaxParts || row0 >= rows_left) continue;
     const size_t step = static_cast<size_t>(H) * M;
     if (item.chunks <= kFewParts) {
-      if (row0 % kCombineRows != 0 || row0 + warp >= rows_left) continue;
+      if (sub != 0 || row0 + warp >= rows_left) continue;
       const uint32_t row = row0 + warp;
       const size_t r0 = (static_cast<size_t>(item.part) * H + h) * M + row;
       const bool in = static_cast<uint32_t>(lane) < item.chunks;
@@ -645,20 +654,20 @@ __global__ __launch_bounds__(kCombineThreads) void q8_combine_kernel(const AttnA
       const bool own = kD >= 128 || lane < kLanes;
       float4 v[kVecs];
 #pragma unroll
-      for (int y = 0; y < kVecs; ++y) v[y] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      for (int z = 0; z < kVecs; ++z) v[z] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       const float* o = a.part_o + r0 * kD + lane * 4;
 #pragma unroll 4
       for (uint32_t p = 0; p < item.chunks; ++p) {
         const float wp = __shfl_sync(0xFFFFFFFFu, w, p);
 #pragma unroll
-        for (int y = 0; y < kVecs; ++y)
-          if (own) add_scaled(v[y], *reinterpret_cast<const float4*>(o + p * step * kD + y * 128), wp);
+        for (int z = 0; z < kVecs; ++z)
+          if (own) add_scaled(v[z], *reinterpret_cast<const float4*>(o + p * step * kD + z * 128), wp);
       }
       const uint32_t rho = item.row0 + row, i = rho / G, hg = rho % G;
       const size_t out_row = static_cast<size_t>(item.q_start + i) * a.n_heads + h * G + hg;
 #pragma unroll
-      for (int y = 0; y < kVecs; ++y)
-        if (own) store_out(a, out_row, kD, lane * 4 + y * 128, v[y], inv);
+      for (int z = 0; z < kVecs; ++z)
+        if (own) store_out(a, out_row, kD, lane * 4 + z * 128, v[z], inv);
       if (lane == 0 && a.lse != nullptr)
         a.lse[out_row] = sum == 0.0f ? -INFINITY : (top + __log2f(sum)) * 0.69314718055994530942f;
       continue;

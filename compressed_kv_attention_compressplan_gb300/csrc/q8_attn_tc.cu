@@ -33,6 +33,7 @@ struct TcCfg {
   static_assert(kD == 256 || kD == 512, "");
   static constexpr bool kLatent = kShared;
   static constexpr bool kGroupScales = false;
+  static constexpr bool kPrefetch = true;
   static constexpr int kRows = 64;
   static constexpr int kSlices = kD / 64;
   static constexpr int kBlocks = kD / 128;  // accumulators of 128 channels

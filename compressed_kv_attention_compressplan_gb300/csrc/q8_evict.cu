@@ -172,7 +172,7 @@ constexpr int kMoveWarps = 8;
 
 // One CTA per (new block, request); a warp per (head, side), or several where
 // there are fewer of those than warps.
-__global__ __launch_bounds__(32 * kMoveWarps) void q8_evict_move_kernel(const EvictArgs a) {
+__global__ __launch_bounds__(32 * kMoveWarps, 4) void q8_evict_move_kernel(const EvictArgs a) {
   __shared__ int32_t s_blk[128];
   __shared__ uint32_t s_slot[128];
   pdl_wait();
@@ -228,7 +228,7 @@ __global__ __launch_bounds__(32 * kMoveWarps) void q8_evict_move_kernel(const Ev
     const float inv = top > 0.0f ? 1.0f / top : 0.0f;
     uint8_t* out = pool + (static_cast<size_t>(dst) * H + h) * T * D;
     const uint32_t step = per * wpu;
-    constexpr int kBatch = 8;  // entries of a lane whose loads are in flight together
+    constexpr int kBatch = 4;  // entries of a lane whose loads are in flight together
 #pragma unroll 1
     for (uint32_t e0 = sub * per; e0 < n; e0 += kBatch * step) {
       const uint32_t c = lane % lanes;

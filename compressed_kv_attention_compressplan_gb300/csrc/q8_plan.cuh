@@ -42,7 +42,8 @@ struct Q8Header {  // 64 bytes
   uint32_t num_q;
   uint32_t ratio;
   uint32_t cap_ctas;
-  uint32_t reserved[7];
+  uint32_t most;  // parts of the tile that has most
+  uint32_t reserved[6];
 };
 static_assert(sizeof(Q8Header) == 64, "");
 

@@ -10,7 +10,9 @@
 //
 // Few rows (a decode step): the keys' bytes bound it.  A warp keeps a head's query
 // fragments and streams its tiles of 16 entries through a ring of its own, as the split
-// attention does; the CTAs share the batch's tiles out evenly, and a CTA's warps take
+// attention does, but with the entries as the product's 16 rows and the queries as its
+// columns, eight or sixteen: a batch of up to eight rows a head then costs half the products
+// and exponentials, and an entry's sum crosses four lanes.  The CTAs share the batch's tiles out evenly, and a CTA's warps take
 // one head each and are summed in head order once per run of 256 entries.
 //
 // Many rows (a window of queries): the products and exponentials bound it.  Up to 128
@@ -190,7 +192,8 @@ struct StreamCfg {
   static constexpr int kRun = 16;  // tiles that are summed over the heads at once
 };
 
-template <int kD>
+// kCols: query rows of a pass, 8 or 16.
+template <int kD, int kCols>
 __global__ __launch_bounds__(kThreads, StreamCfg<kD>::kPerSm) void q8_weigh_stream_kernel(const WeighArgs a) {
   using C = StreamCfg<kD>;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -228,7 +231,7 @@ __global__ __launch_bounds__(kThreads, StreamCfg<kD>::kPerSm) void q8_weigh_stre
     for (uint32_t i = lane; i < C::kRun * kTile; i += 32) s_sum[warp][i] = 0.0f;
     __syncwarp();
     for (uint32_t h = head0; h < H; h += a.head_warps) {
-      for (uint32_t r0 = 0; r0 < rows; r0 += 16) {
+      for (uint32_t r0 = 0; r0 < rows; r0 += kCols) {
         auto issue = [&](uint32_t i) {
           if (i < mine) {
             const uint32_t t = part + i * parts, e = first + t * kTile;
@@ -248,18 +251,26 @@ __global__ __launch_bounds__(kThreads, StreamCfg<kD>::kPerSm) void q8_weigh_stre
         };
 #pragma unroll
         for (int s = 0; s < C::kStages - 1; ++s) issue(s);
-        uint32_t qf[kD / 16][4];
-        float rf[2], off[2];
-        int64_t vis[2];
+        // column g of column tile c is row r0 + 8 c + g; a lane's results are columns 2q and 2q + 1
+        uint32_t qf[kD / 16][4];  // [..][c] and [..][2 + c]: the two halves of a k step
+        float f[kCols / 8][2], off[kCols / 8][2];
+        int64_t vis[kCols / 8][2];
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const bool in = r0 + g + 8 * r < rows;
-          const uint32_t rho = in ? r0 + g + 8 * r : 0, i = rho / G, hg = rho % G;
-          const size_t row = static_cast<size_t>(s_q[b] + i) * a.n_heads + h * G + hg;
-          vis[r] = in ? q8_visible(kv_len, q_len - 1 - i, phase, a.ratio) : 0;
-          const float lse = in ? __ldg(a.lse + row) : 0.0f;
-          off[r] = lse == -INFINITY ? -INFINITY : lse * -kLog2e;  // a row that saw nothing weighs nothing
-          rf[r] = load_query<kD>(a.q + row * kD, in, q, r, qf) * a.scale_log2;
+        for (int c = 0; c < kCols / 8; ++c) {
+          const uint32_t row = r0 + 8 * c + g;
+          const bool in = row < rows;
+          const uint32_t rho = in ? row : 0, i = rho / G, hg = rho % G;
+          const size_t at = static_cast<size_t>(s_q[b] + i) * a.n_heads + h * G + hg;
+          const float lse = in ? __ldg(a.lse + at) : -INFINITY;
+          const float fg = load_query<kD>(a.q + at * kD, in, q, c, qf) * a.scale_log2;
+          const float og = lse == -INFINITY ? -INFINITY : lse * -kLog2e;  // a row that saw nothing weighs nothing
+          const int vg = in ? static_cast<int>(q8_visible(kv_len, q_len - 1 - i, phase, a.ratio)) : 0;
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            f[c][e] = __shfl_sync(0xFFFFFFFFu, fg, (2 * q + e) * 4);
+            off[c][e] = __shfl_sync(0xFFFFFFFFu, og, (2 * q + e) * 4);
+            vis[c][e] = __shfl_sync(0xFFFFFFFFu, vg, (2 * q + e) * 4);
+          }
         }
         for (uint32_t i = 0; i < mine; ++i) {
           cp_async_wait<C::kStages - 2>();
@@ -267,27 +278,37 @@ __global__ __launch_bounds__(kThreads, StreamCfg<kD>::kPerSm) void q8_weigh_stre
           issue(i + C::kStages - 1);
           const uint32_t st = ring + (i % C::kStages) * C::kStageBytes, t = part + i * parts;
           const float ks = lds_f32(st + kTile * kD);
-          float s[2][4];
-          tile_scores<kD>(st, g, q, qf, s);
-          const float f[2] = {rf[0] * ks, rf[1] * ks};
+          float s[kCols / 8][4] = {};
 #pragma unroll
-          for (int n = 0; n < 2; ++n) {
-            float sum[2] = {0.0f, 0.0f};
+          for (int j = 0; j < kD / 64; ++j) {
+            const int cc = lane_chunk<kD>(j, q);
+            const uint4 lo = lds16(st + tile_off<kD>(g, cc)), hi = lds16(st + tile_off<kD>(8 + g, cc));
+            const uint32_t x[4] = {lo.x, lo.y, lo.z, lo.w}, y[4] = {hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+            for (int z = 0; z < 4; ++z) {
+              const uint32_t kf[4] = {q8_lo_f16x2(x[z]), q8_lo_f16x2(y[z]), q8_hi_f16x2(x[z]), q8_hi_f16x2(y[z])};
+#pragma unroll
+              for (int c = 0; c < kCols / 8; ++c) mma_f16(s[c], kf, qf[j * 4 + z][c], qf[j * 4 + z][2 + c]);
+            }
+          }
+          float sum[2] = {0.0f, 0.0f};  // entries g and 8 + g
+#pragma unroll
+          for (int c = 0; c < kCols / 8; ++c) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const int64_t at = first + t * kTile + n * 8 + 2 * q + (e & 1);
-              const float w = ex2(fmaf(s[n][e], f[e >> 1], off[e >> 1]));
-              sum[e & 1] += at < vis[e >> 1] ? w : 0.0f;
+              const int64_t at = first + t * kTile + (e >> 1) * 8 + g;
+              const float w = ex2(fmaf(s[c][e], f[c][e & 1] * ks, off[c][e & 1]));
+              sum[e >> 1] += at < vis[c][e & 1] ? w : 0.0f;
             }
+          }
 #pragma unroll
-            for (int x = 4; x < 32; x <<= 1) {
-              sum[0] += __shfl_xor_sync(0xFFFFFFFFu, sum[0], x);
-              sum[1] += __shfl_xor_sync(0xFFFFFFFFu, sum[1], x);
-            }
-            if (g == 0) {  // one lane to an entry, the same one every time
-              s_sum[warp][t * kTile + n * 8 + 2 * q] += sum[0];
-              s_sum[warp][t * kTile + n * 8 + 2 * q + 1] += sum[1];
-            }
+          for (int x = 1; x < 4; x <<= 1) {
+            sum[0] += __shfl_xor_sync(0xFFFFFFFFu, sum[0], x);
+            sum[1] += __shfl_xor_sync(0xFFFFFFFFu, sum[1], x);
+          }
+          if (q == 0) {  // one lane to an entry, the same one every time
+            s_sum[warp][t * kTile + g] += sum[0];
+            s_sum[warp][t * kTile + 8 + g] += sum[1];
           }
         }
         cp_async_wait<0>();
@@ -314,14 +335,16 @@ __global__ __launch_bounds__(kThreads, StreamCfg<kD>::kPerSm) void q8_weigh_stre
 
 template <int kD>
 int launch_weigh(const WeighArgs& a, cudaStream_t s) {
-  // Rows of a request and kv head: up to 32 (two row tiles) the keys are streamed, once for each tile.
-  if (static_cast<uint64_t>(a.num_q) * a.group <= 32ull * a.batch) {
+  // Rows of a request and kv head: up to 32 the keys are streamed, once for every 8 or 16 of them.
+  const uint64_t all = static_cast<uint64_t>(a.num_q) * a.group;
+  if (all <= 32ull * a.batch) {
     using C = StreamCfg<kD>;
-    static std::atomic<uint64_t> done;
-    const int rc = allow_smem(reinterpret_cast<const void*>(q8_weigh_stream_kernel<kD>), C::kSmem, done);
+    const bool narrow = all <= 8ull * a.batch;
+    auto* kernel = narrow ? q8_weigh_stream_kernel<kD, 8> : q8_weigh_stream_kernel<kD, 16>;
+    static std::atomic<uint64_t> done[2];
+    const int rc = allow_smem(reinterpret_cast<const void*>(kernel), C::kSmem, done[narrow]);
     if (rc) return rc;
-    return launch_pdl(q8_weigh_stream_kernel<kD>, dim3(static_cast<uint32_t>(C::kPerSm * sm_count())), dim3(kThreads),
-                      C::kSmem, s, a);
+    return launch_pdl(kernel, dim3(static_cast<uint32_t>(C::kPerSm * sm_count())), dim3(kThreads), C::kSmem, s, a);
   }
   if (kD <= 128) return launch_q8_weigh_tc(a, s);
   return launch_pdl(q8_weigh_rows_kernel<kD < 256 ? 256 : kD>, dim3(2u * static_cast<uint32_t>(sm_count())), dim3(kThreads), 0, s, a);
