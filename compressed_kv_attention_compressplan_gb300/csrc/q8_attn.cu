@@ -226,9 +226,8 @@ int q8_attn_geom(const Q8Cache& c, uint32_t batch, uint32_t num_q, uint32_t n_he
   if (n_heads == 0 || n_heads % c.heads != 0 || n_heads / c.heads > CKV_Q8_MAX_GROUP) return CKV_ERR_SIZE;
   g->group = n_heads / c.heads;
   if (static_cast<uint64_t>(num_q) * g->group > 0x7FFFFFFFull) return CKV_ERR_SIZE;  // row numbers are 32-bit
-  // The split kernel's tiles are 16 rows; the tensor-core kernel's are 128 (64 from 256 channels on), and separate keys
-  // and values of 512 channels do not fit its shared memory.
-  g->tc = batch > 0 && static_cast<uint64_t>(num_q) * g->group >= 48ull * batch && (c.head_dim < 512 || c.v == nullptr);
+  // The split kernel's tiles are 16 rows; the tensor-core kernels' are 256, or 64 from 256 channels on.
+  g->tc = batch > 0 && static_cast<uint64_t>(num_q) * g->group >= 48ull * batch;
   if (g->tc) {
     g->rows = c.head_dim <= 128 ? 256 : 64;
     g->ctas = std::max<uint32_t>(1, static_cast<uint32_t>(sm_count()) / c.heads);

@@ -2,25 +2,29 @@
 // tensor cores from 256 channels on: decode where many heads share one latent
 // cache, and prefill chunks.  The mathematics is the split kernel's.
 //
-// Transposed products.  A tile is 128 entries, the M of both products:
-//     S^T [128 entries x 64 rows] = K8 Q^T,   O^T [128 channels x 64 rows] += V8^T W^T,
-// one O^T per 128 channels.  The accumulators of 512 channels by 64 rows take
-// 256 columns of tensor memory, so the whole width of a latent entry fits beside the
-// scores and its keys are read and multiplied once.  With entries on the lanes a
-// thread owns one entry: the entry's scales are two registers of its own, row sums
-// stay in registers until the end, and no score crosses lanes but in the rare step
-// that raises a row's reference (one vote a tile asks for it).  The weights W^T go
-// through shared memory as they stand, an entry's row of 64 weights being the
+// Transposed 8-bit products.  A tile is 128 entries, the M of both products, and its
+// e4m3 values are the operands as they lie in the cache -- nothing is converted:
+//     S^T [128 entries x 64 rows] = K8 Q^T,   O^T [128 channels x 64 rows] += V8^T W^T.
+// What is wider than 8 bits is a sum of 8-bit terms.  A query row is scaled by a power of
+// two that puts its largest value in [2^7, 2^8) and is e4m3 + e4m3: bf16's 8 bits are 4
+// and 4, so the two are exact down to 2^-9 of that value, and under it the error is
+// at most 2^-17 of it; both are columns of one product (N = 128), whose halves are added.
+// A weight (at most 2^14, see the split kernel) is e5m2 + e5m2 + e5m2, each the nearest
+// to what the ones before leave: 2^-9 of it in all, with fp16's range below.
+//
+// The accumulators of 512 channels by 64 rows take 256 columns of tensor memory, so the
+// whole width of a latent entry fits beside two buffers of scores, and its entries are read
+// once.  With entries on the lanes a thread owns one entry: the entry's scales are two
+// registers of its own, row sums stay in registers until the end, and no score crosses
+// lanes but in the rare step that raises a row's reference (one vote a tile asks for it).
+// The weights go through shared memory as they stand: an entry's row of 64 of them is the
 // swizzled row that the second product reads.
 //
-// Roles.  Eight warps turn e4m3 into fp16 operands (q8_tc.cuh); one thread issues the
-// products; groups of four warps take 16 rows each through the softmax.  In a latent
-// cache one buffer is both operands, and its slices are handed back as the second
-// product finishes with them.
+// Roles.  Eight warps copy entries into the operands' swizzled layout, a stage ahead; one
+// thread issues the products; groups of four warps take 16 rows each through the softmax.
 //
-// Bound.  Of 512 channels one tile fits in shared memory, so a tile's conversion, products
-// and softmax follow one another: the second product's blocks overlap the next tile's
-// conversion, the first product's slices the rest of it.
+// Bound.  512 channels: a tile is 64 KB from memory, 2.8 k cycles of an SM's share of it;
+// shared memory feeds the products 128 KB and 288 KB, 3.3 k cycles.
 #include <algorithm>
 
 #include "q8_tc.cuh"
@@ -28,43 +32,38 @@
 namespace ckv {
 namespace {
 
+constexpr uint32_t kSlice8 = kEntries * 128;  // bytes of 128 channels of a tile
+constexpr uint32_t kTerm = kEntries * 64;     // bytes of one term of a tile's weights
+
 template <int kD, bool kShared>
 struct TcCfg {
   static_assert(kD == 256 || kD == 512, "");
-  static constexpr bool kLatent = kShared;
-  static constexpr bool kGroupScales = false;
-  static constexpr bool kPrefetch = true;
   static constexpr int kRows = 64;
-  static constexpr int kSlices = kD / 64;
-  static constexpr int kBlocks = kD / 128;  // accumulators of 128 channels
-  static constexpr int kStages = kShared && kD == 256 ? 2 : 1;
-  static constexpr bool kLag = kStages == 2 || !kShared;  // the second product runs a tile behind the first
-  static constexpr int kFree = kShared ? kBlocks : 1;     // barriers that hand a K stage back
-  static constexpr int kGroups = kRows / 16;              // softmax groups of four warps
+  static constexpr int kSlices = kD / 128;  // also the accumulators, of 128 channels each
+  static constexpr int kStages = kD == 512 && !kShared ? 1 : 2;
+  static constexpr int kGroups = kRows / 16;  // softmax groups of four warps
   static constexpr int kSoftWarps = 4 * kGroups;
-  static constexpr int kConvWarps = 8;
-  static constexpr int kWarps = kSoftWarps + kConvWarps + 1;
+  static constexpr int kCopyWarps = 8;
+  static constexpr int kWarps = kSoftWarps + kCopyWarps + 1;
   static constexpr int kThreads = 32 * kWarps;
-  static constexpr int kLoads = kEntries / (8 * kConvWarps);  // 16-byte loads of a converting thread per slice
-  static constexpr int kUnits = kSlices * (kShared ? 1 : 2);  // slices of a tile, K's and V's
-  static constexpr int kAhead = 4;
-  static constexpr uint32_t kQBytes = kSlices * kRows * 128;
-  static constexpr uint32_t kKBytes = kStages * kSlices * kSlice;
+  static constexpr uint32_t kTile = kSlices * kSlice8;
+  static constexpr uint32_t kQBytes = kSlices * kSlice8;  // 64 rows, two terms
+  static constexpr uint32_t kKBytes = kStages * kTile;
   static constexpr uint32_t kVBytes = kShared ? 0 : kKBytes;
-  static constexpr uint32_t kPBytes = kSlice;
+  static constexpr uint32_t kPBytes = 3 * kTerm;
   static constexpr uint32_t kBytes = kQBytes + kKBytes + kVBytes + kPBytes + 1024;  // and the alignment
   // one CTA to an SM: a second would wait for the first one's tensor memory
   static constexpr uint32_t kSmem = kBytes < 120 * 1024 ? 120 * 1024 : kBytes;
-  static constexpr uint32_t kOCol = 2 * kRows;  // scores: two buffers, then the accumulators
-  static constexpr uint32_t kCols = kOCol + kBlocks * kRows <= 256 ? 256 : 512;
-  static_assert(kOCol + kBlocks * kRows <= 512, "");
+  static constexpr uint32_t kSCol = 2 * kRows;   // columns of a buffer of scores: both terms'
+  static constexpr uint32_t kOCol = 2 * kSCol;   // the accumulators
+  static constexpr uint32_t kCols = 512;
+  static_assert(kOCol + kSlices * kRows <= 512, "");
 };
 
 template <int kD, bool kShared>
 struct alignas(16) TcShared {
   using C = TcCfg<kD, kShared>;
-  uint64_t k_full[C::kStages][C::kSlices], k_free[C::kStages][C::kFree];
-  uint64_t v_full[C::kStages][C::kSlices], v_free[C::kStages];
+  uint64_t k_full[C::kStages], k_free[C::kStages], v_full[C::kStages], v_free[C::kStages];
   uint64_t s_full[2], s_free[2], p_full, pv_done, idle;
   alignas(16) float rf[C::kRows];  // read four at a time
   alignas(16) float neg_m[C::kRows];
@@ -77,6 +76,21 @@ struct alignas(16) TcShared {
   int any_nan;
   uint32_t tmem;
 };
+
+// Two fp16 values as the sum of three e5m2 pairs (16 bits each), each the nearest to what is left.
+__device__ __forceinline__ void three_terms(uint32_t h, uint32_t (&t)[3]) {
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    uint16_t b;
+    asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(b) : "r"(h));
+    t[i] = b;
+    if (i < 2) {
+      const uint32_t back = __byte_perm(b, 0, 0x1404);  // e5m2 is fp16's upper byte
+      const __half2 left = __hsub2(*reinterpret_cast<const __half2*>(&h), *reinterpret_cast<const __half2*>(&back));
+      h = *reinterpret_cast<const uint32_t*>(&left);
+    }
+  }
+}
 
 __device__ __forceinline__ bool group_any(int id, bool x) {
   uint32_t r;
@@ -116,17 +130,15 @@ __global__ __launch_bounds__((TcCfg<kD, kShared>::kThreads), 1) void q8_attn_tc_
   const uint32_t base = (smem_addr(raw) + 1023) & ~1023u;
   const uint32_t q_at = base, k_at = q_at + C::kQBytes, v_at = kShared ? k_at : k_at + C::kKBytes;
   const uint32_t p_at = k_at + C::kKBytes + C::kVBytes;
-  const bool conv = warp >= C::kSoftWarps && warp < C::kSoftWarps + C::kConvWarps;
+  const bool copy = warp >= C::kSoftWarps && warp < C::kSoftWarps + C::kCopyWarps;
   const bool soft = warp < C::kSoftWarps;
 
   if (warp == C::kWarps - 1) tmem_alloc(smem_addr(&sh.tmem), C::kCols);
   if (tid == 0) {
     for (int s = 0; s < C::kStages; ++s) {
-      for (int x = 0; x < C::kSlices; ++x) {
-        mbar_init(smem_addr(&sh.k_full[s][x]), C::kConvWarps);
-        mbar_init(smem_addr(&sh.v_full[s][x]), C::kConvWarps);
-      }
-      for (int x = 0; x < C::kFree; ++x) mbar_init(smem_addr(&sh.k_free[s][x]), 1);
+      mbar_init(smem_addr(&sh.k_full[s]), 32 * C::kCopyWarps);
+      mbar_init(smem_addr(&sh.v_full[s]), 32 * C::kCopyWarps);
+      mbar_init(smem_addr(&sh.k_free[s]), 1);
       mbar_init(smem_addr(&sh.v_free[s]), 1);
     }
     for (int s = 0; s < 2; ++s) {
@@ -174,13 +186,33 @@ __global__ __launch_bounds__((TcCfg<kD, kShared>::kThreads), 1) void q8_attn_tc_
       }
 #pragma unroll
       for (int s = 16; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, s));
-      const int ex = min(126, 14 - (static_cast<int>(__float_as_uint(m) >> 23) - 127));
+      const int ex = min(126, 7 - (static_cast<int>(__float_as_uint(m) >> 23) - 127));
       const float up = pow2f(ex);
+      // eight channels at a time; term t of the row is row n + 64 t of the operand
 #pragma unroll
-      for (int e = 0; e < kPer / 2; ++e) {
-        const uint32_t c = lane * kPer + 2 * e;
-        sts_u32(q_at + (c >> 6) * (kN * 128) + n * 128 + ((((c & 63) >> 3) ^ (n & 7)) << 4) + (c & 7) * 2,
-                pack_f16x2(bf16lo(x[e]) * up, bf16hi(x[e]) * up));
+      for (int e = 0; e < kPer; e += 8) {
+        float v[8];
+#pragma unroll
+        for (int z = 0; z < 8; ++z) v[z] = (z & 1 ? bf16hi(x[(e + z) / 2]) : bf16lo(x[(e + z) / 2])) * up;
+        const uint32_t c = lane * kPer + e;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const uint32_t w0 = q8_pack4(v[0], v[1], v[2], v[3]), w1 = q8_pack4(v[4], v[5], v[6], v[7]);
+          const uint32_t r = n + 64 * t;
+          const uint32_t at = q_at + (c >> 7) * kSlice8 + r * 128 + ((((c & 127) >> 4) ^ (r & 7)) << 4) + (c & 15);
+          asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(at), "r"(w0), "r"(w1) : "memory");
+          if (t == 0) {
+            const uint32_t w[2] = {w0, w1};
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              const float2 lo = f16x2_to_f32(q8_lo_f16x2(w[y])), hi = f16x2_to_f32(q8_hi_f16x2(w[y]));
+              v[4 * y] -= lo.x;
+              v[4 * y + 1] -= lo.y;
+              v[4 * y + 2] -= hi.x;
+              v[4 * y + 3] -= hi.y;
+            }
+          }
+        }
       }
       if (lane == 0) {
         sh.rf[n] = pow2f(-ex) * a.scale_log2;
@@ -195,8 +227,68 @@ __global__ __launch_bounds__((TcCfg<kD, kShared>::kThreads), 1) void q8_attn_tc_
     fence_async_smem();
     __syncthreads();
 
-    if (conv) {
-      convert_tiles<C, kShort>(a, item, sh, w, warp - C::kSoftWarps, h, table, n_tiles, tiles_before, vis_min, k_at, v_at);
+    if (copy) {
+      // ---- entries into the operands: lane l takes 16-byte chunk l (of 32 / kLanes entries at once) of entries
+      // cw, cw + 8, ...  A chunk arrives at its barrier when it has landed.
+      constexpr int kLanes = kD / 16, kPer = 32 / kLanes, kSteps = kEntries / (C::kCopyWarps * kPer);
+      const int cw = warp - C::kSoftWarps, cc = lane % kLanes;
+      const uint32_t entry0 = cw * kPer + lane / kLanes;  // entry of step i: entry0 + i * kCopyWarps * kPer
+      bool bad = false;
+      // lane r < 8 keeps the block number of run r (16 entries), asked for a tile ahead
+      auto ask = [&](uint32_t tile) {
+        return __ldg(table + (min(item.kv_begin + tile * kEntries + (lane & 7) * 16, last) >> t_shift));
+      };
+      int32_t runs = ask(0);
+      for (uint32_t j = 0; j < n_tiles; ++j) {
+        const uint32_t g = tiles_before + j, st = g % C::kStages, use = g / C::kStages;
+        const uint32_t e0 = item.kv_begin + j * kEntries;
+        const bool edge = e0 + kEntries > vis_min;
+        const int32_t now = runs;
+        runs = ask(j + 1);
+#pragma unroll 1
+        for (int side = 0; side < (kShared ? 1 : 2); ++side) {
+          const uint8_t* pool = side ? a.c.v : a.c.k;
+          const uint32_t to = (side ? v_at : k_at) + st * C::kTile;
+          uint64_t* full = side ? &sh.v_full[st] : &sh.k_full[st];
+          w.wait<kShort>(side ? &sh.v_free[st] : &sh.k_free[st], (use & 1) ^ 1);
+          auto place = [&](int i) {
+            const uint32_t t = entry0 + i * (C::kCopyWarps * kPer);
+            return to + (cc >> 3) * kSlice8 + t * 128 + (((cc & 7) ^ (t & 7)) << 4);
+          };
+#pragma unroll 4
+          for (int i = 0; i < kSteps; ++i) {
+            const uint32_t t = entry0 + i * (C::kCopyWarps * kPer), e = e0 + t;
+            const int32_t b = __shfl_sync(0xFFFFFFFFu, now, t >> 4);
+            const bool valid = static_cast<uint32_t>(b) < a.c.num_blocks, in = e < item.kv_end;
+            bad |= in && !valid;
+            const uint8_t* src =
+                pool + (((static_cast<size_t>(valid ? b : 0) * H + h) << t_shift) + (e & (T - 1))) * kD + cc * 16;
+            cp_async16(place(i), src, in && valid ? 16u : 0u);  // others read as zeros
+          }
+          if ((side || kShared) && edge) {
+            // some rows do not see some of these entries: their values' NaNs are taken out (see the split kernel)
+            cp_async_commit();
+            cp_async_wait<0>();
+#pragma unroll 1
+            for (int i = 0; i < kSteps; ++i) {
+              const uint32_t at = place(i), e = e0 + entry0 + i * (C::kCopyWarps * kPer);
+              const uint4 x = lds16(at);
+              if (q8_nan_bytes(x.x) | q8_nan_bytes(x.y) | q8_nan_bytes(x.z) | q8_nan_bytes(x.w)) {
+                const uint4 y = without_nans(x, e, kShared ? sh.nan : sh.nan + cc * 16, kShared ? 0 : 1, &sh.any_nan);
+                asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(y.x), "r"(y.y), "r"(y.z), "r"(y.w)
+                             : "memory");
+              }
+            }
+            mbar_arrive(smem_addr(full));
+          } else {
+            cp_async_arrive(smem_addr(full));
+          }
+        }
+      }
+      // none of these copies may land after the CTA is gone
+      cp_async_commit();
+      cp_async_wait<0>();
+      if (bad) status_or(a.d_status, CKV_STATUS_BAD_INDEX);
     } else if (soft) {
       // ---- softmax of 16 rows (columns of S^T); this thread's entry is its lane
       const int group = warp >> 2, quarter = warp & 3, bar = 1 + group;
@@ -231,9 +323,14 @@ __global__ __launch_bounds__((TcCfg<kD, kShared>::kThreads), 1) void q8_attn_tc_
         const bool unset = j == 0 || missed;
         missed = !exists && e0 + entry < item.kv_end;
         const F2 kf2 = f2_pack(kf, kf), lv2 = f2_pack(lv, lv), iv2 = f2_pack(iv, iv);
-        const uint32_t row = p_at + entry * 128;
         float x[16];  // the exponents t - m
-        tmem_load16(tmem + lanes + sb * kN + c0, x);
+        {
+          float y[16];
+          tmem_load16(tmem + lanes + sb * C::kSCol + c0, x);
+          tmem_load16(tmem + lanes + sb * C::kSCol + kN + c0, y);
+#pragma unroll
+          for (int c = 0; c < 16; ++c) x[c] += y[c];
+        }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_addr(&sh.s_free[sb]));
@@ -288,7 +385,7 @@ __global__ __launch_bounds__((TcCfg<kD, kShared>::kThreads), 1) void q8_attn_tc_
             w.wait<kShort>(&sh.pv_done, (g & 1) ^ 1);
             tc_fence_after();
 #pragma unroll 1
-            for (int b = 0; b < C::kBlocks; ++b) {
+            for (int b = 0; b < C::kSlices; ++b) {
               float o[16];
               const uint32_t at = tmem + lanes + C::kOCol + b * kN + c0;
               tmem_load16(at, o);
@@ -299,21 +396,29 @@ __global__ __launch_bounds__((TcCfg<kD, kShared>::kThreads), 1) void q8_attn_tc_
             tc_fence_before();
           }
         }
-        uint32_t p[8];
+        uint32_t p[3][4];
 #pragma unroll
-        for (int c = 0; c < 16; c += 2) {
-          const float w0 = ex2(x[c]), w1 = ex2(x[c + 1]);
-          const F2 sum = f2_fma(f2_pack(w0, w1), iv2, f2_pack(l[c], l[c + 1]));
-          f2_unpack(sum, l[c], l[c + 1]);
-          p[c / 2] = pack_f16x2(w0, w1);
+        for (int c = 0; c < 16; c += 4) {
+          uint32_t t[2][3];
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const int z = c + 2 * y;
+            const float w0 = ex2(x[z]), w1 = ex2(x[z + 1]);
+            const F2 sum = f2_fma(f2_pack(w0, w1), iv2, f2_pack(l[z], l[z + 1]));
+            f2_unpack(sum, l[z], l[z + 1]);
+            three_terms(pack_f16x2(w0, w1), t[y]);
+          }
+#pragma unroll
+          for (int i = 0; i < 3; ++i) p[i][c / 4] = __byte_perm(t[0][i], t[1][i], 0x5410);
         }
         w.wait<kShort>(&sh.pv_done, (g & 1) ^ 1);  // the second product is done with the tile before
+        // rows of 64 bytes: 16-byte chunk c of row r sits at chunk c ^ (r / 2 % 4)
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-          asm volatile(
-              "st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(row + (((group * 2 + i) ^ (entry & 7)) << 4)),
-              "r"(p[4 * i]), "r"(p[4 * i + 1]), "r"(p[4 * i + 2]), "r"(p[4 * i + 3])
-              : "memory");
+        for (int i = 0; i < 3; ++i)
+          asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(p_at + i * kTerm + entry * 64 +
+                                                                     ((group ^ ((entry >> 1) & 3)) << 4)),
+                       "r"(p[i][0]), "r"(p[i][1]), "r"(p[i][2]), "r"(p[i][3])
+                       : "memory");
         fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_addr(&sh.p_full));
@@ -348,7 +453,7 @@ __global__ __launch_bounds__((TcCfg<kD, kShared>::kThreads), 1) void q8_attn_tc_
       tc_fence_after();
       const int any_nan = sh.any_nan;
 #pragma unroll 1
-      for (int b = 0; b < C::kBlocks; ++b) {
+      for (int b = 0; b < C::kSlices; ++b) {
         const int d = b * 128 + entry;  // this lane's channel
         const int nan_at = any_nan ? sh.nan[kShared ? 0 : d] : 0x7FFFFFFF;
         float o[16];
@@ -377,24 +482,26 @@ __global__ __launch_bounds__((TcCfg<kD, kShared>::kThreads), 1) void q8_attn_tc_
       }
       tc_fence_before();
     } else {
-      // ---- the products: the warp waits together, one lane issues
+      // ---- the products: the warp waits together, one thread issues.  The entries were copied by other threads without
+      // a fence of theirs, so the fence between their stores and the tensor core's reads stands here.
       auto scores = [&](uint32_t g) {
         const uint32_t st = g % C::kStages, use = g / C::kStages, sb = g & 1;
         w.wait<kShort>(&sh.s_free[sb], ((g >> 1) & 1) ^ 1);
-#pragma unroll 1
-        for (int s = 0; s < C::kSlices; ++s) {
-          w.wait<kShort>(&sh.k_full[st][s], use & 1);
-          tc_fence_after();
-          if (w.live && elect_one()) {
-            const uint64_t ka = smem_operand(k_at + (st * C::kSlices + s) * kSlice, 0);
-            const uint64_t qb = smem_operand(q_at + s * (kN * 128), 0);
-#pragma unroll
-            for (int x = 0; x < 4; ++x)  // 16 channels, 32 bytes of a row
-              tc_mma(tmem + sb * kN, ka + 2 * x, qb + 2 * x, mma_shape(128, kN, false, false), s > 0 || x > 0);
-          }
-        }
+        w.wait<kShort>(&sh.k_full[st], use & 1);
+        fence_async_smem();
+        tc_fence_after();
         if (elect_one()) {
-          if (!kShared) tc_commit(smem_addr(&sh.k_free[st][0]));
+          if (w.live) {
+#pragma unroll
+            for (int s = 0; s < C::kSlices; ++s) {
+              const uint64_t ka = smem_operand(k_at + st * C::kTile + s * kSlice8, 0);
+              const uint64_t qb = smem_operand(q_at + s * kSlice8, 0);
+#pragma unroll
+              for (int x = 0; x < 4; ++x)  // 32 channels, 32 bytes of a row
+                tc_mma_8(tmem + sb * C::kSCol, ka + 2 * x, qb + 2 * x, mma_shape(128, 2 * kN, false, false), s > 0 || x > 0);
+            }
+          }
+          if (!kShared) tc_commit(smem_addr(&sh.k_free[st]));
           tc_commit(smem_addr(&sh.s_full[sb]));
         }
         __syncwarp();
@@ -402,40 +509,35 @@ __global__ __launch_bounds__((TcCfg<kD, kShared>::kThreads), 1) void q8_attn_tc_
       auto values = [&](uint32_t g, bool fresh) {
         const uint32_t st = g % C::kStages, use = g / C::kStages;
         w.wait<kShort>(&sh.p_full, g & 1);
-        for (int b = 0; b < C::kBlocks; ++b) {
-          if (!kShared) {
-            w.wait<kShort>(&sh.v_full[st][2 * b], use & 1);
-            w.wait<kShort>(&sh.v_full[st][2 * b + 1], use & 1);
-          }
-          tc_fence_after();
-          if (elect_one()) {
-            if (w.live) {
-              const uint64_t va = smem_operand(v_at + (st * C::kSlices + 2 * b) * kSlice, kSlice);
-              const uint64_t pb = smem_operand(p_at, 0);
-#pragma unroll
-              for (int x = 0; x < 8; ++x)  // 16 entries, 16 rows of 128 bytes
-                tc_mma(tmem + C::kOCol + b * kN, va + 128 * x, pb + 128 * x, mma_shape(128, kN, true, true),
-                       !fresh || x > 0);
-            }
-            if (kShared) tc_commit(smem_addr(&sh.k_free[st][b]));
-          }
-          __syncwarp();
-        }
+        if (!kShared) w.wait<kShort>(&sh.v_full[st], use & 1);
+        fence_async_smem();
+        tc_fence_after();
         if (elect_one()) {
-          if (!kShared) tc_commit(smem_addr(&sh.v_free[st]));
+          if (w.live) {
+#pragma unroll
+            for (int b = 0; b < C::kSlices; ++b) {
+              const uint64_t va = smem_operand(v_at + st * C::kTile + b * kSlice8, 0);
+#pragma unroll
+              for (int i = 0; i < 3; ++i) {
+                const uint64_t pb = smem_operand64(p_at + i * kTerm);
+#pragma unroll
+                for (int x = 0; x < 4; ++x)  // 32 entries: 32 rows of 128 and of 64 bytes
+                  tc_mma_8(tmem + C::kOCol + b * kN, va + 256 * x, pb + 128 * x,
+                           mma_shape(128, kN, true, true) | kBIsE5m2, !fresh || i > 0 || x > 0);
+              }
+            }
+          }
+          tc_commit(smem_addr(kShared ? &sh.k_free[st] : &sh.v_free[st]));
           tc_commit(smem_addr(&sh.pv_done));
         }
         __syncwarp();
       };
+      // the second product runs a tile behind the first
       for (uint32_t j = 0; j < n_tiles; ++j) {
-        const uint32_t g = tiles_before + j;
-        scores(g);
-        if (!C::kLag)
-          values(g, j == 0);
-        else if (j > 0)
-          values(g - 1, j == 1);
+        scores(tiles_before + j);
+        if (j > 0) values(tiles_before + j - 1, j == 1);
       }
-      if (C::kLag && n_tiles > 0) values(tiles_before + n_tiles - 1, n_tiles == 1);
+      if (n_tiles > 0) values(tiles_before + n_tiles - 1, n_tiles == 1);
     }
     tiles_before += n_tiles;
     __syncthreads();  // the next item's rows take the place of this one's
@@ -468,7 +570,7 @@ int launch_q8_attn_tc(const AttnArgs& a, cudaStream_t s) {
   const bool shared = a.c.v == nullptr;
   switch (a.c.head_dim) {
     case 256: return shared ? launch<256, true>(a, s) : launch<256, false>(a, s);
-    default: return shared ? launch<512, true>(a, s) : CKV_ERR_SIZE;
+    default: return shared ? launch<512, true>(a, s) : launch<512, false>(a, s);
   }
 }
 

@@ -48,6 +48,12 @@ __device__ __forceinline__ uint64_t smem_operand(uint32_t addr, uint32_t lbo) {
          (static_cast<uint64_t>(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
 }
 
+// The same for 64-byte rows in the 64-byte swizzle (16-byte chunk c of row r sits at chunk c ^ (r / 2 % 4)),
+// 8-row groups 512 bytes apart, of an operand whose rows run along its outer extent, at most 64 bytes of it.
+__device__ __forceinline__ uint64_t smem_operand64(uint32_t addr) {
+  return static_cast<uint64_t>((addr >> 4) & 0x3FFF) | (static_cast<uint64_t>(512 >> 4) << 32) | (1ull << 46) | (4ull << 61);
+}
+
 // Instruction descriptor: fp16 x fp16 -> fp32, M x N; a_outer / b_outer: that
 // operand's shared-memory rows run along M / N instead of K.
 __host__ __device__ constexpr uint32_t mma_shape(int m, int n, bool a_outer, bool b_outer) {
@@ -64,7 +70,18 @@ __device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint3
       : "memory");
 }
 
-// The same with A in tensor memory: fp16, two to a column, the accumulator's lanes.
+// 8-bit operands, 32 of K at a time: e4m3, or e5m2 for B with this bit in the shape.
+constexpr uint32_t kBIsE5m2 = 1u << 10;
+__device__ __forceinline__ void tc_mma_8(uint32_t d, uint64_t a, uint64_t b, uint32_t shape, bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.u32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(shape), "r"(accumulate ? 1u : 0u)
+      : "memory");
+}
+
+// fp16 with A in tensor memory: fp16, two to a column, the accumulator's lanes.
 __device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t shape, bool accumulate) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t"

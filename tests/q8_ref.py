@@ -91,9 +91,9 @@ def _scores(q, k, scale):
 
 
 def attn(k, ks, v, vs, q, rid, seq_lens, q_lens, kv_lens, table, ratio, scale):
-    """(out, lse, mag, top): mag is sum p |v| and top the largest sum |q| |k| scale of a score, the scales of the
-    output's error bound."""
-    out, mag = np.zeros(q.shape), np.zeros(q.shape)
+    """(out, lse, mag, big, flat), the last three the scales of the output's error bound: sum p |v|, and the largest
+    scale * sum |q| |k| and scale * max |q| * sum |k| of a score."""
+    out, mag, flat = np.zeros(q.shape), np.zeros(q.shape), np.zeros(q.shape[:2])
     lse, big = np.full(q.shape[:2], -np.inf), np.zeros(q.shape[:2])
     at = 0
     for b in range(len(rid)):
@@ -112,8 +112,10 @@ def attn(k, ks, v, vs, q, rid, seq_lens, q_lens, kv_lens, table, ratio, scale):
                 out[at] = np.einsum("hgs,hsd->hgd", p / tot, vv[:, :see]).reshape(q.shape[1:])
                 mag[at] = np.einsum("hgs,hsd->hgd", p / tot, np.abs(vv[:, :see])).reshape(q.shape[1:])
                 big[at] = _scores(np.abs(x), np.abs(kk[:, :see]), scale).max(-1).reshape(-1)
+                top_q = np.abs(x).max(-1, keepdims=True) * np.ones(x.shape[-1])
+                flat[at] = _scores(top_q, np.abs(kk[:, :see]), scale).max(-1).reshape(-1)
             at += 1
-    return out, lse, mag, big
+    return out, lse, mag, big, flat
 
 
 def weigh(k, ks, weights, q, lse, rid, seq_lens, q_lens, kv_lens, table, ratio, scale, decay):

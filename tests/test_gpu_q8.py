@@ -78,16 +78,23 @@ def status():
     return ckv.new_status(DEV)
 
 
-def attn_bounds(D, lens_max, out, lse, mag, big, vmax, out_bf16):
+def attn_bounds(D, lens_max, out, lse, mag, big, flat, vmax, out_bf16, eight_bit=False):
     """Worst cases: D products and lens_max weighted values summed in fp32 with truncated additions (2^-23 each), the
     exponent's argument a few roundings of its size (2^-22), the weights rounded to fp16 (2^-11), weights under
-    2^-31 of the largest dropped (of values up to twice vmax), bf16 output (2^-8)."""
-    eps = big * (D + 8) * 2.0 ** -23 + (big * 1.5 + 60) * 2.0 ** -22
+    2^-31 of the largest dropped (of values up to twice vmax), bf16 output (2^-8).  eight_bit: from 256 channels and
+    48 rows on the fp16 weights are three e5m2 terms (each leaves 2^-3 of what it is given: 2^-9), dropped under
+    2^-17 / 2^6 = 2^-23, and a query value is off by up to 2^-17 of its row's largest."""
+    eps = big * (D + 8) * 2.0 ** -23 + (big * 1.5 + 60) * 2.0 ** -22 + (flat * 2.0 ** -17 if eight_bit else 0)
     e = eps[..., None]
-    tol = mag * (2.0 ** -11 + 2 * e + (lens_max + 32) * 2.0 ** -23) + 2 * lens_max * 2.0 ** -31 * vmax
+    weight, drop = (2.0 ** -9 + 2.0 ** -10, 2.0 ** -23) if eight_bit else (2.0 ** -11, 2.0 ** -31)
+    tol = mag * (weight + 2 * e + (lens_max + 32) * 2.0 ** -23) + 2 * lens_max * drop * vmax
     tol = tol + np.abs(out) * (2.0 ** -8 if out_bf16 else 2.0 ** -23) + 1e-30
     with np.errstate(invalid="ignore"):
         return tol, eps + np.where(np.isfinite(lse), np.abs(lse) + 60, 0) * 2.0 ** -22
+
+
+def eight_bit(w, q_lens, heads):
+    return w.D >= 256 and int(np.sum(q_lens)) * (heads // w.H) >= 48 * len(q_lens)
 
 
 def run_attn(w, q, seq, q_lens, heads, ratio, out_dtype=torch.bfloat16, scale=None, lens=None, **kw):
@@ -106,10 +113,11 @@ def check_attn(w, q, seq, q_lens, heads, ratio, out_dtype=torch.bfloat16):
     cache, plan, out, lse, st = run_attn(w, q, seq, q_lens, heads, ratio, out_dtype)
     assert st == 0
     qn = q.float().numpy()
-    want, wl, mag, big = ref.attn(w.k, w.ks, w.v, w.vs, qn, w.rid, seq, q_lens, w.lens, w.table, ratio, scale)
+    want, wl, mag, big, flat = ref.attn(w.k, w.ks, w.v, w.vs, qn, w.rid, seq, q_lens, w.lens, w.table, ratio, scale)
     pool, sc = (w.k, w.ks) if w.v is None else (w.v, w.vs)
     vmax = max([np.abs(ref.entries(pool, sc, w.table[w.rid[b]], int(n))).max() for b, n in enumerate(w.lens) if n] + [0])
-    tol, ltol = attn_bounds(w.D, max(1, w.lens.max()), want, wl, mag, big, vmax, out_dtype == torch.bfloat16)
+    tol, ltol = attn_bounds(w.D, max(1, w.lens.max()), want, wl, mag, big, flat, vmax, out_dtype == torch.bfloat16,
+                            eight_bit(w, q_lens, heads))
     got, gl = out.float().cpu().numpy(), lse.cpu().numpy()
     assert np.isfinite(got).all()
     worst = np.abs(got - want) - tol
@@ -244,6 +252,9 @@ ATTN = [  # lens, q_lens, heads, H, D, T, latent, ratio
     ([260], [70], 16, 1, 512, 64, True, 4),
     ([257], [40], 16, 1, 512, 32, False, 1),
     ([129], [129], 128, 1, 128, 64, True, 1),
+    ([700, 150], [64, 30], 6, 2, 512, 32, False, 1),
+    ([1000], [1], 96, 1, 512, 128, True, 1),
+    ([390], [300], 4, 4, 128, 16, False, 1),
 ]
 
 
@@ -259,14 +270,15 @@ def test_attn(case):
     check_attn(w, q, _seq(lens, q_lens, ratio), q_lens, heads, ratio, torch.float32 if case % 2 else torch.bfloat16)
 
 
-@pytest.mark.parametrize("heads,H,D,latent", [(4, 1, 128, False), (8, 1, 512, True), (2, 2, 64, False), (64, 1, 128, True)])
+@pytest.mark.parametrize("heads,H,D,latent", [(4, 1, 128, False), (8, 1, 512, True), (2, 2, 64, False), (64, 1, 128, True),
+                                                (64, 1, 512, True), (70, 1, 256, False)])
 def test_attn_over_a_long_cache(heads, H, D, latent):
     """One row tile split over many CTAs, and joined."""
     w = World(7, [9001, 20], H, D, 128, latent)
     check_attn(w, w.queries([1, 1], heads), [9001, 20], [1, 1], heads, 1)
 
 
-@pytest.mark.parametrize("D,q_len", [(64, 1), (128, 1), (256, 1), (512, 1), (128, 70), (64, 70), (256, 70)])
+@pytest.mark.parametrize("D,q_len", [(64, 1), (128, 1), (256, 1), (512, 1), (128, 70), (64, 70), (256, 70), (512, 70)])
 def test_attn_with_scales_far_apart(D, q_len):
     """Blocks whose value scales differ by many powers of two, and scores that peak."""
     w = World(8, [400, 90], 1, D, 16, False, spread=9, k_spread=1)
@@ -280,7 +292,7 @@ def test_attn_of_large_and_tiny_queries():
     q[1] *= 2.0 ** -120
     q[2] = 0
     cache, plan, out, lse, st = run_attn(w, q, [100] * 3, [1] * 3, 2, 1, torch.float32)
-    want, wl, _, _ = ref.attn(w.k, w.ks, w.v, w.vs, q.double().numpy(), w.rid, [100] * 3, [1] * 3, w.lens, w.table, 1,
+    want, wl, _, _, _ = ref.attn(w.k, w.ks, w.v, w.vs, q.double().numpy(), w.rid, [100] * 3, [1] * 3, w.lens, w.table, 1,
                               1 / math.sqrt(128))
     got = out.cpu().numpy()
     # one entry takes all of the first query: its value, exactly; the others weigh all entries alike
@@ -298,7 +310,8 @@ def test_attn_of_equal_scores_is_the_mean():
     assert np.abs(lse.cpu().numpy() - math.log(333)).max() <= 2.0 ** -20
 
 
-@pytest.mark.parametrize("heads,D,latent", [(4, 128, False), (4, 64, False), (4, 256, True), (4, 512, True), (32, 128, False)])
+@pytest.mark.parametrize("heads,D,latent", [(4, 128, False), (4, 64, False), (4, 256, True), (4, 512, True), (32, 128, False),
+                                            (16, 64, True), (16, 256, False), (8, 512, True), (8, 512, False)])
 def test_nan_values_reach_only_queries_that_see_them(heads, D, latent):
     n, q_lens = 70, [9]
     w = World(11, [n], 1, D, 16, latent)
@@ -379,7 +392,7 @@ def test_attn_flags_bad_data():
     ckv.q8_attn(cache, q.to(DEV), plan, i32(table), 0.1, out=sent, status=st)
     torch.cuda.synchronize()
     assert int(st[0]) == ckv.STATUS_BAD_LENGTH | ckv.STATUS_BAD_INDEX
-    good, _, _, _ = ref.attn(w.k, w.ks, w.v, w.vs, q.float().numpy(), w.rid, [40] * 3, [1] * 3, w.lens, w.table, 1, 0.1)
+    good = ref.attn(w.k, w.ks, w.v, w.vs, q.float().numpy(), w.rid, [40] * 3, [1] * 3, w.lens, w.table, 1, 0.1)[0]
     got = sent.cpu().numpy()
     assert np.abs(got[0] - good[0]).max() <= 0.01   # an ordinary request
     assert (got[2] == 7.0).all()                    # a refused one is left as it was
@@ -389,6 +402,50 @@ def test_attn_flags_bad_data():
     p = np.exp(z - z.max(1, keepdims=True))
     want = (p / p.sum(1, keepdims=True)) @ ref.entries(w.v, w.vs, w.table[w.rid[1]], 40)[0]
     assert np.abs(got[1] - want).max() <= 0.01
+
+
+@pytest.mark.parametrize("D,latent", [(64, False), (128, True), (256, False), (512, True)])
+def test_missing_blocks_do_not_count_on_the_tensor_cores(D, latent):
+    """The first 128 entries and later ones in blocks that do not exist: the other entries' attention."""
+    n, heads = 300, 64
+    w = World(16, [n], 1, D, 16, latent)
+    q = w.queries([1], heads)
+    good = w.table.copy()
+    for j in [0, 1, 2, 3, 4, 5, 6, 7, 12]:
+        w.table[w.rid[0], j] = [-1, w.blocks, 1 << 30][j % 3]
+    _, _, out, lse, st = run_attn(w, q, [n], [1], heads, 1, torch.float32, scale=0.1)
+    assert st == ckv.STATUS_BAD_INDEX
+    k = ref.entries(w.k, w.ks, good[w.rid[0]], n)[0]
+    v = k if latent else ref.entries(w.v, w.vs, good[w.rid[0]], n)[0]
+    z = q[0].double().numpy() @ k.T * 0.1
+    z[:, :128] = z[:, 192:208] = -np.inf
+    p = np.exp(z - z.max(1, keepdims=True))
+    want = (p / p.sum(1, keepdims=True)) @ v
+    assert np.abs(out.cpu().numpy()[0] - want).max() <= 0.02
+    assert np.abs(lse.cpu().numpy()[0] - np.log(p.sum(1)) - z.max(1)).max() <= 0.002
+
+
+def test_scores_far_under_zero_on_the_tensor_cores():
+    """Every score near -400: the weights are relative to the row's own largest, wherever that is."""
+    for D, latent in [(128, False), (512, True)]:
+        w = World(17, [260], 1, D, 16, latent, spread=0)
+        k = np.zeros((w.blocks, 1, 16, D))
+        r = np.random.RandomState(3)
+        k[:] = r.standard_normal(k.shape)
+        k[..., 0] = -8.0
+        codes_ = ref.round8(k / 0.0625)
+        w.k = np.where(w.k == 0x7F, 0x7F, codes_).astype(np.uint8)
+        w.ks[:] = 0.0625
+        q = torch.zeros(1, 64, D)
+        q[:, :, 0] = 50.0
+        q[:, :, 1:] = torch.as_tensor(r.standard_normal((1, 64, D - 1)) * 0.1)
+        q = q.bfloat16()
+        _, _, out, lse, st = run_attn(w, q, [260], [1], 64, 1, torch.float32, scale=1.0)
+        assert st == 0
+        want, wl, mag, big, flat = ref.attn(w.k, w.ks, w.v, w.vs, q.double().numpy(), w.rid, [260], [1], w.lens, w.table, 1, 1.0)
+        tol, ltol = attn_bounds(D, 260, want, wl, mag, big, flat, 40.0, False, D >= 256)
+        assert (wl < -380).all() and (np.abs(lse.cpu().numpy() - wl) <= ltol).all()
+        assert (np.abs(out.cpu().numpy() - want) <= tol).all()
 
 
 def test_attn_refuses_a_plan_of_another_shape():
@@ -442,7 +499,7 @@ def test_offsets_past_32_bits():
     wk, ws = np.zeros_like(sk), np.ones_like(ss)
     ref.store(wk, ws, x.float().numpy(), ref.store_plan([0], [n], [n], tab, T))
     assert ref.same_codes(sk[:4], wk[:4]) and np.array_equal(ss[:4], ws[:4])
-    want, _, mag, _ = ref.attn(wk, ws, None, None, q.float().numpy(), [0], [n], [1], [n], tab, 1, 0.05)
+    want, _, mag, _, _ = ref.attn(wk, ws, None, None, q.float().numpy(), [0], [n], [1], [n], tab, 1, 0.05)
     assert (np.abs(out.cpu().numpy() - want) <= mag * 2.0 ** -10 + 1e-6).all()
     w4 = np.stack([weights[b].cpu().numpy() for b in small])
     assert abs(w4[:4].sum() - 16) < 1e-3
@@ -621,8 +678,8 @@ def test_a_request_s_life():
         q = torch.as_tensor(r.standard_normal((n, heads, hd)) * 1.5).bfloat16()
         plan = ckv.plan_q8_attn(cache, heads, ratio, i64(rid), i64(seq), i64(ext), i64(kv), n, status=st)
         o, lse = ckv.q8_attn(cache, q.to(DEV), plan, i32(tab), scale, status=st)
-        want, wl, mag, big = ref.attn(k, ks, None, None, q.float().numpy(), rid, seq, ext, kv, tab, ratio, scale)
-        tol, _ = attn_bounds(hd, 200, want, wl, mag, big, 448 * ks.max(), True)
+        want, wl, mag, big, flat = ref.attn(k, ks, None, None, q.float().numpy(), rid, seq, ext, kv, tab, ratio, scale)
+        tol, _ = attn_bounds(hd, 200, want, wl, mag, big, flat, 448 * ks.max(), True)
         assert (np.abs(o.float().cpu().numpy() - want) <= tol).all()
         ckv.q8_weigh(cache, q.to(DEV), lse, weights, ratio, i64(rid), i64(seq), i64(ext), i64(kv), i32(tab), scale,
                      status=st)
@@ -714,8 +771,8 @@ def test_captured_step_replays_with_new_lengths_and_beside_another():
             ref.store(w.k, w.ks, k.float().numpy(), recs)
             ref.store(w.v, w.vs, v.float().numpy(), recs)
             assert ref.same_codes(codes(s.cache.k), w.k) and ref.same_codes(codes(s.cache.v), w.v)
-            want, wl, mag, big = ref.attn(w.k, w.ks, w.v, w.vs, q.float().numpy(), w.rid, kv, [1, 1], kv, w.table, 1, scale)
-            tol, ltol = attn_bounds(D, 200, want, wl, mag, big, 32.0, True)
+            want, wl, mag, big, flat = ref.attn(w.k, w.ks, w.v, w.vs, q.float().numpy(), w.rid, kv, [1, 1], kv, w.table, 1, scale)
+            tol, ltol = attn_bounds(D, 200, want, wl, mag, big, flat, 32.0, True)
             assert (np.abs(s.out.float().cpu().numpy() - want) <= tol).all()
             assert (np.abs(s.lse.cpu().numpy() - wl) <= ltol).all()
     for s in (a, b):
