@@ -20,8 +20,9 @@
 // The weights go through shared memory as they stand: an entry's row of 64 of them is the
 // swizzled row that the second product reads.
 //
-// Roles.  Eight warps copy entries into the operands' swizzled layout, a stage ahead; one
-// thread issues the products; groups of four warps take 16 rows each through the softmax.
+// Roles.  Eight warps copy entries into the operands' swizzled layout, 128 channels at a time, as
+// the second product hands them back; one thread issues the products; groups of four warps
+// take 16 rows each through the softmax.
 //
 // Bound.  512 channels: a tile is 64 KB from memory, 2.8 k cycles of an SM's share of it;
 // shared memory feeds the products 128 KB and 288 KB, 3.3 k cycles.
@@ -41,6 +42,7 @@ struct TcCfg {
   static constexpr int kRows = 64;
   static constexpr int kSlices = kD / 128;  // also the accumulators, of 128 channels each
   static constexpr int kStages = kD == 512 && !kShared ? 1 : 2;
+  static constexpr int kFree = kShared ? kSlices : 1;  // barriers that hand a K stage back
   static constexpr int kGroups = kRows / 16;  // softmax groups of four warps
   static constexpr int kSoftWarps = 4 * kGroups;
   static constexpr int kCopyWarps = 8;
@@ -63,8 +65,9 @@ struct TcCfg {
 template <int kD, bool kShared>
 struct alignas(16) TcShared {
   using C = TcCfg<kD, kShared>;
-  uint64_t k_full[C::kStages], k_free[C::kStages], v_full[C::kStages], v_free[C::kStages];
-  uint64_t s_full[2], s_free[2], p_full, pv_done, idle;
+  uint64_t k_full[C::kStages][C::kSlices], k_free[C::kStages][C::kFree];
+  uint64_t v_full[C::kStages][C::kSlices], v_free[C::kStages];
+  uint64_t s_full[2], s_free[2], q_full, p_full, pv_done, idle;
   alignas(16) float rf[C::kRows];  // read four at a time
   alignas(16) float neg_m[C::kRows];
   float fac[C::kRows], up[C::kRows];
@@ -136,15 +139,18 @@ __global__ __launch_bounds__((TcCfg<kD, kShared>::kThreads), 1) void q8_attn_tc_
   if (warp == C::kWarps - 1) tmem_alloc(smem_addr(&sh.tmem), C::kCols);
   if (tid == 0) {
     for (int s = 0; s < C::kStages; ++s) {
-      mbar_init(smem_addr(&sh.k_full[s]), 32 * C::kCopyWarps);
-      mbar_init(smem_addr(&sh.v_full[s]), 32 * C::kCopyWarps);
-      mbar_init(smem_addr(&sh.k_free[s]), 1);
+      for (int x = 0; x < C::kSlices; ++x) {
+        mbar_init(smem_addr(&sh.k_full[s][x]), 32 * C::kCopyWarps);
+        mbar_init(smem_addr(&sh.v_full[s][x]), 32 * C::kCopyWarps);
+      }
+      for (int x = 0; x < C::kFree; ++x) mbar_init(smem_addr(&sh.k_free[s][x]), 1);
       mbar_init(smem_addr(&sh.v_free[s]), 1);
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(smem_addr(&sh.s_full[s]), 1);
       mbar_init(smem_addr(&sh.s_free[s]), C::kSoftWarps);
     }
+    mbar_init(smem_addr(&sh.q_full), C::kSoftWarps);
     mbar_init(smem_addr(&sh.p_full), C::kSoftWarps);
     mbar_init(smem_addr(&sh.pv_done), 1);
     mbar_init(smem_addr(&sh.idle), 1);
@@ -156,6 +162,7 @@ __global__ __launch_bounds__((TcCfg<kD, kShared>::kThreads), 1) void q8_attn_tc_
   const uint32_t tmem = sh.tmem;
   Waiter w{static_cast<long long>(a.wait_ns) * 2, true};
   uint32_t tiles_before = 0;  // tiles of earlier items: the barriers' phases go on
+  uint32_t items_before = 0;
 
   for (uint32_t it = item0; it < item1; ++it) {
     const Q8Item item = items[it];
@@ -170,70 +177,16 @@ __global__ __launch_bounds__((TcCfg<kD, kShared>::kThreads), 1) void q8_attn_tc_
     const uint32_t last = item.kv_end > 0 ? item.kv_end - 1 : 0;
     const uint32_t vis_min = min(item.kv_end, static_cast<uint32_t>(q8_visible(item.kv_len, item.q_len - 1 - item.row0 / G,
                                                                              item.phase, a.ratio)));
-    // ---- the rows: query operand, scaling, visibility
-    for (int n = warp; n < kN; n += C::kWarps) {
-      constexpr int kPer = kD / 32;  // consecutive channels of a lane
-      const bool in = static_cast<uint32_t>(n) < rows;
-      const uint32_t rho = item.row0 + (in ? n : 0), i = rho / G, hg = rho % G;
-      const size_t row = static_cast<size_t>(item.q_start + i) * a.n_heads + h * G + hg;
-      const uint32_t* p = reinterpret_cast<const uint32_t*>(a.q + row * kD + lane * kPer);
-      uint32_t x[kPer / 2];
-      float m = 0.0f;
-#pragma unroll
-      for (int e = 0; e < kPer / 2; ++e) {
-        x[e] = in ? __ldg(p + e) : 0u;
-        m = fmaxf(m, fmaxf(fabsf(bf16lo(x[e])), fabsf(bf16hi(x[e]))));
-      }
-#pragma unroll
-      for (int s = 16; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, s));
-      const int ex = min(126, 7 - (static_cast<int>(__float_as_uint(m) >> 23) - 127));
-      const float up = pow2f(ex);
-      // eight channels at a time; term t of the row is row n + 64 t of the operand
-#pragma unroll
-      for (int e = 0; e < kPer; e += 8) {
-        float v[8];
-#pragma unroll
-        for (int z = 0; z < 8; ++z) v[z] = (z & 1 ? bf16hi(x[(e + z) / 2]) : bf16lo(x[(e + z) / 2])) * up;
-        const uint32_t c = lane * kPer + e;
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          const uint32_t w0 = q8_pack4(v[0], v[1], v[2], v[3]), w1 = q8_pack4(v[4], v[5], v[6], v[7]);
-          const uint32_t r = n + 64 * t;
-          const uint32_t at = q_at + (c >> 7) * kSlice8 + r * 128 + ((((c & 127) >> 4) ^ (r & 7)) << 4) + (c & 15);
-          asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(at), "r"(w0), "r"(w1) : "memory");
-          if (t == 0) {
-            const uint32_t w[2] = {w0, w1};
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              const float2 lo = f16x2_to_f32(q8_lo_f16x2(w[y])), hi = f16x2_to_f32(q8_hi_f16x2(w[y]));
-              v[4 * y] -= lo.x;
-              v[4 * y + 1] -= lo.y;
-              v[4 * y + 2] -= hi.x;
-              v[4 * y + 3] -= hi.y;
-            }
-          }
-        }
-      }
-      if (lane == 0) {
-        sh.rf[n] = pow2f(-ex) * a.scale_log2;
-        sh.neg_m[n] = 0.0f;
-        sh.set[n] = 0;
-        sh.vis[n] = in ? static_cast<int>(q8_visible(item.kv_len, item.q_len - 1 - i, item.phase, a.ratio)) : 0x7FFFFFFF;
-        sh.out_row[n] = row;
-      }
-    }
-    for (int c = tid; c < (kShared ? 1 : kD); c += C::kThreads) sh.nan[c] = 0x7FFFFFFF;
-    if (tid == 0) sh.any_nan = 0;
-    fence_async_smem();
-    __syncthreads();
-
     if (copy) {
-      // ---- entries into the operands: lane l takes 16-byte chunk l (of 32 / kLanes entries at once) of entries
-      // cw, cw + 8, ...  A chunk arrives at its barrier when it has landed.
-      constexpr int kLanes = kD / 16, kPer = 32 / kLanes, kSteps = kEntries / (C::kCopyWarps * kPer);
-      const int cw = warp - C::kSoftWarps, cc = lane % kLanes;
-      const uint32_t entry0 = cw * kPer + lane / kLanes;  // entry of step i: entry0 + i * kCopyWarps * kPer
+      // ---- entries into the operands, 128 channels (a slice) at a time: lane l takes 16-byte chunk l % 8 of four entries
+      // at once.  A chunk arrives at its barrier when it has landed.
+      constexpr int kSteps = kEntries / (C::kCopyWarps * 4);
+      const int cw = warp - C::kSoftWarps, cc = lane & 7;
+      const uint32_t entry0 = cw * 4 + (lane >> 3);  // entry of step i: entry0 + 32 i
       bool bad = false;
+      for (int c = tid - 32 * C::kSoftWarps; c < (kShared ? 1 : kD); c += 32 * C::kCopyWarps) sh.nan[c] = 0x7FFFFFFF;
+      if (cw == 0 && lane == 0) sh.any_nan = 0;
+      asm volatile("bar.sync 15, 256;" ::: "memory");
       // lane r < 8 keeps the block number of run r (16 entries), asked for a tile ahead
       auto ask = [&](uint32_t tile) {
         return __ldg(table + (min(item.kv_begin + tile * kEntries + (lane & 7) * 16, last) >> t_shift));
@@ -245,36 +198,43 @@ __global__ __launch_bounds__((TcCfg<kD, kShared>::kThreads), 1) void q8_attn_tc_
         const bool edge = e0 + kEntries > vis_min;
         const int32_t now = runs;
         runs = ask(j + 1);
+        size_t off[kSteps];
+        uint32_t in = 0;  // bit i: step i's entry exists
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) {
+          const uint32_t t = entry0 + 32 * i, e = e0 + t;
+          const int32_t b = __shfl_sync(0xFFFFFFFFu, now, t >> 4);
+          const bool valid = static_cast<uint32_t>(b) < a.c.num_blocks;
+          off[i] = (((static_cast<size_t>(valid ? b : 0) * H + h) << t_shift) + (e & (T - 1))) * kD + cc * 16;
+          in |= (valid && e < item.kv_end ? 1u : 0u) << i;
+          bad |= !valid && e < item.kv_end;
+        }
+        const uint32_t put = entry0 * 128 + ((cc ^ (entry0 & 7)) << 4);  // 32 entries on, the swizzle is the same
 #pragma unroll 1
-        for (int side = 0; side < (kShared ? 1 : 2); ++side) {
-          const uint8_t* pool = side ? a.c.v : a.c.k;
-          const uint32_t to = (side ? v_at : k_at) + st * C::kTile;
-          uint64_t* full = side ? &sh.v_full[st] : &sh.k_full[st];
-          w.wait<kShort>(side ? &sh.v_free[st] : &sh.k_free[st], (use & 1) ^ 1);
-          auto place = [&](int i) {
-            const uint32_t t = entry0 + i * (C::kCopyWarps * kPer);
-            return to + (cc >> 3) * kSlice8 + t * 128 + (((cc & 7) ^ (t & 7)) << 4);
-          };
-#pragma unroll 4
-          for (int i = 0; i < kSteps; ++i) {
-            const uint32_t t = entry0 + i * (C::kCopyWarps * kPer), e = e0 + t;
-            const int32_t b = __shfl_sync(0xFFFFFFFFu, now, t >> 4);
-            const bool valid = static_cast<uint32_t>(b) < a.c.num_blocks, in = e < item.kv_end;
-            bad |= in && !valid;
-            const uint8_t* src =
-                pool + (((static_cast<size_t>(valid ? b : 0) * H + h) << t_shift) + (e & (T - 1))) * kD + cc * 16;
-            cp_async16(place(i), src, in && valid ? 16u : 0u);  // others read as zeros
+        for (int u = 0; u < C::kSlices * (kShared ? 1 : 2); ++u) {
+          const bool side = u >= C::kSlices;
+          const int s = side ? u - C::kSlices : u;
+          const uint8_t* pool = (side ? a.c.v : a.c.k) + s * 128;
+          const uint32_t to = (side ? v_at : k_at) + st * C::kTile + s * kSlice8 + put;
+          uint64_t* full = side ? &sh.v_full[st][s] : &sh.k_full[st][s];
+          if (side) {
+            if (s == 0) w.wait<kShort>(&sh.v_free[st], (use & 1) ^ 1);
+          } else if (kShared || s == 0) {
+            w.wait<kShort>(&sh.k_free[st][kShared ? s : 0], (use & 1) ^ 1);
           }
+#pragma unroll
+          for (int i = 0; i < kSteps; ++i) cp_async16(to + i * 4096, pool + off[i], in >> i & 1 ? 16u : 0u);  // others: zeros
           if ((side || kShared) && edge) {
             // some rows do not see some of these entries: their values' NaNs are taken out (see the split kernel)
             cp_async_commit();
             cp_async_wait<0>();
 #pragma unroll 1
             for (int i = 0; i < kSteps; ++i) {
-              const uint32_t at = place(i), e = e0 + entry0 + i * (C::kCopyWarps * kPer);
+              const uint32_t at = to + i * 4096;
               const uint4 x = lds16(at);
               if (q8_nan_bytes(x.x) | q8_nan_bytes(x.y) | q8_nan_bytes(x.z) | q8_nan_bytes(x.w)) {
-                const uint4 y = without_nans(x, e, kShared ? sh.nan : sh.nan + cc * 16, kShared ? 0 : 1, &sh.any_nan);
+                const uint4 y = without_nans(x, e0 + entry0 + 32 * i, kShared ? sh.nan : sh.nan + s * 128 + cc * 16,
+                                             kShared ? 0 : 1, &sh.any_nan);
                 asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(y.x), "r"(y.y), "r"(y.z), "r"(y.w)
                              : "memory");
               }
@@ -290,6 +250,80 @@ __global__ __launch_bounds__((TcCfg<kD, kShared>::kThreads), 1) void q8_attn_tc_
       cp_async_wait<0>();
       if (bad) status_or(a.d_status, CKV_STATUS_BAD_INDEX);
     } else if (soft) {
+      // ---- the rows: query operand, scaling, visibility; a warp takes four rows, and loads two at a time
+      constexpr int kPer = kD / 32;  // consecutive channels of a lane
+#pragma unroll 1
+      for (int n0 = warp; n0 < kN; n0 += 2 * C::kSoftWarps) {
+        uint4 x[2][kPer / 8];
+        size_t row[2];
+        uint32_t query[2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const uint32_t n = n0 + r * C::kSoftWarps;
+          const bool in = n < rows;
+          const uint32_t rho = item.row0 + (in ? n : 0), hg = rho % G;
+          query[r] = rho / G;
+          row[r] = static_cast<size_t>(item.q_start + query[r]) * a.n_heads + h * G + hg;
+#pragma unroll
+          for (int e = 0; e < kPer / 8; ++e)
+            x[r][e] = in ? ld_cached16(a.q + row[r] * kD + lane * kPer + 8 * e) : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const int n = n0 + r * C::kSoftWarps;
+          float m = 0.0f;
+#pragma unroll
+          for (int e = 0; e < kPer / 8; ++e) {
+#pragma unroll
+            for (int z = 0; z < 8; ++z) m = fmaxf(m, fabsf(unpack<__nv_bfloat16>(x[r][e], z)));
+          }
+#pragma unroll
+          for (int s = 16; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, s));
+          const int ex = min(126, 7 - (static_cast<int>(__float_as_uint(m) >> 23) - 127));
+          const float up = pow2f(ex);
+          // eight channels at a time; term t of the row is row n + 64 t of the operand
+#pragma unroll
+          for (int e = 0; e < kPer / 8; ++e) {
+            float v[8];
+#pragma unroll
+            for (int z = 0; z < 8; ++z) v[z] = unpack<__nv_bfloat16>(x[r][e], z) * up;
+            const uint32_t c = lane * kPer + 8 * e;
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              const uint32_t y[2] = {q8_pack4(v[0], v[1], v[2], v[3]), q8_pack4(v[4], v[5], v[6], v[7])};
+              const uint32_t to = n + 64 * t;
+              asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(q_at + (c >> 7) * kSlice8 + to * 128 +
+                                                                   ((((c & 127) >> 4) ^ (to & 7)) << 4) + (c & 15)),
+                           "r"(y[0]), "r"(y[1])
+                           : "memory");
+              if (t == 0) {
+#pragma unroll
+                for (int z = 0; z < 2; ++z) {
+                  const float2 lo = f16x2_to_f32(q8_lo_f16x2(y[z])), hi = f16x2_to_f32(q8_hi_f16x2(y[z]));
+                  v[4 * z] -= lo.x;
+                  v[4 * z + 1] -= lo.y;
+                  v[4 * z + 2] -= hi.x;
+                  v[4 * z + 3] -= hi.y;
+                }
+              }
+            }
+          }
+          if (lane == 0) {
+            sh.rf[n] = pow2f(-ex) * a.scale_log2;
+            sh.neg_m[n] = 0.0f;
+            sh.set[n] = 0;
+            sh.vis[n] = static_cast<uint32_t>(n) < rows
+                            ? static_cast<int>(q8_visible(item.kv_len, item.q_len - 1 - query[r], item.phase, a.ratio))
+                            : 0x7FFFFFFF;
+            sh.out_row[n] = row[r];
+          }
+        }
+      }
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_addr(&sh.q_full));
+      asm volatile("bar.sync 14, 512;" ::: "memory");  // every group reads rows that other warps prepared
+
       // ---- softmax of 16 rows (columns of S^T); this thread's entry is its lane
       const int group = warp >> 2, quarter = warp & 3, bar = 1 + group;
       const int c0 = group * 16, entry = quarter * 32 + lane;
@@ -487,21 +521,22 @@ __global__ __launch_bounds__((TcCfg<kD, kShared>::kThreads), 1) void q8_attn_tc_
       auto scores = [&](uint32_t g) {
         const uint32_t st = g % C::kStages, use = g / C::kStages, sb = g & 1;
         w.wait<kShort>(&sh.s_free[sb], ((g >> 1) & 1) ^ 1);
-        w.wait<kShort>(&sh.k_full[st], use & 1);
-        fence_async_smem();
-        tc_fence_after();
-        if (elect_one()) {
-          if (w.live) {
+#pragma unroll 1
+        for (int s = 0; s < C::kSlices; ++s) {
+          w.wait<kShort>(&sh.k_full[st][s], use & 1);
+          fence_async_smem();
+          tc_fence_after();
+          if (w.live && elect_one()) {
+            const uint64_t ka = smem_operand(k_at + st * C::kTile + s * kSlice8, 0);
+            const uint64_t qb = smem_operand(q_at + s * kSlice8, 0);
 #pragma unroll
-            for (int s = 0; s < C::kSlices; ++s) {
-              const uint64_t ka = smem_operand(k_at + st * C::kTile + s * kSlice8, 0);
-              const uint64_t qb = smem_operand(q_at + s * kSlice8, 0);
-#pragma unroll
-              for (int x = 0; x < 4; ++x)  // 32 channels, 32 bytes of a row
-                tc_mma_8(tmem + sb * C::kSCol, ka + 2 * x, qb + 2 * x, mma_shape(128, 2 * kN, false, false), s > 0 || x > 0);
-            }
+            for (int x = 0; x < 4; ++x)  // 32 channels, 32 bytes of a row
+              tc_mma_8(tmem + sb * C::kSCol, ka + 2 * x, qb + 2 * x, mma_shape(128, 2 * kN, false, false), s > 0 || x > 0);
           }
-          if (!kShared) tc_commit(smem_addr(&sh.k_free[st]));
+          __syncwarp();
+        }
+        if (elect_one()) {
+          if (!kShared) tc_commit(smem_addr(&sh.k_free[st][0]));
           tc_commit(smem_addr(&sh.s_full[sb]));
         }
         __syncwarp();
@@ -509,13 +544,15 @@ __global__ __launch_bounds__((TcCfg<kD, kShared>::kThreads), 1) void q8_attn_tc_
       auto values = [&](uint32_t g, bool fresh) {
         const uint32_t st = g % C::kStages, use = g / C::kStages;
         w.wait<kShort>(&sh.p_full, g & 1);
-        if (!kShared) w.wait<kShort>(&sh.v_full[st], use & 1);
+        if (!kShared) {
+          for (int s = 0; s < C::kSlices; ++s) w.wait<kShort>(&sh.v_full[st][s], use & 1);
+        }
         fence_async_smem();
         tc_fence_after();
         if (elect_one()) {
-          if (w.live) {
 #pragma unroll
-            for (int b = 0; b < C::kSlices; ++b) {
+          for (int b = 0; b < C::kSlices; ++b) {
+            if (w.live) {
               const uint64_t va = smem_operand(v_at + st * C::kTile + b * kSlice8, 0);
 #pragma unroll
               for (int i = 0; i < 3; ++i) {
@@ -526,12 +563,14 @@ __global__ __launch_bounds__((TcCfg<kD, kShared>::kThreads), 1) void q8_attn_tc_
                            mma_shape(128, kN, true, true) | kBIsE5m2, !fresh || i > 0 || x > 0);
               }
             }
+            if (kShared) tc_commit(smem_addr(&sh.k_free[st][b]));
           }
-          tc_commit(smem_addr(kShared ? &sh.k_free[st] : &sh.v_free[st]));
+          if (!kShared) tc_commit(smem_addr(&sh.v_free[st]));
           tc_commit(smem_addr(&sh.pv_done));
         }
         __syncwarp();
       };
+      w.wait<kShort>(&sh.q_full, items_before & 1);
       // the second product runs a tile behind the first
       for (uint32_t j = 0; j < n_tiles; ++j) {
         scores(tiles_before + j);
@@ -540,6 +579,7 @@ __global__ __launch_bounds__((TcCfg<kD, kShared>::kThreads), 1) void q8_attn_tc_
       if (n_tiles > 0) values(tiles_before + n_tiles - 1, n_tiles == 1);
     }
     tiles_before += n_tiles;
+    ++items_before;
     __syncthreads();  // the next item's rows take the place of this one's
     tc_fence_after();
   }
