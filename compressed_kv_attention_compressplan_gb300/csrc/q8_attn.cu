@@ -231,12 +231,13 @@ int q8_attn_geom(const Q8Cache& c, uint32_t batch, uint32_t num_q, uint32_t n_he
   if (g->tc) {
     g->rows = c.head_dim <= 128 ? 256 : 64;
     g->ctas = std::max<uint32_t>(1, static_cast<uint32_t>(sm_count()) / c.heads);
-    g->start_cost = g->grain = g->round = 128;
+    g->grain = g->round = 128;
+    g->start_cost = c.head_dim >= 256 ? 384 : 256;  // what starting a tile takes, in entries' time
     g->min_quota = 256;
   } else {
     g->rows = 16;
     g->ctas = std::max<uint32_t>(1, static_cast<uint32_t>(sm_count()) * per_sm_of(c.head_dim) / c.heads);
-    g->start_cost = 32;
+    g->start_cost = 128;
     g->grain = 16;
     g->round = 64;
     g->min_quota = 128;

@@ -4,10 +4,11 @@
 //
 // A CTA takes 256 rows as two tiles of 128, M of both products:
 //     S [128 rows x 128 entries] = Q K8^T,   O [128 rows x channels] += W V8.
-// A thread owns a row, so its reference, its sum and its scaling are registers, a
-// tile's entries come in eight runs of 16 that share their scales, and nothing
-// crosses lanes.  W takes the place of S in tensor memory, as the A operand of the
-// second product.  The two row tiles take turns: while one's softmax runs, the
+// Two threads own a row, one for each half of a tile's entries, so a row's reference,
+// sum and scaling are registers, a tile's entries come in eight runs of 16 that share
+// their scales, and all that crosses threads is one vote a tile between two warps (and
+// the two maxima when a reference has to rise).  W takes the place of S in tensor memory,
+// as the A operand of the second product.  The two row tiles take turns: while one's softmax runs, the
 // other's products do.  K and V are turned into fp16 once for both.
 //
 // Bound.  Per tile of 128 entries and 256 rows at 128 channels: products 2.0 k
@@ -29,7 +30,7 @@ struct RowsCfg {
   static constexpr int kSlices = kD / 64;
   static constexpr int kStages = 2;
   static constexpr int kFree = 1;
-  static constexpr int kSoftWarps = 8;
+  static constexpr int kSoftWarps = 16;  // of each row tile: four for the first 64 entries, four for the others
   static constexpr int kConvWarps = 8;
   static constexpr int kWarps = kSoftWarps + kConvWarps + 1;
   static constexpr int kThreads = 32 * kWarps;
@@ -57,10 +58,26 @@ struct alignas(16) RowsShared {
   alignas(16) float lv[4][8];
   alignas(16) float iv[4][8];
   float rf[C::kRows];
+  float both[2][C::kRows];  // what the two owners of a row tell each other
   int nan[kShared ? 1 : kD];
   int any_nan;
   uint32_t tmem;
 };
+
+// A vote and a barrier of the two warps that share 32 rows.
+__device__ __forceinline__ bool pair_any(int id, bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %2, 0;\n\t"
+      "bar.red.or.pred q, %1, 64, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(id), "r"(x ? 1u : 0u)
+      : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ void pair_sync(int id) { asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory"); }
 
 template <int kD, bool kShared, bool kShort>
 __global__ __launch_bounds__((RowsCfg<kD, kShared>::kThreads), 1) void q8_attn_rows_kernel(const AttnArgs a) {
@@ -161,11 +178,12 @@ __global__ __launch_bounds__((RowsCfg<kD, kShared>::kThreads), 1) void q8_attn_r
     if (conv) {
       convert_tiles<C, kShort>(a, item, sh, w, warp - C::kSoftWarps, h, table, n_tiles, tiles_before, vis_min, k_at, v_at);
     } else if (soft) {
-      const int rt = warp >> 2;  // row tile
+      const int rt = warp >> 3, half = warp >> 2 & 1, quarter = warp & 3, pair = 1 + rt * 4 + quarter;
       if (rt < tiles) {
-        const uint32_t n = warp * 32 + lane;  // row of the item
-        const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-        const uint32_t s_at = tmem + lanes + rt * 128, o_at = tmem + lanes + C::kOCol + rt * kD;
+        const uint32_t n = rt * 128 + quarter * 32 + lane;  // row of the item
+        const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
+        // this half's scores; its weights take the first 32 of these columns
+        const uint32_t s_at = tmem + lanes + rt * 128 + half * 64, o_at = tmem + lanes + C::kOCol + rt * kD;
         const bool in = n < rows;
         const uint32_t rho = item.row0 + (in ? n : 0), i = rho / G, hg = rho % G;
         const int64_t see = q8_visible(item.kv_len, item.q_len - 1 - i, item.phase, a.ratio);
@@ -179,13 +197,16 @@ __global__ __launch_bounds__((RowsCfg<kD, kShared>::kThreads), 1) void q8_attn_r
           const uint32_t g = tiles_before + j, slot = g & 3;
           const uint32_t e0 = item.kv_begin + j * kEntries;
           const bool edge = e0 + kEntries > vis_min;
-          const int hidden = static_cast<int>(vis) - static_cast<int>(e0);  // entries of the tile from here on
+          const int hidden = static_cast<int>(vis) - static_cast<int>(e0 + half * 64);  // this half's entries from here on
+          const float* f_at = sh.f[slot] + half * 4;
+          const float* lv_at = sh.lv[slot] + half * 4;
+          const float* iv_at = sh.iv[slot] + half * 4;
           w.wait<kShort>(&sh.s_full[rt], g & 1);
           tc_fence_after();
           // the largest exponent: a run's scores share their positive factor, so the largest of each run will do
           float top = -INFINITY;
-#pragma unroll 1
-          for (int c = 0; c < 128; c += 32) {
+#pragma unroll
+          for (int c = 0; c < 64; c += 32) {
             float x[32];
             tmem_load32(s_at + c, x);
             if (edge) {
@@ -197,20 +218,22 @@ __global__ __launch_bounds__((RowsCfg<kD, kShared>::kThreads), 1) void q8_attn_r
               float y = x[16 * r];
 #pragma unroll
               for (int z = 1; z < 16; ++z) y = fmaxf(y, x[16 * r + z]);
-              const float f = factor(sh.f[slot][(c >> 4) + r]), lv = sh.lv[slot][(c >> 4) + r];
-              top = fmaxf(top, y == -INFINITY ? -INFINITY : fmaf(y, f, lv));
+              top = fmaxf(top, y == -INFINITY ? -INFINITY : fmaf(y, factor(f_at[(c >> 4) + r]), lv_at[(c >> 4) + r]));
             }
           }
-          const bool raise = set ? top > m + 14.0f : top > -INFINITY;
-          if (__any_sync(0xFFFFFFFFu, raise)) {
+          if (pair_any(pair, set ? top > m + 14.0f : top > -INFINITY)) {
+            sh.both[half][n] = top;
+            pair_sync(pair);
+            top = fmaxf(top, sh.both[half ^ 1][n]);
+            const bool raise = set ? top > m + 14.0f : top > -INFINITY;
             const float now = raise ? top - 6.0f : m;
             const float fac = set ? ex2(m - now) : 1.0f;
             m = now;
             l *= fac;
             set |= raise;
-            if (j > 0) {  // the scores are in, so the products before them are done
+            if (j > 0) {  // the scores are in, so the products before them are done; each owner takes half the channels
 #pragma unroll 1
-              for (int c = 0; c < kD; c += 16) {
+              for (int c = half * (kD / 2); c < (half + 1) * (kD / 2); c += 16) {
                 float o[16];
                 tmem_load16(o_at + c, o);
 #pragma unroll
@@ -218,46 +241,46 @@ __global__ __launch_bounds__((RowsCfg<kD, kShared>::kThreads), 1) void q8_attn_r
                 tmem_store16(o_at + c, o);
               }
             }
+            pair_sync(pair);  // both have read what the other told
           }
-#pragma unroll 1
-          for (int c = 0; c < 128; c += 32) {
-            float x[32];
-            tmem_load32(s_at + c, x);
+#pragma unroll
+          for (int c = 0; c < 64; c += 16) {
+            float x[16];
+            tmem_load16(s_at + c, x);
             if (edge) {
 #pragma unroll
-              for (int y = 0; y < 32; ++y) x[y] = c + y < hidden ? x[y] : -INFINITY;
+              for (int y = 0; y < 16; ++y) x[y] = c + y < hidden ? x[y] : -INFINITY;
             }
-            uint32_t p[16];
+            uint32_t p[8];
+            const float f = factor(f_at[c >> 4]), b = lv_at[c >> 4] - m;
+            const F2 f2 = f2_pack(f, f), b2 = f2_pack(b, b);
+            F2 sum = f2_pack(0.0f, 0.0f);
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-              const float f = factor(sh.f[slot][(c >> 4) + r]), b = sh.lv[slot][(c >> 4) + r] - m;
-              const F2 f2 = f2_pack(f, f), b2 = f2_pack(b, b);
-              F2 sum = f2_pack(0.0f, 0.0f);
-#pragma unroll
-              for (int z = 0; z < 16; z += 2) {
-                const int y = 16 * r + z;
-                float t0, t1;
-                f2_unpack(f2_fma(f2_pack(x[y], x[y + 1]), f2, b2), t0, t1);
-                const float w0 = ex2(t0), w1 = ex2(t1);
-                sum = f2_add(sum, f2_pack(w0, w1));
-                p[y >> 1] = pack_f16x2(w0, w1);
-              }
-              float s0, s1;
-              f2_unpack(sum, s0, s1);
-              l = fmaf(s0 + s1, sh.iv[slot][(c >> 4) + r], l);
+            for (int y = 0; y < 16; y += 2) {
+              float t0, t1;
+              f2_unpack(f2_fma(f2_pack(x[y], x[y + 1]), f2, b2), t0, t1);
+              const float w0 = ex2(t0), w1 = ex2(t1);
+              sum = f2_add(sum, f2_pack(w0, w1));
+              p[y >> 1] = pack_f16x2(w0, w1);
             }
-            tmem_put16(s_at + (c >> 1), p);  // over scores that are in registers or done with
+            float s0, s1;
+            f2_unpack(sum, s0, s1);
+            l = fmaf(s0 + s1, iv_at[c >> 4], l);
+            tmem_put8(s_at + (c >> 1), p);  // over scores that are in registers or done with
           }
           tmem_store_wait();
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_addr(&sh.p_full[rt]));
         }
-        // ---- the output
+        // ---- the output: each owner writes half the channels
+        sh.both[half][n] = l;
+        pair_sync(pair);
+        l = sh.both[0][n] + sh.both[1][n];
         const size_t out_row = static_cast<size_t>(item.q_start + i) * a.n_heads + h * G + hg;
         const size_t part_row = (static_cast<size_t>(item.part + static_cast<int>(item.chunk)) * H + h) * C::kRows + n;
         const float inv = l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l);
-        if (in) {
+        if (in && half == 0) {
           if (item.part >= 0)
             a.part_ml[part_row] = make_float2(l == 0.0f ? -3.4e38f : m, l);
           else if (a.lse != nullptr)
@@ -267,7 +290,7 @@ __global__ __launch_bounds__((RowsCfg<kD, kShared>::kThreads), 1) void q8_attn_r
         tc_fence_after();
         const int any_nan = sh.any_nan;
 #pragma unroll 1
-        for (int c = 0; c < kD; c += 16) {
+        for (int c = half * (kD / 2); c < (half + 1) * (kD / 2); c += 16) {
           float o[16];
           if (n_tiles > 0) {
             tmem_load16(o_at + c, o);
@@ -330,8 +353,8 @@ __global__ __launch_bounds__((RowsCfg<kD, kShared>::kThreads), 1) void q8_attn_r
         if (w.live && elect_one()) {
           const uint64_t vb = smem_operand(v_at + st * C::kSlices * kSlice, kSlice);
 #pragma unroll
-          for (int x = 0; x < 8; ++x)  // 16 entries: 8 columns of weights, 16 rows of 128 bytes
-            tc_mma_ts(tmem + C::kOCol + rt * kD, tmem + rt * 128 + 8 * x, vb + 128 * x, mma_shape(128, kD, false, true),
+          for (int x = 0; x < 8; ++x)  // 16 entries: 8 columns of weights (each half's from its own 64 on), 16 rows
+            tc_mma_ts(tmem + C::kOCol + rt * kD, tmem + rt * 128 + (x >> 2) * 64 + 8 * (x & 3), vb + 128 * x, mma_shape(128, kD, false, true),
                       !fresh || x > 0);
         }
         __syncwarp();
@@ -354,7 +377,7 @@ __global__ __launch_bounds__((RowsCfg<kD, kShared>::kThreads), 1) void q8_attn_r
     // A row tile that was skipped has no phases of its own: both tiles' barriers go on together
     if (tiles == 1 && n_tiles & 1) {
       if (tid == 0) mbar_arrive(smem_addr(&sh.s_full[1]));
-      if (soft && warp >= 4 && lane == 0) mbar_arrive(smem_addr(&sh.p_full[1]));
+      if (soft && warp >= C::kSoftWarps / 2 && lane == 0) mbar_arrive(smem_addr(&sh.p_full[1]));
     }
     tiles_before += n_tiles;
     items_before += n_tiles > 0;
