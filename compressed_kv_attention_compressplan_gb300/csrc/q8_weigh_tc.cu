@@ -5,8 +5,8 @@
 //     S^T [128 entries x 128 rows] = K8 Q^T   per head and chunk of rows,
 // so an entry is a lane of tensor memory, a thread owns it, and its weight
 //     sum over rows of 2^(scale log2(e) k_scale S - lse log2(e))
-// is one register: no lane or warp exchanges anything until the unit's two column
-// halves are added at its end.  Keys become bf16 (exact), the queries are bf16 and are
+// is one register: no lane or warp exchanges anything until the unit's four column
+// groups are added at its end.  Keys become bf16 (exact), the queries are bf16 and are
 // copied as they are, so a chunk costs its copy, its products and 2.5 instructions
 // for each weight.
 //
@@ -24,22 +24,24 @@ constexpr int kChunk = 128;  // rows
 template <int kD>
 struct WtCfg {
   static constexpr int kSlices = kD / 64;
-  static constexpr int kExpWarps = 8;   // two groups of four; a group takes 64 rows of a chunk
+  static constexpr int kExpWarps = 16;  // four groups of four; a group takes 32 rows of a chunk
   static constexpr int kLoadWarps = 8;
   static constexpr int kWarps = kExpWarps + kLoadWarps + 1;
   static constexpr int kThreads = 32 * kWarps;
   static constexpr uint32_t kTileBytes = kSlices * kSlice;  // 128 rows of kD bf16 values
-  static constexpr uint32_t kBytes = 4 * kTileBytes + 1024;  // two stages of keys, two of queries, the alignment
+  static constexpr int kQStages = 4;
+  static constexpr uint32_t kBytes = (2 + kQStages) * kTileBytes + 1024;  // two stages of keys, the queries', the alignment
   static constexpr uint32_t kSmem = kBytes < 120 * 1024 ? 120 * 1024 : kBytes;  // one CTA to an SM: see the attention
   static constexpr uint32_t kCols = 256;
 };
 
 template <int kD>
 struct alignas(16) WtShared {
-  uint64_t k_full[2], k_free[2], q_full[2], q_free[2], s_full[2], s_free[2], idle;
-  alignas(16) float off[2][kChunk];
-  int vis[2][kChunk];
-  float half[128];
+  static constexpr int kQ = WtCfg<kD>::kQStages;
+  uint64_t k_full[2], k_free[2], q_full[kQ], q_free[kQ], s_full[2], s_free[2], idle;
+  alignas(16) float off[kQ][kChunk];
+  int vis[kQ][kChunk];
+  float part[3][128];
   uint32_t unit[CKV_MAX_BATCH];
   uint32_t first_q[CKV_MAX_BATCH];
   unsigned long long scan64[WtCfg<kD>::kWarps + 1];
@@ -67,11 +69,13 @@ __global__ __launch_bounds__(WtCfg<kD>::kThreads, 1) void q8_weigh_tc_kernel(con
   if (tid == 0) {
     for (int s = 0; s < 2; ++s) {
       mbar_init(smem_addr(&sh.k_full[s]), C::kLoadWarps);
-      mbar_init(smem_addr(&sh.q_full[s]), C::kLoadWarps);
       mbar_init(smem_addr(&sh.k_free[s]), 1);
-      mbar_init(smem_addr(&sh.q_free[s]), C::kExpWarps);
       mbar_init(smem_addr(&sh.s_full[s]), 1);
       mbar_init(smem_addr(&sh.s_free[s]), C::kExpWarps);
+    }
+    for (int s = 0; s < C::kQStages; ++s) {
+      mbar_init(smem_addr(&sh.q_full[s]), 33 * C::kLoadWarps);  // every thread's copies, and a warp's lse and counts
+      mbar_init(smem_addr(&sh.q_free[s]), C::kExpWarps);
     }
     mbar_init(smem_addr(&sh.idle), 1);
     fence_mbar_init();
@@ -116,6 +120,16 @@ __global__ __launch_bounds__(WtCfg<kD>::kThreads, 1) void q8_weigh_tc_kernel(con
         }
       };
       load(0);
+      // lane l keeps row l % 16 of this warp's 16 of a chunk: its place (a division, so once a chunk), its query and its
+      // lse, which is asked for a chunk ahead
+      auto place = [&](uint32_t h, uint32_t c, uint32_t* query) {
+        const uint32_t rho = min(c * kChunk + lw * 16 + (lane & 15), rows - 1);
+        *query = rho / G;
+        return static_cast<unsigned long long>(sh.first_q[b] + *query) * a.n_heads + h * G + (rho - *query * G);
+      };
+      uint32_t query_next;
+      unsigned long long row_next = place(0, 0, &query_next);
+      float lse_next = __ldg(a.lse + row_next);
       for (uint32_t h = 0; h < H; ++h, ++kc) {
         const uint32_t ks = kc & 1;
         w.wait<kShort>(&sh.k_free[ks], ((kc >> 1) & 1) ^ 1);
@@ -138,33 +152,36 @@ __global__ __launch_bounds__(WtCfg<kD>::kThreads, 1) void q8_weigh_tc_kernel(con
         if (lane == 0) mbar_arrive(smem_addr(&sh.k_full[ks]));
         load(h + 1);
         for (uint32_t c = 0; c < chunks; ++c, ++qc) {
-          const uint32_t qs = qc & 1;
-          w.wait<kShort>(&sh.q_free[qs], ((qc >> 1) & 1) ^ 1);
-          // this warp's 16 rows, 16 bytes a lane at a time
+          const uint32_t qs = qc % C::kQStages, query = query_next;
+          const unsigned long long row = row_next;
+          const float lse = lse_next;
+          row_next = c + 1 < chunks ? place(h, c + 1, &query_next) : place(min(h + 1, H - 1), 0, &query_next);
+          lse_next = __ldg(a.lse + row_next);
+          w.wait<kShort>(&sh.q_free[qs], ((qc / C::kQStages) & 1) ^ 1);
+          // this warp's 16 rows, 16 bytes a lane at a time; they arrive at the barrier when they have landed
           constexpr int kRowChunks = kD / 8;  // 16-byte chunks of a row
 #pragma unroll
           for (int x = 0; x < kRowChunks / 2; ++x) {
-            const uint32_t i = x * 32 + lane, n = lw * 16 + i / kRowChunks, cc = i % kRowChunks;
-            const uint32_t rho = min(c * kChunk + n, rows - 1);
-            const size_t row = static_cast<size_t>(sh.first_q[b] + rho / G) * a.n_heads + h * G + rho % G;
+            const uint32_t i = x * 32 + lane, r = i / kRowChunks, n = lw * 16 + r, cc = i % kRowChunks;
+            const unsigned long long from = __shfl_sync(0xFFFFFFFFu, row, r);
             cp_async16(q_at + qs * C::kTileBytes + (cc >> 3) * kSlice + n * 128 + (((cc & 7) ^ (n & 7)) << 4),
-                       a.q + row * kD + cc * 8, 16u);
+                       a.q + from * kD + cc * 8, 16u);
           }
-          cp_async_commit();
+          cp_async_arrive(smem_addr(&sh.q_full[qs]));
           if (lane < 16) {
-            const uint32_t n = lw * 16 + lane, at = c * kChunk + n, rho = min(at, rows - 1), i = rho / G;
-            const float lse = __ldg(a.lse + static_cast<size_t>(sh.first_q[b] + i) * a.n_heads + h * G + rho % G);
-            const int64_t see = at < rows ? q8_visible(kv_len, q_len - 1 - i, phase, a.ratio) : 0;
+            const uint32_t n = lw * 16 + lane, at = c * kChunk + n;
+            const int64_t see = at < rows ? q8_visible(kv_len, q_len - 1 - query, phase, a.ratio) : 0;
             sh.vis[qs][n] = static_cast<int>(see);
             // a row that saw nothing weighs nothing, nor does one past the last
             sh.off[qs][n] = at >= rows || lse == -INFINITY ? -INFINITY : lse * -kLog2e;
           }
-          cp_async_wait<0>();
-          fence_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_addr(&sh.q_full[qs]));
         }
       }
+      // none of these copies may land after the CTA is gone
+      cp_async_commit();
+      cp_async_wait<0>();
     } else if (warp < C::kExpWarps) {
       const int group = warp >> 2, quarter = warp & 3, entry = quarter * 32 + lane;
       const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
@@ -175,61 +192,59 @@ __global__ __launch_bounds__(WtCfg<kD>::kThreads, 1) void q8_weigh_tc_kernel(con
       const float* scales = a.c.k_scale + static_cast<size_t>(valid ? blk : 0) * H;
       float next = __ldg(scales);
       F2 sum = f2_pack(0.0f, 0.0f);
+      // the request's first row sees least: where it sees the whole tile, all do
+      const bool edge = static_cast<int64_t>(e0) + kEntries > q8_visible(kv_len, q_len - 1, phase, a.ratio);
       for (uint32_t h = 0; h < H; ++h) {
         const float f = next * a.scale_log2;
         next = __ldg(scales + min(h + 1, H - 1));
         const F2 f2 = f2_pack(f, f);
         for (uint32_t c = 0; c < chunks; ++c, ++qc) {
-          const uint32_t qs = qc & 1;
-          // rows see more and more: the chunk's first row says whether the tile is whole for all
-          const int64_t least = q8_visible(kv_len, q_len - 1 - (c * kChunk) / G, phase, a.ratio);
-          const bool edge = static_cast<int64_t>(e0) + kEntries > least;
-          w.wait<kShort>(&sh.s_full[qs], (qc >> 1) & 1);
+          const uint32_t sb = qc & 1, qs = qc % C::kQStages;
+          w.wait<kShort>(&sh.s_full[sb], (qc >> 1) & 1);
+          w.wait<kShort>(&sh.q_full[qs], (qc / C::kQStages) & 1);  // long since; for the sight of off and vis
           tc_fence_after();
-#pragma unroll 1
-          for (int x0 = 0; x0 < 64; x0 += 32) {
-            float s[32];
-            tmem_load32(tmem + lanes + qs * kChunk + group * 64 + x0, s);
-            const float* off = sh.off[qs] + group * 64 + x0;
-            const int* vis = sh.vis[qs] + group * 64 + x0;
-#pragma unroll
-            for (int x = 0; x < 32; x += 4) {
-              const float4 o = *reinterpret_cast<const float4*>(off + x);
-              float t0, t1, t2, t3;
-              f2_unpack(f2_fma(f2_pack(s[x], s[x + 1]), f2, f2_pack(o.x, o.y)), t0, t1);
-              f2_unpack(f2_fma(f2_pack(s[x + 2], s[x + 3]), f2, f2_pack(o.z, o.w)), t2, t3);
-              float w0 = ex2(t0), w1 = ex2(t1), w2 = ex2(t2), w3 = ex2(t3);
-              if (edge) {
-                w0 = static_cast<int>(e) < vis[x] ? w0 : 0.0f;
-                w1 = static_cast<int>(e) < vis[x + 1] ? w1 : 0.0f;
-                w2 = static_cast<int>(e) < vis[x + 2] ? w2 : 0.0f;
-                w3 = static_cast<int>(e) < vis[x + 3] ? w3 : 0.0f;
-              }
-              sum = f2_add(sum, f2_add(f2_pack(w0, w1), f2_pack(w2, w3)));
-            }
-          }
+          float s[32];
+          tmem_load32(tmem + lanes + sb * kChunk + group * 32, s);
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(smem_addr(&sh.s_free[qs]));
-            mbar_arrive(smem_addr(&sh.q_free[qs]));
+          if (lane == 0) mbar_arrive(smem_addr(&sh.s_free[sb]));
+          const float* off = sh.off[qs] + group * 32;
+          const int* vis = sh.vis[qs] + group * 32;
+#pragma unroll
+          for (int x = 0; x < 32; x += 4) {
+            const float4 o = *reinterpret_cast<const float4*>(off + x);
+            float t0, t1, t2, t3;
+            f2_unpack(f2_fma(f2_pack(s[x], s[x + 1]), f2, f2_pack(o.x, o.y)), t0, t1);
+            f2_unpack(f2_fma(f2_pack(s[x + 2], s[x + 3]), f2, f2_pack(o.z, o.w)), t2, t3);
+            float w0 = ex2(t0), w1 = ex2(t1), w2 = ex2(t2), w3 = ex2(t3);
+            if (edge) {
+              w0 = static_cast<int>(e) < vis[x] ? w0 : 0.0f;
+              w1 = static_cast<int>(e) < vis[x + 1] ? w1 : 0.0f;
+              w2 = static_cast<int>(e) < vis[x + 2] ? w2 : 0.0f;
+              w3 = static_cast<int>(e) < vis[x + 3] ? w3 : 0.0f;
+            }
+            sum = f2_add(sum, f2_add(f2_pack(w0, w1), f2_pack(w2, w3)));
           }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_addr(&sh.q_free[qs]));
         }
       }
       float s0, s1;
       f2_unpack(sum, s0, s1);
-      if (group == 1) sh.half[entry] = s0 + s1;
-      asm volatile("bar.sync 1, 256;" ::: "memory");
-      if (group == 0 && e < kv_len && valid) put_weight(a, blk, e & (T - 1), (s0 + s1) + sh.half[entry]);
-      asm volatile("bar.sync 1, 256;" ::: "memory");
+      if (group > 0) sh.part[group - 1][entry] = s0 + s1;
+      asm volatile("bar.sync 1, 512;" ::: "memory");
+      if (group == 0 && e < kv_len && valid)
+        put_weight(a, blk, e & (T - 1), ((s0 + s1) + sh.part[0][entry]) + (sh.part[1][entry] + sh.part[2][entry]));
+      asm volatile("bar.sync 1, 512;" ::: "memory");
     } else {
       for (uint32_t h = 0; h < H; ++h, ++kc) {
         const uint32_t ks = kc & 1;
         w.wait<kShort>(&sh.k_full[ks], (kc >> 1) & 1);
         for (uint32_t c = 0; c < chunks; ++c, ++qc) {
-          const uint32_t qs = qc & 1;
-          w.wait<kShort>(&sh.q_full[qs], (qc >> 1) & 1);
-          w.wait<kShort>(&sh.s_free[qs], ((qc >> 1) & 1) ^ 1);
+          const uint32_t sb = qc & 1, qs = qc % C::kQStages;
+          w.wait<kShort>(&sh.q_full[qs], (qc / C::kQStages) & 1);
+          w.wait<kShort>(&sh.s_free[sb], ((qc >> 1) & 1) ^ 1);
+          fence_async_smem();  // other threads' copies come without a fence of theirs
           tc_fence_after();
           if (elect_one()) {
             if (w.live) {
@@ -239,11 +254,11 @@ __global__ __launch_bounds__(WtCfg<kD>::kThreads, 1) void q8_weigh_tc_kernel(con
                 const uint64_t qb = smem_operand(q_at + qs * C::kTileBytes + s * kSlice, 0);
 #pragma unroll
                 for (int x = 0; x < 4; ++x)
-                  tc_mma(tmem + qs * kChunk, ka + 2 * x, qb + 2 * x, mma_shape(128, kChunk, false, false) | kBf16,
+                  tc_mma(tmem + sb * kChunk, ka + 2 * x, qb + 2 * x, mma_shape(128, kChunk, false, false) | kBf16,
                          s > 0 || x > 0);
               }
             }
-            tc_commit(smem_addr(&sh.s_full[qs]));
+            tc_commit(smem_addr(&sh.s_full[sb]));
             if (c + 1 == chunks) tc_commit(smem_addr(&sh.k_free[ks]));
           }
           __syncwarp();
