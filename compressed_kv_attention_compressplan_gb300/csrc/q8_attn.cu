@@ -187,6 +187,7 @@ __global__ __launch_bounds__(kPlanThreads) void plan_q8_attn_kernel(const AttnPl
     head->num_q = a.num_q;
     head->ratio = a.ratio;
     head->cap_ctas = a.g.ctas;
+    head->batch = a.batch;
     head->most = s_most;  // (the last strip ended with a barrier)
     if (total_q != a.num_q) status_or(a.d_status, CKV_STATUS_BAD_TOTAL);
   }
@@ -821,6 +822,7 @@ int ckv_q8_attn(const ckv_q8_cache_t* cache, uint32_t n_heads, uint32_t ratio, f
       (lse != nullptr && !aligned_to(lse, 4)))
     return CKV_ERR_POINTER;
   a.q = static_cast<const __nv_bfloat16*>(q);
+  a.batch = batch;
   a.num_q = num_q;
   a.n_heads = n_heads;
   a.ratio = ratio;

@@ -191,13 +191,27 @@ __global__ __launch_bounds__((TcCfg<kD, kShared>::kThreads), 1) void q8_attn_tc_
       auto ask = [&](uint32_t tile) {
         return __ldg(table + (min(item.kv_begin + tile * kEntries + (lane & 7) * 16, last) >> t_shift));
       };
-      int32_t runs = ask(0);
+      int32_t runs = ask(0), runs_next = ask(1), runs_after = ask(2);
+      // a tile's runs, each one piece of memory, are asked into L2 two tiles before they are copied
+      auto prefetch = [&](uint32_t tile, int32_t b) {
+        const uint32_t e = item.kv_begin + tile * kEntries + lane * 16;
+        if (cw == 0 && lane < 8 && tile < n_tiles && e < item.kv_end && static_cast<uint32_t>(b) < a.c.num_blocks) {
+          const size_t at = (((static_cast<size_t>(b) * H + h) << t_shift) + (e & (T - 1))) * kD;
+          bulk_prefetch_l2(a.c.k + at, 16 * kD);
+          if (!kShared) bulk_prefetch_l2(a.c.v + at, 16 * kD);
+        }
+      };
+      prefetch(0, runs);
+      prefetch(1, runs_next);
       for (uint32_t j = 0; j < n_tiles; ++j) {
         const uint32_t g = tiles_before + j, st = g % C::kStages, use = g / C::kStages;
         const uint32_t e0 = item.kv_begin + j * kEntries;
         const bool edge = e0 + kEntries > vis_min;
         const int32_t now = runs;
-        runs = ask(j + 1);
+        prefetch(j + 2, runs_after);
+        runs = runs_next;
+        runs_next = runs_after;
+        runs_after = ask(j + 3);
         size_t off[kSteps];
         uint32_t in = 0;  // bit i: step i's entry exists
 #pragma unroll

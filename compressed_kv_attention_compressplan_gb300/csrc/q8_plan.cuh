@@ -42,8 +42,9 @@ struct Q8Header {  // 64 bytes
   uint32_t num_q;
   uint32_t ratio;
   uint32_t cap_ctas;
+  uint32_t batch;
   uint32_t most;  // parts of the tile that has most
-  uint32_t reserved[6];
+  uint32_t reserved[5];
 };
 static_assert(sizeof(Q8Header) == 64, "");
 
@@ -71,6 +72,7 @@ struct AttnArgs {
   Q8Cache c;
   Q8Geom g;
   const __nv_bfloat16* q;
+  uint32_t batch;
   uint32_t num_q;
   uint32_t n_heads;
   uint32_t ratio;
@@ -97,7 +99,7 @@ __device__ __forceinline__ bool item_fits(const Q8Item& item, const AttnArgs& a)
 
 __device__ __forceinline__ bool plan_fits(const Q8Header* h, const AttnArgs& a) {
   return h->rows == a.g.rows && h->group == a.g.group && h->num_q == a.num_q && h->ratio == a.ratio &&
-         h->cap_ctas == a.g.ctas;
+         h->cap_ctas == a.g.ctas && h->batch == a.batch;
 }
 
 // Takes the NaNs out of a word of four channels of entry e, noting the first entry with one for each channel.

@@ -829,3 +829,63 @@ def test_shapes_that_the_binding_refuses():
         with pytest.raises((ValueError, ckv.CkvError)):
             f()
             pytest.fail(f"case {k} was taken")
+
+
+@pytest.mark.parametrize("D,latent", [(128, False), (64, True), (512, True), (256, False)])
+def test_waits_that_run_out_are_reported_and_leave_the_context_usable(D, latent):
+    """The kernels whose roles hand tiles to one another, with a wait limit of a nanosecond: they end, say so, and the
+    next launch computes as ever."""
+    n, heads = 1500, 64
+    w = World(61, [n], 1, D, 64, latent)
+    q = w.queries([3], heads)
+    cache, _, want, lse, st = run_attn(w, q, [n], [3], heads, 1)
+    assert st == 0
+    old = ckv.set_wait_limit_ns(1)
+    try:
+        _, _, _, _, st = run_attn(w, q, [n], [3], heads, 1)
+        assert st == ckv.STATUS_TIMEOUT
+        weigh = status()
+        ckv.q8_weigh(cache, q.to(DEV), lse, torch.zeros(w.blocks, 64, device=DEV), 1, i64(w.rid), i64([n]), i64([3]),
+                     i64([n]), i32(w.table), 1 / math.sqrt(D), status=weigh)
+        torch.cuda.synchronize()
+        assert int(weigh[0]) == (ckv.STATUS_TIMEOUT if D <= 128 else 0)  # from 256 channels on it waits for nobody
+    finally:
+        ckv.set_wait_limit_ns(old)
+    _, _, again, _, st = run_attn(w, q, [n], [3], heads, 1)
+    assert st == 0
+    assert torch.equal(again, want)
+
+
+def test_results_repeat_bit_for_bit():
+    for D, latent, heads, q_len in [(128, False, 4, 1), (512, True, 64, 1), (128, False, 16, 60)]:
+        w = World(62, [3000, 700], 1, D, 64, latent)
+        q = w.queries([q_len, q_len], heads)
+        first = run_attn(w, q, [3000, 700], [q_len] * 2, heads, 1)
+        for _ in range(3):
+            more = run_attn(w, q, [3000, 700], [q_len] * 2, heads, 1)
+            assert torch.equal(first[2], more[2]) and torch.equal(first[3], more[3])
+
+
+def test_many_requests_and_a_full_batch():
+    """A batch of 1024 (the most), each of one entry or two, in every operator."""
+    B = 1024
+    lens = np.arange(B) % 3
+    w = World(63, lens, 1, 64, 16, False, extra=2200)
+    heads = 2
+    q = w.queries([1] * B, heads)
+    cache, _, out, lse, st = run_attn(w, q, np.maximum(lens, 1), [1] * B, heads, 1, torch.float32)
+    want, wl, mag, big, flat = ref.attn(w.k, w.ks, w.v, w.vs, q.float().numpy(), w.rid, np.maximum(lens, 1), [1] * B,
+                                        w.lens, w.table, 1, 1 / 8)
+    tol, _ = attn_bounds(64, 2, want, wl, mag, big, flat, 20.0, False)
+    assert st == 0 and (np.abs(out.cpu().numpy() - want) <= tol).all()
+    weights, st = torch.zeros(w.blocks, 16, device=DEV), status()
+    ckv.q8_weigh(cache, q.to(DEV), lse, weights, 1, i64(w.rid), i64(np.maximum(lens, 1)), i64([1] * B), i64(lens),
+                 i32(w.table), 1 / 8, status=st)
+    dst = np.full((w.table.shape[0], 1), -1, np.int32)
+    dst[w.rid, 0] = w.spare[:B]
+    kept, nl = ckv.q8_evict(cache, weights, i64(w.rid), i64(lens), i32(w.table), i32(dst), 1, 0, 1, status=st)
+    torch.cuda.synchronize()
+    assert int(st[0]) == 0
+    assert abs(float(weights.sum()) - heads * (lens > 0).sum()) > 0  # the moved ones count twice
+    assert nl.cpu().tolist() == np.minimum(lens, 1).tolist()
+    assert kept.cpu().numpy()[:, 0].tolist() == [n - 1 for n in lens]
