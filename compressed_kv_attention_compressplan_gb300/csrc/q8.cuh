@@ -170,6 +170,43 @@ __device__ __forceinline__ T block_exclusive(T v, T* total, T* s_warp) {
   return s_warp[warp] + incl - v;
 }
 
+// Two such scans between the same barriers.
+template <int kThreads, typename T>
+__device__ __forceinline__ void block_exclusive2(T v0, T v1, T* out0, T* out1, T* total0, T* total1, T (*s_warp)[kThreads / 32 + 1]) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  T a = v0, b = v1;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const T x = __shfl_up_sync(0xFFFFFFFFu, a, off), y = __shfl_up_sync(0xFFFFFFFFu, b, off);
+    if (lane >= off) {
+      a += x;
+      b += y;
+    }
+  }
+  __syncthreads();  // an earlier scan's reads of s_warp are done
+  if (lane == 31) {
+    s_warp[0][warp] = a;
+    s_warp[1][warp] = b;
+  }
+  __syncthreads();
+  // every warp adds the warps' sums up for itself: one barrier less
+  const T x = lane < kThreads / 32 ? s_warp[0][lane] : T(0), y = lane < kThreads / 32 ? s_warp[1][lane] : T(0);
+  T p = x, q = y;
+#pragma unroll
+  for (int off = 1; off < kThreads / 32; off <<= 1) {
+    const T u = __shfl_up_sync(0xFFFFFFFFu, p, off), v = __shfl_up_sync(0xFFFFFFFFu, q, off);
+    if (lane >= off) {
+      p += u;
+      q += v;
+    }
+  }
+  const T base0 = __shfl_sync(0xFFFFFFFFu, p - x, warp), base1 = __shfl_sync(0xFFFFFFFFu, q - y, warp);
+  *out0 = base0 + a - v0;
+  *out1 = base1 + b - v1;
+  *total0 = __shfl_sync(0xFFFFFFFFu, p, kThreads / 32 - 1);
+  *total1 = __shfl_sync(0xFFFFFFFFu, q, kThreads / 32 - 1);
+}
+
 // The last index i with s[i] <= x, for ascending s[0 .. n) with s[0] <= x.
 template <typename T>
 __device__ __forceinline__ uint32_t last_not_above(const T* s, uint32_t n, T x) {

@@ -51,7 +51,7 @@ __global__ __launch_bounds__(kPlanThreads) void plan_q8_attn_kernel(const AttnPl
       s_ph[kPlanThreads], s_tile[kPlanThreads];
   __shared__ unsigned long long s_pos[kPlanThreads];
   __shared__ uint32_t s_item[kPlanThreads], s_part[kPlanThreads];
-  __shared__ unsigned long long s_scan[kPlanThreads / 32 + 1];
+  __shared__ unsigned long long s_scan[2][kPlanThreads / 32 + 1];
   __shared__ uint32_t s_most;
   pdl_wait();
   pdl_release();
@@ -79,11 +79,9 @@ __global__ __launch_bounds__(kPlanThreads) void plan_q8_attn_kernel(const AttnPl
       rid = static_cast<uint32_t>(r);
     }
   }
-  unsigned long long total_q, total_tiles;
-  const unsigned long long qs = block_exclusive<kPlanThreads>(q_len, &total_q, s_scan);
-  ok = ok && qs + q_len <= a.num_q;
-  const unsigned long long tiles = ok ? (q_len * G + M - 1) / M : 0;
-  const unsigned long long tile0 = block_exclusive<kPlanThreads>(tiles, &total_tiles, s_scan);
+  unsigned long long total_q, total_tiles, qs, tile0;
+  const unsigned long long tiles = ok ? (static_cast<uint32_t>(q_len) * G + M - 1) / M : 0;
+  block_exclusive2<kPlanThreads>(q_len, tiles, &qs, &tile0, &total_q, &total_tiles, s_scan);
   if (t < a.batch) {
     s_rid[t] = rid;
     s_qs[t] = static_cast<uint32_t>(qs);
@@ -93,7 +91,8 @@ __global__ __launch_bounds__(kPlanThreads) void plan_q8_attn_kernel(const AttnPl
     s_tile[t] = static_cast<uint32_t>(tile0);
   }
   __syncthreads();
-  const uint32_t nt = static_cast<uint32_t>(total_tiles);
+  // more queries than num_q have no places, and more tiles than the plan's buffer holds: then nothing is planned
+  const uint32_t nt = total_q > a.num_q ? 0 : static_cast<uint32_t>(total_tiles);
 
   // a tile's entries: those its last query sees
   auto tile_of = [&](uint32_t tile, uint32_t* b) -> uint32_t {
@@ -113,7 +112,7 @@ __global__ __launch_bounds__(kPlanThreads) void plan_q8_attn_kernel(const AttnPl
     mine += cost_of(tile_of(i, &b));
   }
   unsigned long long total;
-  block_exclusive<kPlanThreads>(mine, &total, s_scan);
+  const unsigned long long before = block_exclusive<kPlanThreads>(mine, &total, s_scan[0]);
   unsigned long long quota = (total + a.g.ctas - 1) / a.g.ctas;
   quota = max(static_cast<unsigned long long>(a.g.min_quota), quota);
   quota = (quota + a.g.round - 1) / a.g.round * a.g.round;
@@ -122,16 +121,15 @@ __global__ __launch_bounds__(kPlanThreads) void plan_q8_attn_kernel(const AttnPl
   uint32_t item0 = 0, part0 = 0, split0 = 0;
   for (uint32_t i0 = 0; i0 < nt; i0 += kPlanThreads) {
     const uint32_t i = i0 + t;
-    uint32_t b = 0, n = 0;
-    unsigned long long cost = 0;
-    if (i < nt) cost = cost_of(tile_of(i, &b));
-    unsigned long long cost_sum, packed_sum;
-    const unsigned long long p = pos0 + block_exclusive<kPlanThreads>(cost, &cost_sum, s_scan);
+    uint32_t b, n = 0;
+    const unsigned long long cost = nt <= kPlanThreads ? mine : i < nt ? cost_of(tile_of(i, &b)) : 0;
+    unsigned long long cost_sum = total, packed_sum, p = before;  // a single strip's sums are known
+    if (nt > kPlanThreads) p = pos0 + block_exclusive<kPlanThreads>(cost, &cost_sum, s_scan[0]);
     if (cost) n = static_cast<uint32_t>((p + cost - 1) / quota - p / quota) + 1;
     // items (32 bits), parts (16) and splits (16) of the strip, in one scan: parts are at most twice the CTAs
     const unsigned long long pk = n | (static_cast<unsigned long long>(n > 1 ? n : 0) << 32) |
                                   (static_cast<unsigned long long>(n > 1) << 48);
-    const unsigned long long ex = block_exclusive<kPlanThreads>(pk, &packed_sum, s_scan);
+    const unsigned long long ex = block_exclusive<kPlanThreads>(pk, &packed_sum, s_scan[0]);
     const uint32_t it = item0 + static_cast<uint32_t>(ex);
     s_pos[t] = p;
     s_item[t] = it;

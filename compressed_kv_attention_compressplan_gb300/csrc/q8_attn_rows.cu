@@ -24,8 +24,6 @@ namespace {
 template <int kD, bool kShared>
 struct RowsCfg {
   static constexpr bool kLatent = kShared;
-  static constexpr bool kGroupScales = true;
-  static constexpr bool kPrefetch = false;  // row tiles share their entries: most come from L2 as it is
   static constexpr int kRows = 256;
   static constexpr int kSlices = kD / 64;
   static constexpr int kStages = 2;

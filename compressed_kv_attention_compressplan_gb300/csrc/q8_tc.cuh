@@ -142,28 +142,7 @@ __device__ __forceinline__ void convert_tiles(const AttnArgs& a, const Q8Item& i
     for (int i = 0; i < C::kLoads; ++i) d[i] = ld_stream16_if(o[i] + at, mask >> i & 1);
   };
   GroupScales<Sh> groups(a, item, sh, lane, h, table, tiles_before, last, t_shift);
-  if constexpr (C::kGroupScales) {
-    if (cw == 0) groups.start();
-  }
-  // A run of 16 entries lies in one piece: lanes 0 .. 7 of one warp ask for a tile's eight runs two tiles ahead, so that the
-  // loads above come from L2.
-  int32_t run_blk = 0;
-  auto ask_run = [&](uint32_t tile) {
-    run_blk = __ldg(table + (min(item.kv_begin + tile * kEntries + (lane & 7) * 16, last) >> t_shift));
-  };
-  auto prefetch = [&](uint32_t tile) {
-    const uint32_t e = item.kv_begin + tile * kEntries + lane * 16;
-    if (lane < 8 && tile < n_tiles && e < item.kv_end && static_cast<uint32_t>(run_blk) < a.c.num_blocks) {
-      const size_t at = (((static_cast<size_t>(run_blk) * H + h) << t_shift) + (e & (T - 1))) * kD;
-      bulk_prefetch_l2(a.c.k + at, 16 * kD);
-      if (!kShared) bulk_prefetch_l2(a.c.v + at, 16 * kD);
-    }
-  };
-  if (C::kPrefetch && cw == 1) {
-    ask_run(1);
-    prefetch(1);
-    ask_run(2);
-  }
+  if (cw == 0) groups.start();
   ask(0);
   here = locate(0, src);
   ask(1);
@@ -173,13 +152,7 @@ __device__ __forceinline__ void convert_tiles(const AttnArgs& a, const Q8Item& i
     const uint32_t g = tiles_before + j, st = g % C::kStages, use = g / C::kStages;
     const uint32_t e0 = item.kv_begin + j * kEntries;
     const bool edge = e0 + kEntries > vis_min;
-    if constexpr (C::kGroupScales) {
-      if (cw == 0) groups.put(j);
-    }
-    if (C::kPrefetch && cw == 1) {
-      prefetch(j + 2);
-      ask_run(j + 3);
-    }
+    if (cw == 0) groups.put(j);
     here_next = locate(j + 1, src_next);
     ask(j + 2);
 #pragma unroll 1

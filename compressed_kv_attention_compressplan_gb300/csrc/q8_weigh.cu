@@ -13,7 +13,7 @@
 // attention does, but with the entries as the product's 16 rows and the queries as its
 // columns, eight or sixteen: a batch of up to eight rows a head then costs half the products
 // and exponentials, and an entry's sum crosses four lanes.  The CTAs share the batch's tiles out evenly, and a CTA's warps take
-// one head each and are summed in head order once per run of 256 entries.
+// one head each and are summed in head order once per run of 512 entries.
 //
 // Many rows (a window of queries): the products and exponentials bound it.  Up to 128
 // channels the tensor cores take it (q8_weigh_tc.cu); from 256 on a warp holds 16 entries
@@ -189,7 +189,7 @@ struct StreamCfg {
   static constexpr int kPerSm = kD <= 128 ? 2 : 1;
   static constexpr int kStageBytes = kTile * kD + 16;  // and the tile's scale
   static constexpr int kSmem = kWarps * kStages * kStageBytes;
-  static constexpr int kRun = 16;  // tiles that are summed over the heads at once
+  static constexpr int kRun = 32;  // tiles that are summed over the heads at once: one to a lane
 };
 
 // kCols: query rows of a pass, 8 or 16.
@@ -224,8 +224,8 @@ __global__ __launch_bounds__(kThreads, StreamCfg<kD>::kPerSm) void q8_weigh_stre
     const uint32_t rows = q_len * G;
     const int32_t* table = a.table + static_cast<size_t>(a.rid[b]) * a.stride;
     const uint32_t mine = run > part ? (run - part + parts - 1) / parts : 0;  // tiles part, part + parts, ...
-    // a run has at most 16 tiles: lane t keeps tile t's block number
-    const int32_t blk = __ldg(table + (min(first + (lane & 15) * kTile, kv_len - 1) >> t_shift));
+    // lane t keeps tile t's block number
+    const int32_t blk = __ldg(table + (min(first + lane * kTile, kv_len - 1) >> t_shift));
     const bool blk_ok = static_cast<uint32_t>(blk) < a.c.num_blocks;
     if (!blk_ok && static_cast<uint32_t>(lane) < run) status_or(a.d_status, CKV_STATUS_BAD_INDEX);
     for (uint32_t i = lane; i < C::kRun * kTile; i += 32) s_sum[warp][i] = 0.0f;
