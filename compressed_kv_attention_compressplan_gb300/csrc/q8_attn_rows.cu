@@ -27,14 +27,12 @@ struct RowsCfg {
   static constexpr int kRows = 256;
   static constexpr int kSlices = kD / 64;
   static constexpr int kStages = 2;
-  static constexpr int kFree = 1;
   static constexpr int kSoftWarps = 16;  // of each row tile: four for the first 64 entries, four for the others
   static constexpr int kConvWarps = 8;
   static constexpr int kWarps = kSoftWarps + kConvWarps + 1;
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kLoads = kEntries / (8 * kConvWarps);
   static constexpr int kUnits = kSlices * (kShared ? 1 : 2);
-  static constexpr int kAhead = kUnits;
   static constexpr uint32_t kQBytes = kSlices * 2 * kSlice;
   static constexpr uint32_t kKBytes = kStages * kSlices * kSlice;
   static constexpr uint32_t kVBytes = kShared ? 0 : kKBytes;
@@ -49,8 +47,7 @@ struct RowsCfg {
 template <int kD, bool kShared>
 struct alignas(16) RowsShared {
   using C = RowsCfg<kD, kShared>;
-  uint64_t k_full[C::kStages][C::kSlices], k_free[C::kStages][1];
-  uint64_t v_full[C::kStages][C::kSlices], v_free[C::kStages];
+  uint64_t k_full[C::kStages], k_free[C::kStages], v_full[C::kStages], v_free[C::kStages];
   uint64_t s_full[2], p_full[2], o_done, idle;
   alignas(16) float f[4][8];  // see GroupScales
   alignas(16) float lv[4][8];
@@ -105,11 +102,9 @@ __global__ __launch_bounds__((RowsCfg<kD, kShared>::kThreads), 1) void q8_attn_r
   if (warp == C::kWarps - 1) tmem_alloc(smem_addr(&sh.tmem), C::kCols);
   if (tid == 0) {
     for (int s = 0; s < C::kStages; ++s) {
-      for (int x = 0; x < C::kSlices; ++x) {
-        mbar_init(smem_addr(&sh.k_full[s][x]), C::kConvWarps);
-        mbar_init(smem_addr(&sh.v_full[s][x]), C::kConvWarps);
-      }
-      mbar_init(smem_addr(&sh.k_free[s][0]), 1);
+      mbar_init(smem_addr(&sh.k_full[s]), C::kConvWarps);
+      mbar_init(smem_addr(&sh.v_full[s]), C::kConvWarps);
+      mbar_init(smem_addr(&sh.k_free[s]), 1);
       mbar_init(smem_addr(&sh.v_free[s]), 1);
     }
     for (int t = 0; t < 2; ++t) {
@@ -142,31 +137,39 @@ __global__ __launch_bounds__((RowsCfg<kD, kShared>::kThreads), 1) void q8_attn_r
     const uint32_t vis_min = min(item.kv_end, static_cast<uint32_t>(q8_visible(item.kv_len, item.q_len - 1 - item.row0 / G,
                                                                              item.phase, a.ratio)));
     // ---- the rows' query operand and scaling
-    for (int n = warp; n < tiles * 128; n += C::kWarps) {
-      constexpr int kPer = kD / 32;  // consecutive channels of a lane
-      const bool in = static_cast<uint32_t>(n) < rows;
-      const uint32_t rho = item.row0 + (in ? n : 0), i = rho / G, hg = rho % G;
-      const size_t row = static_cast<size_t>(item.q_start + i) * a.n_heads + h * G + hg;
-      const uint32_t* p = reinterpret_cast<const uint32_t*>(a.q + row * kD + lane * kPer);
-      uint32_t x[kPer / 2];
-      float m = 0.0f;
+    constexpr int kPer = kD / 32, kBatch = 4;  // consecutive channels of a lane; rows whose loads are in flight together
+    for (int n0 = warp; n0 < tiles * 128; n0 += kBatch * C::kWarps) {
+      uint32_t x[kBatch][kPer / 2];
 #pragma unroll
-      for (int e = 0; e < kPer / 2; ++e) {
-        x[e] = in ? __ldg(p + e) : 0u;
-        m = fmaxf(m, fmaxf(fabsf(bf16lo(x[e])), fabsf(bf16hi(x[e]))));
+      for (int b = 0; b < kBatch; ++b) {
+        const uint32_t n = n0 + b * C::kWarps;
+        const bool in = n < rows;
+        const uint32_t rho = item.row0 + (in ? n : 0), i = rho / G, hg = rho % G;
+        const size_t row = static_cast<size_t>(item.q_start + i) * a.n_heads + h * G + hg;
+        const uint32_t* p = reinterpret_cast<const uint32_t*>(a.q + row * kD + lane * kPer);
+#pragma unroll
+        for (int e = 0; e < kPer / 2; ++e) x[b][e] = in ? __ldg(p + e) : 0u;
       }
 #pragma unroll
-      for (int s = 16; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, s));
-      const int ex = min(126, 14 - (static_cast<int>(__float_as_uint(m) >> 23) - 127));
-      const float up = pow2f(ex);
-      const int r = n & 127;
+      for (int b = 0; b < kBatch; ++b) {
+        const int n = n0 + b * C::kWarps;
+        if (n >= tiles * 128) break;
+        float m = 0.0f;
 #pragma unroll
-      for (int e = 0; e < kPer / 2; ++e) {
-        const uint32_t c = lane * kPer + 2 * e;
-        sts_u32(q_at + ((n >> 7) * C::kSlices + (c >> 6)) * kSlice + r * 128 + ((((c & 63) >> 3) ^ (r & 7)) << 4) + (c & 7) * 2,
-                pack_f16x2(bf16lo(x[e]) * up, bf16hi(x[e]) * up));
+        for (int e = 0; e < kPer / 2; ++e) m = fmaxf(m, fmaxf(fabsf(bf16lo(x[b][e])), fabsf(bf16hi(x[b][e]))));
+#pragma unroll
+        for (int s = 16; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, s));
+        const int ex = min(126, 14 - (static_cast<int>(__float_as_uint(m) >> 23) - 127));
+        const float up = pow2f(ex);
+        const int r = n & 127;
+#pragma unroll
+        for (int e = 0; e < kPer / 2; ++e) {
+          const uint32_t c = lane * kPer + 2 * e;
+          sts_u32(q_at + ((n >> 7) * C::kSlices + (c >> 6)) * kSlice + r * 128 + ((((c & 63) >> 3) ^ (r & 7)) << 4) + (c & 7) * 2,
+                  pack_f16x2(bf16lo(x[b][e]) * up, bf16hi(x[b][e]) * up));
+        }
+        if (lane == 0) sh.rf[n] = pow2f(-ex);
       }
-      if (lane == 0) sh.rf[n] = pow2f(-ex);
     }
     for (int c = tid; c < (kShared ? 1 : kD); c += C::kThreads) sh.nan[c] = 0x7FFFFFFF;
     if (tid == 0) sh.any_nan = 0;
@@ -317,61 +320,58 @@ __global__ __launch_bounds__((RowsCfg<kD, kShared>::kThreads), 1) void q8_attn_r
         }
         tc_fence_before();
       }
-    } else {
-      // ---- the products: the warp waits together, one thread issues.  Products run in the order of issue, so a tile's scores
+    } else if (elect_one()) {
+      // ---- the products, by one thread, which also waits for what they need.  Products run in the order of issue, so a tile's scores
       // overwrite the weights that the product before them has read.
-      auto scores = [&](int rt, uint32_t g, bool last_tile) {
-        const uint32_t st = g % C::kStages, use = g / C::kStages;
-#pragma unroll 1
-        for (int s = 0; s < C::kSlices; ++s) {
-          w.wait<kShort>(&sh.k_full[st][s], use & 1);
-          tc_fence_after();
-          if (w.live && elect_one()) {
-            const uint64_t qa = smem_operand(q_at + (rt * C::kSlices + s) * kSlice, 0);
-            const uint64_t kb = smem_operand(k_at + (st * C::kSlices + s) * kSlice, 0);
+      // A wait that is over at once still takes some 130 cycles, so there are few: K and V are waited for once for both row
+      // tiles, and before the weights, so that nothing but the products stands between those and the next scores.
+      auto scores = [&](int rt, uint32_t st) {
+        if (w.live) {
+          const uint64_t qa = smem_operand(q_at + rt * C::kSlices * kSlice, 0);
+          const uint64_t kb = smem_operand(k_at + st * C::kSlices * kSlice, 0);
+#pragma unroll
+          for (int s = 0; s < C::kSlices; ++s) {
 #pragma unroll
             for (int x = 0; x < 4; ++x)  // 16 channels, 32 bytes of a row
-              tc_mma(tmem + rt * 128, qa + 2 * x, kb + 2 * x, mma_shape(128, 128, false, false), s > 0 || x > 0);
+              tc_mma(tmem + rt * 128, qa + s * (kSlice >> 4) + 2 * x, kb + s * (kSlice >> 4) + 2 * x,
+                     mma_shape(128, 128, false, false), s > 0 || x > 0);
           }
-          __syncwarp();
         }
-        if (elect_one()) {
-          tc_commit(smem_addr(&sh.s_full[rt]));
-          if (!kShared && last_tile) tc_commit(smem_addr(&sh.k_free[st][0]));
-        }
-        __syncwarp();
-      };
-      auto values = [&](int rt, uint32_t g, bool fresh, bool last_tile) {
-        const uint32_t st = g % C::kStages, use = g / C::kStages;
-        w.wait<kShort>(&sh.p_full[rt], g & 1);
-        if (!kShared) {
-          for (int s = 0; s < C::kSlices; ++s) w.wait<kShort>(&sh.v_full[st][s], use & 1);
-        }
-        tc_fence_after();
-        if (w.live && elect_one()) {
-          const uint64_t vb = smem_operand(v_at + st * C::kSlices * kSlice, kSlice);
-#pragma unroll
-          for (int x = 0; x < 8; ++x)  // 16 entries: 8 columns of weights (each half's from its own 64 on), 16 rows
-            tc_mma_ts(tmem + C::kOCol + rt * kD, tmem + rt * 128 + (x >> 2) * 64 + 8 * (x & 3), vb + 128 * x, mma_shape(128, kD, false, true),
-                      !fresh || x > 0);
-        }
-        __syncwarp();
-        if (last_tile && elect_one()) tc_commit(smem_addr(kShared ? &sh.k_free[st][0] : &sh.v_free[st]));
-        __syncwarp();
+        tc_commit(smem_addr(&sh.s_full[rt]));
       };
       if (n_tiles > 0) {
-        for (int rt = 0; rt < tiles; ++rt) scores(rt, tiles_before, rt == tiles - 1);
+        uint32_t st = tiles_before % C::kStages;
+        w.wait_alone<kShort>(&sh.k_full[st], (tiles_before / C::kStages) & 1);
+        tc_fence_after();
+        for (int rt = 0; rt < tiles; ++rt) scores(rt, st);
+        if (!kShared) tc_commit(smem_addr(&sh.k_free[st]));
+#pragma unroll 1
         for (uint32_t j = 0; j < n_tiles; ++j) {
-          const uint32_t g = tiles_before + j;
+          const uint32_t g = tiles_before + j, next = (g + 1) % C::kStages;
+          const bool more = j + 1 < n_tiles;
+          if (!kShared) w.wait_alone<kShort>(&sh.v_full[st], (g / C::kStages) & 1);
+          if (more) w.wait_alone<kShort>(&sh.k_full[next], ((g + 1) / C::kStages) & 1);
+#pragma unroll 1
           for (int rt = 0; rt < tiles; ++rt) {
-            values(rt, g, j == 0, rt == tiles - 1);
-            if (j + 1 < n_tiles) scores(rt, g + 1, rt == tiles - 1);
+            w.wait_alone<kShort>(&sh.p_full[rt], g & 1);
+            tc_fence_after();
+            if (w.live) {
+              const uint64_t vb = smem_operand(v_at + st * C::kSlices * kSlice, kSlice);
+#pragma unroll
+              for (int x = 0; x < 8; ++x)  // 16 entries: 8 columns of weights (each half's from its own 64 on), 16 rows
+                tc_mma_ts(tmem + C::kOCol + rt * kD, tmem + rt * 128 + (x >> 2) * 64 + 8 * (x & 3), vb + 128 * x,
+                          mma_shape(128, kD, false, true), j > 0 || x > 0);
+            }
+            if (rt == tiles - 1) tc_commit(smem_addr(kShared ? &sh.k_free[st] : &sh.v_free[st]));
+            if (more) scores(rt, next);
           }
+          if (more && !kShared) tc_commit(smem_addr(&sh.k_free[next]));
+          st = next;
         }
-        if (elect_one()) tc_commit(smem_addr(&sh.o_done));
-        __syncwarp();
+        tc_commit(smem_addr(&sh.o_done));
       }
     }
+    __syncwarp();
     // A row tile that was skipped has no phases of its own: both tiles' barriers go on together
     if (tiles == 1 && n_tiles & 1) {
       if (tid == 0) mbar_arrive(smem_addr(&sh.s_full[1]));
@@ -390,7 +390,7 @@ __global__ __launch_bounds__((RowsCfg<kD, kShared>::kThreads), 1) void q8_attn_r
     if (!done) w.live = false;
     tmem_free(tmem, C::kCols);
   }
-  if (!w.live && lane == 0) status_or(a.d_status, CKV_STATUS_TIMEOUT);
+  if (!w.live) status_or(a.d_status, CKV_STATUS_TIMEOUT);
 }
 
 template <int kD, bool kShared>

@@ -529,62 +529,55 @@ __global__ __launch_bounds__((TcCfg<kD, kShared>::kThreads), 1) void q8_attn_tc_
         }
       }
       tc_fence_before();
-    } else {
-      // ---- the products: the warp waits together, one thread issues.  The entries were copied by other threads without
+    } else if (elect_one()) {
+      // ---- the products, by one thread, which also waits for what they need.  The entries were copied by other threads without
       // a fence of theirs, so the fence between their stores and the tensor core's reads stands here.
       auto scores = [&](uint32_t g) {
         const uint32_t st = g % C::kStages, use = g / C::kStages, sb = g & 1;
-        w.wait<kShort>(&sh.s_free[sb], ((g >> 1) & 1) ^ 1);
+        w.wait_alone<kShort>(&sh.s_free[sb], ((g >> 1) & 1) ^ 1);
 #pragma unroll 1
         for (int s = 0; s < C::kSlices; ++s) {
-          w.wait<kShort>(&sh.k_full[st][s], use & 1);
+          w.wait_alone<kShort>(&sh.k_full[st][s], use & 1);
           fence_async_smem();
           tc_fence_after();
-          if (w.live && elect_one()) {
+          if (w.live) {
             const uint64_t ka = smem_operand(k_at + st * C::kTile + s * kSlice8, 0);
             const uint64_t qb = smem_operand(q_at + s * kSlice8, 0);
 #pragma unroll
             for (int x = 0; x < 4; ++x)  // 32 channels, 32 bytes of a row
               tc_mma_8(tmem + sb * C::kSCol, ka + 2 * x, qb + 2 * x, mma_shape(128, 2 * kN, false, false), s > 0 || x > 0);
           }
-          __syncwarp();
         }
-        if (elect_one()) {
-          if (!kShared) tc_commit(smem_addr(&sh.k_free[st][0]));
-          tc_commit(smem_addr(&sh.s_full[sb]));
-        }
-        __syncwarp();
+        if (!kShared) tc_commit(smem_addr(&sh.k_free[st][0]));
+        tc_commit(smem_addr(&sh.s_full[sb]));
       };
       auto values = [&](uint32_t g, bool fresh) {
         const uint32_t st = g % C::kStages, use = g / C::kStages;
-        w.wait<kShort>(&sh.p_full, g & 1);
+        w.wait_alone<kShort>(&sh.p_full, g & 1);
         if (!kShared) {
-          for (int s = 0; s < C::kSlices; ++s) w.wait<kShort>(&sh.v_full[st][s], use & 1);
+          for (int s = 0; s < C::kSlices; ++s) w.wait_alone<kShort>(&sh.v_full[st][s], use & 1);
         }
         fence_async_smem();
         tc_fence_after();
-        if (elect_one()) {
 #pragma unroll
-          for (int b = 0; b < C::kSlices; ++b) {
-            if (w.live) {
-              const uint64_t va = smem_operand(v_at + st * C::kTile + b * kSlice8, 0);
+        for (int b = 0; b < C::kSlices; ++b) {
+          if (w.live) {
+            const uint64_t va = smem_operand(v_at + st * C::kTile + b * kSlice8, 0);
 #pragma unroll
-              for (int i = 0; i < 3; ++i) {
-                const uint64_t pb = smem_operand64(p_at + i * kTerm);
+            for (int i = 0; i < 3; ++i) {
+              const uint64_t pb = smem_operand64(p_at + i * kTerm);
 #pragma unroll
-                for (int x = 0; x < 4; ++x)  // 32 entries: 32 rows of 128 and of 64 bytes
-                  tc_mma_8(tmem + C::kOCol + b * kN, va + 256 * x, pb + 128 * x,
-                           mma_shape(128, kN, true, true) | kBIsE5m2, !fresh || i > 0 || x > 0);
-              }
+              for (int x = 0; x < 4; ++x)  // 32 entries: 32 rows of 128 and of 64 bytes
+                tc_mma_8(tmem + C::kOCol + b * kN, va + 256 * x, pb + 128 * x,
+                         mma_shape(128, kN, true, true) | kBIsE5m2, !fresh || i > 0 || x > 0);
             }
-            if (kShared) tc_commit(smem_addr(&sh.k_free[st][b]));
           }
-          if (!kShared) tc_commit(smem_addr(&sh.v_free[st]));
-          tc_commit(smem_addr(&sh.pv_done));
+          if (kShared) tc_commit(smem_addr(&sh.k_free[st][b]));
         }
-        __syncwarp();
+        if (!kShared) tc_commit(smem_addr(&sh.v_free[st]));
+        tc_commit(smem_addr(&sh.pv_done));
       };
-      w.wait<kShort>(&sh.q_full, items_before & 1);
+      w.wait_alone<kShort>(&sh.q_full, items_before & 1);
       // the second product runs a tile behind the first
       for (uint32_t j = 0; j < n_tiles; ++j) {
         scores(tiles_before + j);
@@ -592,6 +585,7 @@ __global__ __launch_bounds__((TcCfg<kD, kShared>::kThreads), 1) void q8_attn_tc_
       }
       if (n_tiles > 0) values(tiles_before + n_tiles - 1, n_tiles == 1);
     }
+    __syncwarp();
     tiles_before += n_tiles;
     ++items_before;
     __syncthreads();  // the next item's rows take the place of this one's
@@ -605,7 +599,7 @@ __global__ __launch_bounds__((TcCfg<kD, kShared>::kThreads), 1) void q8_attn_tc_
     if (!done) w.live = false;
     tmem_free(tmem, C::kCols);
   }
-  if (!w.live && lane == 0) status_or(a.d_status, CKV_STATUS_TIMEOUT);
+  if (!w.live) status_or(a.d_status, CKV_STATUS_TIMEOUT);
 }
 
 template <int kD, bool kShared>

@@ -19,9 +19,9 @@ constexpr uint32_t kSlice = kEntries * 128;  // bytes of 64 channels of a tile i
 struct Waiter {
   long long limit;
   bool live;
+  // one thread's wait
   template <bool kShort>
-  __device__ __forceinline__ void wait(uint64_t* barrier, uint32_t parity) {
-    if (!live) return;
+  __device__ __forceinline__ bool passed(uint64_t* barrier, uint32_t parity) {
     const uint32_t bar = smem_addr(barrier);
     bool done = kShort ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity);
     if (!done) {
@@ -30,7 +30,17 @@ struct Waiter {
         done = kShort ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity);
       } while (!done && clock64() - t0 <= limit);
     }
-    live = __all_sync(0xFFFFFFFFu, done);
+    return done;
+  }
+  // a warp's: its lanes decide together
+  template <bool kShort>
+  __device__ __forceinline__ void wait(uint64_t* barrier, uint32_t parity) {
+    if (live) live = __all_sync(0xFFFFFFFFu, passed<kShort>(barrier, parity));
+  }
+  // one thread's that acts alone
+  template <bool kShort>
+  __device__ __forceinline__ void wait_alone(uint64_t* barrier, uint32_t parity) {
+    if (live) live = passed<kShort>(barrier, parity);
   }
 };
 
@@ -92,7 +102,7 @@ struct GroupScales {
 };
 
 // The converting warps' work for one item.  C: kSlices slices of 64 channels, kStages stages, kLoads 16-byte loads of
-// a thread per slice, kUnits slices of a tile (K's, then V's), kAhead of them loaded ahead.
+// a thread per slice, kUnits slices of a tile (K's, then V's).
 template <typename C, bool kShort, typename Sh>
 __device__ __forceinline__ void convert_tiles(const AttnArgs& a, const Q8Item& item, Sh& sh, Waiter& w, int cw, uint32_t h,
                                               const int32_t* table, uint32_t n_tiles, uint32_t tiles_before,
@@ -104,12 +114,10 @@ __device__ __forceinline__ void convert_tiles(const AttnArgs& a, const Q8Item& i
   const uint32_t last = item.kv_end > 0 ? item.kv_end - 1 : 0;
   constexpr bool kShared = C::kLatent;
   constexpr int kD = 64 * C::kSlices;
-  constexpr int kPerFree = C::kSlices / C::kFree;  // slices that one barrier hands back
   const uint32_t tok = cw * 8 + (lane >> 2);  // load i: entry tok + i * (8 * kConvWarps)
   const uint32_t st0 = tok * 128 + (((2 * q) ^ (tok & 7)) << 4), st1 = tok * 128 + (((2 * q + 1) ^ (tok & 7)) << 4);
-  const uint8_t* src[C::kLoads];       // the K addresses of this tile's entries
-  const uint8_t* src_next[C::kLoads];  // and of the next one's
-  uint32_t here = 0, here_next = 0;    // bit i: load i's entry exists
+  const uint8_t* src[C::kLoads];  // the K addresses of a tile's entries
+  uint32_t here = 0;              // bit i: load i's entry exists
   bool bad = false;
   // Block numbers are asked for a tile before the addresses are made from them, at places that always exist, so
   // that no load here waits for another.
@@ -135,7 +143,7 @@ __device__ __forceinline__ void convert_tiles(const AttnArgs& a, const Q8Item& i
     return mask;
   };
   const ptrdiff_t v_off = kShared ? 0 : a.c.v - a.c.k;
-  uint4 buf[C::kAhead][C::kLoads];
+  uint4 buf[C::kUnits][C::kLoads];  // a tile ahead of what is stored
   auto load = [&](uint4(&d)[C::kLoads], int unit, const uint8_t* const(&o)[C::kLoads], uint32_t mask) {
     const ptrdiff_t at = unit < C::kSlices ? unit * 64 : v_off + (unit - C::kSlices) * 64;
 #pragma unroll
@@ -147,56 +155,47 @@ __device__ __forceinline__ void convert_tiles(const AttnArgs& a, const Q8Item& i
   here = locate(0, src);
   ask(1);
 #pragma unroll
-  for (int u = 0; u < C::kAhead; ++u) load(buf[u], u, src, here);
+  for (int u = 0; u < C::kUnits; ++u) load(buf[u], u, src, here);
   for (uint32_t j = 0; j < n_tiles; ++j) {
     const uint32_t g = tiles_before + j, st = g % C::kStages, use = g / C::kStages;
     const uint32_t e0 = item.kv_begin + j * kEntries;
     const bool edge = e0 + kEntries > vis_min;
-    if (cw == 0) groups.put(j);
-    here_next = locate(j + 1, src_next);
-    ask(j + 2);
-#pragma unroll 1
-    for (int u0 = 0; u0 < C::kUnits; u0 += C::kAhead) {
 #pragma unroll
-      for (int x = 0; x < C::kAhead; ++x) {
-        const int u = u0 + x;
-        const bool is_v = u >= C::kSlices;
-        const int s = is_v ? u - C::kSlices : u;
-        if (is_v) {
-          if (s == 0) w.template wait<kShort>(&sh.v_free[st], (use & 1) ^ 1);
-        } else if (s % kPerFree == 0) {
-          w.template wait<kShort>(&sh.k_free[st][s / kPerFree], (use & 1) ^ 1);
-        }
-        if ((is_v || kShared) && edge) {
+    for (int u = 0; u < C::kUnits; ++u) {
+      const bool is_v = u >= C::kSlices;
+      const int s = is_v ? u - C::kSlices : u;
+      if (s == 0) w.template wait<kShort>(is_v ? &sh.v_free[st] : &sh.k_free[st], (use & 1) ^ 1);
+      if ((is_v || kShared) && edge) {
 #pragma unroll
-          for (int i = 0; i < C::kLoads; ++i)
-            buf[x][i] = without_nans(buf[x][i], e0 + tok + i * (8 * C::kConvWarps),
-                                     kShared ? sh.nan : sh.nan + s * 64 + q * 16, kShared ? 0 : 1, &sh.any_nan);
-        }
-        const uint32_t dst = (is_v ? v_at : k_at) + (st * C::kSlices + s) * kSlice;
+        for (int i = 0; i < C::kLoads; ++i)
+          buf[u][i] = without_nans(buf[u][i], e0 + tok + i * (8 * C::kConvWarps),
+                                   kShared ? sh.nan : sh.nan + s * 64 + q * 16, kShared ? 0 : 1, &sh.any_nan);
+      }
+      const uint32_t dst = (is_v ? v_at : k_at) + (st * C::kSlices + s) * kSlice;
 #pragma unroll
-        for (int i = 0; i < C::kLoads; ++i) {
-          const uint4 y = buf[x][i];
-          asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(dst + st0 + i * (8 * C::kConvWarps) * 128),
-                       "r"(q8_lo_f16x2(y.x)), "r"(q8_hi_f16x2(y.x)), "r"(q8_lo_f16x2(y.y)), "r"(q8_hi_f16x2(y.y))
-                       : "memory");
-          asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(dst + st1 + i * (8 * C::kConvWarps) * 128),
-                       "r"(q8_lo_f16x2(y.z)), "r"(q8_hi_f16x2(y.z)), "r"(q8_lo_f16x2(y.w)), "r"(q8_hi_f16x2(y.w))
-                       : "memory");
-        }
+      for (int i = 0; i < C::kLoads; ++i) {
+        const uint4 y = buf[u][i];
+        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(dst + st0 + i * (8 * C::kConvWarps) * 128),
+                     "r"(q8_lo_f16x2(y.x)), "r"(q8_hi_f16x2(y.x)), "r"(q8_lo_f16x2(y.y)), "r"(q8_hi_f16x2(y.y))
+                     : "memory");
+        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(dst + st1 + i * (8 * C::kConvWarps) * 128),
+                     "r"(q8_lo_f16x2(y.z)), "r"(q8_hi_f16x2(y.z)), "r"(q8_lo_f16x2(y.w)), "r"(q8_hi_f16x2(y.w))
+                     : "memory");
+      }
+      if (u == 0) {
+        // The scales, and the next tile's addresses.  Here and not before the tile: what they were loaded for came before the
+        // entries just stored, so nothing waits for the entries of the units to come.
+        if (cw == 0) groups.put(j);
+        here = locate(j + 1, src);
+        ask(j + 2);
+      }
+      if (s == C::kSlices - 1) {
         fence_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_addr(is_v ? &sh.v_full[st][s] : &sh.k_full[st][s]));
-        // the slice that is kAhead units on, of this tile or the next
-        if (u0 + C::kAhead < C::kUnits)
-          load(buf[x], u + C::kAhead, src, here);
-        else
-          load(buf[x], x, src_next, here_next);
+        if (lane == 0) mbar_arrive(smem_addr(is_v ? &sh.v_full[st] : &sh.k_full[st]));
       }
+      load(buf[u], u, src, here);  // the next tile's
     }
-    here = here_next;
-#pragma unroll
-    for (int i = 0; i < C::kLoads; ++i) src[i] = src_next[i];
   }
   if (bad) status_or(a.d_status, CKV_STATUS_BAD_INDEX);
 }
