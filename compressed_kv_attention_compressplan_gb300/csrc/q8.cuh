@@ -319,6 +319,19 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+// A load made well before its use, and issued where it stands: a plain __ldg may be moved down to its first use to save
+// a register, and its latency with it.
+__device__ __forceinline__ int32_t ld_ahead(const int32_t* p) {
+  int32_t v;
+  asm volatile("ld.global.nc.s32 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ float ld_ahead(const float* p) {
+  float v;
+  asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(v) : "l"(p));
+  return v;
+}
+
 // A streamed 16-byte load, or zeros where `in` is false: predicated, so that nothing waits for it
 // before its first use (a branch around the load would, where the paths join).
 __device__ __forceinline__ uint4 ld_stream16_if(const void* p, bool in) {

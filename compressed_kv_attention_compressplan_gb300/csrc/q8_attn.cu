@@ -231,7 +231,7 @@ int q8_attn_geom(const Q8Cache& c, uint32_t batch, uint32_t num_q, uint32_t n_he
     g->rows = c.head_dim <= 128 ? 256 : 64;
     g->ctas = std::max<uint32_t>(1, static_cast<uint32_t>(sm_count()) / c.heads);
     g->grain = g->round = 128;
-    g->start_cost = c.head_dim >= 256 ? 384 : 256;  // what starting a tile takes, in entries' time
+    g->start_cost = c.head_dim >= 256 ? 384 : 768;  // what starting a tile takes, in entries' time
     g->min_quota = 256;
   } else {
     g->rows = 16;

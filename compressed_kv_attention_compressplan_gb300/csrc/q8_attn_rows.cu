@@ -29,7 +29,7 @@ struct RowsCfg {
   static constexpr int kStages = 2;
   static constexpr int kSoftWarps = 16;  // of each row tile: four for the first 64 entries, four for the others
   static constexpr int kConvWarps = 8;
-  static constexpr int kWarps = kSoftWarps + kConvWarps + 1;
+  static constexpr int kWarps = kSoftWarps + kConvWarps + 2;  // the scales' and the products'
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kLoads = kEntries / (8 * kConvWarps);
   static constexpr int kUnits = kSlices * (kShared ? 1 : 2);
@@ -48,8 +48,8 @@ template <int kD, bool kShared>
 struct alignas(16) RowsShared {
   using C = RowsCfg<kD, kShared>;
   uint64_t k_full[C::kStages], k_free[C::kStages], v_full[C::kStages], v_free[C::kStages];
-  uint64_t s_full[2], p_full[2], o_done, idle;
-  alignas(16) float f[4][8];  // see GroupScales
+  uint64_t q_full, s_full[2], p_full[2], o_done, idle;
+  alignas(16) float f[4][8];  // see scale_tiles
   alignas(16) float lv[4][8];
   alignas(16) float iv[4][8];
   float rf[C::kRows];
@@ -102,7 +102,7 @@ __global__ __launch_bounds__((RowsCfg<kD, kShared>::kThreads), 1) void q8_attn_r
   if (warp == C::kWarps - 1) tmem_alloc(smem_addr(&sh.tmem), C::kCols);
   if (tid == 0) {
     for (int s = 0; s < C::kStages; ++s) {
-      mbar_init(smem_addr(&sh.k_full[s]), C::kConvWarps);
+      mbar_init(smem_addr(&sh.k_full[s]), C::kConvWarps + 1);
       mbar_init(smem_addr(&sh.v_full[s]), C::kConvWarps);
       mbar_init(smem_addr(&sh.k_free[s]), 1);
       mbar_init(smem_addr(&sh.v_free[s]), 1);
@@ -111,6 +111,7 @@ __global__ __launch_bounds__((RowsCfg<kD, kShared>::kThreads), 1) void q8_attn_r
       mbar_init(smem_addr(&sh.s_full[t]), 1);
       mbar_init(smem_addr(&sh.p_full[t]), C::kSoftWarps / 2);
     }
+    mbar_init(smem_addr(&sh.q_full), C::kSoftWarps);
     mbar_init(smem_addr(&sh.o_done), 1);
     mbar_init(smem_addr(&sh.idle), 1);
     fence_mbar_init();
@@ -121,10 +122,12 @@ __global__ __launch_bounds__((RowsCfg<kD, kShared>::kThreads), 1) void q8_attn_r
   const uint32_t tmem = sh.tmem;
   Waiter w{static_cast<long long>(a.wait_ns) * 2, true};
   uint32_t tiles_before = 0;  // tiles of earlier items: the barriers' phases go on
-  uint32_t items_before = 0;  // earlier items that had tiles
+  uint32_t items_before = 0;  // earlier items
 
   for (uint32_t it = item0; it < item1; ++it) {
     const Q8Item item = items[it];
+    __syncthreads();  // the item before is done with what this one's takes the place of
+    tc_fence_after();
     if (!item_fits(item, a)) {
       if (tid == 0) status_or(a.d_status, CKV_STATUS_BAD_INDEX);
       continue;
@@ -136,62 +139,82 @@ __global__ __launch_bounds__((RowsCfg<kD, kShared>::kThreads), 1) void q8_attn_r
     const int tiles = rows > 128 ? 2 : 1;  // row tiles with rows
     const uint32_t vis_min = min(item.kv_end, static_cast<uint32_t>(q8_visible(item.kv_len, item.q_len - 1 - item.row0 / G,
                                                                              item.phase, a.ratio)));
-    // ---- the rows' query operand and scaling
-    constexpr int kPer = kD / 32, kBatch = 4;  // consecutive channels of a lane; rows whose loads are in flight together
-    for (int n0 = warp; n0 < tiles * 128; n0 += kBatch * C::kWarps) {
-      uint32_t x[kBatch][kPer / 2];
-#pragma unroll
-      for (int b = 0; b < kBatch; ++b) {
-        const uint32_t n = n0 + b * C::kWarps;
-        const bool in = n < rows;
-        const uint32_t rho = item.row0 + (in ? n : 0), i = rho / G, hg = rho % G;
-        const size_t row = static_cast<size_t>(item.q_start + i) * a.n_heads + h * G + hg;
-        const uint32_t* p = reinterpret_cast<const uint32_t*>(a.q + row * kD + lane * kPer);
-#pragma unroll
-        for (int e = 0; e < kPer / 2; ++e) x[b][e] = in ? __ldg(p + e) : 0u;
-      }
-#pragma unroll
-      for (int b = 0; b < kBatch; ++b) {
-        const int n = n0 + b * C::kWarps;
-        if (n >= tiles * 128) break;
-        float m = 0.0f;
-#pragma unroll
-        for (int e = 0; e < kPer / 2; ++e) m = fmaxf(m, fmaxf(fabsf(bf16lo(x[b][e])), fabsf(bf16hi(x[b][e]))));
-#pragma unroll
-        for (int s = 16; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, s));
-        const int ex = min(126, 14 - (static_cast<int>(__float_as_uint(m) >> 23) - 127));
-        const float up = pow2f(ex);
-        const int r = n & 127;
-#pragma unroll
-        for (int e = 0; e < kPer / 2; ++e) {
-          const uint32_t c = lane * kPer + 2 * e;
-          sts_u32(q_at + ((n >> 7) * C::kSlices + (c >> 6)) * kSlice + r * 128 + ((((c & 63) >> 3) ^ (r & 7)) << 4) + (c & 7) * 2,
-                  pack_f16x2(bf16lo(x[b][e]) * up, bf16hi(x[b][e]) * up));
-        }
-        if (lane == 0) sh.rf[n] = pow2f(-ex);
-      }
-    }
-    for (int c = tid; c < (kShared ? 1 : kD); c += C::kThreads) sh.nan[c] = 0x7FFFFFFF;
-    if (tid == 0) sh.any_nan = 0;
-    fence_async_smem();
-    __syncthreads();
-
     if (conv) {
+      for (int c = tid - 32 * C::kSoftWarps; c < (kShared ? 1 : kD); c += 32 * C::kConvWarps) sh.nan[c] = 0x7FFFFFFF;
+      if (tid == 32 * C::kSoftWarps) sh.any_nan = 0;
+      asm volatile("bar.sync 9, %0;" ::"n"(32 * C::kConvWarps) : "memory");
       convert_tiles<C, kShort>(a, item, sh, w, warp - C::kSoftWarps, h, table, n_tiles, tiles_before, vis_min, k_at, v_at);
     } else if (soft) {
       const int rt = warp >> 3, half = warp >> 2 & 1, quarter = warp & 3, pair = 1 + rt * 4 + quarter;
+      // ---- the rows' query operand and scaling: eight channels of a row to a lane, the loads of several rows in flight together
+      {
+        constexpr int kLanes = kD / 8, kPer = 32 / kLanes;             // lanes of a row, rows of a warp at a time
+        constexpr int kTimes = C::kRows / (kPer * C::kSoftWarps), kBatch = kTimes < 4 ? kTimes : 4;
+        const int sub = lane / kLanes, cl = lane % kLanes;
+#pragma unroll 1
+        for (int t0 = 0; t0 < kTimes; t0 += kBatch) {
+          uint4 x[kBatch];
+#pragma unroll
+          for (int b = 0; b < kBatch; ++b) {
+            const uint32_t n = ((t0 + b) * C::kSoftWarps + warp) * kPer + sub;
+            const bool in = n < rows;
+            const uint32_t rho = item.row0 + (in ? n : 0), i = rho / G, hg = rho % G;
+            const size_t row = static_cast<size_t>(item.q_start + i) * a.n_heads + h * G + hg;
+            x[b] = ld_stream16_if(a.q + row * kD + cl * 8, in);
+          }
+#pragma unroll
+          for (int b = 0; b < kBatch; ++b) {
+            const uint32_t n = ((t0 + b) * C::kSoftWarps + warp) * kPer + sub, r = n & 127;
+            const uint32_t y[4] = {x[b].x, x[b].y, x[b].z, x[b].w};
+            float m = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) m = fmaxf(m, fmaxf(fabsf(bf16lo(y[e])), fabsf(bf16hi(y[e]))));
+#pragma unroll
+            for (int s = kLanes / 2; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, s));
+            const int ex = min(126, 14 - (static_cast<int>(__float_as_uint(m) >> 23) - 127));
+            const float up = pow2f(ex);
+            uint32_t z[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) z[e] = pack_f16x2(bf16lo(y[e]) * up, bf16hi(y[e]) * up);
+            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(q_at + ((n >> 7) * C::kSlices + (cl >> 3)) * kSlice + r * 128 +
+                                                                        (((cl & 7) ^ (r & 7)) << 4)),
+                         "r"(z[0]), "r"(z[1]), "r"(z[2]), "r"(z[3])
+                         : "memory");
+            if (cl == 0) sh.rf[n] = pow2f(-ex);
+          }
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&sh.q_full));
+        asm volatile("bar.sync 10, %0;" ::"n"(32 * C::kSoftWarps) : "memory");
+      }
       if (rt < tiles) {
         const uint32_t n = rt * 128 + quarter * 32 + lane;  // row of the item
         const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
         // this half's scores; its weights take the first 32 of these columns
         const uint32_t s_at = tmem + lanes + rt * 128 + half * 64, o_at = tmem + lanes + C::kOCol + rt * kD;
         const bool in = n < rows;
-        const uint32_t rho = item.row0 + (in ? n : 0), i = rho / G, hg = rho % G;
-        const int64_t see = q8_visible(item.kv_len, item.q_len - 1 - i, item.phase, a.ratio);
-        const uint32_t vis = in ? static_cast<uint32_t>(min(static_cast<int64_t>(item.kv_end), see)) : item.kv_end;
+        const int see = static_cast<int>(q8_visible(item.kv_len, item.q_len - 1 - (item.row0 + (in ? n : 0)) / G, item.phase, a.ratio));
+        const uint32_t vis = in ? min(item.kv_end, static_cast<uint32_t>(see)) : item.kv_end;
         const float rf = sh.rf[n];
         // never 0, which would make NaN of a hidden score's -infinity; a factor this small makes 0 of any other
         auto factor = [&](float f) { return fmaxf(f * rf, 1.2e-38f); };
+        // 16 scores' weights, and their sum over the value scale
+        auto weights = [&](const float(&x)[16], float f, float b, float iv, uint32_t(&p)[8], float& sum_to) {
+          const F2 f2 = f2_pack(f, f), b2 = f2_pack(b, b);
+          F2 sum = f2_pack(0.0f, 0.0f);
+#pragma unroll
+          for (int y = 0; y < 16; y += 2) {
+            float t0, t1;
+            f2_unpack(f2_fma(f2_pack(x[y], x[y + 1]), f2, b2), t0, t1);
+            const float w0 = ex2(t0), w1 = ex2(t1);
+            sum = f2_add(sum, f2_pack(w0, w1));
+            p[y >> 1] = pack_f16x2(w0, w1);
+          }
+          float s0, s1;
+          f2_unpack(sum, s0, s1);
+          sum_to = fmaf(s0 + s1, iv, sum_to);
+        };
         float m = 0.0f, l = 0.0f;
         bool set = false;  // the row's reference has been set: by its first entry, wherever that is; later ones raise it
         for (uint32_t j = 0; j < n_tiles; ++j) {
@@ -204,25 +227,27 @@ __global__ __launch_bounds__((RowsCfg<kD, kShared>::kThreads), 1) void q8_attn_r
           const float* iv_at = sh.iv[slot] + half * 4;
           w.wait<kShort>(&sh.s_full[rt], g & 1);
           tc_fence_after();
-          // the largest exponent: a run's scores share their positive factor, so the largest of each run will do
-          float top = -INFINITY;
+          // The weights under the reference as it stands, kept in registers, and the largest exponent: a run's scores share
+          // their positive factor, so the largest of each run will do.
+          float top = -INFINITY, more = l;
+          uint32_t p[4][8];
 #pragma unroll
-          for (int c = 0; c < 64; c += 32) {
-            float x[32];
-            tmem_load32(s_at + c, x);
+          for (int c = 0; c < 4; ++c) {
+            float x[16];
+            tmem_load16(s_at + 16 * c, x);
+            const float f = factor(f_at[c]), lv = lv_at[c];
+            float y = -INFINITY;
             if (edge) {
 #pragma unroll
-              for (int y = 0; y < 32; ++y) x[y] = c + y < hidden ? x[y] : -INFINITY;
+              for (int z = 0; z < 16; ++z) x[z] = 16 * c + z < hidden ? x[z] : -INFINITY;
             }
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-              float y = x[16 * r];
-#pragma unroll
-              for (int z = 1; z < 16; ++z) y = fmaxf(y, x[16 * r + z]);
-              top = fmaxf(top, y == -INFINITY ? -INFINITY : fmaf(y, factor(f_at[(c >> 4) + r]), lv_at[(c >> 4) + r]));
-            }
+            for (int z = 0; z < 16; ++z) y = fmaxf(y, x[z]);
+            top = fmaxf(top, y == -INFINITY ? -INFINITY : fmaf(y, f, lv));
+            weights(x, f, lv - m, iv_at[c], p[c], more);
           }
           if (pair_any(pair, set ? top > m + 14.0f : top > -INFINITY)) {
+            // a reference rises (the first entry that a row sees sets it): once a row and now and then
             sh.both[half][n] = top;
             pair_sync(pair);
             top = fmaxf(top, sh.both[half ^ 1][n]);
@@ -242,33 +267,22 @@ __global__ __launch_bounds__((RowsCfg<kD, kShared>::kThreads), 1) void q8_attn_r
                 tmem_store16(o_at + c, o);
               }
             }
+            more = l;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              float x[16];
+              tmem_load16(s_at + 16 * c, x);
+              if (edge) {
+#pragma unroll
+                for (int z = 0; z < 16; ++z) x[z] = 16 * c + z < hidden ? x[z] : -INFINITY;
+              }
+              weights(x, factor(f_at[c]), lv_at[c] - m, iv_at[c], p[c], more);
+            }
             pair_sync(pair);  // both have read what the other told
           }
+          l = more;
 #pragma unroll
-          for (int c = 0; c < 64; c += 16) {
-            float x[16];
-            tmem_load16(s_at + c, x);
-            if (edge) {
-#pragma unroll
-              for (int y = 0; y < 16; ++y) x[y] = c + y < hidden ? x[y] : -INFINITY;
-            }
-            uint32_t p[8];
-            const float f = factor(f_at[c >> 4]), b = lv_at[c >> 4] - m;
-            const F2 f2 = f2_pack(f, f), b2 = f2_pack(b, b);
-            F2 sum = f2_pack(0.0f, 0.0f);
-#pragma unroll
-            for (int y = 0; y < 16; y += 2) {
-              float t0, t1;
-              f2_unpack(f2_fma(f2_pack(x[y], x[y + 1]), f2, b2), t0, t1);
-              const float w0 = ex2(t0), w1 = ex2(t1);
-              sum = f2_add(sum, f2_pack(w0, w1));
-              p[y >> 1] = pack_f16x2(w0, w1);
-            }
-            float s0, s1;
-            f2_unpack(sum, s0, s1);
-            l = fmaf(s0 + s1, iv_at[c >> 4], l);
-            tmem_put8(s_at + (c >> 1), p);  // over scores that are in registers or done with
-          }
+          for (int c = 0; c < 4; ++c) tmem_put8(s_at + 8 * c, p[c]);  // over scores that are done with
           tmem_store_wait();
           tc_fence_before();
           __syncwarp();
@@ -278,7 +292,10 @@ __global__ __launch_bounds__((RowsCfg<kD, kShared>::kThreads), 1) void q8_attn_r
         sh.both[half][n] = l;
         pair_sync(pair);
         l = sh.both[0][n] + sh.both[1][n];
-        const size_t out_row = static_cast<size_t>(item.q_start + i) * a.n_heads + h * G + hg;
+        uint32_t again = n;  // (the place is worked out here and not kept over the tiles)
+        asm volatile("" : "+r"(again));
+        const uint32_t rho = item.row0 + (in ? again : 0), i = rho / G, hg = rho % G;
+        const unsigned long long out_row = static_cast<unsigned long long>(item.q_start + i) * a.n_heads + h * G + hg;
         const size_t part_row = (static_cast<size_t>(item.part + static_cast<int>(item.chunk)) * H + h) * C::kRows + n;
         const float inv = l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l);
         if (in && half == 0) {
@@ -287,39 +304,56 @@ __global__ __launch_bounds__((RowsCfg<kD, kShared>::kThreads), 1) void q8_attn_r
           else if (a.lse != nullptr)
             a.lse[out_row] = l == 0.0f ? -INFINITY : (m + __log2f(l)) * 0.69314718055994530942f;
         }
-        if (n_tiles > 0) w.wait<kShort>(&sh.o_done, items_before & 1);
+        w.wait<kShort>(&sh.o_done, items_before & 1);
         tc_fence_after();
-        const int any_nan = sh.any_nan;
+        const bool any_nan = n_tiles > 0 && sh.any_nan != 0;
+        // 32 channels at a time through shared memory (the operands are done with), so that a store takes whole lines: 16 bytes a
+        // lane of 32 rows took 8 k cycles of an item
+        const uint32_t stage = base + warp * 4096, row_sw = lane & 7;
 #pragma unroll 1
-        for (int c = half * (kD / 2); c < (half + 1) * (kD / 2); c += 16) {
-          float o[16];
-          if (n_tiles > 0) {
-            tmem_load16(o_at + c, o);
-          } else {
+        for (int c0 = half * (kD / 2); c0 < (half + 1) * (kD / 2); c0 += 32) {
+#pragma unroll 1
+          for (int c = 0; c < 32; c += 16) {
+            float o[16];
+            if (n_tiles > 0) {
+              tmem_load16(o_at + c0 + c, o);
+            } else {
 #pragma unroll
-            for (int y = 0; y < 16; ++y) o[y] = 0.0f;
+              for (int y = 0; y < 16; ++y) o[y] = 0.0f;
+            }
+            if (any_nan) {
+#pragma unroll
+              for (int y = 0; y < 16; ++y)
+                if (sh.nan[kShared ? 0 : c0 + c + y] < see) o[y] = __int_as_float(0x7FFFFFFF);
+            }
+            const float by = item.part >= 0 ? 1.0f : inv;
+#pragma unroll
+            for (int y = 0; y < 16; y += 4)
+              asm volatile("st.shared.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(stage + lane * 128 + ((((c + y) >> 2) ^ row_sw) << 4)),
+                           "f"(o[y] * by), "f"(o[y + 1] * by), "f"(o[y + 2] * by), "f"(o[y + 3] * by)
+                           : "memory");
           }
-          if (!in) continue;
-          if (any_nan) {
-#pragma unroll
-            for (int y = 0; y < 16; ++y)
-              if (sh.nan[kShared ? 0 : c + y] < see) o[y] = __int_as_float(0x7FFFFFFF);
-          }
-#pragma unroll
-          for (int y = 0; y < 16; y += 8) {
-            float v[8];
-#pragma unroll
-            for (int z = 0; z < 8; ++z) v[z] = item.part >= 0 ? o[y + z] : o[y + z] * inv;
+          __syncwarp();
+#pragma unroll 2
+          for (int r0 = 0; r0 < 32; r0 += 4) {
+            const int r = r0 + (lane >> 3);
+            const uint4 v = lds16(stage + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
+            const size_t to = (item.part >= 0 ? part_row - lane + r : __shfl_sync(0xFFFFFFFFu, out_row, r)) * kD + c0 + (lane & 7) * 4;
+            if (n - lane + r >= rows) continue;
             if (item.part >= 0)
-              store_row_chunk<float, 8>(a.part_o + part_row * kD + c + y, v);
+              *reinterpret_cast<uint4*>(a.part_o + to) = v;
             else if (a.out_f32)
-              store_row_chunk<float, 8>(static_cast<float*>(a.out) + out_row * kD + c + y, v);
+              *reinterpret_cast<uint4*>(static_cast<float*>(a.out) + to) = v;
             else
-              store_row_chunk<__nv_bfloat16, 8>(static_cast<__nv_bfloat16*>(a.out) + out_row * kD + c + y, v);
+              *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + to) =
+                  make_uint2(pack_bf16x2(__uint_as_float(v.x), __uint_as_float(v.y)), pack_bf16x2(__uint_as_float(v.z), __uint_as_float(v.w)));
           }
+          __syncwarp();
         }
         tc_fence_before();
       }
+    } else if (warp == C::kSoftWarps + C::kConvWarps) {
+      scale_tiles<C, kShort>(a, item, sh, w, h, table, n_tiles, tiles_before);
     } else if (elect_one()) {
       // ---- the products, by one thread, which also waits for what they need.  Products run in the order of issue, so a tile's scores
       // overwrite the weights that the product before them has read.
@@ -341,6 +375,7 @@ __global__ __launch_bounds__((RowsCfg<kD, kShared>::kThreads), 1) void q8_attn_r
       };
       if (n_tiles > 0) {
         uint32_t st = tiles_before % C::kStages;
+        w.wait_alone<kShort>(&sh.q_full, items_before & 1);
         w.wait_alone<kShort>(&sh.k_full[st], (tiles_before / C::kStages) & 1);
         tc_fence_after();
         for (int rt = 0; rt < tiles; ++rt) scores(rt, st);
@@ -368,8 +403,8 @@ __global__ __launch_bounds__((RowsCfg<kD, kShared>::kThreads), 1) void q8_attn_r
           if (more && !kShared) tc_commit(smem_addr(&sh.k_free[next]));
           st = next;
         }
-        tc_commit(smem_addr(&sh.o_done));
       }
+      tc_commit(smem_addr(&sh.o_done));
     }
     __syncwarp();
     // A row tile that was skipped has no phases of its own: both tiles' barriers go on together
@@ -378,10 +413,11 @@ __global__ __launch_bounds__((RowsCfg<kD, kShared>::kThreads), 1) void q8_attn_r
       if (soft && warp >= C::kSoftWarps / 2 && lane == 0) mbar_arrive(smem_addr(&sh.p_full[1]));
     }
     tiles_before += n_tiles;
-    items_before += n_tiles > 0;
-    __syncthreads();  // the next item's rows take the place of this one's
-    tc_fence_after();
+    ++items_before;
   }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
   if (warp == C::kWarps - 1) {
     // every product is done before its memory is given back
     if (elect_one()) tc_commit(smem_addr(&sh.idle));

@@ -60,46 +60,44 @@ static __device__ __noinline__ uint4 without_nans(uint4 x, int e, int* nan, int 
 }
 
 // The scales of a tile's eight runs of 16 entries (a run lies in one block), for kernels whose threads see all
-// entries of a tile: lane r < 8 of one converting warp keeps run r's block number two tiles ahead and its scales one
-// ahead, and puts {scale log2(e) k_scale, log2(v_scale), 1 / v_scale} where the softmax reads them.  A run that
-// does not exist gets log2 = -infinity, i.e. no weight.  Four tiles' worth are kept: converting is never three tiles
-// ahead of the softmax.
-template <typename Sh>
-struct GroupScales {
-  const AttnArgs& a;
-  const Q8Item& item;
-  Sh& sh;
-  const int32_t* table;
-  uint32_t run, h, tiles_before, last, t_shift;
+// entries of a tile, by a warp of its own: {scale log2(e) k_scale, log2(v_scale), 1 / v_scale} where the softmax reads
+// them.  Lane r % 8 has run r, its block number two tiles ahead and its scales one ahead.  A run that does not
+// exist gets log2 = -infinity, i.e. no weight.  The warp goes with the converting ones, so it is never three tiles ahead of the
+// softmax, and four tiles' worth are kept.
+template <typename C, bool kShort, typename Sh>
+__device__ __forceinline__ void scale_tiles(const AttnArgs& a, const Q8Item& item, Sh& sh, Waiter& w, uint32_t h,
+                                            const int32_t* table, uint32_t n_tiles, uint32_t tiles_before) {
+  const int lane = threadIdx.x & 31, run = lane & 7;
+  const uint32_t t_shift = __ffs(a.c.block_tokens) - 1, last = item.kv_end > 0 ? item.kv_end - 1 : 0;
+  const float* v_scale = a.c.v != nullptr ? a.c.v_scale : a.c.k_scale;
   int32_t blk;
   float ks, vs;
   bool ok;
-  __device__ __forceinline__ GroupScales(const AttnArgs& args, const Q8Item& it, Sh& s, int lane, uint32_t head,
-                                         const int32_t* t, uint32_t before, uint32_t last_entry, uint32_t shift)
-      : a(args), item(it), sh(s), table(t), run(lane & 7), h(head), tiles_before(before), last(last_entry), t_shift(shift) {}
-  __device__ __forceinline__ void ask(uint32_t tile) {
-    blk = __ldg(table + (min(item.kv_begin + tile * kEntries + run * 16, last) >> t_shift));
-  }
-  __device__ __forceinline__ void load() {
+  auto ask = [&](uint32_t tile) { blk = ld_ahead(table + (min(item.kv_begin + tile * kEntries + run * 16, last) >> t_shift)); };
+  auto load = [&]() {
     ok = static_cast<uint32_t>(blk) < a.c.num_blocks;
     const size_t at = static_cast<size_t>(ok ? blk : 0) * a.c.heads + h;
-    ks = __ldg(a.c.k_scale + at);
-    vs = __ldg((a.c.v != nullptr ? a.c.v_scale : a.c.k_scale) + at);
-  }
-  __device__ __forceinline__ void start() {
-    ask(0);
+    ks = ld_ahead(a.c.k_scale + at);
+    vs = ld_ahead(v_scale + at);
+  };
+  ask(0);
+  load();
+  ask(1);
+  for (uint32_t j = 0; j < n_tiles; ++j) {
+    const uint32_t g = tiles_before + j, st = g % C::kStages, use = g / C::kStages, slot = g & 3;
+    const float f = ok ? ks * a.scale_log2 : 1.0f, lv = ok ? __log2f(vs) : -INFINITY, iv = ok ? __fdiv_rn(1.0f, vs) : 0.0f;
     load();
-    ask(1);
+    ask(j + 2);
+    w.template wait<kShort>(&sh.k_free[st], (use & 1) ^ 1);
+    if (lane < 8) {
+      sh.f[slot][run] = f;
+      sh.lv[slot][run] = lv;
+      sh.iv[slot][run] = iv;
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_addr(&sh.k_full[st]));
   }
-  __device__ __forceinline__ void put(uint32_t tile) {  // all lanes: a run has four copies, which agree
-    const uint32_t slot = (tiles_before + tile) & 3;
-    sh.f[slot][run] = ok ? ks * a.scale_log2 : 1.0f;
-    sh.lv[slot][run] = ok ? __log2f(vs) : -INFINITY;
-    sh.iv[slot][run] = ok ? __fdiv_rn(1.0f, vs) : 0.0f;
-    load();
-    ask(tile + 2);
-  }
-};
+}
 
 // The converting warps' work for one item.  C: kSlices slices of 64 channels, kStages stages, kLoads 16-byte loads of
 // a thread per slice, kUnits slices of a tile (K's, then V's).
@@ -126,7 +124,7 @@ __device__ __forceinline__ void convert_tiles(const AttnArgs& a, const Q8Item& i
 #pragma unroll
     for (int i = 0; i < C::kLoads; ++i) {
       const uint32_t e = item.kv_begin + tile * kEntries + tok + i * (8 * C::kConvWarps);
-      blk[i] = __ldg(table + (min(e, last) >> t_shift));
+      blk[i] = ld_ahead(table + (min(e, last) >> t_shift));
     }
   };
   auto locate = [&](uint32_t tile, const uint8_t*(&o)[C::kLoads]) -> uint32_t {
@@ -149,8 +147,6 @@ __device__ __forceinline__ void convert_tiles(const AttnArgs& a, const Q8Item& i
 #pragma unroll
     for (int i = 0; i < C::kLoads; ++i) d[i] = ld_stream16_if(o[i] + at, mask >> i & 1);
   };
-  GroupScales<Sh> groups(a, item, sh, lane, h, table, tiles_before, last, t_shift);
-  if (cw == 0) groups.start();
   ask(0);
   here = locate(0, src);
   ask(1);
@@ -183,9 +179,7 @@ __device__ __forceinline__ void convert_tiles(const AttnArgs& a, const Q8Item& i
                      : "memory");
       }
       if (u == 0) {
-        // The scales, and the next tile's addresses.  Here and not before the tile: what they were loaded for came before the
-        // entries just stored, so nothing waits for the entries of the units to come.
-        if (cw == 0) groups.put(j);
+        // the next tile's addresses, from block numbers that were asked for before the entries just stored
         here = locate(j + 1, src);
         ask(j + 2);
       }
