@@ -20,7 +20,7 @@
 // The weights go through shared memory as they stand: an entry's row of 64 of them is the
 // swizzled row that the second product reads.
 //
-// Roles.  Eight warps copy entries into the operands' swizzled layout, 128 channels at a time, as
+// Roles.  Four warps copy entries into the operands' swizzled layout, 128 channels at a time, as
 // the second product hands them back; one thread issues the products; groups of four warps
 // take 16 rows each through the softmax.
 //
@@ -45,7 +45,7 @@ struct TcCfg {
   static constexpr int kFree = kShared ? kSlices : 1;  // barriers that hand a K stage back
   static constexpr int kGroups = kRows / 16;  // softmax groups of four warps
   static constexpr int kSoftWarps = 4 * kGroups;
-  static constexpr int kCopyWarps = 8;
+  static constexpr int kCopyWarps = 4;  // four more leave a thread 72 registers, which spill into memory that has next to no L1
   static constexpr int kWarps = kSoftWarps + kCopyWarps + 1;
   static constexpr int kThreads = 32 * kWarps;
   static constexpr uint32_t kTile = kSlices * kSlice8;
@@ -180,13 +180,13 @@ __global__ __launch_bounds__((TcCfg<kD, kShared>::kThreads), 1) void q8_attn_tc_
     if (copy) {
       // ---- entries into the operands, 128 channels (a slice) at a time: lane l takes 16-byte chunk l % 8 of four entries
       // at once.  A chunk arrives at its barrier when it has landed.
-      constexpr int kSteps = kEntries / (C::kCopyWarps * 4);
+      constexpr int kStride = C::kCopyWarps * 4, kSteps = kEntries / kStride;
       const int cw = warp - C::kSoftWarps, cc = lane & 7;
-      const uint32_t entry0 = cw * 4 + (lane >> 3);  // entry of step i: entry0 + 32 i
+      const uint32_t entry0 = cw * 4 + (lane >> 3);  // entry of step i: entry0 + kStride i
       bool bad = false;
       for (int c = tid - 32 * C::kSoftWarps; c < (kShared ? 1 : kD); c += 32 * C::kCopyWarps) sh.nan[c] = 0x7FFFFFFF;
       if (cw == 0 && lane == 0) sh.any_nan = 0;
-      asm volatile("bar.sync 15, 256;" ::: "memory");
+      asm volatile("bar.sync 15, %0;" ::"n"(32 * C::kCopyWarps) : "memory");
       // lane r < 8 keeps the block number of run r (16 entries), asked for a tile ahead
       auto ask = [&](uint32_t tile) {
         return __ldg(table + (min(item.kv_begin + tile * kEntries + (lane & 7) * 16, last) >> t_shift));
@@ -216,14 +216,14 @@ __global__ __launch_bounds__((TcCfg<kD, kShared>::kThreads), 1) void q8_attn_tc_
         uint32_t in = 0;  // bit i: step i's entry exists
 #pragma unroll
         for (int i = 0; i < kSteps; ++i) {
-          const uint32_t t = entry0 + 32 * i, e = e0 + t;
+          const uint32_t t = entry0 + kStride * i, e = e0 + t;
           const int32_t b = __shfl_sync(0xFFFFFFFFu, now, t >> 4);
           const bool valid = static_cast<uint32_t>(b) < a.c.num_blocks;
           off[i] = (((static_cast<size_t>(valid ? b : 0) * H + h) << t_shift) + (e & (T - 1))) * kD + cc * 16;
           in |= (valid && e < item.kv_end ? 1u : 0u) << i;
           bad |= !valid && e < item.kv_end;
         }
-        const uint32_t put = entry0 * 128 + ((cc ^ (entry0 & 7)) << 4);  // 32 entries on, the swizzle is the same
+        const uint32_t put = entry0 * 128 + ((cc ^ (entry0 & 7)) << 4);  // kStride entries on, the swizzle is the same
 #pragma unroll 1
         for (int u = 0; u < C::kSlices * (kShared ? 1 : 2); ++u) {
           const bool side = u >= C::kSlices;
@@ -237,17 +237,17 @@ __global__ __launch_bounds__((TcCfg<kD, kShared>::kThreads), 1) void q8_attn_tc_
             w.wait<kShort>(&sh.k_free[st][kShared ? s : 0], (use & 1) ^ 1);
           }
 #pragma unroll
-          for (int i = 0; i < kSteps; ++i) cp_async16(to + i * 4096, pool + off[i], in >> i & 1 ? 16u : 0u);  // others: zeros
+          for (int i = 0; i < kSteps; ++i) cp_async16(to + i * (kStride * 128), pool + off[i], in >> i & 1 ? 16u : 0u);  // others: zeros
           if ((side || kShared) && edge) {
             // some rows do not see some of these entries: their values' NaNs are taken out (see the split kernel)
             cp_async_commit();
             cp_async_wait<0>();
 #pragma unroll 1
             for (int i = 0; i < kSteps; ++i) {
-              const uint32_t at = to + i * 4096;
+              const uint32_t at = to + i * (kStride * 128);
               const uint4 x = lds16(at);
               if (q8_nan_bytes(x.x) | q8_nan_bytes(x.y) | q8_nan_bytes(x.z) | q8_nan_bytes(x.w)) {
-                const uint4 y = without_nans(x, e0 + entry0 + 32 * i, kShared ? sh.nan : sh.nan + s * 128 + cc * 16,
+                const uint4 y = without_nans(x, e0 + entry0 + kStride * i, kShared ? sh.nan : sh.nan + s * 128 + cc * 16,
                                              kShared ? 0 : 1, &sh.any_nan);
                 asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(y.x), "r"(y.y), "r"(y.z), "r"(y.w)
                              : "memory");
