@@ -40,10 +40,12 @@ __device__ __forceinline__ void put_weight(const WeighArgs& a, int32_t block, ui
   *dst = a.decay == 0.0f ? w : fmaf(a.decay, *dst, w);
 }
 
-// Units (runs of unit_entries entries) before every request that has queries, and its first ragged query; by a block of kThreads.
+// Units (runs of unit_entries entries) before every request that has queries, and its first ragged query; by a block of
+// kThreads.  s_meta, where it is wanted: {entries, queries, phase, rid} of those requests.
 template <int kThreads>
 __device__ __forceinline__ uint32_t scan_requests(const WeighArgs& a, uint32_t unit_entries, uint32_t* s_unit, uint32_t* s_q,
-                                                  uint32_t* s_scan, unsigned long long* s_scan64) {
+                                                  uint32_t* s_scan, unsigned long long* s_scan64,
+                                                  uint4* s_meta = nullptr) {
   uint32_t units = 0;
   unsigned long long queries = 0;
   for (uint32_t b0 = 0; b0 < a.batch; b0 += kThreads) {
@@ -57,6 +59,9 @@ __device__ __forceinline__ uint32_t scan_requests(const WeighArgs& a, uint32_t u
       const bool ok = len_ok && sl >= el && sl <= 0x7FFFFFFF && kl >= 0 && kl <= 0x7FFFFFF0 &&
                       kl <= static_cast<int64_t>(a.stride) * a.c.block_tokens && r >= 0 && r < a.num_reqs;
       if (!ok && blockIdx.x == 0) status_or(a.d_status, CKV_STATUS_BAD_LENGTH);
+      if (ok && s_meta != nullptr)
+        s_meta[b] = make_uint4(static_cast<uint32_t>(kl), static_cast<uint32_t>(el), a.ratio - 1 - static_cast<uint32_t>(sl) % a.ratio,
+                               static_cast<uint32_t>(r));
       n = ok && el > 0 ? static_cast<uint32_t>((kl + unit_entries - 1) / unit_entries) : 0;
     }
     unsigned long long ql_sum;

@@ -25,8 +25,10 @@ template <int kD>
 struct WtCfg {
   static constexpr int kSlices = kD / 64;
   static constexpr int kExpWarps = 16;  // four groups of four; a group takes 32 rows of a chunk
-  static constexpr int kLoadWarps = 8;
-  static constexpr int kWarps = kExpWarps + kLoadWarps + 1;
+  static constexpr int kKeyWarps = 4, kQueryWarps = 4;
+  static constexpr int kWarps = kExpWarps + kKeyWarps + kQueryWarps + 1;
+  static constexpr int kLoads = kEntries / (8 * kKeyWarps);  // entries of a key thread
+  static_assert(kChunk == 32 * kQueryWarps, "a row to a lane");
   static constexpr int kThreads = 32 * kWarps;
   static constexpr uint32_t kTileBytes = kSlices * kSlice;  // 128 rows of kD bf16 values
   static constexpr int kQStages = 4;
@@ -44,6 +46,7 @@ struct alignas(16) WtShared {
   float part[3][128];
   uint32_t unit[CKV_MAX_BATCH];
   uint32_t first_q[CKV_MAX_BATCH];
+  uint4 meta[CKV_MAX_BATCH];
   unsigned long long scan64[WtCfg<kD>::kWarps + 1];
   uint32_t scan[WtCfg<kD>::kWarps + 1];
   uint32_t tmem;
@@ -61,20 +64,20 @@ __global__ __launch_bounds__(WtCfg<kD>::kThreads, 1) void q8_weigh_tc_kernel(con
   pdl_release();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t T = a.c.block_tokens, t_shift = __ffs(T) - 1, H = a.c.heads, G = a.group;
-  const uint32_t units = scan_requests<C::kThreads>(a, kEntries, sh.unit, sh.first_q, sh.scan, sh.scan64);
+  const uint32_t units = scan_requests<C::kThreads>(a, kEntries, sh.unit, sh.first_q, sh.scan, sh.scan64, sh.meta);
   if (blockIdx.x >= units) return;
   const uint32_t base = (smem_addr(raw) + 1023) & ~1023u;
   const uint32_t k_at = base, q_at = base + 2 * C::kTileBytes;
   if (warp == C::kWarps - 1) tmem_alloc(smem_addr(&sh.tmem), C::kCols);
   if (tid == 0) {
     for (int s = 0; s < 2; ++s) {
-      mbar_init(smem_addr(&sh.k_full[s]), C::kLoadWarps);
+      mbar_init(smem_addr(&sh.k_full[s]), C::kKeyWarps);
       mbar_init(smem_addr(&sh.k_free[s]), 1);
       mbar_init(smem_addr(&sh.s_full[s]), 1);
       mbar_init(smem_addr(&sh.s_free[s]), C::kExpWarps);
     }
     for (int s = 0; s < C::kQStages; ++s) {
-      mbar_init(smem_addr(&sh.q_full[s]), 33 * C::kLoadWarps);  // every thread's copies, and a warp's lse and counts
+      mbar_init(smem_addr(&sh.q_full[s]), 33 * C::kQueryWarps);  // every thread's copies, and a warp's lse and counts
       mbar_init(smem_addr(&sh.q_free[s]), C::kExpWarps);
     }
     mbar_init(smem_addr(&sh.idle), 1);
@@ -88,56 +91,57 @@ __global__ __launch_bounds__(WtCfg<kD>::kThreads, 1) void q8_weigh_tc_kernel(con
 
   // every role walks the same (unit, head, chunk) sequence; kc and qc count keys' tiles and chunks
   uint32_t kc = 0, qc = 0;
-  for (uint32_t u = blockIdx.x; u < units; u += gridDim.x) {
-    const uint32_t b = last_not_above(sh.unit, a.batch, u);
-    const uint32_t kv_len = static_cast<uint32_t>(a.kv_lens[b]);
-    const uint32_t q_len = static_cast<uint32_t>(a.extend_lens[b]);
-    const uint32_t phase = a.ratio - 1 - static_cast<uint32_t>(a.seq_lens[b]) % a.ratio;
-    const uint32_t rows = q_len * G, chunks = (rows + kChunk - 1) / kChunk;
-    const uint32_t e0 = (u - sh.unit[b]) * kEntries;
-    const int32_t* table = a.table + static_cast<size_t>(a.rid[b]) * a.stride;
-    if (warp >= C::kExpWarps && warp < C::kExpWarps + C::kLoadWarps) {
-      // ---- keys into bf16, queries as they are
-      const int lw = warp - C::kExpWarps, q = lane & 3;
-      const uint32_t tok = lw * 8 + (lane >> 2);  // and tok + 64
-      const uint8_t* src[2];
-      bool ok[2];
+  if (warp >= C::kExpWarps && warp < C::kExpWarps + C::kKeyWarps) {
+    // ---- keys into bf16, a head ahead of the products; the next unit's block numbers are asked for a unit ahead
+    const int lw = warp - C::kExpWarps, q = lane & 3;
+    constexpr int kStep = 8 * C::kKeyWarps;
+    const uint32_t tok = lw * 8 + (lane >> 2), sw = tok & 7;  // entries tok, tok + kStep, ...
+    int32_t blk[C::kLoads];
+    uint32_t kv_len = 0, e0 = 0;
+    auto ask = [&](uint32_t u) {
+      kv_len = 0;
+      if (u >= units) return;
+      const uint32_t b = last_not_above(sh.unit, a.batch, u);
+      const uint4 meta = sh.meta[b];
+      kv_len = meta.x;
+      e0 = (u - sh.unit[b]) * kEntries;
+      const int32_t* table = a.table + static_cast<size_t>(meta.w) * a.stride;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const uint32_t e = e0 + tok + 64 * i;
-        const int32_t blk = __ldg(table + (min(e, kv_len - 1) >> t_shift));
-        const bool valid = static_cast<uint32_t>(blk) < a.c.num_blocks;
-        ok[i] = valid && e < kv_len;
-        src[i] = a.c.k + ((static_cast<size_t>(valid ? blk : 0) * H << t_shift) + (e & (T - 1))) * kD + q * 16;
+      for (int i = 0; i < C::kLoads; ++i) blk[i] = ld_ahead(table + (min(e0 + tok + kStep * i, kv_len - 1) >> t_shift));
+    };
+    const uint8_t* src[C::kLoads];
+    uint32_t ok = 0;
+    auto open = [&]() {
+      ok = 0;
+#pragma unroll
+      for (int i = 0; i < C::kLoads; ++i) {
+        const uint32_t e = e0 + tok + kStep * i;
+        const bool in = e < kv_len && static_cast<uint32_t>(blk[i]) < a.c.num_blocks;
+        src[i] = a.c.k + ((static_cast<size_t>(in ? blk[i] : 0) * H << t_shift) + (e & (T - 1))) * kD + q * 16;
+        ok |= (in ? 1u : 0u) << i;
       }
-      uint4 buf[C::kSlices][2];
-      auto load = [&](uint32_t h) {
+    };
+    uint4 buf[C::kSlices][C::kLoads];
+    auto load = [&](uint32_t h) {
 #pragma unroll
-        for (int s = 0; s < C::kSlices; ++s) {
+      for (int s = 0; s < C::kSlices; ++s) {
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
-            buf[s][i] = ld_stream16_if(src[i] + (static_cast<size_t>(h) << t_shift) * kD + s * 64, ok[i] && h < H);
-        }
-      };
-      load(0);
-      // lane l keeps row l % 16 of this warp's 16 of a chunk: its place (a division, so once a chunk), its query and its
-      // lse, which is asked for a chunk ahead
-      auto place = [&](uint32_t h, uint32_t c, uint32_t* query) {
-        const uint32_t rho = min(c * kChunk + lw * 16 + (lane & 15), rows - 1);
-        *query = rho / G;
-        return static_cast<unsigned long long>(sh.first_q[b] + *query) * a.n_heads + h * G + (rho - *query * G);
-      };
-      uint32_t query_next;
-      unsigned long long row_next = place(0, 0, &query_next);
-      float lse_next = __ldg(a.lse + row_next);
+        for (int i = 0; i < C::kLoads; ++i)
+          buf[s][i] = ld_stream16_if(src[i] + (static_cast<size_t>(h) << t_shift) * kD + s * 64, ok >> i & 1);
+      }
+    };
+    ask(blockIdx.x);
+    open();
+    load(0);
+    for (uint32_t u = blockIdx.x; u < units; u += gridDim.x) {
       for (uint32_t h = 0; h < H; ++h, ++kc) {
         const uint32_t ks = kc & 1;
         w.wait<kShort>(&sh.k_free[ks], ((kc >> 1) & 1) ^ 1);
 #pragma unroll
         for (int s = 0; s < C::kSlices; ++s) {
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const uint32_t at = k_at + ks * C::kTileBytes + s * kSlice + (tok + 64 * i) * 128, sw = tok & 7;
+          for (int i = 0; i < C::kLoads; ++i) {
+            const uint32_t at = k_at + ks * C::kTileBytes + s * kSlice + (tok + kStep * i) * 128;
             const uint32_t x[4] = {buf[s][i].x, buf[s][i].y, buf[s][i].z, buf[s][i].w};
 #pragma unroll
             for (int y = 0; y < 2; ++y)
@@ -150,53 +154,98 @@ __global__ __launch_bounds__(WtCfg<kD>::kThreads, 1) void q8_weigh_tc_kernel(con
         fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_addr(&sh.k_full[ks]));
-        load(h + 1);
+        if (h == 0) ask(u + gridDim.x);
+        if (h + 1 < H) {
+          load(h + 1);
+        } else {
+          open();
+          load(0);  // the next unit's
+        }
+      }
+    }
+  } else if (warp >= C::kExpWarps && warp < C::kWarps - 1) {
+    // ---- queries as they are, four chunks ahead.  Lane l keeps row l of this warp's 32 of a chunk: its place (a division, so
+    // once a chunk), its query and its lse, which is asked for a chunk ahead.
+    const int lw = warp - C::kExpWarps - C::kKeyWarps;
+    uint32_t query_next = 0;
+    unsigned long long row_next = 0;
+    auto place = [&](uint32_t b, uint32_t h, uint32_t c) {
+      const uint32_t rho = min(c * kChunk + lw * 32 + lane, sh.meta[b].y * G - 1);
+      query_next = rho / G;
+      row_next = static_cast<unsigned long long>(sh.first_q[b] + query_next) * a.n_heads + h * G + (rho - query_next * G);
+    };
+    uint32_t b = last_not_above(sh.unit, a.batch, blockIdx.x);
+    place(b, 0, 0);
+    float lse_next = ld_ahead(a.lse + row_next);
+    for (uint32_t u = blockIdx.x; u < units; u += gridDim.x) {
+      const uint4 meta = sh.meta[b];
+      const uint32_t rows = meta.y * G, chunks = (rows + kChunk - 1) / kChunk;
+      const uint32_t b_next = u + gridDim.x < units ? last_not_above(sh.unit, a.batch, u + gridDim.x) : b;
+      for (uint32_t h = 0; h < H; ++h) {
         for (uint32_t c = 0; c < chunks; ++c, ++qc) {
           const uint32_t qs = qc % C::kQStages, query = query_next;
           const unsigned long long row = row_next;
           const float lse = lse_next;
-          row_next = c + 1 < chunks ? place(h, c + 1, &query_next) : place(min(h + 1, H - 1), 0, &query_next);
-          lse_next = __ldg(a.lse + row_next);
+          if (c + 1 < chunks)
+            place(b, h, c + 1);
+          else if (h + 1 < H)
+            place(b, h + 1, 0);
+          else
+            place(b_next, 0, 0);
+          lse_next = ld_ahead(a.lse + row_next);
           w.wait<kShort>(&sh.q_free[qs], ((qc / C::kQStages) & 1) ^ 1);
-          // this warp's 16 rows, 16 bytes a lane at a time; they arrive at the barrier when they have landed
+          // this warp's 32 rows, 16 bytes a lane at a time; they arrive at the barrier when they have landed
           constexpr int kRowChunks = kD / 8;  // 16-byte chunks of a row
 #pragma unroll
-          for (int x = 0; x < kRowChunks / 2; ++x) {
-            const uint32_t i = x * 32 + lane, r = i / kRowChunks, n = lw * 16 + r, cc = i % kRowChunks;
+          for (int x = 0; x < kRowChunks; ++x) {
+            const uint32_t i = x * 32 + lane, r = i / kRowChunks, n = lw * 32 + r, cc = i % kRowChunks;
             const unsigned long long from = __shfl_sync(0xFFFFFFFFu, row, r);
             cp_async16(q_at + qs * C::kTileBytes + (cc >> 3) * kSlice + n * 128 + (((cc & 7) ^ (n & 7)) << 4),
                        a.q + from * kD + cc * 8, 16u);
           }
           cp_async_arrive(smem_addr(&sh.q_full[qs]));
-          if (lane < 16) {
-            const uint32_t n = lw * 16 + lane, at = c * kChunk + n;
-            const int64_t see = at < rows ? q8_visible(kv_len, q_len - 1 - query, phase, a.ratio) : 0;
-            sh.vis[qs][n] = static_cast<int>(see);
-            // a row that saw nothing weighs nothing, nor does one past the last
-            sh.off[qs][n] = at >= rows || lse == -INFINITY ? -INFINITY : lse * -kLog2e;
-          }
+          const uint32_t n = lw * 32 + lane, at = c * kChunk + n;
+          const int64_t see = at < rows ? q8_visible(meta.x, meta.y - 1 - query, meta.z, a.ratio) : 0;
+          sh.vis[qs][n] = static_cast<int>(see);
+          // a row that saw nothing weighs nothing, nor does one past the last
+          sh.off[qs][n] = at >= rows || lse == -INFINITY ? -INFINITY : lse * -kLog2e;
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_addr(&sh.q_full[qs]));
         }
       }
-      // none of these copies may land after the CTA is gone
-      cp_async_commit();
-      cp_async_wait<0>();
-    } else if (warp < C::kExpWarps) {
-      const int group = warp >> 2, quarter = warp & 3, entry = quarter * 32 + lane;
-      const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
-      const uint32_t e = e0 + entry;
-      const int32_t blk = __ldg(table + (min(e, kv_len - 1) >> t_shift));
+      b = b_next;
+    }
+    // none of these copies may land after the CTA is gone
+    cp_async_commit();
+    cp_async_wait<0>();
+  } else if (warp < C::kExpWarps) {
+    const int group = warp >> 2, quarter = warp & 3, entry = quarter * 32 + lane;
+    const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
+    auto block_of = [&](uint32_t u) -> int32_t {
+      if (u >= units) return 0;
+      const uint32_t b = last_not_above(sh.unit, a.batch, u);
+      const uint4 meta = sh.meta[b];
+      return ld_ahead(a.table + static_cast<size_t>(meta.w) * a.stride +
+                      (min((u - sh.unit[b]) * kEntries + entry, meta.x - 1) >> t_shift));
+    };
+    int32_t blk_next = block_of(blockIdx.x);
+    for (uint32_t u = blockIdx.x; u < units; u += gridDim.x) {
+      const uint32_t b = last_not_above(sh.unit, a.batch, u);
+      const uint4 meta = sh.meta[b];
+      const uint32_t chunks = (meta.y * G + kChunk - 1) / kChunk;
+      const uint32_t kv_len = meta.x, e0 = (u - sh.unit[b]) * kEntries, e = e0 + entry;
+      const int32_t blk = blk_next;
+      blk_next = block_of(u + gridDim.x);
       const bool valid = static_cast<uint32_t>(blk) < a.c.num_blocks;
       if (!valid && e < kv_len && group == 0) status_or(a.d_status, CKV_STATUS_BAD_INDEX);
       const float* scales = a.c.k_scale + static_cast<size_t>(valid ? blk : 0) * H;
-      float next = __ldg(scales);
+      float next = ld_ahead(scales);
       F2 sum = f2_pack(0.0f, 0.0f);
       // the request's first row sees least: where it sees the whole tile, all do
-      const bool edge = static_cast<int64_t>(e0) + kEntries > q8_visible(kv_len, q_len - 1, phase, a.ratio);
+      const bool edge = static_cast<int64_t>(e0) + kEntries > q8_visible(kv_len, meta.y - 1, meta.z, a.ratio);
       for (uint32_t h = 0; h < H; ++h) {
         const float f = next * a.scale_log2;
-        next = __ldg(scales + min(h + 1, H - 1));
+        next = ld_ahead(scales + min(h + 1, H - 1));
         const F2 f2 = f2_pack(f, f);
         for (uint32_t c = 0; c < chunks; ++c, ++qc) {
           const uint32_t sb = qc & 1, qs = qc % C::kQStages;
@@ -236,7 +285,12 @@ __global__ __launch_bounds__(WtCfg<kD>::kThreads, 1) void q8_weigh_tc_kernel(con
       if (group == 0 && e < kv_len && valid)
         put_weight(a, blk, e & (T - 1), ((s0 + s1) + sh.part[0][entry]) + (sh.part[1][entry] + sh.part[2][entry]));
       asm volatile("bar.sync 1, 512;" ::: "memory");
-    } else {
+    }
+  } else {
+    for (uint32_t u = blockIdx.x; u < units; u += gridDim.x) {
+      const uint32_t b = last_not_above(sh.unit, a.batch, u);
+      const uint4 meta = sh.meta[b];
+      const uint32_t chunks = (meta.y * G + kChunk - 1) / kChunk;
       for (uint32_t h = 0; h < H; ++h, ++kc) {
         const uint32_t ks = kc & 1;
         w.wait<kShort>(&sh.k_full[ks], (kc >> 1) & 1);
