@@ -20,6 +20,11 @@
 // bf16 input down to 2^-28 of that value.  Products accumulate in fp32; the
 // weights' rounding to fp16 (2^-11 relative) is the one rounding that costs
 // anything, and is below the bf16 output's.
+//
+// Bound of the split kernel.  The entries' bytes: a warp streams its tiles of 16 entries through a ring of its own, with as many
+// stages as the CTAs that fit an SM leave, so that nothing but the copies is waited for.  64 requests of up to 16384 entries, eight kv
+// heads, 1081 MB: 180 us, 6.0 TB/s or 88 % of the measured copy rate; two requests of 140001 entries, 145 MB: 35 us, 4.1 TB/s, with
+// the first copies and the join of the parts (10 us) no longer small.
 #include <algorithm>
 
 #include "async_copy.cuh"
@@ -43,8 +48,8 @@ struct AttnPlanArgs {
   uint32_t* d_status;
 };
 
-// One CTA: requests are scanned once, then tiles in strips of kPlanThreads.  256 threads where the batch lets them:
-// the block-wide scans are what the kernel's time is made of.
+// One CTA: requests are scanned once, then tiles in strips of kPlanThreads.  Latency bounds it: the lengths' loads, three block-wide
+// scans and the items' stores, 7.4 us for 200 requests with 256 threads and 7.9 with 1024.
 template <int kPlanThreads>
 __global__ __launch_bounds__(kPlanThreads) void plan_q8_attn_kernel(const AttnPlanArgs a) {
   __shared__ uint32_t s_rid[kPlanThreads], s_qs[kPlanThreads], s_ql[kPlanThreads], s_kv[kPlanThreads],
@@ -80,8 +85,12 @@ __global__ __launch_bounds__(kPlanThreads) void plan_q8_attn_kernel(const AttnPl
     }
   }
   unsigned long long total_q, total_tiles, qs, tile0;
-  const unsigned long long tiles = ok ? (static_cast<uint32_t>(q_len) * G + M - 1) / M : 0;
+  unsigned long long tiles = ok ? (static_cast<uint32_t>(q_len) * G + M - 1) / M : 0;
   block_exclusive2<kPlanThreads>(q_len, tiles, &qs, &tile0, &total_q, &total_tiles, s_scan);
+  if (total_q > a.num_q) {  // requests whose queries do not all exist are dropped, and the others' tiles counted again
+    if (qs + q_len > a.num_q) tiles = 0;
+    tile0 = block_exclusive<kPlanThreads>(tiles, &total_tiles, s_scan[0]);
+  }
   if (t < a.batch) {
     s_rid[t] = rid;
     s_qs[t] = static_cast<uint32_t>(qs);
@@ -91,9 +100,8 @@ __global__ __launch_bounds__(kPlanThreads) void plan_q8_attn_kernel(const AttnPl
     s_tile[t] = static_cast<uint32_t>(tile0);
   }
   __syncthreads();
-  // more queries than num_q have no places, and more tiles than the plan's buffer holds: then nothing is planned
-  const uint32_t nt = total_q > a.num_q ? 0 : static_cast<uint32_t>(total_tiles);
 
+  const uint32_t nt = static_cast<uint32_t>(total_tiles);
   // a tile's entries: those its last query sees
   auto tile_of = [&](uint32_t tile, uint32_t* b) -> uint32_t {
     *b = last_not_above(s_tile, a.batch, tile);
@@ -225,13 +233,19 @@ int q8_attn_geom(const Q8Cache& c, uint32_t batch, uint32_t num_q, uint32_t n_he
   if (n_heads == 0 || n_heads % c.heads != 0 || n_heads / c.heads > CKV_Q8_MAX_GROUP) return CKV_ERR_SIZE;
   g->group = n_heads / c.heads;
   if (static_cast<uint64_t>(num_q) * g->group > 0x7FFFFFFFull) return CKV_ERR_SIZE;  // row numbers are 32-bit
-  // The split kernel's tiles are 16 rows; the tensor-core kernels' are 256, or 64 from 256 channels on.
-  g->tc = batch > 0 && static_cast<uint64_t>(num_q) * g->group >= 48ull * batch;
+  // The split kernel's tiles are 16 rows, and it reads a request's entries once for each; the tensor-core kernels' are 256, or 64
+  // from 256 channels on, at nearly the same cost for a few rows as for all.  Where they cross, by rows of a request and kv head (us,
+  // split kernel / tensor cores, 32 to 64 requests of 4096 entries): 64 channels 105 / 112 at 64 and 149 / 113 at 96; 128 channels
+  // 155 / 187 at 48 and 203 / 189 at 64; 256 channels 46 / 64 at 16 and 67 / 65 at 32; 512 channels 64 / 72 at 16 and 107 / 75 at 32.
+  const uint64_t most = c.head_dim == 64 ? 64 : c.head_dim == 128 ? 48 : 16;
+  g->tc = static_cast<uint64_t>(num_q) * g->group > most * batch && batch > 0;
   if (g->tc) {
     g->rows = c.head_dim <= 128 ? 256 : 64;
     g->ctas = std::max<uint32_t>(1, static_cast<uint32_t>(sm_count()) / c.heads);
     g->grain = g->round = 128;
-    g->start_cost = c.head_dim >= 256 ? 384 : 768;  // what starting a tile takes, in entries' time
+    // What starting a tile takes, in entries' time: an item takes 17 k cycles beside 4.5 k for 128 entries (27 k beside 5 k from 256
+    // channels on).  A chunk of three requests, one of them short: 823 us at 384, 773 at 512, 771 at 768, 774 at 896.
+    g->start_cost = c.head_dim >= 256 ? 384 : 768;
     g->min_quota = 256;
   } else {
     g->rows = 16;
@@ -590,7 +604,8 @@ __global__ __launch_bounds__(kAttnThreads, (Cfg<kDw, kNp, kShared>::kPerSm)) voi
 // Joins a split tile's parts, in their order.  Where the parts are few a warp takes a
 // row, so that a row is two trips to memory and no barrier, and a CTA eight rows; else
 // the whole CTA takes a row: work number y + x * (rows / 8) is row x of the eight y,
-// and only tiles of many parts have work beyond x = 0.
+// and only tiles of many parts have work beyond x = 0.  Bound: the parts' bytes (128 KB a part of 64 rows and 512 channels, 40 MB in
+// 12 us), or two trips to memory (8 us from launch to end).
 constexpr int kCombineThreads = 256;
 constexpr int kCombineRows = kCombineThreads / 32;
 constexpr uint32_t kFewParts = 16;

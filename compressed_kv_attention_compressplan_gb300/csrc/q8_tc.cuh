@@ -14,8 +14,9 @@ constexpr uint32_t kSlice = kEntries * 128;  // bytes of 64 channels of a tile i
 
 // A wait that, once it has run out, lets the rest of the loop run without waiting: every barrier is
 // still reached, the kernel ends, and the status says so.  The limit is counted in SM clocks, two to a
-// nanosecond (about the highest rate, so a slower clock only waits longer): the roles hand tiles to one another all the
-// time, and a read of the global timer in a wait that misses its first probe costs more than the wait.
+// nanosecond (about the highest rate, so a slower clock only waits longer).  A wait that is over before it
+// starts still takes some 130 cycles, and one that hands over between two warps as many (262 for a round trip), so a tile's
+// waits are few.
 struct Waiter {
   long long limit;
   bool live;

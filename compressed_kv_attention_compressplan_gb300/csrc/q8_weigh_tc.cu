@@ -6,11 +6,14 @@
 // so an entry is a lane of tensor memory, a thread owns it, and its weight
 //     sum over rows of 2^(scale log2(e) k_scale S - lse log2(e))
 // is one register: no lane or warp exchanges anything until the unit's four column
-// groups are added at its end.  Keys become bf16 (exact), the queries are bf16 and are
-// copied as they are, so a chunk costs its copy, its products and 2.5 instructions
-// for each weight.
+// groups are added at its end.  Keys become bf16 (exact) and queries are bf16 already.
 //
-// Bound.  128 channels: a chunk's products take 512 cycles, its exponentials 512.
+// Roles.  Sixteen warps for the exponentials, four that convert keys, four that copy queries four chunks ahead (row by row:
+// a chunk's rows lie in as many pieces as it has queries), one for the products.
+//
+// Bound.  128 channels: a chunk's products take 512 cycles, its exponentials 512.  Measured: 18 MB of keys and 8.9 GF
+// in 29 us, 10 k cycles for a unit of four chunks: the queries' copies and the handing over of one unit to the next; keys and queries
+// by the same eight warps took 31.6 us.
 #include <algorithm>
 
 #include "q8_tc.cuh"

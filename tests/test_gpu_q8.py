@@ -82,7 +82,7 @@ def attn_bounds(D, lens_max, out, lse, mag, big, flat, vmax, out_bf16, eight_bit
     """Worst cases: D products and lens_max weighted values summed in fp32 with truncated additions (2^-23 each), the
     exponent's argument a few roundings of its size (2^-22), the weights rounded to fp16 (2^-11), weights under
     2^-31 of the largest dropped (of values up to twice vmax), bf16 output (2^-8).  eight_bit: from 256 channels and
-    48 rows on the fp16 weights are three e5m2 terms (each leaves 2^-3 of what it is given: 2^-9), dropped under
+    more than 16 rows on the fp16 weights are three e5m2 terms (each leaves 2^-3 of what it is given: 2^-9), dropped under
     2^-17 / 2^6 = 2^-23, and a query value is off by up to 2^-17 of its row's largest."""
     eps = big * (D + 8) * 2.0 ** -23 + (big * 1.5 + 60) * 2.0 ** -22 + (flat * 2.0 ** -17 if eight_bit else 0)
     e = eps[..., None]
@@ -94,7 +94,7 @@ def attn_bounds(D, lens_max, out, lse, mag, big, flat, vmax, out_bf16, eight_bit
 
 
 def eight_bit(w, q_lens, heads):
-    return w.D >= 256 and int(np.sum(q_lens)) * (heads // w.H) >= 48 * len(q_lens)
+    return w.D >= 256 and int(np.sum(q_lens)) * (heads // w.H) > 16 * len(q_lens)
 
 
 def run_attn(w, q, seq, q_lens, heads, ratio, out_dtype=torch.bfloat16, scale=None, lens=None, **kw):
@@ -255,6 +255,16 @@ ATTN = [  # lens, q_lens, heads, H, D, T, latent, ratio
     ([700, 150], [64, 30], 6, 2, 512, 32, False, 1),
     ([1000], [1], 96, 1, 512, 128, True, 1),
     ([390], [300], 4, 4, 128, 16, False, 1),
+    # rows on both sides of where another kernel takes over
+    ([200], [16], 4, 1, 64, 32, False, 1),
+    ([200], [13], 5, 1, 64, 32, False, 1),
+    ([170, 30], [12, 12], 8, 2, 128, 16, False, 1),
+    ([170], [7], 7, 1, 128, 16, True, 1),
+    ([100], [4], 4, 1, 256, 64, True, 1),
+    ([100], [17], 1, 1, 256, 64, False, 1),
+    ([333], [1], 17, 1, 512, 64, True, 2),
+    ([300, 40], [13, 13], 5, 1, 512, 64, True, 1),
+    ([300], [13], 5, 1, 256, 32, False, 1),
 ]
 
 
@@ -468,6 +478,25 @@ def test_rows_after_the_last_request_are_left_alone():
     torch.cuda.synchronize()
     assert int(st[0]) == ckv.STATUS_BAD_TOTAL
     assert (out[2] == 7.0).all() and (lse[2] == 7.0).all() and not (out[:2] == 7.0).any()
+
+
+def test_requests_whose_queries_do_not_all_exist_are_dropped():
+    w = World(15, [40, 30, 20], 1, 128, 16, False)
+    cache, st = w.cache(), status()
+    q = w.queries([5], 2)
+    out, lse = torch.full((5, 2, 128), 7.0, device=DEV), torch.full((5, 2), 7.0, device=DEV)
+    args = i64(w.rid), i64([40, 30, 20]), i64([2, 4, 1]), i64([40, 30, 20])
+    plan = ckv.plan_q8_attn(cache, 2, 1, *args, 5, status=st)
+    ckv.q8_attn(cache, q.to(DEV), plan, i32(w.table), 0.1, out=out, lse=lse, status=st)
+    torch.cuda.synchronize()
+    assert int(st[0]) == ckv.STATUS_BAD_TOTAL
+    assert (out[2:] == 7.0).all() and (lse[2:] == 7.0).all() and not (out[:2] == 7.0).any()
+    weights, st = torch.zeros(w.blocks, 16, device=DEV), status()
+    ckv.q8_weigh(cache, q.to(DEV), lse, weights, 1, *args, i32(w.table), 0.1, status=st)
+    torch.cuda.synchronize()
+    assert int(st[0]) == ckv.STATUS_BAD_TOTAL
+    got = weights.cpu().numpy()
+    assert got[w.table[w.rid[0], :3]].sum() > 0 and got[w.table[w.rid[1], :2]].sum() == 0 == got[w.table[w.rid[2], :2]].sum()
 
 
 def test_offsets_past_32_bits():
