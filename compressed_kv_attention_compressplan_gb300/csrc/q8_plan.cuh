@@ -55,8 +55,7 @@ struct Q8Geom {
   uint32_t group;      // query heads of a kv head
   uint32_t ctas;       // CTAs of a kv head
   uint32_t min_quota;  // entries
-  uint32_t round;      // the quota is a multiple of this, itself one of grain
-  uint32_t grain;      // entries are counted in these: 16, or the tensor-core kernel's tile
+  uint32_t grain;      // entries are counted in these, and the quota is a multiple: 16, or the tensor-core kernels' tile
   uint32_t cap_items;
   uint32_t cap_parts;
   uint64_t off_first, off_split, off_items, bytes;
