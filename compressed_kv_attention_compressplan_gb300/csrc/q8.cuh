@@ -387,4 +387,28 @@ __device__ __forceinline__ void tile_scores(uint32_t st, int g, int q, const uin
   }
 }
 
+// The same with the entries as the product's rows: score e is that of entry (e >> 1) * 8 + g and column 2q + (e & 1).
+template <int kDw>
+__device__ __forceinline__ void tile_scores_t(uint32_t st, int g, int q, const uint32_t (&qf)[kDw / 16][4], float (&s)[4]) {
+  s[0] = s[1] = s[2] = s[3] = 0.0f;
+#pragma unroll
+  for (int j = 0; j < kDw / 64; ++j) {
+    const int cc = lane_chunk<kDw>(j, q);
+    const uint4 lo = lds16(st + tile_off<kDw>(g, cc)), hi = lds16(st + tile_off<kDw>(8 + g, cc));
+    const uint32_t x[4] = {lo.x, lo.y, lo.z, lo.w}, y[4] = {hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+    for (int z = 0; z < 4; ++z) {
+      const uint32_t kf[4] = {q8_lo_f16x2(x[z]), q8_lo_f16x2(y[z]), q8_hi_f16x2(x[z]), q8_hi_f16x2(y[z])};
+      mma_f16(s, kf, qf[j * 4 + z][0], qf[j * 4 + z][2]);
+    }
+  }
+}
+
+// 8 x 8 values of 16 bits, two to a lane, transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+
 }  // namespace ckv

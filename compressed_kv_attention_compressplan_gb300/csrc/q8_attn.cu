@@ -208,23 +208,27 @@ constexpr int kAttnWarps = 4;
 constexpr int kAttnThreads = 32 * kAttnWarps;
 constexpr int kTile = 16;  // entries a warp takes at a time
 
-// kDw channels of a warp's part of a row, kNp warps to a row (512 channels: 2).
-template <int kDw, int kNp, bool kShared>
+// kDw channels of a warp's part of a row, kNp warps to a row (512 channels: 2); kRows query rows of a tile, 8 or 16.
+template <int kDw, int kNp, bool kShared, int kRows>
 struct Cfg {
   static constexpr int kD = kDw * kNp;
   static constexpr int kGroups = kAttnWarps / kNp;  // warp groups, each with tiles of its own
   static constexpr int kTileBytes = kTile * kDw * (kShared ? 1 : 2);
   static constexpr int kStageBytes = kTileBytes + 16;  // and the tile's two scales
-  // as many stages as let kPerSm CTAs share an SM's 227 KB
-  static constexpr int kPerSm = kDw == 64 ? 4 : kDw == 128 ? 3 : 2;
-  static constexpr int kStages = kDw == 64 ? (kShared ? 8 : 6) : kDw == 128 ? (kShared ? 7 : 4) : (kShared ? 5 : 3);
+  // As many stages as let kPerSm CTAs share an SM's 227 KB.  Eight rows and 128 channels, 64 requests of 8000 entries (1.05 GB): 174 us with two
+  // CTAs of six stages, 182 with three of four, 188 to 194 with four of three, 280 with one of twelve.
+  static constexpr int kPerSm = kDw == 64 ? 4 : kDw == 128 ? (kRows == 8 ? 2 : 3) : 2;
+  static constexpr int kStages = kDw == 64                ? (kShared ? 8 : 6)
+                                 : kDw == 128 && kRows == 8 ? (kShared ? 9 : 6)
+                                 : kDw == 128               ? (kShared ? 7 : 4)
+                                                            : (kShared ? 5 : 3);
   static constexpr int kRingBytes = kAttnWarps * kStages * kStageBytes;
   static constexpr int kMergeStride = kD + 4;  // floats
-  static constexpr int kMergeBytes = kGroups * 16 * kMergeStride * 4;
+  static constexpr int kMergeBytes = kGroups * kRows * kMergeStride * 4;
   static constexpr int kSmem = kRingBytes > kMergeBytes ? kRingBytes : kMergeBytes;
 };
 
-int per_sm_of(uint32_t head_dim) { return head_dim == 64 ? 4 : head_dim == 128 ? 3 : 2; }
+int per_sm_of(uint32_t head_dim, uint32_t rows) { return head_dim == 64 ? 4 : head_dim == 128 && rows == 16 ? 3 : 2; }
 
 }  // namespace
 
@@ -233,7 +237,7 @@ int q8_attn_geom(const Q8Cache& c, uint32_t batch, uint32_t num_q, uint32_t n_he
   if (n_heads == 0 || n_heads % c.heads != 0 || n_heads / c.heads > CKV_Q8_MAX_GROUP) return CKV_ERR_SIZE;
   g->group = n_heads / c.heads;
   if (static_cast<uint64_t>(num_q) * g->group > 0x7FFFFFFFull) return CKV_ERR_SIZE;  // row numbers are 32-bit
-  // The split kernel's tiles are 16 rows, and it reads a request's entries once for each; the tensor-core kernels' are 256, or 64
+  // The split kernel's tiles are 8 or 16 rows, and it reads a request's entries once for each; the tensor-core kernels' are 256, or 64
   // from 256 channels on, at nearly the same cost for a few rows as for all.  Where they cross, by rows of a request and kv head (us,
   // split kernel / tensor cores, 32 to 64 requests of 4096 entries): 64 channels 105 / 112 at 64 and 149 / 113 at 96; 128 channels
   // 155 / 187 at 48 and 203 / 189 at 64; 256 channels 46 / 64 at 16 and 67 / 65 at 32; 512 channels 64 / 72 at 16 and 107 / 75 at 32.
@@ -248,8 +252,8 @@ int q8_attn_geom(const Q8Cache& c, uint32_t batch, uint32_t num_q, uint32_t n_he
     g->start_cost = c.head_dim >= 256 ? 384 : 768;
     g->min_quota = 128;  // one request of 2048 latent entries: 20.6 us with one tile a CTA, 29.9 with two, 36 with four
   } else {
-    g->rows = 16;
-    g->ctas = std::max<uint32_t>(1, static_cast<uint32_t>(sm_count()) * per_sm_of(c.head_dim) / c.heads);
+    g->rows = static_cast<uint64_t>(num_q) * g->group <= 8ull * batch ? 8 : 16;
+    g->ctas = std::max<uint32_t>(1, static_cast<uint32_t>(sm_count()) * per_sm_of(c.head_dim, g->rows) / c.heads);
     g->start_cost = 128;
     g->grain = 16;  // quotas in whole 64 entries: 17.1 us against 15.8 for 8 requests of 1000, 23.2 against 20.8 for 16 of 2000
     g->min_quota = 128;
@@ -279,13 +283,19 @@ namespace {
 // the four entries whose weights it holds from the scores.  Nothing is
 // transposed or exchanged: one permute pairs two entries' bytes, one conversion
 // gives the fragment.
-template <int kDw, int kNp, bool kShared>
-__global__ __launch_bounds__(kAttnThreads, (Cfg<kDw, kNp, kShared>::kPerSm)) void q8_attn_kernel(const AttnArgs a) {
-  using C = Cfg<kDw, kNp, kShared>;
-  constexpr int kChunks = kDw / 16;  // 16-byte chunks of a row part
-  constexpr int kOt = kDw / 8;       // output column tiles
+//
+// Up to eight rows (decode with groups of as many heads) the products are transposed: 16 entries are m, and the eight
+// rows n, of the scores; 16 channels are m, and the rows n again, of the values.  That is half the products, exponentials and
+// accumulators; the weights cross from entries to rows with one 8 x 8 transposition for eight entries.  One request of 777 entries 8.7 us against
+// 9.4 with sixteen rows, 32 of 300 14.8 against 18.2, 64 of 8000 174 against 179.
+template <int kDw, int kNp, bool kShared, int kRows>
+__global__ __launch_bounds__(kAttnThreads, (Cfg<kDw, kNp, kShared, kRows>::kPerSm)) void q8_attn_kernel(const AttnArgs a) {
+  using C = Cfg<kDw, kNp, kShared, kRows>;
+  constexpr bool kFew = kRows == 8;
+  constexpr int kChunks = kDw / 16;             // 16-byte chunks of a row part
+  constexpr int kOt = kFew ? kDw / 16 : kDw / 8;  // output tiles
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ float s_m[C::kGroups][16], s_l[C::kGroups][16];
+  __shared__ float s_m[C::kGroups][kRows], s_l[C::kGroups][kRows];
   __shared__ __align__(16) float s_x[kNp == 2 ? C::kGroups : 1][2][2][kNp == 2 ? 256 : 1];  // partial scores of a row's two warps
   __shared__ int s_nan[C::kD];  // first entry with a NaN value, by channel
   __shared__ int s_any_nan;
@@ -315,7 +325,7 @@ __global__ __launch_bounds__(kAttnThreads, (Cfg<kDw, kNp, kShared>::kPerSm)) voi
       if (tid == 0) status_or(a.d_status, CKV_STATUS_BAD_INDEX);
       continue;
     }
-    const uint32_t rows = min(16u, item.q_len * G - item.row0);
+    const uint32_t rows = min(static_cast<uint32_t>(kRows), item.q_len * G - item.row0);
     const int32_t* table = a.table + static_cast<size_t>(item.rid) * a.stride;
     __syncthreads();  // the previous item's reads of shared memory are done
     for (int c = tid; c < C::kD; c += kAttnThreads) s_nan[c] = 0x7FFFFFFF;
@@ -362,14 +372,14 @@ __global__ __launch_bounds__(kAttnThreads, (Cfg<kDw, kNp, kShared>::kPerSm)) voi
 #pragma unroll
     for (int s = 0; s < C::kStages - 1; ++s) issue(s);
 
-    // ---- query fragments of rows g and g + 8
+    // ---- query fragments of rows g and g + 8 (few rows: of row g, and what belongs to it handed to the lanes with columns 2q and 2q + 1)
     uint32_t qf[kDw / 16][4];
     float rf[2];     // undoes the row's scaling
     int64_t vis[2];  // entries the row sees
     const uint32_t vis_min =
         static_cast<uint32_t>(q8_visible(item.kv_len, item.q_len - 1 - item.row0 / G, item.phase, a.ratio));
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
+    for (int r = 0; r < (kFew ? 1 : 2); ++r) {
       const uint32_t row = g + 8 * r;
       const bool in = row < rows;
       const uint32_t rho = item.row0 + (in ? row : 0);
@@ -379,6 +389,19 @@ __global__ __launch_bounds__(kAttnThreads, (Cfg<kDw, kNp, kShared>::kPerSm)) voi
           a.q + (static_cast<size_t>(item.q_start + i) * a.n_heads + h * G + hg) * C::kD + half * kDw;
       rf[r] = load_query<kDw>(p, in, q, r, qf);
     }
+    if (kFew) {
+      const float rf_g = rf[0];
+      const int vis_g = static_cast<int>(vis[0]);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        rf[e] = __shfl_sync(0xFFFFFFFFu, rf_g, (2 * q + e) * 4);
+        vis[e] = __shfl_sync(0xFFFFFFFFu, vis_g, (2 * q + e) * 4);
+      }
+    }
+    // Score e of half n is that of row r = row_of(e) of this lane's two, and entry score_entry(n, e) of the tile
+    constexpr int kHalves = kFew ? 1 : 2;
+    auto row_of = [](int e) { return kFew ? e & 1 : e >> 1; };
+    auto score_entry = [&](int n, int e) { return kFew ? (e >> 1) * 8 + g : n * 8 + 2 * q + (e & 1); };
 
     float o[kOt][4];
 #pragma unroll
@@ -393,23 +416,24 @@ __global__ __launch_bounds__(kAttnThreads, (Cfg<kDw, kNp, kShared>::kPerSm)) voi
       const float k_scale = lds_f32(st + C::kTileBytes), v_scale = lds_f32(st + C::kTileBytes + 4);
       const bool tile_ok = lds_u32(st + C::kTileBytes + 8) != 0;
       // scores
-      float s[2][4];
-      tile_scores<kDw>(st, g, q, qf, s);
+      float s[kHalves][4];
+      if constexpr (kFew)
+        tile_scores_t<kDw>(st, g, q, qf, s[0]);
+      else
+        tile_scores<kDw>(st, g, q, qf, s);
       float f[2] = {rf[0] * a.scale_log2, rf[1] * a.scale_log2};
       if (kNp == 2) {  // the two warps of a row add their halves of the channels
         float* own = s_x[grp][i & 1][half];
         const float* other = s_x[grp][i & 1][half ^ 1];
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
-          s[n][0] *= rf[0];
-          s[n][1] *= rf[0];
-          s[n][2] *= rf[1];
-          s[n][3] *= rf[1];
+        for (int n = 0; n < kHalves; ++n) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[n][e] *= rf[row_of(e)];
           *reinterpret_cast<float4*>(own + n * 128 + lane * 4) = make_float4(s[n][0], s[n][1], s[n][2], s[n][3]);
         }
         asm volatile("bar.sync %0, 64;" ::"r"(1 + grp) : "memory");
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
+        for (int n = 0; n < kHalves; ++n) {
           const float4 x = *reinterpret_cast<const float4*>(other + n * 128 + lane * 4);
           s[n][0] += x.x;  // addition commutes: both warps get the same sums
           s[n][1] += x.y;
@@ -424,62 +448,80 @@ __global__ __launch_bounds__(kAttnThreads, (Cfg<kDw, kNp, kShared>::kPerSm)) voi
       const uint32_t e0 = entry_of(i);
       const bool edge = e0 + kTile > min(vis_min, item.kv_end) || !tile_ok;
 #pragma unroll
-      for (int n = 0; n < 2; ++n) {
+      for (int n = 0; n < kHalves; ++n) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[n][e] = fmaf(s[n][e], f[e >> 1], lv);
+        for (int e = 0; e < 4; ++e) s[n][e] = fmaf(s[n][e], f[row_of(e)], lv);
       }
       if (edge) {
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
+        for (int n = 0; n < kHalves; ++n) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const int64_t at = e0 + n * 8 + 2 * q + (e & 1);
-            if (at >= vis[e >> 1] || at >= item.kv_end || !tile_ok) s[n][e] = -INFINITY;
+            const int64_t at = e0 + score_entry(n, e);
+            if (at >= vis[row_of(e)] || at >= item.kv_end || !tile_ok) s[n][e] = -INFINITY;
           }
         }
       }
       // raise the reference where a score passes it by 14
-      const float hi0 = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1]));
-      const float hi1 = fmaxf(fmaxf(s[0][2], s[0][3]), fmaxf(s[1][2], s[1][3]));
-      if (__any_sync(0xFFFFFFFFu, hi0 > m[0] + 14.0f || hi1 > m[1] + 14.0f)) {
-        float top[2] = {hi0, hi1};
+      float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+      for (int n = 0; n < kHalves; ++n) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) top[row_of(e)] = fmaxf(top[row_of(e)], s[n][e]);
+      }
+      if (__any_sync(0xFFFFFFFFu, top[0] > m[0] + 14.0f || top[1] > m[1] + 14.0f)) {
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          top[r] = fmaxf(top[r], __shfl_xor_sync(0xFFFFFFFFu, top[r], 1));
-          top[r] = fmaxf(top[r], __shfl_xor_sync(0xFFFFFFFFu, top[r], 2));
+#pragma unroll
+          for (int x = kFew ? 4 : 1; x < (kFew ? 32 : 4); x <<= 1) top[r] = fmaxf(top[r], __shfl_xor_sync(0xFFFFFFFFu, top[r], x));
           const float now = fmaxf(m[r], top[r] - 6.0f);
           const float c = ex2(m[r] - now);
           m[r] = now;
           l[r] *= c;
 #pragma unroll
           for (int x = 0; x < kOt; ++x) {
-            o[x][2 * r] *= c;
-            o[x][2 * r + 1] *= c;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (row_of(e) == r) o[x][e] *= c;
           }
         }
       }
-      uint32_t p[4];
+      uint32_t p[2 * kHalves];
 #pragma unroll
-      for (int n = 0; n < 2; ++n) {
-        const float w0 = ex2(s[n][0] - m[0]), w1 = ex2(s[n][1] - m[0]);
-        const float w2 = ex2(s[n][2] - m[1]), w3 = ex2(s[n][3] - m[1]);
-        l[0] = fmaf(w0 + w1, iv, l[0]);
-        l[1] = fmaf(w2 + w3, iv, l[1]);
+      for (int n = 0; n < kHalves; ++n) {
+        const float w0 = ex2(s[n][0] - m[row_of(0)]), w1 = ex2(s[n][1] - m[row_of(1)]);
+        const float w2 = ex2(s[n][2] - m[row_of(2)]), w3 = ex2(s[n][3] - m[row_of(3)]);
+        if (kFew) {
+          l[0] = fmaf(w0 + w2, iv, l[0]);
+          l[1] = fmaf(w1 + w3, iv, l[1]);
+        } else {
+          l[0] = fmaf(w0 + w1, iv, l[0]);
+          l[1] = fmaf(w2 + w3, iv, l[1]);
+        }
         p[2 * n] = pack_f16x2(w0, w1);
         p[2 * n + 1] = pack_f16x2(w2, w3);
+      }
+      if (kFew) {  // from (entry g, rows 2q and 2q + 1) to (row g, entries 2q and 2q + 1)
+        p[0] = transpose8(p[0]);
+        p[1] = transpose8(p[1]);
       }
       // values.  A NaN must not reach rows that do not see its entry (0 * NaN): where some entries are hidden,
       // NaNs are taken out, and put back at the end into the rows that see them (s_nan).
       const uint32_t vt = kShared ? st : st + kTile * kDw;
       auto two_words = [&](uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, float(*acc)[4]) {
-        uint32_t lo = __byte_perm(a0, a1, 0x5140), hi = __byte_perm(a2, a3, 0x5140);
-        mma_f16(acc[0], p, q8_lo_f16x2(lo), q8_lo_f16x2(hi));
-        mma_f16(acc[1], p, q8_hi_f16x2(lo), q8_hi_f16x2(hi));
-        lo = __byte_perm(a0, a1, 0x7362);
-        hi = __byte_perm(a2, a3, 0x7362);
-        mma_f16(acc[2], p, q8_lo_f16x2(lo), q8_lo_f16x2(hi));
-        mma_f16(acc[3], p, q8_hi_f16x2(lo), q8_hi_f16x2(hi));
+#pragma unroll
+        for (int z = 0; z < 2; ++z) {  // two channels of the word
+          const uint32_t lo = __byte_perm(a0, a1, z ? 0x7362 : 0x5140), hi = __byte_perm(a2, a3, z ? 0x7362 : 0x5140);
+          if constexpr (kFew) {
+            const uint32_t vf[4] = {q8_lo_f16x2(lo), q8_hi_f16x2(lo), q8_lo_f16x2(hi), q8_hi_f16x2(hi)};
+            mma_f16(acc[z], vf, p[0], p[1]);
+          } else {
+            mma_f16(acc[2 * z], p, q8_lo_f16x2(lo), q8_lo_f16x2(hi));
+            mma_f16(acc[2 * z + 1], p, q8_hi_f16x2(lo), q8_hi_f16x2(hi));
+          }
+        }
       };
+      constexpr int kPerWord = kFew ? 2 : 4;  // output tiles of a word
       if (kDw == 64) {
         uint2 w[4];
 #pragma unroll
@@ -492,7 +534,7 @@ __global__ __launch_bounds__(kAttnThreads, (Cfg<kDw, kNp, kShared>::kPerSm)) voi
           }
         }
         two_words(w[0].x, w[1].x, w[2].x, w[3].x, o);
-        two_words(w[0].y, w[1].y, w[2].y, w[3].y, o + 4);
+        two_words(w[0].y, w[1].y, w[2].y, w[3].y, o + kPerWord);
       } else {
 #pragma unroll
         for (int jj = 0; jj < kDw / 128; ++jj) {
@@ -509,10 +551,10 @@ __global__ __launch_bounds__(kAttnThreads, (Cfg<kDw, kNp, kShared>::kPerSm)) voi
               w[x].w = without_nan(w[x].w, e0 + t, nan + 12, &s_any_nan);
             }
           }
-          two_words(w[0].x, w[1].x, w[2].x, w[3].x, o + jj * 16);
-          two_words(w[0].y, w[1].y, w[2].y, w[3].y, o + jj * 16 + 4);
-          two_words(w[0].z, w[1].z, w[2].z, w[3].z, o + jj * 16 + 8);
-          two_words(w[0].w, w[1].w, w[2].w, w[3].w, o + jj * 16 + 12);
+          two_words(w[0].x, w[1].x, w[2].x, w[3].x, o + (jj * 4 + 0) * kPerWord);
+          two_words(w[0].y, w[1].y, w[2].y, w[3].y, o + (jj * 4 + 1) * kPerWord);
+          two_words(w[0].z, w[1].z, w[2].z, w[3].z, o + (jj * 4 + 2) * kPerWord);
+          two_words(w[0].w, w[1].w, w[2].w, w[3].w, o + (jj * 4 + 3) * kPerWord);
         }
       }
     }
@@ -521,31 +563,52 @@ __global__ __launch_bounds__(kAttnThreads, (Cfg<kDw, kNp, kShared>::kPerSm)) voi
     __syncthreads();  // the rings are idle: they become the merge area
 
     // ---- join the warps
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      l[r] += __shfl_xor_sync(0xFFFFFFFFu, l[r], 1);
-      l[r] += __shfl_xor_sync(0xFFFFFFFFu, l[r], 2);
-      if (q == 0 && half == 0) {
-        s_m[grp][g + 8 * r] = m[r];
-        s_l[grp][g + 8 * r] = l[r];
-      }
-    }
-    float* merge = reinterpret_cast<float*>(smem) + grp * 16 * C::kMergeStride;
-    constexpr int kRun = kDw == 64 ? 8 : 16;  // consecutive channels of a lane's column
-#pragma unroll
-    for (int x = 0; x < kOt; x += 4) {
+    constexpr int kRun = kDw == 64 ? 8 : 16;  // consecutive channels of a lane
+    float* merge = reinterpret_cast<float*>(smem) + grp * kRows * C::kMergeStride;
+    if constexpr (kFew) {
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {  // column 2q + n of tile x: channel (8 (x / run) + 2q + n) * run + x % run
-          const int ch = half * kDw + (8 * (x / kRun) + 2 * q + n) * kRun + x % kRun;
-          *reinterpret_cast<float4*>(merge + (g + 8 * r) * C::kMergeStride + ch) =
-              make_float4(o[x][2 * r + n], o[x + 1][2 * r + n], o[x + 2][2 * r + n], o[x + 3][2 * r + n]);
+        for (int x = 4; x < 32; x <<= 1) l[r] += __shfl_xor_sync(0xFFFFFFFFu, l[r], x);
+        if (g == 0 && half == 0) {
+          s_m[grp][2 * q + r] = m[r];
+          s_l[grp][2 * q + r] = l[r];
+        }
+      }
+#pragma unroll
+      for (int x = 0; x < kOt; x += 2) {
+        const int ch = half * kDw + (8 * (x / (kRun / 2)) + g) * kRun + 2 * (x % (kRun / 2));
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+          *reinterpret_cast<float4*>(merge + (2 * q + r) * C::kMergeStride + ch) =
+              make_float4(o[x][r], o[x][2 + r], o[x + 1][r], o[x + 1][2 + r]);
+      }
+    } else {
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        l[r] += __shfl_xor_sync(0xFFFFFFFFu, l[r], 1);
+        l[r] += __shfl_xor_sync(0xFFFFFFFFu, l[r], 2);
+        if (q == 0 && half == 0) {
+          s_m[grp][g + 8 * r] = m[r];
+          s_l[grp][g + 8 * r] = l[r];
+        }
+      }
+#pragma unroll
+      for (int x = 0; x < kOt; x += 4) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {  // column 2q + n of tile x: channel (8 (x / run) + 2q + n) * run + x % run
+            const int ch = half * kDw + (8 * (x / kRun) + 2 * q + n) * kRun + x % kRun;
+            *reinterpret_cast<float4*>(merge + (g + 8 * r) * C::kMergeStride + ch) =
+                make_float4(o[x][2 * r + n], o[x + 1][2 * r + n], o[x + 2][2 * r + n], o[x + 3][2 * r + n]);
+          }
         }
       }
     }
     __syncthreads();
-    const uint32_t row = tid >> 3;
+    constexpr int kPerRow = kAttnThreads / kRows;  // threads of a row
+    const uint32_t row = tid / kPerRow;
     if (row < rows) {
       float top = s_m[0][row];
 #pragma unroll
@@ -559,15 +622,15 @@ __global__ __launch_bounds__(kAttnThreads, (Cfg<kDw, kNp, kShared>::kPerSm)) voi
       const uint32_t rho = item.row0 + row, i = rho / G, hg = rho % G;
       const int64_t see = q8_visible(item.kv_len, item.q_len - 1 - i, item.phase, a.ratio);
       const size_t out_row = static_cast<size_t>(item.q_start + i) * a.n_heads + h * G + hg;
-      const size_t part_row = (static_cast<size_t>(item.part + static_cast<int>(item.chunk)) * H + h) * 16 + row;
+      const size_t part_row = (static_cast<size_t>(item.part + static_cast<int>(item.chunk)) * H + h) * kRows + row;
       const float inv = sum == 0.0f ? 0.0f : __fdiv_rn(1.0f, sum);
       const int any_nan = s_any_nan;
-      for (int ch = (tid & 7) * 4; ch < C::kD; ch += 32) {
+      for (int ch = tid % kPerRow * 4; ch < C::kD; ch += kPerRow * 4) {
         float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int w = 0; w < C::kGroups; ++w) {
           const float4 x = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(smem) +
-                                                            (w * 16 + row) * C::kMergeStride + ch);
+                                                            (w * kRows + row) * C::kMergeStride + ch);
           v[0] = fmaf(x.x, c[w], v[0]);
           v[1] = fmaf(x.y, c[w], v[1]);
           v[2] = fmaf(x.z, c[w], v[2]);
@@ -589,7 +652,7 @@ __global__ __launch_bounds__(kAttnThreads, (Cfg<kDw, kNp, kShared>::kPerSm)) voi
             store_row_chunk<__nv_bfloat16, 4>(static_cast<__nv_bfloat16*>(a.out) + out_row * C::kD + ch, v);
         }
       }
-      if ((tid & 7) == 0) {
+      if (tid % kPerRow == 0) {
         if (item.part >= 0)
           a.part_ml[part_row] = make_float2(top, sum);
         else if (a.lse != nullptr)
@@ -732,23 +795,24 @@ __global__ __launch_bounds__(kCombineThreads) void q8_combine_kernel(const AttnA
   }
 }
 
-template <int kDw, int kNp, bool kShared>
+template <int kDw, int kNp, bool kShared, int kRows>
 int launch_attn(const AttnArgs& a, cudaStream_t s) {
-  using C = Cfg<kDw, kNp, kShared>;
-  auto* kernel = q8_attn_kernel<kDw, kNp, kShared>;
+  using C = Cfg<kDw, kNp, kShared, kRows>;
+  auto* kernel = q8_attn_kernel<kDw, kNp, kShared, kRows>;
   static std::atomic<uint64_t> done;
   const int rc = allow_smem(reinterpret_cast<const void*>(kernel), C::kSmem, done);
   if (rc) return rc;
   return launch_pdl(kernel, dim3(a.g.ctas, a.c.heads), dim3(kAttnThreads), C::kSmem, s, a);
 }
 
+template <int kRows>
 int launch_split(const AttnArgs& a, cudaStream_t s) {
   const bool shared = a.c.v == nullptr;
   switch (a.c.head_dim) {
-    case 64: return shared ? launch_attn<64, 1, true>(a, s) : launch_attn<64, 1, false>(a, s);
-    case 128: return shared ? launch_attn<128, 1, true>(a, s) : launch_attn<128, 1, false>(a, s);
-    case 256: return shared ? launch_attn<256, 1, true>(a, s) : launch_attn<256, 1, false>(a, s);
-    default: return shared ? launch_attn<256, 2, true>(a, s) : launch_attn<256, 2, false>(a, s);
+    case 64: return shared ? launch_attn<64, 1, true, kRows>(a, s) : launch_attn<64, 1, false, kRows>(a, s);
+    case 128: return shared ? launch_attn<128, 1, true, kRows>(a, s) : launch_attn<128, 1, false, kRows>(a, s);
+    case 256: return shared ? launch_attn<256, 1, true, kRows>(a, s) : launch_attn<256, 1, false, kRows>(a, s);
+    default: return shared ? launch_attn<256, 2, true, kRows>(a, s) : launch_attn<256, 2, false, kRows>(a, s);
   }
 }
 
@@ -851,7 +915,7 @@ int ckv_q8_attn(const ckv_q8_cache_t* cache, uint32_t n_heads, uint32_t ratio, f
   a.d_status = d_status;
   a.wait_ns = wait_limit_ns();
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  rc = !a.g.tc ? launch_split(a, s) : a.c.head_dim <= 128 ? launch_q8_attn_rows(a, s) : launch_q8_attn_tc(a, s);
+  rc = !a.g.tc ? (a.g.rows == 8 ? launch_split<8>(a, s) : launch_split<16>(a, s)) : a.c.head_dim <= 128 ? launch_q8_attn_rows(a, s) : launch_q8_attn_tc(a, s);
   return rc ? rc : launch_combine(a, s);
 }
 
