@@ -265,6 +265,12 @@ ATTN = [  # lens, q_lens, heads, H, D, T, latent, ratio
     ([333], [1], 17, 1, 512, 64, True, 2),
     ([300, 40], [13, 13], 5, 1, 512, 64, True, 1),
     ([300], [13], 5, 1, 256, 32, False, 1),
+    # up to eight rows a request on average, some requests with more
+    ([300, 1, 70], [1, 2, 1], 4, 1, 256, 64, True, 1),
+    ([200, 30], [3, 1], 4, 1, 64, 16, True, 1),
+    ([500], [1], 7, 1, 128, 32, True, 4),
+    ([90, 60, 0], [5, 1, 0], 4, 1, 512, 32, False, 1),
+    ([40, 700], [3, 1], 8, 2, 128, 64, False, 1),
 ]
 
 
@@ -338,6 +344,21 @@ def test_nan_values_reach_only_queries_that_see_them(heads, D, latent):
     want[sees, :, 5] = True
     if latent:
         want[sees] = True  # the key is NaN too: the whole row's weights are
+    assert np.array_equal(got, want)
+
+
+@pytest.mark.parametrize("heads,D", [(4, 64), (3, 128), (4, 256), (1, 512)])
+@pytest.mark.parametrize("latent", [False, True])
+def test_nan_values_of_few_rows(heads, D, latent):
+    w = World(16, [70, 33], 1, D, 16, latent)
+    for b, at in ((0, 69), (1, 20)):  # request 0's is hidden from the first of its two queries, request 1's from none
+        (w.k if latent else w.v)[w.table[w.rid[b], at // 16], 0, at % 16, 7] = 0xFF
+    q = w.queries([2, 2], heads)
+    _, _, out, lse, st = run_attn(w, q, [70, 33], [2, 2], heads, 1, torch.float32)
+    assert st == 0
+    got = np.isnan(out.cpu().numpy())
+    want = np.zeros_like(got)
+    want[1:, :, slice(None) if latent else 7] = True
     assert np.array_equal(got, want)
 
 
