@@ -554,17 +554,18 @@ def new_q8_cache(num_blocks: int, n_kv_heads: int, block_tokens: int, head_dim: 
 # These calls are made once a layer on few microseconds of work, so what they check is checked in few Python steps:
 # a tensor's address is taken, with the checks that make it usable, by _at(); lengths by _lens().
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_E4M3, _FP32 = torch.float8_e4m3fn, torch.float32
 
 
 def _at(device: int, t: Optional[torch.Tensor]) -> Optional[int]:
     """The address of a contiguous tensor on the given CUDA device."""
     if t is None:
         return None
-    if t.get_device() != device:
-        raise ValueError("libckv takes CUDA tensors of one device only")
-    if not t.is_contiguous():
-        raise ValueError("libckv takes contiguous tensors only")
-    return t.data_ptr()
+    if t.get_device() == device and t.is_contiguous():
+        return t.data_ptr()
+    raise ValueError("libckv takes CUDA tensors of one device only" if t.get_device() != device else
+                     "libckv takes contiguous tensors only")
 
 
 def _stream_of(device: int, stream):
@@ -589,9 +590,10 @@ def _q8(cache: Q8Cache) -> Tuple[Q8CacheArg, int]:
     """ckv_q8_cache_t, and the device: the cache's, which must be the current one."""
     k, ks, v, vs = cache
     shape = k.shape
-    if k.dtype is not torch.float8_e4m3fn or len(shape) != 4:
+    if k.dtype is not _E4M3 or len(shape) != 4:
         raise ValueError("a q8 cache's k is float8_e4m3fn [num_blocks, n_kv_heads, block_tokens, head_dim]")
-    if ks.dtype is not torch.float32 or ks.shape != shape[:2]:
+    blocks, heads, tokens, dim = shape
+    if ks.dtype is not _FP32 or ks.shape != (blocks, heads):
         raise ValueError("a q8 cache's scales are fp32 [num_blocks, n_kv_heads]")
     device = k.get_device()
     if device < 0:
@@ -600,12 +602,11 @@ def _q8(cache: Q8Cache) -> Tuple[Q8CacheArg, int]:
     if v is not None or vs is not None:
         if v is None or vs is None:
             raise ValueError("v and v_scale go together")
-        if (v.dtype is not torch.float8_e4m3fn or v.shape != shape or vs.dtype is not torch.float32 or
-                vs.shape != ks.shape):
+        if v.dtype is not _E4M3 or v.shape != shape or vs.dtype is not _FP32 or vs.shape != (blocks, heads):
             raise ValueError("a q8 cache's v and v_scale are shaped like its k and k_scale")
         v_at, vs_at = _at(device, v), _at(device, vs)
-    arg = Q8CacheArg(_at(device, k), _at(device, ks), v_at, vs_at, shape[0], shape[2], shape[1], shape[3])
-    if device != torch._C._cuda_getDevice():
+    arg = Q8CacheArg(_at(device, k), _at(device, ks), v_at, vs_at, blocks, tokens, heads, dim)
+    if device != _current_device():
         raise ValueError("the q8 cache is not on the current device")
     return arg, device
 
@@ -731,17 +732,18 @@ def q8_attn(cache: Q8Cache, q: torch.Tensor, plan: Q8AttnPlan, block_table: torc
     arg, dev = _q8(cache)
     buffer, n_heads, ratio, batch, num_q = plan
     _is(q, "q", torch.bfloat16, num_q, n_heads, arg.head_dim)
+    where = q.device
     if out is None:
-        out = torch.empty(q.shape, dtype=out_dtype, device=q.device)
+        out = torch.empty_like(q, dtype=out_dtype)
     else:
         _is(out, "out", out.dtype, num_q, n_heads, arg.head_dim)
     if lse is None:
-        lse = torch.empty((num_q, n_heads), dtype=torch.float32, device=q.device)
+        lse = torch.empty((num_q, n_heads), dtype=_FP32, device=where)
     else:
         _is(lse, "lse", torch.float32, num_q, n_heads)
     if workspace is None:
         workspace = torch.empty(max(lib.ckv_q8_attn_workspace_bytes(arg, n_heads, batch, num_q), 16),
-                                dtype=torch.uint8, device=q.device)
+                                dtype=torch.uint8, device=where)
     table, stride, reqs = _table(dev, block_table)
     rc = lib.ckv_q8_attn(arg, n_heads, ratio, scale, _at(dev, q), batch, num_q, table, stride, reqs,
                          _at(dev, buffer), buffer.numel(), dtype_code(out.dtype), _at(dev, out), _at(dev, lse),

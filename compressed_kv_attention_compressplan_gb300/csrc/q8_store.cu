@@ -7,7 +7,7 @@
 // alone) or was begun by earlier rows, whose scale can only grow: then the
 // earlier entries are divided by the growth, exactly but for subnormals.
 //
-// Bound.  Many rows: the rows' bytes, each read once and held in registers between the scale and the store.  16 requests of eight heads,
+// Bound.  Many rows: the rows' bytes, read from memory for the scale and once more, from L1 or L2, for the codes.  16 requests of eight heads,
 // 255 MB: the store takes 44 us, 5.7 TB/s or 85 % of the measured copy rate; with the plan 48.6.  A decode step (a row for some of 256
 // requests) is two launches, 4.7 and 4.2 us, which the host's two calls (26 us) hide.  A CTA takes one (block, head, side), since its
 // scale needs all its rows before any is stored.
