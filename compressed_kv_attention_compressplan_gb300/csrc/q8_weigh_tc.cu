@@ -46,7 +46,7 @@ struct alignas(16) WtShared {
   uint64_t k_full[2], k_free[2], q_full[kQ], q_free[kQ], s_full[2], s_free[2], idle;
   alignas(16) float off[kQ][kChunk];
   int vis[kQ][kChunk];
-  float part[3][128];
+  float part[2][3][128];
   uint32_t unit[CKV_MAX_BATCH];
   uint32_t first_q[CKV_MAX_BATCH];
   uint4 meta[CKV_MAX_BATCH];
@@ -224,31 +224,46 @@ __global__ __launch_bounds__(WtCfg<kD>::kThreads, 1) void q8_weigh_tc_kernel(con
   } else if (warp < C::kExpWarps) {
     const int group = warp >> 2, quarter = warp & 3, entry = quarter * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
+    // A unit's blocks are asked for a unit ahead, and its first scale and its weights so far before the last head of the unit before.
     auto block_of = [&](uint32_t u) -> int32_t {
-      if (u >= units) return 0;
+      if (u >= units) return -1;
       const uint32_t b = last_not_above(sh.unit, a.batch, u);
       const uint4 meta = sh.meta[b];
       return ld_ahead(a.table + static_cast<size_t>(meta.w) * a.stride +
                       (min((u - sh.unit[b]) * kEntries + entry, meta.x - 1) >> t_shift));
     };
+    auto exists = [&](int32_t blk) { return static_cast<uint32_t>(blk) < a.c.num_blocks; };
+    auto scales_of = [&](int32_t blk) { return a.c.k_scale + static_cast<size_t>(exists(blk) ? blk : 0) * H; };
+    // a unit starts where a block does, so an entry's slot follows from its place in the unit
+    auto weight_of = [&](int32_t blk) {
+      float* at = a.weights + (static_cast<size_t>(exists(blk) ? blk : 0) << t_shift) + (entry & (T - 1));
+      return group == 0 && a.decay != 0.0f ? *static_cast<volatile float*>(at) : 0.0f;
+    };
     int32_t blk_next = block_of(blockIdx.x);
-    for (uint32_t u = blockIdx.x; u < units; u += gridDim.x) {
+    float scale_next = ld_ahead(scales_of(blk_next)), weight_next = weight_of(blk_next);
+    uint32_t turn = 0;
+    for (uint32_t u = blockIdx.x; u < units; u += gridDim.x, turn ^= 1) {
       const uint32_t b = last_not_above(sh.unit, a.batch, u);
       const uint4 meta = sh.meta[b];
       const uint32_t chunks = (meta.y * G + kChunk - 1) / kChunk;
       const uint32_t kv_len = meta.x, e0 = (u - sh.unit[b]) * kEntries, e = e0 + entry;
       const int32_t blk = blk_next;
+      float next = scale_next;
+      const float before = weight_next;
       blk_next = block_of(u + gridDim.x);
-      const bool valid = static_cast<uint32_t>(blk) < a.c.num_blocks;
+      const bool valid = exists(blk);
       if (!valid && e < kv_len && group == 0) status_or(a.d_status, CKV_STATUS_BAD_INDEX);
-      const float* scales = a.c.k_scale + static_cast<size_t>(valid ? blk : 0) * H;
-      float next = ld_ahead(scales);
+      const float* scales = scales_of(blk);
       F2 sum = f2_pack(0.0f, 0.0f);
       // the request's first row sees least: where it sees the whole tile, all do
       const bool edge = static_cast<int64_t>(e0) + kEntries > q8_visible(kv_len, meta.y - 1, meta.z, a.ratio);
       for (uint32_t h = 0; h < H; ++h) {
         const float f = next * a.scale_log2;
         next = ld_ahead(scales + min(h + 1, H - 1));
+        if (h + 1 == H) {
+          scale_next = ld_ahead(scales_of(blk_next));
+          weight_next = weight_of(blk_next);
+        }
         const F2 f2 = f2_pack(f, f);
         for (uint32_t c = 0; c < chunks; ++c, ++qc) {
           const uint32_t sb = qc & 1, qs = qc % C::kQStages;
@@ -283,11 +298,13 @@ __global__ __launch_bounds__(WtCfg<kD>::kThreads, 1) void q8_weigh_tc_kernel(con
       }
       float s0, s1;
       f2_unpack(sum, s0, s1);
-      if (group > 0) sh.part[group - 1][entry] = s0 + s1;
+      float(*part)[128] = sh.part[turn];  // two turns: no group is a whole unit ahead of another
+      if (group > 0) part[group - 1][entry] = s0 + s1;
       asm volatile("bar.sync 1, 512;" ::: "memory");
-      if (group == 0 && e < kv_len && valid)
-        put_weight(a, blk, e & (T - 1), ((s0 + s1) + sh.part[0][entry]) + (sh.part[1][entry] + sh.part[2][entry]));
-      asm volatile("bar.sync 1, 512;" ::: "memory");
+      if (group == 0 && e < kv_len && valid) {
+        const float w = ((s0 + s1) + part[0][entry]) + (part[1][entry] + part[2][entry]);
+        a.weights[(static_cast<size_t>(blk) << t_shift) + (e & (T - 1))] = a.decay == 0.0f ? w : fmaf(a.decay, before, w);
+      }
     }
   } else {
     for (uint32_t u = blockIdx.x; u < units; u += gridDim.x) {
