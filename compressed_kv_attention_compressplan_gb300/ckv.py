@@ -707,10 +707,13 @@ def plan_q8_attn(cache: Q8Cache, n_heads: int, ratio: int, rid: torch.Tensor, se
     arg, dev = _q8(cache)
     batch, (rid_at, seq_at, ext_at, kv_at) = _lens(dev, rid, seq_lens, extend_lens, kv_lens)
     if buffer is None:
-        buffer = torch.empty(max(lib.ckv_q8_attn_plan_bytes(arg, n_heads, batch, num_q), 16), dtype=torch.uint8,
-                             device=rid.device)
-    rc = lib.ckv_plan_q8_attn(arg, n_heads, ratio, rid_at, seq_at, ext_at, kv_at, batch, num_q, _at(dev, buffer),
-                              _bytes_of(buffer, "a plan buffer"), _at(dev, status), _stream_of(dev, stream))
+        size = max(lib.ckv_q8_attn_plan_bytes(arg, n_heads, batch, num_q), 16)
+        buffer = torch.empty(size, dtype=torch.uint8, device=rid.device)
+        buffer_at = buffer.data_ptr()
+    else:
+        size, buffer_at = _bytes_of(buffer, "a plan buffer"), _at(dev, buffer)
+    rc = lib.ckv_plan_q8_attn(arg, n_heads, ratio, rid_at, seq_at, ext_at, kv_at, batch, num_q, buffer_at, size,
+                              _at(dev, status), _stream_of(dev, stream))
     if rc:
         _q8_error(rc, "ckv_plan_q8_attn")
     return Q8AttnPlan(buffer, n_heads, ratio, batch, num_q)
@@ -732,23 +735,29 @@ def q8_attn(cache: Q8Cache, q: torch.Tensor, plan: Q8AttnPlan, block_table: torc
     arg, dev = _q8(cache)
     buffer, n_heads, ratio, batch, num_q = plan
     _is(q, "q", torch.bfloat16, num_q, n_heads, arg.head_dim)
-    where = q.device
+    where = q.device  # what is made here is contiguous and on it
     if out is None:
-        out = torch.empty_like(q, dtype=out_dtype)
+        out = torch.empty_like(q) if out_dtype is torch.bfloat16 else torch.empty(q.shape, dtype=out_dtype, device=where)
+        out_at = out.data_ptr()
     else:
         _is(out, "out", out.dtype, num_q, n_heads, arg.head_dim)
+        out_at = _at(dev, out)
     if lse is None:
         lse = torch.empty((num_q, n_heads), dtype=_FP32, device=where)
+        lse_at = lse.data_ptr()
     else:
-        _is(lse, "lse", torch.float32, num_q, n_heads)
+        _is(lse, "lse", _FP32, num_q, n_heads)
+        lse_at = _at(dev, lse)
     if workspace is None:
-        workspace = torch.empty(max(lib.ckv_q8_attn_workspace_bytes(arg, n_heads, batch, num_q), 16),
-                                dtype=torch.uint8, device=where)
+        size = max(lib.ckv_q8_attn_workspace_bytes(arg, n_heads, batch, num_q), 16)
+        workspace = torch.empty(size, dtype=torch.uint8, device=where)
+        space_at = workspace.data_ptr()
+    else:
+        size, space_at = _bytes_of(workspace, "a workspace"), _at(dev, workspace)
     table, stride, reqs = _table(dev, block_table)
     rc = lib.ckv_q8_attn(arg, n_heads, ratio, scale, _at(dev, q), batch, num_q, table, stride, reqs,
-                         _at(dev, buffer), buffer.numel(), dtype_code(out.dtype), _at(dev, out), _at(dev, lse),
-                         _at(dev, workspace), _bytes_of(workspace, "a workspace"), _at(dev, status),
-                         _stream_of(dev, stream))
+                         _at(dev, buffer), buffer.numel(), dtype_code(out.dtype), out_at, lse_at, space_at, size,
+                         _at(dev, status), _stream_of(dev, stream))
     if rc:
         _q8_error(rc, "ckv_q8_attn")
     return out, lse
