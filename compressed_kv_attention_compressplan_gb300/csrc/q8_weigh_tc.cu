@@ -12,8 +12,8 @@
 // a chunk's rows lie in as many pieces as it has queries), one for the products.
 //
 // Bound.  128 channels: a chunk's products take 512 cycles, its exponentials 512.  Measured: 18 MB of keys and 8.9 GF
-// in 29 us, 10 k cycles for a unit of four chunks: the queries' copies and the handing over of one unit to the next; keys and queries
-// by the same eight warps took 31.6 us.
+// in 28 us, some 10 k cycles for a unit of four chunks: copying a chunk's queries takes 2 k.  Keys and queries by the same eight
+// warps took 31.6 us; the next unit's weights and scales asked for only at its start, 29.0.
 #include <algorithm>
 
 #include "q8_tc.cuh"
