@@ -132,6 +132,13 @@ __device__ __forceinline__ uint32_t q8_rescale4(uint32_t w, float f) {
 // 0xFF in every byte of w that is an e4m3 NaN (0x7F or 0xFF).
 __device__ __forceinline__ uint32_t q8_nan_bytes(uint32_t w) { return __vcmpeq4(w & 0x7F7F7F7Fu, 0x7F7F7F7Fu); }
 
+// 1 / x to a unit in the last place, x normal: one instruction where a division takes ten and a branch.
+__device__ __forceinline__ float rcp(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
 // Two fp32 products at once (see f2_add and f2_fma).
 __device__ __forceinline__ F2 f2_mul(F2 a, F2 b) {
   F2 r;
@@ -305,6 +312,9 @@ __device__ __forceinline__ float load_query(const __nv_bfloat16* p, bool in, int
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
   // bytes 16, or 0 to write zeros (src is not read then)
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");

@@ -353,13 +353,23 @@ __global__ __launch_bounds__(kAttnThreads, (Cfg<kDw, kNp, kShared, kRows>::kPerS
         const uint32_t dst = ring + (i % C::kStages) * C::kStageBytes;
         // entries past the request's end, and blocks that do not exist, read as zeros
         const uint32_t here = ok ? min(static_cast<uint32_t>(kTile), item.kv_len - e0) : 0;
+        const uint8_t* k = a.c.k + base;
+        const uint8_t* v = kShared ? nullptr : a.c.v + base;
+        if (here == kTile) {
 #pragma unroll
-        for (int x = 0; x < kTile * kChunks / 32; ++x) {
-          const uint32_t c = x * 32 + lane, t = c / kChunks, cc = c % kChunks;
-          const uint32_t n = t < here ? 16u : 0u;
-          const size_t src = base + static_cast<size_t>(t) * C::kD + cc * 16;
-          cp_async16(dst + tile_off<kDw>(t, cc), a.c.k + src, n);
-          if (!kShared) cp_async16(dst + kTile * kDw + tile_off<kDw>(t, cc), a.c.v + src, n);
+          for (int x = 0; x < kTile * kChunks / 32; ++x) {
+            const uint32_t c = x * 32 + lane, t = c / kChunks, cc = c % kChunks;
+            cp_async16(dst + tile_off<kDw>(t, cc), k + t * C::kD + cc * 16);
+            if (!kShared) cp_async16(dst + kTile * kDw + tile_off<kDw>(t, cc), v + t * C::kD + cc * 16);
+          }
+        } else {
+#pragma unroll 1
+          for (int x = 0; x < kTile * kChunks / 32; ++x) {
+            const uint32_t c = x * 32 + lane, t = c / kChunks, cc = c % kChunks;
+            const uint32_t n = t < here ? 16u : 0u;
+            cp_async16(dst + tile_off<kDw>(t, cc), k + t * C::kD + cc * 16, n);
+            if (!kShared) cp_async16(dst + kTile * kDw + tile_off<kDw>(t, cc), v + t * C::kD + cc * 16, n);
+          }
         }
         if (lane < 2) {
           const float* s = (kShared || lane == 0 ? a.c.k_scale : a.c.v_scale) + bh;
@@ -444,7 +454,7 @@ __global__ __launch_bounds__(kAttnThreads, (Cfg<kDw, kNp, kShared, kRows>::kPerS
       }
       f[0] *= k_scale;
       f[1] *= k_scale;
-      const float lv = __log2f(v_scale), iv = __fdiv_rn(1.0f, v_scale);
+      const float lv = __log2f(v_scale), iv = rcp(v_scale);
       const uint32_t e0 = entry_of(i);
       const bool edge = e0 + kTile > min(vis_min, item.kv_end) || !tile_ok;
 #pragma unroll
