@@ -23,7 +23,7 @@
 //
 // Bound of the split kernel.  The entries' bytes: a warp streams its tiles of 16 entries through a ring of its own, with as many
 // stages as the CTAs that fit an SM leave, so that nothing but the copies is waited for.  64 requests of up to 16384 entries, eight kv
-// heads, 1081 MB: 178 us, 6.1 TB/s or 89 % of the measured copy rate; two requests of 140001 entries, 145 MB: 32.5 us, 4.5 TB/s, with
+// heads, 1081 MB: 175 us, 6.2 TB/s or 91 % of the measured copy rate; two requests of 140001 entries, 145 MB: 32.5 us, 4.5 TB/s, with
 // the first copies and the join of the parts (7 us) no longer small.
 #include <algorithm>
 
