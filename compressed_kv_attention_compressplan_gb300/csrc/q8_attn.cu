@@ -110,9 +110,9 @@ __global__ __launch_bounds__(kPlanThreads) void plan_q8_attn_kernel(const AttnPl
         min(s_ql[*b] - 1, static_cast<uint32_t>((static_cast<unsigned long long>(j + 1) * M - 1) / G));
     return static_cast<uint32_t>(q8_visible(s_kv[*b], s_ql[*b] - 1 - last, s_ph[*b], a.ratio));
   };
-  const uint32_t start = a.g.start_cost, grain = a.g.grain;
+  const uint32_t start = a.g.start_cost, grain = a.g.grain;  // grain is a power of two
   auto cost_of = [&](uint32_t seen) -> unsigned long long {
-    return start + (static_cast<unsigned long long>(seen) + grain - 1) / grain * grain;
+    return start + ((static_cast<unsigned long long>(seen) + grain - 1) & ~static_cast<unsigned long long>(grain - 1));
   };
   unsigned long long mine = 0;
   for (uint32_t i = t; i < nt; i += kPlanThreads) {
@@ -121,9 +121,14 @@ __global__ __launch_bounds__(kPlanThreads) void plan_q8_attn_kernel(const AttnPl
   }
   unsigned long long total;
   const unsigned long long before = block_exclusive<kPlanThreads>(mine, &total, s_scan[0]);
-  unsigned long long quota = (total + a.g.ctas - 1) / a.g.ctas;
+  // 32-bit divisions where they do: a 64-bit one is some forty instructions that wait for one another, and there were ten
+  const bool narrow = total <= 0x7FFFFFFFull;
+  unsigned long long quota = narrow ? (static_cast<uint32_t>(total) + a.g.ctas - 1) / a.g.ctas : (total + a.g.ctas - 1) / a.g.ctas;
   quota = max(static_cast<unsigned long long>(a.g.min_quota), quota);
-  quota = (quota + a.g.grain - 1) / a.g.grain * a.g.grain;
+  quota = (quota + grain - 1) & ~static_cast<unsigned long long>(grain - 1);
+  auto shares = [&](unsigned long long x) -> unsigned long long {  // x / quota, x <= total + quota
+    return narrow ? static_cast<uint32_t>(x) / static_cast<uint32_t>(quota) : x / quota;
+  };
 
   unsigned long long pos0 = 0;
   uint32_t item0 = 0, part0 = 0, split0 = 0;
@@ -133,7 +138,7 @@ __global__ __launch_bounds__(kPlanThreads) void plan_q8_attn_kernel(const AttnPl
     const unsigned long long cost = nt <= kPlanThreads ? mine : i < nt ? cost_of(tile_of(i, &b)) : 0;
     unsigned long long cost_sum = total, packed_sum, p = before;  // a single strip's sums are known
     if (nt > kPlanThreads) p = pos0 + block_exclusive<kPlanThreads>(cost, &cost_sum, s_scan[0]);
-    if (cost) n = static_cast<uint32_t>((p + cost - 1) / quota - p / quota) + 1;
+    if (cost) n = static_cast<uint32_t>(shares(p + cost - 1) - shares(p)) + 1;
     // items (32 bits), parts (16) and splits (16) of the strip, in one scan: parts are at most twice the CTAs
     const unsigned long long pk = n | (static_cast<unsigned long long>(n > 1 ? n : 0) << 32) |
                                   (static_cast<unsigned long long>(n > 1) << 48);
@@ -154,7 +159,7 @@ __global__ __launch_bounds__(kPlanThreads) void plan_q8_attn_kernel(const AttnPl
       uint32_t rb;
       const uint32_t seen = tile_of(i0 + s, &rb);
       const unsigned long long len = cost_of(seen);
-      const unsigned long long P = s_pos[s], cut = P / quota;
+      const unsigned long long P = s_pos[s], cut = shares(P);
       const uint32_t c = k - s_item[s];
       const unsigned long long lo = c == 0 ? P : (cut + c) * quota;
       const unsigned long long hi = min(P + len, (cut + c + 1) * quota);
@@ -170,10 +175,11 @@ __global__ __launch_bounds__(kPlanThreads) void plan_q8_attn_kernel(const AttnPl
       r.phase = s_ph[rb];
       r.part = static_cast<int32_t>(s_part[s]);
       r.chunk = c;
-      r.chunks = static_cast<uint32_t>((P + len - 1) / quota - cut) + 1;
+      r.chunks = static_cast<uint32_t>(shares(P + len - 1) - cut) + 1;
       r.reserved = 0;
       items[k] = r;
-      if (lo % quota == 0) first[lo / quota] = k;
+      const unsigned long long cta = shares(lo);
+      if (cta * quota == lo) first[cta] = k;
     }
     pos0 += cost_sum;
     item0 = end;
@@ -182,7 +188,7 @@ __global__ __launch_bounds__(kPlanThreads) void plan_q8_attn_kernel(const AttnPl
     __syncthreads();
   }
   if (t == 0) {
-    const uint32_t ctas = static_cast<uint32_t>((total + quota - 1) / quota);
+    const uint32_t ctas = static_cast<uint32_t>(shares(total + quota - 1));
     first[ctas] = item0;
     head->items = item0;
     head->ctas = ctas;

@@ -363,8 +363,9 @@ def test_nan_values_of_few_rows(heads, D, latent):
 
 
 def test_plan_covers_every_tile_once():
-    """The items of a plan, read back: for each tile they tile its entries, and parts are numbered without gaps."""
-    for seed in range(12):
+    """The items of a plan, read back: for each tile they tile its entries, and parts are numbered without gaps.  The last
+    six seeds' lengths add up to more than 32 bits hold."""
+    for seed in range(18):
         r = np.random.RandomState(seed)
         B, H, heads = int(r.randint(1, 40)), int(r.choice([1, 2, 8])), 8 * int(r.choice([1, 2]))
         D = int(r.choice([64, 128, 256, 512]))
@@ -372,6 +373,8 @@ def test_plan_covers_every_tile_once():
         q_lens = r.randint(0, 5, B)
         q_lens[0] = max(q_lens[0], int(r.choice([1, 200])))
         ratio = int(r.choice([1, 4, 128]))
+        if seed >= 12:
+            lens, ratio = r.randint(1 << 29, 1 << 30, B), 1
         seq = _seq(lens, q_lens, ratio)
         pool = torch.zeros(1, H, 16, D, dtype=torch.uint8, device=DEV).view(torch.float8_e4m3fn)
         cache = ckv.Q8Cache(pool, torch.ones(1, H, device=DEV))
