@@ -551,6 +551,9 @@ def new_q8_cache(num_blocks: int, n_kv_heads: int, block_tokens: int, head_dim: 
     return Q8Cache(k, ks, v, vs)
 
 
+# Calls that make tensors make them on the stream that they run on: memory of the current stream could still be in use
+# there, and a workspace is free again when the call returns.
+#
 # These calls are made once a layer on few microseconds of work, so what they check is checked in few Python steps:
 # a tensor's address is taken, with the checks that make it usable, by _at(); lengths by _lens().
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
@@ -649,6 +652,10 @@ def plan_q8_store(cache: Q8Cache, rid: torch.Tensor, kv_lens: torch.Tensor, new_
                   status: Optional[torch.Tensor] = None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
     """The blocks that a step's new rows touch: ``(plan [cap, 16] u8, counts [4] int32)``.  ``kv_lens`` counts the
     new entries (``new_lens``, 0 allowed); the plan serves every layer of the step."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return plan_q8_store(cache, rid, kv_lens, new_lens, num_rows, block_table, capacity, pad_invalid, plan, counts,
+                                 status)
     lib = _lib or load_library()
     arg, dev = _q8(cache)
     batch, (rid_at, kv_at, new_at) = _lens(dev, rid, kv_lens, new_lens)
@@ -703,6 +710,9 @@ def plan_q8_attn(cache: Q8Cache, n_heads: int, ratio: int, rid: torch.Tensor, se
                  status: Optional[torch.Tensor] = None, stream=None) -> Q8AttnPlan:
     """Shares a step's attention out over the SMs.  Request b's ``extend_lens[b]`` queries are the last tokens of
     ``seq_lens[b]``; it has ``kv_lens[b]`` entries of ``ratio`` tokens each.  Serves every layer of the step."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return plan_q8_attn(cache, n_heads, ratio, rid, seq_lens, extend_lens, kv_lens, num_q, buffer, status)
     lib = _lib or load_library()
     arg, dev = _q8(cache)
     batch, (rid_at, seq_at, ext_at, kv_at) = _lens(dev, rid, seq_lens, extend_lens, kv_lens)
@@ -731,6 +741,9 @@ def q8_attn(cache: Q8Cache, q: torch.Tensor, plan: Q8AttnPlan, block_table: torc
             status: Optional[torch.Tensor] = None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
     """Softmax attention of ``q`` (bf16 ``[num_q, n_heads, head_dim]``) over the cache: ``(out, lse)``, ``lse`` fp32
     ``[num_q, n_heads]``.  Queries that see nothing get zeros and -inf."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return q8_attn(cache, q, plan, block_table, scale, out, lse, out_dtype, workspace, status)
     lib = _lib or load_library()
     arg, dev = _q8(cache)
     buffer, n_heads, ratio, batch, num_q = plan
@@ -794,6 +807,10 @@ def q8_evict(cache: Q8Cache, weights: torch.Tensor, rid: torch.Tensor, kv_lens: 
     """Keeps each request's ``budget`` entries of largest weight, its first ``sinks`` and newest ``recent`` among
     them, and moves them (with their weights) into the blocks of ``dst_table``, which must be no source's.  Returns
     ``(kept [batch, budget] int32 old positions, -1 past the end, new_lens [batch] int64)``."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return q8_evict(cache, weights, rid, kv_lens, block_table, dst_table, budget, sinks, recent, kept, new_lens,
+                            status)
     lib = _lib or load_library()
     arg, dev = _q8(cache)
     batch, (rid_at, kv_at) = _lens(dev, rid, kv_lens)

@@ -849,6 +849,28 @@ def test_on_another_stream():
     assert torch.equal(out, want)
 
 
+def test_what_a_call_makes_belongs_to_its_stream():
+    """The current stream still has work to do on memory that it has given back: results on another are not in it."""
+    w = World(52, [300], 1, 128, 16, False)
+    q, cache, table = w.queries([64], 8).to(DEV), w.cache(), i32(w.table)
+    args = i64(w.rid), i64([300]), i64([64]), i64([300])
+    plan = ckv.plan_q8_attn(cache, 8, 1, *args, 64)
+    want, want_lse = ckv.q8_attn(cache, q, plan, table, 0.05, out_dtype=torch.float32)
+    other, weights = ckv.new_q8_cache(64, 1, 16, 128), torch.rand(64, 16, device=DEV)
+    src, dst, zero = i32([list(range(30))]), i32([list(range(30, 60))]), i64([0])
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(20_000_000)  # some milliseconds
+    junk = [torch.full_like(x, 7) for x in (plan.buffer, want, want_lse, ckv.q8_attn_workspace(cache, 8, 1, 64))]
+    del junk
+    plan2 = ckv.plan_q8_attn(cache, 8, 1, *args, 64, stream=s)
+    out, lse = ckv.q8_attn(cache, q, plan2, table, 0.05, out_dtype=torch.float32, stream=s)
+    kept, lens = ckv.q8_evict(other, weights, zero, args[3], src, dst, 400, stream=s)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and torch.equal(lse, want_lse)
+    assert kept[0, :300].tolist() == list(range(300)) and lens.tolist() == [300]
+
+
 def test_shapes_that_the_binding_refuses():
     w = World(52, [20], 2, 128, 16, False)
     cache, q = w.cache(), w.queries([1], 4).to(DEV)
