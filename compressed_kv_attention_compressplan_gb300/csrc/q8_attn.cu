@@ -220,7 +220,7 @@ struct Cfg {
   static constexpr int kD = kDw * kNp;
   static constexpr int kGroups = kAttnWarps / kNp;  // warp groups, each with tiles of its own
   static constexpr int kTileBytes = kTile * kDw * (kShared ? 1 : 2);
-  static constexpr int kStageBytes = kTileBytes + 16;  // and the tile's two scales
+  static constexpr int kStageBytes = kTileBytes;
   // As many stages as let kPerSm CTAs share an SM's 227 KB.  Eight rows and 128 channels, 64 requests of 8000 entries (1.05 GB): 174 us with two
   // CTAs of six stages, 182 with three of four, 188 to 194 with four of three, 280 with one of twelve.
   static constexpr int kPerSm = kDw == 64 ? 4 : kDw == 128 ? (kRows == 8 ? 2 : 3) : 2;
@@ -228,6 +228,7 @@ struct Cfg {
                                  : kDw == 128 && kRows == 8 ? (kShared ? 9 : 6)
                                  : kDw == 128               ? (kShared ? 7 : 4)
                                                             : (kShared ? 5 : 3);
+  static_assert(kStages <= 16, "");
   static constexpr int kRingBytes = kAttnWarps * kStages * kStageBytes;
   static constexpr int kMergeStride = kD + 4;  // floats
   static constexpr int kMergeBytes = kGroups * kRows * kMergeStride * 4;
@@ -377,16 +378,22 @@ __global__ __launch_bounds__(kAttnThreads, (Cfg<kDw, kNp, kShared, kRows>::kPerS
             if (!kShared) cp_async16(dst + kTile * kDw + tile_off<kDw>(t, cc), v + t * C::kD + cc * 16, n);
           }
         }
-        if (lane < 2) {
-          const float* s = (kShared || lane == 0 ? a.c.k_scale : a.c.v_scale) + bh;
-          cp_async4(dst + C::kTileBytes + lane * 4, s);
-        }
-        if (lane == 2) sts_u32(dst + C::kTileBytes + 8, ok ? 1u : 0u);
       }
       cp_async_commit();
     };
 #pragma unroll
     for (int s = 0; s < C::kStages - 1; ++s) issue(s);
+    // Their scales are kept as the block numbers are, a lane to a tile; the next 32 are asked for half way through.  A block that does
+    // not exist gets a negative one.
+    float ks_now, vs_now, ks_next = 1.0f, vs_next = -1.0f;
+    auto ask_scales = [&](int32_t b, float& k, float& v) {
+      const bool ok = b >= 0 && static_cast<uint32_t>(b) < a.c.num_blocks;
+      const size_t at = static_cast<size_t>(ok ? b : 0) * H + h;
+      k = ld_ahead(a.c.k_scale + at);
+      v = kShared ? k : ld_ahead(a.c.v_scale + at);
+      v = ok ? v : -1.0f;
+    };
+    ask_scales(blocks_now, ks_now, vs_now);
 
     // ---- query fragments of rows g and g + 8 (few rows: of row g, and what belongs to it handed to the lanes with columns 2q and 2q + 1)
     uint32_t qf[kDw / 16][4];
@@ -429,8 +436,13 @@ __global__ __launch_bounds__(kAttnThreads, (Cfg<kDw, kNp, kShared, kRows>::kPerS
       __syncwarp();  // every lane's copies of this tile are in; every lane has read the tile before it
       issue(i + C::kStages - 1);  // into the stage that the previous tile left
       const uint32_t st = ring + (i % C::kStages) * C::kStageBytes;
-      const float k_scale = lds_f32(st + C::kTileBytes), v_scale = lds_f32(st + C::kTileBytes + 4);
-      const bool tile_ok = lds_u32(st + C::kTileBytes + 8) != 0;
+      if ((i & 31) == 16) ask_scales(blocks_next, ks_next, vs_next);  // (the copies are less than 16 tiles ahead)
+      if ((i & 31) == 0 && i != 0) {
+        ks_now = ks_next;
+        vs_now = vs_next;
+      }
+      const float k_scale = __shfl_sync(0xFFFFFFFFu, ks_now, i & 31), v_scale = __shfl_sync(0xFFFFFFFFu, vs_now, i & 31);
+      const bool tile_ok = v_scale > 0.0f;
       // scores
       float s[kHalves][4];
       if constexpr (kFew)
