@@ -190,7 +190,7 @@ template <int kD>
 struct StreamCfg {
   static constexpr int kStages = kD == 64 ? 8 : kD == 128 ? 4 : kD == 256 ? 5 : 3;
   static constexpr int kPerSm = kD <= 128 ? 2 : 1;
-  static constexpr int kStageBytes = kTile * kD + 16;  // and the tile's scale
+  static constexpr int kStageBytes = kTile * kD;
   static constexpr int kSmem = kWarps * kStages * kStageBytes;
   static constexpr int kRun = 32;  // tiles that are summed over the heads at once: one to a lane
 };
@@ -234,6 +234,7 @@ __global__ __launch_bounds__(kThreads, StreamCfg<kD>::kPerSm) void q8_weigh_stre
     for (uint32_t i = lane; i < C::kRun * kTile; i += 32) s_sum[warp][i] = 0.0f;
     __syncwarp();
     for (uint32_t h = head0; h < H; h += a.head_warps) {
+      const float scale = ld_ahead(a.c.k_scale + static_cast<size_t>(blk_ok ? blk : 0) * H + h);  // lane t's tile's
       for (uint32_t r0 = 0; r0 < rows; r0 += kCols) {
         auto issue = [&](uint32_t i) {
           if (i < mine) {
@@ -248,7 +249,6 @@ __global__ __launch_bounds__(kThreads, StreamCfg<kD>::kPerSm) void q8_weigh_stre
               const uint32_t c = x * 32 + lane, tok = c / (kD / 16), cc = c % (kD / 16);
               cp_async16(dst + tile_off<kD>(tok, cc), k + tok * kD + cc * 16, ok ? 16u : 0u);
             }
-            if (lane == 0) cp_async4(dst + kTile * kD, a.c.k_scale + bh);
           }
           cp_async_commit();
         };
@@ -280,7 +280,7 @@ __global__ __launch_bounds__(kThreads, StreamCfg<kD>::kPerSm) void q8_weigh_stre
           __syncwarp();  // every lane's copies of this tile are in; every lane has read the tile before it
           issue(i + C::kStages - 1);
           const uint32_t st = ring + (i % C::kStages) * C::kStageBytes, t = part + i * parts;
-          const float ks = lds_f32(st + kTile * kD);
+          const float ks = __shfl_sync(0xFFFFFFFFu, scale, t);
           float s[kCols / 8][4] = {};
 #pragma unroll
           for (int j = 0; j < kD / 64; ++j) {
