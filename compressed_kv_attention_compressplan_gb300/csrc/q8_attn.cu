@@ -23,7 +23,7 @@
 //
 // Bound of the split kernel.  The entries' bytes: a warp streams its tiles of 16 entries through a ring of its own, with as many
 // stages as the CTAs that fit an SM leave, so that nothing but the copies is waited for.  64 requests of up to 16384 entries, eight kv
-// heads, 1081 MB: 175 us, 6.2 TB/s or 91 % of the measured copy rate; two requests of 140001 entries, 145 MB: 32.5 us, 4.5 TB/s, with
+// heads, 1081 MB: 168 us, 6.4 TB/s or 95 % of the measured copy rate; two requests of 140001 entries, 145 MB: 31 us, 4.7 TB/s, with
 // the first copies and the join of the parts (7 us) no longer small.
 #include <algorithm>
 
@@ -221,8 +221,9 @@ struct Cfg {
   static constexpr int kGroups = kAttnWarps / kNp;  // warp groups, each with tiles of its own
   static constexpr int kTileBytes = kTile * kDw * (kShared ? 1 : 2);
   static constexpr int kStageBytes = kTileBytes;
-  // As many stages as let kPerSm CTAs share an SM's 227 KB.  Eight rows and 128 channels, 64 requests of 8000 entries (1.05 GB): 174 us with two
-  // CTAs of six stages, 182 with three of four, 188 to 194 with four of three, 280 with one of twelve.
+  // As many stages as let kPerSm CTAs share an SM's 227 KB.  Eight rows and 128 channels, 64 requests of 8000 entries (1.05 GB): 162 us with two
+  // CTAs of six stages, 186 with three of four; before that by a few instructions a tile more 174, 182, 188 with four of three and 280
+  // with one of twelve.
   static constexpr int kPerSm = kDw == 64 ? 4 : kDw == 128 ? (kRows == 8 ? 2 : 3) : 2;
   static constexpr int kStages = kDw == 64                ? (kShared ? 8 : 6)
                                  : kDw == 128 && kRows == 8 ? (kShared ? 9 : 6)
@@ -294,7 +295,8 @@ namespace {
 // Up to eight rows (decode with groups of as many heads) the products are transposed: 16 entries are m, and the eight
 // rows n, of the scores; 16 channels are m, and the rows n again, of the values.  That is half the products, exponentials and
 // accumulators; the weights cross from entries to rows with one 8 x 8 transposition for eight entries.  One request of 777 entries 8.7 us against
-// 9.4 with sixteen rows, 32 of 300 14.8 against 18.2, 64 of 8000 174 against 179.
+// 9.4 with sixteen rows, 32 of 300 14.8 against 18.2, 64 of 8000 174 against 179.  What a tile costs in instructions counts to the end: a copy for its scales, sizes on whole tiles'
+// copies and a division were 8 % of the 64 requests' time.
 template <int kDw, int kNp, bool kShared, int kRows>
 __global__ __launch_bounds__(kAttnThreads, (Cfg<kDw, kNp, kShared, kRows>::kPerSm)) void q8_attn_kernel(const AttnArgs a) {
   using C = Cfg<kDw, kNp, kShared, kRows>;

@@ -15,8 +15,8 @@
 // and exponentials, and an entry's sum crosses four lanes.  The CTAs share the batch's tiles out evenly, and a CTA's warps take
 // one head each and are summed in head order once per run of 512 entries.
 //
-// 32 requests, 132 MB of keys: 30.6 us, 64 % of the measured copy rate; five stages a warp instead of four 31.4 us, six (one CTA to
-// an SM) 39, the kernel below 90.
+// 32 requests, 132 MB of keys: 29.9 us, 65 % of the measured copy rate (30.5 with a copy for each tile's scale; then five stages a warp instead of
+// four 31.4, six, i.e. one CTA to an SM, 39), the kernel below 90.
 //
 // Many rows (a window of queries): the products and exponentials bound it.  Up to 128
 // channels the tensor cores take it (q8_weigh_tc.cu); from 256 on a warp holds 16 entries
