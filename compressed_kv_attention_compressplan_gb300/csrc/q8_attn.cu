@@ -247,9 +247,9 @@ int q8_attn_geom(const Q8Cache& c, uint32_t batch, uint32_t num_q, uint32_t n_he
   if (static_cast<uint64_t>(num_q) * g->group > 0x7FFFFFFFull) return CKV_ERR_SIZE;  // row numbers are 32-bit
   // The split kernel's tiles are 8 or 16 rows, and it reads a request's entries once for each; the tensor-core kernels' are 256, or 64
   // from 256 channels on, at nearly the same cost for a few rows as for all.  Where they cross, by rows of a request and kv head (us,
-  // split kernel / tensor cores, 32 to 64 requests of 4096 entries): 64 channels 105 / 112 at 64 and 149 / 113 at 96; 128 channels
-  // 155 / 187 at 48 and 203 / 189 at 64; 256 channels 46 / 64 at 16 and 67 / 65 at 32; 512 channels 64 / 72 at 16 and 107 / 75 at 32.
-  const uint64_t most = c.head_dim == 64 ? 64 : c.head_dim == 128 ? 48 : 16;
+  // split kernel / tensor cores, 32 to 64 requests of 4096 entries): 64 channels 98 / 113 at 64 and 122 / 112 at 80; 128 channels
+  // 184 / 188 at 64 and 222 / 190 at 80; 256 channels 62 / 65 at 32 and 82 / 68 at 48; 512 channels 62 / 72 at 16 and 102 / 75 at 32.
+  const uint64_t most = c.head_dim <= 128 ? 64 : c.head_dim == 256 ? 32 : 16;
   g->tc = static_cast<uint64_t>(num_q) * g->group > most * batch && batch > 0;
   if (g->tc) {
     g->rows = c.head_dim <= 128 ? 256 : 64;

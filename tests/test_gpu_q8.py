@@ -81,8 +81,8 @@ def status():
 def attn_bounds(D, lens_max, out, lse, mag, big, flat, vmax, out_bf16, eight_bit=False):
     """Worst cases: D products and lens_max weighted values summed in fp32 with truncated additions (2^-23 each), the
     exponent's argument a few roundings of its size (2^-22), the weights rounded to fp16 (2^-11), weights under
-    2^-31 of the largest dropped (of values up to twice vmax), bf16 output (2^-8).  eight_bit: from 256 channels and
-    more than 16 rows on the fp16 weights are three e5m2 terms (each leaves 2^-3 of what it is given: 2^-9), dropped under
+    2^-31 of the largest dropped (of values up to twice vmax), bf16 output (2^-8).  eight_bit: with more than 32 rows
+    at 256 channels, or 16 at 512, the fp16 weights are three e5m2 terms (each leaves 2^-3 of what it is given: 2^-9), dropped under
     2^-17 / 2^6 = 2^-23, and a query value is off by up to 2^-17 of its row's largest."""
     eps = big * (D + 8) * 2.0 ** -23 + (big * 1.5 + 60) * 2.0 ** -22 + (flat * 2.0 ** -17 if eight_bit else 0)
     e = eps[..., None]
@@ -94,7 +94,7 @@ def attn_bounds(D, lens_max, out, lse, mag, big, flat, vmax, out_bf16, eight_bit
 
 
 def eight_bit(w, q_lens, heads):
-    return w.D >= 256 and int(np.sum(q_lens)) * (heads // w.H) > 16 * len(q_lens)
+    return w.D >= 256 and int(np.sum(q_lens)) * (heads // w.H) > (32 if w.D == 256 else 16) * len(q_lens)
 
 
 def run_attn(w, q, seq, q_lens, heads, ratio, out_dtype=torch.bfloat16, scale=None, lens=None, **kw):
@@ -271,6 +271,11 @@ ATTN = [  # lens, q_lens, heads, H, D, T, latent, ratio
     ([500], [1], 7, 1, 128, 32, True, 4),
     ([90, 60, 0], [5, 1, 0], 4, 1, 512, 32, False, 1),
     ([40, 700], [3, 1], 8, 2, 128, 64, False, 1),
+    # more rows on both sides of where another kernel takes over
+    ([170], [16], 4, 1, 128, 16, False, 1),
+    ([170], [13], 5, 1, 128, 16, True, 1),
+    ([100], [8], 4, 1, 256, 64, False, 1),
+    ([100], [11], 3, 1, 256, 64, True, 1),
 ]
 
 
