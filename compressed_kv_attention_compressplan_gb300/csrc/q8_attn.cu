@@ -396,6 +396,7 @@ __global__ __launch_bounds__(kAttnThreads, (Cfg<kDw, kNp, kShared, kRows>::kPerS
       v = ok ? v : -1.0f;
     };
     ask_scales(blocks_now, ks_now, vs_now);
+    __syncthreads();  // s_nan and s_any_nan are cleared before any warp marks them; the copies are on their way meanwhile
 
     // ---- query fragments of rows g and g + 8 (few rows: of row g, and what belongs to it handed to the lanes with columns 2q and 2q + 1)
     uint32_t qf[kDw / 16][4];

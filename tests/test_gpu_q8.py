@@ -367,6 +367,26 @@ def test_nan_values_of_few_rows(heads, D, latent):
     assert np.array_equal(got, want)
 
 
+@pytest.mark.parametrize("heads,D", [(8, 64), (12, 64), (4, 128), (16, 128), (2, 256), (12, 256), (8, 512), (16, 512)])
+@pytest.mark.parametrize("latent", [False, True])
+def test_nan_values_in_the_first_tile_of_items_that_follow_one_another(heads, D, latent):
+    """A thousand requests of a few entries, several to a CTA, each with one NaN in its only tile: a warp marks it as
+    soon as the copies are in, and the marks of the item before must be gone by then, and its own must stay."""
+    B = 1000
+    lens = 5 + np.arange(B) % 11
+    w = World(18, lens, 1, D, 16, latent)
+    chan = np.arange(B) * 37 % D
+    for b in range(0, B, 2):  # every other request's
+        (w.k if latent else w.v)[w.table[w.rid[b], 0], 0, b % lens[b], chan[b]] = 0xFF
+    _, _, out, lse, st = run_attn(w, w.queries([1] * B, heads), lens, [1] * B, heads, 1, torch.float32)
+    assert st == 0
+    want = np.zeros((B, heads, D), bool)
+    for b in range(0, B, 2):
+        want[b, :, slice(None) if latent else chan[b]] = True
+    assert np.array_equal(np.isnan(out.cpu().numpy()), want)
+    assert np.array_equal(np.isnan(lse.cpu().numpy()), np.repeat((np.arange(B) % 2 == 0)[:, None] & latent, heads, 1))
+
+
 def test_plan_covers_every_tile_once():
     """The items of a plan, read back: for each tile they tile its entries, and parts are numbered without gaps.  The last
     six seeds' lengths add up to more than 32 bits hold."""
