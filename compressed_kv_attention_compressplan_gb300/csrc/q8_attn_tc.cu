@@ -503,7 +503,7 @@ __global__ __launch_bounds__((TcCfg<kD, kShared>::kThreads), 1) void q8_attn_tc_
       }
       if (n_tiles > 0) w.wait<kShort>(&sh.pv_done, (tiles_before + n_tiles - 1) & 1);
       tc_fence_after();
-      const int any_nan = sh.any_nan;
+      const bool any_nan = n_tiles > 0 && sh.any_nan != 0;  // without tiles nothing orders this read after the clearing
 #pragma unroll 1
       for (int b = 0; b < C::kSlices; ++b) {
         const int d = b * 128 + entry;  // this lane's channel

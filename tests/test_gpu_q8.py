@@ -387,6 +387,30 @@ def test_nan_values_in_the_first_tile_of_items_that_follow_one_another(heads, D,
     assert np.array_equal(np.isnan(lse.cpu().numpy()), np.repeat((np.arange(B) % 2 == 0)[:, None] & latent, heads, 1))
 
 
+@pytest.mark.parametrize("heads,D,latent", [(64, 512, True), (48, 512, False), (64, 256, True), (40, 256, False), (96, 128, False),
+                                             (80, 64, True)])
+def test_nan_values_beside_shares_without_entries(heads, D, latent):
+    """Tiles of about a hundred entries, cut so that some CTAs end with a tile's start and none of its entries, after a
+    tile with a NaN: what the one marked must not show in the other's part."""
+    B = 500
+    lens = 80 + np.arange(B) % 40
+    w = World(20, lens, 1, D, 16, latent)
+    for b in range(0, B, 2):
+        (w.k if latent else w.v)[w.table[w.rid[b], 4], 0, b % 16, 9] = 0xFF
+    _, plan, out, lse, st = run_attn(w, w.queries([1] * B, heads), lens, [1] * B, heads, 1, torch.float32)
+    assert st == 0
+    raw = plan.buffer.cpu().numpy()
+    head = raw[:64].view(np.uint32)
+    off = (64 + 4 * (int(head[8]) + 1) + 63) // 64 * 64
+    off = (off + 4 * int(head[8]) + 63) // 64 * 64
+    it = raw[off:off + 48 * int(head[0])].view(np.uint32).reshape(-1, 12)
+    assert (it[:, 4] == it[:, 5]).any()  # there are such shares
+    want = np.zeros((B, heads, D), bool)
+    for b in range(0, B, 2):
+        want[b, :, slice(None) if latent else 9] = True
+    assert np.array_equal(np.isnan(out.cpu().numpy()), want)
+
+
 def test_plan_covers_every_tile_once():
     """The items of a plan, read back: for each tile they tile its entries, and parts are numbered without gaps.  The last
     six seeds' lengths add up to more than 32 bits hold."""
