@@ -300,6 +300,9 @@ __global__ __launch_bounds__((RowsCfg<kD, kShared>::kThreads), 1) void q8_attn_r
         sh.both[half][n] = l;
         pair_sync(pair);
         l = sh.both[0][n] + sh.both[1][n];
+        // (the last tile's scores are in, so its marks are) a latent cache's NaN is a NaN score of the rows that see it
+        const bool any_nan = n_tiles > 0 && sh.any_nan != 0;
+        if (kShared && any_nan && sh.nan[0] < see) l = __int_as_float(0x7FFFFFFF);
         uint32_t again = n;  // (the place is worked out here and not kept over the tiles)
         asm volatile("" : "+r"(again));
         const uint32_t rho = item.row0 + (in ? again : 0), i = rho / G, hg = rho % G;
@@ -314,7 +317,6 @@ __global__ __launch_bounds__((RowsCfg<kD, kShared>::kThreads), 1) void q8_attn_r
         }
         w.wait<kShort>(&sh.o_done, items_before & 1);
         tc_fence_after();
-        const bool any_nan = n_tiles > 0 && sh.any_nan != 0;
         // 32 channels at a time through shared memory (the operands are done with), so that a store takes whole lines: 16 bytes a
         // lane of 32 rows took 8 k cycles of an item
         const uint32_t stage = base + warp * 4096, row_sw = lane & 7;
@@ -329,10 +331,10 @@ __global__ __launch_bounds__((RowsCfg<kD, kShared>::kThreads), 1) void q8_attn_r
 #pragma unroll
               for (int y = 0; y < 16; ++y) o[y] = 0.0f;
             }
-            if (any_nan) {
+            if (!kShared && any_nan) {
 #pragma unroll
               for (int y = 0; y < 16; ++y)
-                if (sh.nan[kShared ? 0 : c0 + c + y] < see) o[y] = __int_as_float(0x7FFFFFFF);
+                if (sh.nan[c0 + c + y] < see) o[y] = __int_as_float(0x7FFFFFFF);
             }
             const float by = item.part >= 0 ? 1.0f : inv;
 #pragma unroll

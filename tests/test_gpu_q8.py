@@ -411,6 +411,27 @@ def test_nan_values_beside_shares_without_entries(heads, D, latent):
     assert np.array_equal(np.isnan(out.cpu().numpy()), want)
 
 
+@pytest.mark.parametrize("heads,D", [(4, 64), (4, 128), (3, 256), (1, 512), (32, 64), (32, 128), (16, 256), (8, 512), (64, 512)])
+@pytest.mark.parametrize("n", [70, 128, 131, 2500])
+def test_lse_of_a_latent_row_that_sees_a_nan_is_nan(heads, D, n):
+    """A NaN entry of a latent cache is a NaN score of the rows that see it: their lse is NaN as well, whichever kernel
+    takes them and wherever in a tile the entry lies; the others' is that of a cache without it."""
+    w = World(22, [n, 60], 1, D, 16, True)
+    q, lens = w.queries([9, 9], heads), [n, 60]
+    _, _, out0, lse0, st0 = run_attn(w, q, lens, [9, 9], heads, 1, torch.float32)
+    at = n - 4  # hidden from the first five of nine queries
+    w.k[w.table[w.rid[0], at // 16], 0, at % 16, 5] = 0xFF
+    cache, _, out, lse, st = run_attn(w, q, lens, [9, 9], heads, 1, torch.float32)
+    assert st == st0 == 0
+    sees = np.zeros(18, bool)
+    sees[:9] = np.arange(9) + (n - 9) >= at
+    got = lse.cpu().numpy()
+    assert np.array_equal(np.isnan(got), np.repeat(sees[:, None], heads, 1))
+    assert np.array_equal(np.isnan(out.cpu().numpy()), np.broadcast_to(sees[:, None, None], out.shape))
+    assert np.array_equal(got[~sees], lse0.cpu().numpy()[~sees])
+    assert np.array_equal(out.cpu().numpy()[~sees], out0.cpu().numpy()[~sees])
+
+
 def test_plan_covers_every_tile_once():
     """The items of a plan, read back: for each tile they tile its entries, and parts are numbered without gaps.  The last
     six seeds' lengths add up to more than 32 bits hold."""
