@@ -9,8 +9,9 @@
 // two that puts its largest value in [2^7, 2^8) and is e4m3 + e4m3: bf16's 8 bits are 4
 // and 4, so the two are exact down to 2^-9 of that value, and under it the error is
 // at most 2^-17 of it; both are columns of one product (N = 128), whose halves are added.
-// A weight (at most 2^14, see the split kernel) is e5m2 + e5m2 + e5m2, each the nearest
-// to what the ones before leave: 2^-9 of it in all, with fp16's range below.
+// A weight (at most 2^15, see kTop) is e5m2 + e5m2 + e5m2, each the nearest
+// to what the ones before leave: off by 2^-9 of it in all, or, where a weight is so small that
+// the terms reach e5m2's last place, by 2^-17, 2^-29 of the row's largest.
 //
 // The accumulators of 512 channels by 64 rows take 256 columns of tensor memory, so the
 // whole width of a latent entry fits beside two buffers of scores, and its entries are read
@@ -39,6 +40,11 @@ namespace {
 
 constexpr uint32_t kSlice8 = kEntries * 128;  // bytes of 128 channels of a tile
 constexpr uint32_t kTerm = kEntries * 64;     // bytes of one term of a tile's weights
+// A row's reference is raised to kRest under its maximum when an exponent passes it by kTop.  e5m2 ends at 57344 above and at 2^-16
+// below, so a row's largest weight stands close under the top: what is left of a weight under 2^-16 is lost, and that is
+// 2^-17, 2^-29 of a largest weight of 2^12.  Latent decode and chunks of 512 queries over 8192 entries of 512 and of 256 channels: 79, 315 and
+// 286 us at 14 and 6, where a weight lost up to 2^-23 of the largest; 81, 320 and 286 at 15 and 12; 82, 327 and 287 at 15.5 and 13.
+constexpr float kTop = 15.0f, kRest = 12.0f;
 
 template <int kD, bool kShared>
 struct TcCfg {
@@ -405,7 +411,7 @@ __global__ __launch_bounds__((TcCfg<kD, kShared>::kThreads), 1) void q8_attn_tc_
         }
 #pragma unroll
         for (int c = 0; c < 16; ++c) most = fmaxf(most, x[c]);
-        if (group_any(bar, most > 14.0f || unset)) {  // raise the rows' references
+        if (group_any(bar, most > kTop || unset)) {  // raise the rows' references
           float top = -INFINITY;
 #pragma unroll
           for (int c = 0; c < 16; ++c) {
@@ -421,7 +427,7 @@ __global__ __launch_bounds__((TcCfg<kD, kShared>::kThreads), 1) void q8_attn_tc_
             top = fmaxf(fmaxf(sh.red[0][c], sh.red[1][c]), fmaxf(sh.red[2][c], sh.red[3][c]));
             // a row's first entry sets its reference, wherever that is; later ones only raise it
             const bool fresh = sh.set[c] == 0 && top > -INFINITY;
-            const float up = fresh ? top - 6.0f : fmaxf(0.0f, top - 6.0f);
+            const float up = fresh ? top - kRest : fmaxf(0.0f, top - kRest);
             sh.neg_m[c] -= up;
             sh.up[c] = up;
             sh.fac[c] = fresh ? 1.0f : ex2(-up);

@@ -550,10 +550,13 @@ int ckv_plan_q8_attn(const ckv_q8_cache_t* cache, uint32_t n_heads, uint32_t rat
  * out [num_q, n_heads, head_dim] in out_dtype; lse (NULL: not wanted) fp32
  * [num_q, n_heads] is log(sum(exp(score))).  A query that sees nothing gets
  * zeros and lse -infinity.  Entries a query does not see, and slots past a request's
- * end, do not count whatever they hold, NaN included.  Weights are rounded to
- * fp16 (2^-11 relative; with more than 32 rows (queries times group) a request
- * on average at 256 channels, or 16 at 512, to three 8-bit terms, 2^-9, and query values under 2^-9 of their row's largest to
- * 2^-17 of it) before they meet the values; everything else is exact
+ * end, do not count whatever they hold, NaN included.  Weights, times their
+ * values' scales, are rounded before they meet the values: to fp16, off by 2^-11
+ * of themselves, or by 2^-31 of the row's largest where they are under 2^-20 of
+ * it; with more than 32 rows (queries times group) a request on average at 256
+ * channels, or 16 at 512, to three 8-bit terms, off by 2^-9 of themselves plus
+ * 2^-29 of the row's largest, and query values under 2^-9 of their row's largest
+ * are off by up to 2^-17 of it.  The sum of the weights has none of these; everything else is exact
  * or fp32.  workspace: ckv_q8_attn_workspace_bytes of device memory that no
  * other call uses meanwhile (calls on one stream may share it); its content does not
  * matter.  A block number outside the pool sets CKV_STATUS_BAD_INDEX and its

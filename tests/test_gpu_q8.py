@@ -432,6 +432,59 @@ def test_lse_of_a_latent_row_that_sees_a_nan_is_nan(heads, D, n):
     assert np.array_equal(out.cpu().numpy()[~sees], out0.cpu().numpy()[~sees])
 
 
+@pytest.mark.parametrize("depth", [14.3, 18.3, 21.3, 24.3])
+@pytest.mark.parametrize("D,latent,heads,n,first", [(512, True, 64, 3000, 0), (512, False, 32, 3000, 1700), (256, False, 48, 3000, 5),
+                                                 (256, True, 64, 3000, 2900), (512, True, 64, 100001, 3), (128, True, 96, 3000, 0),
+                                                 (128, False, 8, 3000, 40)])
+def test_many_small_weights_behind_a_large_one(depth, D, latent, heads, n, first):
+    """One entry with nearly all of a row's weight and none of the values, and many with 2^-depth of it: what the many
+    give is there.  Every SM has whole requests, so a row's entries stand under one reference.
+
+    A weight is off by 2^-9 of it (three e5m2 terms, each leaves 2^-3) and 2^-11 (fp16), and by e5m2's last 2^-17, where the
+    row's largest is 2^12 or more.  The fp16 kernels keep to the same bounds."""
+    B, T = 304, 128
+    scale = depth * math.log(2) / (8 * 14)
+    r = np.random.RandomState(23)
+    blocks = -(-n // T)
+    vals = ref.round8(r.uniform(0.5, 2.0, (n, D)))
+    k = np.zeros((n, D), np.uint8)
+    k[:, 0] = ref.round8(np.full(n, -6.0))
+    k[first, 0] = ref.round8(8.0)
+    if latent:
+        k[:, 1:] = vals[:, 1:]
+        k[first, 1:] = 0
+    vals[first] = 0
+
+    def pool(x):
+        full = np.zeros((blocks * T, D), np.uint8)
+        full[:n] = x
+        t = torch.as_tensor(full.reshape(blocks, 1, T, D), device=DEV).view(torch.float8_e4m3fn)
+        return t, torch.ones(blocks, 1, device=DEV)
+
+    cache = ckv.Q8Cache(*pool(k), *((None, None) if latent else pool(vals)))
+    table = i32(np.arange(blocks)[None])
+    q = torch.zeros(B, heads, D, dtype=torch.bfloat16, device=DEV)
+    q[:, :, 0] = 8.0
+    st, one = status(), i64([1] * B)
+    plan = ckv.plan_q8_attn(cache, heads, 1, i64([0] * B), i64([n] * B), one, i64([n] * B), B, status=st)
+    out, lse = ckv.q8_attn(cache, q, plan, table, scale, out_dtype=torch.float32, status=st)
+    torch.cuda.synchronize()
+    assert int(st[0]) == 0
+    s = np.full(n, -6.0 * 8 * scale)
+    s[first] = 64 * scale
+    p = np.exp(s - s[first])
+    v = ref.E4M3[k if latent else vals]
+    want = (p @ v) / p.sum()
+    mag = (p @ np.abs(v)) / p.sum()
+    eps = 64 * scale * (D + 8) * 2.0 ** -23 + 64 * 2.0 ** -22
+    tol = mag * (2.0 ** -9 + 2.0 ** -11 + 2 * eps + (n + 32) * 2.0 ** -23) + n * 2.0 ** -29 * np.abs(np.delete(v, first, 0)).max(0) / p.sum()
+    got = out.double().cpu().numpy()
+    sl = slice(1, None) if latent else slice(None)  # a latent cache's channel 0 is the score's
+    err = np.abs(got - want)[..., sl] - tol[sl]
+    assert (err <= 0).all(), (err.max(), want[5], got[0, 0, 5], tol[5])
+    assert np.abs(lse.cpu().numpy() - (s[first] + math.log(p.sum()))).max() <= 4 * eps
+
+
 def test_plan_covers_every_tile_once():
     """The items of a plan, read back: for each tile they tile its entries, and parts are numbered without gaps.  The last
     six seeds' lengths add up to more than 32 bits hold."""
