@@ -304,7 +304,8 @@ __global__ __launch_bounds__((TcCfg<kD, kShared>::kThreads), 1) void q8_attn_tc_
 #pragma unroll
           for (int s = 16; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, s));
           const int ex = min(126, 7 - (static_cast<int>(__float_as_uint(m) >> 23) - 127));
-          const float up = pow2f(ex);
+          // e4m3 has no infinity: a row with one is NaN, as its scores' softmax is
+          const float up = m == INFINITY ? __int_as_float(0x7FFFFFFF) : pow2f(ex);
           // eight channels at a time; term t of the row is row n + 64 t of the operand
 #pragma unroll
           for (int e = 0; e < kPer / 8; ++e) {

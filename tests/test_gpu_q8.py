@@ -485,6 +485,25 @@ def test_many_small_weights_behind_a_large_one(depth, D, latent, heads, n, first
     assert np.abs(lse.cpu().numpy() - (s[first] + math.log(p.sum()))).max() <= 4 * eps
 
 
+@pytest.mark.parametrize("heads,D,latent", [(4, 64, False), (4, 128, True), (3, 256, False), (1, 512, True), (40, 64, True), (40, 128, False),
+                                             (40, 256, False), (40, 256, True), (20, 512, False), (64, 512, True)])
+@pytest.mark.parametrize("bad", [math.inf, -math.inf, math.nan])
+def test_queries_that_are_not_finite(heads, D, latent, bad):
+    """inf * k is an infinity of either sign or NaN, so the softmax over such scores is NaN, in that row alone."""
+    w = World(24, [300, 40], 1, D, 16, latent)
+    q = w.queries([2, 2], heads)
+    _, _, out0, lse0, st0 = run_attn(w, q, [300, 40], [2, 2], heads, 1, torch.float32)
+    q[1, heads - 1, 7] = q[2, 0, D - 1] = bad
+    _, _, out, lse, st = run_attn(w, q, [300, 40], [2, 2], heads, 1, torch.float32)
+    assert st == st0 == 0
+    nan = np.zeros((4, heads), bool)
+    nan[1, heads - 1] = nan[2, 0] = True
+    assert np.array_equal(np.isnan(lse.cpu().numpy()), nan)
+    assert np.array_equal(np.isnan(out.cpu().numpy()), np.repeat(nan[..., None], D, 2))
+    assert np.array_equal(lse.cpu().numpy()[~nan], lse0.cpu().numpy()[~nan])
+    assert np.array_equal(out.cpu().numpy()[~nan], out0.cpu().numpy()[~nan])
+
+
 def test_plan_covers_every_tile_once():
     """The items of a plan, read back: for each tile they tile its entries, and parts are numbered without gaps.  The last
     six seeds' lengths add up to more than 32 bits hold."""
