@@ -96,6 +96,7 @@ def load_library():
         lib.ckv_capacity_q8_store.restype = u32
         lib.ckv_plan_q8_store.argtypes = [qc, vp, vp, vp, u32, u32, vp, u64, u32, u32, i32, vp, vp, vp, vp]
         lib.ckv_q8_store.argtypes = [qc, i32, vp, vp, u32, vp, vp, u32, vp, vp]
+        lib.ckv_q8_store_reset.argtypes = [qc, i32, vp, vp, u32, vp, vp, u32, vp, vp, vp]
         for f in (lib.ckv_q8_attn_plan_bytes, lib.ckv_q8_attn_workspace_bytes):
             f.argtypes = [qc, u32, u32, u32]
             f.restype = u64
@@ -677,8 +678,11 @@ def plan_q8_store(cache: Q8Cache, rid: torch.Tensor, kv_lens: torch.Tensor, new_
 
 
 def q8_store(cache: Q8Cache, k_rows: torch.Tensor, v_rows: Optional[torch.Tensor], plan: torch.Tensor,
-             counts: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None, stream=None) -> None:
-    """Quantises rows ``[num_rows, n_kv_heads, head_dim]`` into the cache; ``v_rows`` is None for a latent cache."""
+             counts: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None, stream=None,
+             weights: Optional[torch.Tensor] = None) -> None:
+    """Quantises rows ``[num_rows, n_kv_heads, head_dim]`` into the cache; ``v_rows`` is None for a latent cache.
+    ``weights`` (as ``q8_weigh`` takes them): set to 0 where rows are stored, so that a slot that is used again does not keep
+    its last owner's."""
     lib = _lib or load_library()
     arg, dev = _q8(cache)
     n = k_rows.shape[0]
@@ -690,8 +694,13 @@ def q8_store(cache: Q8Cache, k_rows: torch.Tensor, v_rows: Optional[torch.Tensor
     _store_plan(plan, 0)
     if counts is not None:
         _is(counts, "counts", torch.int32, 4)
-    rc = lib.ckv_q8_store(arg, dtype_code(k_rows.dtype), _at(dev, k_rows), _at(dev, v_rows), n, _at(dev, plan),
-                          _at(dev, counts), plan.shape[0], _at(dev, status), _stream_of(dev, stream))
+    args = (arg, dtype_code(k_rows.dtype), _at(dev, k_rows), _at(dev, v_rows), n, _at(dev, plan), _at(dev, counts),
+            plan.shape[0])
+    if weights is None:
+        rc = lib.ckv_q8_store(*args, _at(dev, status), _stream_of(dev, stream))
+    else:
+        _is(weights, "weights", _FP32, arg.num_blocks, arg.block_tokens)
+        rc = lib.ckv_q8_store_reset(*args, _at(dev, weights), _at(dev, status), _stream_of(dev, stream))
     if rc:
         _q8_error(rc, "ckv_q8_store")
 

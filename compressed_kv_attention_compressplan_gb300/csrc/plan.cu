@@ -806,6 +806,6 @@ const char* ckv_error_string(int code) {
   }
 }
 
-int ckv_version(void) { return 230; }
+int ckv_version(void) { return 240; }
 
 }  // extern "C"

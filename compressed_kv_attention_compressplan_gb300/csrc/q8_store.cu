@@ -115,10 +115,11 @@ struct StoreArgs {
   const uint32_t* d_counts;
   uint32_t capacity;
   uint32_t sides;
+  float* weights;  // NULL: left alone
   uint32_t* d_status;
 };
 
-constexpr int kStoreThreads = 128;
+constexpr int kStoreThreads = 128;  // at least the slots of a block
 
 // 16 channels of a row as fp32.
 __device__ __forceinline__ void load16(const float* p, float (&x)[16]) {
@@ -176,6 +177,9 @@ __global__ __launch_bounds__(kStoreThreads) void q8_store_kernel(const StoreArgs
       if (threadIdx.x == 0) status_or(a.d_status, CKV_STATUS_BAD_INDEX);
       continue;
     }
+    // new entries have had no attention yet, whatever the slots' last owners had
+    if (a.weights != nullptr && blockIdx.y == 0 && threadIdx.x < cnt)
+      a.weights[static_cast<size_t>(block) * T + off + threadIdx.x] = 0.0f;
     for (uint32_t u = blockIdx.y; u < units; u += gridDim.y) {
       const bool second = u >= H;
       const uint32_t h = second ? u - H : u;
@@ -234,6 +238,32 @@ __global__ __launch_bounds__(kStoreThreads) void q8_store_kernel(const StoreArgs
   }
 }
 
+int store_rows(const ckv_q8_cache_t* cache, int in_dtype, const void* k_rows, const void* v_rows, uint32_t num_rows,
+               const ckv_q8_store_plan_t* plan, const uint32_t* d_counts, uint32_t capacity, float* weights,
+               uint32_t* d_status, ckv_stream_t stream) {
+  StoreArgs a{};
+  const int rc = q8_cache_of(cache, &a.c);
+  if (rc) return rc;
+  if (in_dtype != CKV_F32 && in_dtype != CKV_BF16) return CKV_ERR_DTYPE;
+  if (num_rows > CKV_MAX_TOKENS || capacity > CKV_MAX_TOKENS) return CKV_ERR_SIZE;
+  if (num_rows == 0 || capacity == 0) return CKV_OK;
+  if (!aligned16(k_rows) || (a.c.v != nullptr) != (v_rows != nullptr) || (v_rows != nullptr && !aligned16(v_rows)))
+    return CKV_ERR_POINTER;
+  if (!aligned16(plan) || (d_counts != nullptr && !aligned_to(d_counts, 4))) return CKV_ERR_POINTER;
+  a.k_rows = k_rows;
+  a.v_rows = v_rows;
+  a.num_rows = num_rows;
+  a.plan = plan;
+  a.d_counts = d_counts;
+  a.capacity = capacity;
+  a.sides = v_rows != nullptr ? 2 : 1;
+  a.weights = weights;
+  a.d_status = d_status;
+  const dim3 grid(std::min<uint32_t>(capacity, 65536u), a.c.heads * a.sides);
+  return launch_pdl(in_dtype == CKV_BF16 ? q8_store_kernel<__nv_bfloat16> : q8_store_kernel<float>, grid,
+                    dim3(kStoreThreads), 0, reinterpret_cast<cudaStream_t>(stream), a);
+}
+
 }  // namespace
 }  // namespace ckv
 
@@ -283,26 +313,14 @@ int ckv_plan_q8_store(const ckv_q8_cache_t* cache, const int64_t* rid, const int
 int ckv_q8_store(const ckv_q8_cache_t* cache, int in_dtype, const void* k_rows, const void* v_rows, uint32_t num_rows,
                  const ckv_q8_store_plan_t* plan, const uint32_t* d_counts, uint32_t capacity, uint32_t* d_status,
                  ckv_stream_t stream) {
-  StoreArgs a{};
-  const int rc = q8_cache_of(cache, &a.c);
-  if (rc) return rc;
-  if (in_dtype != CKV_F32 && in_dtype != CKV_BF16) return CKV_ERR_DTYPE;
-  if (num_rows > CKV_MAX_TOKENS || capacity > CKV_MAX_TOKENS) return CKV_ERR_SIZE;
-  if (num_rows == 0 || capacity == 0) return CKV_OK;
-  if (!aligned16(k_rows) || (a.c.v != nullptr) != (v_rows != nullptr) || (v_rows != nullptr && !aligned16(v_rows)))
-    return CKV_ERR_POINTER;
-  if (!aligned16(plan) || (d_counts != nullptr && !aligned_to(d_counts, 4))) return CKV_ERR_POINTER;
-  a.k_rows = k_rows;
-  a.v_rows = v_rows;
-  a.num_rows = num_rows;
-  a.plan = plan;
-  a.d_counts = d_counts;
-  a.capacity = capacity;
-  a.sides = v_rows != nullptr ? 2 : 1;
-  a.d_status = d_status;
-  const dim3 grid(std::min<uint32_t>(capacity, 65536u), a.c.heads * a.sides);
-  return launch_pdl(in_dtype == CKV_BF16 ? q8_store_kernel<__nv_bfloat16> : q8_store_kernel<float>, grid,
-                    dim3(kStoreThreads), 0, reinterpret_cast<cudaStream_t>(stream), a);
+  return store_rows(cache, in_dtype, k_rows, v_rows, num_rows, plan, d_counts, capacity, nullptr, d_status, stream);
+}
+
+int ckv_q8_store_reset(const ckv_q8_cache_t* cache, int in_dtype, const void* k_rows, const void* v_rows,
+                       uint32_t num_rows, const ckv_q8_store_plan_t* plan, const uint32_t* d_counts, uint32_t capacity,
+                       float* weights, uint32_t* d_status, ckv_stream_t stream) {
+  if (!aligned_to(weights, 4)) return CKV_ERR_POINTER;
+  return store_rows(cache, in_dtype, k_rows, v_rows, num_rows, plan, d_counts, capacity, weights, d_status, stream);
 }
 
 }  // extern "C"

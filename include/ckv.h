@@ -524,10 +524,16 @@ int ckv_plan_q8_store(const ckv_q8_cache_t* cache, const int64_t* rid, const int
  * step's rows gets its scale from them; one that earlier rows began keeps the
  * larger of its scale and theirs, and when that grows the earlier entries are
  * rewritten with it (exact, but for e4m3's subnormals).  Slots after the
- * stored rows are left as they were.  No two records may name one block. */
+ * stored rows are left as they were.  No two records may name one block.
+ * ckv_q8_store_reset also sets weights (fp32 [num_blocks, block_tokens], see
+ * ckv_q8_weigh) to 0 in the slots that rows are stored in. */
 int ckv_q8_store(const ckv_q8_cache_t* cache, int in_dtype, const void* k_rows, const void* v_rows, uint32_t num_rows,
                  const ckv_q8_store_plan_t* plan, const uint32_t* d_counts, uint32_t capacity, uint32_t* d_status,
                  ckv_stream_t stream);
+
+int ckv_q8_store_reset(const ckv_q8_cache_t* cache, int in_dtype, const void* k_rows, const void* v_rows,
+                       uint32_t num_rows, const ckv_q8_store_plan_t* plan, const uint32_t* d_counts, uint32_t capacity,
+                       float* weights, uint32_t* d_status, ckv_stream_t stream);
 
 /* Attention plan: shares the step's work out evenly over the SMs.  Request b
  * has extend_lens[b] >= 0 queries (the next ones of the ragged num_q), the
@@ -573,7 +579,10 @@ int ckv_q8_attn(const ckv_q8_cache_t* cache, uint32_t n_heads, uint32_t ratio, f
  * queries and heads of the softmax weight it received (0 <= decay <= 1; 0
  * overwrites).  weights is fp32 [num_blocks, block_tokens]; q, ratio, scale and
  * the lengths as in the attention, lse its output.  Deterministic.  Two
- * requests that share a block must not both be in the batch. */
+ * requests that share a block must not both be in the batch.  A slot that a new
+ * entry takes (in a block that is used again, or behind the last entry that an
+ * eviction kept) holds what its last owner received: ckv_q8_store_reset clears
+ * it, or the caller does. */
 int ckv_q8_weigh(const ckv_q8_cache_t* cache, uint32_t n_heads, uint32_t ratio, float scale, float decay,
                  const void* q, const float* lse, uint32_t num_q, const int64_t* rid, const int64_t* seq_lens,
                  const int64_t* extend_lens, const int64_t* kv_lens, uint32_t batch, const int32_t* block_table,
@@ -596,9 +605,10 @@ int ckv_q8_evict(const ckv_q8_cache_t* cache, float* weights, const int64_t* rid
 /* ------------------------------------------------------------------ misc */
 /* Short text for a CKV_OK / CKV_ERR_* code (static storage). */
 const char* ckv_error_string(int code);
-/* Library ABI version: major * 100 + minor (230: 2.00's decode boundary-row
+/* Library ABI version: major * 100 + minor (240: 2.00's decode boundary-row
  * list and prefetch hints, 2.10's prefill prefetch hints, 2.20's fused C4
- * decode + norm + RoPE + store, and the 8-bit paged cache). */
+ * decode + norm + RoPE + store, 2.30's 8-bit paged cache, and its store that
+ * clears weights). */
 int ckv_version(void);
 
 #ifdef __cplusplus

@@ -747,6 +747,51 @@ def test_weights_sum_to_the_heads_and_overwrite():
     assert torch.equal(weights.nan_to_num(-1), again.nan_to_num(-1))  # bit for bit
 
 
+def test_weights_of_slots_that_are_used_again():
+    """A pool whose weights hold what earlier owners received (NaN among it): entries stored with the weights start at
+    0, also behind the last entry that an eviction kept, and every other slot is left as it was."""
+    H, D, T, heads, scale = 2, 64, 16, 4, 0.125
+    r = np.random.RandomState(32)
+    cache, st = ckv.new_q8_cache(16, H, T, D), status()
+    old = r.random_sample((16, T)).astype(np.float32) * 100
+    old[3, 2] = old[5] = np.nan
+    weights = torch.as_tensor(old, device=DEV)
+    table, dst = i32([[5, 0, 3], [9, 1, 12]]), i32([[2, 14], [7, 11]])
+    rid = i64([0, 1])
+
+    def rows(n):
+        return [torch.as_tensor(r.standard_normal((n, H, D))).bfloat16().to(DEV) for _ in range(2)]
+
+    def step(kv, new, tab):
+        plan, counts = ckv.plan_q8_store(cache, rid, i64(kv), i64(new), int(np.sum(new)), tab, status=st)
+        ckv.q8_store(cache, *rows(int(np.sum(new))), plan, counts, status=st, weights=weights)
+
+    want = old.copy()
+    step([35, 20], [35, 20], table)
+    for blocks, n in (([5, 0, 3], 35), ([9, 1, 12], 20)):
+        for p in range(n):
+            want[blocks[p // T], p % T] = 0
+    assert np.array_equal(weights.cpu().numpy(), want, equal_nan=True)
+    q = torch.as_tensor(r.standard_normal((2, heads, D))).bfloat16().to(DEV)
+    one = i64([1, 1])
+    plan = ckv.plan_q8_attn(cache, heads, 1, rid, i64([35, 20]), one, i64([35, 20]), 2, status=st)
+    _, lse = ckv.q8_attn(cache, q, plan, table, scale, status=st)
+    ckv.q8_weigh(cache, q, lse, weights, 1, rid, i64([35, 20]), one, i64([35, 20]), table, scale, status=st)
+    got = weights.cpu().numpy()
+    for blocks, n in (([5, 0, 3], 35), ([9, 1, 12], 20)):
+        assert abs(sum(got[blocks[p // T], p % T] for p in range(n)) - heads) <= 1e-4
+    kept, lens = ckv.q8_evict(cache, weights, rid, i64([35, 20]), table, dst, 18, 1, 4, status=st)
+    before = weights.cpu().numpy()
+    step([21, 19], [3, 1], dst)
+    want = before.copy()
+    want[14, 2:5] = want[11, 2] = 0
+    assert lens.tolist() == [18, 18] and np.array_equal(weights.cpu().numpy(), want, equal_nan=True)
+    torch.cuda.synchronize()
+    assert int(st[0]) == 0
+    with pytest.raises(ValueError):
+        ckv.q8_store(cache, *rows(1), torch.zeros(1, 16, dtype=torch.uint8, device=DEV), weights=weights[:, :8])
+
+
 # ----------------------------------------------------------------------------------------------------------- evict
 EVICT = [  # lens, budget, sinks, recent, H, D, T, latent
     ([100], 40, 4, 10, 1, 64, 16, True),

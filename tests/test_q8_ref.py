@@ -107,6 +107,19 @@ def test_store_refusals(lib):
     assert store(_arg(), cap=0) == 0
 
 
+def test_store_reset_refusals(lib):
+    vp = ctypes.c_void_p
+
+    def store(w, dt=1, rows=4, k=vp(16)):
+        return lib.ckv_q8_store_reset(_arg(), dt, k, None, rows, vp(16), None, 4, w, None, None)
+
+    assert store(None) == -4
+    assert store(vp(18)) == -4
+    assert store(vp(16), dt=7) == -5
+    assert store(vp(16), k=vp(8)) == -4
+    assert store(vp(16), rows=0) == 0
+
+
 def test_attention_refusals(lib):
     vp, f = ctypes.c_void_p, ctypes.c_float
     need = lib.ckv_q8_attn_plan_bytes(_arg(), 8, 2, 4)
