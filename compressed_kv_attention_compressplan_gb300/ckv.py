@@ -639,11 +639,18 @@ def _store_plan(plan: torch.Tensor, capacity: int) -> None:
         raise ValueError("a store plan is a uint8 tensor [capacity, 16]")
 
 
+def _counts(**counts: int) -> None:
+    """For counts of which one is negative or past 32 bits, which ctypes would take modulo 2^32."""
+    raise ValueError("counts must be from 0 to 2^32 - 1 (got %s)" % ", ".join(f"{k} {v}" for k, v in counts.items()))
+
+
 def _q8_error(rc: int, func: str):
     raise CkvError(rc, func, load_library().ckv_error_string(rc).decode())
 
 
 def capacity_q8_store(batch: int, num_rows: int, block_tokens: int) -> int:
+    if (batch | num_rows | block_tokens) >> 32:
+        _counts(batch=batch, num_rows=num_rows, block_tokens=block_tokens)
     return int(load_library().ckv_capacity_q8_store(batch, num_rows, block_tokens))
 
 
@@ -660,6 +667,8 @@ def plan_q8_store(cache: Q8Cache, rid: torch.Tensor, kv_lens: torch.Tensor, new_
     lib = _lib or load_library()
     arg, dev = _q8(cache)
     batch, (rid_at, kv_at, new_at) = _lens(dev, rid, kv_lens, new_lens)
+    if (num_rows | (capacity or 0)) >> 32:
+        _counts(num_rows=num_rows, capacity=capacity or 0)
     if capacity is None:
         capacity = lib.ckv_capacity_q8_store(batch, num_rows, arg.block_tokens)
     if plan is None:
@@ -725,6 +734,8 @@ def plan_q8_attn(cache: Q8Cache, n_heads: int, ratio: int, rid: torch.Tensor, se
     lib = _lib or load_library()
     arg, dev = _q8(cache)
     batch, (rid_at, seq_at, ext_at, kv_at) = _lens(dev, rid, seq_lens, extend_lens, kv_lens)
+    if (n_heads | ratio | num_q) >> 32:
+        _counts(n_heads=n_heads, ratio=ratio, num_q=num_q)
     if buffer is None:
         size = max(lib.ckv_q8_attn_plan_bytes(arg, n_heads, batch, num_q), 16)
         buffer = torch.empty(size, dtype=torch.uint8, device=rid.device)
@@ -740,6 +751,8 @@ def plan_q8_attn(cache: Q8Cache, n_heads: int, ratio: int, rid: torch.Tensor, se
 
 def q8_attn_workspace(cache: Q8Cache, n_heads: int, batch: int, num_q: int) -> torch.Tensor:
     """Workspace for ``q8_attn`` calls of this shape; calls that may run at the same time need one each."""
+    if (n_heads | batch | num_q) >> 32:
+        _counts(n_heads=n_heads, batch=batch, num_q=num_q)
     n = load_library().ckv_q8_attn_workspace_bytes(_q8(cache)[0], n_heads, batch, num_q)
     return torch.empty(max(n, 16), dtype=torch.uint8, device=cache.k.device)
 
@@ -796,6 +809,8 @@ def q8_weigh(cache: Q8Cache, q: torch.Tensor, lse: torch.Tensor, weights: torch.
     batch, (rid_at, seq_at, ext_at, kv_at) = _lens(dev, rid, seq_lens, extend_lens, kv_lens)
     if q.dim() != 3:
         raise ValueError("q is bf16 [num_q, n_heads, head_dim]")
+    if ratio >> 32:
+        _counts(ratio=ratio)
     num_q, n_heads, _ = q.shape
     _is(q, "q", torch.bfloat16, num_q, n_heads, arg.head_dim)
     _is(lse, "lse", torch.float32, num_q, n_heads)
@@ -823,8 +838,8 @@ def q8_evict(cache: Q8Cache, weights: torch.Tensor, rid: torch.Tensor, kv_lens: 
     lib = _lib or load_library()
     arg, dev = _q8(cache)
     batch, (rid_at, kv_at) = _lens(dev, rid, kv_lens)
-    if budget < 0 or sinks < 0 or recent < 0:
-        raise ValueError("budget, sinks and recent are counts")
+    if (budget | sinks | recent) >> 32:
+        _counts(budget=budget, sinks=sinks, recent=recent)
     _is(weights, "weights", torch.float32, arg.num_blocks, arg.block_tokens)
     src, stride, reqs = _table(dev, block_table)
     dst, dst_stride, dst_reqs = _table(dev, dst_table)

@@ -1093,6 +1093,31 @@ def test_shapes_that_the_binding_refuses():
             pytest.fail(f"case {k} was taken")
 
 
+def test_counts_past_32_bits_are_refused():
+    """2^32 and a little more, which modulo 2^32 would be ordinary counts."""
+    w = World(53, [20], 2, 128, 16, False)
+    cache, q, big = w.cache(), w.queries([1], 4).to(DEV), 1 << 32
+    rid, one, table = i64(w.rid), i64([20]), i32(w.table)
+    weights, lse = torch.zeros(w.blocks, 16, device=DEV), torch.zeros(1, 4, device=DEV)
+    bad = [
+        lambda: ckv.plan_q8_store(cache, rid, one, i64([1]), big + 1, table, capacity=1),
+        lambda: ckv.plan_q8_attn(cache, big + 4, 1, rid, one, i64([1]), one, 1),
+        lambda: ckv.plan_q8_attn(cache, 4, big + 1, rid, one, i64([1]), one, 1),
+        lambda: ckv.plan_q8_attn(cache, 4, 1, rid, one, i64([1]), one, big + 1),
+        lambda: ckv.q8_attn_workspace(cache, 4, 1, big + 1),
+        lambda: ckv.q8_attn_workspace(cache, 4, -1, 1),
+        lambda: ckv.q8_weigh(cache, q, lse, weights, big + 1, rid, one, i64([1]), one, table, 0.1),
+        lambda: ckv.q8_weigh(cache, q, lse, weights, -1, rid, one, i64([1]), one, table, 0.1),
+        lambda: ckv.q8_evict(cache, weights, rid, one, table, table, 8, big, 0),
+        lambda: ckv.q8_evict(cache, weights, rid, one, table, table, 8, 0, big + 1),
+        lambda: ckv.q8_evict(cache, weights, rid, one, table, table, big + 8),
+    ]
+    for k, f in enumerate(bad):
+        with pytest.raises(ValueError):
+            f()
+            pytest.fail(f"case {k} was taken")
+
+
 @pytest.mark.parametrize("D,latent", [(128, False), (64, True), (512, True), (256, False)])
 def test_waits_that_run_out_are_reported_and_leave_the_context_usable(D, latent):
     """The kernels whose roles hand tiles to one another, with a wait limit of a nanosecond: they end, say so, and the

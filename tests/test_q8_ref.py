@@ -205,6 +205,12 @@ def test_record_sizes():
     assert ctypes.sizeof(ckv.Q8CacheArg) == 48
 
 
+def test_capacity_refuses_counts_past_32_bits(lib):
+    for args in ((1 << 32, 4, 16), (1, (1 << 32) + 4, 16), (1, -1, 16), (1, 4, (1 << 32) + 16)):
+        with pytest.raises(ValueError):
+            ckv.capacity_q8_store(*args)
+
+
 def test_the_binding_takes_cuda_tensors_only():
     cpu = ckv.Q8Cache(torch.zeros(2, 1, 16, 64, dtype=torch.uint8).view(torch.float8_e4m3fn), torch.ones(2, 1))
     i64 = torch.zeros(1, dtype=torch.int64)
