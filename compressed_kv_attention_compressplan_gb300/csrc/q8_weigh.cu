@@ -42,18 +42,18 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], 
 
 template <int kD>
 __global__ __launch_bounds__(kThreads) void q8_weigh_rows_kernel(const WeighArgs a) {
-  constexpr int kKj = kD / 64, kNt = 1;  // tiles of 16 entries to a warp
+  constexpr int kKj = kD / 64;
   __shared__ uint32_t s_unit[CKV_MAX_BATCH];
   __shared__ uint32_t s_q[CKV_MAX_BATCH];
   __shared__ uint32_t s_scan[kWarps + 1];
   __shared__ unsigned long long s_scan64[kWarps + 1];
-  __shared__ float s_sum[kWarps][kNt * kTile];
+  __shared__ float s_sum[kWarps][kTile];
   pdl_wait();
   pdl_release();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, q = lane & 3;
   const uint32_t T = a.c.block_tokens, H = a.c.heads, G = a.group;
-  const uint32_t unit_entries = kWarps / a.head_warps * (kNt * kTile);
+  const uint32_t unit_entries = kWarps / a.head_warps * kTile;
 
   const uint32_t units = scan_requests<kThreads>(a, unit_entries, s_unit, s_q, s_scan, s_scan64);
   for (uint32_t u = blockIdx.x; u < units; u += gridDim.x) {
@@ -62,49 +62,37 @@ __global__ __launch_bounds__(kThreads) void q8_weigh_rows_kernel(const WeighArgs
     const uint32_t q_len = static_cast<uint32_t>(a.extend_lens[b]);
     const uint32_t phase = a.ratio - 1 - static_cast<uint32_t>(a.seq_lens[b]) % a.ratio;
     const uint32_t rows = q_len * G;
-    const uint32_t e0 = (u - s_unit[b]) * unit_entries + warp / a.head_warps * (kNt * kTile);
-    float sum[kNt][2][2] = {};  // entries 16 t + 8 n + 2q + {0, 1}
-    int32_t block[kNt];
-    bool any = false;
-#pragma unroll
-    for (int t = 0; t < kNt; ++t) {
-      const uint32_t e = e0 + t * kTile;
-      block[t] = -1;
-      if (e < kv_len) {
-        block[t] = __ldg(a.table + static_cast<size_t>(a.rid[b]) * a.stride + e / T);
-        if (static_cast<uint32_t>(block[t]) >= a.c.num_blocks) {
-          if (lane == 0) status_or(a.d_status, CKV_STATUS_BAD_INDEX);
-          block[t] = -1;
-        }
+    const uint32_t e0 = (u - s_unit[b]) * unit_entries + warp / a.head_warps * kTile;
+    float sum[2][2] = {};  // entries 8 n + 2q + {0, 1}
+    int32_t block = -1;
+    if (e0 < kv_len) {
+      block = __ldg(a.table + static_cast<size_t>(a.rid[b]) * a.stride + e0 / T);
+      if (static_cast<uint32_t>(block) >= a.c.num_blocks) {
+        if (lane == 0) status_or(a.d_status, CKV_STATUS_BAD_INDEX);
+        block = -1;
       }
-      any |= block[t] >= 0;
     }
-    if (any) {
+    if (block >= 0) {
       for (uint32_t h = warp % a.head_warps; h < H; h += a.head_warps) {
-        uint32_t kf[kNt][2][kKj * 4][2];
-        float f[kNt];
+        uint32_t kf[2][kKj * 4][2];
+        const size_t bh = static_cast<size_t>(block) * H + h;
+        const uint8_t* k = a.c.k + (bh * T + e0 % T) * kD;
+        const float f = a.scale_log2 * __ldg(a.c.k_scale + bh);
 #pragma unroll
-        for (int t = 0; t < kNt; ++t) {
-          const uint32_t e = e0 + t * kTile;
-          const size_t bh = static_cast<size_t>(max(block[t], 0)) * H + h;
-          const uint8_t* k = a.c.k + (bh * T + e % T) * kD;
-          f[t] = a.scale_log2 * __ldg(a.c.k_scale + bh);
+        for (int n = 0; n < 2; ++n) {
 #pragma unroll
-          for (int n = 0; n < 2; ++n) {
+          for (int j = 0; j < kKj; ++j) {
+            const uint4 w = ld_stream16_if(k + static_cast<size_t>(n * 8 + g) * kD + (j * 4 + q) * 16, true);
+            const uint32_t x[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-            for (int j = 0; j < kKj; ++j) {
-              const uint4 w = ld_stream16_if(k + static_cast<size_t>(n * 8 + g) * kD + (j * 4 + q) * 16, block[t] >= 0);
-              const uint32_t x[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-              for (int s = 0; s < 4; ++s) {
-                kf[t][n][j * 4 + s][0] = f16x2_to_bf16x2(q8_lo_f16x2(x[s]));
-                kf[t][n][j * 4 + s][1] = f16x2_to_bf16x2(q8_hi_f16x2(x[s]));
-              }
+            for (int s = 0; s < 4; ++s) {
+              kf[n][j * 4 + s][0] = f16x2_to_bf16x2(q8_lo_f16x2(x[s]));
+              kf[n][j * 4 + s][1] = f16x2_to_bf16x2(q8_hi_f16x2(x[s]));
             }
           }
         }
         for (uint32_t r0 = 0; r0 < rows; r0 += 16) {
-          float s[kNt][2][4] = {};
+          float s[2][4] = {};
           float off[2];
           int64_t vis[2];
           const __nv_bfloat16* p[2];
@@ -134,23 +122,17 @@ __global__ __launch_bounds__(kThreads) void q8_weigh_rows_kernel(const WeighArgs
               af[1] = st & 1 ? x1.z : x1.x;
               af[2] = st & 1 ? x0.w : x0.y;
               af[3] = st & 1 ? x1.w : x1.y;
-#pragma unroll
-              for (int t = 0; t < kNt; ++t) {
-                mma_bf16(s[t][0], af, kf[t][0][j * 4 + st][0], kf[t][0][j * 4 + st][1]);
-                mma_bf16(s[t][1], af, kf[t][1][j * 4 + st][0], kf[t][1][j * 4 + st][1]);
-              }
+              mma_bf16(s[0], af, kf[0][j * 4 + st][0], kf[0][j * 4 + st][1]);
+              mma_bf16(s[1], af, kf[1][j * 4 + st][0], kf[1][j * 4 + st][1]);
             }
           }
 #pragma unroll
-          for (int t = 0; t < kNt; ++t) {
+          for (int n = 0; n < 2; ++n) {
 #pragma unroll
-            for (int n = 0; n < 2; ++n) {
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const int64_t at = e0 + t * kTile + n * 8 + 2 * q + (e & 1);
-                const float w = ex2(fmaf(s[t][n][e], f[t], off[e >> 1]));
-                sum[t][n][e & 1] += at < vis[e >> 1] ? w : 0.0f;
-              }
+            for (int e = 0; e < 4; ++e) {
+              const int64_t at = e0 + n * 8 + 2 * q + (e & 1);
+              const float w = ex2(fmaf(s[n][e], f, off[e >> 1]));
+              sum[n][e & 1] += at < vis[e >> 1] ? w : 0.0f;
             }
           }
         }
@@ -158,28 +140,19 @@ __global__ __launch_bounds__(kThreads) void q8_weigh_rows_kernel(const WeighArgs
     }
     // rows of the fragment (the lanes of one column), then the heads' warps in order
 #pragma unroll
-    for (int t = 0; t < kNt; ++t) {
+    for (int n = 0; n < 2; ++n) {
 #pragma unroll
-      for (int n = 0; n < 2; ++n) {
+      for (int e = 0; e < 2; ++e) {
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-#pragma unroll
-          for (int x = 4; x < 32; x <<= 1) sum[t][n][e] += __shfl_xor_sync(0xFFFFFFFFu, sum[t][n][e], x);
-          if (g == 0) s_sum[warp][t * kTile + n * 8 + 2 * q + e] = sum[t][n][e];
-        }
+        for (int x = 4; x < 32; x <<= 1) sum[n][e] += __shfl_xor_sync(0xFFFFFFFFu, sum[n][e], x);
+        if (g == 0) s_sum[warp][n * 8 + 2 * q + e] = sum[n][e];
       }
     }
     __syncthreads();
-    if (warp % a.head_warps == 0) {
-#pragma unroll
-      for (int t = 0; t < kNt; ++t) {
-        const uint32_t e = e0 + t * kTile;
-        if (lane < kTile && block[t] >= 0 && e + lane < kv_len) {
-          float w = 0.0f;
-          for (uint32_t x = 0; x < a.head_warps; ++x) w += s_sum[warp + x][t * kTile + lane];
-          put_weight(a, block[t], e % T + lane, w);
-        }
-      }
+    if (warp % a.head_warps == 0 && lane < kTile && block >= 0 && e0 + lane < kv_len) {
+      float w = 0.0f;
+      for (uint32_t x = 0; x < a.head_warps; ++x) w += s_sum[warp + x][lane];
+      put_weight(a, block, e0 % T + lane, w);
     }
     __syncthreads();
   }
@@ -338,10 +311,11 @@ __global__ __launch_bounds__(kThreads, StreamCfg<kD>::kPerSm) void q8_weigh_stre
 
 template <int kD>
 int launch_weigh(const WeighArgs& a, cudaStream_t s) {
-  // Rows of a request and kv head: up to 32 the keys are streamed, once for every 8 or 16 of them.
+  // Rows of a request and kv head: up to 64 on average the keys are streamed, once for every 8 or 16 of them.
   const uint64_t all = static_cast<uint64_t>(a.num_q) * a.group;
   // By rows of a request and kv head (us, streaming / the other kernel, 32 to 64 requests of 4096 entries): 64 channels 59 / 63 at 64 and
-  // 84 / 64 at 96; 128 channels 98 / 100 and 142 / 100; 256 channels 68 / 73 and 96 / 96; 512 channels 148 / 144 and 209 / 190.  Eight
+  // 84 / 64 at 96; 128 channels 98 / 100 and 142 / 100; 256 channels 68 / 73 and 96 / 96; 512 channels 148 / 144 and 209 / 190
+  // (there the two cross a little under 64).  Eight
   // columns against sixteen for at most eight rows: 18.1 / 20.9, 31.5 / 32.3, 21.4 / 24.1, 42 / 48.
   if (all <= 64ull * a.batch) {
     using C = StreamCfg<kD>;

@@ -1,6 +1,7 @@
-// tcgen05.cuh -- the 5th-generation tensor core instructions the attention
-// kernel uses: fp16 products with both operands in shared memory and the
-// fp32 accumulator in tensor memory (sm_103a).
+// tcgen05.cuh -- the 5th-generation tensor core instructions that the 8-bit
+// cache's kernels use (sm_103a): products of fp16, bf16 or 8-bit operands, A in
+// shared or in tensor memory, B in shared memory, with the fp32 accumulator in
+// tensor memory, and the loads and stores of that memory.
 #pragma once
 
 #include <stdint.h>
