@@ -28,7 +28,7 @@
 // Bound.  512 channels: a tile is 64 KB from memory, 2.8 k cycles of an SM's share of it;
 // shared memory feeds the products 128 KB and 288 KB, 3.3 k cycles.  Measured: 5.0 k a tile and 27 k an item (its 64
 // rows of queries split into terms, the first entries, the last product and 128 KB of partial results); the latent case, 140 MB and
-// 33.6 GF, takes 62 us here and 82 in all.  A tile's chain with two stages of entries -- copied 3.5 k, scores, weights 3 k, second
+// 33.6 GF, takes 67 us here (the plan 6.5 before it, the join 11 after it) and 81 in all.  A tile's chain with two stages of entries -- copied 3.5 k, scores, weights 3 k, second
 // product 2.3 k -- is what bounds it; a third stage does not fit.  Entries turned into fp16 for fp16 products took 126 us instead of
 // 109 at that point: twice the shared-memory traffic.
 #include <algorithm>

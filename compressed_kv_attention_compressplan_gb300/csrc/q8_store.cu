@@ -8,7 +8,7 @@
 // earlier entries are divided by the growth, exactly but for subnormals.
 //
 // Bound.  Many rows: the rows' bytes, read from memory for the scale and once more, from L1 or L2, for the codes.  16 requests of eight heads,
-// 255 MB: the store takes 42 us, 6.0 TB/s or 89 % of the measured copy rate (44 us with each value's magnitude taken in fp32); with the plan 47.  A decode step (a row for some of 256
+// 255 MB: the store takes 43 us, 5.9 TB/s or 88 % of the measured copy rate (2 us more with each value's magnitude taken in fp32); with the plan 47.  A decode step (a row for some of 256
 // requests) is two launches, 4.7 and 4.2 us, which the host's two calls (26 us) hide.  A CTA takes one (block, head, side), since its
 // scale needs all its rows before any is stored.
 #include <algorithm>
