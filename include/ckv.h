@@ -560,12 +560,12 @@ int ckv_plan_q8_attn(const ckv_q8_cache_t* cache, uint32_t n_heads, uint32_t rat
  * values' scales, are rounded before they meet the values: to fp16, off by 2^-11
  * of themselves, or by 2^-31 of the row's largest where they are under 2^-20 of
  * it; with more than 32 rows (queries times group) a request on average at 256
- * channels, or 16 at 512, to three 8-bit terms, off by 2^-9 of themselves plus
- * 2^-29 of the row's largest, and query values under 2^-9 of their row's largest
- * are off by up to 2^-17 of it.  The sum of the weights has none of these; everything else is exact
- * or fp32.  workspace: ckv_q8_attn_workspace_bytes of device memory that no
- * other call uses meanwhile (calls on one stream may share it); its content does not
- * matter.  A block number outside the pool sets CKV_STATUS_BAD_INDEX and its
+ * channels, or 16 at 512, to fp16 and then to three 8-bit terms, off by 2^-9 +
+ * 2^-11 of themselves plus 2^-29 of the row's largest, and there query values
+ * under 2^-9 of their row's largest are off by up to 2^-17 of it.  Everything
+ * else, the sum of the weights among it, is exact or fp32.  workspace:
+ * ckv_q8_attn_workspace_bytes of device memory that no other call uses
+ * meanwhile (calls on one stream may share it); its content does not matter.  A block number outside the pool sets CKV_STATUS_BAD_INDEX and its
  * entries do not count; a plan that does not fit the call sets it too. */
 uint64_t ckv_q8_attn_workspace_bytes(const ckv_q8_cache_t* cache, uint32_t n_heads, uint32_t batch, uint32_t num_q);
 
@@ -595,6 +595,8 @@ int ckv_q8_weigh(const ckv_q8_cache_t* cache, uint32_t n_heads, uint32_t ratio, 
  * order, with their weights, into the blocks dst_table[rid * dst_stride + ...],
  * whose scales become the largest of their sources'; the sources are left as they were and
  * may be shared.  No block of dst_table may be a source, or be named twice.
+ * An entry in a block outside the pool weighs as NaN does; if it is kept all the
+ * same, its new slot stays as it was (CKV_STATUS_BAD_INDEX).
  * kept: int32 [batch, budget], the old position of each kept entry, -1 past
  * the end; new_lens: int64 [batch]. */
 int ckv_q8_evict(const ckv_q8_cache_t* cache, float* weights, const int64_t* rid, const int64_t* kv_lens,

@@ -865,6 +865,33 @@ def test_evict_flags_bad_data():
     assert nl.cpu().tolist() == [20, 20, 0] and (kept[2] == -1).all()
 
 
+def test_evict_with_entries_in_blocks_that_do_not_exist():
+    """Such an entry weighs as NaN does (only the others are kept while there are enough); one that is kept all the same, here a
+    first entry, leaves its new slot as it was."""
+    w = World(25, [64], 1, 64, 16, True, extra=4)
+    table = w.table.copy()
+    table[w.rid[0], 0], table[w.rid[0], 2] = -1, w.blocks  # entries 0 .. 15 and 32 .. 47
+    dst = np.full((w.table.shape[0], 2), -1, np.int32)
+    dst[w.rid[0]] = w.spare[:2]
+    cache, st = w.cache(), status()
+    weights = torch.rand(w.blocks, 16, device=DEV) + 1
+    before, wb = codes(cache.k).copy(), weights.cpu().numpy().copy()
+    kept, nl = ckv.q8_evict(cache, weights, i64(w.rid), i64([64]), i32(table), i32(dst), 20, 1, 3, status=st)
+    torch.cuda.synchronize()
+    assert int(st[0]) == ckv.STATUS_BAD_INDEX and nl.tolist() == [20]
+    keep = kept.cpu().numpy()[0]
+    place = lambda p: (w.table[w.rid[0], p // 16], p % 16)
+    free = [p for p in list(range(16, 32)) + list(range(48, 61))]
+    best = sorted(sorted(free, key=lambda p: -wb[place(p)])[:16])
+    assert keep.tolist() == [0] + best + [61, 62, 63]
+    after, wa = codes(cache.k), weights.cpu().numpy()
+    d0 = dst[w.rid[0], 0]
+    assert np.array_equal(after[d0, 0, 0], before[d0, 0, 0]) and wa[d0, 0] == wb[d0, 0]
+    for i, p in enumerate(keep):
+        if i:
+            assert wa[dst[w.rid[0], i // 16], i % 16] == wb[place(p)]
+
+
 # -------------------------------------------------------------------------------------------------------- together
 def test_a_request_s_life():
     """Compressed rows through norm + RoPE into the cache, attention, weights, eviction, and on with the next rows and
