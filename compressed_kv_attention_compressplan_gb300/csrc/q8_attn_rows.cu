@@ -300,9 +300,8 @@ __global__ __launch_bounds__((RowsCfg<kD, kShared>::kThreads), 1) void q8_attn_r
         sh.both[half][n] = l;
         pair_sync(pair);
         l = sh.both[0][n] + sh.both[1][n];
-        // (the last tile's scores are in, so its marks are) a latent cache's NaN is a NaN score of the rows that see it
-        const bool any_nan = n_tiles > 0 && sh.any_nan != 0;
-        if (kShared && any_nan && sh.nan[0] < see) l = __int_as_float(0x7FFFFFFF);
+        // A latent cache's NaN is a NaN score of the rows that see it.  The last tile's scores are in, so its keys' marks are.
+        if (kShared && n_tiles > 0 && sh.any_nan != 0 && sh.nan[0] < see) l = __int_as_float(0x7FFFFFFF);
         uint32_t again = n;  // (the place is worked out here and not kept over the tiles)
         asm volatile("" : "+r"(again));
         const uint32_t rho = item.row0 + (in ? again : 0), i = rho / G, hg = rho % G;
@@ -317,6 +316,7 @@ __global__ __launch_bounds__((RowsCfg<kD, kShared>::kThreads), 1) void q8_attn_r
         }
         w.wait<kShort>(&sh.o_done, items_before & 1);
         tc_fence_after();
+        const bool any_nan = !kShared && n_tiles > 0 && sh.any_nan != 0;  // values may be marked up to their product
         // 32 channels at a time through shared memory (the operands are done with), so that a store takes whole lines: 16 bytes a
         // lane of 32 rows took 8 k cycles of an item
         const uint32_t stage = base + warp * 4096, row_sw = lane & 7;
@@ -331,7 +331,7 @@ __global__ __launch_bounds__((RowsCfg<kD, kShared>::kThreads), 1) void q8_attn_r
 #pragma unroll
               for (int y = 0; y < 16; ++y) o[y] = 0.0f;
             }
-            if (!kShared && any_nan) {
+            if (any_nan) {
 #pragma unroll
               for (int y = 0; y < 16; ++y)
                 if (sh.nan[c0 + c + y] < see) o[y] = __int_as_float(0x7FFFFFFF);

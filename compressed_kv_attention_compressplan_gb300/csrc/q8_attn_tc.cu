@@ -483,8 +483,6 @@ __global__ __launch_bounds__((TcCfg<kD, kShared>::kThreads), 1) void q8_attn_tc_
         if (lane == 0) mbar_arrive(smem_addr(&sh.p_full));
       }
       // ---- the rows' sums, then the output
-      // (the last tile's scores are in, so its marks are; without tiles nothing orders this read after the clearing)
-      const bool any_nan = n_tiles > 0 && sh.any_nan != 0;
       {
         float mine = 0.0f;
 #pragma unroll
@@ -499,8 +497,9 @@ __global__ __launch_bounds__((TcCfg<kD, kShared>::kThreads), 1) void q8_attn_tc_
         if (quarter == 0 && lane < 16) {
           const int c = c0 + lane;
           float sum = (sh.red[0][c] + sh.red[1][c]) + (sh.red[2][c] + sh.red[3][c]);
-          // a latent cache's NaN is a NaN score of the rows that see it
-          if (kShared && any_nan && sh.nan[0] < sh.vis[c]) sum = __int_as_float(0x7FFFFFFF);
+          // A latent cache's NaN is a NaN score of the rows that see it.  The last tile's scores are in, so its keys' marks are;
+          // without tiles nothing orders the read after the clearing.
+          if (kShared && n_tiles > 0 && sh.any_nan != 0 && sh.nan[0] < sh.vis[c]) sum = __int_as_float(0x7FFFFFFF);
           sh.fac[c] = sum == 0.0f ? 0.0f : __fdiv_rn(1.0f, sum);
           if (static_cast<uint32_t>(c) < rows) {
             if (item.part >= 0)
@@ -514,10 +513,11 @@ __global__ __launch_bounds__((TcCfg<kD, kShared>::kThreads), 1) void q8_attn_tc_
       }
       if (n_tiles > 0) w.wait<kShort>(&sh.pv_done, (tiles_before + n_tiles - 1) & 1);
       tc_fence_after();
+      const bool any_nan = !kShared && n_tiles > 0 && sh.any_nan != 0;  // values may be marked up to their product
 #pragma unroll 1
       for (int b = 0; b < C::kSlices; ++b) {
         const int d = b * 128 + entry;  // this lane's channel
-        const int nan_at = !kShared && any_nan ? sh.nan[d] : 0x7FFFFFFF;
+        const int nan_at = any_nan ? sh.nan[d] : 0x7FFFFFFF;
         float o[16];
         if (n_tiles > 0) {
           tmem_load16(tmem + lanes + C::kOCol + b * kN + c0, o);

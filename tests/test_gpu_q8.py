@@ -387,6 +387,23 @@ def test_nan_values_in_the_first_tile_of_items_that_follow_one_another(heads, D,
     assert np.array_equal(np.isnan(lse.cpu().numpy()), np.repeat((np.arange(B) % 2 == 0)[:, None] & latent, heads, 1))
 
 
+@pytest.mark.parametrize("heads,D", [(48, 512), (40, 256), (96, 128), (80, 64), (300, 128)])
+@pytest.mark.parametrize("n", [17, 128, 1000])
+def test_nan_values_in_the_last_slot(heads, D, n):
+    """A NaN in the very last channel of the newest entry's value, the last that a tile's values bring: seen by the last query alone,
+    hidden from the one before."""
+    B = 64
+    H = -(-heads // 256)
+    w = World(21, [n] * B, H, D, 16, False)
+    for b in range(B):
+        w.v[w.table[w.rid[b], (n - 1) // 16], H - 1, (n - 1) % 16, D - 1] = 0x7F
+    _, _, out, lse, st = run_attn(w, w.queries([2] * B, heads), [n] * B, [2] * B, heads, 1, torch.float32)
+    assert st == 0 and bool(torch.isfinite(lse).all())
+    want = np.zeros(out.shape, bool)
+    want[1::2, (H - 1) * (heads // H):, D - 1] = True
+    assert np.array_equal(np.isnan(out.cpu().numpy()), want)
+
+
 @pytest.mark.parametrize("heads,D,latent", [(64, 512, True), (48, 512, False), (64, 256, True), (40, 256, False), (96, 128, False),
                                              (80, 64, True)])
 def test_nan_values_beside_shares_without_entries(heads, D, latent):
