@@ -106,6 +106,16 @@ def load_library():
         lib.ckv_q8_weigh.argtypes = [qc, u32, u32, f32, f32, vp, vp, u32, vp, vp, vp, vp, u32, vp, u64, u32, vp, vp,
                                      vp]
         lib.ckv_q8_evict.argtypes = [qc, vp, vp, vp, u32, vp, u64, vp, u64, u32, u32, u32, u32, vp, vp, vp, vp]
+        lib.ckv_q8_rope_store.argtypes = [qc, i32, vp, u64, vp, u64, u32, vp, vp, f32, vp, u32, u32, u32, i32, vp, vp, u32,
+                                          vp, vp, vp]
+        lib.ckv_q8_bounds.argtypes = [qc, vp, vp, vp, vp, u32, vp, u64, u32, vp, vp]
+        lib.ckv_q8_block_scores.argtypes = [qc, vp, u32, u32, f32, vp, u32, vp, vp, vp, vp, u32, vp, u64, u32, u32, vp, vp,
+                                            vp]
+        lib.ckv_q8_block_select.argtypes = [vp, u32, u32, u32, u32, u32, vp, vp, vp, u32, u32, u32, u32, vp, vp, vp]
+        lib.ckv_q8_attn_blocks_workspace_bytes.argtypes = [qc, u32, u32, u32]
+        lib.ckv_q8_attn_blocks_workspace_bytes.restype = u64
+        lib.ckv_q8_attn_blocks.argtypes = [qc, u32, u32, f32, vp, u32, vp, u32, vp, vp, vp, vp, u32, vp, u64, u32, i32, vp,
+                                           vp, vp, u64, vp, vp]
         lib.ckv_error_string.argtypes = [i32]
         lib.ckv_error_string.restype = ctypes.c_char_p
         lib.ckv_version.restype = i32
@@ -859,6 +869,214 @@ def q8_evict(cache: Q8Cache, weights: torch.Tensor, rid: torch.Tensor, kv_lens: 
     if rc:
         _q8_error(rc, "ckv_q8_evict")
     return kept, new_lens
+
+
+def _rows_at(device: int, t: torch.Tensor, what: str, dtype: torch.dtype, *shape: int) -> Tuple[int, int]:
+    """Address and row stride of rows ``[n, heads, dim]`` whose rows are contiguous but may lie apart."""
+    _is(t, what, dtype, *shape)
+    n, heads, dim = shape
+    s0, s1, s2 = t.stride()
+    if t.get_device() != device:
+        raise ValueError("libckv takes CUDA tensors of one device only")
+    if (s2 != 1 and dim > 1) or (s1 != dim and heads > 1):
+        raise ValueError(f"{what}: a row's heads and channels must be contiguous")
+    return t.data_ptr(), s0 if n > 1 else heads * dim
+
+
+def q8_rope_store(cache: Q8Cache, k_rows: torch.Tensor, v_rows: Optional[torch.Tensor], plan: torch.Tensor,
+                  positions: Optional[torch.Tensor], freqs: Optional[torch.Tensor],
+                  counts: Optional[torch.Tensor] = None, rope_begin: int = 0, halves: bool = False,
+                  norm_weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                  weights: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """``q8_store`` with the keys' norm and rotation on the way.  ``k_rows`` and ``v_rows`` ``[num_rows, n_kv_heads,
+    head_dim]`` may be slices of wider rows.  Channels from ``rope_begin`` on, two for each entry of a row of ``freqs``
+    (fp32 ``[max_pos, rope_dim/2, 2]``: cos, sin), turn by row ``positions[row]`` (int64) of it, as pairs of neighbours or, with
+    ``halves``, of channels ``rope_dim/2`` apart; no ``freqs``: none does.  ``norm_weight`` (fp32 ``[head_dim]``): RMSNorm before that."""
+    lib = _lib or load_library()
+    arg, dev = _q8(cache)
+    n, dt = k_rows.shape[0], k_rows.dtype
+    k_at, k_stride = _rows_at(dev, k_rows, "k_rows", dt, n, arg.n_kv_heads, arg.head_dim)
+    if (v_rows is None) != (cache.v is None):
+        raise ValueError("v_rows go with a cache that has v")
+    v_at, v_stride = None, 0
+    if v_rows is not None:
+        v_at, v_stride = _rows_at(dev, v_rows, "v_rows", dt, n, arg.n_kv_heads, arg.head_dim)
+    _store_plan(plan, 0)
+    if counts is not None:
+        _is(counts, "counts", torch.int32, 4)
+    max_pos = rope_dim = 0
+    if freqs is not None:
+        if positions is None:
+            raise ValueError("freqs need positions")
+        _is(positions, "positions", torch.int64, n)
+        if freqs.dtype is not _FP32 or freqs.dim() != 3 or freqs.shape[2] != 2:
+            raise ValueError("freqs is fp32 [max_pos, rope_dim/2, 2]")
+        max_pos, rope_dim = freqs.shape[0], 2 * freqs.shape[1]
+    if (rope_begin | max_pos) >> 32:
+        _counts(rope_begin=rope_begin, max_pos=max_pos)
+    if norm_weight is not None:
+        _is(norm_weight, "norm_weight", _FP32, arg.head_dim)
+    if weights is not None:
+        _is(weights, "weights", _FP32, arg.num_blocks, arg.block_tokens)
+    rc = lib.ckv_q8_rope_store(arg, dtype_code(dt), k_at, k_stride, v_at, v_stride, n, _at(dev, positions),
+                               _at(dev, norm_weight), eps, _at(dev, freqs), max_pos, rope_begin, rope_dim, int(halves),
+                               _at(dev, plan), _at(dev, counts), plan.shape[0], _at(dev, weights), _at(dev, status),
+                               _stream_of(dev, stream))
+    if rc:
+        _q8_error(rc, "ckv_q8_rope_store")
+
+
+def new_q8_bounds(cache: Q8Cache) -> torch.Tensor:
+    """Storage for a cache's bounds: float8_e4m3fn ``[num_blocks, n_kv_heads, 2, head_dim]`` (zeros)."""
+    blocks, heads, _, dim = cache.k.shape
+    return torch.zeros(blocks, heads, 2, dim, dtype=torch.uint8, device=cache.k.device).view(_E4M3)
+
+
+def q8_bounds(cache: Q8Cache, bounds: torch.Tensor, rid: torch.Tensor, kv_lens: torch.Tensor, new_lens: torch.Tensor,
+              block_table: torch.Tensor, status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Renews the bounds (the largest and smallest k code of each channel) of the blocks that each request's last
+    ``new_lens`` of ``kv_lens`` entries lie in."""
+    lib = _lib or load_library()
+    arg, dev = _q8(cache)
+    batch, (rid_at, kv_at, new_at) = _lens(dev, rid, kv_lens, new_lens)
+    _is(bounds, "bounds", _E4M3, arg.num_blocks, arg.n_kv_heads, 2, arg.head_dim)
+    table, stride, reqs = _table(dev, block_table)
+    rc = lib.ckv_q8_bounds(arg, _at(dev, bounds), rid_at, kv_at, new_at, batch, table, stride, reqs, _at(dev, status),
+                           _stream_of(dev, stream))
+    if rc:
+        _q8_error(rc, "ckv_q8_bounds")
+    return bounds
+
+
+def q8_block_scores(cache: Q8Cache, bounds: torch.Tensor, q: torch.Tensor, ratio: int, rid: torch.Tensor,
+                    seq_lens: torch.Tensor, extend_lens: torch.Tensor, kv_lens: torch.Tensor, block_table: torch.Tensor,
+                    scale: float, width: Optional[int] = None, scores: Optional[torch.Tensor] = None,
+                    status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """What a score of each query (bf16 ``[num_q, n_heads, head_dim]``) with an entry of each block is at most, over the
+    heads of a kv head: fp32 ``[num_q, n_kv_heads, width]`` (by default the table's), -inf for blocks that it does not see."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return q8_block_scores(cache, bounds, q, ratio, rid, seq_lens, extend_lens, kv_lens, block_table, scale, width,
+                                   scores, status)
+    lib = _lib or load_library()
+    arg, dev = _q8(cache)
+    batch, (rid_at, seq_at, ext_at, kv_at) = _lens(dev, rid, seq_lens, extend_lens, kv_lens)
+    if q.dim() != 3:
+        raise ValueError("q is bf16 [num_q, n_heads, head_dim]")
+    num_q, n_heads, _ = q.shape
+    _is(q, "q", torch.bfloat16, num_q, n_heads, arg.head_dim)
+    _is(bounds, "bounds", _E4M3, arg.num_blocks, arg.n_kv_heads, 2, arg.head_dim)
+    table, stride, reqs = _table(dev, block_table)
+    if width is None:
+        width = stride if scores is None else scores.shape[-1]
+    if (ratio | width) >> 32:
+        _counts(ratio=ratio, width=width)
+    if scores is None:
+        scores = torch.empty((num_q, arg.n_kv_heads, width), dtype=_FP32, device=q.device)
+        scores_at = scores.data_ptr()
+    else:
+        _is(scores, "scores", _FP32, num_q, arg.n_kv_heads, width)
+        scores_at = _at(dev, scores)
+    rc = lib.ckv_q8_block_scores(arg, _at(dev, bounds), n_heads, ratio, scale, _at(dev, q), num_q, rid_at, seq_at, ext_at,
+                                 kv_at, batch, table, stride, reqs, width, scores_at, _at(dev, status),
+                                 _stream_of(dev, stream))
+    if rc:
+        _q8_error(rc, "ckv_q8_block_scores")
+    return scores
+
+
+def q8_block_select(scores: torch.Tensor, block_tokens: int, ratio: int, seq_lens: torch.Tensor,
+                    extend_lens: torch.Tensor, kv_lens: torch.Tensor, budget: int, sinks: int = 0, recent: int = 0,
+                    blocks: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
+                    stream=None) -> torch.Tensor:
+    """The blocks that each query reads for each kv head, int32 ``[num_q, n_kv_heads, budget]``, ascending, -1 behind the
+    last: the first ``sinks`` and the last ``recent`` that it sees, and of the others those of largest score (fp32
+    ``[num_q, n_kv_heads, width]``), the lower of equal ones."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return q8_block_select(scores, block_tokens, ratio, seq_lens, extend_lens, kv_lens, budget, sinks, recent,
+                                   blocks, status)
+    lib = _lib or load_library()
+    dev = scores.get_device()
+    if scores.dtype is not _FP32 or scores.dim() != 3:
+        raise ValueError("scores is fp32 [num_q, n_kv_heads, width]")
+    if dev < 0:
+        raise ValueError("libckv takes CUDA tensors only")
+    if dev != _current_device():
+        raise ValueError("the scores are not on the current device")
+    num_q, heads, width = scores.shape
+    batch, (seq_at, ext_at, kv_at) = _lens(dev, seq_lens, extend_lens, kv_lens)
+    if (num_q | width | block_tokens | ratio | budget | sinks | recent) >> 32:
+        _counts(num_q=num_q, width=width, block_tokens=block_tokens, ratio=ratio, budget=budget, sinks=sinks, recent=recent)
+    if blocks is None:
+        blocks = torch.empty((num_q, heads, budget), dtype=torch.int32, device=scores.device)
+        blocks_at = blocks.data_ptr()
+    else:
+        _is(blocks, "blocks", torch.int32, num_q, heads, budget)
+        blocks_at = _at(dev, blocks)
+    rc = lib.ckv_q8_block_select(_at(dev, scores), heads, width, block_tokens, ratio, num_q, seq_at, ext_at, kv_at, batch,
+                                 budget, sinks, recent, blocks_at, _at(dev, status), _stream_of(dev, stream))
+    if rc:
+        _q8_error(rc, "ckv_q8_block_select")
+    return blocks
+
+
+def q8_attn_blocks_workspace(cache: Q8Cache, n_heads: int, num_q: int, budget: int) -> torch.Tensor:
+    """Workspace for ``q8_attn_blocks`` calls of this shape; calls that may run at the same time need one each."""
+    if (n_heads | num_q | budget) >> 32:
+        _counts(n_heads=n_heads, num_q=num_q, budget=budget)
+    n = load_library().ckv_q8_attn_blocks_workspace_bytes(_q8(cache)[0], n_heads, num_q, budget)
+    return torch.empty(max(n, 16), dtype=torch.uint8, device=cache.k.device)
+
+
+def q8_attn_blocks(cache: Q8Cache, q: torch.Tensor, blocks: torch.Tensor, ratio: int, rid: torch.Tensor,
+                   seq_lens: torch.Tensor, extend_lens: torch.Tensor, kv_lens: torch.Tensor, block_table: torch.Tensor,
+                   scale: float, out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                   out_dtype: torch.dtype = torch.bfloat16, workspace: Optional[torch.Tensor] = None,
+                   status: Optional[torch.Tensor] = None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """``q8_attn`` of each query over the entries that it sees in its listed blocks (int32 ``[num_q, n_kv_heads, budget]``,
+    ascending, negative ones passed over): ``(out, lse)``."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return q8_attn_blocks(cache, q, blocks, ratio, rid, seq_lens, extend_lens, kv_lens, block_table, scale, out,
+                                  lse, out_dtype, workspace, status)
+    lib = _lib or load_library()
+    arg, dev = _q8(cache)
+    batch, (rid_at, seq_at, ext_at, kv_at) = _lens(dev, rid, seq_lens, extend_lens, kv_lens)
+    if q.dim() != 3 or blocks.dim() != 3:
+        raise ValueError("q is bf16 [num_q, n_heads, head_dim], blocks int32 [num_q, n_kv_heads, budget]")
+    num_q, n_heads, _ = q.shape
+    budget = blocks.shape[2]
+    _is(q, "q", torch.bfloat16, num_q, n_heads, arg.head_dim)
+    _is(blocks, "blocks", torch.int32, num_q, arg.n_kv_heads, budget)
+    if (ratio | budget) >> 32:
+        _counts(ratio=ratio, budget=budget)
+    where = q.device
+    if out is None:
+        out = torch.empty_like(q) if out_dtype is torch.bfloat16 else torch.empty(q.shape, dtype=out_dtype, device=where)
+        out_at = out.data_ptr()
+    else:
+        _is(out, "out", out.dtype, num_q, n_heads, arg.head_dim)
+        out_at = _at(dev, out)
+    if lse is None:
+        lse = torch.empty((num_q, n_heads), dtype=_FP32, device=where)
+        lse_at = lse.data_ptr()
+    else:
+        _is(lse, "lse", _FP32, num_q, n_heads)
+        lse_at = _at(dev, lse)
+    if workspace is None:
+        size = max(lib.ckv_q8_attn_blocks_workspace_bytes(arg, n_heads, num_q, budget), 16)
+        workspace = torch.empty(size, dtype=torch.uint8, device=where)
+        space_at = workspace.data_ptr()
+    else:
+        size, space_at = _bytes_of(workspace, "a workspace"), _at(dev, workspace)
+    table, stride, reqs = _table(dev, block_table)
+    rc = lib.ckv_q8_attn_blocks(arg, n_heads, ratio, scale, _at(dev, q), num_q, _at(dev, blocks), budget, rid_at, seq_at,
+                                ext_at, kv_at, batch, table, stride, reqs, dtype_code(out.dtype), out_at, lse_at,
+                                space_at, size, _at(dev, status), _stream_of(dev, stream))
+    if rc:
+        _q8_error(rc, "ckv_q8_attn_blocks")
+    return out, lse
 
 
 # ------------------------------------------------------------------------------ convenience

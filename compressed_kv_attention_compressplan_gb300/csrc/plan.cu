@@ -806,6 +806,6 @@ const char* ckv_error_string(int code) {
   }
 }
 
-int ckv_version(void) { return 240; }
+int ckv_version(void) { return 250; }
 
 }  // extern "C"

@@ -54,19 +54,12 @@ template <int kPlanThreads>
 __global__ __launch_bounds__(kPlanThreads) void plan_q8_attn_kernel(const AttnPlanArgs a) {
   __shared__ uint32_t s_rid[kPlanThreads], s_qs[kPlanThreads], s_ql[kPlanThreads], s_kv[kPlanThreads],
       s_ph[kPlanThreads], s_tile[kPlanThreads];
-  __shared__ unsigned long long s_pos[kPlanThreads];
-  __shared__ uint32_t s_item[kPlanThreads], s_part[kPlanThreads];
-  __shared__ unsigned long long s_scan[2][kPlanThreads / 32 + 1];
-  __shared__ uint32_t s_most;
+  __shared__ CutShared<kPlanThreads> s_cut;
+  auto& s_scan = s_cut.scan;
   pdl_wait();
   pdl_release();
   const uint32_t t = threadIdx.x;
-  if (t == 0) s_most = 0;  // the scans' barriers come before its use
   const uint32_t M = a.g.rows, G = a.g.group;
-  Q8Header* head = reinterpret_cast<Q8Header*>(a.plan);
-  uint32_t* first = reinterpret_cast<uint32_t*>(a.plan + a.g.off_first);
-  uint32_t* split = reinterpret_cast<uint32_t*>(a.plan + a.g.off_split);
-  Q8Item* items = reinterpret_cast<Q8Item*>(a.plan + a.g.off_items);
 
   // requests
   unsigned long long q_len = 0;
@@ -101,108 +94,24 @@ __global__ __launch_bounds__(kPlanThreads) void plan_q8_attn_kernel(const AttnPl
   }
   __syncthreads();
 
-  const uint32_t nt = static_cast<uint32_t>(total_tiles);
   // a tile's entries: those its last query sees
-  auto tile_of = [&](uint32_t tile, uint32_t* b) -> uint32_t {
-    *b = last_not_above(s_tile, a.batch, tile);
-    const uint32_t j = tile - s_tile[*b];
+  auto tiles_of = [&](uint32_t tile, Q8Item* r) -> uint32_t {
+    const uint32_t b = last_not_above(s_tile, a.batch, tile);
+    const uint32_t j = tile - s_tile[b];
     const uint32_t last =
-        min(s_ql[*b] - 1, static_cast<uint32_t>((static_cast<unsigned long long>(j + 1) * M - 1) / G));
-    return static_cast<uint32_t>(q8_visible(s_kv[*b], s_ql[*b] - 1 - last, s_ph[*b], a.ratio));
-  };
-  const uint32_t start = a.g.start_cost, grain = a.g.grain;  // grain is a power of two
-  auto cost_of = [&](uint32_t seen) -> unsigned long long {
-    return start + ((static_cast<unsigned long long>(seen) + grain - 1) & ~static_cast<unsigned long long>(grain - 1));
-  };
-  unsigned long long mine = 0;
-  for (uint32_t i = t; i < nt; i += kPlanThreads) {
-    uint32_t b;
-    mine += cost_of(tile_of(i, &b));
-  }
-  unsigned long long total;
-  const unsigned long long before = block_exclusive<kPlanThreads>(mine, &total, s_scan[0]);
-  // 32-bit divisions where they do: a 64-bit one is some forty instructions that wait for one another, and there were ten
-  const bool narrow = total <= 0x7FFFFFFFull;
-  unsigned long long quota = narrow ? (static_cast<uint32_t>(total) + a.g.ctas - 1) / a.g.ctas : (total + a.g.ctas - 1) / a.g.ctas;
-  quota = max(static_cast<unsigned long long>(a.g.min_quota), quota);
-  quota = (quota + grain - 1) & ~static_cast<unsigned long long>(grain - 1);
-  auto shares = [&](unsigned long long x) -> unsigned long long {  // x / quota, x <= total + quota
-    return narrow ? static_cast<uint32_t>(x) / static_cast<uint32_t>(quota) : x / quota;
-  };
-
-  unsigned long long pos0 = 0;
-  uint32_t item0 = 0, part0 = 0, split0 = 0;
-  for (uint32_t i0 = 0; i0 < nt; i0 += kPlanThreads) {
-    const uint32_t i = i0 + t;
-    uint32_t b, n = 0;
-    const unsigned long long cost = nt <= kPlanThreads ? mine : i < nt ? cost_of(tile_of(i, &b)) : 0;
-    unsigned long long cost_sum = total, packed_sum, p = before;  // a single strip's sums are known
-    if (nt > kPlanThreads) p = pos0 + block_exclusive<kPlanThreads>(cost, &cost_sum, s_scan[0]);
-    if (cost) n = static_cast<uint32_t>(shares(p + cost - 1) - shares(p)) + 1;
-    // items (32 bits), parts (16) and splits (16) of the strip, in one scan: parts are at most twice the CTAs
-    const unsigned long long pk = n | (static_cast<unsigned long long>(n > 1 ? n : 0) << 32) |
-                                  (static_cast<unsigned long long>(n > 1) << 48);
-    const unsigned long long ex = block_exclusive<kPlanThreads>(pk, &packed_sum, s_scan[0]);
-    const uint32_t it = item0 + static_cast<uint32_t>(ex);
-    s_pos[t] = p;
-    s_item[t] = it;
-    s_part[t] = n > 1 ? part0 + (static_cast<uint32_t>(ex >> 32) & 0xFFFFu) : kInvalidU32;
-    if (n > 1) {
-      split[split0 + static_cast<uint32_t>(ex >> 48)] = it;
-      atomicMax(&s_most, n);
+        min(s_ql[b] - 1, static_cast<uint32_t>((static_cast<unsigned long long>(j + 1) * M - 1) / G));
+    if (r != nullptr) {
+      r->rid = s_rid[b];
+      r->q_start = s_qs[b];
+      r->q_len = s_ql[b];
+      r->row0 = j * M;
+      r->kv_len = s_kv[b];
+      r->phase = s_ph[b];
     }
-    __syncthreads();
-    const uint32_t strip = min(static_cast<uint32_t>(kPlanThreads), nt - i0);
-    const uint32_t end = item0 + static_cast<uint32_t>(packed_sum);
-    for (uint32_t k = item0 + t; k < end; k += kPlanThreads) {
-      const uint32_t s = last_not_above(s_item, strip, k);
-      uint32_t rb;
-      const uint32_t seen = tile_of(i0 + s, &rb);
-      const unsigned long long len = cost_of(seen);
-      const unsigned long long P = s_pos[s], cut = shares(P);
-      const uint32_t c = k - s_item[s];
-      const unsigned long long lo = c == 0 ? P : (cut + c) * quota;
-      const unsigned long long hi = min(P + len, (cut + c + 1) * quota);
-      const unsigned long long o0 = lo - P, o1 = hi - P;
-      Q8Item r;
-      r.rid = s_rid[rb];
-      r.q_start = s_qs[rb];
-      r.q_len = s_ql[rb];
-      r.row0 = (i0 + s - s_tile[rb]) * M;
-      r.kv_begin = o0 > start ? static_cast<uint32_t>(o0 - start) : 0;
-      r.kv_end = o1 > start ? min(seen, static_cast<uint32_t>(o1 - start)) : 0;
-      r.kv_len = s_kv[rb];
-      r.phase = s_ph[rb];
-      r.part = static_cast<int32_t>(s_part[s]);
-      r.chunk = c;
-      r.chunks = static_cast<uint32_t>(shares(P + len - 1) - cut) + 1;
-      r.reserved = 0;
-      items[k] = r;
-      const unsigned long long cta = shares(lo);
-      if (cta * quota == lo) first[cta] = k;
-    }
-    pos0 += cost_sum;
-    item0 = end;
-    part0 += static_cast<uint32_t>(packed_sum >> 32) & 0xFFFFu;
-    split0 += static_cast<uint32_t>(packed_sum >> 48);
-    __syncthreads();
-  }
-  if (t == 0) {
-    const uint32_t ctas = static_cast<uint32_t>(shares(total + quota - 1));
-    first[ctas] = item0;
-    head->items = item0;
-    head->ctas = ctas;
-    head->parts = part0;
-    head->splits = split0;
-    head->rows = M;
-    head->group = G;
-    head->num_q = a.num_q;
-    head->ratio = a.ratio;
-    head->cap_ctas = a.g.ctas;
-    head->batch = a.batch;
-    head->most = s_most;  // (the last strip ended with a barrier)
-    if (total_q != a.num_q) status_or(a.d_status, CKV_STATUS_BAD_TOTAL);
-  }
+    return static_cast<uint32_t>(q8_visible(s_kv[b], s_ql[b] - 1 - last, s_ph[b], a.ratio));
+  };
+  cut_tiles<kPlanThreads>(a.g, a.plan, static_cast<uint32_t>(total_tiles), a.num_q, a.ratio, a.batch, tiles_of, s_cut);
+  if (t == 0 && total_q != a.num_q) status_or(a.d_status, CKV_STATUS_BAD_TOTAL);
 }
 
 }  // namespace
@@ -241,7 +150,12 @@ int per_sm_of(uint32_t head_dim, uint32_t rows) { return head_dim == 64 ? 4 : he
 }  // namespace
 
 int q8_attn_geom(const Q8Cache& c, uint32_t batch, uint32_t num_q, uint32_t n_heads, Q8Geom* g) {
-  if (batch > CKV_MAX_BATCH || num_q > CKV_MAX_TOKENS) return CKV_ERR_SIZE;
+  if (batch > CKV_MAX_BATCH) return CKV_ERR_SIZE;
+  return q8_attn_geom_of(c, batch, num_q, n_heads, g);
+}
+
+int q8_attn_geom_of(const Q8Cache& c, uint32_t batch, uint32_t num_q, uint32_t n_heads, Q8Geom* g) {
+  if (num_q > CKV_MAX_TOKENS) return CKV_ERR_SIZE;
   if (n_heads == 0 || n_heads % c.heads != 0 || n_heads / c.heads > CKV_Q8_MAX_GROUP) return CKV_ERR_SIZE;
   g->group = n_heads / c.heads;
   if (static_cast<uint64_t>(num_q) * g->group > 0x7FFFFFFFull) return CKV_ERR_SIZE;  // row numbers are 32-bit
@@ -297,7 +211,7 @@ namespace {
 // accumulators; the weights cross from entries to rows with one 8 x 8 transposition for eight entries.  One request of 777 entries 8.7 us against
 // 9.4 with sixteen rows, 32 of 300 14.8 against 18.2, 64 of 8000 174 against 179.  What a tile costs in instructions counts to the end: a copy for its scales, sizes on whole tiles'
 // copies and a division were 8 % of the 64 requests' time.
-template <int kDw, int kNp, bool kShared, int kRows>
+template <int kDw, int kNp, bool kShared, int kRows, bool kLists>
 __global__ __launch_bounds__(kAttnThreads, (Cfg<kDw, kNp, kShared, kRows>::kPerSm)) void q8_attn_kernel(const AttnArgs a) {
   using C = Cfg<kDw, kNp, kShared, kRows>;
   constexpr bool kFew = kRows == 8;
@@ -329,13 +243,13 @@ __global__ __launch_bounds__(kAttnThreads, (Cfg<kDw, kNp, kShared, kRows>::kPerS
   const uint32_t ring = smem_addr(smem) + warp * C::kStages * C::kStageBytes;
 
   for (uint32_t it = item0; it < item1; ++it) {
-    const Q8Item item = items[it];
+    const Q8Item item = item_for<kLists>(items + it, a, h);
     if (!item_fits(item, a)) {
       if (tid == 0) status_or(a.d_status, CKV_STATUS_BAD_INDEX);
       continue;
     }
     const uint32_t rows = min(static_cast<uint32_t>(kRows), item.q_len * G - item.row0);
-    const int32_t* table = a.table + static_cast<size_t>(item.rid) * a.stride;
+    const int32_t* table = table_for<kLists>(a, item, h);
     __syncthreads();  // the previous item's reads of shared memory are done
     for (int c = tid; c < C::kD; c += kAttnThreads) s_nan[c] = 0x7FFFFFFF;
     if (tid == 0) s_any_nan = 0;
@@ -826,14 +740,20 @@ __global__ __launch_bounds__(kCombineThreads) void q8_combine_kernel(const AttnA
   }
 }
 
-template <int kDw, int kNp, bool kShared, int kRows>
-int launch_attn(const AttnArgs& a, cudaStream_t s) {
+template <int kDw, int kNp, bool kShared, int kRows, bool kLists>
+int launch_attn_for(const AttnArgs& a, cudaStream_t s) {
   using C = Cfg<kDw, kNp, kShared, kRows>;
-  auto* kernel = q8_attn_kernel<kDw, kNp, kShared, kRows>;
+  auto* kernel = q8_attn_kernel<kDw, kNp, kShared, kRows, kLists>;
   static std::atomic<uint64_t> done;
   const int rc = allow_smem(reinterpret_cast<const void*>(kernel), C::kSmem, done);
   if (rc) return rc;
   return launch_pdl(kernel, dim3(a.g.ctas, a.c.heads), dim3(kAttnThreads), C::kSmem, s, a);
+}
+
+template <int kDw, int kNp, bool kShared, int kRows>
+int launch_attn(const AttnArgs& a, cudaStream_t s) {
+  return a.lens != nullptr ? launch_attn_for<kDw, kNp, kShared, kRows, true>(a, s)
+                           : launch_attn_for<kDw, kNp, kShared, kRows, false>(a, s);
 }
 
 template <int kRows>
@@ -860,6 +780,14 @@ int launch_combine(const AttnArgs& a, cudaStream_t s) {
 }
 
 }  // namespace
+
+int launch_q8_attn(const AttnArgs& a, cudaStream_t s) {
+  const int rc = !a.g.tc ? (a.g.rows == 8 ? launch_split<8>(a, s) : launch_split<16>(a, s))
+                 : a.c.head_dim <= 128 ? launch_q8_attn_rows(a, s)
+                                       : launch_q8_attn_tc(a, s);
+  return rc ? rc : launch_combine(a, s);
+}
+
 }  // namespace ckv
 
 using namespace ckv;
@@ -945,9 +873,7 @@ int ckv_q8_attn(const ckv_q8_cache_t* cache, uint32_t n_heads, uint32_t ratio, f
   a.part_ml = reinterpret_cast<float2*>(a.part_o + static_cast<size_t>(a.g.cap_parts) * a.c.heads * a.g.rows * a.c.head_dim);
   a.d_status = d_status;
   a.wait_ns = wait_limit_ns();
-  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  rc = !a.g.tc ? (a.g.rows == 8 ? launch_split<8>(a, s) : launch_split<16>(a, s)) : a.c.head_dim <= 128 ? launch_q8_attn_rows(a, s) : launch_q8_attn_tc(a, s);
-  return rc ? rc : launch_combine(a, s);
+  return launch_q8_attn(a, reinterpret_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

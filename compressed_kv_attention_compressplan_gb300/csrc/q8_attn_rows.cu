@@ -82,7 +82,7 @@ __device__ __forceinline__ bool pair_any(int id, bool x) {
 }
 __device__ __forceinline__ void pair_sync(int id) { asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory"); }
 
-template <int kD, bool kShared, bool kShort>
+template <int kD, bool kShared, bool kShort, bool kLists>
 __global__ __launch_bounds__((RowsCfg<kD, kShared>::kThreads), 1) void q8_attn_rows_kernel(const AttnArgs a) {
   using C = RowsCfg<kD, kShared>;
   extern __shared__ uint8_t raw[];
@@ -133,7 +133,7 @@ __global__ __launch_bounds__((RowsCfg<kD, kShared>::kThreads), 1) void q8_attn_r
   uint32_t items_before = 0;  // earlier items
 
   for (uint32_t it = item0; it < item1; ++it) {
-    const Q8Item item = items[it];
+    const Q8Item item = item_for<kLists>(items + it, a, h);
     __syncthreads();  // the item before is done with what this one's takes the place of
     tc_fence_after();
     if (!item_fits(item, a)) {
@@ -141,7 +141,7 @@ __global__ __launch_bounds__((RowsCfg<kD, kShared>::kThreads), 1) void q8_attn_r
       continue;
     }
     const uint32_t rows = min(static_cast<uint32_t>(C::kRows), item.q_len * G - item.row0);
-    const int32_t* table = a.table + static_cast<size_t>(item.rid) * a.stride;
+    const int32_t* table = table_for<kLists>(a, item, h);
     const uint32_t n_tiles =
         item.kv_end > item.kv_begin ? (item.kv_end - item.kv_begin + kEntries - 1) / kEntries : 0;
     const int tiles = rows > 128 ? 2 : 1;  // row tiles with rows
@@ -439,14 +439,20 @@ __global__ __launch_bounds__((RowsCfg<kD, kShared>::kThreads), 1) void q8_attn_r
   if (!w.live) status_or(a.d_status, CKV_STATUS_TIMEOUT);
 }
 
-template <int kD, bool kShared>
-int launch(const AttnArgs& a, cudaStream_t s) {
+template <int kD, bool kShared, bool kLists>
+int launch_for(const AttnArgs& a, cudaStream_t s) {
   using C = RowsCfg<kD, kShared>;
-  auto* kernel = a.wait_ns < kShortWaitNs ? q8_attn_rows_kernel<kD, kShared, true> : q8_attn_rows_kernel<kD, kShared, false>;
+  auto* kernel = a.wait_ns < kShortWaitNs ? q8_attn_rows_kernel<kD, kShared, true, kLists>
+                                          : q8_attn_rows_kernel<kD, kShared, false, kLists>;
   static std::atomic<uint64_t> done[2];
   const int rc = allow_smem(reinterpret_cast<const void*>(kernel), C::kSmem, done[a.wait_ns < kShortWaitNs ? 1 : 0]);
   if (rc) return rc;
   return launch_pdl(kernel, dim3(a.g.ctas, a.c.heads), dim3(C::kThreads), C::kSmem, s, a);
+}
+
+template <int kD, bool kShared>
+int launch(const AttnArgs& a, cudaStream_t s) {
+  return a.lens != nullptr ? launch_for<kD, kShared, true>(a, s) : launch_for<kD, kShared, false>(a, s);
 }
 
 }  // namespace

@@ -119,7 +119,7 @@ __device__ __forceinline__ bool group_any(int id, bool x) {
 }
 __device__ __forceinline__ void group_sync(int id) { asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory"); }
 
-template <int kD, bool kShared, bool kShort>
+template <int kD, bool kShared, bool kShort, bool kLists>
 __global__ __launch_bounds__((TcCfg<kD, kShared>::kThreads), 1) void q8_attn_tc_kernel(const AttnArgs a) {
   using C = TcCfg<kD, kShared>;
   constexpr int kN = C::kRows;
@@ -175,13 +175,13 @@ __global__ __launch_bounds__((TcCfg<kD, kShared>::kThreads), 1) void q8_attn_tc_
   uint32_t items_before = 0;
 
   for (uint32_t it = item0; it < item1; ++it) {
-    const Q8Item item = items[it];
+    const Q8Item item = item_for<kLists>(items + it, a, h);
     if (!item_fits(item, a)) {
       if (tid == 0) status_or(a.d_status, CKV_STATUS_BAD_INDEX);
       continue;
     }
     const uint32_t rows = min(static_cast<uint32_t>(kN), item.q_len * G - item.row0);
-    const int32_t* table = a.table + static_cast<size_t>(item.rid) * a.stride;
+    const int32_t* table = table_for<kLists>(a, item, h);
     const uint32_t n_tiles =
         item.kv_end > item.kv_begin ? (item.kv_end - item.kv_begin + kEntries - 1) / kEntries : 0;
     const uint32_t last = item.kv_end > 0 ? item.kv_end - 1 : 0;
@@ -616,14 +616,20 @@ __global__ __launch_bounds__((TcCfg<kD, kShared>::kThreads), 1) void q8_attn_tc_
   if (!w.live) status_or(a.d_status, CKV_STATUS_TIMEOUT);
 }
 
-template <int kD, bool kShared>
-int launch(const AttnArgs& a, cudaStream_t s) {
+template <int kD, bool kShared, bool kLists>
+int launch_for(const AttnArgs& a, cudaStream_t s) {
   using C = TcCfg<kD, kShared>;
-  auto* kernel = a.wait_ns < kShortWaitNs ? q8_attn_tc_kernel<kD, kShared, true> : q8_attn_tc_kernel<kD, kShared, false>;
+  auto* kernel = a.wait_ns < kShortWaitNs ? q8_attn_tc_kernel<kD, kShared, true, kLists>
+                                          : q8_attn_tc_kernel<kD, kShared, false, kLists>;
   static std::atomic<uint64_t> done[2];
   const int rc = allow_smem(reinterpret_cast<const void*>(kernel), C::kSmem, done[a.wait_ns < kShortWaitNs ? 1 : 0]);
   if (rc) return rc;
   return launch_pdl(kernel, dim3(a.g.ctas, a.c.heads), dim3(C::kThreads), C::kSmem, s, a);
+}
+
+template <int kD, bool kShared>
+int launch(const AttnArgs& a, cudaStream_t s) {
+  return a.lens != nullptr ? launch_for<kD, kShared, true>(a, s) : launch_for<kD, kShared, false>(a, s);
 }
 
 }  // namespace

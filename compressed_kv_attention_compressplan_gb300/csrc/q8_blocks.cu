@@ -1,0 +1,345 @@
+// q8_blocks.cu -- sparse attention over the 8-bit paged cache: which blocks each
+// query reads, and the attention over them.
+//
+// Choosing.  A row is the scores of one (query, kv head).  Scores become order-preserving 32-bit keys; the key at the
+// border is found, and the blocks above it, and as many at it as are missing, are listed in order with ballots.  No
+// sum of rounded numbers is involved, so the choice is exact: equal scores go to the lower block.
+//
+// Attention.  A query's list for one kv head, looked up in its request's block table, is the block table of a request of
+// its own with one query, which sees all of it: the listed blocks ascend, so that the one block of which a query
+// sees a part is the last.  So the attention kernels take lists as they take requests; what is added is a
+// table for each (query, kv head), the entries that it holds, and a plan over the queries, all made on the card.
+#include <algorithm>
+
+#include "q8_blocks.cuh"
+#include "q8_plan.cuh"
+
+namespace ckv {
+namespace {
+
+// ------------------------------------------------------------------- select
+constexpr int kSelThreads = 256;
+
+struct SelectArgs {
+  const float* scores;
+  BlockReqs r;
+  uint32_t heads, width, block_tokens;
+  uint32_t budget, sinks, recent;
+  int32_t* blocks;
+};
+
+// Larger keys for larger scores; NaN below everything, the two zeros alike.
+__device__ __forceinline__ uint32_t score_key(float w) {
+  if (w != w) return 0;
+  const uint32_t u = __float_as_uint(w + 0.0f);
+  return u ^ (u >> 31 ? 0xFFFFFFFFu : 0x80000000u);
+}
+
+// A CTA takes a row.
+__global__ __launch_bounds__(kSelThreads) void q8_select_kernel(const SelectArgs a) {
+  constexpr uint32_t kBins = 256;
+  __shared__ uint32_t s_q[CKV_MAX_BATCH];
+  __shared__ BlockReq s_req[CKV_MAX_BATCH];
+  __shared__ unsigned long long s_scan64[kSelThreads / 32 + 1];
+  __shared__ uint32_t s_scan[kSelThreads / 32 + 1];
+  __shared__ uint32_t s_bin[kBins];
+  __shared__ uint32_t s_pick, s_left;
+  pdl_wait();
+  pdl_release();
+  scan_queries<kSelThreads>(a.r, s_q, s_req, s_scan64);
+  const uint32_t t = threadIdx.x, T = a.block_tokens;
+  const uint64_t rows = static_cast<uint64_t>(a.r.num_q) * a.heads;
+  for (uint64_t row = blockIdx.x; row < rows; row += gridDim.x) {
+    BlockReq req;
+    uint32_t i;
+    if (!request_of(static_cast<uint32_t>(row / a.heads), s_q, s_req, a.r.batch, &req, &i)) continue;
+    const uint32_t n = (seen_by(req, i, a.r.ratio) + T - 1) / T;
+    int32_t* out = a.blocks + row * a.budget;
+    if (n <= a.budget) {
+      for (uint32_t j = t; j < a.budget; j += kSelThreads) out[j] = j < n ? static_cast<int32_t>(j) : -1;
+      continue;
+    }
+    const float* scores = a.scores + row * a.width;
+    const uint32_t lo = a.sinks, hi = n - a.recent, want = a.budget - a.sinks - a.recent;  // candidates lo .. hi - 1: more than wanted
+    // the key at rank `want` from the top, eight bits at a time
+    uint32_t prefix = 0, mask = 0, left = want;
+    if (want > 0) {
+      for (int shift = 24; shift >= 0; shift -= 8) {
+        __syncthreads();
+        s_bin[t] = 0;
+        __syncthreads();
+        for (uint32_t j = lo + t; j < hi; j += kSelThreads) {
+          const uint32_t k = score_key(scores[j]);
+          if ((k & mask) == prefix) atomicAdd(&s_bin[k >> shift & 255], 1u);
+        }
+        __syncthreads();
+        // bin 255 - t: how many are in bins above it
+        const uint32_t c = s_bin[kBins - 1 - t];
+        uint32_t sum;
+        const uint32_t above = block_exclusive<kSelThreads>(c, &sum, s_scan);
+        if (above < left && above + c >= left) {
+          s_pick = kBins - 1 - t;
+          s_left = left - above;
+        }
+        __syncthreads();
+        prefix |= s_pick << shift;
+        mask |= 255u << shift;
+        left = s_left;
+      }
+    }
+    // those above the border, and the first `left` at it, between the first and the last ones
+    for (uint32_t j = t; j < a.sinks; j += kSelThreads) out[j] = static_cast<int32_t>(j);
+    for (uint32_t j = t; j < a.recent; j += kSelThreads) out[a.sinks + want + j] = static_cast<int32_t>(hi + j);
+    if (want > 0) {
+      uint32_t taken = 0, ties = 0;  // so far
+      for (uint32_t j0 = lo; j0 < hi; j0 += kSelThreads) {
+        const uint32_t j = j0 + t;
+        const uint32_t k = j < hi ? score_key(scores[j]) : 0;
+        const bool tie = j < hi && k == prefix, over = j < hi && k > prefix;
+        uint32_t tie_sum, sum;
+        const uint32_t tie_rank = ties + block_exclusive<kSelThreads>(static_cast<uint32_t>(tie), &tie_sum, s_scan);
+        const bool take = over || (tie && tie_rank < left);
+        const uint32_t at = taken + block_exclusive<kSelThreads>(static_cast<uint32_t>(take), &sum, s_scan);
+        if (take) out[a.sinks + at] = static_cast<int32_t>(j);
+        taken += sum;
+        ties += tie_sum;
+      }
+    }
+    __syncthreads();  // s_pick, s_left and s_bin are read
+  }
+}
+
+// ------------------------------------------------------------------- lists
+constexpr int kListThreads = 256;
+
+struct ListArgs {
+  BlockReqs r;
+  uint32_t heads, block_tokens;
+  const int32_t* blocks;
+  uint32_t budget;
+  const int32_t* table;
+  uint32_t stride;
+  int32_t* tables;   // [num_q, heads, budget]: block numbers
+  uint32_t* lens;    // [num_q, heads]: entries in them
+  uint32_t* most;    // [num_q]: of its heads' lists, the most entries; kInvalidU32: no request's query
+};
+
+// A CTA takes a query, its warps the kv heads.
+__global__ __launch_bounds__(kListThreads) void q8_lists_kernel(const ListArgs a) {
+  __shared__ uint32_t s_q[CKV_MAX_BATCH];
+  __shared__ BlockReq s_req[CKV_MAX_BATCH];
+  __shared__ unsigned long long s_scan[kListThreads / 32 + 1];
+  __shared__ uint32_t s_most;
+  pdl_wait();
+  pdl_release();
+  scan_queries<kListThreads>(a.r, s_q, s_req, s_scan);
+  const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5, T = a.block_tokens;
+  for (uint32_t n = blockIdx.x; n < a.r.num_q; n += gridDim.x) {
+    __syncthreads();  // the query before is written
+    if (threadIdx.x == 0) s_most = 0;
+    __syncthreads();
+    BlockReq req;
+    uint32_t i;
+    if (!request_of(n, s_q, s_req, a.r.batch, &req, &i)) {
+      if (threadIdx.x == 0) a.most[n] = kInvalidU32;
+      continue;
+    }
+    const uint32_t seen = seen_by(req, i, a.r.ratio), visible = (seen + T - 1) / T;
+    const int32_t* table = a.table + static_cast<size_t>(req.rid) * a.stride;
+    for (uint32_t h = warp; h < a.heads; h += kListThreads / 32) {
+      const size_t at = static_cast<size_t>(n) * a.heads + h;
+      const int32_t* list = a.blocks + at * a.budget;
+      int32_t* out = a.tables + at * a.budget;
+      int32_t before = -1;  // the largest number so far
+      uint32_t kept = 0;
+      bool part = false, bad = false;
+      for (uint32_t j0 = 0; j0 < a.budget; j0 += 32) {
+        const int32_t v = j0 + lane < a.budget ? list[j0 + lane] : -1;
+        int32_t top = v;  // the largest up to this lane
+#pragma unroll
+        for (int s = 1; s < 32; s <<= 1) {
+          const int32_t x = __shfl_up_sync(0xFFFFFFFFu, top, s);
+          if (static_cast<int>(lane) >= s) top = max(top, x);
+        }
+        const int32_t up = __shfl_up_sync(0xFFFFFFFFu, top, 1);
+        const int32_t prior = max(before, lane == 0 ? -1 : up);
+        before = max(before, __shfl_sync(0xFFFFFFFFu, top, 31));
+        bad |= v >= 0 && v <= prior;
+        const bool take = v > prior && static_cast<uint32_t>(v) < visible;
+        const uint32_t votes = __ballot_sync(0xFFFFFFFFu, take);
+        if (take) out[kept + __popc(votes & ((1u << lane) - 1))] = __ldg(table + v);
+        part |= take && static_cast<uint32_t>(v) == visible - 1;
+        kept += __popc(votes);
+      }
+      if (__any_sync(0xFFFFFFFFu, bad) && lane == 0) status_or(a.r.d_status, CKV_STATUS_BAD_INDEX);
+      const bool last = __any_sync(0xFFFFFFFFu, part);  // the last block that the query sees, maybe in part, is listed
+      const uint32_t entries = kept * T - (last ? visible * T - seen : 0);
+      if (lane == 0) {
+        a.lens[at] = entries;
+        atomicMax(&s_most, entries);
+      }
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) a.most[n] = s_most;
+  }
+}
+
+constexpr int kPlanThreads = 1024;
+
+struct ListPlanArgs {
+  Q8Geom g;
+  const uint32_t* most;
+  uint32_t num_q;
+  uint8_t* plan;
+};
+
+// One CTA.
+__global__ __launch_bounds__(kPlanThreads) void plan_q8_lists_kernel(const ListPlanArgs a) {
+  __shared__ CutShared<kPlanThreads> s_cut;
+  pdl_wait();
+  pdl_release();
+  const uint32_t M = a.g.rows, per = (a.g.group + M - 1) / M;  // tiles of a query
+  auto tiles = [&](uint32_t tile, Q8Item* r) -> uint32_t {
+    const uint32_t n = tile / per, most = __ldg(a.most + n);
+    if (r != nullptr) {
+      r->rid = n;
+      r->q_start = n;
+      r->q_len = 1;
+      r->row0 = (tile - n * per) * M;
+      r->kv_len = most;
+      r->phase = 0;
+    }
+    return most;
+  };
+  cut_tiles<kPlanThreads>(a.g, a.plan, a.num_q * per, a.num_q, 1, a.num_q, tiles, s_cut);
+}
+
+// Where the workspace's pieces lie.
+struct ListSpace {
+  uint64_t plan, tables, lens, most, parts, bytes;
+};
+
+int list_space(const Q8Cache& c, uint32_t n_heads, uint32_t num_q, uint32_t budget, Q8Geom* g, ListSpace* w) {
+  // entries of a list are counted in 32 bits
+  if (budget == 0 || static_cast<uint64_t>(budget) * c.block_tokens > 0x7FFFFFF0ull) return CKV_ERR_SIZE;
+  const int rc = q8_attn_geom_of(c, num_q, num_q, n_heads, g);
+  if (rc) return rc;
+  auto up = [](uint64_t x) { return (x + 255) & ~255ull; };
+  const uint64_t lists = static_cast<uint64_t>(num_q) * c.heads;
+  w->plan = 0;
+  w->tables = up(g->bytes);
+  w->lens = up(w->tables + lists * budget * 4);
+  w->most = up(w->lens + lists * 4);
+  w->parts = up(w->most + static_cast<uint64_t>(num_q) * 4);
+  w->bytes = w->parts + g->workspace;
+  return CKV_OK;
+}
+
+}  // namespace
+}  // namespace ckv
+
+using namespace ckv;
+
+extern "C" {
+
+int ckv_q8_block_select(const float* scores, uint32_t n_kv_heads, uint32_t width, uint32_t block_tokens, uint32_t ratio,
+                        uint32_t num_q, const int64_t* seq_lens, const int64_t* extend_lens, const int64_t* kv_lens,
+                        uint32_t batch, uint32_t budget, uint32_t sinks, uint32_t recent, int32_t* blocks,
+                        uint32_t* d_status, ckv_stream_t stream) {
+  SelectArgs a{};
+  if (block_tokens != 16 && block_tokens != 32 && block_tokens != 64 && block_tokens != 128) return CKV_ERR_SIZE;
+  if (n_kv_heads == 0 || n_kv_heads > CKV_Q8_MAX_KV_HEADS || num_q > CKV_MAX_TOKENS) return CKV_ERR_SIZE;
+  if (width == 0 || width > 0x7FFFFFFFu || budget == 0 || budget > 0x7FFFFFFFu) return CKV_ERR_SIZE;
+  if (sinks > budget || recent > budget - sinks) return CKV_ERR_SIZE;
+  const int rc = check_lens(batch, ratio, seq_lens, extend_lens, kv_lens);
+  if (rc) return rc;
+  if (num_q == 0 || batch == 0) return CKV_OK;
+  if (!aligned_to(scores, 4) || !aligned_to(blocks, 4)) return CKV_ERR_POINTER;
+  a.scores = scores;
+  a.r = {nullptr, seq_lens, extend_lens, kv_lens, batch, num_q, ratio, 1, static_cast<int64_t>(width) * block_tokens, d_status};
+  a.heads = n_kv_heads;
+  a.width = width;
+  a.block_tokens = block_tokens;
+  a.budget = budget;
+  a.sinks = sinks;
+  a.recent = recent;
+  a.blocks = blocks;
+  const uint64_t rows = static_cast<uint64_t>(num_q) * n_kv_heads;
+  const dim3 grid(static_cast<uint32_t>(std::min<uint64_t>(rows, 8ull * sm_count())));
+  return launch_pdl(q8_select_kernel, grid, dim3(kSelThreads), 0, reinterpret_cast<cudaStream_t>(stream), a);
+}
+
+uint64_t ckv_q8_attn_blocks_workspace_bytes(const ckv_q8_cache_t* cache, uint32_t n_heads, uint32_t num_q,
+                                            uint32_t budget) {
+  Q8Cache c;
+  Q8Geom g;
+  ListSpace w;
+  if (q8_cache_of(cache, &c) || list_space(c, n_heads, num_q, budget, &g, &w)) return 0;
+  return w.bytes;
+}
+
+int ckv_q8_attn_blocks(const ckv_q8_cache_t* cache, uint32_t n_heads, uint32_t ratio, float scale, const void* q,
+                       uint32_t num_q, const int32_t* blocks, uint32_t budget, const int64_t* rid,
+                       const int64_t* seq_lens, const int64_t* extend_lens, const int64_t* kv_lens, uint32_t batch,
+                       const int32_t* block_table, uint64_t table_stride, uint32_t num_reqs, int out_dtype, void* out,
+                       float* lse, void* workspace, uint64_t workspace_bytes, uint32_t* d_status, ckv_stream_t stream) {
+  AttnArgs a{};
+  ListSpace w;
+  int rc = q8_cache_of(cache, &a.c);
+  if (rc) return rc;
+  if (out_dtype != CKV_F32 && out_dtype != CKV_BF16) return CKV_ERR_DTYPE;
+  if (!(scale > 0.0f) || !(scale < 1e30f)) return CKV_ERR_SIZE;
+  rc = check_lens(batch, ratio, seq_lens, extend_lens, kv_lens);
+  if (rc) return rc;
+  rc = list_space(a.c, n_heads, num_q, budget, &a.g, &w);
+  if (rc) return rc;
+  if (num_q == 0 || batch == 0) return CKV_OK;
+  rc = check_table(block_table, table_stride, num_reqs);
+  if (rc) return rc;
+  if (workspace_bytes < w.bytes) return CKV_ERR_SIZE;
+  if (!aligned16(q) || !aligned16(out) || !aligned16(workspace) || (lse != nullptr && !aligned_to(lse, 4)) ||
+      !aligned_to(blocks, 4) || !aligned_to(rid, 8))
+    return CKV_ERR_POINTER;
+  uint8_t* space = static_cast<uint8_t*>(workspace);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+
+  ListArgs l{};
+  const int64_t most = static_cast<int64_t>(table_stride) * a.c.block_tokens;
+  l.r = {rid, seq_lens, extend_lens, kv_lens, batch, num_q, ratio, num_reqs, most, d_status};
+  l.heads = a.c.heads;
+  l.block_tokens = a.c.block_tokens;
+  l.blocks = blocks;
+  l.budget = budget;
+  l.table = block_table;
+  l.stride = static_cast<uint32_t>(table_stride);
+  l.tables = reinterpret_cast<int32_t*>(space + w.tables);
+  l.lens = reinterpret_cast<uint32_t*>(space + w.lens);
+  l.most = reinterpret_cast<uint32_t*>(space + w.most);
+  rc = launch_pdl(q8_lists_kernel, dim3(std::min<uint32_t>(num_q, 4 * sm_count())), dim3(kListThreads), 0, s, l);
+  if (rc) return rc;
+  ListPlanArgs p{a.g, l.most, num_q, space + w.plan};
+  rc = launch_pdl(plan_q8_lists_kernel, dim3(1), dim3(kPlanThreads), 0, s, p);
+  if (rc) return rc;
+
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.batch = num_q;
+  a.num_q = num_q;
+  a.n_heads = n_heads;
+  a.ratio = 1;
+  a.scale_log2 = scale * kLog2e;
+  a.table = l.tables;
+  a.stride = budget;
+  a.num_reqs = num_q;
+  a.lens = l.lens;
+  a.plan = p.plan;
+  a.out_f32 = out_dtype == CKV_F32;
+  a.out = out;
+  a.lse = lse;
+  a.part_o = reinterpret_cast<float*>(space + w.parts);
+  a.part_ml = reinterpret_cast<float2*>(a.part_o + static_cast<size_t>(a.g.cap_parts) * a.c.heads * a.g.rows * a.c.head_dim);
+  a.d_status = d_status;
+  a.wait_ns = wait_limit_ns();
+  return launch_q8_attn(a, s);
+}
+
+}  // extern "C"

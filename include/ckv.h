@@ -604,13 +604,101 @@ int ckv_q8_evict(const ckv_q8_cache_t* cache, float* weights, const int64_t* rid
                  uint64_t dst_stride, uint32_t num_reqs, uint32_t budget, uint32_t sinks, uint32_t recent,
                  int32_t* kept, int64_t* new_lens, uint32_t* d_status, ckv_stream_t stream);
 
+/* ------------------------------------- 8-bit cache: rotated append, sparse attention */
+/* ckv_q8_store with the norm and the position rotation on the way: the keys (a
+ * latent cache's entries) are
+ *   y_c = x_c * norm_weight[c] / sqrt(mean_c(x_c^2) + eps)      (norm_weight NULL: y = x)
+ * and then channels rope_begin .. rope_begin + rope_dim - 1 turn in pairs,
+ *   (a, b) -> (a*cos - b*sin, a*sin + b*cos),  (cos, sin) = freqs[positions[row]][i],
+ * pair i being channels rope_begin + 2i and 2i + 1 (halves == 0) or rope_begin + i
+ * and i + rope_dim/2 (halves != 0); values (v_rows) are stored as they come.
+ * Everything is fp32 up to the one rounding to e4m3; no product is fused with a sum.
+ *   k_rows, v_rows  [num_rows, n_kv_heads, head_dim] with k_stride and v_stride
+ *                 elements from row to row (at least n_kv_heads * head_dim, and
+ *                 whole 16 bytes), as rows lie in a fused projection.
+ *   positions     int64 [num_rows]; a row whose position is not in [0, max_pos)
+ *                 is not stored (its slot stays as it was) and sets
+ *                 CKV_STATUS_BAD_INDEX.  With rope_dim 0 neither they nor freqs are
+ *                 read (NULL allowed).
+ *   freqs         fp32 [max_pos, rope_dim/2, 2]; rope_dim a multiple of 32,
+ *                 rope_begin of 16, rope_begin + rope_dim <= head_dim (else
+ *                 CKV_ERR_HEAD_DIM).
+ *   norm_weight   fp32 [head_dim], eps > 0; or NULL.
+ *   weights       NULL, or as for ckv_q8_store_reset.
+ * plan, d_counts, capacity: of ckv_plan_q8_store, as for ckv_q8_store. */
+int ckv_q8_rope_store(const ckv_q8_cache_t* cache, int in_dtype, const void* k_rows, uint64_t k_stride,
+                      const void* v_rows, uint64_t v_stride, uint32_t num_rows, const int64_t* positions,
+                      const float* norm_weight, float eps, const float* freqs, uint32_t max_pos, uint32_t rope_begin,
+                      uint32_t rope_dim, int halves, const ckv_q8_store_plan_t* plan, const uint32_t* d_counts,
+                      uint32_t capacity, float* weights, uint32_t* d_status, ckv_stream_t stream);
+
+/* Sparse attention reads, for each query and kv head, the blocks that a cheap
+ * score selects: ckv_q8_bounds keeps two rows for each block, ckv_q8_block_scores
+ * bounds with them what a query's score can be in it, ckv_q8_block_select chooses, and
+ * ckv_q8_attn_blocks attends.  The lengths (seq_lens, extend_lens, kv_lens, ratio)
+ * mean what they mean to ckv_plan_q8_attn, and a query sees the same entries; block
+ * j of a request is its entries j * block_tokens onwards.  A request whose lengths are
+ * bad, or that has entries past the table, sets CKV_STATUS_BAD_LENGTH, and one whose
+ * queries do not all exist CKV_STATUS_BAD_TOTAL; their rows, and rows after the last
+ * request's, stay as they were.
+ *
+ * bounds: e4m3 [num_blocks, n_kv_heads, 2, head_dim]: the largest, then the
+ * smallest k code of each channel over the entries that the block holds, in units of
+ * its k_scale (NaN where an entry has one).  The call renews the blocks that entries
+ * kv_len - new_len .. kv_len - 1 of each request lie in, from all the entries those
+ * hold up to kv_len: after a store with the store's lengths, after an eviction with
+ * the new tables and new_lens == kv_lens (== its new_lens).  Blocks that several requests
+ * share (whole ones) may be renewed by each. */
+int ckv_q8_bounds(const ckv_q8_cache_t* cache, void* bounds, const int64_t* rid, const int64_t* kv_lens,
+                  const int64_t* new_lens, uint32_t batch, const int32_t* block_table, uint64_t table_stride,
+                  uint32_t num_reqs, uint32_t* d_status, ckv_stream_t stream);
+
+/* scores: fp32 [num_q, n_kv_heads, width].  For block j < ceil(seen / block_tokens)
+ *   scale * k_scale * max over the kv head's query heads of sum_c max(q_c * hi_c, q_c * lo_c),
+ * which no score of the block's entries is above; -infinity for the other j < width.
+ * NaN where a bound or the query has one.  A query row is rounded as in
+ * ckv_q8_attn (exact down to 2^-28 of its largest value), sums are fp32.  A block number
+ * outside the pool scores -infinity and sets CKV_STATUS_BAD_INDEX; a request with
+ * more than width blocks sets CKV_STATUS_BAD_LENGTH, as above.  Only k_scale (and
+ * the shape) of the cache is read. */
+int ckv_q8_block_scores(const ckv_q8_cache_t* cache, const void* bounds, uint32_t n_heads, uint32_t ratio, float scale,
+                        const void* q, uint32_t num_q, const int64_t* rid, const int64_t* seq_lens,
+                        const int64_t* extend_lens, const int64_t* kv_lens, uint32_t batch, const int32_t* block_table,
+                        uint64_t table_stride, uint32_t num_reqs, uint32_t width, float* scores, uint32_t* d_status,
+                        ckv_stream_t stream);
+
+/* blocks: int32 [num_q, n_kv_heads, budget], ascending, -1 behind the last: of the
+ * blocks that a query sees entries of, the first `sinks`, the last `recent` (sinks +
+ * recent <= budget) and those of largest score (equal scores: the lower block; NaN
+ * counts as the least), budget in all; every one where there are no more. */
+int ckv_q8_block_select(const float* scores, uint32_t n_kv_heads, uint32_t width, uint32_t block_tokens, uint32_t ratio,
+                        uint32_t num_q, const int64_t* seq_lens, const int64_t* extend_lens, const int64_t* kv_lens,
+                        uint32_t batch, uint32_t budget, uint32_t sinks, uint32_t recent, int32_t* blocks,
+                        uint32_t* d_status, ckv_stream_t stream);
+
+/* ckv_q8_attn over the listed blocks only: query i of kv head h attends to the
+ * entries that it sees in blocks[i][h][0 .. budget), which ascend; negative places
+ * count for nothing, and one that is not above those before it is skipped and sets
+ * CKV_STATUS_BAD_INDEX.  out, lse, precision and missing blocks as in ckv_q8_attn (of
+ * one query a request).  A query that sees nothing gets zeros and -infinity.  The
+ * workspace holds the call's plan too: ckv_q8_attn_blocks_workspace_bytes (0: bad
+ * sizes) of device memory that no other call uses meanwhile. */
+uint64_t ckv_q8_attn_blocks_workspace_bytes(const ckv_q8_cache_t* cache, uint32_t n_heads, uint32_t num_q,
+                                            uint32_t budget);
+
+int ckv_q8_attn_blocks(const ckv_q8_cache_t* cache, uint32_t n_heads, uint32_t ratio, float scale, const void* q,
+                       uint32_t num_q, const int32_t* blocks, uint32_t budget, const int64_t* rid,
+                       const int64_t* seq_lens, const int64_t* extend_lens, const int64_t* kv_lens, uint32_t batch,
+                       const int32_t* block_table, uint64_t table_stride, uint32_t num_reqs, int out_dtype, void* out,
+                       float* lse, void* workspace, uint64_t workspace_bytes, uint32_t* d_status, ckv_stream_t stream);
+
 /* ------------------------------------------------------------------ misc */
 /* Short text for a CKV_OK / CKV_ERR_* code (static storage). */
 const char* ckv_error_string(int code);
-/* Library ABI version: major * 100 + minor (240: 2.00's decode boundary-row
+/* Library ABI version: major * 100 + minor (250: 2.00's decode boundary-row
  * list and prefetch hints, 2.10's prefill prefetch hints, 2.20's fused C4
- * decode + norm + RoPE + store, 2.30's 8-bit paged cache, and its store that
- * clears weights). */
+ * decode + norm + RoPE + store, 2.30's 8-bit paged cache, 2.40's store that
+ * clears weights, and the 8-bit cache's rotated append and sparse attention). */
 int ckv_version(void);
 
 #ifdef __cplusplus
