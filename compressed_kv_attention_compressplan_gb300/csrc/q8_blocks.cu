@@ -35,6 +35,74 @@ __device__ __forceinline__ uint32_t score_key(float w) {
   return u ^ (u >> 31 ? 0xFFFFFFFFu : 0x80000000u);
 }
 
+// Rows of up to 32 kKeys blocks: a warp takes a row, its keys in registers, block j in lane j % 32.  The border is found a bit at a
+// time: of the keys' common prefix and a one, how many are not under it?  One vote-free sum over the warp (redux) a bit, and an
+// end as soon as the count is right.
+template <int kKeys>
+__global__ __launch_bounds__(kSelThreads) void q8_select_warp_kernel(const SelectArgs a) {
+  __shared__ uint32_t s_q[CKV_MAX_BATCH];
+  __shared__ BlockReq s_req[CKV_MAX_BATCH];
+  __shared__ unsigned long long s_scan64[kSelThreads / 32 + 1];
+  pdl_wait();
+  pdl_release();
+  scan_queries<kSelThreads>(a.r, s_q, s_req, s_scan64);
+  const uint32_t lane = threadIdx.x & 31, T = a.block_tokens;
+  const uint64_t rows = static_cast<uint64_t>(a.r.num_q) * a.heads;
+  for (uint64_t row = blockIdx.x * static_cast<uint64_t>(kSelThreads / 32) + (threadIdx.x >> 5); row < rows;
+       row += gridDim.x * static_cast<uint64_t>(kSelThreads / 32)) {
+    BlockReq req;
+    uint32_t i;
+    if (!request_of(static_cast<uint32_t>(row / a.heads), s_q, s_req, a.r.batch, &req, &i)) continue;
+    const uint32_t n = (seen_by(req, i, a.r.ratio) + T - 1) / T;
+    int32_t* out = a.blocks + row * a.budget;
+    if (n <= a.budget) {
+      for (uint32_t j = lane; j < a.budget; j += 32) out[j] = j < n ? static_cast<int32_t>(j) : -1;
+      continue;
+    }
+    const float* scores = a.scores + row * a.width;
+    const uint32_t hi = n - a.recent;
+    uint32_t key[kKeys];
+#pragma unroll
+    for (int x = 0; x < kKeys; ++x) {
+      const uint32_t j = x * 32 + lane;
+      key[x] = j < n ? __float_as_uint(__ldg(scores + j)) : 0;
+    }
+    // the first and the last ones count as the largest there are, what is not there as nothing
+#pragma unroll
+    for (int x = 0; x < kKeys; ++x) {
+      const uint32_t j = x * 32 + lane;
+      key[x] = j < a.sinks || (j >= hi && j < n) ? 0xFFFFFFFFu : j < n ? score_key(__uint_as_float(key[x])) : 0;
+    }
+    // the largest border that `budget` keys are not under
+    uint32_t border = 0;
+    for (uint32_t bit = 0x80000000u; bit != 0; bit >>= 1) {
+      const uint32_t c = border | bit;
+      uint32_t count = 0;
+#pragma unroll
+      for (int x = 0; x < kKeys; ++x) count += key[x] >= c;
+      count = __reduce_add_sync(0xFFFFFFFFu, count);
+      if (count >= a.budget) border = c;
+      if (count == a.budget) break;
+    }
+    // those above the border, and the first of those at it
+    uint32_t above = 0;
+#pragma unroll
+    for (int x = 0; x < kKeys; ++x) above += key[x] > border;
+    uint32_t left = a.budget - __reduce_add_sync(0xFFFFFFFFu, above), taken = 0;
+#pragma unroll
+    for (int x = 0; x < kKeys; ++x) {
+      const uint32_t j = x * 32 + lane;
+      const uint32_t below = (1u << lane) - 1;
+      const uint32_t ties = __ballot_sync(0xFFFFFFFFu, key[x] == border && j < n);
+      const bool take = key[x] > border || (key[x] == border && j < n && __popc(ties & below) < left);
+      const uint32_t votes = __ballot_sync(0xFFFFFFFFu, take);
+      if (take) out[taken + __popc(votes & below)] = static_cast<int32_t>(j);
+      taken += __popc(votes);
+      left -= min(left, static_cast<uint32_t>(__popc(ties)));
+    }
+  }
+}
+
 // A CTA takes a row.
 __global__ __launch_bounds__(kSelThreads) void q8_select_kernel(const SelectArgs a) {
   constexpr uint32_t kBins = 256;
@@ -265,8 +333,16 @@ int ckv_q8_block_select(const float* scores, uint32_t n_kv_heads, uint32_t width
   a.recent = recent;
   a.blocks = blocks;
   const uint64_t rows = static_cast<uint64_t>(num_q) * n_kv_heads;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (width <= 1024) {
+    const uint64_t ctas = (rows + kSelThreads / 32 - 1) / (kSelThreads / 32);
+    const dim3 grid(static_cast<uint32_t>(std::min<uint64_t>(ctas, 4ull * sm_count())));
+    auto* kernel = width <= 128 ? q8_select_warp_kernel<4> : width <= 256 ? q8_select_warp_kernel<8>
+                   : width <= 512 ? q8_select_warp_kernel<16> : q8_select_warp_kernel<32>;
+    return launch_pdl(kernel, grid, dim3(kSelThreads), 0, s, a);
+  }
   const dim3 grid(static_cast<uint32_t>(std::min<uint64_t>(rows, 8ull * sm_count())));
-  return launch_pdl(q8_select_kernel, grid, dim3(kSelThreads), 0, reinterpret_cast<cudaStream_t>(stream), a);
+  return launch_pdl(q8_select_kernel, grid, dim3(kSelThreads), 0, s, a);
 }
 
 uint64_t ckv_q8_attn_blocks_workspace_bytes(const ckv_q8_cache_t* cache, uint32_t n_heads, uint32_t num_q,
