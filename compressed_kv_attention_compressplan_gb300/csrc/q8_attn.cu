@@ -110,7 +110,7 @@ __global__ __launch_bounds__(kPlanThreads) void plan_q8_attn_kernel(const AttnPl
     }
     return static_cast<uint32_t>(q8_visible(s_kv[b], s_ql[b] - 1 - last, s_ph[b], a.ratio));
   };
-  cut_tiles<kPlanThreads>(a.g, a.plan, static_cast<uint32_t>(total_tiles), a.num_q, a.ratio, a.batch, tiles_of, s_cut);
+  cut_tiles<kPlanThreads, false>(a.g, a.plan, static_cast<uint32_t>(total_tiles), a.num_q, a.ratio, a.batch, tiles_of, s_cut);
   if (t == 0 && total_q != a.num_q) status_or(a.d_status, CKV_STATUS_BAD_TOTAL);
 }
 
@@ -124,7 +124,7 @@ constexpr int kAttnThreads = 32 * kAttnWarps;
 constexpr int kTile = 16;  // entries a warp takes at a time
 
 // kDw channels of a warp's part of a row, kNp warps to a row (512 channels: 2); kRows query rows of a tile, 8 or 16.
-template <int kDw, int kNp, bool kShared, int kRows>
+template <int kDw, int kNp, bool kShared, int kRows, bool kMany = false>
 struct Cfg {
   static constexpr int kD = kDw * kNp;
   static constexpr int kGroups = kAttnWarps / kNp;  // warp groups, each with tiles of its own
@@ -133,9 +133,9 @@ struct Cfg {
   // As many stages as let kPerSm CTAs share an SM's 227 KB.  Eight rows and 128 channels, 64 requests of 8000 entries (1.05 GB): 162 us with two
   // CTAs of six stages, 186 with three of four; before that by a few instructions a tile more 174, 182, 188 with four of three and 280
   // with one of twelve.
-  static constexpr int kPerSm = kDw == 64 ? 4 : kDw == 128 ? (kRows == 8 ? 2 : 3) : 2;
+  static constexpr int kPerSm = kDw == 64 ? 4 : kDw == 128 ? (kRows == 8 && !kMany ? 2 : 3) : 2;
   static constexpr int kStages = kDw == 64                ? (kShared ? 8 : 6)
-                                 : kDw == 128 && kRows == 8 ? (kShared ? 9 : 6)
+                                 : kDw == 128 && kRows == 8 && !kMany ? (kShared ? 9 : 6)
                                  : kDw == 128               ? (kShared ? 7 : 4)
                                                             : (kShared ? 5 : 3);
   static_assert(kStages <= 16, "");
@@ -145,16 +145,16 @@ struct Cfg {
   static constexpr int kSmem = kRingBytes > kMergeBytes ? kRingBytes : kMergeBytes;
 };
 
-int per_sm_of(uint32_t head_dim, uint32_t rows) { return head_dim == 64 ? 4 : head_dim == 128 && rows == 16 ? 3 : 2; }
+int per_sm_of(uint32_t head_dim, uint32_t rows, bool many) { return head_dim == 64 ? 4 : head_dim == 128 && (rows == 16 || many) ? 3 : 2; }
 
 }  // namespace
 
 int q8_attn_geom(const Q8Cache& c, uint32_t batch, uint32_t num_q, uint32_t n_heads, Q8Geom* g) {
   if (batch > CKV_MAX_BATCH) return CKV_ERR_SIZE;
-  return q8_attn_geom_of(c, batch, num_q, n_heads, g);
+  return q8_attn_geom_of(c, batch, num_q, n_heads, false, g);
 }
 
-int q8_attn_geom_of(const Q8Cache& c, uint32_t batch, uint32_t num_q, uint32_t n_heads, Q8Geom* g) {
+int q8_attn_geom_of(const Q8Cache& c, uint32_t batch, uint32_t num_q, uint32_t n_heads, bool many, Q8Geom* g) {
   if (num_q > CKV_MAX_TOKENS) return CKV_ERR_SIZE;
   if (n_heads == 0 || n_heads % c.heads != 0 || n_heads / c.heads > CKV_Q8_MAX_GROUP) return CKV_ERR_SIZE;
   g->group = n_heads / c.heads;
@@ -175,7 +175,7 @@ int q8_attn_geom_of(const Q8Cache& c, uint32_t batch, uint32_t num_q, uint32_t n
     g->min_quota = 128;  // one request of 2048 latent entries: 20.6 us with one tile a CTA, 29.9 with two, 36 with four
   } else {
     g->rows = static_cast<uint64_t>(num_q) * g->group <= 8ull * batch ? 8 : 16;
-    g->ctas = std::max<uint32_t>(1, static_cast<uint32_t>(sm_count()) * per_sm_of(c.head_dim, g->rows) / c.heads);
+    g->ctas = std::max<uint32_t>(1, static_cast<uint32_t>(sm_count()) * per_sm_of(c.head_dim, g->rows, many) / c.heads);
     g->start_cost = 128;
     g->grain = 16;  // quotas in whole 64 entries: 17.1 us against 15.8 for 8 requests of 1000, 23.2 against 20.8 for 16 of 2000
     g->min_quota = 128;
@@ -211,9 +211,9 @@ namespace {
 // accumulators; the weights cross from entries to rows with one 8 x 8 transposition for eight entries.  One request of 777 entries 8.7 us against
 // 9.4 with sixteen rows, 32 of 300 14.8 against 18.2, 64 of 8000 174 against 179.  What a tile costs in instructions counts to the end: a copy for its scales, sizes on whole tiles'
 // copies and a division were 8 % of the 64 requests' time.
-template <int kDw, int kNp, bool kShared, int kRows, bool kLists>
-__global__ __launch_bounds__(kAttnThreads, (Cfg<kDw, kNp, kShared, kRows>::kPerSm)) void q8_attn_kernel(const AttnArgs a) {
-  using C = Cfg<kDw, kNp, kShared, kRows>;
+template <int kDw, int kNp, bool kShared, int kRows, bool kLists, bool kMany>
+__global__ __launch_bounds__(kAttnThreads, (Cfg<kDw, kNp, kShared, kRows, kMany>::kPerSm)) void q8_attn_kernel(const AttnArgs a) {
+  using C = Cfg<kDw, kNp, kShared, kRows, kMany>;
   constexpr bool kFew = kRows == 8;
   constexpr int kChunks = kDw / 16;             // 16-byte chunks of a row part
   constexpr int kOt = kFew ? kDw / 16 : kDw / 8;  // output tiles
@@ -740,10 +740,10 @@ __global__ __launch_bounds__(kCombineThreads) void q8_combine_kernel(const AttnA
   }
 }
 
-template <int kDw, int kNp, bool kShared, int kRows, bool kLists>
+template <int kDw, int kNp, bool kShared, int kRows, bool kLists, bool kMany = false>
 int launch_attn_for(const AttnArgs& a, cudaStream_t s) {
-  using C = Cfg<kDw, kNp, kShared, kRows>;
-  auto* kernel = q8_attn_kernel<kDw, kNp, kShared, kRows, kLists>;
+  using C = Cfg<kDw, kNp, kShared, kRows, kMany>;
+  auto* kernel = q8_attn_kernel<kDw, kNp, kShared, kRows, kLists, kMany>;
   static std::atomic<uint64_t> done;
   const int rc = allow_smem(reinterpret_cast<const void*>(kernel), C::kSmem, done);
   if (rc) return rc;
@@ -752,6 +752,9 @@ int launch_attn_for(const AttnArgs& a, cudaStream_t s) {
 
 template <int kDw, int kNp, bool kShared, int kRows>
 int launch_attn(const AttnArgs& a, cudaStream_t s) {
+  if constexpr (kDw == 128 && kRows == 8) {
+    if (a.lens != nullptr && a.many) return launch_attn_for<kDw, kNp, kShared, kRows, true, true>(a, s);
+  }
   return a.lens != nullptr ? launch_attn_for<kDw, kNp, kShared, kRows, true>(a, s)
                            : launch_attn_for<kDw, kNp, kShared, kRows, false>(a, s);
 }

@@ -188,67 +188,54 @@ struct ListArgs {
   const int32_t* table;
   uint32_t stride;
   int32_t* tables;   // [num_q, heads, budget]: block numbers
-  uint32_t* lens;    // [num_q, heads]: entries in them
-  uint32_t* most;    // [num_q]: of its heads' lists, the most entries; kInvalidU32: no request's query
+  uint32_t* lens;    // [num_q, heads]: entries in them; kInvalidU32: no request's query
 };
 
-// A CTA takes a query, its warps the kv heads.
+// A warp takes a list.
 __global__ __launch_bounds__(kListThreads) void q8_lists_kernel(const ListArgs a) {
   __shared__ uint32_t s_q[CKV_MAX_BATCH];
   __shared__ BlockReq s_req[CKV_MAX_BATCH];
   __shared__ unsigned long long s_scan[kListThreads / 32 + 1];
-  __shared__ uint32_t s_most;
   pdl_wait();
   pdl_release();
   scan_queries<kListThreads>(a.r, s_q, s_req, s_scan);
-  const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5, T = a.block_tokens;
-  for (uint32_t n = blockIdx.x; n < a.r.num_q; n += gridDim.x) {
-    __syncthreads();  // the query before is written
-    if (threadIdx.x == 0) s_most = 0;
-    __syncthreads();
+  const uint32_t lane = threadIdx.x & 31, T = a.block_tokens;
+  const uint64_t lists = static_cast<uint64_t>(a.r.num_q) * a.heads, step = gridDim.x * static_cast<uint64_t>(kListThreads / 32);
+  for (uint64_t at = blockIdx.x * static_cast<uint64_t>(kListThreads / 32) + (threadIdx.x >> 5); at < lists; at += step) {
     BlockReq req;
     uint32_t i;
-    if (!request_of(n, s_q, s_req, a.r.batch, &req, &i)) {
-      if (threadIdx.x == 0) a.most[n] = kInvalidU32;
+    if (!request_of(static_cast<uint32_t>(at / a.heads), s_q, s_req, a.r.batch, &req, &i)) {
+      if (lane == 0) a.lens[at] = kInvalidU32;
       continue;
     }
     const uint32_t seen = seen_by(req, i, a.r.ratio), visible = (seen + T - 1) / T;
     const int32_t* table = a.table + static_cast<size_t>(req.rid) * a.stride;
-    for (uint32_t h = warp; h < a.heads; h += kListThreads / 32) {
-      const size_t at = static_cast<size_t>(n) * a.heads + h;
-      const int32_t* list = a.blocks + at * a.budget;
-      int32_t* out = a.tables + at * a.budget;
-      int32_t before = -1;  // the largest number so far
-      uint32_t kept = 0;
-      bool part = false, bad = false;
-      for (uint32_t j0 = 0; j0 < a.budget; j0 += 32) {
-        const int32_t v = j0 + lane < a.budget ? list[j0 + lane] : -1;
-        int32_t top = v;  // the largest up to this lane
+    const int32_t* list = a.blocks + at * a.budget;
+    int32_t* out = a.tables + at * a.budget;
+    int32_t before = -1;  // the largest number so far
+    uint32_t kept = 0;
+    bool part = false, bad = false;
+    for (uint32_t j0 = 0; j0 < a.budget; j0 += 32) {
+      const int32_t v = j0 + lane < a.budget ? __ldg(list + j0 + lane) : -1;
+      int32_t top = v;  // the largest up to this lane
 #pragma unroll
-        for (int s = 1; s < 32; s <<= 1) {
-          const int32_t x = __shfl_up_sync(0xFFFFFFFFu, top, s);
-          if (static_cast<int>(lane) >= s) top = max(top, x);
-        }
-        const int32_t up = __shfl_up_sync(0xFFFFFFFFu, top, 1);
-        const int32_t prior = max(before, lane == 0 ? -1 : up);
-        before = max(before, __shfl_sync(0xFFFFFFFFu, top, 31));
-        bad |= v >= 0 && v <= prior;
-        const bool take = v > prior && static_cast<uint32_t>(v) < visible;
-        const uint32_t votes = __ballot_sync(0xFFFFFFFFu, take);
-        if (take) out[kept + __popc(votes & ((1u << lane) - 1))] = __ldg(table + v);
-        part |= take && static_cast<uint32_t>(v) == visible - 1;
-        kept += __popc(votes);
+      for (int s = 1; s < 32; s <<= 1) {
+        const int32_t x = __shfl_up_sync(0xFFFFFFFFu, top, s);
+        if (static_cast<int>(lane) >= s) top = max(top, x);
       }
-      if (__any_sync(0xFFFFFFFFu, bad) && lane == 0) status_or(a.r.d_status, CKV_STATUS_BAD_INDEX);
-      const bool last = __any_sync(0xFFFFFFFFu, part);  // the last block that the query sees, maybe in part, is listed
-      const uint32_t entries = kept * T - (last ? visible * T - seen : 0);
-      if (lane == 0) {
-        a.lens[at] = entries;
-        atomicMax(&s_most, entries);
-      }
+      const int32_t up = __shfl_up_sync(0xFFFFFFFFu, top, 1);
+      const int32_t prior = max(before, lane == 0 ? -1 : up);
+      before = max(before, __shfl_sync(0xFFFFFFFFu, top, 31));
+      bad |= v >= 0 && v <= prior;
+      const bool take = v > prior && static_cast<uint32_t>(v) < visible;
+      const uint32_t votes = __ballot_sync(0xFFFFFFFFu, take);
+      if (take) out[kept + __popc(votes & ((1u << lane) - 1))] = __ldg(table + v);
+      part |= take && static_cast<uint32_t>(v) == visible - 1;
+      kept += __popc(votes);
     }
-    __syncthreads();
-    if (threadIdx.x == 0) a.most[n] = s_most;
+    if (__any_sync(0xFFFFFFFFu, bad) && lane == 0) status_or(a.r.d_status, CKV_STATUS_BAD_INDEX);
+    const bool last = __any_sync(0xFFFFFFFFu, part);  // the last block that the query sees, maybe in part, is listed
+    if (lane == 0) a.lens[at] = kept * T - (last ? visible * T - seen : 0);
   }
 }
 
@@ -256,7 +243,8 @@ constexpr int kPlanThreads = 1024;
 
 struct ListPlanArgs {
   Q8Geom g;
-  const uint32_t* most;
+  const uint32_t* lens;
+  uint32_t heads;
   uint32_t num_q;
   uint8_t* plan;
 };
@@ -268,7 +256,9 @@ __global__ __launch_bounds__(kPlanThreads) void plan_q8_lists_kernel(const ListP
   pdl_release();
   const uint32_t M = a.g.rows, per = (a.g.group + M - 1) / M;  // tiles of a query
   auto tiles = [&](uint32_t tile, Q8Item* r) -> uint32_t {
-    const uint32_t n = tile / per, most = __ldg(a.most + n);
+    const uint32_t n = tile / per;
+    uint32_t most = __ldg(a.lens + static_cast<size_t>(n) * a.heads);  // of the heads' lists, the longest
+    for (uint32_t h = 1; h < a.heads; ++h) most = max(most, __ldg(a.lens + static_cast<size_t>(n) * a.heads + h));
     if (r != nullptr) {
       r->rid = n;
       r->q_start = n;
@@ -279,27 +269,32 @@ __global__ __launch_bounds__(kPlanThreads) void plan_q8_lists_kernel(const ListP
     }
     return most;
   };
-  cut_tiles<kPlanThreads>(a.g, a.plan, a.num_q * per, a.num_q, 1, a.num_q, tiles, s_cut);
+  cut_tiles<kPlanThreads, true>(a.g, a.plan, a.num_q * per, a.num_q, 1, a.num_q, tiles, s_cut);
 }
 
 // Where the workspace's pieces lie.
 struct ListSpace {
-  uint64_t plan, tables, lens, most, parts, bytes;
+  uint64_t plan, tables, lens, parts, bytes;
 };
 
-int list_space(const Q8Cache& c, uint32_t n_heads, uint32_t num_q, uint32_t budget, Q8Geom* g, ListSpace* w) {
+int list_space(const Q8Cache& c, uint32_t n_heads, uint32_t num_q, uint32_t budget, bool many, Q8Geom* g, ListSpace* w) {
   // entries of a list are counted in 32 bits
   if (budget == 0 || static_cast<uint64_t>(budget) * c.block_tokens > 0x7FFFFFF0ull) return CKV_ERR_SIZE;
-  const int rc = q8_attn_geom_of(c, num_q, num_q, n_heads, g);
-  if (rc) return rc;
+  // one size for both: the caller asks for it without naming the batch, which decides between them
+  uint64_t plan = 0, parts = 0;
+  for (int i = 0; i < 2; ++i) {
+    const int rc = q8_attn_geom_of(c, num_q, num_q, n_heads, i == 0 ? !many : many, g);
+    if (rc) return rc;
+    plan = std::max(plan, g->bytes);
+    parts = std::max(parts, g->workspace);
+  }
   auto up = [](uint64_t x) { return (x + 255) & ~255ull; };
   const uint64_t lists = static_cast<uint64_t>(num_q) * c.heads;
   w->plan = 0;
-  w->tables = up(g->bytes);
+  w->tables = up(plan);
   w->lens = up(w->tables + lists * budget * 4);
-  w->most = up(w->lens + lists * 4);
-  w->parts = up(w->most + static_cast<uint64_t>(num_q) * 4);
-  w->bytes = w->parts + g->workspace;
+  w->parts = up(w->lens + lists * 4);
+  w->bytes = w->parts + parts;
   return CKV_OK;
 }
 
@@ -350,7 +345,7 @@ uint64_t ckv_q8_attn_blocks_workspace_bytes(const ckv_q8_cache_t* cache, uint32_
   Q8Cache c;
   Q8Geom g;
   ListSpace w;
-  if (q8_cache_of(cache, &c) || list_space(c, n_heads, num_q, budget, &g, &w)) return 0;
+  if (q8_cache_of(cache, &c) || list_space(c, n_heads, num_q, budget, false, &g, &w)) return 0;
   return w.bytes;
 }
 
@@ -367,7 +362,8 @@ int ckv_q8_attn_blocks(const ckv_q8_cache_t* cache, uint32_t n_heads, uint32_t r
   if (!(scale > 0.0f) || !(scale < 1e30f)) return CKV_ERR_SIZE;
   rc = check_lens(batch, ratio, seq_lens, extend_lens, kv_lens);
   if (rc) return rc;
-  rc = list_space(a.c, n_heads, num_q, budget, &a.g, &w);
+  a.many = num_q > 2 * batch;
+  rc = list_space(a.c, n_heads, num_q, budget, a.many, &a.g, &w);
   if (rc) return rc;
   if (num_q == 0 || batch == 0) return CKV_OK;
   rc = check_table(block_table, table_stride, num_reqs);
@@ -390,10 +386,10 @@ int ckv_q8_attn_blocks(const ckv_q8_cache_t* cache, uint32_t n_heads, uint32_t r
   l.stride = static_cast<uint32_t>(table_stride);
   l.tables = reinterpret_cast<int32_t*>(space + w.tables);
   l.lens = reinterpret_cast<uint32_t*>(space + w.lens);
-  l.most = reinterpret_cast<uint32_t*>(space + w.most);
-  rc = launch_pdl(q8_lists_kernel, dim3(std::min<uint32_t>(num_q, 4 * sm_count())), dim3(kListThreads), 0, s, l);
+  const uint64_t ctas = (static_cast<uint64_t>(num_q) * a.c.heads + kListThreads / 32 - 1) / (kListThreads / 32);
+  rc = launch_pdl(q8_lists_kernel, dim3(static_cast<uint32_t>(std::min<uint64_t>(ctas, 4ull * sm_count()))), dim3(kListThreads), 0, s, l);
   if (rc) return rc;
-  ListPlanArgs p{a.g, l.most, num_q, space + w.plan};
+  ListPlanArgs p{a.g, l.lens, a.c.heads, num_q, space + w.plan};
   rc = launch_pdl(plan_q8_lists_kernel, dim3(1), dim3(kPlanThreads), 0, s, p);
   if (rc) return rc;
 

@@ -16,7 +16,7 @@
 
 namespace ckv {
 
-struct Q8Item {  // 48 bytes
+struct alignas(16) Q8Item {  // 48 bytes, read and written 16 at a time
   uint32_t rid;
   uint32_t q_start;   // ragged query of the request's first row
   uint32_t q_len;
@@ -65,7 +65,9 @@ struct Q8Geom {
 // From sizes alone (and the device's SM count), the same for the plan and the
 // attention call.  CKV_OK or CKV_ERR_SIZE.
 int q8_attn_geom(const Q8Cache& c, uint32_t batch, uint32_t num_q, uint32_t n_heads, Q8Geom* g);
-int q8_attn_geom_of(const Q8Cache& c, uint32_t batch, uint32_t num_q, uint32_t n_heads, Q8Geom* g);  // any batch
+// Any batch.  many: several queries a request, whose lists name the same blocks: entries come from L2, and the split kernel hides its
+// own latency with more CTAs instead of memory's with deeper rings.
+int q8_attn_geom_of(const Q8Cache& c, uint32_t batch, uint32_t num_q, uint32_t n_heads, bool many, Q8Geom* g);
 
 // Arguments of the attention kernels.
 struct AttnArgs {
@@ -81,6 +83,7 @@ struct AttnArgs {
   uint32_t stride;
   uint32_t num_reqs;
   const uint32_t* lens;  // NULL; or a table for each (request, kv head), and its entries here
+  bool many;             // see q8_attn_geom_of
   const uint8_t* plan;
   int out_f32;
   void* out;
@@ -137,17 +140,19 @@ struct CutShared {
   unsigned long long pos[kThreads];
   uint32_t item[kThreads], part[kThreads];
   unsigned long long scan[2][kThreads / 32 + 1];
-  uint32_t most;
+  uint32_t most, longest;
 };
 
 // Lays nt tiles' costs end to end, cuts them at multiples of one quota and writes the plan: header, first items, split tiles and items.
+// Fewer tiles than CTAs may be cut evenly instead (kEven), each into pieces of one length and a CTA to a piece: no CTA then starts
+// two tiles, which is most of a piece's time where tiles are short.
 // By one CTA, whose threads all call it.  tiles(tile, item) gives a tile's entries (kInvalidU32: the tile
 // is left out) and, where item is not NULL, its rid, q_start, q_len, row0, kv_len and phase.
-template <int kThreads, typename Tiles>
+template <int kThreads, bool kEven, typename Tiles>
 __device__ __forceinline__ void cut_tiles(const Q8Geom& g, uint8_t* plan, uint32_t nt, uint32_t num_q, uint32_t ratio, uint32_t batch,
                                           const Tiles& tiles, CutShared<kThreads>& sh) {
   const uint32_t t = threadIdx.x;
-  if (t == 0) sh.most = 0;  // the scans' barriers come before its use
+  if (t == 0) sh.most = sh.longest = 0;  // the scans' barriers come before their use
   Q8Header* head = reinterpret_cast<Q8Header*>(plan);
   uint32_t* first = reinterpret_cast<uint32_t*>(plan + g.off_first);
   uint32_t* split = reinterpret_cast<uint32_t*>(plan + g.off_split);
@@ -170,6 +175,17 @@ __device__ __forceinline__ void cut_tiles(const Q8Geom& g, uint8_t* plan, uint32
     return narrow ? static_cast<uint32_t>(x) / static_cast<uint32_t>(quota) : x / quota;
   };
 
+  uint32_t piece = 0;  // entries of an even piece
+  if (kEven && nt <= kThreads) {
+    const uint32_t seen = t < nt ? tiles(t, nullptr) : kInvalidU32;
+    if (seen != kInvalidU32) atomicMax(&sh.longest, seen);
+    const uint32_t valid = __syncthreads_count(seen != kInvalidU32), pieces = valid ? g.ctas / valid : 0;
+    if (pieces > 0) {
+      const uint32_t len = max(g.min_quota, ((sh.longest + pieces - 1) / pieces + grain - 1) & ~(grain - 1));
+      if (len <= quota) piece = len;
+    }
+  }
+
   unsigned long long pos0 = 0;
   uint32_t item0 = 0, part0 = 0, split0 = 0;
   for (uint32_t i0 = 0; i0 < nt; i0 += kThreads) {
@@ -179,6 +195,7 @@ __device__ __forceinline__ void cut_tiles(const Q8Geom& g, uint8_t* plan, uint32
     unsigned long long cost_sum = total, packed_sum, p = before;  // a single strip's sums are known
     if (nt > kThreads) p = pos0 + block_exclusive<kThreads>(cost, &cost_sum, sh.scan[0]);
     if (cost) n = static_cast<uint32_t>(shares(p + cost - 1) - shares(p)) + 1;
+    if (kEven && piece && cost) n = max(1u, (tiles(i, nullptr) + piece - 1) / piece);
     // items (32 bits), parts (16) and splits (16) of the strip, in one scan: parts are at most twice the CTAs
     const unsigned long long pk = n | (static_cast<unsigned long long>(n > 1 ? n : 0) << 32) |
                                   (static_cast<unsigned long long>(n > 1) << 48);
@@ -198,6 +215,17 @@ __device__ __forceinline__ void cut_tiles(const Q8Geom& g, uint8_t* plan, uint32
       const uint32_t s = last_not_above(sh.item, strip, k);
       Q8Item r;
       const uint32_t seen = tiles(i0 + s, &r);
+      if (kEven && piece) {
+        r.chunk = k - sh.item[s];
+        r.chunks = max(1u, (seen + piece - 1) / piece);
+        r.kv_begin = r.chunk * piece;
+        r.kv_end = min(seen, r.kv_begin + piece);
+        r.part = static_cast<int32_t>(sh.part[s]);
+        r.reserved = 0;
+        items[k] = r;
+        first[k] = k;
+        continue;
+      }
       const unsigned long long len = cost_of(seen);
       const unsigned long long P = sh.pos[s], cut = shares(P);
       const uint32_t c = k - sh.item[s];
@@ -221,7 +249,7 @@ __device__ __forceinline__ void cut_tiles(const Q8Geom& g, uint8_t* plan, uint32
     __syncthreads();
   }
   if (t == 0) {
-    const uint32_t ctas = static_cast<uint32_t>(shares(total + quota - 1));
+    const uint32_t ctas = kEven && piece ? item0 : static_cast<uint32_t>(shares(total + quota - 1));
     first[ctas] = item0;
     head->items = item0;
     head->ctas = ctas;

@@ -544,18 +544,24 @@ def test_attn_blocks(case, ragged):
 
 @pytest.mark.parametrize("heads,H,D,latent", [(8, 2, 128, False), (64, 1, 512, True), (96, 1, 256, False), (128, 1, 128, False)])
 def test_all_blocks_listed_is_attention(heads, H, D, latent):
-    """The same kernels over the same entries: bit for bit, whichever way the block table is named."""
+    """The two plans cut a row's entries in other places, so that its sums are rounded in another order: each call is within
+    attn_bounds of the exact result, hence they are within twice that of one another."""
     w = World(740, [700, 90, 0, 16], H, D, 16, latent)
     q, one = w.queries([1] * 4, heads), [1] * 4
     lists = np.full((4, H, 50), -1, np.int32)
     for b, n in enumerate(w.lens):
         lists[b, :, :-(-n // 16)] = np.arange(-(-n // 16))
     seq = seq_of(w.lens, one, 1)
-    out, lse, st = run_attn(w, q, lists, seq, one, 1, F32)
+    out, lse = check_attn(w, q, lists, seq, one, 1, F32)
     cache, args = w.cache(), (i64(w.rid), i64(seq), i64(one), i64(w.lens))
     plan = ckv.plan_q8_attn(cache, heads, 1, *args, 4)
-    want, want_lse = ckv.q8_attn(cache, q.to(DEV), plan, i32(w.table), 1 / math.sqrt(D), out_dtype=F32)
-    assert st == 0 and torch.equal(out, want) and torch.equal(lse, want_lse)
+    other, other_lse = ckv.q8_attn(cache, q.to(DEV), plan, i32(w.table), 1 / math.sqrt(D), out_dtype=F32)
+    want, wl, mag, big, flat = bref.attn(w.k, w.ks, w.v, w.vs, q.float().numpy(), lists, w.rid, seq, one, w.lens, w.table, 1, 1 / math.sqrt(D))
+    tol, ltol = attn_bounds(D, 800, want, wl, mag, big, flat, 448 * np.nanmax(w.ks if latent else w.vs), False, eight_bit(D, heads // H))
+    assert (np.abs((out - other).cpu().numpy()) <= 2 * tol).all()
+    assert torch.equal(torch.isneginf(lse), torch.isneginf(other_lse))
+    fin = np.isfinite(wl)
+    assert (np.abs(lse.cpu().numpy()[fin] - other_lse.cpu().numpy()[fin]) <= 2 * ltol[fin]).all()
 
 
 @pytest.mark.parametrize("heads,D,latent", [(8, 128, False), (64, 512, True), (48, 256, False), (72, 64, False)])
