@@ -12,7 +12,7 @@
 #include <algorithm>
 
 #include "async_copy.cuh"
-#include "q8_blocks.cuh"
+#include "q8_score.cuh"
 
 namespace ckv {
 namespace {
@@ -32,9 +32,6 @@ struct BoundArgs {
   uint32_t num_reqs;
   uint32_t* d_status;
 };
-
-__device__ __forceinline__ __half2 as_half2(uint32_t x) { return *reinterpret_cast<const __half2*>(&x); }
-__device__ __forceinline__ uint32_t as_u32(__half2 x) { return *reinterpret_cast<const uint32_t*>(&x); }
 
 // The e4m3 pairs that two fp16 pairs are (exact, NaN stays NaN).
 __device__ __forceinline__ uint32_t e4m3_of(uint32_t lo, uint32_t hi) {
@@ -137,37 +134,7 @@ __global__ __launch_bounds__(kBoundThreads) void q8_bounds_kernel(const BoundArg
 // add their sums through shared memory.
 constexpr int kScoreWarps = 8;
 constexpr int kScoreThreads = 32 * kScoreWarps;
-constexpr int kTileBlocks = 16;
-
-struct ScoreArgs {
-  Q8Cache c;
-  BlockReqs r;
-  const uint8_t* bounds;
-  const __nv_bfloat16* q;
-  uint32_t n_heads, group;
-  uint32_t span;     // rows that a query takes: the group, up to a power of two or a multiple of eight
-  uint32_t rows;     // query rows in shared memory: whole queries, or a part of one
-  uint32_t queries;  // of a segment
-  uint32_t parts;    // of a query that has more rows
-  float scale;
-  const int32_t* table;
-  uint32_t stride;
-  uint32_t width;
-  float* scores;
-};
-
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
-
-// Tiles of the blocks that a request's queries see.
-__device__ __forceinline__ uint32_t score_tiles(const BlockReq& r, uint32_t ratio, uint32_t t_shift) {
-  if (r.q_len == 0) return 0;
-  const uint32_t blocks = (seen_by(r, r.q_len - 1, ratio) + (1u << t_shift) - 1) >> t_shift;  // later queries see no less
-  return (blocks + kTileBlocks - 1) / kTileBlocks;
-}
+constexpr uint32_t kTileBlocks = 16;
 
 // The requests, the tiles before each, and those of all.
 __device__ __forceinline__ unsigned long long scan_tiles(const ScoreArgs& a, uint32_t* s_q, BlockReq* s_req, unsigned long long* s_tile,
@@ -179,7 +146,7 @@ __device__ __forceinline__ unsigned long long scan_tiles(const ScoreArgs& a, uin
     const uint32_t b = b0 + threadIdx.x;
     unsigned long long n = 0;
     if (b < a.r.batch)
-      n = static_cast<unsigned long long>((s_req[b].q_len + a.queries - 1) / a.queries) * a.c.heads * score_tiles(s_req[b], a.r.ratio, t_shift);
+      n = static_cast<unsigned long long>((s_req[b].q_len + a.queries - 1) / a.queries) * a.c.heads * score_tiles<kTileBlocks>(s_req[b], a.r.ratio, t_shift);
     unsigned long long sum;
     const unsigned long long at = total + block_exclusive<kScoreThreads>(n, &sum, s_scan);
     if (b < a.r.batch) s_tile[b] = at;
@@ -187,18 +154,6 @@ __device__ __forceinline__ unsigned long long scan_tiles(const ScoreArgs& a, uin
   }
   __syncthreads();
   return total;
-}
-
-// -infinity for the blocks behind a request's last tile.
-__device__ __forceinline__ void fill_behind(const ScoreArgs& a, const uint32_t* s_q, const BlockReq* s_req) {
-  const uint32_t H = a.c.heads, lane = threadIdx.x & 31, t_shift = __ffs(a.c.block_tokens) - 1;
-  const uint64_t rows = static_cast<uint64_t>(a.r.num_q) * H, step = gridDim.x * static_cast<uint64_t>(kScoreWarps);
-  for (uint64_t row = blockIdx.x * static_cast<uint64_t>(kScoreWarps) + (threadIdx.x >> 5); row < rows; row += step) {
-    BlockReq req;
-    uint32_t i;
-    if (!request_of(static_cast<uint32_t>(row / H), s_q, s_req, a.r.batch, &req, &i)) continue;
-    for (uint32_t j = score_tiles(req, a.r.ratio, t_shift) * kTileBlocks + lane; j < a.width; j += 32) a.scores[row * a.width + j] = -INFINITY;
-  }
 }
 
 // Few query rows (a decode step): a segment is a (request, kv head, eight query rows), and a share is a warp's, so that
@@ -243,7 +198,7 @@ __global__ __launch_bounds__(kScoreThreads, 2) void q8_score_few_kernel(const Sc
     at.b = last_not_above(s_tile, a.r.batch, begin);
     {
       const BlockReq req = s_req[at.b];
-      at.tiles = score_tiles(req, a.r.ratio, t_shift);
+      at.tiles = score_tiles<kTileBlocks>(req, a.r.ratio, t_shift);
       const unsigned long long rel = begin - s_tile[at.b], seg = rel / at.tiles;
       const uint32_t chunks = (req.q_len + a.queries - 1) / a.queries;
       at.tile = static_cast<uint32_t>(rel - seg * at.tiles);
@@ -259,7 +214,7 @@ __global__ __launch_bounds__(kScoreThreads, 2) void q8_score_few_kernel(const Sc
       if (++x.h < H) return;
       x.h = 0;
       do ++x.b;
-      while (x.b < a.r.batch && (x.tiles = score_tiles(s_req[x.b], a.r.ratio, t_shift)) == 0);
+      while (x.b < a.r.batch && (x.tiles = score_tiles<kTileBlocks>(s_req[x.b], a.r.ratio, t_shift)) == 0);
     };
     // ---- copies, two steps ahead
     const uint32_t ring = smem_addr(smem) + warp * C::kStages * C::kStage;
@@ -411,7 +366,7 @@ __global__ __launch_bounds__(kScoreThreads, 2) void q8_score_few_kernel(const Sc
     }
     cp_async_wait<0>();
   }
-  fill_behind(a, s_q, s_req);
+  fill_behind<kTileBlocks>(a, s_q, s_req);
 }
 
 template <int kD>
@@ -455,7 +410,7 @@ __global__ __launch_bounds__(kScoreThreads, 2) void q8_score_kernel(const ScoreA
   for (unsigned long long pos = blockIdx.x * share; pos < end;) {
     const uint32_t b = last_not_above(s_tile, a.r.batch, pos);
     const BlockReq req = s_req[b];
-    const uint32_t q0 = s_q[b], tiles = score_tiles(req, a.r.ratio, t_shift), chunks = (req.q_len + a.queries - 1) / a.queries;
+    const uint32_t q0 = s_q[b], tiles = score_tiles<kTileBlocks>(req, a.r.ratio, t_shift), chunks = (req.q_len + a.queries - 1) / a.queries;
     const unsigned long long rel = pos - s_tile[b], seg = rel / tiles;
     const uint32_t tile0 = static_cast<uint32_t>(rel - seg * tiles);
     const uint32_t tile1 = static_cast<uint32_t>(min(static_cast<unsigned long long>(tiles), tile0 + (end - pos)));
@@ -645,12 +600,15 @@ __global__ __launch_bounds__(kScoreThreads, 2) void q8_score_kernel(const ScoreA
       cp_async_wait<0>();
     }
   }
-  fill_behind(a, s_q, s_req);
+  fill_behind<kTileBlocks>(a, s_q, s_req);
 }
 
 template <int kD>
 int launch_scores(ScoreArgs a, cudaStream_t s) {
   using C = ScoreCfg<kD>;
+  if constexpr (kD <= 128) {
+    if (a.group <= 64 && static_cast<uint64_t>(a.r.num_q) * a.span > 64ull * a.r.batch) return launch_q8_score_tc(a, s);
+  }
   if (static_cast<uint64_t>(a.r.num_q) * a.span <= 8ull * a.r.batch) {
     static std::atomic<uint64_t> few_done;
     auto* few = q8_score_few_kernel<kD>;
@@ -741,6 +699,7 @@ int ckv_q8_block_scores(const ckv_q8_cache_t* cache, const void* bounds, uint32_
   a.stride = static_cast<uint32_t>(table_stride);
   a.width = width;
   a.scores = scores;
+  a.wait_ns = wait_limit_ns();
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   switch (a.c.head_dim) {
     case 64: return launch_scores<64>(a, s);

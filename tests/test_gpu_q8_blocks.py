@@ -888,3 +888,73 @@ def test_shapes_that_the_binding_refuses():
                  lambda: ckv.q8_attn_blocks(cache, q, lists, 1, *a, table, 0.1, workspace=torch.zeros(64, dtype=torch.uint8, device=DEV))):
         with pytest.raises(ckv.CkvError):
             call()
+
+
+# ------------------------------------------------------------------------------------------ scores of many query rows
+MANY = [  # lens, q_lens, heads, H, D, T, ratio
+    ([700], [200], 4, 1, 128, 16, 1),
+    ([700, 40, 0], [90, 40, 70], 8, 2, 64, 16, 1),
+    ([5000], [130], 1, 1, 128, 32, 1),             # several tiles of blocks
+    ([2100, 2048, 2049], [128, 256, 129], 2, 2, 64, 16, 1),
+    ([900], [70], 7, 1, 128, 64, 4),
+    ([900, 30], [70, 30], 24, 2, 128, 16, 1),      # 12 heads to a kv head: rows of heads that do not exist
+    ([900], [40], 64, 1, 128, 128, 1),
+    ([900], [33], 33, 1, 64, 16, 1),
+    ([3000], [5], 64, 1, 64, 16, 128),
+    ([300] * 20, [20] * 20, 16, 1, 128, 16, 1),
+    ([600], [300], 3, 1, 256, 16, 1),              # more channels than the tensor-core kernel takes
+    ([600], [50], 70, 1, 128, 16, 1),              # and more heads
+]
+
+
+@pytest.mark.parametrize("case", range(len(MANY)))
+def test_scores_of_many_rows(case):
+    lens, q_lens, heads, H, D, T, ratio = MANY[case]
+    w = World(900 + case, lens, H, D, T, True)
+    check_scores(w, w.queries(q_lens, heads), seq_of(lens, q_lens, ratio), q_lens, heads, ratio)
+
+
+def test_scores_of_many_rows_with_nan_missing_blocks_and_other_widths():
+    w = World(930, [700, 300], 2, 128, 16, True)
+    ql, heads = [150, 100], 8
+    bnd, q = bounds_of(w), w.queries(ql, heads)
+    bnd[w.table[w.rid[0], 2], 0, :, 9] = 0x7F
+    q[7, 5, 3] = float("nan")
+    q[200, 0, 7] = float("inf")
+    args = i64(w.rid), i64(w.lens), i64(ql), i64(w.lens)
+    want, mag, flat = bref.scores(bnd, w.ks, q.float().numpy(), w.rid, w.lens, ql, w.lens, w.table, 16, 1, 0.07, 60)
+    st = status()
+    got = ckv.q8_block_scores(w.cache(), up(bnd), q.to(DEV), 1, *args, i32(w.table), 0.07, width=60, status=st).cpu().numpy()
+    assert int(st[0]) == 0 and np.array_equal(np.isnan(got), np.isnan(want))
+    inf = np.isinf(want)
+    assert np.array_equal(got[inf], want[inf])
+    fin = np.isfinite(want)
+    assert (np.abs(got[fin] - want[fin]) <= (mag * 260 * 2.0 ** -23 + flat * 2.0 ** -38)[fin]).all()
+    table = w.table.copy()
+    table[w.rid[1], 3], table[w.rid[1], 0] = -1, w.blocks
+    out = torch.full((260, 2, 60), 3.0, device=DEV)  # ten rows behind the last request's
+    more = torch.cat([q, q[:10]]).to(DEV)
+    ckv.q8_block_scores(w.cache(), up(bnd), more, 1, *args, i32(table), 0.07, scores=out, status=st)
+    assert int(st[0]) == ckv.STATUS_BAD_INDEX | ckv.STATUS_BAD_TOTAL
+    assert (out[250:] == 3.0).all() and torch.isneginf(out[150:250, :, [0, 3]]).all()
+    again = out[:250].cpu().numpy()
+    again[150:, :, [0, 3]] = got[150:, :, [0, 3]]
+    assert np.array_equal(again, got, equal_nan=True)
+
+
+def test_score_waits_that_run_out_are_reported_and_leave_the_context_usable():
+    w = World(931, [3000], 2, 128, 16, True)
+    q, bnd, cache = w.queries([400], 8).to(DEV), up(bounds_of(w)), w.cache()
+    args = i64(w.rid), i64(w.lens), i64([400]), i64(w.lens), i32(w.table)
+    want = ckv.q8_block_scores(cache, bnd, q, 1, *args, 0.1)
+    torch.cuda.synchronize()
+    old = ckv.set_wait_limit_ns(1)
+    try:
+        st = status()
+        ckv.q8_block_scores(cache, bnd, q, 1, *args, 0.1, status=st)
+        torch.cuda.synchronize()
+    finally:
+        ckv.set_wait_limit_ns(old)
+    assert int(st[0]) & ckv.STATUS_TIMEOUT
+    st.zero_()
+    assert torch.equal(ckv.q8_block_scores(cache, bnd, q, 1, *args, 0.1, status=st), want) and int(st[0]) == 0
