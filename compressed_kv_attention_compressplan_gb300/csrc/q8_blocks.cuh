@@ -65,7 +65,9 @@ __device__ __forceinline__ bool request_of(uint32_t n, const uint32_t* s_q, cons
 
 // Entries that query i of a request sees.
 __device__ __forceinline__ uint32_t seen_by(const BlockReq& r, uint32_t i, uint32_t ratio) {
-  return static_cast<uint32_t>(q8_visible(r.kv_len, r.q_len - 1 - i, r.phase, ratio));
+  const uint32_t after = r.q_len - 1 - i;
+  if (ratio == 1) return r.kv_len - min(r.kv_len, after);  // without the division
+  return static_cast<uint32_t>(q8_visible(r.kv_len, after, r.phase, ratio));
 }
 
 // Host checks of the lengths' arrays.

@@ -4,7 +4,7 @@
 // With blocks as the product's rows a thread of the epilogue owns a block: the maximum over a query's heads is one over its own
 // registers, and a warp's scores of a query are 128 consecutive bytes.
 //
-// A unit is 128 blocks of a (request, kv head) and some row tiles of it.  Roles: eight warps make the
+// A unit is 128 blocks of a (request, kv head) and some row tiles of it.  Roles: sixteen warps make the
 // operands (fp16, exact from e4m3; query rows scaled by a power of two), the next tile's loads on their way while one
 // is stored; one thread issues the products; eight warps finish the scores.  Rows of heads that do not exist repeat the
 // group's last head, so that no maximum has to leave them out.
@@ -20,14 +20,14 @@ constexpr uint32_t kTile = 128;  // blocks, and query rows, of a product
 
 template <int kD>
 struct StCfg {
-  static constexpr int kLoadWarps = 8, kOutWarps = 8;
+  static constexpr int kLoadWarps = 16, kOutWarps = 8;
   static constexpr int kWarps = kLoadWarps + kOutWarps + 1;
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kSlices = 2 * kD / 64;  // of 64 values of the depth
   static constexpr uint32_t kOperand = kSlices * kSlice;
   static constexpr int kLanes = kD / 8;          // threads of a query row, and of a block's bounds, 16 bytes each
   static constexpr int kRows = 32 / kLanes;      // rows of a warp at a time
-  static constexpr int kTimes = 16 / kRows;      // for its sixteen of a tile
+  static constexpr int kTimes = kTile / kLoadWarps / kRows;  // for its share of a tile
   static constexpr uint32_t kBytes = 3 * kOperand + 1024;  // bounds, two stages of queries, the alignment
   static constexpr uint32_t kSmem = kBytes < 120 * 1024 ? 120 * 1024 : kBytes;  // one CTA to an SM: see the attention
   static constexpr uint32_t kCols = 256;
@@ -111,8 +111,8 @@ __global__ __launch_bounds__(StCfg<kD>::kThreads, 1) void q8_score_tc_kernel(con
   // every role walks the same (unit, row tile) sequence; uc and qc count units and row tiles
   uint32_t uc = 0, qc = 0;
   if (warp < C::kLoadWarps) {
-    // ---- operands.  A warp makes rows 16 warp .. of each; lane l has 16 bytes, chunk l % kLanes, of a row
-    const uint32_t chunk = lane % C::kLanes, row0 = warp * 16 + lane / C::kLanes;
+    // ---- operands.  A warp makes its share of the rows of each; lane l has 16 bytes, chunk l % kLanes, of a row
+    const uint32_t chunk = lane % C::kLanes, row0 = warp * (kTile / C::kLoadWarps) + lane / C::kLanes;
     const __half2 zero = __float2half2_rn(0.0f);
     int32_t blk[C::kTimes];
     auto ask = [&](unsigned long long u) {
@@ -124,22 +124,6 @@ __global__ __launch_bounds__(StCfg<kD>::kThreads, 1) void q8_score_tc_kernel(con
       for (int i = 0; i < C::kTimes; ++i) {
         const uint32_t j = x.block0 + row0 + i * C::kRows;
         blk[i] = j < blocks ? ld_ahead(a.table + static_cast<size_t>(r.rid) * a.stride + j) : -1;
-      }
-    };
-    uint4 bounds[C::kTimes];
-    float scale[C::kTimes];
-    auto load_bounds = [&](unsigned long long u) {  // by the numbers asked for
-      if (u >= units) return;
-      const StUnit x = unit_of(u);
-      const BlockReq r = sh.req[x.b];
-      const uint32_t blocks = (seen_by(r, r.q_len - 1, a.r.ratio) + T - 1) >> t_shift;
-#pragma unroll
-      for (int i = 0; i < C::kTimes; ++i) {
-        const bool ok = static_cast<uint32_t>(blk[i]) < a.c.num_blocks;
-        if (!ok && chunk == 0 && x.block0 + row0 + i * C::kRows < blocks) status_or(a.r.d_status, CKV_STATUS_BAD_INDEX);
-        const size_t bh = static_cast<size_t>(ok ? blk[i] : 0) * H + x.h;
-        bounds[i] = ld_stream16_if(a.bounds + bh * 2 * kD + chunk * 16, ok);
-        scale[i] = ok ? ld_ahead(a.c.k_scale + bh) : -1.0f;
       }
     };
     uint4 rows[C::kTimes];
@@ -154,11 +138,22 @@ __global__ __launch_bounds__(StCfg<kD>::kThreads, 1) void q8_score_tc_kernel(con
     };
     unsigned long long u = blockIdx.x;
     ask(u);
-    load_bounds(u);
-    if (u < units) load_rows(unit_of(u), 0);
     for (; u < units; u += gridDim.x, ++uc) {
       const StUnit x = unit_of(u);
       const BlockReq r = sh.req[x.b];
+      // A unit's bounds are not kept in registers beside its rows: what does not fit them comes back from L2, as its shared memory
+      // leaves next to no L1 (74 us so, with both a unit ahead).
+      uint4 bounds[C::kTimes];
+      float scale[C::kTimes];
+      const uint32_t blocks = (seen_by(r, r.q_len - 1, a.r.ratio) + T - 1) >> t_shift;
+#pragma unroll
+      for (int i = 0; i < C::kTimes; ++i) {
+        const bool ok = static_cast<uint32_t>(blk[i]) < a.c.num_blocks;
+        if (!ok && chunk == 0 && x.block0 + row0 + i * C::kRows < blocks) status_or(a.r.d_status, CKV_STATUS_BAD_INDEX);
+        const size_t bh = static_cast<size_t>(ok ? blk[i] : 0) * H + x.h;
+        bounds[i] = ld_stream16_if(a.bounds + bh * 2 * kD + chunk * 16, ok);
+        scale[i] = ok ? ld_ahead(a.c.k_scale + bh) : -1.0f;
+      }
       ask(u + gridDim.x);
       w.wait<kShort>(&sh.a_free, (uc & 1) ^ 1);
 #pragma unroll
@@ -173,10 +168,10 @@ __global__ __launch_bounds__(StCfg<kD>::kThreads, 1) void q8_score_tc_kernel(con
                        : "memory");
         if (chunk == 0) sh.ks[uc % 3][n] = scale[i];
       }
+      load_rows(x, 0);
       fence_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_addr(&sh.a_full));
-      load_bounds(u + gridDim.x);
       for (uint32_t t = 0; t < x.tiles; ++t, ++qc) {
         const uint32_t qs = qc & 1;
         w.wait<kShort>(&sh.q_free[qs], ((qc >> 1) & 1) ^ 1);
@@ -212,10 +207,7 @@ __global__ __launch_bounds__(StCfg<kD>::kThreads, 1) void q8_score_tc_kernel(con
           mbar_arrive(smem_addr(&sh.q_full[qs]));
           mbar_arrive(smem_addr(&sh.rows_full[qc & 3]));
         }
-        if (t + 1 < x.tiles)
-          load_rows(x, t + 1);
-        else if (u + gridDim.x < units)
-          load_rows(unit_of(u + gridDim.x), 0);
+        if (t + 1 < x.tiles) load_rows(x, t + 1);
       }
     }
   } else if (warp < C::kLoadWarps + C::kOutWarps) {
@@ -234,50 +226,59 @@ __global__ __launch_bounds__(StCfg<kD>::kThreads, 1) void q8_score_tc_kernel(con
         w.wait<kShort>(&sh.s_full[sb], (qc >> 1) & 1);
         tc_fence_after();
         if (t == 0) ks = sh.ks[uc % 3][entry];
-        float s[2][32];
-        tmem_load32(tmem + lanes + sb * kTile + group * 64, s[0]);
-        tmem_load32(tmem + lanes + sb * kTile + group * 64 + 32, s[1]);
-        tc_fence_before();
-        const float* rf = sh.rf[qc & 3] + group * 64;
-        const uint32_t* lim = sh.lim[qc & 3] + group * 64;
-#pragma unroll
-        for (int c = 0; c < 64; c += 4) {
-          const float4 f = *reinterpret_cast<const float4*>(rf + c);
-          float(&y)[32] = s[c >> 5];
-          y[c & 31] *= f.x;
-          y[(c & 31) + 1] *= f.y;
-          y[(c & 31) + 2] *= f.z;
-          y[(c & 31) + 3] *= f.w;
-        }
         const float k = ks * a.scale;
         const uint32_t n0 = ((x.tile0 + t) * kTile + group * 64) >> span_shift;  // the first row's query
         float* out = a.scores + (static_cast<size_t>(q0 + n0) * H + x.h) * a.width + j;
         const size_t step = static_cast<size_t>(H) * a.width;
+        const uint32_t* lim = sh.lim[qc & 3] + group * 64;
         auto put = [&](uint32_t row, float v) {
           const uint32_t limit = lim[row];
           if (limit == kInvalidU32 || j >= a.width) return;
           out[(row >> span_shift) * step] = j < limit && ks > 0.0f ? v * k : -INFINITY;
         };
-        // a pairwise maximum over a query's rows, in place: after round r every 2^r-th register holds one
-        auto reduce = [&](auto shift) {
-          constexpr int kShift = decltype(shift)::value;
+        float top = -INFINITY;  // of 64 heads, over the first half
+#pragma unroll 1
+        for (int half = 0; half < 64; half += 32) {
+          float s[32];
+          tmem_load32(tmem + lanes + sb * kTile + group * 64 + half, s);
+          const float* rf = sh.rf[qc & 3] + group * 64 + half;
 #pragma unroll
-          for (int d = 1; d < (1 << kShift); d <<= 1) {
-#pragma unroll
-            for (int c = 0; c < 64; c += 2 * d) s[c >> 5][c & 31] = max_nan(s[c >> 5][c & 31], s[(c + d) >> 5][(c + d) & 31]);
+          for (int c = 0; c < 32; c += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(rf + c);
+            s[c] *= f.x;
+            s[c + 1] *= f.y;
+            s[c + 2] *= f.z;
+            s[c + 3] *= f.w;
           }
+          // a pairwise maximum over a query's rows, in place: after round r every 2^r-th register holds one
+          auto reduce = [&](auto shift) {
+            constexpr int kShift = decltype(shift)::value;
 #pragma unroll
-          for (int c = 0; c < 64; c += 1 << kShift) put(c, s[c >> 5][c & 31]);
-        };
-        switch (span_shift) {
-          case 0: reduce(std::integral_constant<int, 0>()); break;
-          case 1: reduce(std::integral_constant<int, 1>()); break;
-          case 2: reduce(std::integral_constant<int, 2>()); break;
-          case 3: reduce(std::integral_constant<int, 3>()); break;
-          case 4: reduce(std::integral_constant<int, 4>()); break;
-          case 5: reduce(std::integral_constant<int, 5>()); break;
-          default: reduce(std::integral_constant<int, 6>()); break;
+            for (int d = 1; d < (1 << kShift); d <<= 1) {
+#pragma unroll
+              for (int c = 0; c < 32; c += 2 * d) s[c] = max_nan(s[c], s[c + d]);
+            }
+          };
+          auto finish = [&](auto shift) {
+            constexpr int kShift = decltype(shift)::value;
+            reduce(shift);
+#pragma unroll
+            for (int c = 0; c < 32; c += 1 << kShift) put(half + c, s[c]);
+          };
+          switch (span_shift) {
+            case 0: finish(std::integral_constant<int, 0>()); break;
+            case 1: finish(std::integral_constant<int, 1>()); break;
+            case 2: finish(std::integral_constant<int, 2>()); break;
+            case 3: finish(std::integral_constant<int, 3>()); break;
+            case 4: finish(std::integral_constant<int, 4>()); break;
+            case 5: finish(std::integral_constant<int, 5>()); break;
+            default:
+              reduce(std::integral_constant<int, 5>());
+              top = max_nan(top, s[0]);
+              if (half != 0) put(0, top);
+          }
         }
+        tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_addr(&sh.s_free[sb]));  // and its rows' factors and limits
       }
