@@ -33,17 +33,29 @@ struct BoundArgs {
   uint32_t* d_status;
 };
 
-// The e4m3 pairs that two fp16 pairs are (exact, NaN stays NaN).
-__device__ __forceinline__ uint32_t e4m3_of(uint32_t lo, uint32_t hi) {
-  uint16_t a, b;
-  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(a) : "r"(lo));
-  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(b) : "r"(hi));
-  return a | (static_cast<uint32_t>(b) << 16);
+// The bounds are looked for in the codes themselves.  An e4m3 code as the upper byte of a bf16 orders as the e4m3 value does, whatever
+// the lower byte holds (it only decides between equal codes), and is finite but for NaN codes: so two channels are compared
+// at once where they lie, and the two between them after one shift, without a conversion.  A NaN code is larger than every other of its
+// sign, or a bf16 NaN that both operations hand on: it is in hi or in lo, and is copied to the other at the end.
+__device__ __forceinline__ void widen(uint32_t w, uint32_t* hi, uint32_t* lo) {
+  auto bf = [](uint32_t x) { return *reinterpret_cast<const __nv_bfloat162*>(&x); };
+  auto word = [](__nv_bfloat162 x) { return *reinterpret_cast<const uint32_t*>(&x); };
+  hi[0] = word(__hmax2_nan(bf(hi[0]), bf(w << 8)));
+  lo[0] = word(__hmin2_nan(bf(lo[0]), bf(w << 8)));
+  hi[1] = word(__hmax2_nan(bf(hi[1]), bf(w)));
+  lo[1] = word(__hmin2_nan(bf(lo[1]), bf(w)));
+}
+__device__ __forceinline__ void codes_of(const uint32_t* hi, const uint32_t* lo, uint32_t* h, uint32_t* l) {
+  *h = __byte_perm(hi[0], hi[1], 0x7351);  // the upper bytes: channels 0, 2 of the first word, 1, 3 of the second
+  *l = __byte_perm(lo[0], lo[1], 0x7351);
+  const uint32_t nan = q8_nan_bytes(*h) | q8_nan_bytes(*l);
+  *h |= nan & 0x7F7F7F7Fu;
+  *l |= nan & 0x7F7F7F7Fu;
 }
 
 // A warp takes a (block, head): lane l holds 16 channels, chunk l % (kD / 16), of every (512 / kD)th entry.
 template <int kD>
-__global__ __launch_bounds__(kBoundThreads) void q8_bounds_kernel(const BoundArgs a) {
+__global__ __launch_bounds__(kBoundThreads, 4) void q8_bounds_kernel(const BoundArgs a) {
   constexpr uint32_t kChunks = kD / 16, kRows = 32 / kChunks;  // chunks of an entry, entries that a warp reads at once
   __shared__ unsigned long long s_unit[CKV_MAX_BATCH];
   __shared__ uint32_t s_first[CKV_MAX_BATCH], s_len[CKV_MAX_BATCH], s_rid[CKV_MAX_BATCH];
@@ -73,52 +85,67 @@ __global__ __launch_bounds__(kBoundThreads) void q8_bounds_kernel(const BoundArg
     units += sum;
   }
   __syncthreads();
+  // An equal share of (block, head) pairs to a warp, the heads of a block one after the other.
   const int lane = threadIdx.x & 31;
-  const unsigned long long warps = static_cast<unsigned long long>(gridDim.x) * (kBoundThreads / 32);
-  for (unsigned long long w = static_cast<unsigned long long>(blockIdx.x) * (kBoundThreads / 32) + (threadIdx.x >> 5); w < units * H;
-       w += warps) {
-    const unsigned long long u = w / H;
-    const uint32_t h = static_cast<uint32_t>(w % H);
-    const uint32_t b = last_not_above(s_unit, a.batch, u);
-    const uint32_t j = s_first[b] + static_cast<uint32_t>(u - s_unit[b]);
-    const int32_t block = __ldg(a.table + static_cast<size_t>(s_rid[b]) * a.stride + j);
-    if (static_cast<uint32_t>(block) >= a.c.num_blocks) {
-      if (lane == 0) status_or(a.d_status, CKV_STATUS_BAD_INDEX);
-      continue;
+  const uint32_t chunk = lane % kChunks, row = lane / kChunks;
+  const unsigned long long pairs = units * H, warps = static_cast<unsigned long long>(gridDim.x) * (kBoundThreads / 32);
+  const unsigned long long share = (pairs + warps - 1) / warps;
+  const unsigned long long first = (static_cast<unsigned long long>(blockIdx.x) * (kBoundThreads / 32) + (threadIdx.x >> 5)) * share;
+  if (first >= pairs) return;
+  const unsigned long long u = first / H;
+  uint32_t h = static_cast<uint32_t>(first - u * H), b = last_not_above(s_unit, a.batch, u);
+  uint32_t j = s_first[b] + static_cast<uint32_t>(u - s_unit[b]);
+  auto number = [&]() { return __ldg(a.table + static_cast<size_t>(s_rid[b]) * a.stride + j); };
+  int32_t block = number();
+  for (uint32_t left = static_cast<uint32_t>(min(share, pairs - first)); left > 0; --left) {
+    const bool ok = static_cast<uint32_t>(block) < a.c.num_blocks;
+    if (!ok && lane == 0) status_or(a.d_status, CKV_STATUS_BAD_INDEX);
+    const uint32_t n = ok ? min(T, s_len[b] - j * T) : 0;
+    const uint8_t* k = a.c.k + (static_cast<size_t>(ok ? block : 0) * H + h) * T * kD + chunk * 16;
+    uint8_t* to = a.bounds + (static_cast<size_t>(ok ? block : 0) * H + h) * 2 * kD + chunk * 16;
+    // the next pair's place; a block's number is asked for before this pair's work
+    if (++h == H) {
+      h = 0;
+      if (left > 1) {
+        if (++j >= (s_len[b] + T - 1) / T) {
+          do ++b;
+          while (b + 1 < a.batch && s_unit[b + 1] == s_unit[b]);
+          j = s_first[b];
+        }
+        block = number();
+      }
     }
-    const uint32_t n = min(T, s_len[b] - j * T), chunk = lane % kChunks, row = lane / kChunks;
-    const uint8_t* k = a.c.k + (static_cast<size_t>(block) * H + h) * T * kD + chunk * 16;
-    uint32_t hi[8], lo[8];  // fp16 pairs
+    if (!ok) continue;
+    uint32_t hi[8], lo[8];
 #pragma unroll
     for (int z = 0; z < 8; ++z) {
-      hi[z] = 0xFC00FC00u;  // -infinity
-      lo[z] = 0x7C007C00u;
+      hi[z] = 0xFF80FF80u;  // -infinity
+      lo[z] = 0x7F807F80u;
     }
 #pragma unroll 8
     for (uint32_t r = row; r < n; r += kRows) {
       const uint4 v = ld_stream16(k + r * kD);
-      const uint32_t x[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-      for (int z = 0; z < 4; ++z) {
-        const __half2 p = as_half2(q8_lo_f16x2(x[z])), q = as_half2(q8_hi_f16x2(x[z]));
-        hi[2 * z] = as_u32(__hmax2_nan(as_half2(hi[2 * z]), p));
-        lo[2 * z] = as_u32(__hmin2_nan(as_half2(lo[2 * z]), p));
-        hi[2 * z + 1] = as_u32(__hmax2_nan(as_half2(hi[2 * z + 1]), q));
-        lo[2 * z + 1] = as_u32(__hmin2_nan(as_half2(lo[2 * z + 1]), q));
-      }
+      widen(v.x, hi, lo);
+      widen(v.y, hi + 2, lo + 2);
+      widen(v.z, hi + 4, lo + 4);
+      widen(v.w, hi + 6, lo + 6);
     }
+    auto bf = [](uint32_t x) { return *reinterpret_cast<const __nv_bfloat162*>(&x); };
+    auto word = [](__nv_bfloat162 x) { return *reinterpret_cast<const uint32_t*>(&x); };
 #pragma unroll
     for (uint32_t s = kChunks; s < 32; s <<= 1) {
 #pragma unroll
       for (int z = 0; z < 8; ++z) {
-        hi[z] = as_u32(__hmax2_nan(as_half2(hi[z]), as_half2(__shfl_xor_sync(0xFFFFFFFFu, hi[z], s))));
-        lo[z] = as_u32(__hmin2_nan(as_half2(lo[z]), as_half2(__shfl_xor_sync(0xFFFFFFFFu, lo[z], s))));
+        hi[z] = word(__hmax2_nan(bf(hi[z]), bf(__shfl_xor_sync(0xFFFFFFFFu, hi[z], s))));
+        lo[z] = word(__hmin2_nan(bf(lo[z]), bf(__shfl_xor_sync(0xFFFFFFFFu, lo[z], s))));
       }
     }
     if (row == 0) {
-      uint8_t* to = a.bounds + (static_cast<size_t>(block) * H + h) * 2 * kD + chunk * 16;
-      st16(to, make_uint4(e4m3_of(hi[0], hi[1]), e4m3_of(hi[2], hi[3]), e4m3_of(hi[4], hi[5]), e4m3_of(hi[6], hi[7])));
-      st16(to + kD, make_uint4(e4m3_of(lo[0], lo[1]), e4m3_of(lo[2], lo[3]), e4m3_of(lo[4], lo[5]), e4m3_of(lo[6], lo[7])));
+      uint32_t h4[4], l4[4];
+#pragma unroll
+      for (int z = 0; z < 4; ++z) codes_of(hi + 2 * z, lo + 2 * z, h4 + z, l4 + z);
+      st16(to, make_uint4(h4[0], h4[1], h4[2], h4[3]));
+      st16(to + kD, make_uint4(l4[0], l4[1], l4[2], l4[3]));
     }
   }
 }
@@ -606,9 +633,6 @@ __global__ __launch_bounds__(kScoreThreads, 2) void q8_score_kernel(const ScoreA
 template <int kD>
 int launch_scores(ScoreArgs a, cudaStream_t s) {
   using C = ScoreCfg<kD>;
-  if constexpr (kD <= 128) {
-    if (a.group <= 64 && static_cast<uint64_t>(a.r.num_q) * a.span > 64ull * a.r.batch) return launch_q8_score_tc(a, s);
-  }
   if (static_cast<uint64_t>(a.r.num_q) * a.span <= 8ull * a.r.batch) {
     static std::atomic<uint64_t> few_done;
     auto* few = q8_score_few_kernel<kD>;
@@ -619,6 +643,12 @@ int launch_scores(ScoreArgs a, cudaStream_t s) {
   }
   static std::atomic<uint64_t> done;
   auto* kernel = q8_score_kernel<kD>;
+  // The tensor-core kernel takes 128 query rows at nearly the cost of sixteen (32 requests of up to 512 blocks, 8 kv heads of 128
+  // channels, us here / there: 31.5 / 27.6 at 12 rows a request, 47 / 27.7 at 32, 85 / 28.8 at 64; one request of 1024 blocks 7.9 / 8.8
+  // at 16 and 14.7 / 9.0 at 64; 64 channels 26.8 / 22.2 at 16).
+  if constexpr (kD <= 128) {
+    if (a.group <= 64) return launch_q8_score_tc(a, s);
+  }
   // 64 query rows let two CTAs share an SM; up to 128 where a query has more
   a.rows = a.span <= 64 ? 64 / a.span * a.span : std::min<uint32_t>(128, a.span);
   if (C::smem(a.rows, a.r.batch) > C::kMost) a.rows = 64;  // 512 channels, and a batch near the largest
