@@ -39,7 +39,7 @@ __device__ __forceinline__ uint32_t score_key(float w) {
 // time: of the keys' common prefix and a one, how many are not under it?  One vote-free sum over the warp (redux) a bit, and an
 // end as soon as the count is right.
 template <int kKeys>
-__global__ __launch_bounds__(kSelThreads) void q8_select_warp_kernel(const SelectArgs a) {
+__global__ __launch_bounds__(kSelThreads, kKeys == 32 ? 3 : kKeys == 16 ? 5 : 6) void q8_select_warp_kernel(const SelectArgs a) {
   __shared__ uint32_t s_q[CKV_MAX_BATCH];
   __shared__ BlockReq s_req[CKV_MAX_BATCH];
   __shared__ unsigned long long s_scan64[kSelThreads / 32 + 1];
@@ -331,7 +331,8 @@ int ckv_q8_block_select(const float* scores, uint32_t n_kv_heads, uint32_t width
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (width <= 1024) {
     const uint64_t ctas = (rows + kSelThreads / 32 - 1) / (kSelThreads / 32);
-    const dim3 grid(static_cast<uint32_t>(std::min<uint64_t>(ctas, 4ull * sm_count())));
+    const uint32_t per_sm = width <= 256 ? 6 : width <= 512 ? 5 : 3;  // that fit it
+    const dim3 grid(static_cast<uint32_t>(std::min<uint64_t>(ctas, static_cast<uint64_t>(per_sm) * sm_count())));
     auto* kernel = width <= 128 ? q8_select_warp_kernel<4> : width <= 256 ? q8_select_warp_kernel<8>
                    : width <= 512 ? q8_select_warp_kernel<16> : q8_select_warp_kernel<32>;
     return launch_pdl(kernel, grid, dim3(kSelThreads), 0, s, a);
