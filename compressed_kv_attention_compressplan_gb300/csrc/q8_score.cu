@@ -376,7 +376,7 @@ __global__ __launch_bounds__(kScoreThreads, 2) void q8_score_few_kernel(const Sc
         float x1 = f[1] != 0.0f ? (s[0][2 * r + 1] + s[1][2 * r + 1]) * f[1] * k : -INFINITY;
         const uint32_t j = at.tile * kTileBlocks + g + 8 * r;
         auto put = [&](float* to_row, uint32_t limit, float v) {
-          if (limit != 0xFFFFFFFFu && j < a.width) to_row[j] = j < limit && k > 0.0f ? v : -INFINITY;
+          if (limit != 0xFFFFFFFFu && j < a.width) to_row[j] = j < limit && ks[r] > 0.0f ? v : -INFINITY;
         };
         if (a.span > 1) {
           x0 = max_nan(x0, x1);
@@ -633,7 +633,8 @@ __global__ __launch_bounds__(kScoreThreads, 2) void q8_score_kernel(const ScoreA
 template <int kD>
 int launch_scores(ScoreArgs a, cudaStream_t s) {
   using C = ScoreCfg<kD>;
-  if (static_cast<uint64_t>(a.r.num_q) * a.span <= 8ull * a.r.batch) {
+  // up to eight heads to a kv head, so that a segment's rows are whole queries: a batch may have fewer queries than requests
+  if (a.span <= 8 && static_cast<uint64_t>(a.r.num_q) * a.span <= 8ull * a.r.batch) {
     static std::atomic<uint64_t> few_done;
     auto* few = q8_score_few_kernel<kD>;
     const int rc = allow_smem(reinterpret_cast<const void*>(few), FewCfg<kD>::smem(CKV_MAX_BATCH), few_done);

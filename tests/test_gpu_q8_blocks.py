@@ -45,6 +45,11 @@ ROPE = [  # lens before, new, H, D, T, latent, dtype, norm, halves, rope_dim, be
     ([1, 30], [130, 3], 1, 512, 128, False, BF, False, True, 512, 0, 0),
     ([0, 2], [70, 61], 2, 64, 64, True, F32, False, False, 64, 0, 3),
     ([5], [40], 4, 256, 16, False, BF, False, True, 256, 0, 0),
+    ([0, 3], [128, 200], 2, 512, 128, False, F32, False, False, 64, 448, 0),   # blocks whose rows do not fit the registers
+    ([60, 3], [70, 1], 2, 512, 64, False, F32, False, True, 128, 384, 1),
+    ([9], [250], 3, 256, 128, False, F32, False, False, 256, 0, 0),
+    ([9], [250], 3, 256, 64, True, F32, False, False, 32, 0, 0),
+    ([3] * 1024, [2] * 1024, 1, 64, 16, True, BF, False, False, 32, 32, 0),
 ]
 
 
@@ -299,6 +304,14 @@ SCORES = [  # lens, q_lens, heads, H, D, T, ratio
     ([160], [2], 136, 1, 256, 32, 1),
     ([50] * 300, [1] * 300, 2, 2, 64, 16, 1),
     ([700, 90], [3, 9], 24, 1, 512, 64, 1),
+    ([90, 200], [1, 0], 16, 1, 128, 16, 1),    # fewer queries than requests
+    ([90, 200, 30, 30, 30, 30], [0, 1, 0, 0, 0, 2], 12, 1, 512, 16, 1),
+    ([40] * 12, [0] * 11 + [1], 72, 1, 256, 16, 1),
+    ([90, 0, 30, 700, 30, 30], [0, 1, 0, 5, 0, 0], 6, 2, 64, 16, 4),
+    ([17] * 1024, [1] * 1024, 8, 1, 128, 16, 1),   # the largest batch: each kernel's tables of requests
+    ([17] * 1024, [2] * 1024, 66, 1, 512, 16, 1),
+    ([17] * 1024, [1, 3] * 512, 16, 1, 64, 16, 1),
+    ([17] * 1024, [1] * 1024, 2, 1, 512, 16, 1),
 ]
 
 
@@ -407,6 +420,7 @@ SELECT = [  # lens, q_lens, H, T, ratio, budget, sinks, recent
     ([1024, 1040, 1008], [1, 1, 1], 2, 16, 1, 1, 0, 0),
     ([4096, 4112], [2, 1], 2, 16, 1, 128, 1, 0),
     ([16384, 16400], [1, 1], 1, 16, 1, 1000, 0, 8),
+    ([64] * 1024, [3, 0] * 512, 2, 16, 1, 2, 0, 1),
 ]
 
 
@@ -529,6 +543,9 @@ ATTN = [  # lens, q_lens, heads, H, D, T, latent, ratio, budget
     ([700, 90], [2, 1], 256, 1, 128, 64, True, 4, 5),
     ([400] * 150, [1] * 150, 4, 2, 64, 16, False, 1, 9),
     ([90, 1200], [90, 1100], 2, 2, 64, 16, False, 1, 4),  # more queries than a plan has requests
+    ([20] * 1024, [1] * 1024, 8, 2, 128, 16, False, 1, 2),   # the largest batch
+    ([20] * 1024, [2, 0] * 512, 64, 1, 512, 16, True, 1, 2),
+    ([200] * 40, [0] * 39 + [1], 8, 2, 128, 16, False, 1, 3),
 ]
 
 
