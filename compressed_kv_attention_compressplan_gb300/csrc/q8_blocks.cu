@@ -37,7 +37,9 @@ __device__ __forceinline__ uint32_t score_key(float w) {
 
 // Rows of up to 32 kKeys blocks: a warp takes a row, its keys in registers, block j in lane j % 32.  The border is found a bit at a
 // time: of the keys' common prefix and a one, how many are not under it?  One vote-free sum over the warp (redux) a bit, and an
-// end as soon as the count is right.
+// end as soon as the count is right.  Comparisons bound it (81 % of the issue slots): 25 MB of scores, rows of up to 512 blocks, in 36 us;
+// 512 rows of up to 1024 in 10.9, a launch and a row's chain; the rows of the first with up to 1024 blocks 100.  Bits that all keys share looked for
+// first: 39 us; the keys near the border gathered, 36, but 13 and 193 for the others.
 template <int kKeys>
 __global__ __launch_bounds__(kSelThreads, kKeys == 32 ? 3 : kKeys == 16 ? 5 : 6) void q8_select_warp_kernel(const SelectArgs a) {
   __shared__ uint32_t s_q[CKV_MAX_BATCH];
@@ -103,7 +105,7 @@ __global__ __launch_bounds__(kSelThreads, kKeys == 32 ? 3 : kKeys == 16 ? 5 : 6)
   }
 }
 
-// A CTA takes a row.
+// Longer rows: a CTA takes a row, and reads it five times, from L2 after the first.  Each of them ends in a barrier and a scan, which bound it.
 __global__ __launch_bounds__(kSelThreads) void q8_select_kernel(const SelectArgs a) {
   constexpr uint32_t kBins = 256;
   __shared__ uint32_t s_q[CKV_MAX_BATCH];
@@ -191,7 +193,7 @@ struct ListArgs {
   uint32_t* lens;    // [num_q, heads]: entries in them; kInvalidU32: no request's query
 };
 
-// A warp takes lists first, first + step, ...
+// A warp takes lists first, first + step, ..., 32 numbers at a time; three dependent reads and a scan over the lanes, 5 us a launch.
 __device__ __forceinline__ void make_lists(const ListArgs& a, const uint32_t* s_q, const BlockReq* s_req, uint64_t first,
                                            uint64_t step) {
   const uint32_t lane = threadIdx.x & 31, T = a.block_tokens;

@@ -8,6 +8,11 @@
 // two runs of eight channels half the rotated width apart, so that no value crosses
 // threads in either style.  Products are rounded by themselves (no fused multiply-add), so a rotated value
 // does not depend on how a compiler would contract it.
+//
+// Bound.  The rows' bytes, and a thread's work for sixteen channels: 276 MB of bf16 rows and codes (16 requests of up to 4096 new rows, eight kv
+// heads of 128 channels, K and V) take 66 us, 4.2 TB/s or 62 % of the copy rate, with half of the issue slots taken and the registers
+// (128) leaving 16 warps to an SM.  A first pass for the scale and a second for the codes took 93 us; one unit to a CTA, 90; rows
+// ahead by asynchronous copies, 73; one vector a thread instead of two, 82; four, 74.
 #include <algorithm>
 
 #include "async_copy.cuh"
@@ -414,7 +419,8 @@ __global__ __launch_bounds__(512, 1) void q8_rope_store_hold_kernel(const RopeSt
   }
 }
 
-// Units whose rows do not fit the registers (128 entries of 512 channels in fp32): a row is read again for its codes.
+// Units whose rows do not fit the registers (128 entries of 512 channels): a row is read again for its codes, which comes from L2.
+// 42 to 53 us for the latent rows of which blocks of 64 entries take 40.
 constexpr int kWideThreads = 512;
 
 template <typename TIn, int kD>
