@@ -37,9 +37,9 @@ __device__ __forceinline__ uint32_t score_key(float w) {
 
 // Rows of up to 32 kKeys blocks: a warp takes a row, its keys in registers, block j in lane j % 32.  The border is found a bit at a
 // time: of the keys' common prefix and a one, how many are not under it?  One vote-free sum over the warp (redux) a bit, and an
-// end as soon as the count is right.  Comparisons bound it (81 % of the issue slots): 25 MB of scores, rows of up to 512 blocks, in 36 us;
-// 512 rows of up to 1024 in 10.9, a launch and a row's chain; the rows of the first with up to 1024 blocks 100.  Bits that all keys share looked for
-// first: 39 us; the keys near the border gathered, 36, but 13 and 193 for the others.
+// end as soon as the count is right.  Instructions bound it (four of five issue slots): 25 MB of scores, rows of up to 512 blocks, in 32 us;
+// 512 rows of up to 1024 in 10.1, a launch and a row's chain; the rows of the first with up to 1024 blocks 81.  With 32-bit comparisons for every bit
+// 36, 10.9 and 100; and then with the bits that all keys share looked for first 39, or the keys near the border gathered 36, 13 and 193.
 template <int kKeys>
 __global__ __launch_bounds__(kSelThreads, kKeys == 32 ? 3 : kKeys == 16 ? 5 : 6) void q8_select_warp_kernel(const SelectArgs a) {
   __shared__ uint32_t s_q[CKV_MAX_BATCH];
@@ -67,34 +67,61 @@ __global__ __launch_bounds__(kSelThreads, kKeys == 32 ? 3 : kKeys == 16 ? 5 : 6)
 #pragma unroll
     for (int x = 0; x < kKeys; ++x) {
       const uint32_t j = x * 32 + lane;
-      key[x] = j < n ? __float_as_uint(__ldg(scores + j)) : 0;
+      key[x] = j < n ? __float_as_uint(__ldg(scores + j)) : 0x7FFFFFFFu;
     }
-    // the first and the last ones count as the largest there are, what is not there as nothing
+    // the first and the last ones count as the largest there are, what is not there as nothing, as NaN does
 #pragma unroll
     for (int x = 0; x < kKeys; ++x) {
       const uint32_t j = x * 32 + lane;
-      key[x] = j < a.sinks || (j >= hi && j < n) ? 0xFFFFFFFFu : j < n ? score_key(__uint_as_float(key[x])) : 0;
+      key[x] = j < a.sinks || (j >= hi && j < n) ? 0xFFFFFFFFu : score_key(__uint_as_float(key[x]));
     }
-    // the largest border that `budget` keys are not under
-    uint32_t border = 0;
-    for (uint32_t bit = 0x80000000u; bit != 0; bit >>= 1) {
+    // the largest border that `budget` keys are not under: its upper 15 bits from two keys a register, min(key - c + 1, 1) or 0 for each
+    uint32_t pairs[kKeys / 2];
+#pragma unroll
+    for (int x = 0; x < kKeys / 2; ++x) pairs[x] = __byte_perm(key[2 * x] >> 1, key[2 * x + 1] >> 1, 0x7632);
+    uint32_t border = 0, count = 0;
+    for (uint32_t bit = 0x4000u; bit != 0 && count != a.budget; bit >>= 1) {
+      const uint32_t c = border | bit, add = ((1 - c) & 0xFFFFu) * 0x10001u;
+      uint32_t sum = 0;
+#pragma unroll
+      for (int x = 0; x < kKeys / 4; ++x) sum += __viaddmin_s16x2_relu(pairs[x], add, 0x10001u);
+      if (n > kKeys * 16) {  // the other half of the keys
+#pragma unroll
+        for (int x = kKeys / 4; x < kKeys / 2; ++x) sum += __viaddmin_s16x2_relu(pairs[x], add, 0x10001u);
+      }
+      sum = __reduce_add_sync(0xFFFFFFFFu, sum);
+      count = (sum & 0xFFFFu) + (sum >> 16);
+      if (count >= a.budget) border = c;
+    }
+    border <<= 17;
+    for (uint32_t bit = 0x10000u; bit != 0 && count != a.budget; bit >>= 1) {
       const uint32_t c = border | bit;
-      uint32_t count = 0;
+      count = 0;
 #pragma unroll
       for (int x = 0; x < kKeys; ++x) count += key[x] >= c;
       count = __reduce_add_sync(0xFFFFFFFFu, count);
       if (count >= a.budget) border = c;
-      if (count == a.budget) break;
+    }
+    const uint32_t below = (1u << lane) - 1;
+    uint32_t taken = 0;
+    if (count == a.budget) {
+#pragma unroll
+      for (int x = 0; x < kKeys; ++x) {
+        const bool take = key[x] >= border;
+        const uint32_t votes = __ballot_sync(0xFFFFFFFFu, take);
+        if (take) out[taken + __popc(votes & below)] = static_cast<int32_t>(x * 32 + lane);
+        taken += __popc(votes);
+      }
+      continue;
     }
     // those above the border, and the first of those at it
     uint32_t above = 0;
 #pragma unroll
     for (int x = 0; x < kKeys; ++x) above += key[x] > border;
-    uint32_t left = a.budget - __reduce_add_sync(0xFFFFFFFFu, above), taken = 0;
+    uint32_t left = a.budget - __reduce_add_sync(0xFFFFFFFFu, above);
 #pragma unroll
     for (int x = 0; x < kKeys; ++x) {
       const uint32_t j = x * 32 + lane;
-      const uint32_t below = (1u << lane) - 1;
       const uint32_t ties = __ballot_sync(0xFFFFFFFFu, key[x] == border && j < n);
       const bool take = key[x] > border || (key[x] == border && j < n && __popc(ties & below) < left);
       const uint32_t votes = __ballot_sync(0xFFFFFFFFu, take);
