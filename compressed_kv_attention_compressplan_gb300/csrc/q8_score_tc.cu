@@ -4,7 +4,8 @@
 // With blocks as the product's rows a thread of the epilogue owns a block: the maximum over a query's heads is one over its own
 // registers, and a warp's scores of a query are 128 consecutive bytes.
 //
-// A unit is 128 blocks of a (request, kv head) and some row tiles of it.  Roles: sixteen warps make the
+// A segment is 128 blocks of a (request, kv head) and all row tiles of the request; segments are laid end to end, and every CTA takes as many of
+// their tiles, so that it loads bounds as seldom as possible.  A unit is a CTA's part of a segment.  Roles: sixteen warps make the
 // operands (fp16, exact from e4m3; query rows scaled by a power of two), the next tile's loads on their way while one
 // is stored; one thread issues the products; eight warps finish the scores.  Rows of heads that do not exist repeat the
 // group's last head, so that no maximum has to leave them out.
@@ -44,7 +45,9 @@ struct alignas(16) StShared {
   float ks[3][kTile];              // of three units: the blocks' scales; negative: a block that does not exist
   uint32_t first_q[CKV_MAX_BATCH];
   BlockReq req[CKV_MAX_BATCH];
-  unsigned long long unit[CKV_MAX_BATCH];
+  unsigned long long first_tile[CKV_MAX_BATCH];
+  unsigned long long begin;  // of this CTA's tiles
+  uint32_t tiles;
   uint32_t tmem;
 };
 
@@ -53,7 +56,7 @@ struct StUnit {
 };
 
 template <int kD, bool kShort>
-__global__ __launch_bounds__(StCfg<kD>::kThreads, 1) void q8_score_tc_kernel(const ScoreArgs a, uint32_t span_shift, uint32_t tiles_of_unit) {
+__global__ __launch_bounds__(StCfg<kD>::kThreads, 1) void q8_score_tc_kernel(const ScoreArgs a, uint32_t span_shift) {
   using C = StCfg<kD>;
   extern __shared__ uint8_t raw[];
   __shared__ StShared sh;
@@ -64,21 +67,25 @@ __global__ __launch_bounds__(StCfg<kD>::kThreads, 1) void q8_score_tc_kernel(con
   unsigned long long* scan = reinterpret_cast<unsigned long long*>(sh.lim);  // before the roles begin
   scan_queries<C::kThreads>(a.r, sh.first_q, sh.req, scan);
   auto row_tiles = [&](const BlockReq& r) { return ((r.q_len << span_shift) + kTile - 1) / kTile; };
-  auto groups_of = [&](const BlockReq& r) { return (row_tiles(r) + tiles_of_unit - 1) / tiles_of_unit; };
-  unsigned long long units = 0;
+  unsigned long long total = 0;  // tiles
   for (uint32_t b0 = 0; b0 < a.r.batch; b0 += C::kThreads) {
     const uint32_t b = b0 + tid;
     unsigned long long n = 0;
     if (b < a.r.batch)
-      n = static_cast<unsigned long long>(groups_of(sh.req[b])) * H * score_tiles<kTile>(sh.req[b], a.r.ratio, t_shift);
+      n = static_cast<unsigned long long>(row_tiles(sh.req[b])) * H * score_tiles<kTile>(sh.req[b], a.r.ratio, t_shift);
     unsigned long long sum;
-    const unsigned long long at = units + block_exclusive<C::kThreads>(n, &sum, scan);
-    if (b < a.r.batch) sh.unit[b] = at;
-    units += sum;
+    const unsigned long long at = total + block_exclusive<C::kThreads>(n, &sum, scan);
+    if (b < a.r.batch) sh.first_tile[b] = at;
+    total += sum;
+  }
+  const unsigned long long share = (total + gridDim.x - 1) / gridDim.x, begin = blockIdx.x * share;
+  const bool idle = begin >= total;
+  if (tid == 0) {
+    sh.begin = begin;
+    sh.tiles = idle ? 0 : static_cast<uint32_t>(min(share, total - begin));
   }
   const uint32_t base = (smem_addr(raw) + 1023) & ~1023u;
   const uint32_t a_at = base, q_at = base + C::kOperand;
-  const bool idle = blockIdx.x >= units;
   if (warp == C::kWarps - 1 && !idle) tmem_alloc(smem_addr(&sh.tmem), C::kCols);
   if (tid == 0) {
     mbar_init(smem_addr(&sh.a_full), C::kLoadWarps);
@@ -99,15 +106,15 @@ __global__ __launch_bounds__(StCfg<kD>::kThreads, 1) void q8_score_tc_kernel(con
   const uint32_t tmem = sh.tmem;
   Waiter w{static_cast<long long>(a.wait_ns) * 2, true};
 
-  auto unit_of = [&](unsigned long long u) -> StUnit {
+  auto unit_of = [&](uint32_t done) -> StUnit {
     StUnit x;
-    x.b = last_not_above(sh.unit, a.r.batch, u);
+    const unsigned long long at = sh.begin + done;
+    x.b = last_not_above(sh.first_tile, a.r.batch, at);
     const BlockReq r = sh.req[x.b];
-    const uint32_t groups = groups_of(r);
-    const unsigned long long rel = u - sh.unit[x.b], y = rel / groups;
-    const uint32_t block_tiles = score_tiles<kTile>(r, a.r.ratio, t_shift);
-    x.tile0 = static_cast<uint32_t>(rel - y * groups) * tiles_of_unit;
-    x.tiles = min(tiles_of_unit, row_tiles(r) - x.tile0);
+    const uint32_t tiles = row_tiles(r), block_tiles = score_tiles<kTile>(r, a.r.ratio, t_shift);
+    const unsigned long long rel = at - sh.first_tile[x.b], y = rel / tiles;
+    x.tile0 = static_cast<uint32_t>(rel - y * tiles);
+    x.tiles = min(sh.tiles - done, tiles - x.tile0);
     x.h = static_cast<uint32_t>(y / block_tiles);
     x.block0 = static_cast<uint32_t>(y % block_tiles) * kTile;
     return x;
@@ -119,9 +126,9 @@ __global__ __launch_bounds__(StCfg<kD>::kThreads, 1) void q8_score_tc_kernel(con
     const uint32_t chunk = lane % C::kLanes, row0 = warp * (kTile / C::kLoadWarps) + lane / C::kLanes;
     const __half2 zero = __float2half2_rn(0.0f);
     int32_t blk[C::kTimes];
-    auto ask = [&](unsigned long long u) {
-      if (u >= units) return;
-      const StUnit x = unit_of(u);
+    auto ask = [&](uint32_t done) {
+      if (done >= sh.tiles) return;
+      const StUnit x = unit_of(done);
       const BlockReq r = sh.req[x.b];
       const uint32_t blocks = (seen_by(r, r.q_len - 1, a.r.ratio) + T - 1) >> t_shift;
 #pragma unroll
@@ -140,10 +147,9 @@ __global__ __launch_bounds__(StCfg<kD>::kThreads, 1) void q8_score_tc_kernel(con
         rows[i] = ld_stream16_if(a.q + (static_cast<size_t>(sh.first_q[x.b] + n) * a.n_heads + x.h * G + head) * kD + chunk * 8, n < q_len);
       }
     };
-    unsigned long long u = blockIdx.x;
-    ask(u);
-    for (; u < units; u += gridDim.x, ++uc) {
-      const StUnit x = unit_of(u);
+    ask(0);
+    for (; qc < sh.tiles; ++uc) {
+      const StUnit x = unit_of(qc);
       const BlockReq r = sh.req[x.b];
       // A unit's bounds are not kept in registers beside its rows: what does not fit them comes back from L2, as its shared memory
       // leaves next to no L1 (74 us so, with both a unit ahead).
@@ -158,7 +164,7 @@ __global__ __launch_bounds__(StCfg<kD>::kThreads, 1) void q8_score_tc_kernel(con
         bounds[i] = ld_stream16_if(a.bounds + bh * 2 * kD + chunk * 16, ok);
         scale[i] = ok ? ld_ahead(a.c.k_scale + bh) : -1.0f;
       }
-      ask(u + gridDim.x);
+      ask(qc + x.tiles);
       w.wait<kShort>(&sh.a_free, (uc & 1) ^ 1);
 #pragma unroll
       for (int i = 0; i < C::kTimes; ++i) {
@@ -218,8 +224,8 @@ __global__ __launch_bounds__(StCfg<kD>::kThreads, 1) void q8_score_tc_kernel(con
     // ---- scores: a thread owns a block (its lane of tensor memory) and 64 of a tile's query rows
     const int group = (warp - C::kLoadWarps) >> 2, quarter = warp & 3, entry = quarter * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
-    for (unsigned long long u = blockIdx.x; u < units; u += gridDim.x, ++uc) {
-      const StUnit x = unit_of(u);
+    for (; qc < sh.tiles; ++uc) {
+      const StUnit x = unit_of(qc);
       const uint32_t j = x.block0 + entry, q0 = sh.first_q[x.b];
       float ks = 0.0f;
       for (uint32_t t = 0; t < x.tiles; ++t, ++qc) {
@@ -288,8 +294,8 @@ __global__ __launch_bounds__(StCfg<kD>::kThreads, 1) void q8_score_tc_kernel(con
       }
     }
   } else {
-    for (unsigned long long u = blockIdx.x; u < units; u += gridDim.x, ++uc) {
-      const StUnit x = unit_of(u);
+    for (; qc < sh.tiles; ++uc) {
+      const StUnit x = unit_of(qc);
       w.wait<kShort>(&sh.a_full, uc & 1);
       for (uint32_t t = 0; t < x.tiles; ++t, ++qc) {
         const uint32_t sb = qc & 1;
@@ -340,10 +346,7 @@ int launch(const ScoreArgs& a, cudaStream_t s) {
   if (rc) return rc;
   uint32_t shift = 0;
   while ((1u << shift) < a.group) ++shift;
-  // row tiles to a unit: as many as leave every SM four units, so that a tile of bounds serves several
-  const uint64_t all = static_cast<uint64_t>(a.c.heads) * ((a.width + kTile - 1) / kTile) * (((static_cast<uint64_t>(a.r.num_q) << shift) + kTile - 1) / kTile);
-  const uint32_t tiles = static_cast<uint32_t>(std::clamp<uint64_t>(all / (4ull * sm_count()), 1, 16));
-  return launch_pdl(kernel, dim3(static_cast<uint32_t>(sm_count())), dim3(C::kThreads), C::kSmem, s, a, shift, tiles);
+  return launch_pdl(kernel, dim3(static_cast<uint32_t>(sm_count())), dim3(C::kThreads), C::kSmem, s, a, shift);
 }
 
 }  // namespace
