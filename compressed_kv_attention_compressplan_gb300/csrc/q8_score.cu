@@ -162,7 +162,7 @@ __global__ __launch_bounds__(kBoundThreads, 4) void q8_bounds_kernel(const Bound
 // are read alike (sums over k may run in any order).  One query fragment serves both halves of the product: as max(q, 0)
 // against hi and as min(q, 0) against lo.  From 256 channels on a block's channels are split over the warps of a set, which
 // add their sums through shared memory.  Conversions and products bound it: a chunk of 128 channels takes 135 us where the 5th-generation
-// tensor cores take 40 (see the launch).
+// tensor cores take 37.5 (see the launch).
 constexpr int kScoreWarps = 8;
 constexpr int kScoreThreads = 32 * kScoreWarps;
 constexpr uint32_t kTileBlocks = 16;
