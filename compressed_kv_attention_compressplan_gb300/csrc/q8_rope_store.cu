@@ -10,9 +10,9 @@
 // does not depend on how a compiler would contract it.
 //
 // Bound.  The rows' bytes, and a thread's work for sixteen channels: 276 MB of bf16 rows and codes (16 requests of up to 4096 new rows, eight kv
-// heads of 128 channels, K and V) take 66 us, 4.2 TB/s or 62 % of the copy rate, with half of the issue slots taken and the registers
-// (128) leaving 16 warps to an SM.  A first pass for the scale and a second for the codes took 93 us; one unit to a CTA, 90; rows
-// ahead by asynchronous copies, 73; one vector a thread instead of two, 82; four, 74.
+// heads of 128 channels, K and V) take 55 us, 5.0 TB/s or 75 % of the copy rate, with the registers (96) leaving 20 warps to an SM.  With angles
+// in registers (128, so 16 warps) 66 us; and then a first pass for the scale and a second for the codes 93, one unit to a CTA 90, rows ahead by
+// asynchronous copies 73.
 #include <algorithm>
 
 #include "async_copy.cuh"
@@ -220,14 +220,15 @@ struct Unit {
 };
 
 // A CTA takes a record and some of its units, one after the other.  A thread keeps its places in the block, kVecs rows and
-// sixteen channels of each: positions, angles and the norm's weights are read once for all heads and stay in registers, and
-// a unit's values from the search for the scale to the codes, while the next unit's rows are on their way.
-template <typename TIn, int kD, int kVecs, int kMaxThreads, int kPerSm>
-__global__ __launch_bounds__(kMaxThreads, kPerSm) void q8_rope_store_kernel(const RopeStoreArgs a, uint32_t units_of_cta, uint32_t parts) {
+// sixteen channels of each: positions, angles and the norm's weights are read once for all heads and stay in shared memory, where nobody else
+// touches them, and a unit's values in registers from the search for the scale to the codes, while the next unit's rows are on their way.
+template <typename TIn, int kD, int kVecs, int kThreads, int kPerSm>
+__global__ __launch_bounds__(kThreads, kPerSm) void q8_rope_store_kernel(const RopeStoreArgs a, uint32_t units_of_cta, uint32_t parts) {
   constexpr uint32_t kLanes = kD / 16;      // threads of a row
   constexpr uint32_t kLoads = sizeof(TIn);  // 16-byte loads of sixteen channels
   constexpr uint32_t kElems = 16 / sizeof(TIn);
   __shared__ float s_max[2][32];
+  __shared__ float4 s_cs[kVecs][4][kThreads], s_w[4][kThreads];  // angles, weights: a thread reads back what itself has put
   pdl_wait();
   pdl_release();
   const uint32_t n = count_or_capacity(a.d_counts, 0, a.capacity), H = a.c.heads, T = a.c.block_tokens, step = blockDim.x / kLanes;
@@ -235,10 +236,12 @@ __global__ __launch_bounds__(kMaxThreads, kPerSm) void q8_rope_store_kernel(cons
   const Lane l = lane_of(a, j);
   const uint32_t u0 = blockIdx.x % parts * units_of_cta, u1 = min(H * a.sides, u0 + units_of_cta);
   uint32_t flip = 0;
-  float w[16];
   if (a.weight != nullptr && u0 < H) {
+    float w[16];
     load8(a.weight + l.c0, w);
     load8(a.weight + l.c1, w + 8);
+#pragma unroll
+    for (int z = 0; z < 4; ++z) s_w[z][threadIdx.x] = make_float4(w[4 * z], w[4 * z + 1], w[4 * z + 2], w[4 * z + 3]);
   }
   for (uint32_t i = blockIdx.x / parts; i < n; i += gridDim.x / parts) {
     const uint4 rec = __ldg(reinterpret_cast<const uint4*>(a.plan + i));
@@ -274,13 +277,17 @@ __global__ __launch_bounds__(kMaxThreads, kPerSm) void q8_rope_store_kernel(cons
     };
     load_unit(u0);
     bool bad = false;
-    float cs[kVecs][16];
 #pragma unroll
     for (int v = 0; v < kVecs; ++v) {
       const bool here = r0 + v * step < cnt, at = a.dim == 0 || (pos[v] >= 0 && pos[v] < a.max_pos);
       bad |= here && !at;
       in |= (here && at ? 1u : 0u) << v;
-      if (l.turns && here && at && u0 < H) angles(a, l, static_cast<uint32_t>(pos[v]), cs[v]);
+      if (l.turns && here && at && u0 < H) {
+        float cs[16];
+        angles(a, l, static_cast<uint32_t>(pos[v]), cs);
+#pragma unroll
+        for (int z = 0; z < 4; ++z) s_cs[v][z][threadIdx.x] = make_float4(cs[4 * z], cs[4 * z + 1], cs[4 * z + 2], cs[4 * z + 3]);
+      }
     }
     if (bad && j == 0) status_or(a.d_status, CKV_STATUS_BAD_INDEX);
     // a new entry has had no attention yet, whatever the slot's last owner had
@@ -316,8 +323,22 @@ __global__ __launch_bounds__(kMaxThreads, kPerSm) void q8_rope_store_kernel(cons
       if (u + 1 < u1) load_unit(u + 1);
 #pragma unroll
       for (int v = 0; v < kVecs; ++v) {
-        if (a.weight != nullptr) normalise<kD>(a, w, x[v]);
-        if (l.turns) rotate(a, cs[v], x[v]);
+        auto back = [&](const float4 (&from)[4][kThreads], float (&y)[16]) {
+#pragma unroll
+          for (int z = 0; z < 4; ++z) {
+            const float4 c = from[z][threadIdx.x];
+            y[4 * z] = c.x, y[4 * z + 1] = c.y, y[4 * z + 2] = c.z, y[4 * z + 3] = c.w;
+          }
+        };
+        float y[16];
+        if (a.weight != nullptr) {
+          back(s_w, y);
+          normalise<kD>(a, y, x[v]);
+        }
+        if (l.turns) {
+          back(s_cs[v], y);
+          rotate(a, y, x[v]);
+        }
         if (in >> v & 1) m = largest(m, x[v]);
       }
       finish(x, m, old, a.c.k + (block0 + u) * T * kD, a.c.k_scale + block0 + u);
@@ -502,9 +523,14 @@ int launch(const RopeStoreArgs& a, cudaStream_t s) {
   const uint32_t per = (units + parts - 1) / parts;
   parts = (units + per - 1) / per;
   const dim3 grid(records * parts);
-  if (vecs <= 128) return launch_pdl(q8_rope_store_kernel<TIn, kD, 2, 64, 8>, grid, dim3(vecs / 2), 0, s, a, per, parts);
-  if (vecs <= 256) return launch_pdl(q8_rope_store_kernel<TIn, kD, 2, 128, 4>, grid, dim3(vecs / 2), 0, s, a, per, parts);
-  if (vecs <= 512) return launch_pdl(q8_rope_store_kernel<TIn, kD, 2, 256, 2>, grid, dim3(vecs / 2), 0, s, a, per, parts);
+  // Threads that a barrier joins, against registers: 16 requests of up to 4096 new rows, eight kv heads, K and V, us (whole call): blocks of 32
+  // entries of 128 channels 60 with two vectors a thread and five CTAs of 128 an SM, 61 with four vectors and 64 threads, 68 with one and 256; 64
+  // entries 77 with four vectors and three CTAs of 128, 85 to 89 with two vectors and two or three CTAs of 256, 101 with one and 512; 16 entries
+  // of 64 channels 27.6 with 16 CTAs of 32 an SM and 31 with 20.  In fp32 five CTAs spill: 32 entries 81 with four and 90 with five.
+  if (vecs <= 64) return launch_pdl(q8_rope_store_kernel<TIn, kD, 2, 32, 16>, grid, dim3(32), 0, s, a, per, parts);
+  if (vecs <= 128) return launch_pdl(q8_rope_store_kernel<TIn, kD, 2, 64, 8>, grid, dim3(64), 0, s, a, per, parts);
+  if (vecs <= 256) return launch_pdl(q8_rope_store_kernel<TIn, kD, 2, 128, sizeof(TIn) == 2 ? 5 : 4>, grid, dim3(128), 0, s, a, per, parts);
+  if (vecs <= 512) return launch_pdl(q8_rope_store_kernel<TIn, kD, 4, 128, 3>, grid, dim3(128), 0, s, a, per, parts);
   if (vecs <= 2048) return launch_pdl(q8_rope_store_hold_kernel<TIn, kD>, dim3(records, units), dim3(vecs / 4), 0, s, a);
   if constexpr (kD == 512) return launch_pdl(q8_rope_store_wide_kernel<TIn, kD>, dim3(records, units), dim3(kWideThreads), 0, s, a);
   return CKV_ERR_SIZE;  // not reached

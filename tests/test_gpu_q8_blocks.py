@@ -50,6 +50,10 @@ ROPE = [  # lens before, new, H, D, T, latent, dtype, norm, halves, rope_dim, be
     ([9], [250], 3, 256, 128, False, F32, False, False, 256, 0, 0),
     ([9], [250], 3, 256, 64, True, F32, False, False, 32, 0, 0),
     ([3] * 1024, [2] * 1024, 1, 64, 16, True, BF, False, False, 32, 32, 0),
+    ([0, 63, 10], [200, 3, 60], 3, 128, 64, False, BF, False, True, 128, 0, 3),   # four vectors a thread
+    ([5, 16], [43, 1], 2, 512, 16, True, BF, False, False, 64, 448, 0),
+    ([5, 16], [43, 1], 2, 128, 16, False, F32, False, True, 64, 32, 1),
+    ([5, 16], [43, 1], 2, 64, 16, False, F32, False, False, 64, 0, 0),
 ]
 
 
