@@ -37,7 +37,7 @@ __device__ __forceinline__ uint32_t score_key(float w) {
 
 // Rows of up to 32 kKeys blocks: a warp takes a row, its keys in registers, block j in lane j % 32.  The border is found a bit at a
 // time: of the keys' common prefix and a one, how many are not under it?  One vote-free sum over the warp (redux) a bit, and an
-// end as soon as the count is right.  Instructions bound it (four of five issue slots): 25 MB of scores, rows of up to 512 blocks, in 32 us;
+// end as soon as the count is right.  Instructions (two thirds of the issue slots) and that chain bound it: 25 MB of scores, rows of up to 512 blocks, in 32 us;
 // 512 rows of up to 1024 in 10.1, a launch and a row's chain; the rows of the first with up to 1024 blocks 81.  With 32-bit comparisons for every bit
 // 36, 10.9 and 100; and then with the bits that all keys share looked for first 39, or the keys near the border gathered 36, 13 and 193.
 template <int kKeys>
