@@ -141,14 +141,10 @@ __global__ __launch_bounds__(StCfg<kD>::kThreads, 1) void q8_score_tc_kernel(con
       }
     };
     uint4 rows[C::kTimes];
-    auto load_rows = [&](const StUnit& x, uint32_t t) {
-      const uint32_t q_len = sh.req[x.b].q_len;
-#pragma unroll
-      for (int i = 0; i < C::kTimes; ++i) {
-        const uint32_t rho = (x.tile0 + t) * kTile + row0 + i * C::kRows, n = rho >> span_shift;
-        const uint32_t head = min(rho & ((1u << span_shift) - 1), G - 1);
-        rows[i] = ld_stream16_if(a.q + (static_cast<size_t>(sh.first_q[x.b] + n) * a.n_heads + x.h * G + head) * kD + chunk * 8, n < q_len);
-      }
+    auto load_row = [&](const StUnit& x, uint32_t t, int i) {
+      const uint32_t rho = (x.tile0 + t) * kTile + row0 + i * C::kRows, n = rho >> span_shift;
+      const uint32_t head = min(rho & ((1u << span_shift) - 1), G - 1);
+      rows[i] = ld_stream16_if(a.q + (static_cast<size_t>(sh.first_q[x.b] + n) * a.n_heads + x.h * G + head) * kD + chunk * 8, n < sh.req[x.b].q_len);
     };
     ask(0);
     for (; qc < sh.tiles; ++uc) {
@@ -181,7 +177,8 @@ __global__ __launch_bounds__(StCfg<kD>::kThreads, 1) void q8_score_tc_kernel(con
                        : "memory");
         if (chunk == 0) sh.ks[uc % 3][n] = scale[i];
       }
-      load_rows(x, 0);
+#pragma unroll
+      for (int i = 0; i < C::kTimes; ++i) load_row(x, 0, i);
       fence_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_addr(&sh.a_full));
@@ -205,6 +202,7 @@ __global__ __launch_bounds__(StCfg<kD>::kThreads, 1) void q8_score_tc_kernel(con
             hi[z] = as_u32(__hmax2_nan(v, zero));
             lo[z] = as_u32(__hmin2_nan(v, zero));
           }
+          if (t + 1 < x.tiles) load_row(x, t + 1, i);  // its place is free
           const uint32_t to = q_at + qs * C::kOperand + (chunk >> 3) * kSlice + n * 128 + (((chunk & 7) ^ (n & 7)) << 4);
           asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(to), "r"(hi[0]), "r"(hi[1]), "r"(hi[2]), "r"(hi[3]) : "memory");
           asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(to + (kD / 64) * kSlice), "r"(lo[0]), "r"(lo[1]), "r"(lo[2]), "r"(lo[3]) : "memory");
@@ -220,7 +218,6 @@ __global__ __launch_bounds__(StCfg<kD>::kThreads, 1) void q8_score_tc_kernel(con
           mbar_arrive(smem_addr(&sh.q_full[qs]));
           mbar_arrive(smem_addr(&sh.rows_full[qc & 3]));
         }
-        if (t + 1 < x.tiles) load_rows(x, t + 1);
       }
     }
   } else if (warp < C::kLoadWarps + C::kOutWarps) {
