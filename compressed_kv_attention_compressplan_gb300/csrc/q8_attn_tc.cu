@@ -175,7 +175,7 @@ __global__ __launch_bounds__((TcCfg<kD, kShared>::kThreads), 1) void q8_attn_tc_
   uint32_t items_before = 0;
 
   for (uint32_t it = item0; it < item1; ++it) {
-    const Q8Item item = item_for<kLists>(items + it, a, h);
+    const Q8Item item = item_for<kLists, true>(items + it, a, h);
     if (!item_fits(item, a)) {
       if (tid == 0) status_or(a.d_status, CKV_STATUS_BAD_INDEX);
       continue;

@@ -108,9 +108,23 @@ __device__ __forceinline__ bool plan_fits(const Q8Header* h, const AttnArgs& a) 
 
 // An item, and its block table, for kv head h.  Where the heads have tables of their own (kLists), the item, which was planned
 // for the longest, is cut down to the head's entries.  A template: the same test at run time cost a prefill chunk 1.8 %.
-template <bool kLists>
+// kWords: read by words, where registers in fours would spill (the 8-bit kernel).
+template <bool kLists, bool kWords = false>
 __device__ __forceinline__ Q8Item item_for(const Q8Item* at, const AttnArgs& a, uint32_t h) {
-  Q8Item r = *at;
+  Q8Item r;
+  if constexpr (kWords) {
+    const uint32_t* from = reinterpret_cast<const uint32_t*>(at);
+    uint32_t* to = reinterpret_cast<uint32_t*>(&r);
+#pragma unroll
+    for (int w = 0; w < static_cast<int>(sizeof(Q8Item) / 4); ++w) to[w] = from[w];
+  } else {
+    r = *at;
+  }
+  if (kLists) {  // as they were planned
+    r.q_start = r.rid;
+    r.q_len = 1;
+    r.phase = 0;
+  }
   if (kLists && r.rid < a.num_reqs) {
     r.kv_len = min(r.kv_len, a.lens[static_cast<size_t>(r.rid) * a.c.heads + h]);
     r.kv_end = min(r.kv_end, r.kv_len);
