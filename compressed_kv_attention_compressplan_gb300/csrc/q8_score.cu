@@ -323,7 +323,7 @@ __global__ __launch_bounds__(kScoreThreads, 2) void q8_score_few_kernel(const Sc
         m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
         m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
         const int ex = min(126, 14 - (static_cast<int>(__float_as_uint(m) >> 23) - 127));
-        const float up = pow2f(ex), back = in ? pow2f(-ex) : 0.0f;
+        const float up = pow2f(ex), back = in ? row_factor(a, ex) : 0.0f;
 #pragma unroll
         for (int c = 0; c < kD / 64; ++c) {  // loaded again: 128 registers would hold a row's 512 channels
           const uint4 x[2] = {ld_stream16_if(src + c * 64, in), ld_stream16_if(src + c * 64 + 8, in)};
@@ -524,7 +524,7 @@ __global__ __launch_bounds__(kScoreThreads, 2) void q8_score_kernel(const ScoreA
         for (int z = 0; z < kPer; z += 2)
           *reinterpret_cast<uint32_t*>(s_rows + r * C::kRowBytes + (lane * kPer + z) * 2) = pack_f16x2(v[z] * up, v[z + 1] * up);
         if (lane == 0) {
-          s_rf[r] = in ? pow2f(-ex) : 0.0f;
+          s_rf[r] = in ? row_factor(a, ex) : 0.0f;
           s_lim[r] = i < i1 ? blocks_of(i) : 0xFFFFFFFFu;
         }
       }
@@ -730,7 +730,7 @@ int ckv_q8_block_scores(const ckv_q8_cache_t* cache, const void* bounds, uint32_
   a.span = 1;
   while (a.span < a.group && a.span < 8) a.span *= 2;
   if (a.group > 8) a.span = (a.group + 7) / 8 * 8;
-  a.scale = scale;
+  split_scale(scale, &a);
   a.table = block_table;
   a.stride = static_cast<uint32_t>(table_stride);
   a.width = width;

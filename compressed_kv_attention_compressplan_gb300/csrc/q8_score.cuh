@@ -1,6 +1,9 @@
 // q8_score.cuh -- what the kernels for the blocks' scores share.
 #pragma once
 
+#include <algorithm>
+#include <cmath>
+
 #include "q8_blocks.cuh"
 
 namespace ckv {
@@ -18,7 +21,7 @@ struct ScoreArgs {
   uint32_t rows;     // query rows in shared memory: whole queries, or a part of one
   uint32_t queries;  // of a segment
   uint32_t parts;    // of a query that has more rows
-  float scale;
+  float scale, row_scale;  // the score's scale, as the blocks' and the rows' factors of it
   const int32_t* table;
   uint32_t stride;
   uint32_t width;
@@ -30,6 +33,24 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   float r;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
+}
+
+// A score is s 2^-ex k_scale scale, s being the sum over a query row that was scaled by 2^ex.  These factors pass fp32's range where a
+// score need not: 2^-ex s is up to 2^18 times the row's largest value (448 by 512 channels), and k_scale may bring it back; and scale alone may take the others'
+// product out.  So a row's factor leaves 2^18 out, the block's makes up for it, and of a scale that would not let every
+// k_scale times it be a normal number the rest goes to the rows: it is above one only where every block's factor is, and under one only where
+// none is.  One product for a row and one for a block are then in range as long as the score is; a row of values under 2^-102 pays for the
+// 2^18 with a subnormal product's steps, 2^-30 of its largest value and more.
+constexpr int kHeadroom = 18;
+inline void split_scale(float scale, ScoreArgs* a) {
+  int e;
+  const float m = std::frexp(scale, &e);
+  const int kept = std::min(std::max(e, -126 - kHeadroom - kQ8ExpMin + 1), 126 - kHeadroom - kQ8ExpMax);
+  a->scale = std::ldexp(m, kept + kHeadroom);
+  a->row_scale = std::ldexp(1.0f, e - kept - kHeadroom);
+}
+__device__ __forceinline__ float row_factor(const ScoreArgs& a, int ex) {  // never 0, nor infinite
+  return fminf(fmaxf(pow2f(-ex) * a.row_scale, 0x1p-149f), 0x1p127f);
 }
 
 // Tiles of the blocks that a request's queries see.

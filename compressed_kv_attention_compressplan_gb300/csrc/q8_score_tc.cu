@@ -208,7 +208,7 @@ __global__ __launch_bounds__(StCfg<kD>::kThreads, 1) void q8_score_tc_kernel(con
           asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(to + (kD / 64) * kSlice), "r"(lo[0]), "r"(lo[1]), "r"(lo[2]), "r"(lo[3]) : "memory");
           if (chunk == 0) {
             const uint32_t q = ((x.tile0 + t) * kTile + n) >> span_shift;
-            sh.rf[qc & 3][n] = pow2f(-ex);
+            sh.rf[qc & 3][n] = row_factor(a, ex);
             sh.lim[qc & 3][n] = q < r.q_len ? (seen_by(r, q, a.r.ratio) + T - 1) >> t_shift : kInvalidU32;
           }
         }

@@ -979,3 +979,36 @@ def test_score_waits_that_run_out_are_reported_and_leave_the_context_usable():
     assert int(st[0]) & ckv.STATUS_TIMEOUT
     st.zero_()
     assert torch.equal(ckv.q8_block_scores(cache, bnd, q, 1, *args, 0.1, status=st), want) and int(st[0]) == 0
+
+
+# ------------------------------------------------------------------------------------------------ scores' range
+RANGE = [  # heads, H, D, q_lens: the kernel for few rows, the one for many channels or heads, the tensor cores'
+    (1, 1, 64, [2]), (8, 2, 128, [1]), (6, 1, 256, [1]), (4, 2, 512, [1]),
+    (12, 1, 512, [2]), (4, 1, 256, [40]), (200, 1, 256, [2]), (70, 1, 128, [5]),
+    (4, 1, 128, [40]), (24, 2, 64, [9]), (64, 1, 128, [3]),
+]
+
+
+@pytest.mark.parametrize("q_exp,k_exp,scale", [(124, -38, 0.07), (124, -38, 1e-30), (124, 36, 1e-36), (124, -38, 1e-40),
+                                               (-90, 36, 1e29), (-90, -38, 1e29), (0, 36, 1e-44), (0, -38, 0.07)])
+@pytest.mark.parametrize("case", range(len(RANGE)))
+def test_scores_whose_factors_pass_the_range_that_they_stay_in(case, q_exp, k_exp, scale):
+    heads, H, D, q_lens = RANGE[case]
+    w = World(960 + case, [100], H, D, 16, True)
+    w.ks *= np.float32(2.0) ** k_exp
+    q = w.queries(q_lens, heads)
+    q[:, ::2] *= 2.0 ** q_exp  # beside heads of ordinary size
+    assert torch.isfinite(q).all()
+    scale, bnd, st = float(np.float32(scale)), bounds_of(w), status()
+    got = ckv.q8_block_scores(w.cache(), up(bnd), q.to(DEV), 1, i64(w.rid), i64([100]), i64(q_lens), i64([100]), i32(w.table),
+                              scale, status=st).cpu().numpy().astype(np.float64)
+    want, mag, flat = bref.scores(bnd, w.ks, q.float().numpy(), w.rid, [100], q_lens, [100], w.table, 16, 1, scale, got.shape[2])
+    assert int(st[0]) == 0
+    # as check_scores, but what fp32 does not hold is an infinity: with k_exp 36 and a scale of 1e29 an ordinary head's score is
+    # some 2^9 2^29 2^96; below 2^-126 its steps are 2^-149 each, which the row's factor, 2^-18 of the score's, and the block's may add
+    most = float(np.finfo(np.float32).max)
+    tol = mag * (2 * D + 4) * 2.0 ** -23 + flat * 2.0 ** -38 + 2.0 ** -149
+    over = np.abs(want) > most + tol
+    assert np.array_equal(got[over], np.sign(want[over]) * np.inf)
+    inside = np.abs(want) < most - tol
+    assert (over | inside).all() and (np.abs(got[inside] - want[inside]) <= tol[inside]).all()
