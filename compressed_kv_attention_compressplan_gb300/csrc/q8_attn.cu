@@ -372,12 +372,14 @@ __global__ __launch_bounds__(kAttnThreads, (Cfg<kDw, kNp, kShared, kRows, kMany>
         tile_scores<kDw>(st, g, q, qf, s);
       float f[2] = {rf[0] * a.scale_log2, rf[1] * a.scale_log2};
       if (kNp == 2) {  // the two warps of a row add their halves of the channels
+        // a sum may be 448 by 512 channels times its row's largest value, which fp32 need not hold before the scales
+        constexpr float kHeadroom = 1 << 18;
         float* own = s_x[grp][i & 1][half];
         const float* other = s_x[grp][i & 1][half ^ 1];
 #pragma unroll
         for (int n = 0; n < kHalves; ++n) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s[n][e] *= rf[row_of(e)];
+          for (int e = 0; e < 4; ++e) s[n][e] *= rf[row_of(e)] * (1.0f / kHeadroom);
           *reinterpret_cast<float4*>(own + n * 128 + lane * 4) = make_float4(s[n][0], s[n][1], s[n][2], s[n][3]);
         }
         asm volatile("bar.sync %0, 64;" ::"r"(1 + grp) : "memory");
@@ -389,7 +391,7 @@ __global__ __launch_bounds__(kAttnThreads, (Cfg<kDw, kNp, kShared, kRows, kMany>
           s[n][2] += x.z;
           s[n][3] += x.w;
         }
-        f[0] = f[1] = a.scale_log2;
+        f[0] = f[1] = a.scale_log2 * kHeadroom;
       }
       f[0] *= k_scale;
       f[1] *= k_scale;

@@ -1012,3 +1012,25 @@ def test_scores_whose_factors_pass_the_range_that_they_stay_in(case, q_exp, k_ex
     assert np.array_equal(got[over], np.sign(want[over]) * np.inf)
     inside = np.abs(want) < most - tol
     assert (over | inside).all() and (np.abs(got[inside] - want[inside]) <= tol[inside]).all()
+
+
+@pytest.mark.parametrize("q_exp,k_exp", [(122, -36), (-80, 36)])
+@pytest.mark.parametrize("heads,H,D,latent", [(4, 1, 64, False), (8, 2, 128, False), (32, 1, 256, True), (8, 1, 512, True), (20, 2, 512, False),
+                                              (64, 1, 512, True), (80, 2, 256, False), (72, 1, 128, True)])
+def test_attention_whose_factors_pass_the_range_that_its_scores_stay_in(heads, H, D, latent, q_exp, k_exp):
+    """Scores of ordinary size, made of queries, entries and a scale that are not."""
+    w = World(980, [300, 40], H, D, 16, latent)
+    w.ks *= np.float32(2.0) ** k_exp
+    seq, q_lens = [300, 40], [2, 1]
+    q = w.queries(q_lens, heads) * 2.0 ** q_exp
+    assert torch.isfinite(q).all()
+    lists = lists_of(w, seq, q_lens, 1, 12, ragged=False)
+    scale = float(np.float32(D ** -0.5 * 2.0 ** (-q_exp - k_exp)))
+    out, lse, st = run_attn(w, q, lists, seq, q_lens, 1, F32, scale=scale)
+    assert st == 0
+    want, wl, mag, big, flat = bref.attn(w.k, w.ks, w.v, w.vs, q.float().numpy(), lists, w.rid, seq, q_lens, w.lens, w.table, 1, scale)
+    pool, sc = (w.k, w.ks) if latent else (w.v, w.vs)
+    vmax = 448 * np.nanmax(sc)
+    tol, ltol = attn_bounds(D, 12 * 16, want, wl, mag, big, flat, vmax, False, eight_bit(D, heads // H))
+    assert (np.abs(out.cpu().numpy() - want) <= tol).all()
+    assert (np.abs(lse.cpu().numpy() - wl) <= ltol).all()
