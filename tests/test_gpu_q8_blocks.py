@@ -1034,3 +1034,135 @@ def test_attention_whose_factors_pass_the_range_that_its_scores_stay_in(heads, H
     tol, ltol = attn_bounds(D, 12 * 16, want, wl, mag, big, flat, vmax, False, eight_bit(D, heads // H))
     assert (np.abs(out.cpu().numpy() - want) <= tol).all()
     assert (np.abs(lse.cpu().numpy() - wl) <= ltol).all()
+
+
+# ----------------------------------------------------------------------------- rotated append: every kernel's special cases
+APPEND = [  # T, D: two vectors of sixteen channels to a thread of 32, 64 and 128, four, a unit held by 256 and 512, one read twice
+    (16, 64), (16, 128), (32, 128), (64, 128), (64, 256), (64, 512), (128, 512),
+]
+
+
+@pytest.mark.parametrize("dt,latent,halves", [(BF, False, True), (F32, True, False)])
+@pytest.mark.parametrize("T,D", APPEND)
+def test_every_append_leaves_rows_of_positions_outside_the_table(T, D, dt, latent, halves):
+    w = World(1000 + T + D, [3, 0, T + 4], 2, D, T, latent, more=2 * T)
+    new = [T + 4, 2 * T, 2]
+    n, dim = sum(new), 64
+    k, v = rope_inputs(w.r, n, 2, D, dt, 1, 1 if latent else 2)
+    freqs, pos = table_of_angles(100, dim), w.r.randint(0, 100, n)
+    # single rows, the first and the last of a record, all of one
+    bad = np.r_[0, T - 4, T - 3, T + 1, T + 4:2 * T + 4, 3 * T + 3, n - 1]
+    pos[bad] = np.resize([-1, 100, 1 << 40, -(1 << 40), 1 << 32], len(bad))
+    cache, st, kv = w.cache(), status(), w.lens + new
+    weights = torch.full((w.blocks, T), 5.0, device=DEV)
+    plan, counts = ckv.plan_q8_store(cache, i64(w.rid), i64(kv), i64(new), n, i32(w.table), status=st)
+    ckv.q8_rope_store(cache, k, v, plan, i64(pos), f32(freqs), counts, rope_begin=D - dim, halves=halves, weights=weights, status=st)
+    assert int(st[0]) == ckv.STATUS_BAD_INDEX
+    recs = ref.store_plan(w.rid, kv, new, w.table, T)
+    safe = np.where(np.isin(np.arange(n), bad), 0, pos)
+    sides = [(w.k, w.ks, bref.rope(k.float().cpu().numpy(), None, 0, freqs, safe, D - dim, halves, np.float32), cache.k, cache.k_scale)]
+    if not latent:
+        sides.append((w.v, w.vs, v.float().cpu().numpy(), cache.v, cache.v_scale))
+    for pool, scale, rows, got, got_scale in sides:
+        rows = rows.copy()
+        rows[bad] = 0  # zeros do not count for a scale
+        old = pool.copy()
+        ref.store(pool, scale, rows, recs)
+        for block, row, slot, cnt in recs:
+            for i in range(cnt):
+                if row + i in bad:
+                    pool[block, :, slot + i] = old[block, :, slot + i]
+        assert ref.same_codes(codes(got), pool)
+        assert np.array_equal(got_scale.cpu().numpy(), scale, equal_nan=True)
+    want = np.full((w.blocks, T), 5.0, np.float32)
+    for block, row, slot, cnt in recs:
+        want[block, slot:slot + cnt] = np.where(np.isin(np.arange(row, row + cnt), bad), 5.0, 0.0)
+    assert np.array_equal(weights.cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("dt,latent", [(BF, True), (F32, False)])
+@pytest.mark.parametrize("T,D", APPEND)
+def test_every_append_of_infinities_and_nan(T, D, dt, latent):
+    """On fresh and on begun blocks; a block of nothing finite among them."""
+    w = World(1100 + T + D, [5, 0], 1, D, T, latent, more=2 * T)
+    new = [T, T + 3]
+    n = sum(new)
+    k, v = rope_inputs(w.r, n, 1, D, dt, 0, 1 if latent else 2)
+    for x in (k,) if latent else (k, v):
+        x[1, 0, 3], x[2, 0, D - 1], x[3, 0, 5] = np.inf, np.nan, -np.inf
+        x[4], x[7, 0, :D // 2] = 0, -np.inf
+        x[T:T + T] = np.nan
+        x[2 * T:, 0, 1::3] = np.inf  # the last block's rows
+        x[2 * T:, 0, ::3] = 0
+    freqs, pos = table_of_angles(n, 32), np.arange(n)
+    cache, kv = w.cache(), w.lens + new
+    plan, counts = ckv.plan_q8_store(cache, i64(w.rid), i64(kv), i64(new), n, i32(w.table))
+    ckv.q8_rope_store(cache, k, v, plan, i64(pos), f32(freqs), counts)
+    recs = ref.store_plan(w.rid, kv, new, w.table, T)
+    with np.errstate(invalid="ignore"):
+        ref.store(w.k, w.ks, bref.rope(k.float().cpu().numpy(), None, 0, freqs, pos, 0, False, np.float32), recs)
+    assert ref.same_codes(codes(cache.k), w.k)
+    assert np.array_equal(cache.k_scale.cpu().numpy(), w.ks, equal_nan=True)
+    if not latent:
+        ref.store(w.v, w.vs, v.float().cpu().numpy(), recs)
+        assert ref.same_codes(codes(cache.v), w.v)
+        assert np.array_equal(cache.v_scale.cpu().numpy(), w.vs, equal_nan=True)
+
+
+@pytest.mark.parametrize("dt,latent,halves,dim", [(BF, False, False, 64), (F32, True, True, 32), (BF, True, False, 0)])
+@pytest.mark.parametrize("T,D", APPEND)
+def test_every_append_with_a_norm_to_begun_blocks(T, D, dt, latent, halves, dim):
+    """As test_rope_store_with_a_norm; a begun block keeps the larger scale, and its earlier entries follow it; some rows hold an infinity,
+    which its norm makes NaN and the row's others 0, or a NaN, which makes all of it NaN."""
+    w = World(1200 + T + D, [3, T + 5, 2 * T - 1], 2, D, T, latent, spread=2, more=T + 9)
+    new = [T + 9, 4, 1]
+    n = sum(new)
+    k, v = rope_inputs(w.r, n, 2, D, dt, 2, 1 if latent else 2)
+    k[2, 0, 7], k[6, 1, D - 1], k[5, 0, 0] = np.inf, -np.inf, np.nan
+    weight = (1 + 0.2 * w.r.standard_normal(D)).astype(np.float32)
+    freqs, pos = table_of_angles(300, dim) if dim else None, w.r.randint(0, 300, n)
+    cache, st, kv = w.cache(), status(), w.lens + new
+    weights = torch.full((w.blocks, T), 5.0, device=DEV)
+    plan, counts = ckv.plan_q8_store(cache, i64(w.rid), i64(kv), i64(new), n, i32(w.table), status=st)
+    ckv.q8_rope_store(cache, k, v, plan, i64(pos) if dim else None, f32(freqs) if dim else None, counts, halves=halves,
+                      norm_weight=f32(weight), eps=1e-5, weights=weights, status=st)
+    with np.errstate(invalid="ignore"):
+        y = bref.rope(k.float().cpu().numpy(), weight, 1e-5, freqs, pos, 0, halves)
+    off = ((D + 4) / 2 + 8) * 2.0 ** -24
+    got, gs, cleared = codes(cache.k), cache.k_scale.cpu().numpy(), weights.cpu().numpy()
+    recs = ref.store_plan(w.rid, kv, new, w.table, T)
+    for block, row, slot, cnt in recs:
+        for h in range(2):
+            x, s = y[row:row + cnt, h], float(gs[block, h])
+            fin = np.abs(x[np.isfinite(x)]).max()
+            old = float(w.ks[block, h]) if slot else 0.0
+            assert s in [max(old, ref.need_scale(fin * (1 + d))) for d in (-off, off)]
+            e = ref.E4M3[got[block, h, slot:slot + cnt]] * s
+            assert np.array_equal(np.isnan(e), np.isnan(x))
+            with np.errstate(invalid="ignore"):
+                near = off * 2 * np.nanmax(np.abs(np.where(np.isnan(x), 0, x)), -1, keepdims=True)
+                assert (np.isnan(x) | (np.abs(e - x) <= np.maximum(np.abs(x) * 2.0 ** -4, s * 2.0 ** -10) + near)).all()
+            if slot:
+                assert ref.same_codes(got[block, h, :slot], ref.round8(ref.E4M3[w.k[block, h, :slot]] * (old / s)))
+        assert (cleared[block, slot:slot + cnt] == 0).all() and (cleared[block, :slot] == 5).all()
+    assert (cleared == 0).sum() == n
+    if not latent:
+        ref.store(w.v, w.vs, v.float().cpu().numpy(), recs)
+        assert ref.same_codes(codes(cache.v), w.v)
+    assert int(st[0]) == 0
+
+
+# --------------------------------------------------------------------------------- missing blocks, within the derived bounds
+@pytest.mark.parametrize("heads,H,D,latent", [(4, 1, 128, False), (8, 2, 128, False), (64, 1, 512, True), (8, 1, 512, False),
+                                              (80, 2, 256, False), (72, 1, 64, False)])
+def test_missing_blocks_in_every_part_of_a_list(heads, H, D, latent):
+    """Lists long enough to be split; blocks missing at the beginning, in later parts and at the end, and all of a list's."""
+    w = World(1300, [1500, 60, 700], H, D, 16, latent)
+    q, seq, q_lens = w.queries([1, 2, 1], heads), [1500, 60, 700], [1, 2, 1]
+    lists = lists_of(w, seq, q_lens, 1, 90, ragged=False)
+    first, last = w.rid[0], w.rid[2]
+    w.table[first, [0, 17, 40, 41, 66, 93]] = [-3, w.blocks, -1, 0x7FFFFFFF, -0x80000000, w.blocks + 7]
+    w.table[last, :44] = -3
+    skip = {-3, -1, w.blocks, 0x7FFFFFFF, -0x80000000, w.blocks + 7}
+    assert any(w.table[first, j] in skip for j in lists[0].ravel())
+    check_attn(w, q, lists, seq, q_lens, 1, F32, skip=skip, flags=ckv.STATUS_BAD_INDEX)
