@@ -132,7 +132,7 @@ struct Cfg {
   static constexpr int kStageBytes = kTileBytes;
   // As many stages as let kPerSm CTAs share an SM's 227 KB.  Eight rows and 128 channels, 64 requests of 8000 entries (1.05 GB): 162 us with two
   // CTAs of six stages, 186 with three of four; before that by a few instructions a tile more 174, 182, 188 with four of three and 280
-  // with one of twelve.  kMany (entries come from L2, and short items follow one another): two queries' chunks of lists of 24 blocks of 64
+  // with one of twelve.  kMany (short items follow one another): two requests' chunks of lists of 24 blocks of 64
   // 234, 190 and 181 us with two, three and four CTAs.
   static constexpr int kPerSm = kDw == 64 ? 4 : kDw == 128 ? (kRows == 8 ? (kMany ? 4 : 2) : 3) : 2;
   static constexpr int kStages = kDw == 64                            ? (kShared ? 8 : 6)

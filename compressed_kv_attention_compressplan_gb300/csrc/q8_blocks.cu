@@ -132,7 +132,9 @@ __global__ __launch_bounds__(kSelThreads, kKeys == 32 ? 3 : kKeys == 16 ? 5 : 6)
   }
 }
 
-// Longer rows: a CTA takes a row, and reads it five times, from L2 after the first.  Each of them ends in a barrier and a scan, which bound it.
+// Longer rows than a warp's registers hold: a CTA takes a row, and reads it five times, from L2 after the first.  Each of them ends in a barrier and
+// a scan, which bound it: 512 rows of 2048 blocks 18.0 us, of 8192 62; 18144 rows of 2048 382 us, of 8192 1220.  At 1024 blocks, which the warps still take, 512
+// rows 11.3 here and 10.1 there, 18144 rows 222 and 69; at 256 512 rows 6.8 and 5.2.
 __global__ __launch_bounds__(kSelThreads) void q8_select_kernel(const SelectArgs a) {
   constexpr uint32_t kBins = 256;
   __shared__ uint32_t s_q[CKV_MAX_BATCH];
@@ -403,6 +405,10 @@ int ckv_q8_attn_blocks(const ckv_q8_cache_t* cache, uint32_t n_heads, uint32_t r
   if (!(scale > 0.0f) || !(scale < 1e30f)) return CKV_ERR_SIZE;
   rc = check_lens(batch, ratio, seq_lens, extend_lens, kv_lens);
   if (rc) return rc;
+  // Three queries a request and more take four CTAs an SM with shorter rings instead of two (128 channels, up to eight heads to a kv head), us there
+  // instead of: lists of 32 blocks of 64, eight kv heads, 64 requests of three queries 137 / 152, of four 175 / 195 (161 / 194 where a request's lists are alike),
+  // of eight 326 / 367, eight requests of four 36.7 / 42.7, one of four 20.5 / 19.0; chunks of 430 queries 180 / 232.  Of one query it depends on how many
+  // there are: one to six requests 18.7 to 21.4 / 17.7 to 21.1, eight 23.6 / 23.6, sixteen 30.4 / 31.9, 64 60 / 66, and with lists of 128 blocks 173 / 166.
   a.many = num_q > 2 * batch;
   rc = list_space(a.c, n_heads, num_q, budget, a.many, &a.g, &w);
   if (rc) return rc;

@@ -65,8 +65,8 @@ struct Q8Geom {
 // From sizes alone (and the device's SM count), the same for the plan and the
 // attention call.  CKV_OK or CKV_ERR_SIZE.
 int q8_attn_geom(const Q8Cache& c, uint32_t batch, uint32_t num_q, uint32_t n_heads, Q8Geom* g);
-// Any batch.  many: several queries a request, whose lists name the same blocks: entries come from L2, and the split kernel hides its
-// own latency with more CTAs instead of memory's with deeper rings.
+// Any batch.  many: lists of several queries a request: the split kernel hides its items' starts with more CTAs an SM instead of
+// memory's latency with deeper rings (ckv_q8_attn_blocks has the rule).
 int q8_attn_geom_of(const Q8Cache& c, uint32_t batch, uint32_t num_q, uint32_t n_heads, bool many, Q8Geom* g);
 
 // Arguments of the attention kernels.

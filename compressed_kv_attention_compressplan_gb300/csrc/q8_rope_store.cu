@@ -441,7 +441,7 @@ __global__ __launch_bounds__(512, 1) void q8_rope_store_hold_kernel(const RopeSt
 }
 
 // Units whose rows do not fit the registers (128 entries of 512 channels): a row is read again for its codes, which comes from L2.
-// 42 to 53 us for the latent rows of which blocks of 64 entries take 40.
+// 37545 latent rows with a norm, 67 MB, take 45 us here, 36 in blocks of 64 entries (the kernel above), 35 in blocks of 32 and 33 in blocks of 16.
 constexpr int kWideThreads = 512;
 
 template <typename TIn, int kD>
@@ -523,7 +523,8 @@ int launch(const RopeStoreArgs& a, cudaStream_t s) {
   const uint32_t per = (units + parts - 1) / parts;
   parts = (units + per - 1) / per;
   const dim3 grid(records * parts);
-  // Threads that a barrier joins, against registers: 16 requests of up to 4096 new rows, eight kv heads, K and V, us (whole call): blocks of 32
+  // Threads that a barrier joins, against registers: 16 requests of up to 4096 new rows, eight kv heads, K and V, us (whole call; each size of
+  // blocks with lengths of its own, so that only figures of one size compare): blocks of 32
   // entries of 128 channels 60 with two vectors a thread and five CTAs of 128 an SM, 61 with four vectors and 64 threads, 68 with one and 256; 64
   // entries 77 with four vectors and three CTAs of 128, 85 to 89 with two vectors and two or three CTAs of 256, 101 with one and 512; 16 entries
   // of 64 channels 27.6 with 16 CTAs of 32 an SM and 31 with 20.  In fp32 five CTAs spill: 32 entries 81 with four and 90 with five.

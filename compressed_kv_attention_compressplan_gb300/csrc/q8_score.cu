@@ -162,7 +162,9 @@ __global__ __launch_bounds__(kBoundThreads, 4) void q8_bounds_kernel(const Bound
 // are read alike (sums over k may run in any order).  One query fragment serves both halves of the product: as max(q, 0)
 // against hi and as min(q, 0) against lo.  From 256 channels on a block's channels are split over the warps of a set, which
 // add their sums through shared memory.  Conversions and products bound it: a chunk of 128 channels takes 135 us where the 5th-generation
-// tensor cores take 37.5 (see the launch).
+// tensor cores take 37.5 (see the launch).  What it is for: 64 requests of up to 16384 latent entries of 512 channels, one query of 64 heads each, 34 us
+// (13 MB), of 128 heads 57; 2475 queries of 64 heads over such a cache 787 (50 GF), 1993 queries of 16 heads over four of 256 channels 95 (12 GF),
+// of 128 heads over one of 128 channels 374 (47 GF).
 constexpr int kScoreWarps = 8;
 constexpr int kScoreThreads = 32 * kScoreWarps;
 constexpr uint32_t kTileBlocks = 16;
@@ -638,7 +640,12 @@ __global__ __launch_bounds__(kScoreThreads, 2) void q8_score_kernel(const ScoreA
 template <int kD>
 int launch_scores(ScoreArgs a, cudaStream_t s) {
   using C = ScoreCfg<kD>;
-  // up to eight heads to a kv head, so that a segment's rows are whole queries: a batch may have fewer queries than requests
+  // Up to eight heads to a kv head, so that a segment's rows are whole queries (a batch may have fewer queries than requests), and up to eight rows
+  // a request on average.  us of this kernel / of the one that takes more rows, four heads to a kv head, contexts of up to 32768 entries: 128 channels, 64
+  // requests 15 / 51 at 8 rows, 42 / 50 at 32, 58 / 50 at 48, one request 6.1 / 9.0 at 8 and 9.3 / 9.5 at 128; 256 channels at 8 rows, 64 requests 11.1 / 14.6, one
+  // 6.5 / 5.7; 512 channels 19 / 27 and 9.9 / 5.4.  So equal requests cross at some 40 rows; but one kernel takes a whole batch, and this one reads a request's bounds again
+  // for every eight of its rows: 255 single tokens of 1024 entries beside a chunk of 257 queries that see 65536, eight rows on average, take 68 / 90,
+  // 64 of them beside 256 such queries, twenty on average, 66 / 37.  (Chunks no longer than the rest: 200 tokens beside 512 queries of 8192 entries 37 / 68.)
   if (a.span <= 8 && static_cast<uint64_t>(a.r.num_q) * a.span <= 8ull * a.r.batch) {
     static std::atomic<uint64_t> few_done;
     auto* few = q8_score_few_kernel<kD>;
@@ -650,7 +657,7 @@ int launch_scores(ScoreArgs a, cudaStream_t s) {
   static std::atomic<uint64_t> done;
   auto* kernel = q8_score_kernel<kD>;
   // The tensor-core kernel takes 128 query rows at nearly the cost of sixteen (32 requests of up to 512 blocks, 8 kv heads of 128
-  // channels, us here / there: 31.5 / 27.6 at 12 rows a request, 47 / 27.7 at 32, 85 / 28.8 at 64; one request of 1024 blocks 7.9 / 8.8
+  // channels, us of q8_score_kernel / there: 31.5 / 27.6 at 12 rows a request, 47 / 27.7 at 32, 85 / 28.8 at 64; one request of 1024 blocks 7.9 / 8.8
   // at 16 and 14.7 / 9.0 at 64; 64 channels 26.8 / 22.2 at 16).
   if constexpr (kD <= 128) {
     if (a.group <= 64) return launch_q8_score_tc(a, s);

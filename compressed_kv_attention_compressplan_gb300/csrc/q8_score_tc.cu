@@ -10,9 +10,11 @@
 // is stored; one thread issues the products; eight warps finish the scores.  Rows of heads that do not exist repeat the
 // group's last head, so that no maximum has to leave them out.
 //
-// Bound.  Three things of one size that share the SM's issue slots (63 %) and shared memory: the products, which read both operands from
-// it, the operands' conversions, and the scores' way out.  3 requests of up to 512 blocks, 500 to 1024 queries each, 32 heads over eight kv heads of
-// 128 channels: 37.5 us.  Without the conversions 34.6, without the scores' way out 32.7, without both 26.  Units of four for each SM, dealt out one by one, 40;
+// Bound.  The roles' sequence itself: 3 requests of up to 512 blocks, 500 to 1024 queries each, 32 heads over eight kv heads of 128 channels, eleven tiles a
+// CTA, take 37.5 us, and 20.9 are left without loads, conversions, products and the scores' way out: the launch, the requests' scan and a unit's place
+// (9 us is a call of one tile a CTA), the barriers between the roles and the operands' stores of 64 KB a tile.  Without the conversions
+// 34.9, without the scores' way out 32.5, without both 26.7; then without the products too 23.9, without the rows' loads too 23.5, without the bounds' 26.6.
+// Tried: units of four for each SM, dealt out one by one, 40;
 // rows kept and bounds streamed past them 43 (a unit's start, three dependent reads, then comes every four tiles); eight warps making operands
 // 74, with spilled registers for the loads on their way, or 46 beside kept rows; sixteen warps for the scores there 51; the places behind
 // the last tile filled first 39.

@@ -612,7 +612,11 @@ int ckv_q8_evict(const ckv_q8_cache_t* cache, float* weights, const int64_t* rid
  *   (a, b) -> (a*cos - b*sin, a*sin + b*cos),  (cos, sin) = freqs[positions[row]][i],
  * pair i being channels rope_begin + 2i and 2i + 1 (halves == 0) or rope_begin + i
  * and i + rope_dim/2 (halves != 0); values (v_rows) are stored as they come.
- * Everything is fp32 up to the one rounding to e4m3; no product is fused with a sum.
+ * Everything is fp32 up to the one rounding to e4m3.  Each product of the rotation, and of a
+ * value with its weight and its row's factor, is rounded by itself; the mean of squares is
+ * summed with fused products, in an order of the kernel's own, so that normed codes may
+ * differ by a step from those of another order, and a row whose squares pass fp32's range
+ * (values above 1e18) becomes zeros.
  *   k_rows, v_rows  [num_rows, n_kv_heads, head_dim] with k_stride and v_stride
  *                 elements from row to row (at least n_kv_heads * head_dim, and
  *                 whole 16 bytes), as rows lie in a fused projection.
@@ -657,7 +661,8 @@ int ckv_q8_bounds(const ckv_q8_cache_t* cache, void* bounds, const int64_t* rid,
  *   scale * k_scale * max over the kv head's query heads of sum_c max(q_c * hi_c, q_c * lo_c),
  * which no score of the block's entries is above; -infinity for the other j < width.
  * NaN where a bound or the query has one.  A query row is rounded as in
- * ckv_q8_attn (exact down to 2^-28 of its largest value), sums are fp32.  A block number
+ * ckv_q8_attn (exact down to 2^-28 of its largest value), sums are fp32, and no step
+ * leaves fp32's range where the score stays in it.  A block number
  * outside the pool scores -infinity and sets CKV_STATUS_BAD_INDEX; a request with
  * more than width blocks sets CKV_STATUS_BAD_LENGTH, as above.  Only k_scale (and
  * the shape) of the cache is read. */
