@@ -1166,3 +1166,22 @@ def test_missing_blocks_in_every_part_of_a_list(heads, H, D, latent):
     skip = {-3, -1, w.blocks, 0x7FFFFFFF, -0x80000000, w.blocks + 7}
     assert any(w.table[first, j] in skip for j in lists[0].ravel())
     check_attn(w, q, lists, seq, q_lens, 1, F32, skip=skip, flags=ckv.STATUS_BAD_INDEX)
+
+
+@pytest.mark.parametrize("T,D", APPEND)
+def test_every_append_with_a_norm_of_rows_whose_squares_overflow(T, D):
+    """1e20 squared is past fp32: the mean is infinite and the row's factor 0; its neighbours are normed as ever."""
+    w = World(1400 + T + D, [0], 1, D, T, True, more=T)
+    x = w.r.standard_normal((T, 1, D)).astype(np.float32)
+    x[3] *= 1e20
+    cache, st = w.cache(), status()
+    plan, counts = ckv.plan_q8_store(cache, i64(w.rid), i64([T]), i64([T]), T, i32(w.table), status=st)
+    ckv.q8_rope_store(cache, torch.as_tensor(x, device=DEV), None, plan, None, None, counts, norm_weight=torch.ones(D, device=DEV), status=st)
+    blk = w.table[w.rid[0], 0]
+    got, s = ref.E4M3[codes(cache.k)[blk, 0]], float(cache.k_scale[blk, 0])
+    assert (got[3] == 0).all() and int(st[0]) == 0
+    y = bref.rope(x, np.ones(D, np.float32), 1e-6, None, None, 0, False)[:, 0]
+    y[3] = 0
+    off = ((D + 4) / 2 + 8) * 2.0 ** -24
+    near = off * 2 * np.abs(y).max(-1, keepdims=True)
+    assert (np.abs(got * s - y) <= np.maximum(np.abs(y) * 2.0 ** -4, s * 2.0 ** -10) + near).all()
